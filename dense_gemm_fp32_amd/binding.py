@@ -59,12 +59,31 @@ _lib.gemm_probe_mfma.argtypes = [_I, _I, _P, ctypes.c_size_t, _P, ctypes.c_size_
                                  ctypes.POINTER(ctypes.c_double), _P]
 _lib.gemm_probe_mfma.restype = _I
 
+_L = ctypes.c_longlong
+_Z = ctypes.c_size_t
+_LORA = [_I, _I, _I, _F, _P, _I, _P, _I, _F, _P, _I, _I, _I, _P, _I, _L, _P, _I, _L, _P, _P, _P,
+         _P, _Z, _P]
+_LORA_GRAD = [_I, _I, _I, _F, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _L, _P, _I, _L, _P, _P, _P,
+              _F, _P, _I, _F, _P, _I, _L, _P, _I, _L, _P, _Z, _P]
+_MOE = [_I, _I, _I, _I, _I, _I, _F, _P, _I, _P, _I, _P, _I, _L, _P, _I, _L, _F, _P, _I, _P, _P,
+        _P, _Z, _P]
+ROW_NAMES = ("gemm_lora_f16", "gemm_lora_f32", "gemm_lora_grad_f16", "gemm_lora_grad_f32",
+             "gemm_moe_f16", "gemm_moe_f32", "gemm_lora_workspace", "gemm_lora_grad_workspace",
+             "gemm_moe_workspace")
+for _n, _args in (("gemm_lora", _LORA), ("gemm_lora_grad", _LORA_GRAD), ("gemm_moe", _MOE)):
+    for _t in ("f16", "f32"):
+        getattr(_lib, "%s_%s" % (_n, _t)).argtypes = _args
+        getattr(_lib, "%s_%s" % (_n, _t)).restype = _I
+    getattr(_lib, _n + "_workspace").argtypes = [_I] * 6
+    getattr(_lib, _n + "_workspace").restype = _Z
+
 EXPORTS = ("gemm_f32", "gemm_f16", "gemm_f16f32", "gemm_f32_valu", "gemm_f32_noalloc",
            "gemm_f32_colmajor", "gemm_f16_colmajor", "gemm_f16f32_colmajor", "gemm_status_string",
            "gemm_describe", "gemm_set_load_mode", "gemm_set_tile_config", "gemm_set_split",
            "gemm_set_tail_split", "gemm_set_pack", "gemm_set_stream_k", "gemm_set_workspace_limit",
-           "gemm_probe_mfma") + LAYOUT_NAMES
+           "gemm_probe_mfma") + LAYOUT_NAMES + ROW_NAMES
 GEMM_ERR_SCRATCH_LIMIT = -200
+GEMM_ERR_NO_WORKSPACE = -201
 
 
 class GemmError(RuntimeError):
@@ -288,3 +307,199 @@ def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):
     if rc != 0:
         raise GemmError(rc)
     return C
+
+
+def _row_entry(name):
+    fn = getattr(_lib, name)
+    # pointers and the stream may be torch objects; numbers pass as they are
+    at = [i for i, t in enumerate(fn.argtypes) if t is _P]
+
+    def call(*args):
+        args = list(args)
+        if len(args) == len(fn.argtypes) - 1:
+            args.append(None)
+        for i in at[:-1]:
+            args[i] = _addr(args[i])
+        args[-1] = _stream(args[-1])
+        return fn(*args)
+    call.__name__ = name
+    call.__doc__ = "%s (see include/gemm.h).  Returns the status code." % name
+    return call
+
+
+for _n in ROW_NAMES:
+    globals()[_n] = getattr(_lib, _n) if _n.endswith("_workspace") else _row_entry(_n)
+
+_KINDS = {torch.float16: ("f16", 1), torch.float32: ("f32", 0)}
+
+
+def _rows(name, t, rows, cols, dtype):
+    """Leading dimension of a rows x cols matrix with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must be %d x %d, not %s" % (name, rows, cols, tuple(t.shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError("%s must have contiguous rows (stride(1) == 1)" % name)
+    return ld if ld > 1 else 1
+
+
+def _stack(name, t, n, rows, cols, dtype):
+    """(leading dimension, stride) of n stacked rows x cols matrices."""
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != rows or t.shape[2] != cols:
+        raise ValueError("%s must be %d x %d x %d, not %s" % (name, n, rows, cols,
+                                                              tuple(t.shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    ld = t.stride(1) if rows > 1 else cols
+    if (cols > 1 and t.stride(2) != 1) or ld < cols or t.stride(0) < 0:
+        raise ValueError("%s must have contiguous rows (stride(2) == 1)" % name)
+    return (ld if ld > 1 else 1), (t.stride(0) if n > 1 else 0)
+
+
+def _vector(name, t, n, dtype):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be %d contiguous values of %s" % (name, n, dtype))
+    return t.data_ptr()
+
+
+def _one_device(first, *others):
+    if not first.is_cuda:
+        raise ValueError("the tensors must be GPU tensors")
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("the tensors must be on one device")
+    return dev
+
+
+def _call_rows(name, dev, stream, workspace, need, args):
+    """Run entry point `name` on the current stream of `dev` or the one given.
+    Without a workspace, one comes from torch's allocator on the current
+    stream, or from the library's pool on a stream that was given."""
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif stream is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, size = workspace.data_ptr(), need
+    else:
+        ws, size = None, 0
+    stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    rc = getattr(_lib, name)(*args, ws, size, stream)
+    if rc != 0:
+        raise GemmError(rc)
+
+
+def lora(X, W, A, B, rows, Y, scale=None, ranks=None, alpha=1.0, beta=0.0, workspace=None,
+         stream=None):
+    """Y := alpha*(X @ W.t() + the low-rank term of each row's adapter) + beta*Y
+    (in place): row i adds scale[a] * (X[i] @ A[a].t()) @ B[a].t() for a =
+    rows[i], nothing where rows[i] is outside 0 .. L-1.
+
+    X is M x K, W N x K, Y M x N, A L x R x K, B L x N x R (float16, or all
+    float32; rows contiguous, possibly padded).  rows: M int32; scale: L
+    float32 or None (1); ranks: L int32 or None (R), the ranks in use.
+    workspace: a uint8 tensor of gemm_lora_workspace bytes to use instead of
+    a new one.  Uses the current torch stream unless one is given; see
+    gemm_lora_f16 in include/gemm.h."""
+    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3:
+        raise ValueError("X and W must be 2-D and A 3-D")
+    M, K = X.shape
+    N = W.shape[0]
+    L, R = A.shape[0], A.shape[1]
+    dt = X.dtype
+    if dt not in _KINDS:
+        raise ValueError("unsupported dtype %s" % dt)
+    kind, code = _KINDS[dt]
+    dev = _one_device(X, W, A, B, rows, Y, scale, ranks)
+    ldx, ldw, ldy = _rows("X", X, M, K, dt), _rows("W", W, N, K, dt), _rows("Y", Y, M, N, dt)
+    lda, sa = _stack("A", A, L, R, K, dt)
+    ldb, sb = _stack("B", B, L, N, R, dt)
+    _call_rows("gemm_lora_" + kind, dev, stream, workspace,
+               _lib.gemm_lora_workspace(code, M, N, K, L, R),
+               (M, N, K, alpha, X.data_ptr(), ldx, W.data_ptr(), ldw, beta, Y.data_ptr(), ldy, L,
+                R, A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb,
+                _vector("scale", scale, L, torch.float32),
+                _vector("ranks", ranks, L, torch.int32), _vector("rows", rows, M, torch.int32)))
+    return Y
+
+
+def lora_grad(dY, X, W, A, B, rows, dX=None, dA=None, dB=None, scale=None, ranks=None, alpha=1.0,
+              beta_x=0.0, beta_ab=0.0, workspace=None, stream=None):
+    """Gradients of lora() for dY (M x N), into those of dX (M x K, X's type),
+    dA and dB (A's and B's shapes, float32) that are given:
+
+        dX := alpha*(dY @ W + G @ A[a]) + beta_x*dX,  G[i] = scale[a] * dY[i] @ B[a]
+        dA[a] := alpha * sum of G[i]^T X[i] over a's rows + beta_ab*dA[a]
+        dB[a] := alpha*scale[a] * sum of dY[i]^T (X[i] @ A[a].t()) + beta_ab*dB[a]
+
+    The other arguments are lora()'s; see gemm_lora_grad_f16 in
+    include/gemm.h.  Returns (dX, dA, dB)."""
+    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3:
+        raise ValueError("X and W must be 2-D and A 3-D")
+    M, K = X.shape
+    N = W.shape[0]
+    L, R = A.shape[0], A.shape[1]
+    dt = X.dtype
+    if dt not in _KINDS:
+        raise ValueError("unsupported dtype %s" % dt)
+    kind, code = _KINDS[dt]
+    dev = _one_device(X, W, A, B, rows, dY, scale, ranks, dX, dA, dB)
+    lddy = _rows("dY", dY, M, N, dt)
+    ldx, ldw = _rows("X", X, M, K, dt), _rows("W", W, N, K, dt)
+    lda, sa = _stack("A", A, L, R, K, dt)
+    ldb, sb = _stack("B", B, L, N, R, dt)
+    lddx = ldda = sda = lddb = sdb = 0
+    if dX is not None:
+        lddx = _rows("dX", dX, M, K, dt)
+    if dA is not None:
+        ldda, sda = _stack("dA", dA, L, R, K, torch.float32)
+    if dB is not None:
+        lddb, sdb = _stack("dB", dB, L, N, R, torch.float32)
+    _call_rows("gemm_lora_grad_" + kind, dev, stream, workspace,
+               _lib.gemm_lora_grad_workspace(code, M, N, K, L, R),
+               (M, N, K, alpha, dY.data_ptr(), lddy, X.data_ptr(), ldx, W.data_ptr(), ldw, L, R,
+                A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb,
+                _vector("scale", scale, L, torch.float32),
+                _vector("ranks", ranks, L, torch.int32), _vector("rows", rows, M, torch.int32),
+                beta_x, _addr(dX), lddx, beta_ab, _addr(dA), ldda, sda, _addr(dB), lddb, sdb))
+    return dX, dA, dB
+
+
+def moe(X, router, W1, W2, top_k, Y, renorm=True, alpha=1.0, beta=0.0, ids=None, weights=None,
+        workspace=None, stream=None):
+    """A mixture-of-experts layer for a few tokens: Y := alpha * (the weighted
+    sum of each token's top_k gated experts) + beta*Y (in place).
+
+    X is M x D (1 <= M <= 256), router E x D, W1 E x 2F x D (gate rows, then up
+    rows), W2 E x D x F, Y M x D (float16, or all float32).  ids (M x top_k
+    int32) and weights (M x top_k float32), if given, receive the experts
+    chosen, largest logit first, and their weights: softmax over the chosen
+    (renorm) or over all experts.  workspace: a uint8 tensor of
+    gemm_moe_workspace bytes to use instead of a new one.  Uses the current
+    torch stream unless one is given; see gemm_moe_f16 in include/gemm.h."""
+    if X.dim() != 2 or W2.dim() != 3:
+        raise ValueError("X must be 2-D and W2 3-D")
+    M, D = X.shape
+    E, F = W2.shape[0], W2.shape[2]
+    dt = X.dtype
+    if dt not in _KINDS:
+        raise ValueError("unsupported dtype %s" % dt)
+    kind, code = _KINDS[dt]
+    dev = _one_device(X, router, W1, W2, Y, ids, weights)
+    ldx, ldr, ldy = _rows("X", X, M, D, dt), _rows("router", router, E, D, dt), \
+        _rows("Y", Y, M, D, dt)
+    ld1, s1 = _stack("W1", W1, E, 2 * F, D, dt)
+    ld2, s2 = _stack("W2", W2, E, D, F, dt)
+    _call_rows("gemm_moe_" + kind, dev, stream, workspace,
+               _lib.gemm_moe_workspace(code, M, D, F, E, top_k),
+               (M, D, F, E, top_k, 1 if renorm else 0, alpha, X.data_ptr(), ldx,
+                router.data_ptr(), ldr, W1.data_ptr(), ld1, s1, W2.data_ptr(), ld2, s2, beta,
+                Y.data_ptr(), ldy, _vector("ids", ids, M * top_k, torch.int32),
+                _vector("weights", weights, M * top_k, torch.float32)))
+    return Y

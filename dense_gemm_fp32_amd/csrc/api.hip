@@ -140,6 +140,11 @@ int run_gemm(int kind, bool ta, bool tb, int M, int N, int K, float alpha, const
 
 }  // namespace
 
+namespace dgemm {
+long long workspace_limit() { return g_ws_limit.load(std::memory_order_relaxed); }
+bool force_scalar_loads() { return g_load_mode.load(std::memory_order_relaxed) == 1; }
+}  // namespace dgemm
+
 extern "C" {
 
 int gemm_f32(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb,
@@ -299,6 +304,7 @@ const char *gemm_status_string(int status) {
     case -10: return "invalid argument 10: C is NULL";
     case -11: return "invalid argument 11: ldc < max(1, N) (row-major) or max(1, M) (column-major)";
     case GEMM_ERR_SCRATCH_LIMIT: return "gemm_f32_noalloc: the call's workspace (split K) would exceed the library's fixed scratch region (64 MiB); nothing was enqueued";
+    case GEMM_ERR_NO_WORKSPACE: return "the call's workspace could not be had from the library's pool (gemm_set_workspace_limit, or out of memory); nothing was enqueued";
     case -101: return "invalid probe argument 1: dtype is not 0 (fp32) or 1 (fp16)";
     case -102: return "invalid probe argument 2: iters < 1";
     case -103: return "invalid probe argument 3: operands is NULL";
@@ -306,6 +312,71 @@ const char *gemm_status_string(int status) {
     case -105: return "invalid probe argument 5: out is NULL";
     case -106: return "invalid probe argument 6: out buffer smaller than 1 MiB";
     case -107: return "invalid probe argument 7: flops is NULL";
+    case -301: return "gemm_lora: invalid argument 1: M < 0";
+    case -302: return "gemm_lora: invalid argument 2: N < 0";
+    case -303: return "gemm_lora: invalid argument 3: K < 0";
+    case -305: return "gemm_lora: invalid argument 5: X is NULL";
+    case -306: return "gemm_lora: invalid argument 6: ldx < max(1, K)";
+    case -307: return "gemm_lora: invalid argument 7: W is NULL";
+    case -308: return "gemm_lora: invalid argument 8: ldw < max(1, K)";
+    case -310: return "gemm_lora: invalid argument 10: Y is NULL";
+    case -311: return "gemm_lora: invalid argument 11: ldy < max(1, N)";
+    case -312: return "gemm_lora: invalid argument 12: L outside 0 .. 65535";
+    case -313: return "gemm_lora: invalid argument 13: R outside 0 .. 256";
+    case -314: return "gemm_lora: invalid argument 14: A is NULL";
+    case -315: return "gemm_lora: invalid argument 15: lda < max(1, K)";
+    case -316: return "gemm_lora: invalid argument 16: stride_a < 0";
+    case -317: return "gemm_lora: invalid argument 17: B is NULL";
+    case -318: return "gemm_lora: invalid argument 18: ldb < max(1, R)";
+    case -319: return "gemm_lora: invalid argument 19: stride_b < 0";
+    case -322: return "gemm_lora: invalid argument 22: rows is NULL";
+    case -323: return "gemm_lora: invalid argument 23: workspace not 256-byte aligned";
+    case -324: return "gemm_lora: invalid argument 24: workspace_bytes too small (gemm_lora_workspace)";
+    case -401: return "gemm_lora_grad: invalid argument 1: M < 0";
+    case -402: return "gemm_lora_grad: invalid argument 2: N < 0";
+    case -403: return "gemm_lora_grad: invalid argument 3: K < 0";
+    case -405: return "gemm_lora_grad: invalid argument 5: dY is NULL";
+    case -406: return "gemm_lora_grad: invalid argument 6: lddy < max(1, N)";
+    case -407: return "gemm_lora_grad: invalid argument 7: X is NULL";
+    case -408: return "gemm_lora_grad: invalid argument 8: ldx < max(1, K)";
+    case -409: return "gemm_lora_grad: invalid argument 9: W is NULL";
+    case -410: return "gemm_lora_grad: invalid argument 10: ldw < max(1, K)";
+    case -411: return "gemm_lora_grad: invalid argument 11: L outside 0 .. 65535";
+    case -412: return "gemm_lora_grad: invalid argument 12: R outside 0 .. 256";
+    case -413: return "gemm_lora_grad: invalid argument 13: A is NULL";
+    case -414: return "gemm_lora_grad: invalid argument 14: lda < max(1, K)";
+    case -415: return "gemm_lora_grad: invalid argument 15: stride_a < 0";
+    case -416: return "gemm_lora_grad: invalid argument 16: B is NULL";
+    case -417: return "gemm_lora_grad: invalid argument 17: ldb < max(1, R)";
+    case -418: return "gemm_lora_grad: invalid argument 18: stride_b < 0";
+    case -421: return "gemm_lora_grad: invalid argument 21: rows is NULL";
+    case -424: return "gemm_lora_grad: invalid argument 24: lddx < max(1, K)";
+    case -427: return "gemm_lora_grad: invalid argument 27: ldda < max(1, K)";
+    case -428: return "gemm_lora_grad: invalid argument 28: stride_da less than one matrix";
+    case -430: return "gemm_lora_grad: invalid argument 30: lddb < max(1, R)";
+    case -431: return "gemm_lora_grad: invalid argument 31: stride_db less than one matrix";
+    case -432: return "gemm_lora_grad: invalid argument 32: workspace not 256-byte aligned";
+    case -433: return "gemm_lora_grad: invalid argument 33: workspace_bytes too small (gemm_lora_grad_workspace)";
+    case -501: return "gemm_moe: invalid argument 1: M outside 0 .. 256";
+    case -502: return "gemm_moe: invalid argument 2: D < 1";
+    case -503: return "gemm_moe: invalid argument 3: F < 1";
+    case -504: return "gemm_moe: invalid argument 4: E outside 1 .. 1024";
+    case -505: return "gemm_moe: invalid argument 5: top_k outside 1 .. min(E, 64)";
+    case -506: return "gemm_moe: invalid argument 6: renorm is not 0 or 1";
+    case -508: return "gemm_moe: invalid argument 8: X is NULL";
+    case -509: return "gemm_moe: invalid argument 9: ldx < D";
+    case -510: return "gemm_moe: invalid argument 10: Wr is NULL";
+    case -511: return "gemm_moe: invalid argument 11: ldr < D";
+    case -512: return "gemm_moe: invalid argument 12: W1 is NULL";
+    case -513: return "gemm_moe: invalid argument 13: ld1 < D";
+    case -514: return "gemm_moe: invalid argument 14: stride1 < 0";
+    case -515: return "gemm_moe: invalid argument 15: W2 is NULL";
+    case -516: return "gemm_moe: invalid argument 16: ld2 < F";
+    case -517: return "gemm_moe: invalid argument 17: stride2 < 0";
+    case -519: return "gemm_moe: invalid argument 19: Y is NULL";
+    case -520: return "gemm_moe: invalid argument 20: ldy < D";
+    case -523: return "gemm_moe: invalid argument 23: workspace not 256-byte aligned";
+    case -524: return "gemm_moe: invalid argument 24: workspace_bytes too small (gemm_moe_workspace)";
     default: break;
   }
   if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));

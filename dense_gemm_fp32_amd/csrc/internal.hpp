@@ -200,6 +200,86 @@ hipError_t launch_f16(const Call &c);
 hipError_t launch_scale_f32(int M, int N, float beta, float *C, int ldc, hipStream_t s);
 hipError_t launch_scale_f16(int M, int N, float beta, uint16_t *C, int ldc, hipStream_t s);
 
+// Low-rank adapters beside a shared projection, and their gradients
+// (lora.hip).  One validated call, M, N, K > 0 and alpha != 0 (lora: L and R
+// > 0 too).  half: fp16 matrices, else fp32; dA and dB are always fp32.
+struct LoraCall {
+  bool half;
+  int M, N, K;
+  float alpha;
+  const void *X;
+  int ldx;
+  const void *W;
+  int ldw;
+  float beta;              // lora: of Y
+  void *Y;
+  int ldy;
+  int L, R;
+  const void *A;
+  int lda;
+  long long stride_a;
+  const void *B;
+  int ldb;
+  long long stride_b;
+  const float *scale;
+  const int *ranks, *rows;
+  const void *dY;          // gradients only, from here
+  int lddy;
+  float beta_x;
+  void *dX;
+  int lddx;
+  float beta_ab;
+  float *dA;
+  int ldda;
+  long long stride_da;
+  float *dB;
+  int lddb;
+  long long stride_db;
+  bool force_scalar;
+  hipStream_t stream;
+};
+size_t lora_workspace(const LoraCall &c);
+hipError_t launch_lora(const LoraCall &c, void *ws);
+size_t lora_grad_workspace(const LoraCall &c);
+hipError_t launch_lora_grad(const LoraCall &c, void *ws);
+// Gradients of a call without a product term (alpha == 0): D_a := beta * D_a
+// for the L adapters' rows x cols matrices.
+hipError_t launch_scale_batch_f32(int L, int rows, int cols, float beta, float *D, int ldd,
+                                  long long stride, hipStream_t s);
+
+// A mixture-of-experts layer for a few tokens (moe.hip); validated, M, D > 0.
+struct MoeCall {
+  bool half;
+  int M, D, F, E, k;
+  bool renorm;
+  float alpha;
+  const void *X;
+  int ldx;
+  const void *Wr;
+  int ldr;
+  const void *W1;
+  int ld1;
+  long long stride1;
+  const void *W2;
+  int ld2;
+  long long stride2;
+  float beta;
+  void *Y;
+  int ldy;
+  int *ids;
+  float *weights;
+  bool force_scalar;
+  hipStream_t stream;
+};
+constexpr int kMoeMaxTokens = 256;
+constexpr int kMoeMaxExperts = 1024;
+size_t moe_workspace(const MoeCall &c);
+hipError_t launch_moe(const MoeCall &c, void *ws);
+
+// The process-wide switches the calls above go by (api.hip).
+long long workspace_limit();
+bool force_scalar_loads();
+
 inline bool aligned_to(const void *p, uintptr_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) % bytes) == 0;
 }

@@ -140,6 +140,7 @@ typedef uint16_t gemm_half_t;
 
 #define GEMM_SUCCESS 0
 #define GEMM_ERR_SCRATCH_LIMIT (-200)
+#define GEMM_ERR_NO_WORKSPACE (-201)
 
 /*
  * fp32 GEMM: A, B, C hold binary32 values; products are accumulated in fp32
@@ -296,6 +297,167 @@ int gemm_f16f32_tn(int M, int N, int K, float alpha, const gemm_half_t *A, int l
 int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int lda,
                    const gemm_half_t *B, int ldb, float beta, float *C, int ldc,
                    void *stream);
+
+/*
+ * Products whose rows choose their own weights
+ * --------------------------------------------
+ *
+ * The calls below multiply each row of a batch by weights that the row picks
+ * by an index: the low-rank adapter of its request beside the projection
+ * that all rows share, or the experts its router chose.  As above: row-major
+ * device matrices, element (i, j) of X at X[i*ldX + j], pad elements never
+ * read or written, work enqueued on `stream` only, fp32 accumulation, one
+ * rounding to the output type, results that do not change from call to call,
+ * and outputs that must not overlap inputs.
+ *
+ * Workspace: `workspace` is device memory of at least the bytes that the
+ * call's *_workspace function names for its sizes (256-byte aligned), the
+ * call's alone until its work on `stream` is done; NULL takes it from the
+ * library's pool in stream order (gemm_set_workspace_limit applies;
+ * GEMM_ERR_NO_WORKSPACE if it cannot be had, nothing enqueued).  Nothing in it
+ * needs an initial value.  The shared product inside a low-rank call may
+ * split K as gemm_* does, with workspace of its own from the pool.
+ *
+ * Status: 0; a positive hipError_t; or for invalid argument i (from 1, in
+ * signature order) -300-i (gemm_lora_*), -400-i (gemm_lora_grad_*), -500-i
+ * (gemm_moe_*); checked before any HIP call.
+ */
+#define GEMM_LORA_MAX_RANK 256
+#define GEMM_LORA_MAX_ADAPTERS 65535
+#define GEMM_MOE_MAX_TOKENS 256
+#define GEMM_MOE_MAX_EXPERTS 1024
+#define GEMM_MOE_MAX_CHOICES 64
+
+/*
+ * Low-rank adapters of many requests beside a shared projection:
+ *
+ *     Y[i] := alpha * (W x_i + scale[a] * B_a (A_a x_i)) + beta * Y[i],  a = rows[i]
+ *
+ *   X, ldx    M x K, row i = x_i;  ldx >= max(1, K)
+ *   W, ldw    N x K, the shared projection (as gemm_*_nt's B); ldw >= max(1, K)
+ *   Y, ldy    M x N, not read when beta == 0;  ldy >= max(1, N)
+ *   L, R      adapters (0 .. GEMM_LORA_MAX_ADAPTERS) and the rank their
+ *             storage has room for (0 .. GEMM_LORA_MAX_RANK); either 0: no
+ *             adapter term
+ *   A, lda, stride_a   adapter a's R x K matrix at A + a*stride_a, lda >= max(1, K)
+ *   B, ldb, stride_b   its N x R matrix at B + a*stride_b, ldb >= max(1, R)
+ *   scale     device, L floats (NULL: 1)
+ *   ranks     device, L ints (NULL: R): the ranks in use, clamped to 0 .. R;
+ *             A's rows and B's columns from there on are not read
+ *   rows      device, M ints in any order: the adapter of each row; an index
+ *             outside 0 .. L-1 (-1, say) means no adapter for that row
+ *
+ * A row is touched by its own adapter only: an infinity or NaN in another's
+ * weights does not reach it.  V = A_a x_i is summed in fp32 and enters the
+ * second product in at least 21 significant bits; the sum with W x_i is
+ * formed in fp32 and rounded once.  Accuracy, with q = |W||x| + |scale||B|(|A||x|):
+ * |err| <= 4*(K+R+4)*u*|alpha|*q + 4*u*|beta*Y| plus the one rounding, u = 2^-24.
+ * alpha == 0 or K == 0: Y := beta * Y.
+ */
+int gemm_lora_f16(int M, int N, int K, float alpha,
+                  const gemm_half_t *X, int ldx,
+                  const gemm_half_t *W, int ldw,
+                  float beta, gemm_half_t *Y, int ldy,
+                  int L, int R,
+                  const gemm_half_t *A, int lda, long long stride_a,
+                  const gemm_half_t *B, int ldb, long long stride_b,
+                  const float *scale, const int *ranks, const int *rows,
+                  void *workspace, size_t workspace_bytes, void *stream);
+int gemm_lora_f32(int M, int N, int K, float alpha,
+                  const float *X, int ldx,
+                  const float *W, int ldw,
+                  float beta, float *Y, int ldy,
+                  int L, int R,
+                  const float *A, int lda, long long stride_a,
+                  const float *B, int ldb, long long stride_b,
+                  const float *scale, const int *ranks, const int *rows,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of a gemm_lora_* call (dtype: 0 = fp32, 1 = fp16); 0 for
+ * sizes that need none or are invalid. */
+size_t gemm_lora_workspace(int dtype, int M, int N, int K, int L, int R);
+
+/*
+ * Gradients of gemm_lora_* (of alpha * (...)), for dY the gradient of its
+ * result and the shared projection W frozen:
+ *
+ *     dX   := alpha * (dY W + G A) + beta_x * dX,   G[i] = scale[a] B_a^T dy_i
+ *     dA_a := alpha * sum_{i: rows[i] = a} G[i]^T x_i + beta_ab * dA_a
+ *     dB_a := alpha * scale[a] * sum_{i: rows[i] = a} dy_i^T (A_a x_i)^T + beta_ab * dB_a
+ *
+ * dY is M x N (lddy >= max(1, N)), dX M x K, both of the matrices' type; dA
+ * and dB are fp32 for either type, laid out as A and B are with strides of
+ * their own (of at least one matrix, so that no two overlap).  The other
+ * arguments are gemm_lora_*'s.  dX, dA and dB may each be NULL: not wanted
+ * (W is not read without dX, X not without dA or dB).  With a beta of 0 the
+ * output is not read.  Ranks beyond an adapter's, and adapters without rows,
+ * get the gradient 0 (beta_ab * dA_a stays).
+ */
+int gemm_lora_grad_f16(int M, int N, int K, float alpha,
+                       const gemm_half_t *dY, int lddy,
+                       const gemm_half_t *X, int ldx,
+                       const gemm_half_t *W, int ldw,
+                       int L, int R,
+                       const gemm_half_t *A, int lda, long long stride_a,
+                       const gemm_half_t *B, int ldb, long long stride_b,
+                       const float *scale, const int *ranks, const int *rows,
+                       float beta_x, gemm_half_t *dX, int lddx,
+                       float beta_ab, float *dA, int ldda, long long stride_da,
+                       float *dB, int lddb, long long stride_db,
+                       void *workspace, size_t workspace_bytes, void *stream);
+int gemm_lora_grad_f32(int M, int N, int K, float alpha,
+                       const float *dY, int lddy,
+                       const float *X, int ldx,
+                       const float *W, int ldw,
+                       int L, int R,
+                       const float *A, int lda, long long stride_a,
+                       const float *B, int ldb, long long stride_b,
+                       const float *scale, const int *ranks, const int *rows,
+                       float beta_x, float *dX, int lddx,
+                       float beta_ab, float *dA, int ldda, long long stride_da,
+                       float *dB, int lddb, long long stride_db,
+                       void *workspace, size_t workspace_bytes, void *stream);
+size_t gemm_lora_grad_workspace(int dtype, int M, int N, int K, int L, int R);
+
+/*
+ * A mixture-of-experts layer for a few tokens (1 .. GEMM_MOE_MAX_TOKENS):
+ *
+ *     l = Wr x;  e_1 .. e_k: the top_k largest logits, largest first, the
+ *                lower index first among equals;
+ *     w = softmax of l over the chosen (renorm = 1) or over all E (renorm = 0);
+ *     Y := alpha * sum_j w_j W2_e (silu(g) * u) + beta * Y,   [g; u] = W1_e x,
+ *
+ * silu(g) = g / (1 + exp(-g)).
+ *   X, ldx             M x D
+ *   Wr, ldr            E x D, the router
+ *   W1, ld1, stride1   expert e's 2F x D matrix (gate rows, then up rows) at
+ *                      W1 + e*stride1
+ *   W2, ld2, stride2   its D x F matrix at W2 + e*stride2
+ *   Y, ldy             M x D, not read when beta == 0
+ *   ids, weights       device, M x top_k, dense: the experts chosen (int) and
+ *                      w (float); either may be NULL
+ * Logits are summed in 64 bits, since which expert a token takes hangs on
+ * their order; a NaN logit ranks below every number.  Weights of experts that
+ * no token chose are not read.  alpha == 0: Y := beta * Y, nothing else is
+ * read or written (ids and weights included).
+ */
+int gemm_moe_f16(int M, int D, int F, int E, int top_k, int renorm, float alpha,
+                 const gemm_half_t *X, int ldx,
+                 const gemm_half_t *Wr, int ldr,
+                 const gemm_half_t *W1, int ld1, long long stride1,
+                 const gemm_half_t *W2, int ld2, long long stride2,
+                 float beta, gemm_half_t *Y, int ldy,
+                 int *ids, float *weights,
+                 void *workspace, size_t workspace_bytes, void *stream);
+int gemm_moe_f32(int M, int D, int F, int E, int top_k, int renorm, float alpha,
+                 const float *X, int ldx,
+                 const float *Wr, int ldr,
+                 const float *W1, int ld1, long long stride1,
+                 const float *W2, int ld2, long long stride2,
+                 float beta, float *Y, int ldy,
+                 int *ids, float *weights,
+                 void *workspace, size_t workspace_bytes, void *stream);
+size_t gemm_moe_workspace(int dtype, int M, int D, int F, int E, int top_k);
 
 /* Static, human-readable text for a status code returned above (never NULL). */
 const char *gemm_status_string(int status);

@@ -1,0 +1,532 @@
+"""The products whose rows choose their own weights on the GPU: low-rank
+adapters beside a shared projection, their gradients and the
+mixture-of-experts layer, against 64-bit references within derived bounds."""
+import pytest
+import torch
+
+import rows_reference as ref
+from gemm_harness import note
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "f32": torch.float32}
+GPU = "cuda:0"
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, shape, dtype, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+def padded(t, pad, fill=float("nan")):
+    """A device copy of t (... x rows x cols) with `pad` elements of `fill`
+    after each row, and the view of t in it."""
+    big = torch.full(t.shape[:-1] + (t.shape[-1] + pad,), fill, dtype=t.dtype)
+    big[..., :t.shape[-1]] = t
+    big = big.to(GPU)
+    return big, big[..., :t.shape[-1]]
+
+
+def pads_intact(big, cols):
+    return bool(torch.isnan(big[..., cols:].float()).all()) if big.shape[-1] > cols else True
+
+
+def pattern(g, how, M, L):
+    """Adapter indices: segments, any order, none, or out of range among them."""
+    if how == "none":
+        return torch.full((M,), -1, dtype=torch.int32)
+    if how == "one":
+        return torch.full((M,), L - 1, dtype=torch.int32)
+    if how == "mixed":
+        return torch.randint(-1, L, (M,), generator=g).to(torch.int32)
+    if how == "wild":
+        v = torch.randint(-1, L, (M,), generator=g).to(torch.int32)
+        odd = torch.tensor([L, -7, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+        pick = torch.rand(M, generator=g) < 0.3
+        v[pick] = odd[torch.randint(0, 4, (int(pick.sum()),), generator=g)]
+        return v
+    cuts = torch.randint(0, L, (M // 21 + 1,), generator=g).to(torch.int32)
+    return cuts[torch.arange(M) // 21]
+
+
+def adapters(g, L, N, K, R, dtype, with_ranks):
+    A, B = normal(g, (L, R, K), dtype, K ** -0.5), normal(g, (L, N, R), dtype, 0.5)
+    scale = 0.25 + torch.rand(L, generator=g)
+    ranks = None
+    if with_ranks:
+        ranks = torch.randint(0, R + 3, (L,), generator=g).to(torch.int32)   # some beyond R
+        ranks[0] = 0
+        for a in range(L):                    # what is beyond the rank is never read
+            A[a, min(int(ranks[a]), R):] = float("nan")
+            B[a, :, min(int(ranks[a]), R):] = float("nan")
+    return A, B, scale, ranks
+
+
+LORA = [
+    # M, N, K, L, R, rows, pad, ranks, alpha, beta
+    (1, 64, 64, 1, 8, "one", 0, False, 1.0, 0.0),
+    (1, 1, 1, 1, 1, "one", 0, False, 1.0, 0.0),
+    (3, 5, 7, 2, 3, "mixed", 1, False, 1.5, -0.5),
+    (16, 256, 512, 16, 16, "mixed", 0, True, 1.0, 0.0),
+    (17, 130, 264, 40, 9, "wild", 8, True, 1.0, 1.0),
+    (48, 1024, 1024, 64, 16, "mixed", 0, True, 1.0, 0.0),
+    (64, 96, 2000, 3, 64, "segments", 0, False, 0.5, 0.0),
+    (65, 515, 333, 5, 12, "segments", 3, True, 1.0, 0.5),
+    (100, 300, 260, 4, 33, "none", 0, True, 1.0, 0.0),
+    (129, 128, 64, 7, 256, "mixed", 0, False, 1.0, 0.0),
+    (300, 520, 512, 6, 16, "segments", 0, True, 1.0, 0.0),
+    (513, 264, 72, 300, 4, "mixed", 8, True, 1.0, 1.0),
+    (700, 1032, 640, 8, 24, "wild", 0, True, -1.0, 0.25),
+    (1024, 2048, 256, 3, 32, "segments", 0, True, 1.0, 0.0),
+    (2100, 4160, 128, 5, 64, "segments", 0, True, 1.0, 0.0),
+    (2048, 4096, 192, 17, 16, "mixed", 0, True, 1.0, 1.0),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", LORA, ids=lambda c: "x".join(map(str, c[:5])) + c[5])
+def test_lora(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, N, K, L, R, how, pad, with_ranks, alpha, beta = case
+    note("lora %s %r" % (dt, case))
+    g, dtype = gen(M * 31 + N), DT[dt]
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, K ** -0.5)
+    A, B, scale, ranks = adapters(g, L, N, K, R, dtype, with_ranks)
+    rows = pattern(g, how, M, L)
+    Y = normal(g, (M, N), dtype) if beta else torch.full((M, N), float("nan"), dtype=dtype)
+    want, bound = ref.lora(X, W, A, B, rows, Y, scale, ranks, alpha, beta)
+    dX, dW, dA, dB = (padded(t, pad)[1] for t in (X, W, A, B))
+    big, dY = padded(Y, pad)
+    dg.lora(dX, dW, dA, dB, rows.to(GPU), dY, scale=scale.to(GPU),
+            ranks=None if ranks is None else ranks.to(GPU), alpha=alpha, beta=beta)
+    torch.cuda.synchronize()
+    assert ref.worst(dY, want, bound) <= 1.0
+    assert pads_intact(big, N)
+
+
+GRAD = [
+    # M, N, K, L, R, rows, pad, ranks, alpha, beta_x, beta_ab
+    (1, 64, 64, 1, 8, "one", 0, False, 1.0, 0.0, 0.0),
+    (1, 1, 1, 1, 1, "one", 0, False, 1.0, 0.0, 0.0),
+    (5, 3, 7, 2, 3, "mixed", 1, False, 1.5, -0.5, 1.0),
+    (33, 256, 512, 16, 16, "mixed", 0, True, 1.0, 0.0, 0.0),
+    (64, 130, 264, 40, 9, "wild", 8, True, 1.0, 1.0, 1.0),
+    (100, 300, 260, 4, 33, "none", 0, True, 1.0, 0.0, 0.5),
+    (129, 515, 333, 5, 12, "segments", 3, True, 1.0, 0.5, 0.0),
+    (257, 512, 640, 3, 8, "segments", 0, True, 1.0, 0.0, 0.0),
+    (300, 128, 64, 7, 256, "mixed", 0, False, 1.0, 0.0, 1.0),
+    (1000, 264, 1032, 1, 16, "one", 0, False, 2.0, 0.0, 0.0),
+    (1500, 640, 320, 6, 64, "segments", 0, True, 1.0, 1.0, 0.0),
+    (2050, 2048, 256, 2, 32, "segments", 0, True, 1.0, 0.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", GRAD, ids=lambda c: "x".join(map(str, c[:5])) + c[5])
+def test_lora_grad(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, N, K, L, R, how, pad, with_ranks, alpha, beta_x, beta_ab = case
+    note("lora_grad %s %r" % (dt, case))
+    g, dtype = gen(M * 37 + N), DT[dt]
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, K ** -0.5)
+    dY = normal(g, (M, N), dtype, 2.0 ** -6)
+    A, B, scale, ranks = adapters(g, L, N, K, R, dtype, with_ranks)
+    rows = pattern(g, how, M, L)
+
+    def old(shape, t, beta):
+        return normal(g, shape, t) if beta else torch.full(shape, float("nan"), dtype=t)
+    oX = old((M, K), dtype, beta_x)
+    oA, oB = old((L, R, K), torch.float32, beta_ab), old((L, N, R), torch.float32, beta_ab)
+    want = ref.lora_grad(dY, X, W, A, B, rows, oX, oA, oB, scale, ranks, alpha, beta_x, beta_ab)
+    gY, gX, gW, gA, gB = (padded(t, pad)[1] for t in (dY, X, W, A, B))
+    big = {n: padded(t, pad) for n, t in (("dX", oX), ("dA", oA), ("dB", oB))}
+    out = {n: v[1] for n, v in big.items()}
+    dg.lora_grad(gY, gX, gW, gA, gB, rows.to(GPU), scale=scale.to(GPU),
+                 ranks=None if ranks is None else ranks.to(GPU), alpha=alpha, beta_x=beta_x,
+                 beta_ab=beta_ab, **out)
+    torch.cuda.synchronize()
+    for n in ("dX", "dA", "dB"):
+        assert ref.worst(out[n], *want[n]) <= 1.0, n
+        assert pads_intact(big[n][0], out[n].shape[-1]), n
+    # each output alone is the same
+    for n in ("dX", "dA", "dB"):
+        one = padded({"dX": oX, "dA": oA, "dB": oB}[n], pad)[1]
+        dg.lora_grad(gY, gX, gW, gA, gB, rows.to(GPU), scale=scale.to(GPU),
+                     ranks=None if ranks is None else ranks.to(GPU), alpha=alpha, beta_x=beta_x,
+                     beta_ab=beta_ab, **{n: one})
+        assert torch.equal(one, out[n]), n
+
+
+def test_lora_grad_against_differences():
+    """<gradient, direction> against central differences of the 64-bit
+    forward; Y is linear in X and in A and B each, so a difference is exact up
+    to its own rounding (1e-16 / step of 2^-10)."""
+    import dense_gemm_fp32_amd as dg
+    M, N, K, L, R = 70, 48, 40, 3, 5
+    note("lora_grad differences")
+    g = gen(9)
+    X, W = normal(g, (M, K), torch.float32), normal(g, (N, K), torch.float32, K ** -0.5)
+    A, B, scale, _ = adapters(g, L, N, K, R, torch.float32, False)
+    rows = pattern(g, "mixed", M, L)
+    dY = normal(g, (M, N), torch.float32)
+    o = {"dX": torch.empty(M, K), "dA": torch.empty(L, R, K), "dB": torch.empty(L, N, R)}
+    want = ref.lora_grad(dY, X, W, A, B, rows, None, None, None, scale, None, 1.0, 0, 0)
+    o = {n: t.to(GPU) for n, t in o.items()}
+    dg.lora_grad(dY.to(GPU), X.to(GPU), W.to(GPU), A.to(GPU), B.to(GPU), rows.to(GPU),
+                 scale=scale.to(GPU), **o)
+    torch.cuda.synchronize()
+    h = 2.0 ** -10
+    for n, at in (("dX", 0), ("dA", 2), ("dB", 3)):
+        args = [X.double(), W.double(), A.double(), B.double()]
+        d = torch.randn(args[at].shape, generator=g).double()
+
+        def loss(sign):
+            moved = list(args)
+            moved[at] = args[at] + sign * h * d
+            return float((ref.lora(*moved, rows, None, scale, None, 1.0, 0)[0] * dY.double()).sum())
+        diff = (loss(1) - loss(-1)) / (2 * h)
+        got = float((o[n].double().cpu() * d).sum())
+        slack = float((want[n][1] * d.abs()).sum()) + 1e-9 * abs(diff) + 1e-9
+        assert abs(got - diff) <= slack, n
+
+
+def test_lora_keeps_infinities_with_their_rows():
+    """An infinity or NaN in one adapter, or in one row of X, reaches no other row."""
+    import dense_gemm_fp32_amd as dg
+    for dt in ("f16", "f32"):
+        for M in (20, 400):
+            note("lora inf %s %d" % (dt, M))
+            g, dtype = gen(5), DT[dt]
+            N, K, L, R = 200, 96, 4, 16
+            X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, 0.1)
+            A, B, scale, _ = adapters(g, L, N, K, R, dtype, False)
+            rows = pattern(g, "mixed", M, L)
+            clean = torch.empty(M, N, dtype=dtype, device=GPU)
+            up = [t.to(GPU) for t in (X, W, A, B)]
+            dg.lora(*up, rows.to(GPU), clean, scale=scale.to(GPU))
+            A[1, 3, 5], B[2, 7, 4], X[11, 2] = float("inf"), float("nan"), float("nan")
+            got = torch.empty(M, N, dtype=dtype, device=GPU)
+            dg.lora(X.to(GPU), up[1], A.to(GPU), B.to(GPU), rows.to(GPU), got,
+                    scale=scale.to(GPU))
+            clean, got = clean.cpu(), got.cpu()
+            for i in range(M):
+                if i == 11:
+                    assert got[i].isnan().all()
+                elif rows[i] == 1:
+                    assert not got[i].isfinite().any()
+                elif rows[i] == 2:
+                    keep = torch.arange(N) != 7
+                    assert got[i, 7].isnan() and torch.equal(got[i, keep], clean[i, keep])
+                else:
+                    assert torch.equal(got[i], clean[i])
+
+
+def test_lora_large_intermediate():
+    """A x beyond fp16's range, and far below it, with B the other way round."""
+    import dense_gemm_fp32_amd as dg
+    for M in (7, 300):
+        for up in (2.0 ** 13, 2.0 ** -12):
+            note("lora range %d %g" % (M, up))
+            g = gen(6)
+            N, K, L, R = 128, 256, 2, 16
+            X, W = normal(g, (M, K), torch.float16), normal(g, (N, K), torch.float16, 0.05)
+            A = normal(g, (L, R, K), torch.float16, up)
+            B = normal(g, (L, N, R), torch.float16, min(1.0 / up, 2.0 ** 8) / 64)
+            rows, Y = pattern(g, "mixed", M, L), torch.empty(M, N, dtype=torch.float16)
+            want, bound = ref.lora(X, W, A, B, rows, Y, None, None, 1.0, 0)
+            Y = Y.to(GPU)
+            dg.lora(X.to(GPU), W.to(GPU), A.to(GPU), B.to(GPU), rows.to(GPU), Y)
+            assert ref.worst(Y, want, bound) <= 1.0
+
+
+def test_lora_strides_of_adapters():
+    """Adapters as slices of a larger pool, and one shared by all (stride 0)."""
+    import dense_gemm_fp32_amd as dg
+    g, dtype = gen(8), torch.float16
+    M, N, K, L, R = 40, 96, 128, 3, 8
+    note("lora strides")
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, 0.1)
+    pool_a, pool_b = normal(g, (L, R + 5, K), dtype, 0.1), normal(g, (L, N, 2 * R), dtype)
+    rows = pattern(g, "mixed", M, L)
+    for A, B in ((pool_a[:, 2:2 + R], pool_b[:, :, 3:3 + R]),
+                 (pool_a[:1, :R].expand(L, R, K), pool_b[:1, :, :R].expand(L, N, R))):
+        want, bound = ref.lora(X, W, A, B, rows, None, None, None, 1.0, 0)
+        Y = torch.empty(M, N, dtype=dtype, device=GPU)
+        ga, gb = pool_a.to(GPU), pool_b.to(GPU)
+        gA = ga[:, 2:2 + R] if A.stride(0) else ga[:1, :R].expand(L, R, K)
+        gB = gb[:, :, 3:3 + R] if B.stride(0) else gb[:1, :, :R].expand(L, N, R)
+        dg.lora(X.to(GPU), W.to(GPU), gA, gB, rows.to(GPU), Y)
+        assert ref.worst(Y, want, bound) <= 1.0
+
+
+MOE = [
+    # M, D, F, E, top_k, pad, renorm, alpha, beta
+    (1, 64, 64, 4, 2, 0, True, 1.0, 0.0),
+    (1, 1, 1, 1, 1, 0, True, 1.0, 0.0),
+    (1, 1024, 512, 8, 2, 0, False, 1.0, 0.0),
+    (2, 40, 24, 5, 5, 1, True, 0.5, 1.0),
+    (3, 129, 67, 70, 8, 3, False, 1.0, -0.5),
+    (5, 1001, 499, 16, 3, 2, True, 1.0, 0.0),
+    (16, 512, 256, 64, 6, 0, True, 1.0, 1.0),
+    (17, 96, 200, 3, 1, 8, True, 1.0, 0.0),
+    (33, 256, 128, 2, 2, 0, True, 1.0, 0.0),
+    (64, 320, 192, 130, 4, 0, False, 1.0, 0.0),
+    (100, 72, 80, 9, 3, 8, True, 1.0, 0.0),
+    (256, 64, 48, 6, 2, 0, True, 2.0, 0.0),
+    (256, 128, 32, 200, 8, 0, True, 1.0, 1.0),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", MOE, ids=lambda c: "x".join(map(str, c[:5])))
+def test_moe(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, D, F, E, k, pad, renorm, alpha, beta = case
+    note("moe %s %r" % (dt, case))
+    g, dtype = gen(M * 41 + D), DT[dt]
+    X, router = normal(g, (M, D), dtype), normal(g, (E, D), dtype, 1.5 * D ** -0.5)
+    W1, W2 = normal(g, (E, 2 * F, D), dtype, D ** -0.5), normal(g, (E, D, F), dtype, F ** -0.5)
+    Y = normal(g, (M, D), dtype) if beta else torch.full((M, D), float("nan"), dtype=dtype)
+    want, bound, ids, w, dw = ref.moe(X, router, W1, W2, k, Y, renorm, alpha, beta)
+    gX, gr, g1, g2 = (padded(t, pad)[1] for t in (X, router, W1, W2))
+    big, gY = padded(Y, pad)
+    gi = torch.full((M, k), -9, dtype=torch.int32, device=GPU)
+    gw = torch.full((M, k), float("nan"), device=GPU)
+    dg.moe(gX, gr, g1, g2, k, gY, renorm=renorm, alpha=alpha, beta=beta, ids=gi, weights=gw)
+    torch.cuda.synchronize()
+    assert torch.equal(gi.cpu().long(), ids)
+    assert ref.worst(gw, w, dw) <= 1.0
+    assert ref.worst(gY, want, bound) <= 1.0
+    assert pads_intact(big, D)
+    # without the optional outputs
+    again = padded(Y, pad)[1]
+    dg.moe(gX, gr, g1, g2, k, again, renorm=renorm, alpha=alpha, beta=beta)
+    assert torch.equal(again, gY)
+
+
+def test_moe_ties_and_odd_logits():
+    """Equal logits go to the lowest index; a NaN logit is chosen last; NaN in
+    one token, or in an expert that nobody chose, stays there."""
+    import dense_gemm_fp32_amd as dg
+    for dt in ("f16", "f32"):
+        note("moe ties " + dt)
+        g, dtype = gen(12), DT[dt]
+        M, D, F, E, k = 6, 64, 32, 12, 4
+        X, router = normal(g, (M, D), dtype), normal(g, (E, D), dtype, 0.2)
+        router[3:9] = router[2]                       # seven equal logits a token
+        router[10] = float("nan")                     # never among the first four
+        W1, W2 = normal(g, (E, 2 * F, D), dtype, 0.1), normal(g, (E, D, F), dtype, 0.1)
+        W1[10], W2[10] = float("nan"), float("nan")
+        want, bound, ids, w, dw = ref.moe(X, router, W1, W2, k, None, True, 1.0, 0)
+        unused = [e for e in range(E) if not (ids == e).any()]
+        for e in unused:
+            W1[e], W2[e] = float("inf"), float("nan")
+        X2 = torch.cat([X, torch.full((1, D), float("nan"), dtype=dtype)])
+        Y = torch.empty(M + 1, D, dtype=dtype, device=GPU)
+        gi = torch.empty(M + 1, k, dtype=torch.int32, device=GPU)
+        dg.moe(X2.to(GPU), router.to(GPU), W1.to(GPU), W2.to(GPU), k, Y, ids=gi)
+        assert torch.equal(gi[:M].cpu().long(), ids)
+        assert gi[M].tolist() == [0, 1, 2, 3]         # all NaN: equals
+        assert ref.worst(Y[:M], want, bound) <= 1.0
+        assert Y[M].isnan().all()
+
+
+def test_moe_large_hidden_values():
+    """silu(g) * u beyond fp16's range does not overflow inside the layer."""
+    import dense_gemm_fp32_amd as dg
+    note("moe range")
+    g = gen(13)
+    for M in (2, 40):
+        D, F, E, k = 64, 96, 4, 2
+        X, router = normal(g, (M, D), torch.float16, 8.0), normal(g, (E, D), torch.float16, 0.02)
+        W1 = normal(g, (E, 2 * F, D), torch.float16, 16.0)
+        W2 = normal(g, (E, D, F), torch.float16, 2.0 ** -12)
+        want, bound, ids, _, _ = ref.moe(X, router, W1, W2, k, None, True, 1.0, 0)
+        Y = torch.empty(M, D, dtype=torch.float16, device=GPU)
+        dg.moe(X.to(GPU), router.to(GPU), W1.to(GPU), W2.to(GPU), k, Y)
+        assert ref.worst(Y, want, bound) <= 1.0
+
+
+def three_calls(dg, s, ws=None):
+    """A step as it is used: adapters beside a projection, then the expert layer
+    added to the residual, then the adapters' gradients."""
+    ws = ws or {}
+    dg.lora(s["X"], s["W"], s["A"], s["B"], s["rows"], s["Y"], scale=s["scale"],
+            workspace=ws.get("lora"))
+    s["Z"].copy_(s["Y"])
+    dg.moe(s["Y"], s["router"], s["W1"], s["W2"], 2, s["Z"], beta=1.0, ids=s["ids"],
+           workspace=ws.get("moe"))
+    dg.lora_grad(s["Z"], s["X"], s["W"], s["A"], s["B"], s["rows"], dX=s["dX"], dA=s["dA"],
+                 dB=s["dB"], scale=s["scale"], workspace=ws.get("grad"))
+
+
+OUT = ("Y", "Z", "ids", "dX", "dA", "dB")
+
+
+def step_state(seed, dtype=torch.float16, M=40, N=128, K=96, L=3, R=8, E=6, F=64):
+    g = gen(seed)
+    s = {"X": normal(g, (M, K), dtype), "W": normal(g, (N, K), dtype, K ** -0.5),
+         "router": normal(g, (E, N), dtype, 0.2), "W1": normal(g, (E, 2 * F, N), dtype, 0.1),
+         "W2": normal(g, (E, N, F), dtype, 0.1), "rows": pattern(g, "mixed", M, L)}
+    s["A"], s["B"], s["scale"], _ = adapters(g, L, N, K, R, dtype, False)
+    for n, shape, t in (("Y", (M, N), dtype), ("Z", (M, N), dtype), ("ids", (M, 2), torch.int32),
+                        ("dX", (M, K), dtype), ("dA", (L, R, K), torch.float32),
+                        ("dB", (L, N, R), torch.float32)):
+        s[n] = torch.zeros(shape, dtype=t)
+    return {n: t.to(GPU) for n, t in s.items()}
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_step_together(dt):
+    """The three calls in a row, against the references fed with each other's
+    actual results."""
+    import dense_gemm_fp32_amd as dg
+    note("step " + dt)
+    s = step_state(21, DT[dt])
+    three_calls(dg, s)
+    torch.cuda.synchronize()
+    c = {n: t.cpu() for n, t in s.items()}
+    assert ref.worst(c["Y"], *ref.lora(c["X"], c["W"], c["A"], c["B"], c["rows"], None,
+                                       c["scale"], None, 1.0, 0)) <= 1.0
+    want, bound, ids, _, _ = ref.moe(c["Y"], c["router"], c["W1"], c["W2"], 2, c["Y"], True, 1.0,
+                                     1.0)
+    assert torch.equal(c["ids"].long(), ids)
+    assert ref.worst(c["Z"], want, bound) <= 1.0
+    grads = ref.lora_grad(c["Z"], c["X"], c["W"], c["A"], c["B"], c["rows"], None, None, None,
+                          c["scale"], None, 1.0, 0, 0)
+    for n in ("dX", "dA", "dB"):
+        assert ref.worst(c[n], *grads[n]) <= 1.0, n
+
+
+def snapshot(s):
+    torch.cuda.synchronize()
+    return {n: s[n].clone() for n in OUT}
+
+
+def equal(a, b):
+    return all(torch.equal(a[n], b[n]) for n in OUT)
+
+
+def test_repeats_streams_and_workspaces():
+    """The same bits on every call, on another stream, with a workspace full of
+    NaN, one from the library's pool, and two streams at once."""
+    import dense_gemm_fp32_amd as dg
+    note("repeats")
+    s, t = step_state(31), step_state(32)
+    three_calls(dg, s)
+    three_calls(dg, t)
+    want_s, want_t = snapshot(s), snapshot(t)
+    M, N, K, L, R, E, F = 40, 128, 96, 3, 8, 6, 64
+    size = {"lora": dg.gemm_lora_workspace(1, M, N, K, L, R),
+            "grad": dg.gemm_lora_grad_workspace(1, M, N, K, L, R),
+            "moe": dg.gemm_moe_workspace(1, M, N, F, E, 2)}
+    ws = {n: torch.full((b,), 0xFF, dtype=torch.uint8, device=GPU) for n, b in size.items()}
+    three_calls(dg, s, ws)
+    assert equal(snapshot(s), want_s)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(one):
+            three_calls(dg, s)
+        with torch.cuda.stream(two):
+            three_calls(dg, t)
+    assert equal(snapshot(s), want_s) and equal(snapshot(t), want_t)
+    s["Y"].zero_()
+    torch.cuda.synchronize()
+    dg.lora(s["X"], s["W"], s["A"], s["B"], s["rows"], s["Y"], scale=s["scale"], stream=one)
+    torch.cuda.synchronize()
+    assert torch.equal(s["Y"], want_s["Y"])
+
+
+def test_captured_graphs():
+    """Two graphs of the step, replayed in turn with eager work between, give the
+    eager bits each time, with inputs changed in place."""
+    import dense_gemm_fp32_amd as dg
+    note("graphs")
+    states, graphs = [step_state(41), step_state(42)], []
+    side = torch.cuda.Stream()
+    for s in states:
+        with torch.cuda.stream(side):
+            three_calls(dg, s)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            three_calls(dg, s)
+        graphs.append(g)
+    for turn in range(4):
+        want = []
+        for i, s in enumerate(states):
+            fresh = step_state(100 + 10 * turn + i)
+            for n in ("X", "W", "A", "B", "rows", "scale", "router", "W1", "W2"):
+                s[n].copy_(fresh[n])
+            three_calls(dg, fresh)
+            want.append(snapshot(fresh))
+            for n in OUT:
+                s[n].zero_()
+        for g in graphs:
+            g.replay()
+        for s, w in zip(states, want):
+            assert equal(snapshot(s), w), turn
+
+
+def test_refusals_on_the_gpu():
+    """A workspace that is too small or cannot be had is refused before any work."""
+    import dense_gemm_fp32_amd as dg
+    note("refusals")
+    s = step_state(51)
+    s["Y"].fill_(7.0)
+    small = torch.empty(128, dtype=torch.uint8, device=GPU)
+    with pytest.raises(dg.GemmError) as e:
+        dg.lora(s["X"], s["W"], s["A"], s["B"], s["rows"], s["Y"], workspace=small)
+    assert e.value.status == -324
+    before = dg.gemm_set_workspace_limit(0)
+    try:
+        with pytest.raises(dg.GemmError) as e:
+            dg.lora(s["X"], s["W"], s["A"], s["B"], s["rows"], s["Y"],
+                    stream=torch.cuda.current_stream())
+        assert e.value.status == dg.GEMM_ERR_NO_WORKSPACE
+    finally:
+        dg.gemm_set_workspace_limit(before)
+    torch.cuda.synchronize()
+    assert bool((s["Y"] == 7.0).all())
+    for bad in (dict(W=s["W"].cpu()), dict(A=s["A"].float()), dict(rows=s["rows"].long()),
+                dict(X=s["X"].t()), dict(Y=s["Y"][:, :5])):
+        a = {n: s[n] for n in ("X", "W", "A", "B", "rows", "Y")}
+        a.update(bad)
+        with pytest.raises(ValueError):
+            dg.lora(*a.values())
+
+
+def test_empty_products():
+    """No rows, no adapters, rank 0, alpha 0: outputs are scaled or the plain
+    product."""
+    import dense_gemm_fp32_amd as dg
+    note("empty")
+    for dt in ("f16", "f32"):
+        dtype = DT[dt]
+        s = step_state(61, dtype)
+        plain = torch.empty_like(s["Y"])
+        dg.gemm(s["X"], s["W"].t(), plain)
+        for A, B in ((s["A"][:0], s["B"][:0]), (s["A"][:, :0], s["B"][:, :, :0])):
+            dg.lora(s["X"], s["W"], A, B, s["rows"], s["Y"])
+            assert torch.equal(s["Y"], plain)
+        s["Y"].fill_(3.0)
+        dg.lora(s["X"], s["W"], s["A"], s["B"], s["rows"], s["Y"], alpha=0.0, beta=0.5)
+        assert bool((s["Y"] == 1.5).all())
+        for alpha, M in ((0.0, 40), (1.0, 0)):
+            for n in ("dX", "dA", "dB"):
+                s[n].fill_(2.0)
+            dg.lora_grad(s["Y"][:M], s["X"][:M], s["W"], s["A"], s["B"], s["rows"][:M],
+                         dX=s["dX"][:M], dA=s["dA"], dB=s["dB"], alpha=alpha, beta_x=0.5,
+                         beta_ab=0.25)
+            assert bool((s["dX"][:M] == 1.0).all())
+            assert bool((s["dA"] == 0.5).all()) and bool((s["dB"] == 0.5).all())
+        s["Z"].fill_(4.0)
+        dg.moe(s["Y"], s["router"], s["W1"], s["W2"], 2, s["Z"], alpha=0.0, beta=0.25)
+        assert bool((s["Z"] == 1.0).all())
+        dg.moe(s["Y"][:0], s["router"], s["W1"], s["W2"], 2, s["Z"][:0])

@@ -142,7 +142,6 @@ int run_gemm(int kind, bool ta, bool tb, int M, int N, int K, float alpha, const
 
 namespace dgemm {
 long long workspace_limit() { return g_ws_limit.load(std::memory_order_relaxed); }
-bool force_scalar_loads() { return g_load_mode.load(std::memory_order_relaxed) == 1; }
 }  // namespace dgemm
 
 extern "C" {

@@ -235,7 +235,6 @@ struct LoraCall {
   float *dB;
   int lddb;
   long long stride_db;
-  bool force_scalar;
   hipStream_t stream;
 };
 size_t lora_workspace(const LoraCall &c);
@@ -268,7 +267,6 @@ struct MoeCall {
   int ldy;
   int *ids;
   float *weights;
-  bool force_scalar;
   hipStream_t stream;
 };
 constexpr int kMoeMaxTokens = 256;
@@ -276,9 +274,8 @@ constexpr int kMoeMaxExperts = 1024;
 size_t moe_workspace(const MoeCall &c);
 hipError_t launch_moe(const MoeCall &c, void *ws);
 
-// The process-wide switches the calls above go by (api.hip).
+// The process-wide switch the calls above go by (api.hip).
 long long workspace_limit();
-bool force_scalar_loads();
 
 inline bool aligned_to(const void *p, uintptr_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) % bytes) == 0;

@@ -34,7 +34,6 @@ struct ShrinkParams {
   const int *rows, *ranks;
   long long stride;
   int M, K, L, R, Rp, ldx, ldw;
-  int vec_x, vec_w;
 };
 
 // V[16 rows, 16 ranks] per workgroup and distinct adapter among the rows; the
@@ -68,9 +67,9 @@ __global__ __launch_bounds__(kShrinkThreads) void lora_shrink(ShrinkParams p) {
 #pragma unroll 4
     for (int k = wave * KS; k < p.K; k += kShrinkWaves * KS) {
       const int kk = k + lg * El<T>::VEC;
-      const Frag x = load_frag<T>(xrow, kk, p.K, p.vec_x);
+      const Frag x = load_frag(xrow, kk, p.K);
       Frag b;
-      if constexpr (KMAJ) b = load_frag<T>(w + (size_t)r * p.ldw, kk, p.K, p.vec_w);
+      if constexpr (KMAJ) b = load_frag(w + (size_t)r * p.ldw, kk, p.K);
       else b = load_frag_strided<T>(w + r, p.ldw, kk, p.K);
       acc = mma16(x, b, acc);
     }
@@ -327,11 +326,6 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 int rank_pad(int R) { return (R + 15) / 16 * 16; }
 
-template <typename T>
-bool rows16(const void *p, int ld) {
-  return ld % El<T>::VEC == 0 && aligned_to(p, 16);
-}
-
 template <typename T, bool KMAJ>
 hipError_t shrink(const LoraCall &c, const void *X, int ldx, int K, const void *W, int ldw,
                   long long stride, float *V) {
@@ -349,8 +343,6 @@ hipError_t shrink(const LoraCall &c, const void *X, int ldx, int K, const void *
   p.Rp = rank_pad(c.R);
   p.ldx = ldx;
   p.ldw = ldw;
-  p.vec_x = !c.force_scalar && rows16<T>(X, ldx);
-  p.vec_w = !c.force_scalar && rows16<T>(W, ldw) && stride % El<T>::VEC == 0;
   const int blocks = (c.M + 15) / 16;
   const int z = c.L < 16 ? c.L : 16;
   hipLaunchKernelGGL((lora_shrink<T, KMAJ>),

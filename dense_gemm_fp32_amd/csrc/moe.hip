@@ -24,33 +24,44 @@ namespace {
 
 // ---------------------------------------------------------------- router
 
-// l[t, e] for 4 experts (one a wave) x 4 tokens a workgroup.  Products of
-// halves are exact in fp32, products of floats in fp64.
+// l[t, e] for one expert and 4 tokens a workgroup, whose 4 waves divide D.
+// Products of halves are exact in fp32, products of floats in fp64.  The
+// workgroups also clear `top` for the next launch.
 template <typename T>
 __global__ __launch_bounds__(256) void moe_logits(const T *X, int ldx, const T *Wr, int ldr, int M,
-                                                  int D, int E, int vec, double *logits) {
+                                                  int D, int E, double *logits, unsigned *top,
+                                                  int pairs) {
+  __shared__ double part[4][4];
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < pairs; i += 256) top[i] = 0u;
   const int lane = threadIdx.x % kWave, wave = wave_id();
-  const int e = blockIdx.x * 4 + wave, t0 = blockIdx.y * 4;
-  if (e >= E) return;
+  const int e = blockIdx.x, t0 = blockIdx.y * 4;
   const T *w = Wr + (size_t)e * (size_t)ldr;
   const T *x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = X + (size_t)(t0 + i < M ? t0 + i : M - 1) * (size_t)ldx;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
-  for (int k = lane * El<T>::VEC; k < D; k += kWave * El<T>::VEC) {
-    const typename El<T>::Frag wf = load_frag<T>(w, k, D, vec);
+#pragma unroll 2
+  for (int k = threadIdx.x * El<T>::VEC; k < D; k += 256 * El<T>::VEC) {
+    const typename El<T>::Frag wf = load_frag(w, k, D);
+    typename El<T>::Frag xf[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const typename El<T>::Frag xf = load_frag<T>(x[i], k, D, vec);
+    for (int i = 0; i < 4; ++i) xf[i] = load_frag(x[i], k, D);
 #pragma unroll
-      for (int j = 0; j < El<T>::VEC; ++j) s[i] += (double)wf[j] * (double)xf[j];
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < El<T>::VEC; ++j) s[i] += (double)wf[j] * (double)xf[i][j];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s[i] += __shfl_xor(s[i], o);
-    if (lane == 0 && t0 + i < M) logits[(size_t)(t0 + i) * E + e] = s[i];
+    if (lane == 0) part[wave][i] = s[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < 4 && t0 + (int)threadIdx.x < M) {
+    const int i = threadIdx.x;
+    logits[(size_t)(t0 + i) * E + e] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
   }
 }
 
@@ -63,40 +74,59 @@ struct MoeParams {
   float *prob;            // M x k: each choice's exp(l - max), over their sum unless renorm
   int *count, *list;      // tokens of expert e; their pairs t*k + choice: list[e*M ..]
   float *H;               // M*k x F
+  unsigned *top;          // M*k: bits of the largest |H| of the row
   void *Y;
   int *ids;
   float *weights;
   long long stride1, stride2;
   int M, D, F, E, k, renorm;
   int ldx, ld1, ld2, ldy;
-  int vec_x, vec_1, vec_2;
   float alpha, beta;
 };
 
 // ---------------------------------------------------------------- gate and up
 
-// grid: (ceil(F/16), E), 4 waves.
-template <typename T>
-__global__ __launch_bounds__(256) void moe_up(MoeParams p) {
+constexpr int kUpWaves = 4;
+
+// grid: (ceil(F / (8 NF)), E), 4 waves that divide D.  NF blocks of 16 weight
+// rows: 8 NF of the gate's and the same 8 NF of the up projection's; NB blocks
+// of 16 tokens at a time.
+template <typename T, int NF, int NB>
+__global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
   __shared__ int rank[kMoeMaxTokens];
   __shared__ int pairs[kMoeMaxTokens];
   __shared__ int total;
-  __shared__ float red[2][4][16][17];
-  typedef typename El<T>::Frag Frag;
+  __shared__ float red[kUpWaves][16 * NF][17];
   constexpr int KS = El<T>::KSTEP;
+  constexpr int FS = 8 * NF;
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
-  const int f0 = blockIdx.x * 16, e = blockIdx.y;
-  for (int t = wave; t < p.M; t += 4) {
-    const double *l = p.logits + (size_t)t * p.E;
-    const double mine = logit_key(l[e]);
-    int larger = 0;
+  const int f0 = blockIdx.x * FS, e = blockIdx.y;
+  // four tokens a wave at a time, so that their logits are on the way together
+  for (int t0 = 4 * wave; t0 < p.M; t0 += 4 * kUpWaves) {
+    const double *l[4];
+    double mine[4];
+    int larger[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      l[i] = p.logits + (size_t)(t0 + i < p.M ? t0 + i : p.M - 1) * p.E;
+      mine[i] = logit_key(l[i][e]);
+      larger[i] = 0;
+    }
     for (int j0 = 0; j0 < p.E; j0 += kWave) {
       const int j = j0 + lane;
-      const double v = j < p.E ? logit_key(l[j]) : 0.0;
-      larger += __popcll(__ballot(j < p.E && (v > mine || (v == mine && j < e))));
+      double v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = l[i][j < p.E ? j : p.E - 1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const double k = logit_key(v[i]);
+        larger[i] += __popcll(__ballot(j < p.E && (k > mine[i] || (k == mine[i] && j < e))));
+      }
     }
-    if (lane == 0) rank[t] = larger < p.k ? larger : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lane == 0 && t0 + i < p.M) rank[t0 + i] = larger[i] < p.k ? larger[i] : -1;
   }
   __syncthreads();
   if (wave == 0) {
@@ -114,8 +144,8 @@ __global__ __launch_bounds__(256) void moe_up(MoeParams p) {
   const int n = total;
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) p.count[e] = n;
-    for (int i = threadIdx.x; i < n; i += 256) p.list[(size_t)e * p.M + i] = pairs[i];
-    for (int i = wave; i < n; i += 4) {
+    for (int i = threadIdx.x; i < n; i += kUpWaves * kWave) p.list[(size_t)e * p.M + i] = pairs[i];
+    for (int i = wave; i < n; i += kUpWaves) {
       const int t = pairs[i] / p.k;
       const double *l = p.logits + (size_t)t * p.E;
       double top = -__builtin_inf();
@@ -137,65 +167,172 @@ __global__ __launch_bounds__(256) void moe_up(MoeParams p) {
     }
   }
   if (n == 0) return;
-  const int f = f0 + li < p.F ? f0 + li : p.F - 1;
   const T *w1 = static_cast<const T *>(p.W1) + (size_t)e * (size_t)p.stride1;
-  const T *wg = w1 + (size_t)f * (size_t)p.ld1;
-  const T *wu = w1 + (size_t)(p.F + f) * (size_t)p.ld1;
-  for (int i0 = 0; i0 < n; i0 += 16) {
-    const int t = pairs[i0 + li < n ? i0 + li : n - 1] / p.k;
-    const T *x = static_cast<const T *>(p.X) + (size_t)t * (size_t)p.ldx;
-    f32x4 g = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, u = g;
-#pragma unroll 4
-    for (int k = wave * KS; k < p.D; k += 4 * KS) {
-      const int kk = k + lg * El<T>::VEC;
-      const Frag xf = load_frag<T>(x, kk, p.D, p.vec_x);
-      g = mma16(load_frag<T>(wg, kk, p.D, p.vec_1), xf, g);
-      u = mma16(load_frag<T>(wu, kk, p.D, p.vec_1), xf, u);
-    }
+  const T *w[NF];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      red[0][wave][li][4 * lg + j] = g[j];
-      red[1][wave][li][4 * lg + j] = u[j];
-    }
-    __syncthreads();
-    const int c = threadIdx.x / 16, r = threadIdx.x % 16;
-    if (i0 + c < n && f0 + r < p.F) {
-      float gs = 0.0f, us = 0.0f;
+  for (int b = 0; b < NF; ++b) {
+    // row 16b + li of the workgroup's: the first half gate rows, the rest up rows
+    const int r = 16 * b + li;
+    const int f = f0 + (r < FS ? r : r - FS);
+    w[b] = w1 + (size_t)((r < FS ? 0 : p.F) + (f < p.F ? f : p.F - 1)) * (size_t)p.ld1;
+  }
+  // each wave a stretch of D, whole steps (of at least 128 bytes a row) long
+  constexpr int G = 2 * KS;
+  const int part = ((p.D + kUpWaves - 1) / kUpWaves + G - 1) / G * G;
+  const int k0 = wave * part;
+  const int k1 = k0 + part < p.D ? k0 + part : p.D;
+  for (int i0 = 0; i0 < n; i0 += 16 * NB) {
+    RowLoader<T, NB> x;
+    x.lim = k1;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        gs += red[0][w][c][r];
-        us += red[1][w][c][r];
+    for (int b = 0; b < NB; ++b) {
+      const int i = i0 + 16 * b + li;
+      x.row[b] = static_cast<const T *>(p.X) + (size_t)(pairs[i < n ? i : n - 1] / p.k) * (size_t)p.ldx;
+    }
+    f32x4 acc[NF][NB];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[f][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    stream_mac<T, (NF * NB >= 8 ? 2 : 4)>(w, k0, k1, k1, k1, x, acc);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (i0 + 16 * b >= n) break;
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) red[wave][16 * f + 4 * lg + j][li] = acc[f][b][j];
+      __syncthreads();
+      // 8 lanes share a token: a row's largest |h| takes one atomic per 8 f
+      for (int q = threadIdx.x; q < 16 * FS; q += kUpWaves * kWave) {
+        const int c = q / 8 % 16, r = q % 8 + q / 128 * 8;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kUpWaves; ++v) {
+          g += red[v][r][c];
+          u += red[v][FS + r][c];
+        }
+        const int i = i0 + 16 * b + c;
+        const bool ok = i < n && f0 + r < p.F;
+        const float h = g / (1.0f + expf(-g)) * u;
+        const int pair = pairs[i < n ? i : n - 1];
+        if (ok) p.H[(size_t)pair * p.F + f0 + r] = h;
+        if constexpr (sizeof(T) == 2) {
+          unsigned m = ok ? __builtin_bit_cast(unsigned, fabsf(h)) : 0u;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) {
+            const unsigned v = __shfl_xor(m, o);
+            m = m > v ? m : v;
+          }
+          if (r % 8 == 0 && m != 0u) atomicMax(&p.top[pair], m);
+        }
       }
-      p.H[(size_t)pairs[i0 + c] * p.F + f0 + r] = gs / (1.0f + expf(-gs)) * us;
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------- down and weighted sum
 
-// grid: ceil(D/16), 4 waves; dynamic LDS: 4 x M x 16 floats.
+// Power of two that brings a row whose largest magnitude has these bits to
+// [2^14, 2^15) as fp16, and its inverse (1 for a row of zeros, infinities or
+// NaN); its exponent, at least -100.
+__device__ __forceinline__ int row_exponent(unsigned bits) {
+  const int e = (int)(bits >> 23);
+  if (e == 0 || e == 255) return 0;
+  return e - 141 > -100 ? e - 141 : -100;
+}
+
+// A row of H as fragments of T: for fp16, scaled by the row's power of two
+// and rounded to 11 bits (those of every value within 2^-28 of the row's
+// largest).
 template <typename T>
-__global__ __launch_bounds__(256) void moe_down(MoeParams p) {
-  __shared__ int act[kMoeMaxExperts];
+struct HiddenLoader;
+
+template <>
+struct HiddenLoader<_Float16> {
+  struct Raw {
+    f32x4 a, b;
+  };
+  const float *row;
+  int lim;
+  float down;
+  __device__ __forceinline__ Raw whole(int, int k) const {
+    return Raw{load_whole(row + k), load_whole(row + k + 4)};
+  }
+  __device__ __forceinline__ Raw masked(int, int k) const {
+    return Raw{load_frag(row, k, lim), load_frag(row, k + 4, lim)};
+  }
+  __device__ __forceinline__ f16x8 frag(const Raw &r) const {
+    f16x8 f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = (_Float16)(r.a[j] * down);
+      f[4 + j] = (_Float16)(r.b[j] * down);
+    }
+    return f;
+  }
+};
+
+template <>
+struct HiddenLoader<float> {
+  typedef f32x4 Raw;
+  const float *row;
+  int lim;
+  float down;
+  __device__ __forceinline__ Raw whole(int, int k) const { return load_whole(row + k); }
+  __device__ __forceinline__ Raw masked(int, int k) const { return load_frag(row, k, lim); }
+  __device__ __forceinline__ f32x4 frag(const Raw &r) const { return r; }
+};
+
+// grid: ceil(D/ROWS), NW waves.  The work items are (chosen expert, part of F),
+// dealt to the waves in turn; a wave multiplies its rows of W2 by the expert's
+// tokens and adds the weighted result to its own copy of the ROWS x M outputs
+// in LDS, which are summed in wave order at the end.
+//
+// ROWS = 16 is the matrix instruction's own shape.  ROWS = 8, for layers that
+// make too few workgroups of 16, puts two halves of the item's k into one
+// instruction: lanes 8..15 of each 16 hold the same 8 weight rows, and the
+// same 8 tokens, at the second half's k; of the 16 x 16 products the two 8 x 8
+// blocks on the diagonal are the halves' sums, and the rest is dropped.
+// Dynamic LDS: NW x M x ROWS floats, then M*k pair numbers.
+template <typename T, int NW, int ROWS>
+__global__ __launch_bounds__(NW *kWave) void moe_down(MoeParams p) {
+  __shared__ unsigned short act[kMoeMaxExperts];
+  __shared__ unsigned short first[kMoeMaxExperts + 1];
   __shared__ int n_act;
   __shared__ float den[kMoeMaxTokens];
-  extern __shared__ float y[];
+  extern __shared__ __attribute__((aligned(16))) float y[];
+  unsigned short *pl = reinterpret_cast<unsigned short *>(y + (size_t)NW * p.M * ROWS);
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
-  const int d0 = blockIdx.x * 16;
+  const int d0 = blockIdx.x * ROWS;
   if (wave == 0) {
-    int n = 0;
+    int n = 0, at = 0;
     for (int e0 = 0; e0 < p.E; e0 += kWave) {
       const int e = e0 + lane;
-      const bool in = e < p.E && p.count[e] > 0;
-      const unsigned long long m = __ballot(in);
-      if (in) act[n + __popcll(m & ((1ull << lane) - 1))] = e;
+      const int c = e < p.E ? p.count[e] : 0;
+      const unsigned long long m = __ballot(c > 0);
+      const int pos = n + __popcll(m & ((1ull << lane) - 1));
+      int upto = c;
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1) {
+        const int v = __shfl_up(upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (c > 0) {
+        act[pos] = (unsigned short)e;
+        first[pos] = (unsigned short)(at + upto - c);
+      }
       n += __popcll(m);
+      at += __shfl(upto, kWave - 1);
     }
-    if (lane == 0) n_act = n;
+    if (lane == 0) {
+      n_act = n;
+      first[n] = (unsigned short)at;
+    }
   }
-  for (int t = threadIdx.x; t < p.M; t += 256) {
+  for (int t = threadIdx.x; t < p.M; t += NW * kWave) {
     float s = 1.0f;
     if (p.renorm) {
       s = 0.0f;
@@ -205,48 +342,73 @@ __global__ __launch_bounds__(256) void moe_down(MoeParams p) {
     if (blockIdx.x == 0 && p.weights)
       for (int j = 0; j < p.k; ++j) p.weights[t * p.k + j] = p.prob[t * p.k + j] / s;
   }
-  for (int i = threadIdx.x; i < 4 * p.M * 16; i += 256) y[i] = 0.0f;
+  for (int i = threadIdx.x; i < NW * p.M * (ROWS / 4); i += NW * kWave)
+    reinterpret_cast<f32x4 *>(y)[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
   const int na = n_act;
-  const int parts = na < 4 ? 4 / na : 1;             // parts of F per expert
-  const int chunk = ((p.F + parts - 1) / parts + 15) / 16 * 16;
-  const int d = d0 + li < p.D ? d0 + li : p.D - 1;
-  float *yw = y + (size_t)wave * p.M * 16;
-  for (int i = wave; i < na * parts; i += 4) {
-    const int e = act[i / parts];
-    const int k0 = i % parts * chunk;
-    const int k1 = k0 + chunk < p.F ? k0 + chunk : p.F;
-    const int n = p.count[e];
-    const T *w2 = static_cast<const T *>(p.W2) + (size_t)e * (size_t)p.stride2 +
-                  (size_t)d * (size_t)p.ld2;
-    for (int i0 = 0; i0 < n; i0 += 16) {
-      const int pair = p.list[(size_t)e * p.M + (i0 + li < n ? i0 + li : n - 1)];
-      const float *h = p.H + (size_t)pair * p.F;
-      f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int k = k0; k < k1; k += 16) {
-        const int kk = k + 4 * lg;
-        f32x4 wf, hf;
+  for (int i = threadIdx.x / 16; i < na; i += NW * 4) {
+    const int at = first[i], n = first[i + 1] - at;
+    for (int j = li; j < n; j += 16)
+      pl[at + j] = (unsigned short)p.list[(size_t)act[i] * p.M + j];
+  }
+  __syncthreads();
+  // enough items that the last round's idle waves cost little, at least 128
+  // bytes of a row each
+  constexpr int G = 2 * El<T>::KSTEP;
+  constexpr int HALVES = 16 / ROWS;
+  int parts = (8 * NW + na - 1) / na;
+  const int most = (p.F + HALVES * G - 1) / (HALVES * G);
+  parts = parts < most ? parts : most;
+  const int half = (p.F + parts * HALVES - 1) / (parts * HALVES);
+  const int len = (half + G - 1) / G * G;       // k per half of an item
+  const int sel = li / ROWS;                    // this lane's half
+  const int lr = li % ROWS;
+  const int d = d0 + lr < p.D ? d0 + lr : p.D - 1;
+  float *yw = y + (size_t)wave * p.M * ROWS;
+  for (int i = wave; i < na * parts; i += NW) {
+    const int ia = i / parts;
+    const int k0 = i % parts * HALVES * len;
+    if (k0 >= p.F) continue;
+    // the halves cover k0 .. k0+len and k0+len .. k0+2*len, as far as F goes:
+    // with the lane's pointers moved by its half, its rows end at `lim`
+    const int lim = p.F - sel * len;
+    const int last = p.F - (HALVES - 1) * len;
+    const int k1 = k0 + len < p.F ? k0 + len : p.F;
+    const int kw = last < k1 ? last : k1;
+    const int e = act[ia], at = first[ia], n = first[ia + 1] - at;
+    const T *w[1] = {static_cast<const T *>(p.W2) + (size_t)e * (size_t)p.stride2 +
+                     (size_t)d * (size_t)p.ld2 + sel * len};
+    for (int i0 = 0; i0 < n; i0 += ROWS) {
+      const int pair = pl[at + (i0 + lr < n ? i0 + lr : n - 1)];
+      const int t = pair / p.k;
+      const float pr = p.prob[pair];
+      int ex = 0;
+      if constexpr (sizeof(T) == 2) ex = row_exponent(p.top[pair]);
+      const HiddenLoader<T> h = {p.H + (size_t)pair * p.F + sel * len, lim, ldexpf(1.0f, -ex)};
+      f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
+      stream_mac<T, 4>(w, k0, k1, kw, lim, h, acc);
+      f32x4 sum = acc[0][0];
+      if constexpr (ROWS == 8) {
+        // rows 8.. of columns 8.. (lane + 32 + 8) hold the second half's sums
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          wf[j] = kk + j < p.F ? (float)w2[kk + j] : 0.0f;
-          hf[j] = kk + j < p.F ? h[kk + j] : 0.0f;
-        }
-        acc = mma16(wf, hf, acc);
+        for (int j = 0; j < 4; ++j) sum[j] += __shfl(sum[j], lane + 40);
       }
-      if (i0 + li < n) {
-        const int t = pair / p.k;
-        const float w = p.prob[pair] / den[t];
+      if (4 * lg < ROWS && li < ROWS && i0 + li < n) {
+        const float wt = ldexpf(pr / den[t], ex);
+        f32x4 *o = reinterpret_cast<f32x4 *>(yw + t * ROWS + 4 * lg);
+        f32x4 v = *o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) yw[t * 16 + 4 * lg + j] += w * acc[j];
+        for (int j = 0; j < 4; ++j) v[j] += wt * sum[j];
+        *o = v;
       }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.M * 16; i += 256) {
-    const int t = i / 16, c = d0 + i % 16;
+  for (int i = threadIdx.x; i < p.M * ROWS; i += NW * kWave) {
+    const int t = i / ROWS, c = d0 + i % ROWS;
     if (c >= p.D) continue;
     float s = 0.0f;
-    for (int w = 0; w < 4; ++w) s += y[((size_t)w * p.M + t) * 16 + i % 16];
+    for (int v = 0; v < NW; ++v) s += y[((size_t)v * p.M + t) * ROWS + i % ROWS];
     T *out = static_cast<T *>(p.Y) + (size_t)t * (size_t)p.ldy + c;
     float o = p.alpha * s;
     if (p.beta != 0.0f) o = __builtin_fmaf(p.beta, (float)*out, o);
@@ -259,6 +421,7 @@ __global__ __launch_bounds__(256) void moe_down(MoeParams p) {
 struct MoeSpace {
   double *logits;
   float *prob, *H;
+  unsigned *top;
   int *count, *list;
 };
 
@@ -272,24 +435,65 @@ size_t carve(const MoeCall &c, void *base, MoeSpace *s) {
   };
   s->logits = reinterpret_cast<double *>(take((size_t)c.M * c.E * sizeof(double)));
   s->prob = reinterpret_cast<float *>(take((size_t)c.M * c.k * sizeof(float)));
+  s->top = reinterpret_cast<unsigned *>(take((size_t)c.M * c.k * sizeof(unsigned)));
   s->H = reinterpret_cast<float *>(take((size_t)c.M * c.k * (size_t)c.F * sizeof(float)));
   s->count = reinterpret_cast<int *>(take((size_t)c.E * sizeof(int)));
   s->list = reinterpret_cast<int *>(take((size_t)c.E * c.M * sizeof(int)));
   return used;
 }
 
+// Weight rows a workgroup of `up` takes: 32 of F where that still makes two
+// workgroups per CU of the experts that some token is likely to choose, else
+// 16 or 8.
+int up_blocks(const MoeCall &c) {
+  const long long active = (long long)c.M * c.k < c.E ? (long long)c.M * c.k : c.E;
+  if (active * ((c.F + 31) / 32) >= 2 * kCUs) return 4;
+  return active * ((c.F + 15) / 16) >= 2 * kCUs ? 2 : 1;
+}
+
+template <typename T, int NF>
+void launch_up(const MoeCall &c, const MoeParams &p) {
+  const dim3 g((unsigned)((c.F + 8 * NF - 1) / (8 * NF)), (unsigned)c.E), b(kUpWaves * kWave);
+  // more than 8 tokens per expert on average: several blocks of 16 at a time,
+  // so that the weights are read once for them
+  if (c.M > 16 && (long long)c.M * c.k > 8LL * c.E)
+    hipLaunchKernelGGL((moe_up<T, NF, 4>), g, b, 0, c.stream, p);
+  else
+    hipLaunchKernelGGL((moe_up<T, NF, 1>), g, b, 0, c.stream, p);
+}
+
 template <typename T>
-bool rows16(const void *p, int ld, long long stride = 0) {
-  return ld % El<T>::VEC == 0 && stride % El<T>::VEC == 0 && aligned_to(p, 16);
+void launch_up(const MoeCall &c, const MoeParams &p) {
+  switch (up_blocks(c)) {
+    case 4: return launch_up<T, 4>(c, p);
+    case 2: return launch_up<T, 2>(c, p);
+    default: return launch_up<T, 1>(c, p);
+  }
+}
+
+template <typename T, int NW, int ROWS>
+void launch_down(const MoeCall &c, const MoeParams &p) {
+  hipLaunchKernelGGL((moe_down<T, NW, ROWS>), dim3((unsigned)((c.D + ROWS - 1) / ROWS)),
+                     dim3(NW * kWave),
+                     (size_t)NW * c.M * ROWS * 4 + (size_t)c.M * c.k * 2, c.stream, p);
+}
+
+// As many waves as their copies of the outputs leave room for in 64 KB of LDS;
+// 8 rows where 16 would leave CUs without a workgroup and an expert has few
+// tokens (with more than 8 of them its weights are read again).
+template <typename T>
+void launch_down(const MoeCall &c, const MoeParams &p) {
+  if (c.M > 128) launch_down<T, 4, 16>(c, p);
+  else if (c.M > 64) launch_down<T, 8, 16>(c, p);
+  else if (c.D < 16 * kCUs && (long long)c.M * c.k <= 4LL * c.E) launch_down<T, 16, 8>(c, p);
+  else launch_down<T, 16, 16>(c, p);
 }
 
 template <typename T>
 hipError_t run(const MoeCall &c, const MoeSpace &s) {
-  const bool vec_x = !c.force_scalar && rows16<T>(c.X, c.ldx);
-  const bool vec_r = !c.force_scalar && rows16<T>(c.Wr, c.ldr);
-  hipLaunchKernelGGL((moe_logits<T>), dim3((unsigned)((c.E + 3) / 4), (unsigned)((c.M + 3) / 4)),
-                     dim3(256), 0, c.stream, static_cast<const T *>(c.X), c.ldx,
-                     static_cast<const T *>(c.Wr), c.ldr, c.M, c.D, c.E, vec_x && vec_r, s.logits);
+  hipLaunchKernelGGL((moe_logits<T>), dim3((unsigned)c.E, (unsigned)((c.M + 3) / 4)), dim3(256), 0, c.stream, static_cast<const T *>(c.X), c.ldx,
+                     static_cast<const T *>(c.Wr), c.ldr, c.M, c.D, c.E, s.logits, s.top,
+                     c.M * c.k);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   MoeParams p;
@@ -301,6 +505,7 @@ hipError_t run(const MoeCall &c, const MoeSpace &s) {
   p.count = s.count;
   p.list = s.list;
   p.H = s.H;
+  p.top = s.top;
   p.Y = c.Y;
   p.ids = c.ids;
   p.weights = c.weights;
@@ -316,17 +521,12 @@ hipError_t run(const MoeCall &c, const MoeSpace &s) {
   p.ld1 = c.ld1;
   p.ld2 = c.ld2;
   p.ldy = c.ldy;
-  p.vec_x = vec_x;
-  p.vec_1 = !c.force_scalar && rows16<T>(c.W1, c.ld1, c.stride1);
-  p.vec_2 = !c.force_scalar && rows16<T>(c.W2, c.ld2, c.stride2);
   p.alpha = c.alpha;
   p.beta = c.beta;
-  hipLaunchKernelGGL((moe_up<T>), dim3((unsigned)((c.F + 15) / 16), (unsigned)c.E), dim3(256), 0,
-                     c.stream, p);
+  launch_up<T>(c, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down<T>), dim3((unsigned)((c.D + 15) / 16)), dim3(256),
-                     (size_t)4 * c.M * 16 * sizeof(float), c.stream, p);
+  launch_down<T>(c, p);
   return hipGetLastError();
 }
 

@@ -42,21 +42,22 @@ __device__ __forceinline__ f32x4 mma16(f32x4 a, f32x4 b, f32x4 c) {
   return c;
 }
 
+// VEC consecutive elements at any element's address.  Global loads of 16
+// bytes need no more than the element's own alignment on this target, so rows
+// of any length, padding and offset take the same path; only the last, partly
+// filled step of a row is loaded element by element, since what lies behind a
+// row is never read.
 template <typename T>
-__device__ __forceinline__ typename El<T>::Frag zero_frag() {
-  typename El<T>::Frag f;
-#pragma unroll
-  for (int e = 0; e < El<T>::VEC; ++e) f[e] = (T)0.0f;
-  return f;
+__device__ __forceinline__ typename El<T>::Frag load_whole(const T *p) {
+  typedef T Any __attribute__((ext_vector_type(El<T>::VEC), aligned(sizeof(T))));
+  return *reinterpret_cast<const Any *>(p);
 }
 
-// Elements k .. k+VEC-1 of a row of K elements (0 beyond its end).  vec: the
-// row starts 16-byte aligned and k is a multiple of VEC.
+// Elements k .. k+VEC-1 of a row of K elements, 0 beyond its end.
 template <typename T>
-__device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, int K, bool vec) {
-  typedef typename El<T>::Frag Frag;
-  if (vec && k + El<T>::VEC <= K) return *reinterpret_cast<const Frag *>(row + k);
-  Frag f;
+__device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, int K) {
+  if (k + El<T>::VEC <= K) return load_whole(row + k);
+  typename El<T>::Frag f;
 #pragma unroll
   for (int e = 0; e < El<T>::VEC; ++e) f[e] = k + e < K ? row[k + e] : (T)0.0f;
   return f;
@@ -72,6 +73,67 @@ __device__ __forceinline__ typename El<T>::Frag load_frag_strided(const T *col, 
   for (int e = 0; e < El<T>::VEC; ++e) f[e] = k + e < K ? col[(size_t)(k + e) * ld] : (T)0.0f;
   return f;
 }
+
+// acc[f][b] += W block f (16 rows, this lane's at w[f]) times activation block
+// b over k in [k0, k1).  Activations come from `x`: x.whole(b, kk) loads this
+// lane's values at kk = k + VEC * lane group, x.masked(b, kk) the same with 0
+// at and beyond this lane's end of the row, x.frag makes a fragment of them.
+// Steps that end at or before `kw` are whole for every lane; `lim` is this
+// lane's end of the weights' rows.  The loads of U steps are issued together,
+// ahead of their products (the scheduling barrier keeps the compiler from
+// pairing each load with its use, which left too few bytes in flight).  k0 is
+// a multiple of KSTEP.
+template <typename T, int U, int NF, int NB, class X>
+__device__ __forceinline__ void stream_mac(const T *const (&w)[NF], int k0, int k1, int kw,
+                                           int lim, X x, f32x4 (&acc)[NF][NB]) {
+  typedef typename El<T>::Frag Frag;
+  constexpr int KS = El<T>::KSTEP;
+  const int lk = (int)(threadIdx.x % kWave) / 16 * El<T>::VEC;
+  int k = k0;
+  for (; k + U * KS <= kw; k += U * KS) {
+    Frag wf[U][NF];
+    typename X::Raw xr[U][NB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) wf[u][f] = load_whole(w[f] + k + u * KS + lk);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) xr[u][b] = x.whole(b, k + u * KS + lk);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const Frag xf = x.frag(xr[u][b]);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[u][f], xf, acc[f][b]);
+      }
+  }
+  for (; k < k1; k += KS) {
+    Frag wf[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+      wf[f] = k + KS <= kw ? load_whole(w[f] + k + lk) : load_frag(w[f], k + lk, lim);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const Frag xf = x.frag(k + KS <= kw ? x.whole(b, k + lk) : x.masked(b, k + lk));
+#pragma unroll
+      for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[f], xf, acc[f][b]);
+    }
+  }
+}
+
+// Activations of the weights' own type: this lane's row of block b at row[b].
+template <typename T, int NB>
+struct RowLoader {
+  typedef typename El<T>::Frag Raw;
+  const T *row[NB];
+  int lim;
+  __device__ __forceinline__ Raw whole(int b, int k) const { return load_whole(row[b] + k); }
+  __device__ __forceinline__ Raw masked(int b, int k) const { return load_frag(row[b], k, lim); }
+  __device__ __forceinline__ Raw frag(const Raw &r) const { return r; }
+};
 
 // The adapter of a row: -1 when it has none (or an index out of range), or
 // when that adapter's rank is at most `r0` (nothing of it from rank r0 on).

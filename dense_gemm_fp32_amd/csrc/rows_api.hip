@@ -104,7 +104,6 @@ int lora(bool half, int M, int N, int K, float alpha, const void *X, int ldx, co
   c.scale = scale;
   c.ranks = ranks;
   c.rows = rows;
-  c.force_scalar = dgemm::force_scalar_loads();
   c.stream = s;
   Space space;
   const int rc = space.open(ws, ws_bytes, dgemm::lora_workspace(c), s, -323);
@@ -202,7 +201,6 @@ int lora_grad(bool half, int M, int N, int K, float alpha, const void *dY, int l
   c.dB = want_b ? dB : nullptr;
   c.lddb = lddb;
   c.stride_db = stride_db;
-  c.force_scalar = dgemm::force_scalar_loads();
   c.stream = s;
   Space space;
   const int rc = space.open(ws, ws_bytes, dgemm::lora_grad_workspace(c), s, -432);
@@ -266,7 +264,6 @@ int moe(bool half, int M, int D, int F, int E, int top_k, int renorm, float alph
   c.ldy = ldy;
   c.ids = ids;
   c.weights = weights;
-  c.force_scalar = dgemm::force_scalar_loads();
   c.stream = s;
   Space space;
   const int rc = space.open(ws, ws_bytes, dgemm::moe_workspace(c), s, -523);

@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
     for (int f = 0; f < NF; ++f)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[f][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    stream_mac<T, (NF * NB >= 8 ? 2 : 4)>(w, k0, k1, k1, k1, x, acc);
+    stream_mac<T, (NF * NB >= 8 ? 2 : 4), 1>(w, k0, k1, k1, k1, x, acc);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if (i0 + 16 * b >= n) break;
@@ -290,11 +290,9 @@ struct HiddenLoader<float> {
 // tokens and adds the weighted result to its own copy of the ROWS x M outputs
 // in LDS, which are summed in wave order at the end.
 //
-// ROWS = 16 is the matrix instruction's own shape.  ROWS = 8, for layers that
-// make too few workgroups of 16, puts two halves of the item's k into one
-// instruction: lanes 8..15 of each 16 hold the same 8 weight rows, and the
-// same 8 tokens, at the second half's k; of the 16 x 16 products the two 8 x 8
-// blocks on the diagonal are the halves' sums, and the rest is dropped.
+// ROWS = 16 is the matrix instruction's own shape; ROWS = 8 and 4, for layers
+// that make too few workgroups of 16 and whose experts have few tokens, put 2
+// or 4 stretches of k into one instruction (stream_mac).
 // Dynamic LDS: NW x M x ROWS floats, then M*k pair numbers.
 template <typename T, int NW, int ROWS>
 __global__ __launch_bounds__(NW *kWave) void moe_down(MoeParams p) {
@@ -352,54 +350,40 @@ __global__ __launch_bounds__(NW *kWave) void moe_down(MoeParams p) {
       pl[at + j] = (unsigned short)p.list[(size_t)act[i] * p.M + j];
   }
   __syncthreads();
-  // enough items that the last round's idle waves cost little, at least 128
-  // bytes of a row each
-  constexpr int G = 2 * El<T>::KSTEP;
-  constexpr int HALVES = 16 / ROWS;
-  int parts = (8 * NW + na - 1) / na;
-  const int most = (p.F + HALVES * G - 1) / (HALVES * G);
-  parts = parts < most ? parts : most;
-  const int half = (p.F + parts * HALVES - 1) / (parts * HALVES);
-  const int len = (half + G - 1) / G * G;       // k per half of an item
-  const int sel = li / ROWS;                    // this lane's half
-  const int lr = li % ROWS;
+  // enough items that the last round's idle waves cost little, each a whole
+  // number of steps that are loaded together
+  constexpr int U = 4;
+  constexpr int P = 16 / ROWS;
+  constexpr int G = U * P * El<T>::KSTEP;
+  const int want = (8 * NW + na - 1) / na;
+  const int len = p.F / want / G * G > G ? p.F / want / G * G : G;   // k per item
+  const int parts = (p.F + len - 1) / len;
+  const int lr = li / P;
   const int d = d0 + lr < p.D ? d0 + lr : p.D - 1;
   float *yw = y + (size_t)wave * p.M * ROWS;
   for (int i = wave; i < na * parts; i += NW) {
     const int ia = i / parts;
-    const int k0 = i % parts * HALVES * len;
-    if (k0 >= p.F) continue;
-    // the halves cover k0 .. k0+len and k0+len .. k0+2*len, as far as F goes:
-    // with the lane's pointers moved by its half, its rows end at `lim`
-    const int lim = p.F - sel * len;
-    const int last = p.F - (HALVES - 1) * len;
+    const int k0 = i % parts * len;
     const int k1 = k0 + len < p.F ? k0 + len : p.F;
-    const int kw = last < k1 ? last : k1;
     const int e = act[ia], at = first[ia], n = first[ia + 1] - at;
     const T *w[1] = {static_cast<const T *>(p.W2) + (size_t)e * (size_t)p.stride2 +
-                     (size_t)d * (size_t)p.ld2 + sel * len};
+                     (size_t)d * (size_t)p.ld2};
     for (int i0 = 0; i0 < n; i0 += ROWS) {
       const int pair = pl[at + (i0 + lr < n ? i0 + lr : n - 1)];
       const int t = pair / p.k;
       const float pr = p.prob[pair];
       int ex = 0;
       if constexpr (sizeof(T) == 2) ex = row_exponent(p.top[pair]);
-      const HiddenLoader<T> h = {p.H + (size_t)pair * p.F + sel * len, lim, ldexpf(1.0f, -ex)};
+      const HiddenLoader<T> h = {p.H + (size_t)pair * p.F, k1, ldexpf(1.0f, -ex)};
       f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
-      stream_mac<T, 4>(w, k0, k1, kw, lim, h, acc);
-      f32x4 sum = acc[0][0];
-      if constexpr (ROWS == 8) {
-        // rows 8.. of columns 8.. (lane + 32 + 8) hold the second half's sums
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j] += __shfl(sum[j], lane + 40);
-      }
-      if (4 * lg < ROWS && li < ROWS && i0 + li < n) {
+      stream_mac<T, U, P>(w, k0, k1, k1, k1, h, acc);
+      float sum[4 / P];
+      diagonal_sum<P>(acc[0][0], sum);
+      if (li % P == 0 && i0 + lr < n) {
         const float wt = ldexpf(pr / den[t], ex);
-        f32x4 *o = reinterpret_cast<f32x4 *>(yw + t * ROWS + 4 * lg);
-        f32x4 v = *o;
+        float *o = yw + t * ROWS + 4 / P * lg;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += wt * sum[j];
-        *o = v;
+        for (int j = 0; j < 4 / P; ++j) o[j] += wt * sum[j];
       }
     }
   }
@@ -479,13 +463,16 @@ void launch_down(const MoeCall &c, const MoeParams &p) {
 }
 
 // As many waves as their copies of the outputs leave room for in 64 KB of LDS;
-// 8 rows where 16 would leave CUs without a workgroup and an expert has few
-// tokens (with more than 8 of them its weights are read again).
+// fewer rows where more would leave CUs without a workgroup, as long as an
+// expert's tokens are likely to fit their block (beyond it its weights are
+// read again).
 template <typename T>
 void launch_down(const MoeCall &c, const MoeParams &p) {
+  const long long pairs = (long long)c.M * c.k;
   if (c.M > 128) launch_down<T, 4, 16>(c, p);
   else if (c.M > 64) launch_down<T, 8, 16>(c, p);
-  else if (c.D < 16 * kCUs && (long long)c.M * c.k <= 4LL * c.E) launch_down<T, 16, 8>(c, p);
+  else if (c.D < 8 * kCUs && (c.M <= 4 || pairs <= c.E)) launch_down<T, 16, 4>(c, p);
+  else if (c.D < 16 * kCUs && (c.M <= 8 || pairs <= 4LL * c.E)) launch_down<T, 16, 8>(c, p);
   else launch_down<T, 16, 16>(c, p);
 }
 

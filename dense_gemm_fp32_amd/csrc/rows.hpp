@@ -83,44 +83,84 @@ __device__ __forceinline__ typename El<T>::Frag load_frag_strided(const T *col, 
 // ahead of their products (the scheduling barrier keeps the compiler from
 // pairing each load with its use, which left too few bytes in flight).  k0 is
 // a multiple of KSTEP.
-template <typename T, int U, int NF, int NB, class X>
-__device__ __forceinline__ void stream_mac(const T *const (&w)[NF], int k0, int k1, int kw,
-                                           int lim, X x, f32x4 (&acc)[NF][NB]) {
+//
+// P > 1 puts P neighbouring stretches of k into one instruction: lane l % 16
+// holds row l % 16 / P of 16 / P rows, stretch l % P, so that P neighbouring
+// lanes read 16 P consecutive bytes; a step then covers P * KSTEP k, and of the
+// 16 x 16 products those whose row and column hold the same stretch count
+// (diagonal_sum adds them up).
+template <typename T, int U, int P, int NF, int NB, class X>
+__device__ __forceinline__ void stream_steps(const T *const (&w)[NF], int k, const X &x,
+                                             f32x4 (&acc)[NF][NB]) {
   typedef typename El<T>::Frag Frag;
-  constexpr int KS = El<T>::KSTEP;
-  const int lk = (int)(threadIdx.x % kWave) / 16 * El<T>::VEC;
-  int k = k0;
-  for (; k + U * KS <= kw; k += U * KS) {
-    Frag wf[U][NF];
-    typename X::Raw xr[U][NB];
+  constexpr int KS = P * El<T>::KSTEP;
+  Frag wf[U][NF];
+  typename X::Raw xr[U][NB];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+  for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int f = 0; f < NF; ++f) wf[u][f] = load_whole(w[f] + k + u * KS + lk);
+    for (int f = 0; f < NF; ++f) wf[u][f] = load_whole(w[f] + k + u * KS);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) xr[u][b] = x.whole(b, k + u * KS + lk);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const Frag xf = x.frag(xr[u][b]);
-#pragma unroll
-        for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[u][f], xf, acc[f][b]);
-      }
+    for (int b = 0; b < NB; ++b) xr[u][b] = x.whole(b, k + u * KS);
   }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const Frag xf = x.frag(xr[u][b]);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[u][f], xf, acc[f][b]);
+    }
+}
+
+template <typename T, int U, int P, int NF, int NB, class X>
+__device__ __forceinline__ void stream_mac(const T *const (&w)[NF], int k0, int k1, int kw,
+                                           int lim, const X &x, f32x4 (&acc)[NF][NB]) {
+  typedef typename El<T>::Frag Frag;
+  constexpr int KS = P * El<T>::KSTEP;
+  const int lane = threadIdx.x % kWave;
+  const int lk = (lane / 16 * P + lane % P) * El<T>::VEC;
+  int k = k0;
+  for (; k + U * KS <= kw; k += U * KS) stream_steps<T, U, P>(w, k + lk, x, acc);
+  // what is left of the whole steps, in halves, so that it too is loaded together
+  if constexpr (U >= 8)
+    if (k + 4 * KS <= kw) {
+      stream_steps<T, 4, P>(w, k + lk, x, acc);
+      k += 4 * KS;
+    }
+  if constexpr (U >= 4)
+    if (k + 2 * KS <= kw) {
+      stream_steps<T, 2, P>(w, k + lk, x, acc);
+      k += 2 * KS;
+    }
+  for (; k + KS <= kw; k += KS) stream_steps<T, 1, P>(w, k + lk, x, acc);
   for (; k < k1; k += KS) {
     Frag wf[NF];
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
-      wf[f] = k + KS <= kw ? load_whole(w[f] + k + lk) : load_frag(w[f], k + lk, lim);
+    for (int f = 0; f < NF; ++f) wf[f] = load_frag(w[f], k + lk, lim);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const Frag xf = x.frag(k + KS <= kw ? x.whole(b, k + lk) : x.masked(b, k + lk));
+      const Frag xf = x.frag(x.masked(b, k + lk));
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[f], xf, acc[f][b]);
     }
+  }
+}
+
+// The sums of a product made with P stretches (above): element q of the result
+// is row lane/16 * 4/P + q, column lane % 16 / P, in every lane.
+template <int P>
+__device__ __forceinline__ void diagonal_sum(const f32x4 &v, float (&out)[4 / P]) {
+  const int p = threadIdx.x % P;
+#pragma unroll
+  for (int q = 0; q < 4 / P; ++q) {
+    float s = v[q * P];
+#pragma unroll
+    for (int j = 1; j < P; ++j) s = p == j ? v[q * P + j] : s;
+#pragma unroll
+    for (int o = 1; o < P; o <<= 1) s += __shfl_xor(s, o);
+    out[q] = s;
   }
 }
 

@@ -246,6 +246,20 @@ hipError_t launch_lora_grad(const LoraCall &c, void *ws);
 hipError_t launch_scale_batch_f32(int L, int rows, int cols, float beta, float *D, int ldd,
                                   long long stride, hipStream_t s);
 
+// Parts of a workspace, in order, each 256-byte aligned; a null base only
+// counts.
+struct Carve {
+  char *base;
+  size_t used = 0;
+  explicit Carve(void *b) : base(static_cast<char *>(b)) {}
+  template <typename T>
+  T *take(size_t count) {
+    char *p = base ? base + used : nullptr;
+    used += (count * sizeof(T) + 255) / 256 * 256;
+    return reinterpret_cast<T *>(p);
+  }
+};
+
 // A mixture-of-experts layer for a few tokens (moe.hip); validated, M, D > 0.
 struct MoeCall {
   bool half;

@@ -322,8 +322,6 @@ __global__ __launch_bounds__(256) void lora_outer_sum(const float *P, float *D, 
 
 // ---------------------------------------------------------------- host side
 
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-
 int rank_pad(int R) { return (R + 15) / 16 * 16; }
 
 template <typename T, bool KMAJ>
@@ -418,19 +416,6 @@ hipError_t outer(const LoraCall &c, const float *V, const void *X, int ldx, int 
                      c.beta_ab);
   return hipGetLastError();
 }
-
-// Parts of a workspace, in order; a null base only counts.
-struct Carve {
-  char *base;
-  size_t used = 0;
-  explicit Carve(void *b) : base(static_cast<char *>(b)) {}
-  template <typename T>
-  T *take(size_t count) {
-    char *p = base ? base + used : nullptr;
-    used += round256(count * sizeof(T));
-    return reinterpret_cast<T *>(p);
-  }
-};
 
 struct LoraSpace {
   float *V, *T;

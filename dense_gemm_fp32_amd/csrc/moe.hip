@@ -75,6 +75,7 @@ struct MoeParams {
   int *count, *list;      // tokens of expert e; their pairs t*k + choice: list[e*M ..]
   float *H;               // M*k x F
   unsigned *top;          // M*k: bits of the largest |H| of the row
+  float *O;               // M*k x D (many tokens only)
   void *Y;
   int *ids;
   float *weights;
@@ -88,44 +89,46 @@ struct MoeParams {
 
 constexpr int kUpWaves = 4;
 
-// grid: (ceil(F / (8 NF)), E), 4 waves that divide D.  NF blocks of 16 weight
-// rows: 8 NF of the gate's and the same 8 NF of the up projection's; NB blocks
-// of 16 tokens at a time.
-template <typename T, int NF, int NB>
+// grid: (ceil(F / FS), E), 4 waves that divide D.  NF blocks of 16 / P weight
+// rows: FS = 8 NF / P of the gate's and as many of the up projection's; NB
+// blocks of 16 / P tokens at a time, with P stretches of k in one instruction
+// (stream_mac).
+template <typename T, int NF, int NB, int P>
 __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
   __shared__ int rank[kMoeMaxTokens];
   __shared__ int pairs[kMoeMaxTokens];
   __shared__ int total;
-  __shared__ float red[kUpWaves][16 * NF][17];
-  constexpr int KS = El<T>::KSTEP;
-  constexpr int FS = 8 * NF;
+  constexpr int BR = 16 / P;           // rows, and tokens, of a block
+  constexpr int FS = BR * NF / 2;
+  __shared__ float red[kUpWaves][BR * NF][17];
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
   const int f0 = blockIdx.x * FS, e = blockIdx.y;
+  constexpr int TB = 4;
   // four tokens a wave at a time, so that their logits are on the way together
-  for (int t0 = 4 * wave; t0 < p.M; t0 += 4 * kUpWaves) {
-    const double *l[4];
-    double mine[4];
-    int larger[4];
+  for (int t0 = TB * wave; t0 < p.M; t0 += TB * kUpWaves) {
+    const double *l[TB];
+    double mine[TB];
+    int larger[TB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < TB; ++i) {
       l[i] = p.logits + (size_t)(t0 + i < p.M ? t0 + i : p.M - 1) * p.E;
       mine[i] = logit_key(l[i][e]);
       larger[i] = 0;
     }
     for (int j0 = 0; j0 < p.E; j0 += kWave) {
       const int j = j0 + lane;
-      double v[4];
+      double v[TB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = l[i][j < p.E ? j : p.E - 1];
+      for (int i = 0; i < TB; ++i) v[i] = l[i][j < p.E ? j : p.E - 1];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < TB; ++i) {
         const double k = logit_key(v[i]);
         larger[i] += __popcll(__ballot(j < p.E && (k > mine[i] || (k == mine[i] && j < e))));
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TB; ++i)
       if (lane == 0 && t0 + i < p.M) rank[t0 + i] = larger[i] < p.k ? larger[i] : -1;
   }
   __syncthreads();
@@ -171,22 +174,22 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
   const T *w[NF];
 #pragma unroll
   for (int b = 0; b < NF; ++b) {
-    // row 16b + li of the workgroup's: the first half gate rows, the rest up rows
-    const int r = 16 * b + li;
+    // row r of the workgroup's: the first half gate rows, the rest up rows
+    const int r = BR * b + li / P;
     const int f = f0 + (r < FS ? r : r - FS);
     w[b] = w1 + (size_t)((r < FS ? 0 : p.F) + (f < p.F ? f : p.F - 1)) * (size_t)p.ld1;
   }
   // each wave a stretch of D, whole steps (of at least 128 bytes a row) long
-  constexpr int G = 2 * KS;
+  constexpr int G = 2 * El<T>::KSTEP * P;
   const int part = ((p.D + kUpWaves - 1) / kUpWaves + G - 1) / G * G;
   const int k0 = wave * part;
   const int k1 = k0 + part < p.D ? k0 + part : p.D;
-  for (int i0 = 0; i0 < n; i0 += 16 * NB) {
+  for (int i0 = 0; i0 < n; i0 += BR * NB) {
     RowLoader<T, NB> x;
     x.lim = k1;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int i = i0 + 16 * b + li;
+      const int i = i0 + BR * b + li / P;
       x.row[b] = static_cast<const T *>(p.X) + (size_t)(pairs[i < n ? i : n - 1] / p.k) * (size_t)p.ldx;
     }
     f32x4 acc[NF][NB];
@@ -194,25 +197,30 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
     for (int f = 0; f < NF; ++f)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[f][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    stream_mac<T, (NF * NB >= 8 ? 2 : 4), 1>(w, k0, k1, k1, k1, x, acc);
+    stream_mac<T, (NF * NB >= 8 ? 2 : 4), P>(w, k0, k1, k1, k1, x, acc);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      if (i0 + 16 * b >= n) break;
+      if (i0 + BR * b >= n) break;
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
+      for (int f = 0; f < NF; ++f) {
+        float v[4 / P];
+        diagonal_sum<P>(acc[f][b], v);
+        if (li % P == 0)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) red[wave][16 * f + 4 * lg + j][li] = acc[f][b][j];
+          for (int j = 0; j < 4 / P; ++j) red[wave][BR * f + 4 / P * lg + j][li / P] = v[j];
+      }
       __syncthreads();
-      // 8 lanes share a token: a row's largest |h| takes one atomic per 8 f
-      for (int q = threadIdx.x; q < 16 * FS; q += kUpWaves * kWave) {
-        const int c = q / 8 % 16, r = q % 8 + q / 128 * 8;
+      // RG lanes share a token: a row's largest |h| takes one atomic per RG f
+      constexpr int RG = FS < 8 ? FS : 8;
+      for (int q = threadIdx.x; q < BR * FS; q += kUpWaves * kWave) {
+        const int c = q / RG % BR, r = q % RG + q / (RG * BR) * RG;
         float g = 0.0f, u = 0.0f;
 #pragma unroll
         for (int v = 0; v < kUpWaves; ++v) {
           g += red[v][r][c];
           u += red[v][FS + r][c];
         }
-        const int i = i0 + 16 * b + c;
+        const int i = i0 + BR * b + c;
         const bool ok = i < n && f0 + r < p.F;
         const float h = g / (1.0f + expf(-g)) * u;
         const int pair = pairs[i < n ? i : n - 1];
@@ -220,11 +228,11 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
         if constexpr (sizeof(T) == 2) {
           unsigned m = ok ? __builtin_bit_cast(unsigned, fabsf(h)) : 0u;
 #pragma unroll
-          for (int o = 4; o > 0; o >>= 1) {
+          for (int o = RG / 2; o > 0; o >>= 1) {
             const unsigned v = __shfl_xor(m, o);
             m = m > v ? m : v;
           }
-          if (r % 8 == 0 && m != 0u) atomicMax(&p.top[pair], m);
+          if (r % RG == 0 && m != 0u) atomicMax(&p.top[pair], m);
         }
       }
       __syncthreads();
@@ -246,43 +254,43 @@ __device__ __forceinline__ int row_exponent(unsigned bits) {
 // A row of H as fragments of T: for fp16, scaled by the row's power of two
 // and rounded to 11 bits (those of every value within 2^-28 of the row's
 // largest).
-template <typename T>
+template <typename T, int NB>
 struct HiddenLoader;
 
-template <>
-struct HiddenLoader<_Float16> {
+template <int NB>
+struct HiddenLoader<_Float16, NB> {
   struct Raw {
     f32x4 a, b;
   };
-  const float *row;
+  const float *row[NB];
+  float down[NB];
   int lim;
-  float down;
-  __device__ __forceinline__ Raw whole(int, int k) const {
-    return Raw{load_whole(row + k), load_whole(row + k + 4)};
+  __device__ __forceinline__ Raw whole(int b, int k) const {
+    return Raw{load_whole(row[b] + k), load_whole(row[b] + k + 4)};
   }
-  __device__ __forceinline__ Raw masked(int, int k) const {
-    return Raw{load_frag(row, k, lim), load_frag(row, k + 4, lim)};
+  __device__ __forceinline__ Raw masked(int b, int k) const {
+    return Raw{load_frag(row[b], k, lim), load_frag(row[b], k + 4, lim)};
   }
-  __device__ __forceinline__ f16x8 frag(const Raw &r) const {
+  __device__ __forceinline__ f16x8 frag(int b, const Raw &r) const {
     f16x8 f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f[j] = (_Float16)(r.a[j] * down);
-      f[4 + j] = (_Float16)(r.b[j] * down);
+      f[j] = (_Float16)(r.a[j] * down[b]);
+      f[4 + j] = (_Float16)(r.b[j] * down[b]);
     }
     return f;
   }
 };
 
-template <>
-struct HiddenLoader<float> {
+template <int NB>
+struct HiddenLoader<float, NB> {
   typedef f32x4 Raw;
-  const float *row;
+  const float *row[NB];
+  float down[NB];
   int lim;
-  float down;
-  __device__ __forceinline__ Raw whole(int, int k) const { return load_whole(row + k); }
-  __device__ __forceinline__ Raw masked(int, int k) const { return load_frag(row, k, lim); }
-  __device__ __forceinline__ f32x4 frag(const Raw &r) const { return r; }
+  __device__ __forceinline__ Raw whole(int b, int k) const { return load_whole(row[b] + k); }
+  __device__ __forceinline__ Raw masked(int b, int k) const { return load_frag(row[b], k, lim); }
+  __device__ __forceinline__ f32x4 frag(int, const Raw &r) const { return r; }
 };
 
 // grid: ceil(D/ROWS), NW waves.  The work items are (chosen expert, part of F),
@@ -290,16 +298,20 @@ struct HiddenLoader<float> {
 // tokens and adds the weighted result to its own copy of the ROWS x M outputs
 // in LDS, which are summed in wave order at the end.
 //
-// ROWS = 16 is the matrix instruction's own shape; ROWS = 8 and 4, for layers
-// that make too few workgroups of 16 and whose experts have few tokens, put 2
-// or 4 stretches of k into one instruction (stream_mac).
+// The experts here have few tokens, so an instruction holds 8 rows and 2
+// stretches of k, or 4 and 4 (stream_mac): neighbouring lanes then read
+// neighbouring pieces of a row, and there are more workgroups.
 // Dynamic LDS: NW x M x ROWS floats, then M*k pair numbers.
-template <typename T, int NW, int ROWS>
-__global__ __launch_bounds__(NW *kWave) void moe_down(MoeParams p) {
+constexpr int kDownWaves = 16;
+constexpr int kNarrowTokens = 64;   // their copies of the outputs fit the LDS
+
+template <typename T, int ROWS>
+__global__ __launch_bounds__(kDownWaves *kWave) void moe_down(MoeParams p) {
+  constexpr int NW = kDownWaves;
   __shared__ unsigned short act[kMoeMaxExperts];
   __shared__ unsigned short first[kMoeMaxExperts + 1];
   __shared__ int n_act;
-  __shared__ float den[kMoeMaxTokens];
+  __shared__ float den[kNarrowTokens];
   extern __shared__ __attribute__((aligned(16))) float y[];
   unsigned short *pl = reinterpret_cast<unsigned short *>(y + (size_t)NW * p.M * ROWS);
   const int lane = threadIdx.x % kWave, wave = wave_id();
@@ -374,7 +386,7 @@ __global__ __launch_bounds__(NW *kWave) void moe_down(MoeParams p) {
       const float pr = p.prob[pair];
       int ex = 0;
       if constexpr (sizeof(T) == 2) ex = row_exponent(p.top[pair]);
-      const HiddenLoader<T> h = {p.H + (size_t)pair * p.F, k1, ldexpf(1.0f, -ex)};
+      const HiddenLoader<T, 1> h = {{p.H + (size_t)pair * p.F}, {ldexpf(1.0f, -ex)}, k1};
       f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
       stream_mac<T, U, P>(w, k0, k1, k1, k1, h, acc);
       float sum[4 / P];
@@ -400,80 +412,203 @@ __global__ __launch_bounds__(NW *kWave) void moe_down(MoeParams p) {
   }
 }
 
+// ---------------------------------------------------------------- down, many tokens
+
+constexpr int kWideWaves = 4;
+
+// O[pair, d] = the pair's unweighted output.  grid: (ceil(D / (16 NF)), E), 4
+// waves that divide F; NB blocks of 16 tokens at a time.
+template <typename T, int NF, int NB>
+__global__ __launch_bounds__(kWideWaves *kWave) void moe_down_wide(MoeParams p) {
+  __shared__ float red[kWideWaves][16 * NF][17];
+  const int e = blockIdx.y;
+  const int n = p.count[e];
+  if (n == 0) return;
+  const int lane = threadIdx.x % kWave, wave = wave_id();
+  const int li = lane % 16, lg = lane / 16;
+  const int d0 = blockIdx.x * 16 * NF;
+  const int *list = p.list + (size_t)e * p.M;
+  const T *w[NF];
+#pragma unroll
+  for (int b = 0; b < NF; ++b) {
+    const int d = d0 + 16 * b + li;
+    w[b] = static_cast<const T *>(p.W2) + (size_t)e * (size_t)p.stride2 +
+           (size_t)(d < p.D ? d : p.D - 1) * (size_t)p.ld2;
+  }
+  constexpr int G = 2 * El<T>::KSTEP;
+  const int part = ((p.F + kWideWaves - 1) / kWideWaves + G - 1) / G * G;
+  const int k0 = wave * part;
+  const int k1 = k0 + part < p.F ? k0 + part : p.F;
+  for (int i0 = 0; i0 < n; i0 += 16 * NB) {
+    HiddenLoader<T, NB> h;
+    h.lim = k1;
+    int ex[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int i = i0 + 16 * b + li;
+      const int pair = list[i < n ? i : n - 1];
+      h.row[b] = p.H + (size_t)pair * p.F;
+      ex[b] = 0;
+      if constexpr (sizeof(T) == 2) ex[b] = row_exponent(p.top[pair]);
+      h.down[b] = ldexpf(1.0f, -ex[b]);
+    }
+    f32x4 acc[NF][NB];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[f][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    stream_mac<T, (NF * NB >= 8 ? 2 : 4), 1>(w, k0, k1, k1, k1, h, acc);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (i0 + 16 * b >= n) break;
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          red[wave][16 * f + 4 * lg + j][li] = ldexpf(acc[f][b][j], ex[b]);
+      __syncthreads();
+      for (int q = threadIdx.x; q < 256 * NF; q += kWideWaves * kWave) {
+        const int c = q / (16 * NF), r = q % (16 * NF);
+        const int i = i0 + 16 * b + c;
+        if (i >= n || d0 + r >= p.D) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWideWaves; ++v) s += red[v][r][c];
+        p.O[(size_t)list[i] * p.D + d0 + r] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Y[t] := alpha * sum_j w_j O[t, j] + beta * Y[t], choices in order.  grid:
+// (ceil(D/256), M).
+template <typename T>
+__global__ __launch_bounds__(256) void moe_combine(MoeParams p) {
+  const int t = blockIdx.y, d = blockIdx.x * 256 + threadIdx.x;
+  const float *prob = p.prob + t * p.k;
+  float den = 1.0f;
+  if (p.renorm) {
+    den = 0.0f;
+    for (int j = 0; j < p.k; ++j) den += prob[j];
+  }
+  if (blockIdx.x == 0 && p.weights && (int)threadIdx.x < p.k)
+    p.weights[t * p.k + threadIdx.x] = prob[threadIdx.x] / den;
+  if (d >= p.D) return;
+  const float *o = p.O + (size_t)t * p.k * p.D + d;
+  float s = 0.0f;
+  for (int j = 0; j < p.k; ++j) s += prob[j] / den * o[(size_t)j * p.D];
+  T *out = static_cast<T *>(p.Y) + (size_t)t * (size_t)p.ldy + d;
+  s *= p.alpha;
+  if (p.beta != 0.0f) s = __builtin_fmaf(p.beta, (float)*out, s);
+  *out = (T)s;
+}
+
 // ---------------------------------------------------------------- host side
 
 struct MoeSpace {
   double *logits;
-  float *prob, *H;
+  float *prob, *H, *O;
   unsigned *top;
   int *count, *list;
 };
 
-size_t carve(const MoeCall &c, void *base, MoeSpace *s) {
-  char *b = static_cast<char *>(base);
-  size_t used = 0;
-  auto take = [&](size_t bytes) {
-    char *p = b ? b + used : nullptr;
-    used += (bytes + 255) / 256 * 256;
-    return p;
-  };
-  s->logits = reinterpret_cast<double *>(take((size_t)c.M * c.E * sizeof(double)));
-  s->prob = reinterpret_cast<float *>(take((size_t)c.M * c.k * sizeof(float)));
-  s->top = reinterpret_cast<unsigned *>(take((size_t)c.M * c.k * sizeof(unsigned)));
-  s->H = reinterpret_cast<float *>(take((size_t)c.M * c.k * (size_t)c.F * sizeof(float)));
-  s->count = reinterpret_cast<int *>(take((size_t)c.E * sizeof(int)));
-  s->list = reinterpret_cast<int *>(take((size_t)c.E * c.M * sizeof(int)));
-  return used;
+// One pass over the outputs (moe_down) where an expert's tokens are likely to
+// fit the 8 of its blocks, else by expert with a pass that combines them.
+bool narrow(const MoeCall &c) {
+  return c.M <= 8 || (c.M <= kNarrowTokens && (long long)c.M * c.k <= 4LL * c.E);
 }
 
-// Weight rows a workgroup of `up` takes: 32 of F where that still makes two
+size_t carve(const MoeCall &c, void *base, MoeSpace *s) {
+  Carve w(base);
+  const size_t pairs = (size_t)c.M * c.k;
+  s->logits = w.take<double>((size_t)c.M * c.E);
+  s->prob = w.take<float>(pairs);
+  s->top = w.take<unsigned>(pairs);
+  s->H = w.take<float>(pairs * (size_t)c.F);
+  s->O = narrow(c) ? nullptr : w.take<float>(pairs * (size_t)c.D);
+  s->count = w.take<int>((size_t)c.E);
+  s->list = w.take<int>((size_t)c.E * c.M);
+  return w.used;
+}
+
+// Blocks of 16 weight rows a workgroup takes: 4 where that still makes two
 // workgroups per CU of the experts that some token is likely to choose, else
-// 16 or 8.
-int up_blocks(const MoeCall &c) {
+// 2 or 1 (an expert has `blocks` of them).
+int row_blocks(const MoeCall &c, int blocks) {
   const long long active = (long long)c.M * c.k < c.E ? (long long)c.M * c.k : c.E;
-  if (active * ((c.F + 31) / 32) >= 2 * kCUs) return 4;
-  return active * ((c.F + 15) / 16) >= 2 * kCUs ? 2 : 1;
+  if (active * ((blocks + 3) / 4) >= 2 * kCUs) return 4;
+  return active * ((blocks + 1) / 2) >= 2 * kCUs ? 2 : 1;
+}
+
+// Whether workgroups take several blocks of 16 tokens at a time, so that the
+// weights are read once for them: more than 8 tokens per expert on average.
+bool several_blocks(const MoeCall &c) {
+  return c.M > 16 && (long long)c.M * c.k > 8LL * c.E;
+}
+
+template <typename T, int NF, int NB, int P>
+void launch_up(const MoeCall &c, const MoeParams &p) {
+  constexpr int FS = 8 * NF / P;
+  hipLaunchKernelGGL((moe_up<T, NF, NB, P>), dim3((unsigned)((c.F + FS - 1) / FS), (unsigned)c.E),
+                     dim3(kUpWaves * kWave), 0, c.stream, p);
 }
 
 template <typename T, int NF>
 void launch_up(const MoeCall &c, const MoeParams &p) {
-  const dim3 g((unsigned)((c.F + 8 * NF - 1) / (8 * NF)), (unsigned)c.E), b(kUpWaves * kWave);
-  // more than 8 tokens per expert on average: several blocks of 16 at a time,
-  // so that the weights are read once for them
-  if (c.M > 16 && (long long)c.M * c.k > 8LL * c.E)
-    hipLaunchKernelGGL((moe_up<T, NF, 4>), g, b, 0, c.stream, p);
-  else
-    hipLaunchKernelGGL((moe_up<T, NF, 1>), g, b, 0, c.stream, p);
+  if (several_blocks(c)) launch_up<T, NF, 4, 1>(c, p);
+  else launch_up<T, NF, 1, 1>(c, p);
 }
 
 template <typename T>
 void launch_up(const MoeCall &c, const MoeParams &p) {
-  switch (up_blocks(c)) {
+  if (narrow(c)) {
+    switch (row_blocks(c, (2 * c.F + 7) / 8)) {
+      case 4: return launch_up<T, 4, 1, 2>(c, p);
+      case 2: return launch_up<T, 2, 1, 2>(c, p);
+      default: return launch_up<T, 1, 1, 2>(c, p);
+    }
+  }
+  switch (row_blocks(c, (2 * c.F + 15) / 16)) {
     case 4: return launch_up<T, 4>(c, p);
     case 2: return launch_up<T, 2>(c, p);
     default: return launch_up<T, 1>(c, p);
   }
 }
 
-template <typename T, int NW, int ROWS>
-void launch_down(const MoeCall &c, const MoeParams &p) {
-  hipLaunchKernelGGL((moe_down<T, NW, ROWS>), dim3((unsigned)((c.D + ROWS - 1) / ROWS)),
-                     dim3(NW * kWave),
-                     (size_t)NW * c.M * ROWS * 4 + (size_t)c.M * c.k * 2, c.stream, p);
+template <typename T, int ROWS>
+void launch_narrow(const MoeCall &c, const MoeParams &p) {
+  hipLaunchKernelGGL((moe_down<T, ROWS>), dim3((unsigned)((c.D + ROWS - 1) / ROWS)),
+                     dim3(kDownWaves * kWave),
+                     (size_t)kDownWaves * c.M * ROWS * 4 + (size_t)c.M * c.k * 2, c.stream, p);
 }
 
-// As many waves as their copies of the outputs leave room for in 64 KB of LDS;
-// fewer rows where more would leave CUs without a workgroup, as long as an
-// expert's tokens are likely to fit their block (beyond it its weights are
-// read again).
+template <typename T, int NF>
+void launch_wide(const MoeCall &c, const MoeParams &p) {
+  const dim3 g((unsigned)((c.D + 16 * NF - 1) / (16 * NF)), (unsigned)c.E), b(kWideWaves * kWave);
+  if (several_blocks(c)) hipLaunchKernelGGL((moe_down_wide<T, NF, 4>), g, b, 0, c.stream, p);
+  else hipLaunchKernelGGL((moe_down_wide<T, NF, 1>), g, b, 0, c.stream, p);
+}
+
 template <typename T>
-void launch_down(const MoeCall &c, const MoeParams &p) {
-  const long long pairs = (long long)c.M * c.k;
-  if (c.M > 128) launch_down<T, 4, 16>(c, p);
-  else if (c.M > 64) launch_down<T, 8, 16>(c, p);
-  else if (c.D < 8 * kCUs && (c.M <= 4 || pairs <= c.E)) launch_down<T, 16, 4>(c, p);
-  else if (c.D < 16 * kCUs && (c.M <= 8 || pairs <= 4LL * c.E)) launch_down<T, 16, 8>(c, p);
-  else launch_down<T, 16, 16>(c, p);
+hipError_t launch_down(const MoeCall &c, const MoeParams &p) {
+  if (narrow(c)) {
+    // 4 rows where 8 would leave CUs without a workgroup and 4 tokens are
+    // likely to be all that an expert has
+    if (c.D < 8 * kCUs && (c.M <= 4 || (long long)c.M * c.k <= c.E)) launch_narrow<T, 4>(c, p);
+    else launch_narrow<T, 8>(c, p);
+    return hipGetLastError();
+  }
+  switch (row_blocks(c, (c.D + 15) / 16)) {
+    case 4: launch_wide<T, 4>(c, p); break;
+    case 2: launch_wide<T, 2>(c, p); break;
+    default: launch_wide<T, 1>(c, p); break;
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_combine<T>), dim3((unsigned)((c.D + 255) / 256), (unsigned)c.M),
+                     dim3(256), 0, c.stream, p);
+  return hipGetLastError();
 }
 
 template <typename T>
@@ -493,6 +628,7 @@ hipError_t run(const MoeCall &c, const MoeSpace &s) {
   p.list = s.list;
   p.H = s.H;
   p.top = s.top;
+  p.O = s.O;
   p.Y = c.Y;
   p.ids = c.ids;
   p.weights = c.weights;
@@ -513,8 +649,7 @@ hipError_t run(const MoeCall &c, const MoeSpace &s) {
   launch_up<T>(c, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  launch_down<T>(c, p);
-  return hipGetLastError();
+  return launch_down<T>(c, p);
 }
 
 }  // namespace

@@ -108,7 +108,7 @@ __device__ __forceinline__ void stream_steps(const T *const (&w)[NF], int k, con
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const Frag xf = x.frag(xr[u][b]);
+      const Frag xf = x.frag(b, xr[u][b]);
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[u][f], xf, acc[f][b]);
     }
@@ -141,7 +141,7 @@ __device__ __forceinline__ void stream_mac(const T *const (&w)[NF], int k0, int 
     for (int f = 0; f < NF; ++f) wf[f] = load_frag(w[f], k + lk, lim);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const Frag xf = x.frag(x.masked(b, k + lk));
+      const Frag xf = x.frag(b, x.masked(b, k + lk));
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[f], xf, acc[f][b]);
     }
@@ -172,7 +172,7 @@ struct RowLoader {
   int lim;
   __device__ __forceinline__ Raw whole(int b, int k) const { return load_whole(row[b] + k); }
   __device__ __forceinline__ Raw masked(int b, int k) const { return load_frag(row[b], k, lim); }
-  __device__ __forceinline__ Raw frag(const Raw &r) const { return r; }
+  __device__ __forceinline__ Raw frag(int, const Raw &r) const { return r; }
 };
 
 // The adapter of a row: -1 when it has none (or an index out of range), or

@@ -36,54 +36,194 @@ struct ShrinkParams {
   int M, K, L, R, Rp, ldx, ldw;
 };
 
-// V[16 rows, 16 ranks] per workgroup and distinct adapter among the rows; the
-// waves divide K and their sums meet in LDS.  grid: (row blocks, rank blocks,
-// Z); workgroup z takes the distinct adapters z, z + Z, ... of its rows.
+// V[16 rows, 16 ranks] for the distinct adapters z, z + Z, ... among the rows:
+// the workgroup's waves divide K and their sums meet in LDS.
 template <typename T, bool KMAJ>
-__global__ __launch_bounds__(kShrinkThreads) void lora_shrink(ShrinkParams p) {
-  __shared__ float red[kShrinkWaves][16][17];
+__device__ __forceinline__ void shrink_block(const ShrinkParams &p, int row0, int r0, int z, int Z,
+                                             float (*red)[16][17]) {
   typedef typename El<T>::Frag Frag;
   constexpr int KS = El<T>::KSTEP;
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
-  const int row0 = blockIdx.x * 16, r0 = blockIdx.y * 16;
   const int row = row0 + li;
   int id = adapter_of(p.rows, row, p.M, p.L);
   if (id >= 0 && rank_of(p.ranks, id, p.R) <= r0) id = -1;
   unsigned left = (unsigned)(__ballot(id >= 0) & 0xffffu);
   const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-  if (blockIdx.z == 0 && threadIdx.x < 256 && row0 + tr < p.M && !((left >> tr) & 1))
+  if (z == 0 && threadIdx.x < 256 && row0 + tr < p.M && !((left >> tr) & 1))
     p.V[(size_t)(row0 + tr) * p.Rp + r0 + tc] = 0.0f;
-  const T *xrow = static_cast<const T *>(p.X) + (size_t)(row < p.M ? row : p.M - 1) * p.ldx;
+  // each wave a stretch of K, whole steps of at least 128 bytes a row long
+  constexpr int G = 2 * KS;
+  const int part = ((p.K + kShrinkWaves - 1) / kShrinkWaves + G - 1) / G * G;
+  const int k0 = wave * part;
+  const int k1 = k0 + part < p.K ? k0 + part : p.K;
+  RowLoader<T, 1> x;
+  x.row[0] = static_cast<const T *>(p.X) + (size_t)(row < p.M ? row : p.M - 1) * p.ldx;
+  x.lim = k1;
   for (int d = 0; left != 0; ++d) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
     const unsigned same = (unsigned)(__ballot(id == a) & 0xffffu);
     left &= ~same;
-    if (d % (int)gridDim.z != (int)blockIdx.z) continue;
+    if (d % Z != z) continue;
     const int rk = rank_of(p.ranks, a, p.R);
     const int r = r0 + li < rk ? r0 + li : rk - 1;
     const T *w = static_cast<const T *>(p.W) + (size_t)a * (size_t)p.stride;
-    f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
+    if constexpr (KMAJ) {
+      const T *wr[1] = {w + (size_t)r * p.ldw};
+      stream_mac<T, 4, 1>(wr, k0, k1, k1, k1, x, acc);
+    } else {
 #pragma unroll 4
-    for (int k = wave * KS; k < p.K; k += kShrinkWaves * KS) {
-      const int kk = k + lg * El<T>::VEC;
-      const Frag x = load_frag(xrow, kk, p.K);
-      Frag b;
-      if constexpr (KMAJ) b = load_frag(w + (size_t)r * p.ldw, kk, p.K);
-      else b = load_frag_strided<T>(w + r, p.ldw, kk, p.K);
-      acc = mma16(x, b, acc);
+      for (int k = k0; k < k1; k += KS) {
+        const int kk = k + lg * El<T>::VEC;
+        const Frag wf = load_frag_strided<T>(w + r, p.ldw, kk, k1);
+        acc[0][0] = mma16(wf, x.masked(0, kk), acc[0][0]);
+      }
     }
+    // the result holds ranks down its rows, activations across its columns
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[wave][4 * lg + j][li] = acc[j];
+    for (int j = 0; j < 4; ++j) red[wave][li][4 * lg + j] = acc[0][0][j];
     __syncthreads();
     if (threadIdx.x < 256 && ((same >> tr) & 1)) {
       float s = 0.0f;
 #pragma unroll
-      for (int w8 = 0; w8 < kShrinkWaves; ++w8) s += red[w8][tr][tc];
+      for (int v = 0; v < kShrinkWaves; ++v) s += red[v][tr][tc];
       p.V[(size_t)(row0 + tr) * p.Rp + r0 + tc] = r0 + tc < rk ? s : 0.0f;
     }
     __syncthreads();
   }
+}
+
+// grid: (row blocks, rank blocks, Z).
+template <typename T, bool KMAJ>
+__global__ __launch_bounds__(kShrinkThreads) void lora_shrink(ShrinkParams p) {
+  __shared__ float red[kShrinkWaves][16][17];
+  shrink_block<T, KMAJ>(p, blockIdx.x * 16, blockIdx.y * 16, blockIdx.z, gridDim.z, red);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Rows up to which the shared product is done here (a stream over W) rather
+// than by the tiled kernels.
+constexpr int kSkinnyRows = 64;
+
+struct SkinnyParams {
+  ShrinkParams shrink;
+  const void *W;          // N x K
+  float *S;               // parts x M x N: sums over a part of K each
+  int N, ldw, tiles, parts, chunk;
+  int blocks, ranks16, z; // the shrink workgroups, first in the grid
+};
+
+// The shared product X W^T over parts of K and, in the same launch, the
+// shrink step: neither needs the other.  A workgroup takes 16 NF / P rows of W
+// against NB blocks of 16 / P rows of X (all there are), its 8 waves dividing
+// its part of K.
+template <typename T, int NF, int NB, int P>
+__global__ __launch_bounds__(kShrinkThreads) void lora_skinny(SkinnyParams p) {
+  constexpr int BR = 16 / P;
+  constexpr int ROWS = BR * NF;
+  __shared__ float red[kShrinkWaves][ROWS < 16 ? 16 : ROWS][17];
+  int bid = blockIdx.x;
+  const int shrinks = p.blocks * p.ranks16 * p.z;
+  if (bid < shrinks) {
+    const int z = bid % p.z, q = bid / p.z;
+    shrink_block<T, true>(p.shrink, q % p.blocks * 16, q / p.blocks * 16, z, p.z,
+                          reinterpret_cast<float (*)[16][17]>(red));
+    return;
+  }
+  bid -= shrinks;
+  const int M = p.shrink.M, K = p.shrink.K;
+  const int n0 = bid % p.tiles * ROWS, part = bid / p.tiles;
+  const int lane = threadIdx.x % kWave, wave = wave_id();
+  const int li = lane % 16, lg = lane / 16;
+  const T *w[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    const int n = n0 + BR * f + li / P;
+    w[f] = static_cast<const T *>(p.W) + (size_t)(n < p.N ? n : p.N - 1) * (size_t)p.ldw;
+  }
+  RowLoader<T, NB> x;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int i = BR * b + li / P;
+    x.row[b] = static_cast<const T *>(p.shrink.X) + (size_t)(i < M ? i : M - 1) * p.shrink.ldx;
+  }
+  const int k0 = (part * kShrinkWaves + wave) * p.chunk;
+  const int k1 = k0 + p.chunk < K ? k0 + p.chunk : K;
+  x.lim = k1;
+  f32x4 acc[NF][NB];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[f][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  stream_mac<T, (NF * NB >= 8 ? 2 : 4), P>(w, k0, k1, k1, k1, x, acc);
+  float *out = p.S + (size_t)part * M * p.N;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (b > 0) __syncthreads();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      float v[4 / P];
+      diagonal_sum<P>(acc[f][b], v);
+      if (li % P == 0)
+#pragma unroll
+        for (int j = 0; j < 4 / P; ++j) red[wave][BR * f + 4 / P * lg + j][li / P] = v[j];
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < BR * ROWS; q += kShrinkThreads) {
+      const int c = q / ROWS, r = q % ROWS;
+      const int i = BR * b + c, n = n0 + r;
+      if (i >= M || n >= p.N) continue;
+      float s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < kShrinkWaves; ++v) s += red[v][r][c];
+      out[(size_t)i * p.N + n] = s;
+    }
+  }
+}
+
+struct JoinParams {
+  const float *S, *V;
+  const void *B;
+  void *Y;
+  const int *rows, *ranks;
+  const float *scale;
+  long long stride;
+  int M, N, L, R, Rp, ldb, ldy, parts;
+  float alpha, beta;
+};
+
+// Y := alpha * (the parts' sums + s_a B_a V) + beta * Y, one output a thread.
+// grid: (ceil(N/256), M).
+template <typename T>
+__global__ __launch_bounds__(256) void lora_join(JoinParams p) {
+  const int i = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= p.N) return;
+  const float *s = p.S + (size_t)i * p.N + n;
+  float sum = 0.0f;
+  for (int q = 0; q < p.parts; ++q) sum += s[(size_t)q * p.M * p.N];
+  const int a = adapter_of(p.rows, i, p.M, p.L);
+  if (a >= 0) {
+    const int rk = rank_of(p.ranks, a, p.R);
+    const T *u = static_cast<const T *>(p.B) + (size_t)a * (size_t)p.stride +
+                 (size_t)n * (size_t)p.ldb;
+    const float *v = p.V + (size_t)i * p.Rp;
+    float t = 0.0f;
+    constexpr int VEC = El<T>::VEC;
+    int r = 0;
+    for (; r + VEC <= rk; r += VEC) {
+      const typename El<T>::Frag f = load_whole(u + r);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) t = __builtin_fmaf((float)f[e], v[r + e], t);
+    }
+    for (; r < rk; ++r) t = __builtin_fmaf((float)u[r], v[r], t);
+    if (rk > 0) sum = __builtin_fmaf(p.scale ? p.scale[a] : 1.0f, t, sum);
+  }
+  T *y = static_cast<T *>(p.Y) + (size_t)i * (size_t)p.ldy + n;
+  float o = p.alpha * sum;
+  if (p.beta != 0.0f) o = __builtin_fmaf(p.beta, (float)*y, o);
+  *y = (T)o;
 }
 
 // ---------------------------------------------------------------- expand
@@ -324,9 +464,8 @@ __global__ __launch_bounds__(256) void lora_outer_sum(const float *P, float *D, 
 
 int rank_pad(int R) { return (R + 15) / 16 * 16; }
 
-template <typename T, bool KMAJ>
-hipError_t shrink(const LoraCall &c, const void *X, int ldx, int K, const void *W, int ldw,
-                  long long stride, float *V) {
+ShrinkParams shrink_params(const LoraCall &c, const void *X, int ldx, int K, const void *W,
+                           int ldw, long long stride, float *V) {
   ShrinkParams p;
   p.X = X;
   p.W = W;
@@ -341,11 +480,114 @@ hipError_t shrink(const LoraCall &c, const void *X, int ldx, int K, const void *
   p.Rp = rank_pad(c.R);
   p.ldx = ldx;
   p.ldw = ldw;
+  return p;
+}
+
+// Workgroups per block of 16 rows: one for each adapter that may be among
+// them while the blocks are few, so that a decode batch's adapters are read
+// side by side; longer batches mostly have one adapter per block.
+int shrink_z(const LoraCall &c) {
   const int blocks = (c.M + 15) / 16;
+  if (blocks > 64) return 1;
   const int z = c.L < 16 ? c.L : 16;
+  return z < c.M ? z : c.M;
+}
+
+template <typename T, bool KMAJ>
+hipError_t shrink(const LoraCall &c, const void *X, int ldx, int K, const void *W, int ldw,
+                  long long stride, float *V) {
+  const ShrinkParams p = shrink_params(c, X, ldx, K, W, ldw, stride, V);
   hipLaunchKernelGGL((lora_shrink<T, KMAJ>),
-                     dim3((unsigned)blocks, (unsigned)(p.Rp / 16), (unsigned)(blocks <= 64 ? z : 1)),
+                     dim3((unsigned)((c.M + 15) / 16), (unsigned)(p.Rp / 16),
+                          (unsigned)shrink_z(c)),
                      dim3(kShrinkThreads), 0, c.stream, p);
+  return hipGetLastError();
+}
+
+// The shape of a skinny product: blocks of 16 rows of W a workgroup takes, and
+// the parts K is divided into so that there are two workgroups per CU, each
+// wave with at least two steps.
+struct SkinnyPlan {
+  int P, NB, NF, tiles, parts, chunk;
+};
+
+SkinnyPlan skinny_plan(const LoraCall &c) {
+  SkinnyPlan s;
+  s.P = c.M <= 4 ? 4 : (c.M <= 8 ? 2 : 1);
+  const int br = 16 / s.P;
+  s.NB = (c.M + br - 1) / br;
+  const int kstep = (c.half ? 32 : 16) * s.P;
+  const int steps = (c.K + kstep - 1) / kstep;
+  const int most = steps / (2 * kShrinkWaves) > 1 ? steps / (2 * kShrinkWaves) : 1;
+  for (s.NF = 4;; s.NF /= 2) {
+    s.tiles = (c.N + br * s.NF - 1) / (br * s.NF);
+    s.parts = (2 * kCUs + s.tiles - 1) / s.tiles;
+    if (s.parts > most) s.parts = most;
+    if (s.NF == 1 || s.tiles * s.parts >= kCUs) break;
+  }
+  const int waves = s.parts * kShrinkWaves;
+  s.chunk = (steps + waves - 1) / waves * kstep;
+  s.parts = (c.K + kShrinkWaves * s.chunk - 1) / (kShrinkWaves * s.chunk);
+  return s;
+}
+
+template <typename T, int NF, int NB, int P>
+void launch_skinny(const SkinnyParams &p, hipStream_t stream) {
+  const unsigned wgs = (unsigned)(p.blocks * p.ranks16 * p.z + p.tiles * p.parts);
+  hipLaunchKernelGGL((lora_skinny<T, NF, NB, P>), dim3(wgs), dim3(kShrinkThreads), 0, stream, p);
+}
+
+template <typename T, int NF>
+void launch_skinny(const SkinnyPlan &s, const SkinnyParams &p, hipStream_t stream) {
+  if (s.P == 4) launch_skinny<T, NF, 1, 4>(p, stream);
+  else if (s.P == 2) launch_skinny<T, NF, 1, 2>(p, stream);
+  else if (s.NB == 1) launch_skinny<T, NF, 1, 1>(p, stream);
+  else if (s.NB == 2) launch_skinny<T, NF, 2, 1>(p, stream);
+  else if (s.NB == 3) launch_skinny<T, NF, 3, 1>(p, stream);
+  else launch_skinny<T, NF, 4, 1>(p, stream);
+}
+
+template <typename T>
+hipError_t skinny(const LoraCall &c, float *V, float *S) {
+  const SkinnyPlan s = skinny_plan(c);
+  SkinnyParams p;
+  p.shrink = shrink_params(c, c.X, c.ldx, c.K, c.A, c.lda, c.stride_a, V);
+  p.W = c.W;
+  p.S = S;
+  p.N = c.N;
+  p.ldw = c.ldw;
+  p.tiles = s.tiles;
+  p.parts = s.parts;
+  p.chunk = s.chunk;
+  p.blocks = (c.M + 15) / 16;
+  p.ranks16 = p.shrink.Rp / 16;
+  p.z = shrink_z(c);
+  if (s.NF == 4) launch_skinny<T, 4>(s, p, c.stream);
+  else if (s.NF == 2) launch_skinny<T, 2>(s, p, c.stream);
+  else launch_skinny<T, 1>(s, p, c.stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  JoinParams j;
+  j.S = S;
+  j.V = V;
+  j.B = c.B;
+  j.Y = c.Y;
+  j.rows = c.rows;
+  j.ranks = c.ranks;
+  j.scale = c.scale;
+  j.stride = c.stride_b;
+  j.M = c.M;
+  j.N = c.N;
+  j.L = c.L;
+  j.R = c.R;
+  j.Rp = p.shrink.Rp;
+  j.ldb = c.ldb;
+  j.ldy = c.ldy;
+  j.parts = s.parts;
+  j.alpha = c.alpha;
+  j.beta = c.beta;
+  hipLaunchKernelGGL((lora_join<T>), dim3((unsigned)((c.N + 255) / 256), (unsigned)c.M), dim3(256),
+                     0, c.stream, j);
   return hipGetLastError();
 }
 
@@ -424,7 +666,9 @@ struct LoraSpace {
 size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
   Carve w(base);
   s->V = w.take<float>((size_t)c.M * rank_pad(c.R));
-  s->T = c.half ? w.take<float>((size_t)c.M * (size_t)c.N) : nullptr;
+  if (c.M <= kSkinnyRows)
+    s->T = w.take<float>((size_t)skinny_plan(c).parts * c.M * (size_t)c.N);
+  else s->T = c.half ? w.take<float>((size_t)c.M * (size_t)c.N) : nullptr;
   return w.used;
 }
 
@@ -449,6 +693,7 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
 
 template <typename T>
 hipError_t run(const LoraCall &c, const LoraSpace &s) {
+  if (c.M <= kSkinnyRows) return skinny<T>(c, s.V, s.T);
   hipError_t e = shrink<T, true>(c, c.X, c.ldx, c.K, c.A, c.lda, c.stride_a, s.V);
   if (e != hipSuccess) return e;
   if (!c.half) {

@@ -25,7 +25,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 POISON_LIB = os.path.join(HERE, "libgemm_lds_poison.so")
 POISON_BUILD_DIR = os.path.join(HERE, "_build_lds_poison")
 SOURCES = ["api.hip", "gemm_f32.hip", "gemm_f16.hip", "gemm_valu.hip", "scale.hip", "splitk.hip",
-           "pack.hip", "probe.hip", "lora.hip", "moe.hip", "rows_api.hip"]
+           "pack.hip", "probe.hip", "gemm_f16_lora.hip", "lora.hip",
+           "moe.hip", "rows_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -56,7 +57,7 @@ def _compile(src, verbose=False, build_dir=BUILD_DIR, extra=()):
 # build verifies that no compiler-generated instruction in these sources
 # touches it: the asm's m0 writes then cannot disturb compiled code.  The
 # same assembly is checked for spills (and that of gemm_valu.hip).
-M0_ASM_SOURCES = ["gemm_f16.hip", "gemm_f32.hip"]
+M0_ASM_SOURCES = ["gemm_f16.hip", "gemm_f16_lora.hip", "gemm_f32.hip"]
 SPILL_ONLY_SOURCES = ["gemm_valu.hip"]
 
 

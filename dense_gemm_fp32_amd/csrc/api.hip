@@ -109,6 +109,7 @@ dgemm::Call make_call(int M, int N, int K, float alpha, const void *A, int lda, 
   c.ws_fixed_bytes = 0;
   c.pack_mode = g_pack_mode.load(std::memory_order_relaxed);
   c.streamk_mode = g_streamk_mode.load(std::memory_order_relaxed);
+  c.term = nullptr;
   c.stream = static_cast<hipStream_t>(stream);
   return c;
 }

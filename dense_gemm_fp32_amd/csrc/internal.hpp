@@ -7,6 +7,21 @@
 
 namespace dgemm {
 
+// A low-rank term that a product's accumulators start from (fp16 products):
+// scale[i] * sum_r V[i, r] U_a[n, r] in row i, column n, a = rows[i].  V: rows
+// of ldv halves, for every 16 ranks 16 high parts, then 16 low parts; U:
+// adapter a's rows of ranks at U + a*stride, row n at n*ldu; ranks NULL: R.
+struct LowRank {
+  const void *V;
+  int ldv;
+  const float *scale;
+  const void *U;
+  int ldu;
+  long long stride;
+  const int *rows, *ranks;
+  int L, R;
+};
+
 // One validated GEMM call, after quick returns have been taken: M, N, K > 0
 // and alpha != 0.
 struct Call {
@@ -54,6 +69,7 @@ struct Call {
   // streamk_geometry) whenever the four-wave 64x64 tile or a forced tile
   // configuration (1, 5, 6, 7) is taken.
   int streamk_mode;
+  const LowRank *term;   // launch_f16_lora only
   hipStream_t stream;
 };
 
@@ -195,6 +211,7 @@ size_t probe_out_bytes();
 double probe_flops(int dtype, int iters);
 hipError_t launch_probe(int dtype, int iters, const void *operands, float *out, hipStream_t s);
 hipError_t launch_f16(const Call &c);
+hipError_t launch_f16_lora(const Call &c);   // on top of *c.term
 
 // C := beta * C over an M x N matrix (beta == 0 writes zeros without reading).
 hipError_t launch_scale_f32(int M, int N, float beta, float *C, int ldc, hipStream_t s);

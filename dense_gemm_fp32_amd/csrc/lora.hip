@@ -29,7 +29,7 @@ constexpr int kShrinkThreads = kShrinkWaves * kWave;
 
 struct ShrinkParams {
   const void *X;          // M x K
-  const void *W;          // L adapters: R x K rows (KMAJ) or K x R (k down the rows)
+  const void *W;          // L adapters of R x K
   float *V;               // M x Rp
   const int *rows, *ranks;
   long long stride;
@@ -38,10 +38,9 @@ struct ShrinkParams {
 
 // V[16 rows, 16 ranks] for the distinct adapters z, z + Z, ... among the rows:
 // the workgroup's waves divide K and their sums meet in LDS.
-template <typename T, bool KMAJ>
+template <typename T>
 __device__ __forceinline__ void shrink_block(const ShrinkParams &p, int row0, int r0, int z, int Z,
                                              float (*red)[16][17]) {
-  typedef typename El<T>::Frag Frag;
   constexpr int KS = El<T>::KSTEP;
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
@@ -52,37 +51,56 @@ __device__ __forceinline__ void shrink_block(const ShrinkParams &p, int row0, in
   const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
   if (z == 0 && threadIdx.x < 256 && row0 + tr < p.M && !((left >> tr) & 1))
     p.V[(size_t)(row0 + tr) * p.Rp + r0 + tc] = 0.0f;
-  // each wave a stretch of K, whole steps of at least 128 bytes a row long
-  constexpr int G = 2 * KS;
+  // each wave a stretch of K, whole steps of 256 bytes a row long
+  constexpr int G = 4 * KS;
   const int part = ((p.K + kShrinkWaves - 1) / kShrinkWaves + G - 1) / G * G;
   const int k0 = wave * part;
   const int k1 = k0 + part < p.K ? k0 + part : p.K;
-  RowLoader<T, 1> x;
-  x.row[0] = static_cast<const T *>(p.X) + (size_t)(row < p.M ? row : p.M - 1) * p.ldx;
-  x.lim = k1;
   for (int d = 0; left != 0; ++d) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
     const unsigned same = (unsigned)(__ballot(id == a) & 0xffffu);
     left &= ~same;
     if (d % Z != z) continue;
     const int rk = rank_of(p.ranks, a, p.R);
-    const int r = r0 + li < rk ? r0 + li : rk - 1;
     const T *w = static_cast<const T *>(p.W) + (size_t)a * (size_t)p.stride;
-    f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
-    if constexpr (KMAJ) {
+    const int n = __popc(same);
+    if (n <= 4) {
+      // few rows, as in a decode batch: 4 of them and 4 ranks by 4 stretches of
+      // k in an instruction, so that the adapter is read in whole lines
+      const int c = li / 4;
+      unsigned m = same;
+      for (int i = 0; i < c; ++i) m = (m & (m - 1)) ? m & (m - 1) : m;
+      RowLoader<T, 1> x4;
+      x4.row[0] = static_cast<const T *>(p.X) + (size_t)(row0 + __builtin_ctz(m)) * p.ldx;
+      x4.lim = k1;
+      const T *wr[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int r = r0 + 4 * f + c;
+        wr[f] = w + (size_t)(r < rk ? r : rk - 1) * p.ldw;
+      }
+      f32x4 acc[4][1];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) acc[f][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      stream_mac<T, 4, 4>(wr, k0, k1, k1, k1, x4, acc);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        float v[1];
+        diagonal_sum<4>(acc[f][0], v);
+        if (li % 4 == 0 && c < n) red[wave][__builtin_ctz(m)][4 * f + lg] = v[0];
+      }
+    } else {
+      const int r = r0 + li < rk ? r0 + li : rk - 1;
+      RowLoader<T, 1> x;
+      x.row[0] = static_cast<const T *>(p.X) + (size_t)(row < p.M ? row : p.M - 1) * p.ldx;
+      x.lim = k1;
+      f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
       const T *wr[1] = {w + (size_t)r * p.ldw};
       stream_mac<T, 4, 1>(wr, k0, k1, k1, k1, x, acc);
-    } else {
-#pragma unroll 4
-      for (int k = k0; k < k1; k += KS) {
-        const int kk = k + lg * El<T>::VEC;
-        const Frag wf = load_frag_strided<T>(w + r, p.ldw, kk, k1);
-        acc[0][0] = mma16(wf, x.masked(0, kk), acc[0][0]);
-      }
-    }
-    // the result holds ranks down its rows, activations across its columns
+      // the result holds ranks down its rows, activations across its columns
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[wave][li][4 * lg + j] = acc[0][0][j];
+      for (int j = 0; j < 4; ++j) red[wave][li][4 * lg + j] = acc[0][0][j];
+    }
     __syncthreads();
     if (threadIdx.x < 256 && ((same >> tr) & 1)) {
       float s = 0.0f;
@@ -92,13 +110,6 @@ __device__ __forceinline__ void shrink_block(const ShrinkParams &p, int row0, in
     }
     __syncthreads();
   }
-}
-
-// grid: (row blocks, rank blocks, Z).
-template <typename T, bool KMAJ>
-__global__ __launch_bounds__(kShrinkThreads) void lora_shrink(ShrinkParams p) {
-  __shared__ float red[kShrinkWaves][16][17];
-  shrink_block<T, KMAJ>(p, blockIdx.x * 16, blockIdx.y * 16, blockIdx.z, gridDim.z, red);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -120,7 +131,7 @@ struct SkinnyParams {
 // against NB blocks of 16 / P rows of X (all there are), its 8 waves dividing
 // its part of K.
 template <typename T, int NF, int NB, int P>
-__global__ __launch_bounds__(kShrinkThreads) void lora_skinny(SkinnyParams p) {
+__global__ __launch_bounds__(kShrinkThreads, 4) void lora_skinny(SkinnyParams p) {
   constexpr int BR = 16 / P;
   constexpr int ROWS = BR * NF;
   __shared__ float red[kShrinkWaves][ROWS < 16 ? 16 : ROWS][17];
@@ -128,7 +139,7 @@ __global__ __launch_bounds__(kShrinkThreads) void lora_skinny(SkinnyParams p) {
   const int shrinks = p.blocks * p.ranks16 * p.z;
   if (bid < shrinks) {
     const int z = bid % p.z, q = bid / p.z;
-    shrink_block<T, true>(p.shrink, q % p.blocks * 16, q / p.blocks * 16, z, p.z,
+    shrink_block<T>(p.shrink, q % p.blocks * 16, q / p.blocks * 16, z, p.z,
                           reinterpret_cast<float (*)[16][17]>(red));
     return;
   }
@@ -226,6 +237,224 @@ __global__ __launch_bounds__(256) void lora_join(JoinParams p) {
   *y = (T)o;
 }
 
+// ---------------------------------------------------------------- many rows: shrink
+
+// One first product of a call: V = X A^T (kmaj) or G = dY B (B's rows run
+// along the ranks).
+struct ShrinkJob {
+  const void *X;          // M x K
+  const void *W;          // L adapters: R x K (kmaj) or K x R
+  long long stride;
+  int K, ldx, ldw, kmaj, chunk;
+  float *S;               // parts x M x Rp: sums over a part of K each
+  float *V;               // M x Rp (NULL: not wanted)
+  _Float16 *split;        // M x 2 Rp: high and low parts (NULL: not wanted)
+  float *scale;           // M: what a row of `split` is to be multiplied by
+};
+
+struct TileShrinkParams {
+  ShrinkJob job[2];
+  const int *rows, *ranks;
+  const int *start, *perm;   // rows in adapter order (NULL: as they come)
+  const float *ascale;
+  int M, L, R, Rp, parts, z;
+};
+
+constexpr int kShrinkTile = 64;   // rows, and ranks, of a workgroup's tile
+
+// S[part][rows, ranks] of 64 rows by 64 ranks over a part of K.  Both tiles go
+// through LDS in steps of 128 bytes a row, 16-byte pieces XOR-swizzled by row,
+// the next step's loads in flight behind this one's products: every piece of X
+// is loaded once per adapter among the rows, in whole lines.  Rows in adapter
+// order (perm) have one adapter per tile but where two meet.  grid: (row
+// tiles, rank tiles * parts * z, jobs); workgroup z takes the distinct adapters
+// z, z + Z, ... of its rows.
+template <typename T>
+__global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
+  constexpr int VEC = El<T>::VEC;
+  constexpr int BK = 128 / (int)sizeof(T);
+  __shared__ __attribute__((aligned(16))) char lds[2][2][kShrinkTile * 128];
+  typedef typename El<T>::Frag Frag;
+  const ShrinkJob j = p.job[blockIdx.z];
+  const int lane = threadIdx.x % kWave, wave = wave_id();
+  const int li = lane % 16, lg = lane / 16;
+  const int zi = blockIdx.y % p.z, part = blockIdx.y / p.z % p.parts;
+  const int r0 = blockIdx.y / p.z / p.parts * kShrinkTile;
+  const int k0 = part * j.chunk;
+  const int k1 = k0 + j.chunk < j.K ? k0 + j.chunk : j.K;
+  if (k0 >= j.K) return;
+  const int count = p.perm ? p.start[p.L] : p.M;
+  const int pos0 = blockIdx.x * kShrinkTile;
+  if (pos0 >= count) return;
+  // the row at each position of the tile, one a lane
+  const int pos = pos0 + lane < count ? pos0 + lane : count - 1;
+  const int row = p.perm ? p.perm[pos] : pos;
+  int id = pos0 + lane < count ? adapter_of(p.rows, row, p.M, p.L) : -1;
+  if (id >= 0 && rank_of(p.ranks, id, p.R) <= r0) id = -1;
+  unsigned long long left = __ballot(id >= 0);
+  // X: this thread loads piece c of tile rows t, t + 32
+  const int c = threadIdx.x % 8, t = threadIdx.x / 8;
+  const T *x[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    x[q] = static_cast<const T *>(j.X) + (size_t)__shfl(row, t + 32 * q) * (size_t)j.ldx;
+  for (int d = 0; left != 0; ++d) {
+    const int src = __builtin_ctzll(left);
+    const int a = __builtin_amdgcn_readlane(id, src);
+    const unsigned long long same = __ballot(id == a);
+    left &= ~same;
+    if (d % p.z != zi) continue;
+    const int rk = rank_of(p.ranks, a, p.R);
+    const int nr = rk - r0 < kShrinkTile ? rk - r0 : kShrinkTile;   // ranks of this tile
+    const int nb = (nr + 15) / 16;
+    const T *w = static_cast<const T *>(j.W) + (size_t)a * (size_t)j.stride;
+    Frag xr[2], wr[2];
+    // pieces of W: (rank, k piece) of a rank-major tile, (k, rank piece) of the other
+    const int per = j.kmaj ? 8 : (16 * nb + VEC - 1) / VEC;   // pieces per row
+    const int pieces = j.kmaj ? 16 * nb * 8 : BK * per;
+    auto load = [&](int k) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) xr[q] = load_frag(x[q], k + c * VEC, k1);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = threadIdx.x + 256 * q;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) wr[q][e] = (T)0.0f;
+        if (i >= pieces) continue;
+        const int u = i / per, v = i % per;
+        if (j.kmaj) {
+          if (u < nr) wr[q] = load_frag(w + (size_t)(r0 + u) * (size_t)j.ldw, k + v * VEC, k1);
+        } else if (k + u < k1) {
+          wr[q] = load_frag(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, rk);
+        }
+      }
+    };
+    auto store = [&](int slot) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<Frag *>(lds[slot][0] + (t + 32 * q) * 128 + 16 * (c ^ (t & 7))) = xr[q];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = threadIdx.x + 256 * q;
+        if (i >= pieces) continue;
+        const int u = i / per, v = i % per;
+        if (j.kmaj) {
+          *reinterpret_cast<Frag *>(lds[slot][1] + u * 128 + 16 * (v ^ (u & 7))) = wr[q];
+        } else {
+          // k u of ranks v*VEC .. +VEC-1
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const int r = v * VEC + e;
+            *reinterpret_cast<T *>(lds[slot][1] + r * 128 + 16 * ((u / VEC) ^ (r & 7)) +
+                                   u % VEC * sizeof(T)) = wr[q][e];
+          }
+        }
+      }
+    };
+    f32x4 acc[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    load(k0);
+    store(0);
+    __syncthreads();
+    int slot = 0;
+    for (int k = k0; k < k1; k += BK, slot ^= 1) {
+      const bool more = k + BK < k1;
+      if (more) load(k + BK);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int xrow = 16 * wave + li;
+        const Frag xf = *reinterpret_cast<const Frag *>(lds[slot][0] + xrow * 128 +
+                                                        16 * ((4 * s + lg) ^ (xrow & 7)));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (b >= nb) break;
+          const int wrow = 16 * b + li;
+          const Frag wf = *reinterpret_cast<const Frag *>(lds[slot][1] + wrow * 128 +
+                                                          16 * ((4 * s + lg) ^ (wrow & 7)));
+          acc[b] = mma16(xf, wf, acc[b]);
+        }
+      }
+      if (more) store(slot ^ 1);
+      __syncthreads();
+    }
+    // rows 16 wave + 4 lg + e of the tile, ranks r0 + 16 b + li
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * wave + 4 * lg + e;
+      const int m = __shfl(row, i);
+      if (!((same >> i) & 1)) continue;
+      float *out = j.S + ((size_t)part * p.M + m) * p.Rp + r0 + li;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b < nb) out[16 * b] = acc[b][e];
+    }
+  }
+}
+
+// Sums the parts of each row's V, a wave a row: as fp32, and as the pairs of
+// halves that the fp16 product takes, scaled to [2^14, 2^15) by the row's power
+// of two so that neither range nor the low part is lost (22 bits of every
+// number within 2^-17 of the row's largest).  grid: (ceil(M/4), jobs).
+__global__ __launch_bounds__(256) void lora_shrink_sum(TileShrinkParams p) {
+  const ShrinkJob j = p.job[blockIdx.y];
+  const int lane = threadIdx.x % kWave, row = blockIdx.x * 4 + wave_id();
+  if (row >= p.M) return;
+  const int a = adapter_of(p.rows, row, p.M, p.L);
+  const int rk = a >= 0 ? rank_of(p.ranks, a, p.R) : 0;
+  const int used = (j.K + j.chunk - 1) / j.chunk;
+  float v[4];
+  float top = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = lane + 64 * q;
+    v[q] = 0.0f;
+    if (r < rk) {
+      const float *s = j.S + (size_t)row * p.Rp + r;
+      for (int u = 0; u < used; ++u) v[q] += s[(size_t)u * p.M * p.Rp];
+    }
+    top = fmaxf(top, fabsf(v[q]));
+    if (j.V && r < p.Rp) j.V[(size_t)row * p.Rp + r] = v[q];
+  }
+  if (!j.split) return;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  const int e = row_exponent(__builtin_bit_cast(unsigned, top));
+  const float down = ldexpf(1.0f, -e);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = lane + 64 * q;
+    if (r >= p.Rp) continue;
+    const float f = v[q] * down;
+    const _Float16 hi = (_Float16)f;
+    const float rest = f - (float)hi;
+    _Float16 *o = j.split + (size_t)row * (2 * p.Rp) + r / 16 * 32 + r % 16;
+    o[0] = hi;
+    o[16] = (_Float16)(rest == rest ? rest : 0.0f);   // an infinity has no rest
+  }
+  if (lane == 0) j.scale[row] = ldexpf(a >= 0 && p.ascale ? p.ascale[a] : 1.0f, e);
+}
+
+// T_a[k, r] = A_a[r, k] for the adapters that some row has, ranks padded with
+// zeros to Rp: the right operand of G A as the fp16 product takes it.  grid:
+// (ceil(K/256), L).
+__global__ __launch_bounds__(256) void lora_transpose(const _Float16 *A, int lda, long long stride,
+                                                      const int *start, const int *ranks, int K,
+                                                      int R, int Rp, _Float16 *out) {
+  const int a = blockIdx.y, k = blockIdx.x * 256 + threadIdx.x;
+  if (start[a + 1] == start[a] || k >= K) return;
+  const int rk = rank_of(ranks, a, R);
+  const _Float16 *src = A + (size_t)a * (size_t)stride + k;
+  _Float16 *dst = out + ((size_t)a * K + k) * Rp;
+  for (int r = 0; r < Rp; r += 8) {
+    f16x8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      f[e] = r + e < rk ? src[(size_t)(r + e) * (size_t)lda] : (_Float16)0.0f;
+    *reinterpret_cast<f16x8 *>(dst + r) = f;
+  }
+}
+
 // ---------------------------------------------------------------- expand
 
 struct ExpandParams {
@@ -317,20 +546,6 @@ __global__ __launch_bounds__(256) void scale_batch(int rows, int cols, float bet
   }
 }
 
-// Y := alpha * T + beta * Y, T fp32 M x N dense, Y fp16.
-__global__ __launch_bounds__(256) void lora_finish(const float *T, _Float16 *Y, int M, int N,
-                                                   int ldy, float alpha, float beta) {
-  const long long total = (long long)M * N;
-  for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total;
-       t += (long long)gridDim.x * 256) {
-    const long long i = t / N;
-    _Float16 *y = Y + (size_t)i * (size_t)ldy + (t - i * N);
-    float o = alpha * T[t];
-    if (beta != 0.0f) o = __builtin_fmaf(beta, (float)*y, o);
-    *y = (_Float16)o;
-  }
-}
-
 // ---------------------------------------------------------------- rows of each adapter
 
 // perm[start[a] .. start[a+1]) := the rows of adapter a, in order.  One
@@ -389,74 +604,146 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group(const int *rows, int
 
 // ---------------------------------------------------------------- dA, dB
 
-struct OuterParams {
-  const float *V;         // M x Rp (G or V)
-  const void *X;          // M x K (X or dY)
-  float *P;               // partial sums: S x L x Rp x K
-  const int *start, *perm;
-  int K, L, Rp, ldx, S;
+// One gradient of a call: D_a[r, k] (or, tr, D_a[k, r]) := alpha * s_a * sum
+// over a's rows of V[i, r] X[i, k] + beta * D_a.
+struct OuterJob {
+  const float *V;         // M x Rp
+  const void *X;          // M x K
+  float *D;
+  long long stride;
+  int K, ldx, ldd, tr;
+  float *P;               // partial sums: (chunks + L) x Rp x K
 };
 
-// P[s, a, r, k] = sum over part s of adapter a's rows of V[i, r] X[i, k]: fp32
-// products.  grid: (L * Rp/16, ceil(K/256), S); 16 ranks x 64 columns a wave.
+struct OuterParams {
+  OuterJob job[2];
+  const int *rows, *ranks, *start, *perm;
+  const float *scale;
+  int L, R, Rp, chunk;    // rows, in adapter order, per chunk
+  float alpha, beta;
+};
+
+constexpr int kOuterWaves = 8;
+constexpr int kOuterThreads = kOuterWaves * kWave;
+constexpr int kOuterCols = 128;    // columns of X a workgroup takes
+constexpr int kOuterRanks = 32;    // ranks a workgroup takes
+
+// P[chunk + a] = the sums over the rows of adapter a in a chunk of the rows in
+// adapter order.  chunk + a names a slot of its own: along the order either
+// number only ever grows.  A lane loads 8 consecutive columns of one row (a
+// row's 128 columns in whole lines); element e of the lanes is the right operand
+// of product e, whose 16 columns are then 8 apart, and four rows make one
+// step.  The products are fp32: V is, and with the ranks as few as they are the
+// pass over X costs more.  The waves take the steps in turn and their sums
+// meet in LDS.  grid: (column tiles, chunks, jobs * rank tiles).
 template <typename T>
-__global__ __launch_bounds__(256) void lora_outer(OuterParams p) {
+__global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
+  __shared__ float red[kOuterWaves][16][kOuterCols + 4];
+  constexpr int NR = kOuterRanks / 16;
+  constexpr int VEC = El<T>::VEC;
+  const int rtiles = (p.Rp + kOuterRanks - 1) / kOuterRanks;
+  const OuterJob j = p.job[blockIdx.z / rtiles];
+  const int r0 = blockIdx.z % rtiles * kOuterRanks;
+  const int k0 = blockIdx.x * kOuterCols;
+  if (k0 >= j.K) return;
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
-  const int rblocks = p.Rp / 16;
-  const int a = blockIdx.x / rblocks, r0 = blockIdx.x % rblocks * 16;
-  const int k0 = blockIdx.y * 256 + wave * 64;
-  if (k0 >= p.K) return;
-  const int b = p.start[a], n = p.start[a + 1] - b;
-  const int chunk = (n + p.S - 1) / p.S;
-  const int i0 = blockIdx.z * chunk;
-  const int i1 = i0 + chunk < n ? i0 + chunk : n;
-  f32x4 acc[4];
+  const int kc = k0 + 8 * li;
+  const int total = p.start[p.L];
+  int at = blockIdx.y * p.chunk;
+  const int end = at + p.chunk < total ? at + p.chunk : total;
+  while (at < end) {
+    const int a = p.rows[p.perm[at]];
+    const int stop = p.start[a + 1] < end ? p.start[a + 1] : end;
+    const int rk = rank_of(p.ranks, a, p.R);
+    const int nb = rk - r0 <= 0 ? 0 : (rk - r0 > 16 ? NR : 1);
+    if (nb > 0) {
+      f32x4 acc[NR][8];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = i0; i < i1; i += 4) {
-    const bool ok = i + lg < i1;
-    const int row = ok ? p.perm[b + i + lg] : 0;
-    const float v = ok ? p.V[(size_t)row * p.Rp + r0 + li] : 0.0f;
-    const T *x = static_cast<const T *>(p.X) + (size_t)row * (size_t)p.ldx;
+      for (int b = 0; b < NR; ++b)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int k = k0 + 16 * c + li;
-      const float xv = ok && k < p.K ? (float)x[k] : 0.0f;
-      acc[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, xv, acc[c], 0, 0, 0);
+        for (int e = 0; e < 8; ++e) acc[b][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      constexpr int U = 4;               // steps loaded together
+      for (int i0 = at + 4 * U * wave; i0 < stop; i0 += 4 * U * kOuterWaves) {
+        float v[U][NR];
+        float x[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + 4 * u + lg;
+          const bool ok = i < stop;
+          const int row = p.perm[ok ? i : stop - 1];
+          const float *vr = j.V + (size_t)row * p.Rp + r0 + li;
+#pragma unroll
+          for (int b = 0; b < NR; ++b) v[u][b] = ok && b < nb ? vr[16 * b] : 0.0f;
+          const T *xr = static_cast<const T *>(j.X) + (size_t)row * (size_t)j.ldx;
+          // rows behind the last enter as zeros on both sides
+          const int lim = ok ? j.K : 0;
+#pragma unroll
+          for (int h = 0; h < 8; h += VEC) {
+            const typename El<T>::Frag f = load_frag(xr, kc + h, lim);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[u][h + e] = (float)f[e];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int b = 0; b < NR; ++b)
+            if (b < nb)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                acc[b][e] =
+                    __builtin_amdgcn_mfma_f32_16x16x4f32(v[u][b], x[u][e], acc[b][e], 0, 0, 0);
+      }
+      float *out = j.P + (size_t)(blockIdx.y + a) * p.Rp * j.K;
+#pragma unroll
+      for (int b = 0; b < NR; ++b) {
+        if (b >= nb) break;
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 8; e += 4)
+            *reinterpret_cast<f32x4 *>(&red[wave][4 * lg + q][8 * li + e]) =
+                f32x4{acc[b][e][q], acc[b][e + 1][q], acc[b][e + 2][q], acc[b][e + 3][q]};
+        __syncthreads();
+        for (int q = threadIdx.x; q < 16 * kOuterCols; q += kOuterThreads) {
+          const int r = q / kOuterCols, k = q % kOuterCols;
+          if (k0 + k >= j.K) continue;
+          float s = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kOuterWaves; ++w) s += red[w][r][k];
+          out[(size_t)(r0 + 16 * b + r) * j.K + k0 + k] = s;
+        }
+      }
     }
-  }
-  float *out = p.P + ((size_t)blockIdx.z * p.L + a) * (size_t)p.Rp * p.K;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int k = k0 + 16 * c + li;
-    if (k >= p.K) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) out[(size_t)(r0 + 4 * lg + j) * p.K + k] = acc[c][j];
+    at = stop;
   }
 }
 
-// D_a[r, k] (or, TR, D_a[k, r]) := alpha * s_a * sum_s P[s, a, r, k] + beta * D.
-template <bool TR>
-__global__ __launch_bounds__(256) void lora_outer_sum(const float *P, float *D, int ldd,
-                                                      long long stride, const float *scale,
-                                                      const int *ranks, int K, int L, int R,
-                                                      int Rp, int S, float alpha, float beta) {
+// grid: (blocks, L, jobs).
+__global__ __launch_bounds__(256) void lora_outer_sum(OuterParams p) {
+  const OuterJob j = p.job[blockIdx.z];
   const int a = blockIdx.y;
-  const int rk = rank_of(ranks, a, R);
-  const float s = alpha * (scale ? scale[a] : 1.0f);
-  const long long total = (long long)R * K;
+  const int rk = rank_of(p.ranks, a, p.R);
+  const int b = p.start[a], n = p.start[a + 1] - b;
+  const int c0 = b / p.chunk, c1 = n > 0 ? (b + n - 1) / p.chunk : c0 - 1;
+  const float s = p.alpha * (p.scale ? p.scale[a] : 1.0f);
+  const long long total = (long long)p.R * j.K;
+  const size_t slot = (size_t)p.Rp * j.K;
   for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total;
        t += (long long)gridDim.x * 256) {
-    const int r = TR ? (int)(t % R) : (int)(t / K);
-    const int k = TR ? (int)(t / R) : (int)(t % K);
+    const int r = j.tr ? (int)(t % p.R) : (int)(t / j.K);
+    const int k = j.tr ? (int)(t / p.R) : (int)(t % j.K);
     float sum = 0.0f;
-    if (r < rk)
-      for (int q = 0; q < S; ++q) sum += P[(((size_t)q * L + a) * Rp + r) * K + k];
-    float *d = D + (size_t)a * (size_t)stride +
-               (TR ? (size_t)k * (size_t)ldd + r : (size_t)r * (size_t)ldd + k);
-    const float o = r < rk ? s * sum : 0.0f;
-    *d = beta != 0.0f ? __builtin_fmaf(beta, *d, o) : o;
+    if (r < rk) {
+      const float *q = j.P + (size_t)(c0 + a) * slot + (size_t)r * j.K + k;
+      for (int c = c0; c <= c1; ++c, q += slot) sum += *q;
+    }
+    float *d = j.D + (size_t)a * (size_t)j.stride +
+               (j.tr ? (size_t)k * (size_t)j.ldd + r : (size_t)r * (size_t)j.ldd + k);
+    const float o = r < rk && n > 0 ? s * sum : 0.0f;
+    *d = p.beta != 0.0f ? __builtin_fmaf(p.beta, *d, o) : o;
   }
 }
 
@@ -493,19 +780,70 @@ int shrink_z(const LoraCall &c) {
   return z < c.M ? z : c.M;
 }
 
-template <typename T, bool KMAJ>
-hipError_t shrink(const LoraCall &c, const void *X, int ldx, int K, const void *W, int ldw,
-                  long long stride, float *V) {
-  const ShrinkParams p = shrink_params(c, X, ldx, K, W, ldw, stride, V);
-  hipLaunchKernelGGL((lora_shrink<T, KMAJ>),
-                     dim3((unsigned)((c.M + 15) / 16), (unsigned)(p.Rp / 16),
-                          (unsigned)shrink_z(c)),
-                     dim3(kShrinkThreads), 0, c.stream, p);
+// First products of a call with many rows (one or two jobs): the parts K is
+// divided into, so that there are about four workgroups per CU, and the
+// workgroups per tile of 64 rows that share its adapters out.  Tiles of long
+// batches mostly hold one adapter; in a batch of some hundred rows every row may
+// have its own.
+struct TilePlan {
+  int tiles, rtiles, parts, z;
+};
+
+TilePlan tile_plan(const LoraCall &c, bool ordered) {
+  TilePlan t;
+  t.tiles = (c.M + kShrinkTile - 1) / kShrinkTile;
+  t.rtiles = (rank_pad(c.R) + kShrinkTile - 1) / kShrinkTile;
+  const int bk = c.half ? 64 : 32;
+  const int longest = c.K > c.N ? c.K : c.N;
+  const int most = (longest + 4 * bk - 1) / (4 * bk);   // at least four steps a part
+  int parts = 4 * kCUs / (t.tiles * t.rtiles);
+  parts = parts < 8 ? parts : 8;
+  parts = parts < most ? parts : most;
+  t.parts = parts > 1 ? parts : 1;
+  int z = ordered ? 2 : 4 * kCUs / (t.tiles * t.rtiles * t.parts);
+  z = z < c.L ? z : c.L;
+  z = z < kShrinkTile ? z : kShrinkTile;
+  t.z = z > 1 ? z : 1;
+  return t;
+}
+
+int tile_chunk(const LoraCall &c, const TilePlan &t, int K) {
+  const int bk = c.half ? 64 : 32;
+  return ((K + t.parts - 1) / t.parts + bk - 1) / bk * bk;
+}
+
+template <typename T>
+hipError_t shrink_tiles(const LoraCall &c, const TileShrinkParams &p, const TilePlan &t,
+                        int jobs) {
+  hipLaunchKernelGGL((lora_shrink_tile<T>),
+                     dim3((unsigned)t.tiles, (unsigned)(t.rtiles * t.parts * t.z),
+                          (unsigned)jobs),
+                     dim3(256), 0, c.stream, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(lora_shrink_sum, dim3((unsigned)((c.M + 3) / 4), (unsigned)jobs), dim3(256), 0,
+                     c.stream, p);
   return hipGetLastError();
 }
 
+TileShrinkParams tile_params(const LoraCall &c, const TilePlan &t) {
+  TileShrinkParams p = {};
+  p.rows = c.rows;
+  p.ranks = c.ranks;
+  p.ascale = c.scale;
+  p.M = c.M;
+  p.L = c.L;
+  p.R = c.R;
+  p.Rp = rank_pad(c.R);
+  p.parts = t.parts;
+  p.z = t.z;
+  return p;
+}
+
 // The shape of a skinny product: blocks of 16 rows of W a workgroup takes, and
-// the parts K is divided into so that there are two workgroups per CU, each
+// the parts K is divided into so that there is one workgroup per CU (the adapters beside
+// them then fit in too, two to a CU: 8 parts 18.5 us, 4 parts 14.8 us at 48 x
+// 4096 x 4096), each
 // wave with at least two steps.
 struct SkinnyPlan {
   int P, NB, NF, tiles, parts, chunk;
@@ -521,7 +859,7 @@ SkinnyPlan skinny_plan(const LoraCall &c) {
   const int most = steps / (2 * kShrinkWaves) > 1 ? steps / (2 * kShrinkWaves) : 1;
   for (s.NF = 4;; s.NF /= 2) {
     s.tiles = (c.N + br * s.NF - 1) / (br * s.NF);
-    s.parts = (2 * kCUs + s.tiles - 1) / s.tiles;
+    s.parts = kCUs / s.tiles > 1 ? kCUs / s.tiles : 1;
     if (s.parts > most) s.parts = most;
     if (s.NF == 1 || s.tiles * s.parts >= kCUs) break;
   }
@@ -565,29 +903,6 @@ hipError_t skinny(const LoraCall &c, float *V, float *S) {
   if (s.NF == 4) launch_skinny<T, 4>(s, p, c.stream);
   else if (s.NF == 2) launch_skinny<T, 2>(s, p, c.stream);
   else launch_skinny<T, 1>(s, p, c.stream);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  JoinParams j;
-  j.S = S;
-  j.V = V;
-  j.B = c.B;
-  j.Y = c.Y;
-  j.rows = c.rows;
-  j.ranks = c.ranks;
-  j.scale = c.scale;
-  j.stride = c.stride_b;
-  j.M = c.M;
-  j.N = c.N;
-  j.L = c.L;
-  j.R = c.R;
-  j.Rp = p.shrink.Rp;
-  j.ldb = c.ldb;
-  j.ldy = c.ldy;
-  j.parts = s.parts;
-  j.alpha = c.alpha;
-  j.beta = c.beta;
-  hipLaunchKernelGGL((lora_join<T>), dim3((unsigned)((c.N + 255) / 256), (unsigned)c.M), dim3(256),
-                     0, c.stream, j);
   return hipGetLastError();
 }
 
@@ -623,78 +938,141 @@ unsigned flat_grid(long long total) {
   return (unsigned)(b < 1 ? 1 : (b > 8192 ? 8192 : b));
 }
 
-int outer_parts(const LoraCall &c, int K) {
-  const long long wgs = (long long)((K + 255) / 256) * c.L * (rank_pad(c.R) / 16);
-  int s = (int)((512 + wgs - 1) / wgs);
-  const int most = (c.M + 63) / 64;
-  if (s > most) s = most;
-  return s < 1 ? 1 : s;
+// Rows per chunk of the gradients' sums: as many chunks as give every CU a
+// workgroup, but at least 64 rows each, since each leaves partial sums of the
+// adapter's own size behind.
+int outer_chunk(const LoraCall &c) {
+  const int cols = ((c.K + kOuterCols - 1) / kOuterCols + (c.N + kOuterCols - 1) / kOuterCols) *
+                   ((rank_pad(c.R) + kOuterRanks - 1) / kOuterRanks);
+  const int want = (2 * kCUs + cols - 1) / cols;
+  const int rows = (c.M + want - 1) / want;
+  return rows > 64 ? rows : 64;
 }
 
-template <typename T, bool TR>
-hipError_t outer(const LoraCall &c, const float *V, const void *X, int ldx, int K,
-                 const int *start, const int *perm, float *P, float *D, int ldd,
-                 long long stride_d) {
-  OuterParams p;
-  p.V = V;
-  p.X = X;
-  p.P = P;
-  p.start = start;
-  p.perm = perm;
-  p.K = K;
-  p.L = c.L;
-  p.Rp = rank_pad(c.R);
-  p.ldx = ldx;
-  p.S = outer_parts(c, K);
-  hipLaunchKernelGGL((lora_outer<T>),
-                     dim3((unsigned)(c.L * (p.Rp / 16)), (unsigned)((K + 255) / 256),
-                          (unsigned)p.S),
-                     dim3(256), 0, c.stream, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((lora_outer_sum<TR>),
-                     dim3(flat_grid((long long)c.R * K), (unsigned)c.L), dim3(256), 0, c.stream, P,
-                     D, ldd, stride_d, c.scale, c.ranks, K, c.L, c.R, p.Rp, p.S, c.alpha,
-                     c.beta_ab);
-  return hipGetLastError();
-}
+// Rows up to which the fp16 product goes to fp32 and the adapters' term is
+// added in a pass of its own: batches in which every row may have another
+// adapter, which the pass does not mind and the product's epilogue does.
+constexpr int kJoinRows = 512;
 
 struct LoraSpace {
-  float *V, *T;
+  float *V, *S, *T, *scale;
+  _Float16 *split;
 };
 
 size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
   Carve w(base);
-  s->V = w.take<float>((size_t)c.M * rank_pad(c.R));
-  if (c.M <= kSkinnyRows)
-    s->T = w.take<float>((size_t)skinny_plan(c).parts * c.M * (size_t)c.N);
-  else s->T = c.half ? w.take<float>((size_t)c.M * (size_t)c.N) : nullptr;
+  *s = LoraSpace{};
+  const size_t rp = (size_t)rank_pad(c.R);
+  if (c.M <= kSkinnyRows) {
+    s->V = w.take<float>((size_t)c.M * rp);
+    s->S = w.take<float>((size_t)skinny_plan(c).parts * c.M * (size_t)c.N);
+    return w.used;
+  }
+  s->S = w.take<float>((size_t)tile_plan(c, false).parts * c.M * rp);
+  if (!c.half || c.M <= kJoinRows) {
+    s->V = w.take<float>((size_t)c.M * rp);
+    if (c.half) s->T = w.take<float>((size_t)c.M * (size_t)c.N);
+  } else {
+    s->split = w.take<_Float16>((size_t)c.M * 2 * rp);
+    s->scale = w.take<float>((size_t)c.M + 256);   // read in whole tiles of rows
+  }
   return w.used;
 }
 
 struct GradSpace {
-  float *V, *G, *T, *P;
+  float *V, *G, *SV, *SG, *PA, *PB, *scale;
+  _Float16 *split, *At;
   int *start, *perm;
 };
 
 size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   Carve w(base);
+  *s = GradSpace{};
   const size_t rp = (size_t)rank_pad(c.R);
-  s->G = w.take<float>((size_t)c.M * rp);
-  s->V = w.take<float>((size_t)c.M * rp);
-  s->T = c.half && c.dX ? w.take<float>((size_t)c.M * (size_t)c.K) : nullptr;
-  const size_t pa = c.dA ? (size_t)outer_parts(c, c.K) * c.L * rp * (size_t)c.K : 0;
-  const size_t pb = c.dB ? (size_t)outer_parts(c, c.N) * c.L * rp * (size_t)c.N : 0;
-  s->P = w.take<float>(pa > pb ? pa : pb);
+  const size_t parts = (size_t)tile_plan(c, true).parts;
   s->start = w.take<int>((size_t)c.L + 1);
   s->perm = w.take<int>((size_t)c.M);
+  if (c.dX || c.dA) {
+    s->G = w.take<float>((size_t)c.M * rp);
+    s->SG = w.take<float>(parts * c.M * rp);
+  }
+  if (c.dX && c.half) {
+    s->split = w.take<_Float16>((size_t)c.M * 2 * rp);
+    s->scale = w.take<float>((size_t)c.M + 256);
+    s->At = w.take<_Float16>((size_t)c.L * (size_t)c.K * rp);
+  }
+  if (c.dB) {
+    s->V = w.take<float>((size_t)c.M * rp);
+    s->SV = w.take<float>(parts * c.M * rp);
+  }
+  const int chunk = outer_chunk(c);
+  const size_t slots = (size_t)((c.M + chunk - 1) / chunk) + c.L;
+  if (c.dA) s->PA = w.take<float>(slots * rp * (size_t)c.K);
+  if (c.dB) s->PB = w.take<float>(slots * rp * (size_t)c.N);
   return w.used;
+}
+
+// C := alpha * (A op(B) + the term) + beta * C with the fp16 kernels.
+hipError_t product_on_term(const LoraCall &c, const LowRank &term, bool tb, int N, int K,
+                           const void *A, int lda, const void *B, int ldb, float beta, void *C,
+                           int ldc) {
+  Call g = {};
+  g.M = c.M;
+  g.N = N;
+  g.K = K;
+  g.alpha = c.alpha;
+  g.beta = beta;
+  g.A = A;
+  g.lda = lda;
+  g.B = B;
+  g.ldb = ldb;
+  g.C = C;
+  g.ldc = ldc;
+  g.tb = tb;
+  g.splits = 1;
+  g.ws_limit = workspace_limit();
+  g.term = &term;
+  g.stream = c.stream;
+  return launch_f16_lora(g);
+}
+
+hipError_t join(const LoraCall &c, const float *V, const float *S, int parts) {
+  JoinParams j;
+  j.S = S;
+  j.V = V;
+  j.B = c.B;
+  j.Y = c.Y;
+  j.rows = c.rows;
+  j.ranks = c.ranks;
+  j.scale = c.scale;
+  j.stride = c.stride_b;
+  j.M = c.M;
+  j.N = c.N;
+  j.L = c.L;
+  j.R = c.R;
+  j.Rp = rank_pad(c.R);
+  j.ldb = c.ldb;
+  j.ldy = c.ldy;
+  j.parts = parts;
+  j.alpha = c.alpha;
+  j.beta = c.beta;
+  const dim3 g((unsigned)((c.N + 255) / 256), (unsigned)c.M);
+  if (c.half) hipLaunchKernelGGL((lora_join<_Float16>), g, dim3(256), 0, c.stream, j);
+  else hipLaunchKernelGGL((lora_join<float>), g, dim3(256), 0, c.stream, j);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t run(const LoraCall &c, const LoraSpace &s) {
-  if (c.M <= kSkinnyRows) return skinny<T>(c, s.V, s.T);
-  hipError_t e = shrink<T, true>(c, c.X, c.ldx, c.K, c.A, c.lda, c.stride_a, s.V);
+  if (c.M <= kSkinnyRows) {
+    const hipError_t e = skinny<T>(c, s.V, s.S);
+    return e != hipSuccess ? e : join(c, s.V, s.S, skinny_plan(c).parts);
+  }
+  const TilePlan t = tile_plan(c, false);
+  TileShrinkParams p = tile_params(c, t);
+  p.job[0] = ShrinkJob{c.X, c.A, c.stride_a, c.K, c.ldx, c.lda, 1, tile_chunk(c, t, c.K), s.S,
+                       s.V, s.split, s.scale};
+  hipError_t e = shrink_tiles<T>(c, p, t, 1);
   if (e != hipSuccess) return e;
   if (!c.half) {
     e = expand<T, true>(c, s.V, c.B, c.ldb, c.stride_b, c.N, c.alpha, c.beta,
@@ -704,61 +1082,89 @@ hipError_t run(const LoraCall &c, const LoraSpace &s) {
                                    static_cast<const float *>(c.W), c.ldw, 1.0f,
                                    static_cast<float *>(c.Y), c.ldy, c.stream);
   }
-  e = expand<T, true>(c, s.V, c.B, c.ldb, c.stride_b, c.N, 1.0f, 0.0f, s.T, c.N);
-  if (e != hipSuccess) return e;
-  const int rc = gemm_f16f32_nt(c.M, c.N, c.K, 1.0f, static_cast<const gemm_half_t *>(c.X), c.ldx,
-                                static_cast<const gemm_half_t *>(c.W), c.ldw, 1.0f, s.T, c.N,
-                                c.stream);
-  if (rc != 0) return (hipError_t)rc;
-  hipLaunchKernelGGL(lora_finish, dim3(flat_grid((long long)c.M * c.N)), dim3(256), 0, c.stream,
-                     s.T, static_cast<_Float16 *>(c.Y), c.M, c.N, c.ldy, c.alpha, c.beta);
-  return hipGetLastError();
+  if (c.M <= kJoinRows) {
+    const int rc = gemm_f16f32_nt(c.M, c.N, c.K, 1.0f, static_cast<const gemm_half_t *>(c.X),
+                                  c.ldx, static_cast<const gemm_half_t *>(c.W), c.ldw, 0.0f, s.T,
+                                  c.N, c.stream);
+    return rc != 0 ? (hipError_t)rc : join(c, s.V, s.T, 1);
+  }
+  const LowRank term = {s.split, 2 * p.Rp, s.scale, c.B, c.ldb, c.stride_b, c.rows, c.ranks, c.L,
+                        c.R};
+  return product_on_term(c, term, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw, c.beta, c.Y, c.ldy);
 }
 
 template <typename T>
 hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
-  hipError_t e;
-  const bool adapters = c.L > 0 && c.R > 0;
-  if (adapters && (c.dX || c.dA)) {
-    e = shrink<T, false>(c, c.dY, c.lddy, c.N, c.B, c.ldb, c.stride_b, s.G);
-    if (e != hipSuccess) return e;
-  }
-  if (c.dX) {
-    float *t = c.half ? s.T : static_cast<float *>(c.dX);
-    const int ldt = c.half ? c.K : c.lddx;
-    const float al = c.half ? 1.0f : c.alpha, be = c.half ? 0.0f : c.beta_x;
-    e = expand<T, false>(c, s.G, c.A, c.lda, c.stride_a, c.K, al, be, t, ldt);
-    if (e != hipSuccess) return e;
-    const int rc =
-        c.half ? gemm_f16f32(c.M, c.K, c.N, 1.0f, static_cast<const gemm_half_t *>(c.dY), c.lddy,
-                             static_cast<const gemm_half_t *>(c.W), c.ldw, 1.0f, t, ldt, c.stream)
-               : gemm_f32(c.M, c.K, c.N, c.alpha, static_cast<const float *>(c.dY), c.lddy,
-                          static_cast<const float *>(c.W), c.ldw, 1.0f, t, ldt, c.stream);
-    if (rc != 0) return (hipError_t)rc;
-    if (c.half) {
-      hipLaunchKernelGGL(lora_finish, dim3(flat_grid((long long)c.M * c.K)), dim3(256), 0,
-                         c.stream, s.T, static_cast<_Float16 *>(c.dX), c.M, c.K, c.lddx, c.alpha,
-                         c.beta_x);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-  }
-  if (!adapters || (!c.dA && !c.dB)) return hipSuccess;
   hipLaunchKernelGGL(lora_group, dim3((unsigned)c.L), dim3(kGroupThreads), 0, c.stream, c.rows,
                      c.M, c.L, s.start, s.perm);
-  e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (c.dA) {
-    e = outer<T, false>(c, s.G, c.X, c.ldx, c.K, s.start, s.perm, s.P, c.dA, c.ldda, c.stride_da);
+  const TilePlan t = tile_plan(c, true);
+  TileShrinkParams p = tile_params(c, t);
+  p.start = s.start;
+  p.perm = s.perm;
+  int jobs = 0;
+  if (s.G)
+    p.job[jobs++] = ShrinkJob{c.dY, c.B, c.stride_b, c.N, c.lddy, c.ldb, 0, tile_chunk(c, t, c.N),
+                              s.SG, s.G, s.split, s.scale};
+  if (s.V)
+    p.job[jobs++] = ShrinkJob{c.X, c.A, c.stride_a, c.K, c.ldx, c.lda, 1, tile_chunk(c, t, c.K),
+                              s.SV, s.V, nullptr, nullptr};
+  e = shrink_tiles<T>(c, p, t, jobs);
+  if (e != hipSuccess) return e;
+  if (c.dX && c.half) {
+    hipLaunchKernelGGL(lora_transpose, dim3((unsigned)((c.K + 255) / 256), (unsigned)c.L),
+                       dim3(256), 0, c.stream, static_cast<const _Float16 *>(c.A), c.lda,
+                       c.stride_a, s.start, c.ranks, c.K, c.R, p.Rp, s.At);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
+    const LowRank term = {s.split, 2 * p.Rp, s.scale, s.At, p.Rp, (long long)c.K * p.Rp,
+                          c.rows, c.ranks, c.L, c.R};
+    e = product_on_term(c, term, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw, c.beta_x, c.dX,
+                        c.lddx);
+    if (e != hipSuccess) return e;
+  } else if (c.dX) {
+    e = expand<T, false>(c, s.G, c.A, c.lda, c.stride_a, c.K, c.alpha, c.beta_x,
+                         static_cast<float *>(c.dX), c.lddx);
+    if (e != hipSuccess) return e;
+    const int rc = gemm_f32(c.M, c.K, c.N, c.alpha, static_cast<const float *>(c.dY), c.lddy,
+                            static_cast<const float *>(c.W), c.ldw, 1.0f,
+                            static_cast<float *>(c.dX), c.lddx, c.stream);
+    if (rc != 0) return (hipError_t)rc;
+  }
+  if (!c.dA && !c.dB) return hipSuccess;
+  OuterParams o = {};
+  o.rows = c.rows;
+  o.ranks = c.ranks;
+  o.start = s.start;
+  o.perm = s.perm;
+  o.scale = c.scale;
+  o.L = c.L;
+  o.R = c.R;
+  o.Rp = p.Rp;
+  o.chunk = outer_chunk(c);
+  o.alpha = c.alpha;
+  o.beta = c.beta_ab;
+  int n = 0, widest = 0;
+  if (c.dA) {
+    o.job[n++] = OuterJob{s.G, c.X, c.dA, c.stride_da, c.K, c.ldx, c.ldda, 0, s.PA};
+    widest = c.K;
   }
   if (c.dB) {
-    e = shrink<T, true>(c, c.X, c.ldx, c.K, c.A, c.lda, c.stride_a, s.V);
-    if (e != hipSuccess) return e;
-    e = outer<T, true>(c, s.V, c.dY, c.lddy, c.N, s.start, s.perm, s.P, c.dB, c.lddb,
-                       c.stride_db);
+    o.job[n++] = OuterJob{s.V, c.dY, c.dB, c.stride_db, c.N, c.lddy, c.lddb, 1, s.PB};
+    widest = widest > c.N ? widest : c.N;
   }
-  return e;
+  const int rtiles = (p.Rp + kOuterRanks - 1) / kOuterRanks;
+  hipLaunchKernelGGL((lora_outer<T>),
+                     dim3((unsigned)((widest + kOuterCols - 1) / kOuterCols),
+                          (unsigned)((c.M + o.chunk - 1) / o.chunk), (unsigned)(n * rtiles)),
+                     dim3(kOuterThreads), 0, c.stream, o);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(lora_outer_sum,
+                     dim3(flat_grid((long long)c.R * widest), (unsigned)c.L, (unsigned)n),
+                     dim3(256), 0, c.stream, o);
+  return hipGetLastError();
 }
 
 }  // namespace

@@ -242,15 +242,6 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
 
 // ---------------------------------------------------------------- down and weighted sum
 
-// Power of two that brings a row whose largest magnitude has these bits to
-// [2^14, 2^15) as fp16, and its inverse (1 for a row of zeros, infinities or
-// NaN); its exponent, at least -100.
-__device__ __forceinline__ int row_exponent(unsigned bits) {
-  const int e = (int)(bits >> 23);
-  if (e == 0 || e == 255) return 0;
-  return e - 141 > -100 ? e - 141 : -100;
-}
-
 // A row of H as fragments of T: for fp16, scaled by the row's power of two
 // and rounded to 11 bits (those of every value within 2^-28 of the row's
 // largest).

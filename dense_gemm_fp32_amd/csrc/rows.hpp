@@ -175,6 +175,15 @@ struct RowLoader {
   __device__ __forceinline__ Raw frag(int, const Raw &r) const { return r; }
 };
 
+// Power of two that brings a row whose largest magnitude has these bits to
+// [2^14, 2^15) as fp16, and its inverse (1 for a row of zeros, infinities or
+// NaN); its exponent, at least -100.
+__device__ __forceinline__ int row_exponent(unsigned bits) {
+  const int e = (int)(bits >> 23);
+  if (e == 0 || e == 255) return 0;
+  return e - 141 > -100 ? e - 141 : -100;
+}
+
 // The adapter of a row: -1 when it has none (or an index out of range), or
 // when that adapter's rank is at most `r0` (nothing of it from rank r0 on).
 __device__ __forceinline__ int adapter_of(const int *rows, int row, int M, int L) {

@@ -587,84 +587,285 @@ struct NoTerm {
   }
 };
 
-// This lane's fragment of 8 ranks r .. r+7 of a row of U, 0 from `rank` on.
-__device__ __forceinline__ f16x8 low_rank_load(const _Float16 *u, int r, int rank) {
+// Eight halves at any half's address (16-byte loads need no more).
+__device__ __forceinline__ f16x8 low_rank_whole(const _Float16 *u) {
   typedef _Float16 Any __attribute__((ext_vector_type(8), aligned(2)));
-  if (r + 8 <= rank) return *reinterpret_cast<const Any *>(u + r);
-  f16x8 f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = r + e < rank ? u[r + e] : (_Float16)0.0f;
-  return f;
+  return *reinterpret_cast<const Any *>(u);
 }
 
-// The low-rank term of a wave's rows: row i, column n gets scale[i] * sum_r
-// V[i, r] U_a[n, r] for the row's adapter a (0 without one).
+// The first `count` of 8 elements `stride` apart, the others 0: one at a time,
+// since this is for the ends of rows only and unrolled it costs the kernel the
+// registers of its 8 addresses.
+__device__ __forceinline__ f16x8 low_rank_part(const _Float16 *u, int count, size_t stride) {
+  unsigned long long lo = 0, hi = 0;
+#pragma unroll 1
+  for (int e = (count < 8 ? count : 8) - 1; e >= 0; --e) {
+    hi = (hi << 16) | (lo >> 48);
+    lo = (lo << 16) | __builtin_bit_cast(uint16_t, u[(size_t)e * stride]);
+  }
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(f16x8, u64x2{lo, hi});
+}
+
+// Elements r .. r+7 of a row, 0 from `end` on.
+__device__ __forceinline__ f16x8 low_rank_load(const _Float16 *u, int r, int end) {
+  return r + 8 <= end ? low_rank_whole(u + r) : low_rank_part(u + r, end - r, 1);
+}
+
+// The low-rank term: row i, column n gets scale[i] * sum_r V[i, r] U_a[n, r]
+// for the row's adapter a (nothing without one).  V holds each number as the
+// sum of two halves, 16 ranks' high parts next to their low parts, so a K step
+// of the product holds BK/2 ranks, each of U's standing twice.
 //
-// It is formed where the accumulators leave for LDS, 16 rows by CB columns at
-// a time, so that its own small accumulators are all it needs beside them.
-// (Started in the accumulators before the K loop, as it could be, the branches
-// below over 128 accumulator registers spill.)  V holds each number as the sum
-// of two halves, 16 ranks' high parts next to their low parts, so one 16x16x32
-// step covers 16 ranks with the first 16 k on the high parts and the last on
-// the low against the same U.  A block of rows takes its distinct adapters in
-// turn and keeps, by selection, the rows that have that adapter: another
-// adapter's infinities never enter a row's sum.
+// low_rank_start runs such steps ahead of the product's own, through the same
+// LDS slots: for each adapter among the tile's rows, V with the other rows'
+// zeroed against that adapter's U (rank 64: two steps of 64 k beside the K/64
+// of the product).  Zeroed rows must not meet an infinity or NaN of U, which
+// would make them NaN: U passes through registers on its way, the workgroup
+// votes, and an adapter whose U is not finite in the tile's columns is left to
+// LowRankTerm, as are adapters beyond kStartAdapters in one tile.
+//
+// LowRankTerm adds what was left while the accumulators are staged for the
+// stores, 16 rows by 32 columns at a time, keeping by selection the rows that
+// have the adapter.  Doing all of the term so took 31 us more at 4096 x 4096 x
+// 4096 with eight adapters of rank 64 (153 against 122 us): its operands come
+// in fragments of 16 bytes a row, U once more for every 16 rows.
+constexpr int kStartAdapters = 16;
+
+// The distinct adapters among the rows of a workgroup's tile, in the order of
+// their first rows; the same in every wave.
+template <int BM>
+struct TileAdapters {
+  int id[BM / 64];                     // row 64 j + lane's adapter, -1: none
+  unsigned long long left[BM / 64];
+
+  __device__ __forceinline__ TileAdapters(const LowRank &t, int m0, int M) {
+#pragma unroll
+    for (int j = 0; j < BM / 64; ++j) {
+      const int row = m0 + 64 * j + (int)threadIdx.x % kWave;
+      const int a = t.rows[row < M ? row : M - 1];
+      id[j] = row < M && a >= 0 && a < t.L ? a : -1;
+      left[j] = __ballot(id[j] >= 0);
+    }
+  }
+
+  // The next adapter, -1 after the last.
+  __device__ __forceinline__ int next() {
+    int a = -1;
+#pragma unroll
+    for (int j = BM / 64 - 1; j >= 0; --j)
+      if (left[j] != 0) a = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
+#pragma unroll
+    for (int j = 0; j < BM / 64; ++j) left[j] &= ~__ballot(id[j] == a);
+    return a;
+  }
+};
+
+__device__ __forceinline__ int low_rank_of(const LowRank &t, int a) {
+  if (t.ranks == nullptr) return t.R;
+  const int r = t.ranks[a];
+  return r < 0 ? 0 : (r < t.R ? r : t.R);
+}
+
+__device__ __forceinline__ bool not_finite(u32x4 v) {
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    bad |= (v[e] & 0x7c00u) == 0x7c00u || (v[e] & 0x7c000000u) == 0x7c000000u;
+  return bad;
+}
+
+// Piece j of this lane of an adapter's step from rank r0 on: 8 ranks of a
+// column, or 8 columns of a rank.
+template <class T, class L>
+__device__ __forceinline__ u32x4 low_rank_piece(const GemmParams &p, const LowRank &t, int n0,
+                                                int a, int rank, int r0, int j) {
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  int idx, kk;
+  L::RB::chunk(wave * T::QB_W + j, lane, idx, kk);
+  const int r = r0 + kk / 32 * 16 + kk % 16, n = n0 + idx;
+  if (n >= p.N || r >= rank) return u32x4{0u, 0u, 0u, 0u};
+  const _Float16 *u = static_cast<const _Float16 *>(t.U) + (size_t)a * (size_t)t.stride;
+  return __builtin_bit_cast(u32x4, L::TB ? low_rank_load(u + (size_t)n * (size_t)t.ldu, r, rank)
+                                         : low_rank_load(u + (size_t)r * (size_t)t.ldu, n, p.N));
+}
+
+// The steps to run, as (adapter, first rank) in `steps` (LDS), apart from the
+// accumulators' loop so that one plain loop is all that carries them: one that
+// always runs at least once (a loop that may not run has its accumulators
+// copied around it), so where there is nothing to do there is one step of no
+// adapter, which adds zeros.  Returns their number; `out`: the adapters left
+// out, bit i for the tile's i-th (bit 31: from the 31st on).
+template <class T, class L>
+__device__ __forceinline__ int low_rank_steps(const GemmParams &p, const LowRank &t, int m0,
+                                              int n0, bool on, int2 *steps, unsigned &out) {
+  constexpr int RANKS = T::BK / 2;     // ranks of a step
+  static_assert(kStartAdapters * (256 / RANKS) * 8 <= T::STAGE_BYTES, "room for the steps");
+  TileAdapters<T::BM> tile(t, m0, p.M);
+  int n = 0, i = 0;
+  out = 0;
+  for (int a = on ? tile.next() : -1; a >= 0; a = tile.next(), ++i) {
+    bool skip = i >= kStartAdapters;
+    if (!skip) {
+      const int rank = low_rank_of(t, a);
+      bool bad = false;
+      for (int r0 = 0; r0 < rank; r0 += RANKS)
+#pragma unroll
+        for (int j = 0; j < T::QB_W; ++j)
+          bad |= not_finite(low_rank_piece<T, L>(p, t, n0, a, rank, r0, j));
+      skip = __syncthreads_or(bad);
+      if (!skip)
+        for (int r0 = 0; r0 < rank; r0 += RANKS, ++n)
+          if (threadIdx.x == 0) steps[n] = int2{a, r0};
+    }
+    if (skip) out |= 1u << (i < 31 ? i : 31);
+  }
+  if (n == 0) {
+    if (threadIdx.x == 0) steps[0] = int2{-1, 0};
+    n = 1;
+  }
+  __syncthreads();
+  return n;
+}
+
+template <class T, class L>
+__device__ __forceinline__ void low_rank_start(const GemmParams &p, const LowRank &t, int m0,
+                                               int n0, char *slot, const int2 *steps, int n,
+                                               int wm0, int wn0,
+                                               typename T::Acc (&acc)[T::FM][T::FN]) {
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  FragAddr<T, L> fa;
+  frag_setup<T, L>(wm0, wn0, fa);
+  int i = 0;
+#pragma unroll 1
+  do {
+    const int a = __builtin_amdgcn_readfirstlane(steps[i].x);
+    const int r0 = __builtin_amdgcn_readfirstlane(steps[i].y);
+    const int rank = a >= 0 ? low_rank_of(t, a) : 0;
+    RegTile<T> reg;
+#pragma unroll
+    for (int j = 0; j < T::QB_W; ++j) reg.b[j] = low_rank_piece<T, L>(p, t, n0, a, rank, r0, j);
+#pragma unroll
+    for (int j = 0; j < T::QA_W; ++j) {
+      int idx, kk;
+      L::RA::chunk(wave * T::QA_W + j, lane, idx, kk);
+      const int row = m0 + idx < p.M ? m0 + idx : p.M - 1;
+      const int k = 2 * r0 + kk;
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(static_cast<const _Float16 *>(t.V) +
+                                                       (size_t)row * (size_t)t.ldv +
+                                                       (k < t.ldv ? k : 0));
+      reg.a[j] = a >= 0 && t.rows[row] == a && k < t.ldv ? v : u32x4{0u, 0u, 0u, 0u};
+    }
+    __syncthreads();   // every wave has read the slot's last contents
+    reg_store<T>(reg, slot);
+    __syncthreads();
+    Frag<T> fr;
+#pragma unroll
+    for (int s = 0; s < T::SUB; ++s) {
+      frag_read<T, L>(slot, fa, s, fr);
+      mfma_rows<T, 0, T::FM>(fr, acc);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } while (++i < n);
+  // the rows' scales
+  const int lg = lane / T::MF;
+#pragma unroll
+  for (int bi = 0; bi < T::FM; ++bi)
+#pragma unroll
+    for (int e = 0; e < T::ACC_N; e += 4) {
+      const f32x4 f = *reinterpret_cast<const f32x4 *>(
+          t.scale + m0 + wm0 + T::MF * bi + (T::MF == 16 ? 0 : 2 * e) + 4 * lg);
+#pragma unroll
+      for (int bj = 0; bj < T::FN; ++bj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[bi][bj][e + q] *= f[q];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  __syncthreads();
+}
+
+// What a chain of loads would stand in front of every block -- the rows'
+// adapters and their ranks -- is loaded once per wave, a row a lane.
+template <int BM, int WTM, bool UT>
 struct LowRankTerm {
   static constexpr bool kNone = false;
   const LowRank &t;
+  bool some;
+  int id[WTM / 64], rank[WTM / 64];
+
+  // `out`: the adapters of the tile (rows m0 ..) to add; the wave's rows start
+  // wm0 further.
+  __device__ __forceinline__ LowRankTerm(const LowRank &term, int m0, int wm0, int M, unsigned out)
+      : t(term), some(out != 0) {
+#pragma unroll
+    for (int j = 0; j < WTM / 64; ++j) id[j] = rank[j] = -1;
+    if (!some) return;
+    TileAdapters<BM> tile(t, m0, M);
+    int i = 0;
+    for (int a = tile.next(); a >= 0; a = tile.next(), ++i) {
+      if (!((out >> (i < 31 ? i : 31)) & 1)) continue;
+      const int r = low_rank_of(t, a);
+#pragma unroll
+      for (int j = 0; j < WTM / 64; ++j) {
+        const int row = m0 + wm0 + 64 * j + (int)threadIdx.x % kWave;
+        if (row < M && t.rows[row] == a) {
+          id[j] = a;
+          rank[j] = r;
+        }
+      }
+    }
+  }
 
   template <class T>
   __device__ __forceinline__ void stage(float *out, const typename T::Acc (&acc)[T::FM][T::FN],
                                         int g, int lane, const GemmParams &p, int r0,
                                         int c0) const {
+    if (!some) {
+      stage_rows<T>(out, acc, g, lane);
+      return;
+    }
     constexpr int CB = 32;                                // columns at a time
     constexpr int NB = CB / 16;
     const int li = lane % 16, lg = lane / 16;
     const int ur = 8 * (lg & 1);                          // this lane's ranks within 16
 #pragma unroll 1
     for (int part = 0; part < 2 * (T::WTN / CB); ++part) {
-      const int b0 = 32 * g + 16 * (part & 1);            // the block's first row in the wave's
+      const int h = part & 1;
+      const int b0 = 32 * g + 16 * h;                     // the block's first row in the wave's
       const int n0 = CB * (part >> 1);                    // ... and first column
       const int row = r0 + b0 + li;
       const int m = row < p.M ? row : p.M - 1;
-      int id = t.rows[m];
-      if (id < 0 || id >= t.L) id = -1;
+      const int at = (b0 & 63) + li;
+      const int ida = __shfl(id[g / 2], at), ranka = __shfl(rank[g / 2], at);
       const _Float16 *v = static_cast<const _Float16 *>(t.V) + (size_t)m * (size_t)t.ldv + 8 * lg;
       const f32x4 f = *reinterpret_cast<const f32x4 *>(t.scale + r0 + b0 + 4 * lg);
-      float *o = out + (16 * (part & 1) + 4 * lg) * T::EP_STRIDE + n0 + li;
-      unsigned left = (unsigned)(__ballot(id >= 0) & 0xffffu);
-      if (left != 0xffffu) {
-        // rows without an adapter
+      float *o = out + (16 * h + 4 * lg) * T::EP_STRIDE + n0 + li;
+      unsigned left = (unsigned)(__ballot(ida >= 0) & 0xffffu);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) o[q * T::EP_STRIDE + 16 * b] = 0.0f;
-      }
+        for (int b = 0; b < NB; ++b) o[q * T::EP_STRIDE + 16 * b] = 0.0f;
       while (left != 0) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-        const unsigned same = (unsigned)(__ballot(id == a) & 0xffffu);
+        const int src = __builtin_ctz(left);
+        const int a = __builtin_amdgcn_readlane(ida, src);
+        const int rk = __builtin_amdgcn_readlane(ranka, src);
+        const unsigned same = (unsigned)(__ballot(ida == a) & 0xffffu);
         left &= ~same;
-        int rank = t.R;
-        if (t.ranks != nullptr) {
-          rank = t.ranks[a];
-          rank = rank < 0 ? 0 : (rank < t.R ? rank : t.R);
-        }
         f32x4 s[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) s[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const _Float16 *u0 = static_cast<const _Float16 *>(t.U) + (size_t)a * (size_t)t.stride;
-        for (int r = 0; r < rank; r += 16) {
-          const f16x8 v0 = *reinterpret_cast<const f16x8 *>(v + 2 * r);
-          f16x8 u[NB];
+        for (int r = 0; r < rk; r += 16) {
+          const f16x8 vf = *reinterpret_cast<const f16x8 *>(v + 2 * r);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const int n = c0 + n0 + 16 * b + li;
-            u[b] = low_rank_load(u0 + (size_t)(n < p.N ? n : p.N - 1) * (size_t)t.ldu, r + ur,
-                                 rank);
+            int n = c0 + n0 + 16 * b + li;
+            n = n < p.N ? n : p.N - 1;
+            const f16x8 u = UT ? low_rank_load(u0 + (size_t)n * (size_t)t.ldu, r + ur, rk)
+                               : low_rank_part(u0 + (size_t)(r + ur) * (size_t)t.ldu + n,
+                                               rk - r - ur, (size_t)t.ldu);
+            s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, u, s[b], 0, 0, 0);
           }
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, u[b], s[b], 0, 0, 0);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -1082,38 +1283,39 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma(GemmParams p) {
 }
 
 // The same product on top of a low-rank term (added by the first split of a
-// split-K pass).
-template <class T, bool TA, bool TB, bool VC, bool OUT32>
+// split-K pass).  DIRECT: every tile takes the direct loads; false: the
+// register-staged ones.  (With both loops in one kernel the accumulators that
+// the term leaves are copied for either: twice their registers, and spills.)
+template <class T, bool TB, bool VC, bool OUT32, bool DIRECT>
 __global__ __launch_bounds__(T::NT) void hgemm_mfma_lora(GemmParams p, LowRank t) {
-  typedef HLayout<T, TA, TB> L;
+  typedef HLayout<T, false, TB> L;
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
   lds_poison(lds, T::LDS_BYTES);
   int tm, tn, split;
   tile_of_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
-  select_split<uint16_t, float, TA, TB>(p, split);   // split-K passes always write fp32 slabs
+  select_split<uint16_t, float, false, TB>(p, split);   // split-K passes always write fp32 slabs
   const int m0 = tm * T::BM;
   const int n0 = tn * T::BN;
   const int wave = threadIdx.x / kWave;
   const int wm0 = (wave / T::WAVES_N) * T::WTM;
   const int wn0 = (wave % T::WAVES_N) * T::WTN;
   typename T::Acc acc[T::FM][T::FN];
+  unsigned out;
+  int2 *steps = reinterpret_cast<int2 *>(lds + T::STAGE_BYTES);
+  const int n = low_rank_steps<T, L>(p, t, m0, n0, split == 0, steps, out);
   zero_acc<T>(acc);
+  low_rank_start<T, L>(p, t, m0, n0, lds, steps, n, wm0, wn0, acc);
 
-  const bool m_edge = m0 + T::BM > p.M;
-  const bool n_edge = n0 + T::BN > p.N;
-  const int va = vec_width_a(p.vec_ab), vb = vec_width_b(p.vec_ab);
-  const bool direct = va == 2 && vb == 2 && direct_ok<typename L::RA, T::BK>(m_edge, p.M, p.lda) &&
-                      direct_ok<typename L::RB, T::BK>(n_edge, p.N, p.ldb);
-  if (direct) mainloop_direct<T, L>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
-  else mainloop_staged<T, L>(p, m0, n0, lds, wm0, wn0, va, vb, acc);
+  if constexpr (DIRECT) mainloop_direct<T, L>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
+  else
+    mainloop_staged<T, L>(p, m0, n0, lds, wm0, wn0, vec_width_a(p.vec_ab), vec_width_b(p.vec_ab),
+                          acc);
 
   __builtin_amdgcn_s_waitcnt(kWaitAll);
   __syncthreads();   // every wave is done with the pipeline slots
-  const LowRankTerm term{t};
+  const LowRankTerm<T::BM, T::WTM, TB> term(t, m0, wm0, p.M, out);
   if constexpr (OUT32) {
-    // only split-K passes: the first split's slab takes the term
-    if (split != 0) epilogue_out32<T, VC, true>(p, m0 + wm0, n0 + wn0, lds, acc, NoTerm{});
-    else epilogue_out32<T, VC, true>(p, m0 + wm0, n0 + wn0, lds, acc, term);
+    epilogue_out32<T, VC, true>(p, m0 + wm0, n0 + wn0, lds, acc, term);
   } else {
     epilogue<T, VC, true>(p, m0 + wm0, n0 + wn0, lds, acc, term);
   }
@@ -1131,6 +1333,13 @@ typedef H16Tile<64, 128, 32, 1, 2, 4, 8> F16Small;    // 2 waves,  48 KB LDS, 3 
 
 static bool vec_ok(const void *p, int ld, int elems) {
   return (ld % elems) == 0 && aligned_to(p, (uintptr_t)elems * 2);
+}
+
+// Whether every tile of a call on top of a term takes the direct loads: the
+// kernel's conditions (direct_ok) for the largest tile.
+static bool term_direct(const Call &c) {
+  return vec_ok(c.A, c.lda, 8) && vec_ok(c.B, c.ldb, 8) && (c.tb || c.N % 8 == 0) &&
+         256LL * c.lda < (1LL << 31) && 256LL * c.ldb < (1LL << 31);
 }
 
 template <class T>
@@ -1187,10 +1396,15 @@ static hipError_t launch_variant(const Call &c, const Plan &pl) {
   p.tile_count = 0;
   p.c_tiles = 0;
   const dim3 grid((unsigned)(pl.blocks * c.splits));
-  if constexpr (TERM)
-    hipLaunchKernelGGL((hgemm_mfma_lora<T, TA, TB, VC, OUT32>), grid, dim3(T::NT), 0, c.stream, p,
-                       *c.term);
-  else
+  if constexpr (TERM) {
+    constexpr bool STAGED = T::NWAVES < 8;   // the tiles that have a staged form
+    if (STAGED && !term_direct(c))
+      hipLaunchKernelGGL((hgemm_mfma_lora<T, TB, VC, OUT32, !STAGED>), grid, dim3(T::NT), 0,
+                         c.stream, p, *c.term);
+    else
+      hipLaunchKernelGGL((hgemm_mfma_lora<T, TB, VC, OUT32, true>), grid, dim3(T::NT), 0,
+                         c.stream, p, *c.term);
+  } else
     hipLaunchKernelGGL((hgemm_mfma<T, TA, TB, VC, OUT32>), grid, dim3(T::NT), 0, c.stream, p);
   return hipGetLastError();
 }
@@ -1396,10 +1610,17 @@ static hipError_t launch_cfg(const Call &c, int want) {
 
 template <bool TERM>
 static hipError_t launch_f16_as_is(const Call &c) {
-  const F16Choice ch = choose_f16(c);
+  F16Choice ch = choose_f16(c);
+  // the large tiles have no register-staged form on top of a term
+  if (TERM && (ch.cfg == F16Cfg::kBig || ch.cfg == F16Cfg::kBig32) && !term_direct(c))
+    ch.cfg = F16Cfg::kMid;
   switch (ch.cfg) {
     case F16Cfg::kBig: return launch_cfg<TERM, F16Big>(c, ch.splits);
-    case F16Cfg::kBig32: return launch_cfg<TERM, F16Big32>(c, ch.splits);
+    case F16Cfg::kBig32:
+      // on top of a term the large tile takes 16x16x32 blocks throughout: with
+      // 32x32x16 ones its accumulators' scaling spills
+      if constexpr (TERM) return launch_cfg<TERM, F16Big>(c, ch.splits);
+      else return launch_cfg<TERM, F16Big32>(c, ch.splits);
     case F16Cfg::kMid: return launch_cfg<TERM, F16Mid>(c, ch.splits);
     default: return launch_cfg<TERM, F16Small>(c, ch.splits);
   }

@@ -1,7 +1,7 @@
 // gemm_f16_lora.hip -- the fp16 GEMM on top of a low-rank term of each row's own
-// adapter: the kernel of gemm_f16_kernel.hpp with its accumulators started by
-// low_rank_init.  The term costs ceil(rank/16) more steps of 32 k per tile
-// than the product's K/32, and no pass over C of its own.
+// adapter (low_rank_start and LowRankTerm of gemm_f16_kernel.hpp).  The term
+// costs a tile ceil(rank/32) more K steps of 64 for each adapter among its
+// rows, and no pass over C of its own.
 #include "gemm_f16_kernel.hpp"
 
 namespace dgemm {

@@ -10,7 +10,8 @@ namespace dgemm {
 // A low-rank term that a product's accumulators start from (fp16 products):
 // scale[i] * sum_r V[i, r] U_a[n, r] in row i, column n, a = rows[i].  V: rows
 // of ldv halves, for every 16 ranks 16 high parts, then 16 low parts; U:
-// adapter a's rows of ranks at U + a*stride, row n at n*ldu; ranks NULL: R.
+// adapter a's matrix at U + a*stride, column n of C its row n (a product with B
+// stored transposed) or its column n (with B as stored); ranks NULL: R.
 struct LowRank {
   const void *V;
   int ldv;

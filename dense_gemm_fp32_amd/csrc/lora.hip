@@ -263,17 +263,24 @@ struct TileShrinkParams {
 constexpr int kShrinkTile = 64;   // rows, and ranks, of a workgroup's tile
 
 // S[part][rows, ranks] of 64 rows by 64 ranks over a part of K.  Both tiles go
-// through LDS in steps of 128 bytes a row, 16-byte pieces XOR-swizzled by row,
-// the next step's loads in flight behind this one's products: every piece of X
-// is loaded once per adapter among the rows, in whole lines.  Rows in adapter
-// order (perm) have one adapter per tile but where two meet.  grid: (row
-// tiles, rank tiles * parts * z, jobs); workgroup z takes the distinct adapters
-// z, z + Z, ... of its rows.
+// through LDS in steps of 512 bytes a row, 16-byte pieces XOR-swizzled by row:
+// every piece of X is loaded once per adapter among the rows, in whole lines.
+// A step's loads (up to 64 KB a workgroup, two workgroups per CU) are issued as
+// soon as the registers of the last are in LDS and arrive behind its products;
+// steps of 128 bytes left a quarter of that in flight (26.7 against XXX us at
+// 4096 rows of 4096, rank 64).  Rows in adapter order (perm) have one adapter
+// per tile but where two meet.  grid: (row tiles, rank tiles * parts * z,
+// jobs); workgroup z takes the distinct adapters z, z + Z, ... of its rows.
+constexpr int kStepBytes = 512;
+
 template <typename T>
 __global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
   constexpr int VEC = El<T>::VEC;
-  constexpr int BK = 128 / (int)sizeof(T);
-  __shared__ __attribute__((aligned(16))) char lds[2][2][kShrinkTile * 128];
+  constexpr int BK = kStepBytes / (int)sizeof(T);
+  constexpr int CH = kStepBytes / 16;              // pieces of a row
+  constexpr int PER = kShrinkTile * CH / 256;      // pieces a thread loads of either tile
+  __shared__ __attribute__((aligned(16))) char ldx_[kShrinkTile * kStepBytes];
+  __shared__ __attribute__((aligned(16))) char ldw_[kShrinkTile * kStepBytes];
   typedef typename El<T>::Frag Frag;
   const ShrinkJob j = p.job[blockIdx.z];
   const int lane = threadIdx.x % kWave, wave = wave_id();
@@ -292,12 +299,9 @@ __global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
   int id = pos0 + lane < count ? adapter_of(p.rows, row, p.M, p.L) : -1;
   if (id >= 0 && rank_of(p.ranks, id, p.R) <= r0) id = -1;
   unsigned long long left = __ballot(id >= 0);
-  // X: this thread loads piece c of tile rows t, t + 32
-  const int c = threadIdx.x % 8, t = threadIdx.x / 8;
-  const T *x[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    x[q] = static_cast<const T *>(j.X) + (size_t)__shfl(row, t + 32 * q) * (size_t)j.ldx;
+  // X: this thread loads piece c of tile rows t, t + 8, ...
+  const int c = threadIdx.x % CH, t = threadIdx.x / CH;
+  constexpr int ROWS = 256 / CH;                   // rows one pass of the threads covers
   for (int d = 0; left != 0; ++d) {
     const int src = __builtin_ctzll(left);
     const int a = __builtin_amdgcn_readlane(id, src);
@@ -308,44 +312,46 @@ __global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
     const int nr = rk - r0 < kShrinkTile ? rk - r0 : kShrinkTile;   // ranks of this tile
     const int nb = (nr + 15) / 16;
     const T *w = static_cast<const T *>(j.W) + (size_t)a * (size_t)j.stride;
-    Frag xr[2], wr[2];
+    Frag xr[PER], wr[PER];
     // pieces of W: (rank, k piece) of a rank-major tile, (k, rank piece) of the other
-    const int per = j.kmaj ? 8 : (16 * nb + VEC - 1) / VEC;   // pieces per row
-    const int pieces = j.kmaj ? 16 * nb * 8 : BK * per;
+    const int per = j.kmaj ? CH : 16 * nb / VEC;   // pieces per row
     auto load = [&](int k) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) xr[q] = load_frag(x[q], k + c * VEC, k1);
+      for (int q = 0; q < PER; ++q) {
+        const T *x = static_cast<const T *>(j.X) + (size_t)__shfl(row, t + ROWS * q) * (size_t)j.ldx;
+        xr[q] = load_frag(x, k + c * VEC, k1);
+      }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < PER; ++q) {
+        if (q >= PER / 4 * nb) break;              // 16 nb rows of CH pieces, or BK of per
         const int i = threadIdx.x + 256 * q;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) wr[q][e] = (T)0.0f;
-        if (i >= pieces) continue;
         const int u = i / per, v = i % per;
-        if (j.kmaj) {
-          if (u < nr) wr[q] = load_frag(w + (size_t)(r0 + u) * (size_t)j.ldw, k + v * VEC, k1);
-        } else if (k + u < k1) {
-          wr[q] = load_frag(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, rk);
-        }
+        // outside the matrix: the length 0 gives zeros and reads nothing
+        if (j.kmaj)
+          wr[q] = load_frag(w + (size_t)(r0 + u) * (size_t)j.ldw, k + v * VEC, u < nr ? k1 : 0);
+        else
+          wr[q] = load_frag(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, k + u < k1 ? rk : 0);
       }
     };
-    auto store = [&](int slot) {
+    auto store = [&]() {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        *reinterpret_cast<Frag *>(lds[slot][0] + (t + 32 * q) * 128 + 16 * (c ^ (t & 7))) = xr[q];
+      for (int q = 0; q < PER; ++q) {
+        const int u = t + ROWS * q;
+        *reinterpret_cast<Frag *>(ldx_ + u * kStepBytes + 16 * (c ^ (u & 7))) = xr[q];
+      }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < PER; ++q) {
+        if (q >= PER / 4 * nb) break;
         const int i = threadIdx.x + 256 * q;
-        if (i >= pieces) continue;
         const int u = i / per, v = i % per;
         if (j.kmaj) {
-          *reinterpret_cast<Frag *>(lds[slot][1] + u * 128 + 16 * (v ^ (u & 7))) = wr[q];
+          *reinterpret_cast<Frag *>(ldw_ + u * kStepBytes + 16 * (v ^ (u & 7))) = wr[q];
         } else {
           // k u of ranks v*VEC .. +VEC-1
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
             const int r = v * VEC + e;
-            *reinterpret_cast<T *>(lds[slot][1] + r * 128 + 16 * ((u / VEC) ^ (r & 7)) +
+            *reinterpret_cast<T *>(ldw_ + r * kStepBytes + 16 * ((u / VEC) ^ (r & 7)) +
                                    u % VEC * sizeof(T)) = wr[q][e];
           }
         }
@@ -355,27 +361,24 @@ __global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     load(k0);
-    store(0);
-    __syncthreads();
-    int slot = 0;
-    for (int k = k0; k < k1; k += BK, slot ^= 1) {
-      const bool more = k + BK < k1;
-      if (more) load(k + BK);
+    for (int k = k0; k < k1; k += BK) {
+      store();
+      __syncthreads();
+      if (k + BK < k1) load(k + BK);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < CH / 4; ++s) {
         const int xrow = 16 * wave + li;
-        const Frag xf = *reinterpret_cast<const Frag *>(lds[slot][0] + xrow * 128 +
+        const Frag xf = *reinterpret_cast<const Frag *>(ldx_ + xrow * kStepBytes +
                                                         16 * ((4 * s + lg) ^ (xrow & 7)));
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           if (b >= nb) break;
           const int wrow = 16 * b + li;
-          const Frag wf = *reinterpret_cast<const Frag *>(lds[slot][1] + wrow * 128 +
+          const Frag wf = *reinterpret_cast<const Frag *>(ldw_ + wrow * kStepBytes +
                                                           16 * ((4 * s + lg) ^ (wrow & 7)));
           acc[b] = mma16(xf, wf, acc[b]);
         }
       }
-      if (more) store(slot ^ 1);
       __syncthreads();
     }
     // rows 16 wave + 4 lg + e of the tile, ranks r0 + 16 b + li
@@ -433,26 +436,6 @@ __global__ __launch_bounds__(256) void lora_shrink_sum(TileShrinkParams p) {
     o[16] = (_Float16)(rest == rest ? rest : 0.0f);   // an infinity has no rest
   }
   if (lane == 0) j.scale[row] = ldexpf(a >= 0 && p.ascale ? p.ascale[a] : 1.0f, e);
-}
-
-// T_a[k, r] = A_a[r, k] for the adapters that some row has, ranks padded with
-// zeros to Rp: the right operand of G A as the fp16 product takes it.  grid:
-// (ceil(K/256), L).
-__global__ __launch_bounds__(256) void lora_transpose(const _Float16 *A, int lda, long long stride,
-                                                      const int *start, const int *ranks, int K,
-                                                      int R, int Rp, _Float16 *out) {
-  const int a = blockIdx.y, k = blockIdx.x * 256 + threadIdx.x;
-  if (start[a + 1] == start[a] || k >= K) return;
-  const int rk = rank_of(ranks, a, R);
-  const _Float16 *src = A + (size_t)a * (size_t)stride + k;
-  _Float16 *dst = out + ((size_t)a * K + k) * Rp;
-  for (int r = 0; r < Rp; r += 8) {
-    f16x8 f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      f[e] = r + e < rk ? src[(size_t)(r + e) * (size_t)lda] : (_Float16)0.0f;
-    *reinterpret_cast<f16x8 *>(dst + r) = f;
-  }
 }
 
 // ---------------------------------------------------------------- expand
@@ -612,7 +595,7 @@ struct OuterJob {
   float *D;
   long long stride;
   int K, ldx, ldd, tr;
-  float *P;               // partial sums: (chunks + L) x Rp x K
+  float *P;               // partial sums: (chunks + L) x Rp x K (tr: K x Rp)
 };
 
 struct OuterParams {
@@ -664,14 +647,18 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[b][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       constexpr int U = 4;               // steps loaded together
+      // 16 rows' numbers a lane group, those of the next turn ahead of their use
+      auto rows_at = [&](int i) { return p.perm[i + li < stop ? i + li : stop - 1]; };
+      int next = rows_at(at + 4 * U * wave);
       for (int i0 = at + 4 * U * wave; i0 < stop; i0 += 4 * U * kOuterWaves) {
+        const int here = next;
+        next = rows_at(i0 + 4 * U * kOuterWaves);
         float v[U][NR];
         float x[U][8];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int i = i0 + 4 * u + lg;
-          const bool ok = i < stop;
-          const int row = p.perm[ok ? i : stop - 1];
+          const bool ok = i0 + 4 * u + lg < stop;
+          const int row = __shfl(here, 4 * u + lg);
           const float *vr = j.V + (size_t)row * p.Rp + r0 + li;
 #pragma unroll
           for (int b = 0; b < NR; ++b) v[u][b] = ok && b < nb ? vr[16 * b] : 0.0f;
@@ -708,12 +695,13 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
                 f32x4{acc[b][e][q], acc[b][e + 1][q], acc[b][e + 2][q], acc[b][e + 3][q]};
         __syncthreads();
         for (int q = threadIdx.x; q < 16 * kOuterCols; q += kOuterThreads) {
-          const int r = q / kOuterCols, k = q % kOuterCols;
+          const int r = j.tr ? q % 16 : q / kOuterCols, k = j.tr ? q / 16 : q % kOuterCols;
           if (k0 + k >= j.K) continue;
           float s = 0.0f;
 #pragma unroll
           for (int w = 0; w < kOuterWaves; ++w) s += red[w][r][k];
-          out[(size_t)(r0 + 16 * b + r) * j.K + k0 + k] = s;
+          const int rr = r0 + 16 * b + r;
+          out[j.tr ? (size_t)(k0 + k) * p.Rp + rr : (size_t)rr * j.K + k0 + k] = s;
         }
       }
     }
@@ -737,7 +725,8 @@ __global__ __launch_bounds__(256) void lora_outer_sum(OuterParams p) {
     const int k = j.tr ? (int)(t / p.R) : (int)(t % j.K);
     float sum = 0.0f;
     if (r < rk) {
-      const float *q = j.P + (size_t)(c0 + a) * slot + (size_t)r * j.K + k;
+      const float *q = j.P + (size_t)(c0 + a) * slot +
+                       (j.tr ? (size_t)k * p.Rp + r : (size_t)r * j.K + k);
       for (int c = c0; c <= c1; ++c, q += slot) sum += *q;
     }
     float *d = j.D + (size_t)a * (size_t)j.stride +
@@ -781,22 +770,22 @@ int shrink_z(const LoraCall &c) {
 }
 
 // First products of a call with many rows (one or two jobs): the parts K is
-// divided into, so that there are about four workgroups per CU, and the
-// workgroups per tile of 64 rows that share its adapters out.  Tiles of long
+// divided into, so that there are two workgroups per CU, and the workgroups per tile of 64 rows that share its adapters out.  Tiles of long
 // batches mostly hold one adapter; in a batch of some hundred rows every row may
 // have its own.
 struct TilePlan {
   int tiles, rtiles, parts, z;
 };
 
+int tile_step(const LoraCall &c) { return kStepBytes / (c.half ? 2 : 4); }
+
 TilePlan tile_plan(const LoraCall &c, bool ordered) {
   TilePlan t;
   t.tiles = (c.M + kShrinkTile - 1) / kShrinkTile;
   t.rtiles = (rank_pad(c.R) + kShrinkTile - 1) / kShrinkTile;
-  const int bk = c.half ? 64 : 32;
   const int longest = c.K > c.N ? c.K : c.N;
-  const int most = (longest + 4 * bk - 1) / (4 * bk);   // at least four steps a part
-  int parts = 4 * kCUs / (t.tiles * t.rtiles);
+  const int most = (longest + tile_step(c) - 1) / tile_step(c);
+  int parts = 2 * kCUs / (t.tiles * t.rtiles);
   parts = parts < 8 ? parts : 8;
   parts = parts < most ? parts : most;
   t.parts = parts > 1 ? parts : 1;
@@ -808,8 +797,8 @@ TilePlan tile_plan(const LoraCall &c, bool ordered) {
 }
 
 int tile_chunk(const LoraCall &c, const TilePlan &t, int K) {
-  const int bk = c.half ? 64 : 32;
-  return ((K + t.parts - 1) / t.parts + bk - 1) / bk * bk;
+  const int step = tile_step(c);
+  return ((K + t.parts - 1) / t.parts + step - 1) / step * step;
 }
 
 template <typename T>
@@ -981,7 +970,7 @@ size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
 
 struct GradSpace {
   float *V, *G, *SV, *SG, *PA, *PB, *scale;
-  _Float16 *split, *At;
+  _Float16 *split;
   int *start, *perm;
 };
 
@@ -999,7 +988,6 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   if (c.dX && c.half) {
     s->split = w.take<_Float16>((size_t)c.M * 2 * rp);
     s->scale = w.take<float>((size_t)c.M + 256);
-    s->At = w.take<_Float16>((size_t)c.L * (size_t)c.K * rp);
   }
   if (c.dB) {
     s->V = w.take<float>((size_t)c.M * rp);
@@ -1113,13 +1101,8 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
   e = shrink_tiles<T>(c, p, t, jobs);
   if (e != hipSuccess) return e;
   if (c.dX && c.half) {
-    hipLaunchKernelGGL(lora_transpose, dim3((unsigned)((c.K + 255) / 256), (unsigned)c.L),
-                       dim3(256), 0, c.stream, static_cast<const _Float16 *>(c.A), c.lda,
-                       c.stride_a, s.start, c.ranks, c.K, c.R, p.Rp, s.At);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const LowRank term = {s.split, 2 * p.Rp, s.scale, s.At, p.Rp, (long long)c.K * p.Rp,
-                          c.rows, c.ranks, c.L, c.R};
+    const LowRank term = {s.split, 2 * p.Rp, s.scale, c.A, c.lda, c.stride_a, c.rows,
+                          c.ranks, c.L, c.R};
     e = product_on_term(c, term, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw, c.beta_x, c.dX,
                         c.lddx);
     if (e != hipSuccess) return e;

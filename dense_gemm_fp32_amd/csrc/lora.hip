@@ -82,7 +82,7 @@ __device__ __forceinline__ void shrink_block(const ShrinkParams &p, int row0, in
       f32x4 acc[4][1];
 #pragma unroll
       for (int f = 0; f < 4; ++f) acc[f][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      stream_mac<T, 4, 4>(wr, k0, k1, k1, k1, x4, acc);
+      stream_mac<T, 2, 4>(wr, k0, k1, k1, k1, x4, acc);
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         float v[1];
@@ -168,7 +168,9 @@ __global__ __launch_bounds__(kShrinkThreads, 4) void lora_skinny(SkinnyParams p)
   for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[f][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  stream_mac<T, (NF * NB >= 8 ? 2 : 4), P>(w, k0, k1, k1, k1, x, acc);
+  // as many steps together as two workgroups' registers allow
+  constexpr int U = NF * NB >= 12 ? 1 : (NF * NB >= 8 ? 2 : 4);
+  stream_mac<T, U, P>(w, k0, k1, k1, k1, x, acc);
   float *out = p.S + (size_t)part * M * p.N;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -273,16 +275,102 @@ constexpr int kShrinkTile = 64;   // rows, and ranks, of a workgroup's tile
 // jobs); workgroup z takes the distinct adapters z, z + Z, ... of its rows.
 constexpr int kStepBytes = 512;
 
-template <typename T>
-__global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
-  constexpr int VEC = El<T>::VEC;
-  constexpr int BK = kStepBytes / (int)sizeof(T);
-  constexpr int CH = kStepBytes / 16;              // pieces of a row
-  constexpr int PER = kShrinkTile * CH / 256;      // pieces a thread loads of either tile
-  __shared__ __attribute__((aligned(16))) char ldx_[kShrinkTile * kStepBytes];
-  __shared__ __attribute__((aligned(16))) char ldw_[kShrinkTile * kStepBytes];
+// The tiles of one adapter's step in LDS, X's then W's: 64 rows of kStepBytes,
+// piece c of row u at c ^ (u % 8).
+template <typename T, bool KMAJ>
+struct ShrinkTiles {
   typedef typename El<T>::Frag Frag;
-  const ShrinkJob j = p.job[blockIdx.z];
+  static constexpr int VEC = El<T>::VEC;
+  static constexpr int BK = kStepBytes / (int)sizeof(T);
+  static constexpr int CH = kStepBytes / 16;              // pieces of a row
+  static constexpr int PER = kShrinkTile * CH / 256;      // pieces a thread loads of either tile
+  static constexpr int RP = kShrinkTile / VEC;            // rank pieces of a k (not KMAJ)
+  const ShrinkJob &j;
+  char *lds;
+  const T *w;                                             // the adapter's matrix
+  int row, r0, rk, nr, k1;                                // row: of the tile, one a lane
+
+  // X: piece c of tile row u; W: piece v of rank u, or rank piece v of k u
+  __device__ __forceinline__ const T *x_at(int q, int k, int &u, int &c) const {
+    c = threadIdx.x % CH;
+    u = threadIdx.x / CH + 256 / CH * q;
+    return static_cast<const T *>(j.X) + (size_t)__shfl(row, u) * (size_t)j.ldx + k + c * VEC;
+  }
+  __device__ __forceinline__ void w_piece(int q, int &u, int &v) const {
+    const int i = threadIdx.x + 256 * q;
+    u = i / (KMAJ ? CH : RP);
+    v = i % (KMAJ ? CH : RP);
+  }
+  __device__ __forceinline__ void put_x(int u, int c, const Frag &f) const {
+    *reinterpret_cast<Frag *>(lds + u * kStepBytes + 16 * (c ^ (u & 7))) = f;
+  }
+  __device__ __forceinline__ void put_w(int u, int v, const Frag &f) const {
+    char *l = lds + kShrinkTile * kStepBytes;
+    if constexpr (KMAJ) {
+      *reinterpret_cast<Frag *>(l + u * kStepBytes + 16 * (v ^ (u & 7))) = f;
+    } else {
+      // k u of ranks v*VEC .. +VEC-1
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int r = v * VEC + e;
+        *reinterpret_cast<T *>(l + r * kStepBytes + 16 * ((u / VEC) ^ (r & 7)) +
+                               u % VEC * sizeof(T)) = f[e];
+      }
+    }
+  }
+
+  // A step that loads without a condition: all of it inside the rows, ranks
+  // past the last repeated (their sums are dropped).
+  __device__ __forceinline__ bool whole(int k) const {
+    return k + BK <= k1 && (KMAJ || rk % VEC == 0);
+  }
+  __device__ __forceinline__ void load(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      int u, c;
+      xr[q] = load_whole(x_at(q, k, u, c));
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      int u, v;
+      w_piece(q, u, v);
+      const int r = r0 + (KMAJ ? u : v * VEC), last = rk - (KMAJ ? 1 : VEC);
+      const int rr = r < last ? r : last;
+      wr[q] = load_whole(KMAJ ? w + (size_t)rr * (size_t)j.ldw + k + v * VEC
+                              : w + (size_t)(k + u) * (size_t)j.ldw + rr);
+    }
+  }
+  __device__ __forceinline__ void store(const Frag (&xr)[PER], const Frag (&wr)[PER]) const {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      put_x(threadIdx.x / CH + 256 / CH * q, threadIdx.x % CH, xr[q]);
+      int u, v;
+      w_piece(q, u, v);
+      put_w(u, v, wr[q]);
+    }
+  }
+  // Any other step, piece by piece, zeros outside the matrices.
+  __device__ __forceinline__ void fill(int k) const {
+#pragma unroll 1
+    for (int q = 0; q < PER; ++q) {
+      int u, c;
+      const T *x = x_at(q, k, u, c);
+      put_x(u, c, load_part(x, k1 - k - c * VEC));
+      int v;
+      w_piece(q, u, v);
+      put_w(u, v, KMAJ ? load_part(w + (size_t)(r0 + u) * (size_t)j.ldw + k + v * VEC,
+                                   u < nr ? k1 - k - v * VEC : 0)
+                       : load_part(w + (size_t)(k + u) * (size_t)j.ldw + r0 + v * VEC,
+                                   k + u < k1 ? rk - r0 - v * VEC : 0));
+    }
+  }
+};
+
+template <typename T, bool KMAJ>
+__device__ __forceinline__ void shrink_tile(const TileShrinkParams &p, const ShrinkJob &j,
+                                            char *lds) {
+  typedef ShrinkTiles<T, KMAJ> Tiles;
+  typedef typename El<T>::Frag Frag;
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
   const int zi = blockIdx.y % p.z, part = blockIdx.y / p.z % p.parts;
@@ -299,82 +387,36 @@ __global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
   int id = pos0 + lane < count ? adapter_of(p.rows, row, p.M, p.L) : -1;
   if (id >= 0 && rank_of(p.ranks, id, p.R) <= r0) id = -1;
   unsigned long long left = __ballot(id >= 0);
-  // X: this thread loads piece c of tile rows t, t + 8, ...
-  const int c = threadIdx.x % CH, t = threadIdx.x / CH;
-  constexpr int ROWS = 256 / CH;                   // rows one pass of the threads covers
   for (int d = 0; left != 0; ++d) {
-    const int src = __builtin_ctzll(left);
-    const int a = __builtin_amdgcn_readlane(id, src);
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
     const unsigned long long same = __ballot(id == a);
     left &= ~same;
     if (d % p.z != zi) continue;
     const int rk = rank_of(p.ranks, a, p.R);
     const int nr = rk - r0 < kShrinkTile ? rk - r0 : kShrinkTile;   // ranks of this tile
     const int nb = (nr + 15) / 16;
-    const T *w = static_cast<const T *>(j.W) + (size_t)a * (size_t)j.stride;
-    Frag xr[PER], wr[PER];
-    // pieces of W: (rank, k piece) of a rank-major tile, (k, rank piece) of the other
-    const int per = j.kmaj ? CH : 16 * nb / VEC;   // pieces per row
-    auto load = [&](int k) {
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const T *x = static_cast<const T *>(j.X) + (size_t)__shfl(row, t + ROWS * q) * (size_t)j.ldx;
-        xr[q] = load_frag(x, k + c * VEC, k1);
-      }
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        if (q >= PER / 4 * nb) break;              // 16 nb rows of CH pieces, or BK of per
-        const int i = threadIdx.x + 256 * q;
-        const int u = i / per, v = i % per;
-        // outside the matrix: the length 0 gives zeros and reads nothing
-        if (j.kmaj)
-          wr[q] = load_frag(w + (size_t)(r0 + u) * (size_t)j.ldw, k + v * VEC, u < nr ? k1 : 0);
-        else
-          wr[q] = load_frag(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, k + u < k1 ? rk : 0);
-      }
-    };
-    auto store = [&]() {
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const int u = t + ROWS * q;
-        *reinterpret_cast<Frag *>(ldx_ + u * kStepBytes + 16 * (c ^ (u & 7))) = xr[q];
-      }
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        if (q >= PER / 4 * nb) break;
-        const int i = threadIdx.x + 256 * q;
-        const int u = i / per, v = i % per;
-        if (j.kmaj) {
-          *reinterpret_cast<Frag *>(ldw_ + u * kStepBytes + 16 * (v ^ (u & 7))) = wr[q];
-        } else {
-          // k u of ranks v*VEC .. +VEC-1
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const int r = v * VEC + e;
-            *reinterpret_cast<T *>(ldw_ + r * kStepBytes + 16 * ((u / VEC) ^ (r & 7)) +
-                                   u % VEC * sizeof(T)) = wr[q][e];
-          }
-        }
-      }
-    };
+    const Tiles tiles = {j, lds, static_cast<const T *>(j.W) + (size_t)a * (size_t)j.stride, row,
+                         r0, rk, nr, k1};
+    Frag xr[Tiles::PER], wr[Tiles::PER];
     f32x4 acc[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    load(k0);
-    for (int k = k0; k < k1; k += BK) {
-      store();
+    if (tiles.whole(k0)) tiles.load(k0, xr, wr);
+    for (int k = k0; k < k1; k += Tiles::BK) {
+      if (tiles.whole(k)) tiles.store(xr, wr);
+      else tiles.fill(k);
       __syncthreads();
-      if (k + BK < k1) load(k + BK);
-#pragma unroll
-      for (int s = 0; s < CH / 4; ++s) {
+      if (tiles.whole(k + Tiles::BK)) tiles.load(k + Tiles::BK, xr, wr);
+#pragma unroll 2
+      for (int s = 0; s < Tiles::CH / 4; ++s) {
         const int xrow = 16 * wave + li;
-        const Frag xf = *reinterpret_cast<const Frag *>(ldx_ + xrow * kStepBytes +
+        const Frag xf = *reinterpret_cast<const Frag *>(lds + xrow * kStepBytes +
                                                         16 * ((4 * s + lg) ^ (xrow & 7)));
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           if (b >= nb) break;
-          const int wrow = 16 * b + li;
-          const Frag wf = *reinterpret_cast<const Frag *>(ldw_ + wrow * kStepBytes +
+          const int wrow = kShrinkTile + 16 * b + li;
+          const Frag wf = *reinterpret_cast<const Frag *>(lds + wrow * kStepBytes +
                                                           16 * ((4 * s + lg) ^ (wrow & 7)));
           acc[b] = mma16(xf, wf, acc[b]);
         }
@@ -393,6 +435,14 @@ __global__ __launch_bounds__(256) void lora_shrink_tile(TileShrinkParams p) {
         if (b < nb) out[16 * b] = acc[b][e];
     }
   }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256, 2) void lora_shrink_tile(TileShrinkParams p) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * kShrinkTile * kStepBytes];
+  const ShrinkJob &j = p.job[blockIdx.z];
+  if (j.kmaj) shrink_tile<T, true>(p, j, lds);
+  else shrink_tile<T, false>(p, j, lds);
 }
 
 // Sums the parts of each row's V, a wave a row: as fp32, and as the pairs of
@@ -632,6 +682,7 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
   const int kc = k0 + 8 * li;
+  const bool whole = k0 + kOuterCols <= j.K;
   const int total = p.start[p.L];
   int at = blockIdx.y * p.chunk;
   const int end = at + p.chunk < total ? at + p.chunk : total;
@@ -655,23 +706,31 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
         next = rows_at(i0 + 4 * U * kOuterWaves);
         float v[U][NR];
         float x[U][8];
+        typename El<T>::Frag xf[U][8 / VEC];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const bool ok = i0 + 4 * u + lg < stop;
           const int row = __shfl(here, 4 * u + lg);
           const float *vr = j.V + (size_t)row * p.Rp + r0 + li;
 #pragma unroll
-          for (int b = 0; b < NR; ++b) v[u][b] = ok && b < nb ? vr[16 * b] : 0.0f;
-          const T *xr = static_cast<const T *>(j.X) + (size_t)row * (size_t)j.ldx;
-          // rows behind the last enter as zeros on both sides
-          const int lim = ok ? j.K : 0;
-#pragma unroll
-          for (int h = 0; h < 8; h += VEC) {
-            const typename El<T>::Frag f = load_frag(xr, kc + h, lim);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[u][h + e] = (float)f[e];
+          for (int b = 0; b < NR; ++b) {
+            const float f = vr[b < nb ? 16 * b : 0];
+            v[u][b] = ok ? f : 0.0f;
           }
+          const T *xr = static_cast<const T *>(j.X) + (size_t)row * (size_t)j.ldx + kc;
+#pragma unroll
+          for (int h = 0; h < 8 / VEC; ++h)
+            xf[u][h] = whole ? load_whole(xr + h * VEC) : load_part(xr + h * VEC, j.K - kc - h * VEC);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        // rows behind the last enter as zeros on both sides
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int h = 0; h < 8 / VEC; ++h)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              x[u][h * VEC + e] = i0 + 4 * u + lg < stop ? (float)xf[u][h][e] : 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll

@@ -41,16 +41,28 @@ __global__ __launch_bounds__(256) void moe_logits(const T *X, int ldx, const T *
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = X + (size_t)(t0 + i < M ? t0 + i : M - 1) * (size_t)ldx;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
+  constexpr int VEC = El<T>::VEC;
+  auto add = [&](const typename El<T>::Frag &wf, const typename El<T>::Frag (&xf)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[i] += (double)wf[j] * (double)xf[i][j];
+  };
+  int k = threadIdx.x * VEC;
 #pragma unroll 2
-  for (int k = threadIdx.x * El<T>::VEC; k < D; k += 256 * El<T>::VEC) {
+  for (; k - (int)threadIdx.x * VEC + 256 * VEC <= D; k += 256 * VEC) {
+    const typename El<T>::Frag wf = load_whole(w + k);
+    typename El<T>::Frag xf[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xf[i] = load_whole(x[i] + k);
+    add(wf, xf);
+  }
+  if (k < D) {
     const typename El<T>::Frag wf = load_frag(w, k, D);
     typename El<T>::Frag xf[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) xf[i] = load_frag(x[i], k, D);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < El<T>::VEC; ++j) s[i] += (double)wf[j] * (double)xf[i][j];
+    add(wf, xf);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -53,25 +53,31 @@ __device__ __forceinline__ typename El<T>::Frag load_whole(const T *p) {
   return *reinterpret_cast<const Any *>(p);
 }
 
-// Elements k .. k+VEC-1 of a row of K elements, 0 beyond its end.
-template <typename T>
-__device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, int K) {
-  if (k + El<T>::VEC <= K) return load_whole(row + k);
-  typename El<T>::Frag f;
-#pragma unroll
-  for (int e = 0; e < El<T>::VEC; ++e) f[e] = k + e < K ? row[k + e] : (T)0.0f;
+// The first n of VEC elements, the others 0: one at a time, since this is for
+// the ends of rows only and unrolled it costs a kernel that has several of
+// them in flight the registers of every element's address.
+__device__ __forceinline__ f16x8 load_part(const _Float16 *p, int n) {
+  unsigned long long lo = 0, hi = 0;
+#pragma unroll 1
+  for (int e = (n < 8 ? n : 8) - 1; e >= 0; --e) {
+    hi = (hi << 16) | (lo >> 48);
+    lo = (lo << 16) | __builtin_bit_cast(uint16_t, p[e]);
+  }
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(f16x8, u64x2{lo, hi});
+}
+
+__device__ __forceinline__ f32x4 load_part(const float *p, int n) {
+  f32x4 f = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+  for (int e = (n < 4 ? n : 4) - 1; e >= 0; --e) f = f32x4{p[e], f[0], f[1], f[2]};
   return f;
 }
 
-// The same elements where consecutive k lie ld elements apart (col: the
-// address of k = 0).
+// Elements k .. k+VEC-1 of a row of K elements, 0 beyond its end.
 template <typename T>
-__device__ __forceinline__ typename El<T>::Frag load_frag_strided(const T *col, size_t ld, int k,
-                                                                  int K) {
-  typename El<T>::Frag f;
-#pragma unroll
-  for (int e = 0; e < El<T>::VEC; ++e) f[e] = k + e < K ? col[(size_t)(k + e) * ld] : (T)0.0f;
-  return f;
+__device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, int K) {
+  return k + El<T>::VEC <= K ? load_whole(row + k) : load_part(row + k, K - k);
 }
 
 // acc[f][b] += W block f (16 rows, this lane's at w[f]) times activation block

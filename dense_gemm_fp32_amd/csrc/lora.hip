@@ -288,7 +288,7 @@ struct ShrinkTiles {
   const ShrinkJob &j;
   char *lds;
   const T *w;                                             // the adapter's matrix
-  int row, r0, rk, nr, k1;                                // row: of the tile, one a lane
+  int row, r0, rk, R;                                     // row: of the tile, one a lane
 
   // X: piece c of tile row u; W: piece v of rank u, or rank piece v of k u
   __device__ __forceinline__ const T *x_at(int q, int k, int &u, int &c) const {
@@ -319,12 +319,9 @@ struct ShrinkTiles {
     }
   }
 
-  // A step that loads without a condition: all of it inside the rows, ranks
-  // past the last repeated (their sums are dropped).
-  __device__ __forceinline__ bool whole(int k) const {
-    return k + BK <= k1 && (KMAJ || rk % VEC == 0);
-  }
-  __device__ __forceinline__ void load(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
+  // A step all of which lies inside the rows; ranks past the last are repeated
+  // or, where they are there, taken as they are (their sums are dropped).
+  __device__ __forceinline__ void load_whole_step(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       int u, c;
@@ -334,11 +331,40 @@ struct ShrinkTiles {
     for (int q = 0; q < PER; ++q) {
       int u, v;
       w_piece(q, u, v);
-      const int r = r0 + (KMAJ ? u : v * VEC), last = rk - (KMAJ ? 1 : VEC);
-      const int rr = r < last ? r : last;
-      wr[q] = load_whole(KMAJ ? w + (size_t)rr * (size_t)j.ldw + k + v * VEC
-                              : w + (size_t)(k + u) * (size_t)j.ldw + rr);
+      if (KMAJ) {
+        const int r = r0 + u < rk ? r0 + u : rk - 1;
+        wr[q] = load_whole(w + (size_t)r * (size_t)j.ldw + k + v * VEC);
+      } else {
+        wr[q] = load_frag(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, R);
+      }
     }
+  }
+  // The step in which the rows end: zeros behind the end on both sides.
+  __device__ __forceinline__ void load_last_step(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      int u, c;
+      const T *x = x_at(q, 0, u, c) - c * VEC;
+      xr[q] = load_frag(x, k + c * VEC, j.K);
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      int u, v;
+      w_piece(q, u, v);
+      if (KMAJ) {
+        const int r = r0 + u < rk ? r0 + u : rk - 1;
+        wr[q] = load_frag(w + (size_t)r * (size_t)j.ldw, k + v * VEC, j.K);
+      } else {
+        const bool in = k + u < j.K;
+        wr[q] = move_down(load_frag(w + (size_t)(in ? k + u : j.K - 1) * (size_t)j.ldw,
+                                    r0 + v * VEC, R),
+                          in ? 0 : VEC);
+      }
+    }
+  }
+  __device__ __forceinline__ void load(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
+    if (k + BK <= j.K) load_whole_step(k, xr, wr);
+    else load_last_step(k, xr, wr);
   }
   __device__ __forceinline__ void store(const Frag (&xr)[PER], const Frag (&wr)[PER]) const {
 #pragma unroll
@@ -347,21 +373,6 @@ struct ShrinkTiles {
       int u, v;
       w_piece(q, u, v);
       put_w(u, v, wr[q]);
-    }
-  }
-  // Any other step, piece by piece, zeros outside the matrices.
-  __device__ __forceinline__ void fill(int k) const {
-#pragma unroll 1
-    for (int q = 0; q < PER; ++q) {
-      int u, c;
-      const T *x = x_at(q, k, u, c);
-      put_x(u, c, load_part(x, k1 - k - c * VEC));
-      int v;
-      w_piece(q, u, v);
-      put_w(u, v, KMAJ ? load_part(w + (size_t)(r0 + u) * (size_t)j.ldw + k + v * VEC,
-                                   u < nr ? k1 - k - v * VEC : 0)
-                       : load_part(w + (size_t)(k + u) * (size_t)j.ldw + r0 + v * VEC,
-                                   k + u < k1 ? rk - r0 - v * VEC : 0));
     }
   }
 };
@@ -396,17 +407,16 @@ __device__ __forceinline__ void shrink_tile(const TileShrinkParams &p, const Shr
     const int nr = rk - r0 < kShrinkTile ? rk - r0 : kShrinkTile;   // ranks of this tile
     const int nb = (nr + 15) / 16;
     const Tiles tiles = {j, lds, static_cast<const T *>(j.W) + (size_t)a * (size_t)j.stride, row,
-                         r0, rk, nr, k1};
+                         r0, rk, p.R};
     Frag xr[Tiles::PER], wr[Tiles::PER];
     f32x4 acc[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (tiles.whole(k0)) tiles.load(k0, xr, wr);
+    tiles.load(k0, xr, wr);
     for (int k = k0; k < k1; k += Tiles::BK) {
-      if (tiles.whole(k)) tiles.store(xr, wr);
-      else tiles.fill(k);
+      tiles.store(xr, wr);
       __syncthreads();
-      if (tiles.whole(k + Tiles::BK)) tiles.load(k + Tiles::BK, xr, wr);
+      if (k + Tiles::BK < k1) tiles.load(k + Tiles::BK, xr, wr);
 #pragma unroll 2
       for (int s = 0; s < Tiles::CH / 4; ++s) {
         const int xrow = 16 * wave + li;
@@ -905,7 +915,8 @@ SkinnyPlan skinny_plan(const LoraCall &c) {
   const int kstep = (c.half ? 32 : 16) * s.P;
   const int steps = (c.K + kstep - 1) / kstep;
   const int most = steps / (2 * kShrinkWaves) > 1 ? steps / (2 * kShrinkWaves) : 1;
-  for (s.NF = 4;; s.NF /= 2) {
+  // (four blocks of each would spill at two workgroups per CU)
+  for (s.NF = s.NB > 3 ? 2 : 4;; s.NF /= 2) {
     s.tiles = (c.N + br * s.NF - 1) / (br * s.NF);
     s.parts = kCUs / s.tiles > 1 ? kCUs / s.tiles : 1;
     if (s.parts > most) s.parts = most;
@@ -930,7 +941,7 @@ void launch_skinny(const SkinnyPlan &s, const SkinnyParams &p, hipStream_t strea
   else if (s.NB == 1) launch_skinny<T, NF, 1, 1>(p, stream);
   else if (s.NB == 2) launch_skinny<T, NF, 2, 1>(p, stream);
   else if (s.NB == 3) launch_skinny<T, NF, 3, 1>(p, stream);
-  else launch_skinny<T, NF, 4, 1>(p, stream);
+  else if constexpr (NF < 4) launch_skinny<T, NF, 4, 1>(p, stream);
 }
 
 template <typename T>

@@ -74,10 +74,37 @@ __device__ __forceinline__ f32x4 load_part(const float *p, int n) {
   return f;
 }
 
-// Elements k .. k+VEC-1 of a row of K elements, 0 beyond its end.
+// v's elements moved down by s places (none for s <= 0, all out for s >= VEC),
+// zeros behind them.
+__device__ __forceinline__ f16x8 move_down(f16x8 v, int s) {
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  const u64x2 w = __builtin_bit_cast(u64x2, v);
+  unsigned long long lo = w[0], hi = w[1];
+  s = s > 0 ? s : 0;
+  if (s & 4) lo = hi, hi = 0;
+  if (s & 2) lo = (lo >> 32) | (hi << 32), hi >>= 32;
+  if (s & 1) lo = (lo >> 16) | (hi << 48), hi >>= 16;
+  if (s >= 8) lo = hi = 0;
+  return __builtin_bit_cast(f16x8, u64x2{lo, hi});
+}
+
+__device__ __forceinline__ f32x4 move_down(f32x4 v, int s) {
+  s = s > 0 ? s : 0;
+  if (s & 2) v = f32x4{v[2], v[3], 0.0f, 0.0f};
+  if (s & 1) v = f32x4{v[1], v[2], v[3], 0.0f};
+  if (s >= 4) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  return v;
+}
+
+// Elements k .. k+VEC-1 of a row of K elements, 0 beyond its end.  A row of at
+// least VEC elements is read by one load that stays inside it, whatever k, and
+// moved into place, so that several such loads can be on their way together.
 template <typename T>
 __device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, int K) {
-  return k + El<T>::VEC <= K ? load_whole(row + k) : load_part(row + k, K - k);
+  constexpr int VEC = El<T>::VEC;
+  if (K < VEC) return load_part(row + k, K - k);
+  const int last = K - VEC;
+  return move_down(load_whole(row + (k < last ? k : last)), k - last);
 }
 
 // acc[f][b] += W block f (16 rows, this lane's at w[f]) times activation block

@@ -343,7 +343,7 @@ int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int l
  *   B, ldb, stride_b   its N x R matrix at B + a*stride_b, ldb >= max(1, R)
  *   scale     device, L floats (NULL: 1)
  *   ranks     device, L ints (NULL: R): the ranks in use, clamped to 0 .. R;
- *             A's rows and B's columns from there on are not read
+ *             whatever A's rows and B's columns from there on hold has no effect
  *   rows      device, M ints in any order: the adapter of each row; an index
  *             outside 0 .. L-1 (-1, say) means no adapter for that row
  *

@@ -257,7 +257,7 @@ struct ShrinkJob {
 struct TileShrinkParams {
   ShrinkJob job[2];
   const int *rows, *ranks;
-  const int *start, *perm;   // rows in adapter order (NULL: as they come)
+  const int *start, *perm, *owner;   // rows in adapter order (NULL: as they come)
   const float *ascale;
   int M, L, R, Rp, parts, z;
 };
@@ -288,7 +288,7 @@ struct ShrinkTiles {
   const ShrinkJob &j;
   char *lds;
   const T *w;                                             // the adapter's matrix
-  int row, r0, rk, R;                                     // row: of the tile, one a lane
+  int row, r0, rk, R, nb;                                 // row: of the tile, one a lane
 
   // X: piece c of tile row u; W: piece v of rank u, or rank piece v of k u
   __device__ __forceinline__ const T *x_at(int q, int k, int &u, int &c) const {
@@ -300,6 +300,11 @@ struct ShrinkTiles {
     const int i = threadIdx.x + 256 * q;
     u = i / (KMAJ ? CH : RP);
     v = i % (KMAJ ? CH : RP);
+  }
+  // Whether any rank of this thread's piece q is in a block of 16 that the
+  // adapter has (not KMAJ: the same for all q).
+  __device__ __forceinline__ bool wanted(int q) const {
+    return KMAJ ? 256 / CH * q < 16 * nb : (int)threadIdx.x % RP * VEC < 16 * nb;
   }
   __device__ __forceinline__ void put_x(int u, int c, const Frag &f) const {
     *reinterpret_cast<Frag *>(lds + u * kStepBytes + 16 * (c ^ (u & 7))) = f;
@@ -329,6 +334,7 @@ struct ShrinkTiles {
     }
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
+      if (!wanted(q)) break;
       int u, v;
       w_piece(q, u, v);
       if (KMAJ) {
@@ -349,6 +355,7 @@ struct ShrinkTiles {
     }
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
+      if (!wanted(q)) break;
       int u, v;
       w_piece(q, u, v);
       if (KMAJ) {
@@ -370,6 +377,10 @@ struct ShrinkTiles {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       put_x(threadIdx.x / CH + 256 / CH * q, threadIdx.x % CH, xr[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      if (!wanted(q)) break;
       int u, v;
       w_piece(q, u, v);
       put_w(u, v, wr[q]);
@@ -395,8 +406,8 @@ __device__ __forceinline__ void shrink_tile(const TileShrinkParams &p, const Shr
   // the row at each position of the tile, one a lane
   const int pos = pos0 + lane < count ? pos0 + lane : count - 1;
   const int row = p.perm ? p.perm[pos] : pos;
-  int id = pos0 + lane < count ? adapter_of(p.rows, row, p.M, p.L) : -1;
-  if (id >= 0 && rank_of(p.ranks, id, p.R) <= r0) id = -1;
+  int id = p.perm ? p.owner[pos] : adapter_of(p.rows, row, p.M, p.L);
+  if (pos0 + lane >= count || (id >= 0 && rank_of(p.ranks, id, p.R) <= r0)) id = -1;
   unsigned long long left = __ballot(id >= 0);
   for (int d = 0; left != 0; ++d) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
@@ -407,7 +418,7 @@ __device__ __forceinline__ void shrink_tile(const TileShrinkParams &p, const Shr
     const int nr = rk - r0 < kShrinkTile ? rk - r0 : kShrinkTile;   // ranks of this tile
     const int nb = (nr + 15) / 16;
     const Tiles tiles = {j, lds, static_cast<const T *>(j.W) + (size_t)a * (size_t)j.stride, row,
-                         r0, rk, p.R};
+                         r0, rk, p.R, nb};
     Frag xr[Tiles::PER], wr[Tiles::PER];
     f32x4 acc[4];
 #pragma unroll
@@ -417,7 +428,7 @@ __device__ __forceinline__ void shrink_tile(const TileShrinkParams &p, const Shr
       tiles.store(xr, wr);
       __syncthreads();
       if (k + Tiles::BK < k1) tiles.load(k + Tiles::BK, xr, wr);
-#pragma unroll 2
+#pragma unroll 1
       for (int s = 0; s < Tiles::CH / 4; ++s) {
         const int xrow = 16 * wave + li;
         const Frag xf = *reinterpret_cast<const Frag *>(lds + xrow * kStepBytes +
@@ -591,13 +602,14 @@ __global__ __launch_bounds__(256) void scale_batch(int rows, int cols, float bet
 
 // ---------------------------------------------------------------- rows of each adapter
 
-// perm[start[a] .. start[a+1]) := the rows of adapter a, in order.  One
+// perm[start[a] .. start[a+1]) := the rows of adapter a, in order, and
+// owner[...] := a.  One
 // workgroup per adapter (grid: L): it counts the rows of smaller adapters and
 // its own, then writes its own.
 constexpr int kGroupThreads = 1024;
 
 __global__ __launch_bounds__(kGroupThreads) void lora_group(const int *rows, int M, int L,
-                                                            int *start, int *perm) {
+                                                            int *start, int *perm, int *owner) {
   __shared__ int cnt[2][kGroupThreads / kWave];
   const int a = blockIdx.x;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -640,7 +652,11 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group(const int *rows, int
       before += w < wave ? cnt[0][w] : 0;
       all += cnt[0][w];
     }
-    if (is) perm[at + before + __popcll(m & ((1ull << lane) - 1))] = i;
+    if (is) {
+      const int pos = at + before + __popcll(m & ((1ull << lane) - 1));
+      perm[pos] = i;
+      owner[pos] = a;
+    }
     at += all;
   }
 }
@@ -660,7 +676,7 @@ struct OuterJob {
 
 struct OuterParams {
   OuterJob job[2];
-  const int *rows, *ranks, *start, *perm;
+  const int *ranks, *start, *perm, *owner;
   const float *scale;
   int L, R, Rp, chunk;    // rows, in adapter order, per chunk
   float alpha, beta;
@@ -697,8 +713,9 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
   int at = blockIdx.y * p.chunk;
   const int end = at + p.chunk < total ? at + p.chunk : total;
   while (at < end) {
-    const int a = p.rows[p.perm[at]];
-    const int stop = p.start[a + 1] < end ? p.start[a + 1] : end;
+    const int a = p.owner[at];
+    const int s0 = p.start[a], s1 = p.start[a + 1];
+    const int stop = s1 < end ? s1 : end;
     const int rk = rank_of(p.ranks, a, p.R);
     const int nb = rk - r0 <= 0 ? 0 : (rk - r0 > 16 ? NR : 1);
     if (nb > 0) {
@@ -751,6 +768,8 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
                 acc[b][e] =
                     __builtin_amdgcn_mfma_f32_16x16x4f32(v[u][b], x[u][e], acc[b][e], 0, 0, 0);
       }
+      // an adapter all of whose rows lie in this chunk needs no partial sums
+      const bool all = s0 >= (int)blockIdx.y * p.chunk && s1 <= end;
       float *out = j.P + (size_t)(blockIdx.y + a) * p.Rp * j.K;
 #pragma unroll
       for (int b = 0; b < NR; ++b) {
@@ -770,7 +789,15 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
 #pragma unroll
           for (int w = 0; w < kOuterWaves; ++w) s += red[w][r][k];
           const int rr = r0 + 16 * b + r;
-          out[j.tr ? (size_t)(k0 + k) * p.Rp + rr : (size_t)rr * j.K + k0 + k] = s;
+          if (!all) {
+            out[j.tr ? (size_t)(k0 + k) * p.Rp + rr : (size_t)rr * j.K + k0 + k] = s;
+          } else if (rr < rk) {
+            float *d = j.D + (size_t)a * (size_t)j.stride +
+                       (j.tr ? (size_t)(k0 + k) * (size_t)j.ldd + rr
+                             : (size_t)rr * (size_t)j.ldd + k0 + k);
+            const float o = p.alpha * (p.scale ? p.scale[a] : 1.0f) * s;
+            *d = p.beta != 0.0f ? __builtin_fmaf(p.beta, *d, o) : o;
+          }
         }
       }
     }
@@ -778,30 +805,51 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
   }
 }
 
-// grid: (blocks, L, jobs).
+// D_a from its partial sums, four adjacent elements a thread; what lora_outer
+// wrote itself is left, but for the ranks beyond the adapter's.  grid: (blocks,
+// L, jobs).
 __global__ __launch_bounds__(256) void lora_outer_sum(OuterParams p) {
   const OuterJob j = p.job[blockIdx.z];
   const int a = blockIdx.y;
   const int rk = rank_of(p.ranks, a, p.R);
   const int b = p.start[a], n = p.start[a + 1] - b;
   const int c0 = b / p.chunk, c1 = n > 0 ? (b + n - 1) / p.chunk : c0 - 1;
+  const bool done = n > 0 && c0 == c1;
+  if (done && rk == p.R) return;
   const float s = p.alpha * (p.scale ? p.scale[a] : 1.0f);
-  const long long total = (long long)p.R * j.K;
   const size_t slot = (size_t)p.Rp * j.K;
+  // rows of `len`: ranks of one k (tr), or k of one rank
+  const int len = j.tr ? p.R : j.K, pitch = j.tr ? p.Rp : j.K;
+  const long long quads = (len + 3) / 4;
+  const long long total = quads * (j.tr ? j.K : p.R);
   for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total;
        t += (long long)gridDim.x * 256) {
-    const int r = j.tr ? (int)(t % p.R) : (int)(t / j.K);
-    const int k = j.tr ? (int)(t / p.R) : (int)(t % j.K);
-    float sum = 0.0f;
-    if (r < rk) {
-      const float *q = j.P + (size_t)(c0 + a) * slot +
-                       (j.tr ? (size_t)k * p.Rp + r : (size_t)r * j.K + k);
-      for (int c = c0; c <= c1; ++c, q += slot) sum += *q;
+    const int i = (int)(t / quads), e0 = 4 * (int)(t % quads);
+    const int count = len - e0 < 4 ? len - e0 : 4;
+    // of these, the ones within the rank
+    const int in = j.tr ? (rk - e0 < count ? rk - e0 : count) : (i < rk ? count : 0);
+    if (done && in == count) continue;
+    f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (in > 0 && !done) {
+      const float *q = j.P + (size_t)(c0 + a) * slot + (size_t)i * pitch + e0;
+      for (int c = c0; c <= c1; ++c, q += slot)
+        sum += count == 4 ? load_whole(q) : load_part(q, count);
     }
-    float *d = j.D + (size_t)a * (size_t)j.stride +
-               (j.tr ? (size_t)k * (size_t)j.ldd + r : (size_t)r * (size_t)j.ldd + k);
-    const float o = r < rk && n > 0 ? s * sum : 0.0f;
-    *d = p.beta != 0.0f ? __builtin_fmaf(p.beta, *d, o) : o;
+    float *d = j.D + (size_t)a * (size_t)j.stride + (size_t)i * (size_t)j.ldd + e0;
+    const bool all = count == 4 && !(done && in > 0);
+    f32x4 old = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.beta != 0.0f) old = all ? load_whole(d) : load_part(d, count);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float o = e < in ? s * sum[e] : 0.0f;
+      old[e] = p.beta != 0.0f ? __builtin_fmaf(p.beta, old[e], o) : o;
+    }
+    if (all) {
+      typedef float Any __attribute__((ext_vector_type(4), aligned(4)));
+      *reinterpret_cast<Any *>(d) = old;
+    } else {
+      for (int e = done ? (in > 0 ? in : 0) : 0; e < count; ++e) d[e] = old[e];
+    }
   }
 }
 
@@ -1041,7 +1089,7 @@ size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
 struct GradSpace {
   float *V, *G, *SV, *SG, *PA, *PB, *scale;
   _Float16 *split;
-  int *start, *perm;
+  int *start, *perm, *owner;
 };
 
 size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
@@ -1051,6 +1099,7 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   const size_t parts = (size_t)tile_plan(c, true).parts;
   s->start = w.take<int>((size_t)c.L + 1);
   s->perm = w.take<int>((size_t)c.M);
+  s->owner = w.take<int>((size_t)c.M);
   if (c.dX || c.dA) {
     s->G = w.take<float>((size_t)c.M * rp);
     s->SG = w.take<float>(parts * c.M * rp);
@@ -1068,6 +1117,32 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   if (c.dA) s->PA = w.take<float>(slots * rp * (size_t)c.K);
   if (c.dB) s->PB = w.take<float>(slots * rp * (size_t)c.N);
   return w.used;
+}
+
+// C := alpha * A op(B) + C with the fp32 kernels.  Operands whose rows do not
+// allow 16-byte loads are copied first, whatever the size: the calls here that
+// stay below the library's own threshold for it have a long K (1000 x 517 x
+// 3000 with odd rows: 78 us as they are, XXX us copied).
+hipError_t product_f32(const LoraCall &c, bool tb, int N, int K, const void *A, int lda,
+                       const void *B, int ldb, void *C, int ldc) {
+  Call g = {};
+  g.M = c.M;
+  g.N = N;
+  g.K = K;
+  g.alpha = c.alpha;
+  g.beta = 1.0f;
+  g.A = A;
+  g.lda = lda;
+  g.B = B;
+  g.ldb = ldb;
+  g.C = C;
+  g.ldc = ldc;
+  g.tb = tb;
+  g.splits = 1;
+  g.ws_limit = workspace_limit();
+  g.pack_mode = 2;
+  g.stream = c.stream;
+  return launch_f32(g);
 }
 
 // C := alpha * (A op(B) + the term) + beta * C with the fp16 kernels.
@@ -1136,9 +1211,7 @@ hipError_t run(const LoraCall &c, const LoraSpace &s) {
     e = expand<T, true>(c, s.V, c.B, c.ldb, c.stride_b, c.N, c.alpha, c.beta,
                         static_cast<float *>(c.Y), c.ldy);
     if (e != hipSuccess) return e;
-    return (hipError_t)gemm_f32_nt(c.M, c.N, c.K, c.alpha, static_cast<const float *>(c.X), c.ldx,
-                                   static_cast<const float *>(c.W), c.ldw, 1.0f,
-                                   static_cast<float *>(c.Y), c.ldy, c.stream);
+    return product_f32(c, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw, c.Y, c.ldy);
   }
   if (c.M <= kJoinRows) {
     const int rc = gemm_f16f32_nt(c.M, c.N, c.K, 1.0f, static_cast<const gemm_half_t *>(c.X),
@@ -1154,13 +1227,14 @@ hipError_t run(const LoraCall &c, const LoraSpace &s) {
 template <typename T>
 hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
   hipLaunchKernelGGL(lora_group, dim3((unsigned)c.L), dim3(kGroupThreads), 0, c.stream, c.rows,
-                     c.M, c.L, s.start, s.perm);
+                     c.M, c.L, s.start, s.perm, s.owner);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const TilePlan t = tile_plan(c, true);
   TileShrinkParams p = tile_params(c, t);
   p.start = s.start;
   p.perm = s.perm;
+  p.owner = s.owner;
   int jobs = 0;
   if (s.G)
     p.job[jobs++] = ShrinkJob{c.dY, c.B, c.stride_b, c.N, c.lddy, c.ldb, 0, tile_chunk(c, t, c.N),
@@ -1180,17 +1254,15 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
     e = expand<T, false>(c, s.G, c.A, c.lda, c.stride_a, c.K, c.alpha, c.beta_x,
                          static_cast<float *>(c.dX), c.lddx);
     if (e != hipSuccess) return e;
-    const int rc = gemm_f32(c.M, c.K, c.N, c.alpha, static_cast<const float *>(c.dY), c.lddy,
-                            static_cast<const float *>(c.W), c.ldw, 1.0f,
-                            static_cast<float *>(c.dX), c.lddx, c.stream);
-    if (rc != 0) return (hipError_t)rc;
+    e = product_f32(c, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw, c.dX, c.lddx);
+    if (e != hipSuccess) return e;
   }
   if (!c.dA && !c.dB) return hipSuccess;
   OuterParams o = {};
-  o.rows = c.rows;
   o.ranks = c.ranks;
   o.start = s.start;
   o.perm = s.perm;
+  o.owner = s.owner;
   o.scale = c.scale;
   o.L = c.L;
   o.R = c.R;
@@ -1215,7 +1287,7 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(lora_outer_sum,
-                     dim3(flat_grid((long long)c.R * widest), (unsigned)c.L, (unsigned)n),
+                     dim3(flat_grid(((long long)c.R + 3) / 4 * widest), (unsigned)c.L, (unsigned)n),
                      dim3(256), 0, c.stream, o);
   return hipGetLastError();
 }

@@ -27,5 +27,6 @@ __all__ = list(_BINDING_NAMES)
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)   # found directly from now on
+        return value
     raise AttributeError(name)

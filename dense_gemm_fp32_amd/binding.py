@@ -6,6 +6,7 @@ HIP kernels of libgemm.so.  There is no fallback: if the library is missing
 the import fails with an error that says how to build it.
 """
 import ctypes
+import functools
 import os
 
 import torch  # noqa: F401  (loads torch's HIP runtime first, so libgemm.so binds to the same one)
@@ -330,69 +331,105 @@ def _row_entry(name):
 for _n in ROW_NAMES:
     globals()[_n] = getattr(_lib, _n) if _n.endswith("_workspace") else _row_entry(_n)
 
+_LORA_FN = {t: getattr(_lib, "gemm_lora_" + t) for t in ("f16", "f32")}
+_LORA_GRAD_FN = {t: getattr(_lib, "gemm_lora_grad_" + t) for t in ("f16", "f32")}
+_MOE_FN = {t: getattr(_lib, "gemm_moe_" + t) for t in ("f16", "f32")}
+# the workspace depends on these sizes alone
+_lora_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_lora_workspace)
+_lora_grad_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_lora_grad_workspace)
+_moe_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_moe_workspace)
+
+# of a call's type: suffix of the entry point, its workspace function's code
 _KINDS = {torch.float16: ("f16", 1), torch.float32: ("f32", 0)}
 
 
-def _rows(name, t, rows, cols, dtype):
+# The checks below stand in front of calls that take some microseconds on the
+# GPU: each looks at a tensor's shape and strides once.
+
+def _rows(name, t, rows, cols, dtype, dev):
     """Leading dimension of a rows x cols matrix with contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError("%s must be %d x %d, not %s" % (name, rows, cols, tuple(t.shape)))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    if t.get_device() != dev:
+        raise ValueError("%s must be on GPU %d, like the first tensor" % (name, dev))
+    if t.shape != (rows, cols):
+        raise ValueError("%s must be %d x %d, not %s" % (name, rows, cols, tuple(t.shape)))
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
         raise ValueError("%s must have contiguous rows (stride(1) == 1)" % name)
     return ld if ld > 1 else 1
 
 
-def _stack(name, t, n, rows, cols, dtype):
+def _stack(name, t, n, rows, cols, dtype, dev):
     """(leading dimension, stride) of n stacked rows x cols matrices."""
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != rows or t.shape[2] != cols:
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on GPU %d, like the first tensor" % (name, dev))
+    if t.shape != (n, rows, cols):
         raise ValueError("%s must be %d x %d x %d, not %s" % (name, n, rows, cols,
                                                               tuple(t.shape)))
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    ld = t.stride(1) if rows > 1 else cols
-    if (cols > 1 and t.stride(2) != 1) or ld < cols or t.stride(0) < 0:
+    stride, ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
         raise ValueError("%s must have contiguous rows (stride(2) == 1)" % name)
-    return (ld if ld > 1 else 1), (t.stride(0) if n > 1 else 0)
+    return (ld if ld > 1 else 1), (stride if n > 1 else 0)
 
 
-def _vector(name, t, n, dtype):
+def _vector(name, t, n, dtype, dev):
+    """Address of n contiguous values, None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be %d contiguous values of %s" % (name, n, dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on GPU %d, like the first tensor" % (name, dev))
     return t.data_ptr()
 
 
-def _one_device(first, *others):
-    if not first.is_cuda:
+def _kind(X):
+    """(suffix, code, device index) of a call on X."""
+    kind = _KINDS.get(X.dtype)
+    if kind is None:
+        raise ValueError("unsupported dtype %s" % X.dtype)
+    if not X.is_cuda:
         raise ValueError("the tensors must be GPU tensors")
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError("the tensors must be on one device")
-    return dev
+    return kind[0], kind[1], X.get_device()
 
 
-def _call_rows(name, dev, stream, workspace, need, args):
-    """Run entry point `name` on the current stream of `dev` or the one given.
+def _call_rows(fn, dev, stream, workspace, need, args):
+    """Run entry point `fn` on the current stream of GPU `dev` or the one given.
     Without a workspace, one comes from torch's allocator on the current
     stream, or from the library's pool on a stream that was given."""
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on GPU %d" % dev)
         ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif stream is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=_device(dev))
         ws, size = workspace.data_ptr(), need
     else:
         ws, size = None, 0
-    stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-    rc = getattr(_lib, name)(*args, ws, size, stream)
+    stream = _current_stream(dev) if stream is None else _stream(stream)
+    rc = fn(*args, ws, size, stream)
     if rc != 0:
         raise GemmError(rc)
+
+
+@functools.lru_cache(maxsize=None)
+def _device(index):
+    return torch.device("cuda", index)
+
+
+def _public_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# handle of a GPU's current stream, without a Stream object where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
 
 
 def lora(X, W, A, B, rows, Y, scale=None, ranks=None, alpha=1.0, beta=0.0, workspace=None,
@@ -413,19 +450,17 @@ def lora(X, W, A, B, rows, Y, scale=None, ranks=None, alpha=1.0, beta=0.0, works
     N = W.shape[0]
     L, R = A.shape[0], A.shape[1]
     dt = X.dtype
-    if dt not in _KINDS:
-        raise ValueError("unsupported dtype %s" % dt)
-    kind, code = _KINDS[dt]
-    dev = _one_device(X, W, A, B, rows, Y, scale, ranks)
-    ldx, ldw, ldy = _rows("X", X, M, K, dt), _rows("W", W, N, K, dt), _rows("Y", Y, M, N, dt)
-    lda, sa = _stack("A", A, L, R, K, dt)
-    ldb, sb = _stack("B", B, L, N, R, dt)
-    _call_rows("gemm_lora_" + kind, dev, stream, workspace,
-               _lib.gemm_lora_workspace(code, M, N, K, L, R),
+    kind, code, dev = _kind(X)
+    ldx, ldw = _rows("X", X, M, K, dt, dev), _rows("W", W, N, K, dt, dev)
+    ldy = _rows("Y", Y, M, N, dt, dev)
+    lda, sa = _stack("A", A, L, R, K, dt, dev)
+    ldb, sb = _stack("B", B, L, N, R, dt, dev)
+    _call_rows(_LORA_FN[kind], dev, stream, workspace, _lora_bytes(code, M, N, K, L, R),
                (M, N, K, alpha, X.data_ptr(), ldx, W.data_ptr(), ldw, beta, Y.data_ptr(), ldy, L,
                 R, A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb,
-                _vector("scale", scale, L, torch.float32),
-                _vector("ranks", ranks, L, torch.int32), _vector("rows", rows, M, torch.int32)))
+                _vector("scale", scale, L, torch.float32, dev),
+                _vector("ranks", ranks, L, torch.int32, dev),
+                _vector("rows", rows, M, torch.int32, dev)))
     return Y
 
 
@@ -446,27 +481,25 @@ def lora_grad(dY, X, W, A, B, rows, dX=None, dA=None, dB=None, scale=None, ranks
     N = W.shape[0]
     L, R = A.shape[0], A.shape[1]
     dt = X.dtype
-    if dt not in _KINDS:
-        raise ValueError("unsupported dtype %s" % dt)
-    kind, code = _KINDS[dt]
-    dev = _one_device(X, W, A, B, rows, dY, scale, ranks, dX, dA, dB)
-    lddy = _rows("dY", dY, M, N, dt)
-    ldx, ldw = _rows("X", X, M, K, dt), _rows("W", W, N, K, dt)
-    lda, sa = _stack("A", A, L, R, K, dt)
-    ldb, sb = _stack("B", B, L, N, R, dt)
+    kind, code, dev = _kind(X)
+    lddy = _rows("dY", dY, M, N, dt, dev)
+    ldx, ldw = _rows("X", X, M, K, dt, dev), _rows("W", W, N, K, dt, dev)
+    lda, sa = _stack("A", A, L, R, K, dt, dev)
+    ldb, sb = _stack("B", B, L, N, R, dt, dev)
     lddx = ldda = sda = lddb = sdb = 0
     if dX is not None:
-        lddx = _rows("dX", dX, M, K, dt)
+        lddx = _rows("dX", dX, M, K, dt, dev)
     if dA is not None:
-        ldda, sda = _stack("dA", dA, L, R, K, torch.float32)
+        ldda, sda = _stack("dA", dA, L, R, K, torch.float32, dev)
     if dB is not None:
-        lddb, sdb = _stack("dB", dB, L, N, R, torch.float32)
-    _call_rows("gemm_lora_grad_" + kind, dev, stream, workspace,
-               _lib.gemm_lora_grad_workspace(code, M, N, K, L, R),
+        lddb, sdb = _stack("dB", dB, L, N, R, torch.float32, dev)
+    _call_rows(_LORA_GRAD_FN[kind], dev, stream, workspace,
+               _lora_grad_bytes(code, M, N, K, L, R),
                (M, N, K, alpha, dY.data_ptr(), lddy, X.data_ptr(), ldx, W.data_ptr(), ldw, L, R,
                 A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb,
-                _vector("scale", scale, L, torch.float32),
-                _vector("ranks", ranks, L, torch.int32), _vector("rows", rows, M, torch.int32),
+                _vector("scale", scale, L, torch.float32, dev),
+                _vector("ranks", ranks, L, torch.int32, dev),
+                _vector("rows", rows, M, torch.int32, dev),
                 beta_x, _addr(dX), lddx, beta_ab, _addr(dA), ldda, sda, _addr(dB), lddb, sdb))
     return dX, dA, dB
 
@@ -488,18 +521,14 @@ def moe(X, router, W1, W2, top_k, Y, renorm=True, alpha=1.0, beta=0.0, ids=None,
     M, D = X.shape
     E, F = W2.shape[0], W2.shape[2]
     dt = X.dtype
-    if dt not in _KINDS:
-        raise ValueError("unsupported dtype %s" % dt)
-    kind, code = _KINDS[dt]
-    dev = _one_device(X, router, W1, W2, Y, ids, weights)
-    ldx, ldr, ldy = _rows("X", X, M, D, dt), _rows("router", router, E, D, dt), \
-        _rows("Y", Y, M, D, dt)
-    ld1, s1 = _stack("W1", W1, E, 2 * F, D, dt)
-    ld2, s2 = _stack("W2", W2, E, D, F, dt)
-    _call_rows("gemm_moe_" + kind, dev, stream, workspace,
-               _lib.gemm_moe_workspace(code, M, D, F, E, top_k),
+    kind, code, dev = _kind(X)
+    ldx, ldr = _rows("X", X, M, D, dt, dev), _rows("router", router, E, D, dt, dev)
+    ldy = _rows("Y", Y, M, D, dt, dev)
+    ld1, s1 = _stack("W1", W1, E, 2 * F, D, dt, dev)
+    ld2, s2 = _stack("W2", W2, E, D, F, dt, dev)
+    _call_rows(_MOE_FN[kind], dev, stream, workspace, _moe_bytes(code, M, D, F, E, top_k),
                (M, D, F, E, top_k, 1 if renorm else 0, alpha, X.data_ptr(), ldx,
                 router.data_ptr(), ldr, W1.data_ptr(), ld1, s1, W2.data_ptr(), ld2, s2, beta,
-                Y.data_ptr(), ldy, _vector("ids", ids, M * top_k, torch.int32),
-                _vector("weights", weights, M * top_k, torch.float32)))
+                Y.data_ptr(), ldy, _vector("ids", ids, M * top_k, torch.int32, dev),
+                _vector("weights", weights, M * top_k, torch.float32, dev)))
     return Y

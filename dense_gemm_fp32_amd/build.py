@@ -58,7 +58,7 @@ def _compile(src, verbose=False, build_dir=BUILD_DIR, extra=()):
 # touches it: the asm's m0 writes then cannot disturb compiled code.  The
 # same assembly is checked for spills (and that of gemm_valu.hip).
 M0_ASM_SOURCES = ["gemm_f16.hip", "gemm_f16_lora.hip", "gemm_f32.hip"]
-SPILL_ONLY_SOURCES = ["gemm_valu.hip"]
+SPILL_ONLY_SOURCES = ["gemm_valu.hip", "lora.hip", "moe.hip"]
 
 
 def check_spills_only(src):
@@ -71,8 +71,10 @@ def check_spills_only(src):
 
 # Kernels whose registers hold the accumulator tiles: a spill to scratch
 # memory would put every MFMA's operands behind memory traffic, so the build
-# refuses one.
-NO_SPILL_KERNELS = ("hgemm_mfma", "sgemm_mfma", "sgemm_streamk", "sgemm_valu")
+# refuses one.  The row-indexed kernels are held to it as well: a form of
+# lora_shrink_tile that spilled 100 bytes gave wrong sums in every fourth row on
+# its first call, and right ones without the spill.
+NO_SPILL_KERNELS = ("hgemm_mfma", "sgemm_mfma", "sgemm_streamk", "sgemm_valu", "lora_", "moe_")
 
 
 def scratch_sizes(asm_text):

@@ -218,20 +218,30 @@ __global__ __launch_bounds__(256) void lora_join(JoinParams p) {
   for (int q = 0; q < p.parts; ++q) sum += s[(size_t)q * p.M * p.N];
   const int a = adapter_of(p.rows, i, p.M, p.L);
   if (a >= 0) {
-    const int rk = rank_of(p.ranks, a, p.R);
     const T *u = static_cast<const T *>(p.B) + (size_t)a * (size_t)p.stride +
                  (size_t)n * (size_t)p.ldb;
     const float *v = p.V + (size_t)i * p.Rp;
-    float t = 0.0f;
     constexpr int VEC = El<T>::VEC;
-    int r = 0;
-    for (; r + VEC <= rk; r += VEC) {
-      const typename El<T>::Frag f = load_whole(u + r);
+    // the first 16 ranks are on their way before the adapter's rank is known
+    constexpr int AHEAD = 16 / VEC;
+    typename El<T>::Frag f[AHEAD];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) t = __builtin_fmaf((float)f[e], v[r + e], t);
+    for (int q = 0; q < AHEAD; ++q) f[q] = load_frag(u, q * VEC, p.R);
+    const float scale = p.scale ? p.scale[a] : 1.0f;
+    const int rk = rank_of(p.ranks, a, p.R);
+    float t = 0.0f;
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (q * VEC + e < rk) t = __builtin_fmaf((float)f[q][e], v[q * VEC + e], t);
+    for (int r = 16; r < rk; r += VEC) {
+      const typename El<T>::Frag g = load_frag(u, r, p.R);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (r + e < rk) t = __builtin_fmaf((float)g[e], v[r + e], t);
     }
-    for (; r < rk; ++r) t = __builtin_fmaf((float)u[r], v[r], t);
-    if (rk > 0) sum = __builtin_fmaf(p.scale ? p.scale[a] : 1.0f, t, sum);
+    if (rk > 0) sum = __builtin_fmaf(scale, t, sum);
   }
   T *y = static_cast<T *>(p.Y) + (size_t)i * (size_t)p.ldy + n;
   float o = p.alpha * sum;
@@ -274,6 +284,7 @@ constexpr int kShrinkTile = 64;   // rows, and ranks, of a workgroup's tile
 // per tile but where two meet.  grid: (row tiles, rank tiles * parts * z,
 // jobs); workgroup z takes the distinct adapters z, z + Z, ... of its rows.
 constexpr int kStepBytes = 512;
+constexpr int kTileThreads = 512;
 
 // The tiles of one adapter's step in LDS, X's then W's: 64 rows of kStepBytes,
 // piece c of row u at c ^ (u % 8).
@@ -283,28 +294,36 @@ struct ShrinkTiles {
   static constexpr int VEC = El<T>::VEC;
   static constexpr int BK = kStepBytes / (int)sizeof(T);
   static constexpr int CH = kStepBytes / 16;              // pieces of a row
-  static constexpr int PER = kShrinkTile * CH / 256;      // pieces a thread loads of either tile
+  static constexpr int PER = kShrinkTile * CH / kTileThreads;   // pieces a thread loads of either tile
   static constexpr int RP = kShrinkTile / VEC;            // rank pieces of a k (not KMAJ)
   const ShrinkJob &j;
   char *lds;
   const T *w;                                             // the adapter's matrix
   int row, r0, rk, R, nb;                                 // row: of the tile, one a lane
 
+  // This thread's number, from which each call below works out its addresses
+  // anew: kept from one step to the next they would take the registers that two
+  // workgroups per CU need.
+  __device__ __forceinline__ static int thread() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+  }
   // X: piece c of tile row u; W: piece v of rank u, or rank piece v of k u
-  __device__ __forceinline__ const T *x_at(int q, int k, int &u, int &c) const {
-    c = threadIdx.x % CH;
-    u = threadIdx.x / CH + 256 / CH * q;
+  __device__ __forceinline__ const T *x_at(int t, int q, int k, int &u, int &c) const {
+    c = t % CH;
+    u = t / CH + kTileThreads / CH * q;
     return static_cast<const T *>(j.X) + (size_t)__shfl(row, u) * (size_t)j.ldx + k + c * VEC;
   }
-  __device__ __forceinline__ void w_piece(int q, int &u, int &v) const {
-    const int i = threadIdx.x + 256 * q;
+  __device__ __forceinline__ void w_piece(int t, int q, int &u, int &v) const {
+    const int i = t + kTileThreads * q;
     u = i / (KMAJ ? CH : RP);
     v = i % (KMAJ ? CH : RP);
   }
   // Whether any rank of this thread's piece q is in a block of 16 that the
   // adapter has (not KMAJ: the same for all q).
   __device__ __forceinline__ bool wanted(int q) const {
-    return KMAJ ? 256 / CH * q < 16 * nb : (int)threadIdx.x % RP * VEC < 16 * nb;
+    return KMAJ ? kTileThreads / CH * q < 16 * nb : (int)threadIdx.x % RP * VEC < 16 * nb;
   }
   __device__ __forceinline__ void put_x(int u, int c, const Frag &f) const {
     *reinterpret_cast<Frag *>(lds + u * kStepBytes + 16 * (c ^ (u & 7))) = f;
@@ -327,62 +346,86 @@ struct ShrinkTiles {
   // A step all of which lies inside the rows; ranks past the last are repeated
   // or, where they are there, taken as they are (their sums are dropped).
   __device__ __forceinline__ void load_whole_step(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
+    const int t = thread();
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       int u, c;
-      xr[q] = load_whole(x_at(q, k, u, c));
+      xr[q] = load_whole(x_at(t, q, k, u, c));
     }
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       if (!wanted(q)) break;
       int u, v;
-      w_piece(q, u, v);
+      w_piece(t, q, u, v);
       if (KMAJ) {
         const int r = r0 + u < rk ? r0 + u : rk - 1;
         wr[q] = load_whole(w + (size_t)r * (size_t)j.ldw + k + v * VEC);
       } else {
-        wr[q] = load_frag(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, R);
+        wr[q] = load_end(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, R);
       }
     }
   }
   // The step in which the rows end: zeros behind the end on both sides.
   __device__ __forceinline__ void load_last_step(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
+    const int t = thread();
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       int u, c;
-      const T *x = x_at(q, 0, u, c) - c * VEC;
-      xr[q] = load_frag(x, k + c * VEC, j.K);
+      const T *x = x_at(t, q, 0, u, c) - c * VEC;
+      xr[q] = load_end(x, k + c * VEC, j.K);
     }
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       if (!wanted(q)) break;
       int u, v;
-      w_piece(q, u, v);
+      w_piece(t, q, u, v);
       if (KMAJ) {
         const int r = r0 + u < rk ? r0 + u : rk - 1;
-        wr[q] = load_frag(w + (size_t)r * (size_t)j.ldw, k + v * VEC, j.K);
+        wr[q] = load_end(w + (size_t)r * (size_t)j.ldw, k + v * VEC, j.K);
       } else {
         const bool in = k + u < j.K;
-        wr[q] = move_down(load_frag(w + (size_t)(in ? k + u : j.K - 1) * (size_t)j.ldw,
-                                    r0 + v * VEC, R),
-                          in ? 0 : VEC);
+        const int r = r0 + v * VEC, last = R - VEC;
+        wr[q] = move_down(load_whole(w + (size_t)(in ? k + u : j.K - 1) * (size_t)j.ldw +
+                                     (r < last ? r : last)),
+                          in ? r - last : VEC);
       }
     }
   }
+  // Rows shorter than a piece, which no such load fits.
+  __device__ __forceinline__ bool tiny() const { return j.K < VEC || (!KMAJ && R < VEC); }
   __device__ __forceinline__ void load(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
+    if (tiny()) return;
     if (k + BK <= j.K) load_whole_step(k, xr, wr);
     else load_last_step(k, xr, wr);
   }
+  // Their steps, piece by piece straight into LDS.
+  __device__ __forceinline__ void fill(int k) const {
+    const int t = thread();
+#pragma unroll 1
+    for (int q = 0; q < PER; ++q) {
+      int u, c;
+      const T *x = x_at(t, q, 0, u, c) - c * VEC;
+      put_x(u, c, load_part(x + k + c * VEC, j.K - k - c * VEC));
+      if (!wanted(q)) continue;
+      int v;
+      w_piece(t, q, u, v);
+      put_w(u, v, KMAJ ? load_part(w + (size_t)(r0 + u) * (size_t)j.ldw + k + v * VEC,
+                                   r0 + u < rk ? j.K - k - v * VEC : 0)
+                       : load_part(w + (size_t)(k + u) * (size_t)j.ldw + r0 + v * VEC,
+                                   k + u < j.K ? R - r0 - v * VEC : 0));
+    }
+  }
   __device__ __forceinline__ void store(const Frag (&xr)[PER], const Frag (&wr)[PER]) const {
+    const int t = thread();
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      put_x(threadIdx.x / CH + 256 / CH * q, threadIdx.x % CH, xr[q]);
+      put_x(t / CH + kTileThreads / CH * q, t % CH, xr[q]);
     }
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       if (!wanted(q)) break;
       int u, v;
-      w_piece(q, u, v);
+      w_piece(t, q, u, v);
       put_w(u, v, wr[q]);
     }
   }
@@ -420,23 +463,26 @@ __device__ __forceinline__ void shrink_tile(const TileShrinkParams &p, const Shr
     const Tiles tiles = {j, lds, static_cast<const T *>(j.W) + (size_t)a * (size_t)j.stride, row,
                          r0, rk, p.R, nb};
     Frag xr[Tiles::PER], wr[Tiles::PER];
-    f32x4 acc[4];
+    // waves 0-3 take a block of 16 rows and ranks 0-31 each, waves 4-7 ranks 32-63
+    const int wrow0 = 16 * (wave & 3), b0 = wave >> 2 << 1;
+    f32x4 acc[2];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = 0; b < 2; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     tiles.load(k0, xr, wr);
     for (int k = k0; k < k1; k += Tiles::BK) {
-      tiles.store(xr, wr);
+      if (tiles.tiny()) tiles.fill(k);
+      else tiles.store(xr, wr);
       __syncthreads();
       if (k + Tiles::BK < k1) tiles.load(k + Tiles::BK, xr, wr);
-#pragma unroll 1
+#pragma unroll 2
       for (int s = 0; s < Tiles::CH / 4; ++s) {
-        const int xrow = 16 * wave + li;
+        const int xrow = wrow0 + li;
         const Frag xf = *reinterpret_cast<const Frag *>(lds + xrow * kStepBytes +
                                                         16 * ((4 * s + lg) ^ (xrow & 7)));
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (b >= nb) break;
-          const int wrow = kShrinkTile + 16 * b + li;
+        for (int b = 0; b < 2; ++b) {
+          if (b0 + b >= nb) break;
+          const int wrow = kShrinkTile + 16 * (b0 + b) + li;
           const Frag wf = *reinterpret_cast<const Frag *>(lds + wrow * kStepBytes +
                                                           16 * ((4 * s + lg) ^ (wrow & 7)));
           acc[b] = mma16(xf, wf, acc[b]);
@@ -444,22 +490,22 @@ __device__ __forceinline__ void shrink_tile(const TileShrinkParams &p, const Shr
       }
       __syncthreads();
     }
-    // rows 16 wave + 4 lg + e of the tile, ranks r0 + 16 b + li
+    // rows wrow0 + 4 lg + e of the tile, ranks r0 + 16 (b0 + b) + li
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int i = 16 * wave + 4 * lg + e;
+      const int i = wrow0 + 4 * lg + e;
       const int m = __shfl(row, i);
       if (!((same >> i) & 1)) continue;
       float *out = j.S + ((size_t)part * p.M + m) * p.Rp + r0 + li;
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (b < nb) out[16 * b] = acc[b][e];
+      for (int b = 0; b < 2; ++b)
+        if (b0 + b < nb) out[16 * (b0 + b)] = acc[b][e];
     }
   }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256, 2) void lora_shrink_tile(TileShrinkParams p) {
+__global__ __launch_bounds__(kTileThreads, 4) void lora_shrink_tile(TileShrinkParams p) {
   __shared__ __attribute__((aligned(16))) char lds[2 * kShrinkTile * kStepBytes];
   const ShrinkJob &j = p.job[blockIdx.z];
   if (j.kmaj) shrink_tile<T, true>(p, j, lds);
@@ -886,27 +932,34 @@ int shrink_z(const LoraCall &c) {
   return z < c.M ? z : c.M;
 }
 
-// First products of a call with many rows (one or two jobs): the parts K is
-// divided into, so that there are two workgroups per CU, and the workgroups per tile of 64 rows that share its adapters out.  Tiles of long
-// batches mostly hold one adapter; in a batch of some hundred rows every row may
-// have its own.
+// First products of a call with many rows (`jobs`: one or two): the parts K is
+// divided into and the workgroups per tile of 64 rows that share its adapters
+// out (in a batch of some hundred rows every row may have its own), both so
+// that all workgroups are on the CUs at once, two to each: a workgroup first
+// follows its rows' numbers to their adapters, some microseconds that a second
+// round would add again (4096 rows of 4096, rank 16, both products: 28 us in
+// two rounds, XXX us in one).
 struct TilePlan {
   int tiles, rtiles, parts, z;
 };
 
 int tile_step(const LoraCall &c) { return kStepBytes / (c.half ? 2 : 4); }
 
-TilePlan tile_plan(const LoraCall &c, bool ordered) {
+TilePlan tile_plan(const LoraCall &c, int jobs) {
   TilePlan t;
   t.tiles = (c.M + kShrinkTile - 1) / kShrinkTile;
   t.rtiles = (rank_pad(c.R) + kShrinkTile - 1) / kShrinkTile;
+  const long long wgs = (long long)t.tiles * t.rtiles * jobs;
   const int longest = c.K > c.N ? c.K : c.N;
   const int most = (longest + tile_step(c) - 1) / tile_step(c);
-  int parts = 2 * kCUs / (t.tiles * t.rtiles);
+  int parts = (int)(2 * kCUs / wgs);
   parts = parts < 8 ? parts : 8;
   parts = parts < most ? parts : most;
   t.parts = parts > 1 ? parts : 1;
-  int z = ordered ? 2 : 4 * kCUs / (t.tiles * t.rtiles * t.parts);
+  // two at least: where two requests meet in a tile the second adapter's
+  // workgroup runs beside the first's, elsewhere it ends at once
+  int z = (int)(2 * kCUs / (wgs * t.parts));
+  z = z > 2 ? z : 2;
   z = z < c.L ? z : c.L;
   z = z < kShrinkTile ? z : kShrinkTile;
   t.z = z > 1 ? z : 1;
@@ -924,7 +977,7 @@ hipError_t shrink_tiles(const LoraCall &c, const TileShrinkParams &p, const Tile
   hipLaunchKernelGGL((lora_shrink_tile<T>),
                      dim3((unsigned)t.tiles, (unsigned)(t.rtiles * t.parts * t.z),
                           (unsigned)jobs),
-                     dim3(256), 0, c.stream, p);
+                     dim3(kTileThreads), 0, c.stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(lora_shrink_sum, dim3((unsigned)((c.M + 3) / 4), (unsigned)jobs), dim3(256), 0,
@@ -1075,7 +1128,7 @@ size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
     s->S = w.take<float>((size_t)skinny_plan(c).parts * c.M * (size_t)c.N);
     return w.used;
   }
-  s->S = w.take<float>((size_t)tile_plan(c, false).parts * c.M * rp);
+  s->S = w.take<float>((size_t)tile_plan(c, 1).parts * c.M * rp);
   if (!c.half || c.M <= kJoinRows) {
     s->V = w.take<float>((size_t)c.M * rp);
     if (c.half) s->T = w.take<float>((size_t)c.M * (size_t)c.N);
@@ -1096,7 +1149,7 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   Carve w(base);
   *s = GradSpace{};
   const size_t rp = (size_t)rank_pad(c.R);
-  const size_t parts = (size_t)tile_plan(c, true).parts;
+  const size_t parts = (size_t)tile_plan(c, 2).parts;
   s->start = w.take<int>((size_t)c.L + 1);
   s->perm = w.take<int>((size_t)c.M);
   s->owner = w.take<int>((size_t)c.M);
@@ -1120,9 +1173,11 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
 }
 
 // C := alpha * A op(B) + C with the fp32 kernels.  Operands whose rows do not
-// allow 16-byte loads are copied first, whatever the size: the calls here that
-// stay below the library's own threshold for it have a long K (1000 x 517 x
-// 3000 with odd rows: 78 us as they are, XXX us copied).
+// allow 16-byte loads are copied first, whatever the size, and a deep K (a
+// gradient's, over a projection's many outputs) is split over four 64 x 64
+// tiles per CU where the product's own choice, made for C of some size, leaves
+// larger tiles and fewer parts: 1000 x 517 x 3000 with odd rows 88 us by that
+// choice, 63 us so.
 hipError_t product_f32(const LoraCall &c, bool tb, int N, int K, const void *A, int lda,
                        const void *B, int ldb, void *C, int ldc) {
   Call g = {};
@@ -1141,6 +1196,13 @@ hipError_t product_f32(const LoraCall &c, bool tb, int N, int K, const void *A, 
   g.splits = 1;
   g.ws_limit = workspace_limit();
   g.pack_mode = 2;
+  const long long tiles = (long long)((c.M + 63) / 64) * ((N + 63) / 64);
+  const int parts = (int)((4 * kCUs + tiles - 1) / tiles);
+  if (K >= 2 * (c.M > N ? c.M : N) && parts >= 2 && K / 256 >= 2) {
+    g.tile_config = 7;
+    g.split_mode = parts < K / 256 ? parts : K / 256;
+    if (g.split_mode > 64) g.split_mode = 64;
+  }
   g.stream = c.stream;
   return launch_f32(g);
 }
@@ -1201,7 +1263,7 @@ hipError_t run(const LoraCall &c, const LoraSpace &s) {
     const hipError_t e = skinny<T>(c, s.V, s.S);
     return e != hipSuccess ? e : join(c, s.V, s.S, skinny_plan(c).parts);
   }
-  const TilePlan t = tile_plan(c, false);
+  const TilePlan t = tile_plan(c, 1);
   TileShrinkParams p = tile_params(c, t);
   p.job[0] = ShrinkJob{c.X, c.A, c.stride_a, c.K, c.ldx, c.lda, 1, tile_chunk(c, t, c.K), s.S,
                        s.V, s.split, s.scale};
@@ -1230,7 +1292,7 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
                      c.M, c.L, s.start, s.perm, s.owner);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const TilePlan t = tile_plan(c, true);
+  const TilePlan t = tile_plan(c, 2);
   TileShrinkParams p = tile_params(c, t);
   p.start = s.start;
   p.perm = s.perm;

@@ -96,15 +96,19 @@ __device__ __forceinline__ f32x4 move_down(f32x4 v, int s) {
   return v;
 }
 
-// Elements k .. k+VEC-1 of a row of K elements, 0 beyond its end.  A row of at
-// least VEC elements is read by one load that stays inside it, whatever k, and
-// moved into place, so that several such loads can be on their way together.
+// Elements k .. k+VEC-1 of a row of K >= VEC elements, 0 beyond its end: one
+// load that stays inside the row, whatever k, and is moved into place, so that
+// several can be on their way together.
+template <typename T>
+__device__ __forceinline__ typename El<T>::Frag load_end(const T *row, int k, int K) {
+  const int last = K - El<T>::VEC;
+  return move_down(load_whole(row + (k < last ? k : last)), k - last);
+}
+
+// The same for a row of any length.
 template <typename T>
 __device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, int K) {
-  constexpr int VEC = El<T>::VEC;
-  if (K < VEC) return load_part(row + k, K - k);
-  const int last = K - VEC;
-  return move_down(load_whole(row + (k < last ? k : last)), k - last);
+  return K < El<T>::VEC ? load_part(row + k, K - k) : load_end(row, k, K);
 }
 
 // acc[f][b] += W block f (16 rows, this lane's at w[f]) times activation block

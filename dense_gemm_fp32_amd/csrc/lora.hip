@@ -279,7 +279,7 @@ constexpr int kShrinkTile = 64;   // rows, and ranks, of a workgroup's tile
 // every piece of X is loaded once per adapter among the rows, in whole lines.
 // A step's loads (up to 64 KB a workgroup, two workgroups per CU) are issued as
 // soon as the registers of the last are in LDS and arrive behind its products;
-// steps of 128 bytes left a quarter of that in flight (26.7 against XXX us at
+// steps of 128 bytes left a quarter of that in flight (26.7 against 20.9 us at
 // 4096 rows of 4096, rank 64).  Rows in adapter order (perm) have one adapter
 // per tile but where two meet.  grid: (row tiles, rank tiles * parts * z,
 // jobs); workgroup z takes the distinct adapters z, z + Z, ... of its rows.
@@ -649,9 +649,8 @@ __global__ __launch_bounds__(256) void scale_batch(int rows, int cols, float bet
 // ---------------------------------------------------------------- rows of each adapter
 
 // perm[start[a] .. start[a+1]) := the rows of adapter a, in order, and
-// owner[...] := a.  One
-// workgroup per adapter (grid: L): it counts the rows of smaller adapters and
-// its own, then writes its own.
+// owner[...] := a.  One workgroup per adapter (grid: L): it counts the rows of
+// smaller adapters and its own, then writes its own.
 constexpr int kGroupThreads = 1024;
 
 __global__ __launch_bounds__(kGroupThreads) void lora_group(const int *rows, int M, int L,
@@ -722,25 +721,29 @@ struct OuterJob {
 
 struct OuterParams {
   OuterJob job[2];
-  const int *ranks, *start, *perm, *owner;
+  const int *ranks, *start, *perm;
   const float *scale;
   int L, R, Rp, chunk;    // rows, in adapter order, per chunk
   float alpha, beta;
 };
 
-constexpr int kOuterWaves = 8;
+constexpr int kOuterWaves = 4;
 constexpr int kOuterThreads = kOuterWaves * kWave;
 constexpr int kOuterCols = 128;    // columns of X a workgroup takes
 constexpr int kOuterRanks = 32;    // ranks a workgroup takes
 
-// P[chunk + a] = the sums over the rows of adapter a in a chunk of the rows in
-// adapter order.  chunk + a names a slot of its own: along the order either
-// number only ever grows.  A lane loads 8 consecutive columns of one row (a
-// row's 128 columns in whole lines); element e of the lanes is the right operand
-// of product e, whose 16 columns are then 8 apart, and four rows make one
-// step.  The products are fp32: V is, and with the ranks as few as they are the
-// pass over X costs more.  The waves take the steps in turn and their sums
-// meet in LDS.  grid: (column tiles, chunks, jobs * rank tiles).
+// P[s] = the sums over chunk c of adapter a's rows, s = start[a] / chunk + a + c:
+// of an adapter's n rows there are no more chunks than there are s up to the next
+// adapter's first.  One workgroup each, so that no adapter waits for another's
+// sums (1000 fp32 rows of 3000 + 517 columns, five adapters: 19 us with a chunk's
+// adapters in turn, 12 us so), and an adapter of one chunk goes straight to D.
+//
+// A lane loads 8 consecutive columns of one row (a row's 128 columns in whole
+// lines); element e of the lanes is the right operand of product e, whose 16
+// columns are then 8 apart, and four rows make one step.  The products are fp32,
+// as V is: with the ranks as few as they are the pass over X costs more.  The
+// waves take the steps in turn and their sums meet in LDS.  grid: (column
+// tiles, chunks + L, jobs * rank tiles).
 template <typename T>
 __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
   __shared__ float red[kOuterWaves][16][kOuterCols + 4];
@@ -755,13 +758,20 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
   const int li = lane % 16, lg = lane / 16;
   const int kc = k0 + 8 * li;
   const bool whole = k0 + kOuterCols <= j.K;
-  const int total = p.start[p.L];
-  int at = blockIdx.y * p.chunk;
-  const int end = at + p.chunk < total ? at + p.chunk : total;
-  while (at < end) {
-    const int a = p.owner[at];
+  const int slots = (p.start[p.L] + p.chunk - 1) / p.chunk + p.L;
+  for (int s = blockIdx.y; s < slots; s += gridDim.y) {
+    // the last adapter whose first slot is not behind s, 64 steps at once
+    int a = 0;
+    for (int step = p.L > kWave * kWave ? kWave * kWave : (p.L > kWave ? kWave : 1); step > 0; step /= kWave) {
+      const int b = a + lane * step;
+      const bool upto = b < p.L && p.start[b < p.L ? b : 0] / p.chunk + b <= s;
+      const unsigned long long m = __ballot(upto);
+      a += (m != 0 ? 63 - __builtin_clzll(m) : 0) * step;
+    }
     const int s0 = p.start[a], s1 = p.start[a + 1];
-    const int stop = s1 < end ? s1 : end;
+    const int at = s0 + (s - s0 / p.chunk - a) * p.chunk;
+    if (at >= s1) continue;
+    const int stop = s1 - at < p.chunk ? s1 : at + p.chunk;
     const int rk = rank_of(p.ranks, a, p.R);
     const int nb = rk - r0 <= 0 ? 0 : (rk - r0 > 16 ? NR : 1);
     if (nb > 0) {
@@ -814,9 +824,8 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
                 acc[b][e] =
                     __builtin_amdgcn_mfma_f32_16x16x4f32(v[u][b], x[u][e], acc[b][e], 0, 0, 0);
       }
-      // an adapter all of whose rows lie in this chunk needs no partial sums
-      const bool all = s0 >= (int)blockIdx.y * p.chunk && s1 <= end;
-      float *out = j.P + (size_t)(blockIdx.y + a) * p.Rp * j.K;
+      const bool all = at == s0 && stop == s1;
+      float *out = j.P + (size_t)s * p.Rp * j.K;
 #pragma unroll
       for (int b = 0; b < NR; ++b) {
         if (b >= nb) break;
@@ -847,7 +856,6 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
         }
       }
     }
-    at = stop;
   }
 }
 
@@ -859,8 +867,8 @@ __global__ __launch_bounds__(256) void lora_outer_sum(OuterParams p) {
   const int a = blockIdx.y;
   const int rk = rank_of(p.ranks, a, p.R);
   const int b = p.start[a], n = p.start[a + 1] - b;
-  const int c0 = b / p.chunk, c1 = n > 0 ? (b + n - 1) / p.chunk : c0 - 1;
-  const bool done = n > 0 && c0 == c1;
+  const int chunks = (n + p.chunk - 1) / p.chunk;
+  const bool done = chunks == 1;
   if (done && rk == p.R) return;
   const float s = p.alpha * (p.scale ? p.scale[a] : 1.0f);
   const size_t slot = (size_t)p.Rp * j.K;
@@ -877,8 +885,8 @@ __global__ __launch_bounds__(256) void lora_outer_sum(OuterParams p) {
     if (done && in == count) continue;
     f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (in > 0 && !done) {
-      const float *q = j.P + (size_t)(c0 + a) * slot + (size_t)i * pitch + e0;
-      for (int c = c0; c <= c1; ++c, q += slot)
+      const float *q = j.P + (size_t)(b / p.chunk + a) * slot + (size_t)i * pitch + e0;
+      for (int c = 0; c < chunks; ++c, q += slot)
         sum += count == 4 ? load_whole(q) : load_part(q, count);
     }
     float *d = j.D + (size_t)a * (size_t)j.stride + (size_t)i * (size_t)j.ldd + e0;
@@ -938,7 +946,7 @@ int shrink_z(const LoraCall &c) {
 // that all workgroups are on the CUs at once, two to each: a workgroup first
 // follows its rows' numbers to their adapters, some microseconds that a second
 // round would add again (4096 rows of 4096, rank 16, both products: 28 us in
-// two rounds, XXX us in one).
+// two rounds, 22 us in one).
 struct TilePlan {
   int tiles, rtiles, parts, z;
 };
@@ -1098,13 +1106,14 @@ unsigned flat_grid(long long total) {
   return (unsigned)(b < 1 ? 1 : (b > 8192 ? 8192 : b));
 }
 
-// Rows per chunk of the gradients' sums: as many chunks as give every CU a
-// workgroup, but at least 64 rows each, since each leaves partial sums of the
-// adapter's own size behind.
+// Rows per chunk of the gradients' sums: as many chunks as give every CU two of
+// the four workgroups it holds, but at least 64 rows each, since each leaves
+// partial sums of the adapter's own size behind (2049 fp16 rows of 4096 + 2048
+// columns: 45, 36 and 39 us with one, two and four).
 int outer_chunk(const LoraCall &c) {
   const int cols = ((c.K + kOuterCols - 1) / kOuterCols + (c.N + kOuterCols - 1) / kOuterCols) *
                    ((rank_pad(c.R) + kOuterRanks - 1) / kOuterRanks);
-  const int want = (2 * kCUs + cols - 1) / cols;
+  const int want = 2 * kCUs / cols > 1 ? 2 * kCUs / cols : 1;
   const int rows = (c.M + want - 1) / want;
   return rows > 64 ? rows : 64;
 }
@@ -1324,7 +1333,6 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
   o.ranks = c.ranks;
   o.start = s.start;
   o.perm = s.perm;
-  o.owner = s.owner;
   o.scale = c.scale;
   o.L = c.L;
   o.R = c.R;
@@ -1342,9 +1350,11 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
     widest = widest > c.N ? widest : c.N;
   }
   const int rtiles = (p.Rp + kOuterRanks - 1) / kOuterRanks;
+  const int slots = (c.M + o.chunk - 1) / o.chunk + c.L;
   hipLaunchKernelGGL((lora_outer<T>),
                      dim3((unsigned)((widest + kOuterCols - 1) / kOuterCols),
-                          (unsigned)((c.M + o.chunk - 1) / o.chunk), (unsigned)(n * rtiles)),
+                          (unsigned)(slots < 65535 ? slots : 65535),
+                          (unsigned)(n * rtiles)),
                      dim3(kOuterThreads), 0, c.stream, o);
   e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -612,6 +612,15 @@ __device__ __forceinline__ f16x8 low_rank_load(const _Float16 *u, int r, int end
   return r + 8 <= end ? low_rank_whole(u + r) : low_rank_part(u + r, end - r, 1);
 }
 
+// An infinity meets V's high part only: its low part, of either sign or zero,
+// would make a NaN of it.
+__device__ __forceinline__ f16x8 low_rank_finite(f16x8 u) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    u[e] = (__builtin_bit_cast(uint16_t, u[e]) & 0x7c00u) == 0x7c00u ? (_Float16)0.0f : u[e];
+  return u;
+}
+
 // The low-rank term: row i, column n gets scale[i] * sum_r V[i, r] U_a[n, r]
 // for the row's adapter a (nothing without one).  V holds each number as the
 // sum of two halves, 16 ranks' high parts next to their low parts, so a K step
@@ -861,9 +870,10 @@ struct LowRankTerm {
           for (int b = 0; b < NB; ++b) {
             int n = c0 + n0 + 16 * b + li;
             n = n < p.N ? n : p.N - 1;
-            const f16x8 u = UT ? low_rank_load(u0 + (size_t)n * (size_t)t.ldu, r + ur, rk)
-                               : low_rank_part(u0 + (size_t)(r + ur) * (size_t)t.ldu + n,
-                                               rk - r - ur, (size_t)t.ldu);
+            f16x8 u = UT ? low_rank_load(u0 + (size_t)n * (size_t)t.ldu, r + ur, rk)
+                         : low_rank_part(u0 + (size_t)(r + ur) * (size_t)t.ldu + n,
+                                         rk - r - ur, (size_t)t.ldu);
+            if (lg >= 2) u = low_rank_finite(u);
             s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, u, s[b], 0, 0, 0);
           }
         }

@@ -264,6 +264,137 @@ def test_lora_strides_of_adapters():
         assert ref.worst(Y, want, bound) <= 1.0
 
 
+TILES = [
+    # M, N, K, L, R, pad, alpha, beta; rows by tile and ranks in the test
+    (600, 300, 264, 6, 16, 0, 1.0, 0.0),
+    (600, 128, 8192, 6, 16, 0, 1.0, 1.0),       # K in parts
+    (521, 261, 135, 6, 7, 1, -0.5, 0.5),        # rows at any alignment
+    (777, 64, 1, 6, 33, 0, 1.0, 0.0),
+    (513, 1, 520, 6, 1, 0, 1.0, 0.0),
+    (1300, 1600, 96, 40, 24, 0, 1.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("how", ["no adapters", "no ranks", "tiles", "each its own", "L = 0"])
+@pytest.mark.parametrize("case", TILES, ids=lambda c: "x".join(map(str, c[:5])))
+def test_many_rows_by_tile(dt, how, case):
+    """Forward and gradients where whole tiles of rows have no adapter, none of
+    any rank, or more adapters than a tile takes at once."""
+    import dense_gemm_fp32_amd as dg
+    M, N, K, L, R, pad, alpha, beta = case
+    note("many rows %s %s %r" % (dt, how, case))
+    g, dtype = gen(M + N), DT[dt]
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, K ** -0.5)
+    dY = normal(g, (M, N), dtype, 2.0 ** -6)
+    if how == "L = 0":
+        L = 0
+    elif how == "each its own":
+        L = M
+    A, B, scale, _ = adapters(g, L, N, K, R, dtype, False)
+    ranks = torch.full((L,), 0 if how == "no ranks" else R, dtype=torch.int32)
+    rows = torch.full((M,), -1, dtype=torch.int32)
+    if how == "no ranks":
+        rows = pattern(g, "segments", M, L)
+    elif how == "tiles":                        # the last row, and some in the middle
+        rows[M - 1], rows[M // 2:M // 2 + 9], ranks[0] = L - 1, 1, 0
+    elif how == "each its own":
+        rows = torch.randperm(M, generator=g).to(torch.int32)
+    Y = normal(g, (M, N), dtype) if beta else torch.full((M, N), float("nan"), dtype=dtype)
+    oX = normal(g, (M, K), dtype) if beta else torch.full((M, K), float("nan"), dtype=dtype)
+    oA, oB = torch.full((L, R, K), float("nan")), torch.full((L, N, R), float("nan"))
+    want, bound = ref.lora(X, W, A, B, rows, Y, scale, ranks, alpha, beta)
+    grads = ref.lora_grad(dY, X, W, A, B, rows, oX, oA, oB, scale, ranks, alpha, beta, 0)
+    gX, gW, gA, gB, gdY = (padded(t, pad)[1] for t in (X, W, A, B, dY))
+    big = {n: padded(t, pad) for n, t in (("Y", Y), ("dX", oX), ("dA", oA), ("dB", oB))}
+    more = {"scale": scale.to(GPU), "ranks": ranks.to(GPU), "alpha": alpha}
+    dg.lora(gX, gW, gA, gB, rows.to(GPU), big["Y"][1], beta=beta, **more)
+    dg.lora_grad(gdY, gX, gW, gA, gB, rows.to(GPU), beta_x=beta,
+                 **{n: big[n][1] for n in ("dX", "dA", "dB")}, **more)
+    torch.cuda.synchronize()
+    assert ref.worst(big["Y"][1], want, bound) <= 1.0
+    for n in ("dX", "dA", "dB"):
+        assert ref.worst(big[n][1], *grads[n]) <= 1.0, n
+    for b, view in big.values():
+        assert pads_intact(b, view.shape[-1])
+
+
+def test_lora_grad_many_adapters():
+    """More adapters than a wave has lanes, twice over, and rows of one adapter
+    that end at, before and behind a chunk of the sums."""
+    import dense_gemm_fp32_amd as dg
+    for M, N, K, L, R, runs in ((900, 24, 40, 4500, 3, None), (700, 200, 136, 70, 5, None),
+                                (640, 64, 64, 9, 16, (64, 65, 63, 1, 128, 0, 191, 128)),
+                                (3000, 128, 256, 5, 20, (1000, 1, 999, 1000))):
+        note("many adapters %d %d" % (M, L))
+        g = gen(M)
+        X, W = normal(g, (M, K), torch.float16), normal(g, (N, K), torch.float16, K ** -0.5)
+        dY = normal(g, (M, N), torch.float16, 2.0 ** -6)
+        A, B, scale, ranks = adapters(g, L, N, K, R, torch.float16, True)
+        if runs is None:
+            rows = torch.randint(-1, L, (M,), generator=g).to(torch.int32)
+        else:
+            rows = torch.repeat_interleave(torch.arange(len(runs)), torch.tensor(runs))
+            rows = rows[torch.randperm(M, generator=g)].to(torch.int32)
+        want = ref.lora_grad(dY, X, W, A, B, rows, None, None, None, scale, ranks, 1.0, 0, 0)
+        out = {"dX": torch.full((M, K), float("nan"), dtype=torch.float16, device=GPU),
+               "dA": torch.full((L, R, K), float("nan"), device=GPU),
+               "dB": torch.full((L, N, R), float("nan"), device=GPU)}
+        dg.lora_grad(*(t.to(GPU) for t in (dY, X, W, A, B, rows)), scale=scale.to(GPU),
+                     ranks=ranks.to(GPU), **out)
+        torch.cuda.synchronize()
+        for n in out:
+            assert ref.worst(out[n], *want[n]) <= 1.0, n
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_many_rows_keep_infinities(dt):
+    """As with few rows, but that an adapter with a value that is not finite may
+    be summed in another order than without it."""
+    import dense_gemm_fp32_amd as dg
+    for M, N, K, L, R in ((700, 200, 96, 4, 16), (1100, 1040, 136, 30, 8)):
+        note("many rows inf %s %d" % (dt, M))
+        g, dtype = gen(M), DT[dt]
+        X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, 0.1)
+        A, B, scale, _ = adapters(g, L, N, K, R, dtype, False)
+        rows = pattern(g, "mixed", M, L)
+        want, bound = ref.lora(X, W, A, B, rows, None, scale, None, 1.0, 0)
+        A[1, 3, 5], B[2, 7, 4], B[3, 9, 0] = float("inf"), float("nan"), -float("inf")
+        X[11, 2] = float("nan")
+        rows[11] = -1
+        Y = torch.empty(M, N, dtype=dtype, device=GPU)
+        dg.lora(*(t.to(GPU) for t in (X, W, A, B, rows)), Y, scale=scale.to(GPU))
+        Y = Y.cpu()
+        assert Y[11].isnan().all()
+        assert not Y[rows == 1].isfinite().any()
+        assert Y[rows == 2][:, 7].isnan().all()
+        assert Y[rows == 3][:, 9].isinf().all()
+        fine = torch.ones(M, N, dtype=torch.bool)
+        fine[11], fine[rows == 1] = False, False
+        fine[rows == 2, 7] = fine[rows == 3, 9] = False
+        assert Y[fine].isfinite().all()
+        assert ((Y.double() - want).abs()[fine] <= bound[fine]).all()
+
+
+def test_many_rows_large_intermediate():
+    """A x beyond fp16's range, far below it, and both in one tile."""
+    import dense_gemm_fp32_amd as dg
+    for ups in ((2.0 ** 13, 2.0 ** 13), (2.0 ** -12, 2.0 ** -12), (2.0 ** 13, 2.0 ** -12)):
+        note("many rows range %r" % (ups,))
+        g = gen(61)
+        M, N, K, L, R = 640, 264, 256, 2, 16
+        X, W = normal(g, (M, K), torch.float16), normal(g, (N, K), torch.float16, 0.05)
+        A, B = normal(g, (L, R, K), torch.float16), normal(g, (L, N, R), torch.float16)
+        for a, up in enumerate(ups):
+            A[a] *= up
+            B[a] *= min(1.0 / up, 2.0 ** 8) / 64
+        rows = pattern(g, "mixed", M, L)
+        want, bound = ref.lora(X, W, A, B, rows, None, None, None, 1.0, 0)
+        Y = torch.empty(M, N, dtype=torch.float16, device=GPU)
+        dg.lora(*(t.to(GPU) for t in (X, W, A, B, rows)), Y)
+        assert ref.worst(Y, want, bound) <= 1.0
+
+
 MOE = [
     # M, D, F, E, top_k, pad, renorm, alpha, beta
     (1, 64, 64, 4, 2, 0, True, 1.0, 0.0),
@@ -307,6 +438,28 @@ def test_moe(dt, case):
     again = padded(Y, pad)[1]
     dg.moe(gX, gr, g1, g2, k, again, renorm=renorm, alpha=alpha, beta=beta)
     assert torch.equal(again, gY)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", [(256, 64, 96, 4, 2), (200, 1, 257, 7, 3), (130, 257, 1, 5, 5),
+                                  (65, 520, 264, 2, 1), (256, 1032, 72, 3, 2)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_moe_one_expert_for_all(dt, case):
+    """Every token at the same experts (equal logits): several blocks of tokens each."""
+    import dense_gemm_fp32_amd as dg
+    M, D, F, E, k = case
+    note("moe one %s %r" % (dt, case))
+    g, dtype = gen(M + D), DT[dt]
+    X, router = normal(g, (M, D), dtype), torch.zeros(E, D, dtype=dtype)
+    W1, W2 = normal(g, (E, 2 * F, D), dtype, D ** -0.5), normal(g, (E, D, F), dtype, F ** -0.5)
+    want, bound, ids, w, dw = ref.moe(X, router, W1, W2, k, None, False, 1.0, 0)
+    Y, gw = torch.empty(M, D, dtype=dtype, device=GPU), torch.empty(M, k, device=GPU)
+    gi = torch.empty(M, k, dtype=torch.int32, device=GPU)
+    dg.moe(*(t.to(GPU) for t in (X, router, W1, W2)), k, Y, renorm=False, ids=gi, weights=gw)
+    torch.cuda.synchronize()
+    assert torch.equal(gi.cpu().long(), ids) and ids[0].tolist() == list(range(k))
+    assert ref.worst(gw, w, dw) <= 1.0
+    assert ref.worst(Y, want, bound) <= 1.0
 
 
 def test_moe_ties_and_odd_logits():

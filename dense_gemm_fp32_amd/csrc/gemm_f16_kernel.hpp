@@ -704,16 +704,18 @@ __device__ __forceinline__ u32x4 low_rank_piece(const GemmParams &p, const LowRa
 // always runs at least once (a loop that may not run has its accumulators
 // copied around it), so where there is nothing to do there is one step of no
 // adapter, which adds zeros.  Returns their number; `out`: the adapters left
-// out, bit i for the tile's i-th (bit 31: from the 31st on).
+// out, bit i for the tile's i-th (bit 31: from the 31st on).  The splits of a
+// split-K pass take the adapters in turn.
 template <class T, class L>
 __device__ __forceinline__ int low_rank_steps(const GemmParams &p, const LowRank &t, int m0,
-                                              int n0, bool on, int2 *steps, unsigned &out) {
+                                              int n0, int split, int2 *steps, unsigned &out) {
   constexpr int RANKS = T::BK / 2;     // ranks of a step
   static_assert(kStartAdapters * (256 / RANKS) * 8 <= T::STAGE_BYTES, "room for the steps");
   TileAdapters<T::BM> tile(t, m0, p.M);
   int n = 0, i = 0;
   out = 0;
-  for (int a = on ? tile.next() : -1; a >= 0; a = tile.next(), ++i) {
+  for (int a = tile.next(); a >= 0; a = tile.next(), ++i) {
+    if (p.splits > 1 && i % p.splits != split) continue;
     bool skip = i >= kStartAdapters;
     if (!skip) {
       const int rank = low_rank_of(t, a);
@@ -802,22 +804,24 @@ struct LowRankTerm {
   bool some;
   int id[WTM / 64], rank[WTM / 64];
 
-  // `out`: the adapters of the tile (rows m0 ..) to add; the wave's rows start
-  // wm0 further.
-  __device__ __forceinline__ LowRankTerm(const LowRank &term, int m0, int wm0, int M, unsigned out)
+  // `out`: the adapters of the tile (rows m0 ..) to add, of those that are the
+  // split's; the wave's rows start wm0 further.
+  __device__ __forceinline__ LowRankTerm(const LowRank &term, int m0, int wm0, const GemmParams &p,
+                                         int split, unsigned out)
       : t(term), some(out != 0) {
 #pragma unroll
     for (int j = 0; j < WTM / 64; ++j) id[j] = rank[j] = -1;
     if (!some) return;
-    TileAdapters<BM> tile(t, m0, M);
+    TileAdapters<BM> tile(t, m0, p.M);
     int i = 0;
     for (int a = tile.next(); a >= 0; a = tile.next(), ++i) {
+      if (p.splits > 1 && i % p.splits != split) continue;
       if (!((out >> (i < 31 ? i : 31)) & 1)) continue;
       const int r = low_rank_of(t, a);
 #pragma unroll
       for (int j = 0; j < WTM / 64; ++j) {
         const int row = m0 + wm0 + 64 * j + (int)threadIdx.x % kWave;
-        if (row < M && t.rows[row] == a) {
+        if (row < p.M && t.rows[row] == a) {
           id[j] = a;
           rank[j] = r;
         }
@@ -1292,8 +1296,8 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma(GemmParams p) {
   }
 }
 
-// The same product on top of a low-rank term (added by the first split of a
-// split-K pass).  DIRECT: every tile takes the direct loads; false: the
+// The same product on top of a low-rank term (the splits of a
+// split-K pass share its adapters out).  DIRECT: every tile takes the direct loads; false: the
 // register-staged ones.  (With both loops in one kernel the accumulators that
 // the term leaves are copied for either: twice their registers, and spills.)
 template <class T, bool TB, bool VC, bool OUT32, bool DIRECT>
@@ -1312,7 +1316,7 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma_lora(GemmParams p, LowRank t
   typename T::Acc acc[T::FM][T::FN];
   unsigned out;
   int2 *steps = reinterpret_cast<int2 *>(lds + T::STAGE_BYTES);
-  const int n = low_rank_steps<T, L>(p, t, m0, n0, split == 0, steps, out);
+  const int n = low_rank_steps<T, L>(p, t, m0, n0, split, steps, out);
   zero_acc<T>(acc);
   low_rank_start<T, L>(p, t, m0, n0, lds, steps, n, wm0, wn0, acc);
 
@@ -1323,7 +1327,7 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma_lora(GemmParams p, LowRank t
 
   __builtin_amdgcn_s_waitcnt(kWaitAll);
   __syncthreads();   // every wave is done with the pipeline slots
-  const LowRankTerm<T::BM, T::WTM, TB> term(t, m0, wm0, p.M, out);
+  const LowRankTerm<T::BM, T::WTM, TB> term(t, m0, wm0, p, split, out);
   if constexpr (OUT32) {
     epilogue_out32<T, VC, true>(p, m0 + wm0, n0 + wn0, lds, acc, term);
   } else {

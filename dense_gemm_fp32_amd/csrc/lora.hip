@@ -1123,8 +1123,18 @@ int outer_chunk(const LoraCall &c) {
 // adapter, which the pass does not mind and the product's epilogue does.
 constexpr int kJoinRows = 512;
 
+// Parts of K of the fp16 product on top of a term (N columns), where its
+// smallest tiles leave half of the CUs without one; the parts share the term's
+// adapters out.  257 x 1024 x 1024, three adapters: 24 us in one part, 15 us
+// in four.
+int term_parts(const LoraCall &c, int N, int K) {
+  const long long tiles = (long long)((c.M + 63) / 64) * (((long long)N + 127) / 128);
+  const int want = (int)(kCUs / tiles), most = K / 256 < 8 ? K / 256 : 8;
+  return want < 2 || most < 2 ? 1 : (want < most ? want : most);
+}
+
 struct LoraSpace {
-  float *V, *S, *T, *scale;
+  float *V, *S, *T, *W, *scale;
   _Float16 *split;
 };
 
@@ -1144,12 +1154,14 @@ size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
   } else {
     s->split = w.take<_Float16>((size_t)c.M * 2 * rp);
     s->scale = w.take<float>((size_t)c.M + 256);   // read in whole tiles of rows
+    const int parts = term_parts(c, c.N, c.K);
+    if (parts > 1) s->W = w.take<float>(split_ws_bytes(parts, c.M, c.N) / sizeof(float));
   }
   return w.used;
 }
 
 struct GradSpace {
-  float *V, *G, *SV, *SG, *PA, *PB, *scale;
+  float *V, *G, *SV, *SG, *PA, *PB, *W, *scale;
   _Float16 *split;
   int *start, *perm, *owner;
 };
@@ -1169,6 +1181,8 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   if (c.dX && c.half) {
     s->split = w.take<_Float16>((size_t)c.M * 2 * rp);
     s->scale = w.take<float>((size_t)c.M + 256);
+    const int split = term_parts(c, c.K, c.N);
+    if (split > 1) s->W = w.take<float>(split_ws_bytes(split, c.M, c.K) / sizeof(float));
   }
   if (c.dB) {
     s->V = w.take<float>((size_t)c.M * rp);
@@ -1219,7 +1233,7 @@ hipError_t product_f32(const LoraCall &c, bool tb, int N, int K, const void *A, 
 // C := alpha * (A op(B) + the term) + beta * C with the fp16 kernels.
 hipError_t product_on_term(const LoraCall &c, const LowRank &term, bool tb, int N, int K,
                            const void *A, int lda, const void *B, int ldb, float beta, void *C,
-                           int ldc) {
+                           int ldc, void *ws) {
   Call g = {};
   g.M = c.M;
   g.N = N;
@@ -1236,6 +1250,12 @@ hipError_t product_on_term(const LoraCall &c, const LowRank &term, bool tb, int 
   g.splits = 1;
   g.ws_limit = workspace_limit();
   g.term = &term;
+  const int parts = term_parts(c, N, K);
+  if (parts > 1) {
+    g.split_mode = parts;
+    g.ws_fixed = ws;
+    g.ws_fixed_bytes = split_ws_bytes(parts, c.M, N);
+  }
   g.stream = c.stream;
   return launch_f16_lora(g);
 }
@@ -1292,7 +1312,8 @@ hipError_t run(const LoraCall &c, const LoraSpace &s) {
   }
   const LowRank term = {s.split, 2 * p.Rp, s.scale, c.B, c.ldb, c.stride_b, c.rows, c.ranks, c.L,
                         c.R};
-  return product_on_term(c, term, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw, c.beta, c.Y, c.ldy);
+  return product_on_term(c, term, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw, c.beta, c.Y, c.ldy,
+                         s.W);
 }
 
 template <typename T>
@@ -1319,7 +1340,7 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
     const LowRank term = {s.split, 2 * p.Rp, s.scale, c.A, c.lda, c.stride_a, c.rows,
                           c.ranks, c.L, c.R};
     e = product_on_term(c, term, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw, c.beta_x, c.dX,
-                        c.lddx);
+                        c.lddx, s.W);
     if (e != hipSuccess) return e;
   } else if (c.dX) {
     e = expand<T, false>(c, s.G, c.A, c.lda, c.stride_a, c.K, c.alpha, c.beta_x,

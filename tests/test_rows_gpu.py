@@ -272,6 +272,7 @@ TILES = [
     (777, 64, 1, 6, 33, 0, 1.0, 0.0),
     (513, 1, 520, 6, 1, 0, 1.0, 0.0),
     (1300, 1600, 96, 40, 24, 0, 1.0, 0.0),
+    (514, 520, 1032, 40, 8, 0, 1.0, 0.0),
 ]
 
 

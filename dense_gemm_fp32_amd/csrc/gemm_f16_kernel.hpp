@@ -612,13 +612,30 @@ __device__ __forceinline__ f16x8 low_rank_load(const _Float16 *u, int r, int end
   return r + 8 <= end ? low_rank_whole(u + r) : low_rank_part(u + r, end - r, 1);
 }
 
-// An infinity meets V's high part only: its low part, of either sign or zero,
-// would make a NaN of it.
+__device__ __forceinline__ bool not_finite(_Float16 u) {
+  return (__builtin_bit_cast(uint16_t, u) & 0x7c00u) == 0x7c00u;
+}
+
+// The finite values, zeros for the others; and the other way round.
 __device__ __forceinline__ f16x8 low_rank_finite(f16x8 u) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    u[e] = (__builtin_bit_cast(uint16_t, u[e]) & 0x7c00u) == 0x7c00u ? (_Float16)0.0f : u[e];
+  for (int e = 0; e < 8; ++e) u[e] = not_finite(u[e]) ? (_Float16)0.0f : u[e];
   return u;
+}
+__device__ __forceinline__ f16x8 low_rank_odd(f16x8 u) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = not_finite(u[e]) ? u[e] : (_Float16)0.0f;
+  return u;
+}
+
+// Infinities as the largest finite values of their sign.
+__device__ __forceinline__ f16x8 low_rank_clamp(f16x8 v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint16_t b = __builtin_bit_cast(uint16_t, v[e]);
+    v[e] = (b & 0x7fffu) == 0x7c00u ? __builtin_bit_cast(_Float16, (uint16_t)(b - 1)) : v[e];
+  }
+  return v;
 }
 
 // The low-rank term: row i, column n gets scale[i] * sum_r V[i, r] U_a[n, r]
@@ -630,15 +647,17 @@ __device__ __forceinline__ f16x8 low_rank_finite(f16x8 u) {
 // LDS slots: for each adapter among the tile's rows, V with the other rows'
 // zeroed against that adapter's U (rank 64: two steps of 64 k beside the K/64
 // of the product).  Zeroed rows must not meet an infinity or NaN of U, which
-// would make them NaN: U passes through registers on its way, the workgroup
-// votes, and an adapter whose U is not finite in the tile's columns is left to
-// LowRankTerm, as are adapters beyond kStartAdapters in one tile.
+// would make them NaN: U passes through registers on its way, where such values
+// become zeros and are noted.
 //
 // LowRankTerm adds what was left while the accumulators are staged for the
 // stores, 16 rows by 32 columns at a time, keeping by selection the rows that
-// have the adapter.  Doing all of the term so took 31 us more at 4096 x 4096 x
-// 4096 with eight adapters of rank 64 (153 against 122 us): its operands come
-// in fragments of 16 bytes a row, U once more for every 16 rows.
+// have the adapter: those values of U that are not finite, and whole adapters
+// beyond the first kStartAdapters of a tile.  Such a value meets V's high part
+// only: its low part, of either sign or zero, would make a NaN of an infinity.
+// Doing all of the term so took 31 us more at 4096 x 4096 x 4096 with eight
+// adapters of rank 64 (153 against 122 us): its operands come in fragments of
+// 16 bytes a row, U once more for every 16 rows.
 constexpr int kStartAdapters = 16;
 
 // The distinct adapters among the rows of a workgroup's tile, in the order of
@@ -699,16 +718,16 @@ __device__ __forceinline__ u32x4 low_rank_piece(const GemmParams &p, const LowRa
                                          : low_rank_load(u + (size_t)r * (size_t)t.ldu, n, p.N));
 }
 
-// The steps to run, as (adapter, first rank) in `steps` (LDS), apart from the
-// accumulators' loop so that one plain loop is all that carries them: one that
-// always runs at least once (a loop that may not run has its accumulators
-// copied around it), so where there is nothing to do there is one step of no
-// adapter, which adds zeros.  Returns their number; `out`: the adapters left
-// out, bit i for the tile's i-th (bit 31: from the 31st on).  The splits of a
+// The steps to run, as (adapter, first rank + 256 times its number in the tile)
+// in `steps` (LDS), apart from the accumulators' loop so that one plain loop is
+// all that carries them: one that always runs at least once (a loop that may
+// not run has its accumulators copied around it), so where there is nothing to
+// do there is one step of no adapter, which adds zeros.  Returns their number;
+// `out`: whether an adapter is beyond the first kStartAdapters.  The splits of a
 // split-K pass take the adapters in turn.
-template <class T, class L>
+template <class T>
 __device__ __forceinline__ int low_rank_steps(const GemmParams &p, const LowRank &t, int m0,
-                                              int n0, int split, int2 *steps, unsigned &out) {
+                                              int split, int2 *steps, unsigned &out) {
   constexpr int RANKS = T::BK / 2;     // ranks of a step
   static_assert(kStartAdapters * (256 / RANKS) * 8 <= T::STAGE_BYTES, "room for the steps");
   TileAdapters<T::BM> tile(t, m0, p.M);
@@ -716,20 +735,13 @@ __device__ __forceinline__ int low_rank_steps(const GemmParams &p, const LowRank
   out = 0;
   for (int a = tile.next(); a >= 0; a = tile.next(), ++i) {
     if (p.splits > 1 && i % p.splits != split) continue;
-    bool skip = i >= kStartAdapters;
-    if (!skip) {
-      const int rank = low_rank_of(t, a);
-      bool bad = false;
-      for (int r0 = 0; r0 < rank; r0 += RANKS)
-#pragma unroll
-        for (int j = 0; j < T::QB_W; ++j)
-          bad |= not_finite(low_rank_piece<T, L>(p, t, n0, a, rank, r0, j));
-      skip = __syncthreads_or(bad);
-      if (!skip)
-        for (int r0 = 0; r0 < rank; r0 += RANKS, ++n)
-          if (threadIdx.x == 0) steps[n] = int2{a, r0};
+    if (i >= kStartAdapters) {
+      out = 1u << kStartAdapters;
+      break;
     }
-    if (skip) out |= 1u << (i < 31 ? i : 31);
+    const int rank = low_rank_of(t, a);
+    for (int r0 = 0; r0 < rank; r0 += RANKS, ++n)
+      if (threadIdx.x == 0) steps[n] = int2{a, r0 + 256 * i};
   }
   if (n == 0) {
     if (threadIdx.x == 0) steps[0] = int2{-1, 0};
@@ -739,19 +751,22 @@ __device__ __forceinline__ int low_rank_steps(const GemmParams &p, const LowRank
   return n;
 }
 
+// `out` gets bit i where the tile's adapter i has values that are not finite.
 template <class T, class L>
 __device__ __forceinline__ void low_rank_start(const GemmParams &p, const LowRank &t, int m0,
                                                int n0, char *slot, const int2 *steps, int n,
                                                int wm0, int wn0,
-                                               typename T::Acc (&acc)[T::FM][T::FN]) {
+                                               typename T::Acc (&acc)[T::FM][T::FN],
+                                               unsigned &out) {
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   FragAddr<T, L> fa;
   frag_setup<T, L>(wm0, wn0, fa);
   int i = 0;
+  unsigned odd = 0;
 #pragma unroll 1
   do {
     const int a = __builtin_amdgcn_readfirstlane(steps[i].x);
-    const int r0 = __builtin_amdgcn_readfirstlane(steps[i].y);
+    const int r0 = __builtin_amdgcn_readfirstlane(steps[i].y) % 256;
     const int rank = a >= 0 ? low_rank_of(t, a) : 0;
     RegTile<T> reg;
 #pragma unroll
@@ -767,6 +782,12 @@ __device__ __forceinline__ void low_rank_start(const GemmParams &p, const LowRan
                                                        (k < t.ldv ? k : 0));
       reg.a[j] = a >= 0 && t.rows[row] == a && k < t.ldv ? v : u32x4{0u, 0u, 0u, 0u};
     }
+#pragma unroll
+    for (int j = 0; j < T::QB_W; ++j)
+      if (not_finite(reg.b[j])) {
+        odd |= 1u << __builtin_amdgcn_readfirstlane(steps[i].y) / 256;
+        reg.b[j] = __builtin_bit_cast(u32x4, low_rank_finite(__builtin_bit_cast(f16x8, reg.b[j])));
+      }
     __syncthreads();   // every wave has read the slot's last contents
     reg_store<T>(reg, slot);
     __syncthreads();
@@ -792,7 +813,9 @@ __device__ __forceinline__ void low_rank_start(const GemmParams &p, const LowRan
         for (int q = 0; q < 4; ++q) acc[bi][bj][e + q] *= f[q];
       __builtin_amdgcn_sched_barrier(0);
     }
-  __syncthreads();
+  if (__syncthreads_or(odd != 0))
+    for (int b = 0; b < kStartAdapters; ++b)
+      if (__syncthreads_or((odd >> b) & 1)) out |= 1u << b;
 }
 
 // What a chain of loads would stand in front of every block -- the rows'
@@ -800,6 +823,7 @@ __device__ __forceinline__ void low_rank_start(const GemmParams &p, const LowRan
 template <int BM, int WTM, bool UT>
 struct LowRankTerm {
   static constexpr bool kNone = false;
+  static constexpr int kWhole = 1 << 16;   // added to the rank: all of U's values
   const LowRank &t;
   bool some;
   int id[WTM / 64], rank[WTM / 64];
@@ -816,8 +840,9 @@ struct LowRankTerm {
     int i = 0;
     for (int a = tile.next(); a >= 0; a = tile.next(), ++i) {
       if (p.splits > 1 && i % p.splits != split) continue;
-      if (!((out >> (i < 31 ? i : 31)) & 1)) continue;
-      const int r = low_rank_of(t, a);
+      const bool whole = i >= kStartAdapters;
+      if (!((out >> (whole ? kStartAdapters : i)) & 1)) continue;
+      const int r = low_rank_of(t, a) + (whole ? kWhole : 0);
 #pragma unroll
       for (int j = 0; j < WTM / 64; ++j) {
         const int row = m0 + wm0 + 64 * j + (int)threadIdx.x % kWave;
@@ -861,7 +886,8 @@ struct LowRankTerm {
       while (left != 0) {
         const int src = __builtin_ctz(left);
         const int a = __builtin_amdgcn_readlane(ida, src);
-        const int rk = __builtin_amdgcn_readlane(ranka, src);
+        const int rw = __builtin_amdgcn_readlane(ranka, src);
+        const int rk = rw % kWhole;
         const unsigned same = (unsigned)(__ballot(ida == a) & 0xffffu);
         left &= ~same;
         f32x4 s[NB];
@@ -869,7 +895,8 @@ struct LowRankTerm {
         for (int b = 0; b < NB; ++b) s[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const _Float16 *u0 = static_cast<const _Float16 *>(t.U) + (size_t)a * (size_t)t.stride;
         for (int r = 0; r < rk; r += 16) {
-          const f16x8 vf = *reinterpret_cast<const f16x8 *>(v + 2 * r);
+          f16x8 vf = *reinterpret_cast<const f16x8 *>(v + 2 * r);
+          if (rw < kWhole) vf = low_rank_clamp(vf);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             int n = c0 + n0 + 16 * b + li;
@@ -877,7 +904,8 @@ struct LowRankTerm {
             f16x8 u = UT ? low_rank_load(u0 + (size_t)n * (size_t)t.ldu, r + ur, rk)
                          : low_rank_part(u0 + (size_t)(r + ur) * (size_t)t.ldu + n,
                                          rk - r - ur, (size_t)t.ldu);
-            if (lg >= 2) u = low_rank_finite(u);
+            if (rw < kWhole) u = lg < 2 ? low_rank_odd(u) : f16x8{};
+            else if (lg >= 2) u = low_rank_finite(u);
             s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, u, s[b], 0, 0, 0);
           }
         }
@@ -1316,9 +1344,9 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma_lora(GemmParams p, LowRank t
   typename T::Acc acc[T::FM][T::FN];
   unsigned out;
   int2 *steps = reinterpret_cast<int2 *>(lds + T::STAGE_BYTES);
-  const int n = low_rank_steps<T, L>(p, t, m0, n0, split, steps, out);
+  const int n = low_rank_steps<T>(p, t, m0, split, steps, out);
   zero_acc<T>(acc);
-  low_rank_start<T, L>(p, t, m0, n0, lds, steps, n, wm0, wn0, acc);
+  low_rank_start<T, L>(p, t, m0, n0, lds, steps, n, wm0, wn0, acc, out);
 
   if constexpr (DIRECT) mainloop_direct<T, L>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
   else

@@ -92,7 +92,8 @@ def _code_only(text):
 # Sources of the kernels whose HBM traffic the committed counter summary
 # holds (the 4096^3 GEMM kernels: their templates, tile tables and shared
 # device code); the other sources build other kernels.
-TRAFFIC_SOURCES = ("common.hpp", "gemm_f16.hip", "gemm_f32.hip", "internal.hpp")
+TRAFFIC_SOURCES = ("common.hpp", "gemm_f16.hip", "gemm_f16_kernel.hpp", "gemm_f32.hip",
+                   "internal.hpp")
 
 
 def kernel_source_hash():

@@ -655,9 +655,10 @@ __device__ __forceinline__ f16x8 low_rank_clamp(f16x8 v) {
 // have the adapter: those values of U that are not finite, and whole adapters
 // beyond the first kStartAdapters of a tile.  Such a value meets V's high part
 // only: its low part, of either sign or zero, would make a NaN of an infinity.
-// Doing all of the term so took 31 us more at 4096 x 4096 x 4096 with eight
-// adapters of rank 64 (153 against 122 us): its operands come in fragments of
-// 16 bytes a row, U once more for every 16 rows.
+// Doing all of the term so took 153 us at 4096 x 4096 x 4096 with eight adapters
+// of rank 64 (128 us as steps, 122 us the product alone): its operands come in
+// fragments of 16 bytes a row, U once more for every 16 rows.  A step costs
+// about what one of the product's does, 2 us a tile of 256 x 256.
 constexpr int kStartAdapters = 16;
 
 // The distinct adapters among the rows of a workgroup's tile, in the order of

@@ -404,6 +404,11 @@ def _call_rows(fn, dev, stream, workspace, need, args):
     """Run entry point `fn` on the current stream of GPU `dev` or the one given.
     Without a workspace, one comes from torch's allocator on the current
     stream, or from the library's pool on a stream that was given."""
+    if dev != _current_device():      # a default stream means the current GPU's
+        with torch.cuda.device(dev):
+            return _call_rows(fn, dev, stream, workspace, need, args)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError("the stream must be one of GPU %d, like the first tensor" % dev)
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on GPU %d" % dev)
@@ -428,6 +433,7 @@ def _public_stream(dev):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # handle of a GPU's current stream, without a Stream object where torch offers that
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
 

@@ -1133,9 +1133,74 @@ int term_parts(const LoraCall &c, int N, int K) {
   return want < 2 || most < 2 ? 1 : (want < most ? want : most);
 }
 
+// The shared product of a call, op(B) K x N: fp32 on top of C, fp16 on top of a
+// term (`term`, whose kernel the launch takes) or, `join`, alone into fp32.
+//
+// fp32 operands whose rows do not allow 16-byte loads are copied first, whatever
+// the size, and a deep K (a gradient's, over a projection's many outputs) is
+// split over four 64 x 64 tiles per CU where the product's own choice, made for
+// C of some size, leaves larger tiles and fewer parts: 1000 x 517 x 3000 with odd
+// rows 88 us by that choice, 63 us so.
+Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A, int lda,
+             const void *B, int ldb, float beta, void *C, int ldc) {
+  Call g = {};
+  g.M = c.M;
+  g.N = N;
+  g.K = K;
+  g.alpha = join ? 1.0f : c.alpha;
+  g.beta = join ? 0.0f : (c.half ? beta : 1.0f);
+  g.A = A;
+  g.lda = lda;
+  g.B = B;
+  g.ldb = ldb;
+  g.C = C;
+  g.ldc = ldc;
+  g.tb = tb;
+  g.out32 = join;
+  g.splits = 1;
+  g.pack_mode = c.half ? 1 : 2;
+  g.stream = c.stream;
+  if (c.half) {
+    const int parts = join ? 1 : term_parts(c, N, K);
+    if (parts > 1) g.split_mode = parts;
+    return g;
+  }
+  const long long tiles = (long long)((c.M + 63) / 64) * ((N + 63) / 64);
+  const int parts = (int)((4 * kCUs + tiles - 1) / tiles);
+  if (K >= 2 * (c.M > N ? c.M : N) && parts >= 2 && K / 256 >= 2) {
+    g.tile_config = 7;
+    g.split_mode = parts < K / 256 ? parts : K / 256;
+    if (g.split_mode > 64) g.split_mode = 64;
+  }
+  return g;
+}
+
+// Workspace of a product (split K, copies): a part of the call's own, so that a
+// captured call allocates nothing.  It is planned for operands all of whose rows
+// allow the widest loads, or none of whose do, the larger of the two before they
+// are known (A NULL); what a call's own plan takes beyond it it does without.
+size_t product_bytes(const LoraCall &c, bool join, bool tb, int N, int K, const void *A, int lda,
+                     const void *B, int ldb) {
+  const int vec = c.half ? 8 : 4;
+  const bool wide = lda % vec == 0 && ldb % vec == 0 && aligned_to(A, 16) && aligned_to(B, 16);
+  void *p = reinterpret_cast<void *>((uintptr_t)256);
+  size_t most = 256;
+  for (int odd = 0; odd < 2; ++odd) {
+    if (A != nullptr && wide == (odd != 0)) continue;
+    auto ld = [&](int cols) { return odd ? cols | 1 : (cols + 7) / 8 * 8; };
+    Call g = product(c, join, tb, N, K, p, ld(K), p, ld(tb ? K : N), 0.0f, p, ld(N));
+    g.ws_fixed_bytes = (size_t)1 << 30;
+    const size_t n = (c.half ? plan_f16(g) : plan_f32(g)).ws_bytes;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
 struct LoraSpace {
-  float *V, *S, *T, *W, *scale;
+  float *V, *S, *T, *scale;
   _Float16 *split;
+  char *W;
+  size_t w_bytes;
 };
 
 size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
@@ -1154,15 +1219,17 @@ size_t carve(const LoraCall &c, void *base, LoraSpace *s) {
   } else {
     s->split = w.take<_Float16>((size_t)c.M * 2 * rp);
     s->scale = w.take<float>((size_t)c.M + 256);   // read in whole tiles of rows
-    const int parts = term_parts(c, c.N, c.K);
-    if (parts > 1) s->W = w.take<float>(split_ws_bytes(parts, c.M, c.N) / sizeof(float));
   }
+  s->w_bytes = product_bytes(c, c.half && c.M <= kJoinRows, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw);
+  s->W = w.take<char>(s->w_bytes);
   return w.used;
 }
 
 struct GradSpace {
-  float *V, *G, *SV, *SG, *PA, *PB, *W, *scale;
+  float *V, *G, *SV, *SG, *PA, *PB, *scale;
   _Float16 *split;
+  char *W;
+  size_t w_bytes;
   int *start, *perm, *owner;
 };
 
@@ -1181,8 +1248,10 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   if (c.dX && c.half) {
     s->split = w.take<_Float16>((size_t)c.M * 2 * rp);
     s->scale = w.take<float>((size_t)c.M + 256);
-    const int split = term_parts(c, c.K, c.N);
-    if (split > 1) s->W = w.take<float>(split_ws_bytes(split, c.M, c.K) / sizeof(float));
+  }
+  if (c.dX) {
+    s->w_bytes = product_bytes(c, false, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw);
+    s->W = w.take<char>(s->w_bytes);
   }
   if (c.dB) {
     s->V = w.take<float>((size_t)c.M * rp);
@@ -1193,71 +1262,6 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
   if (c.dA) s->PA = w.take<float>(slots * rp * (size_t)c.K);
   if (c.dB) s->PB = w.take<float>(slots * rp * (size_t)c.N);
   return w.used;
-}
-
-// C := alpha * A op(B) + C with the fp32 kernels.  Operands whose rows do not
-// allow 16-byte loads are copied first, whatever the size, and a deep K (a
-// gradient's, over a projection's many outputs) is split over four 64 x 64
-// tiles per CU where the product's own choice, made for C of some size, leaves
-// larger tiles and fewer parts: 1000 x 517 x 3000 with odd rows 88 us by that
-// choice, 63 us so.
-hipError_t product_f32(const LoraCall &c, bool tb, int N, int K, const void *A, int lda,
-                       const void *B, int ldb, void *C, int ldc) {
-  Call g = {};
-  g.M = c.M;
-  g.N = N;
-  g.K = K;
-  g.alpha = c.alpha;
-  g.beta = 1.0f;
-  g.A = A;
-  g.lda = lda;
-  g.B = B;
-  g.ldb = ldb;
-  g.C = C;
-  g.ldc = ldc;
-  g.tb = tb;
-  g.splits = 1;
-  g.ws_limit = workspace_limit();
-  g.pack_mode = 2;
-  const long long tiles = (long long)((c.M + 63) / 64) * ((N + 63) / 64);
-  const int parts = (int)((4 * kCUs + tiles - 1) / tiles);
-  if (K >= 2 * (c.M > N ? c.M : N) && parts >= 2 && K / 256 >= 2) {
-    g.tile_config = 7;
-    g.split_mode = parts < K / 256 ? parts : K / 256;
-    if (g.split_mode > 64) g.split_mode = 64;
-  }
-  g.stream = c.stream;
-  return launch_f32(g);
-}
-
-// C := alpha * (A op(B) + the term) + beta * C with the fp16 kernels.
-hipError_t product_on_term(const LoraCall &c, const LowRank &term, bool tb, int N, int K,
-                           const void *A, int lda, const void *B, int ldb, float beta, void *C,
-                           int ldc, void *ws) {
-  Call g = {};
-  g.M = c.M;
-  g.N = N;
-  g.K = K;
-  g.alpha = c.alpha;
-  g.beta = beta;
-  g.A = A;
-  g.lda = lda;
-  g.B = B;
-  g.ldb = ldb;
-  g.C = C;
-  g.ldc = ldc;
-  g.tb = tb;
-  g.splits = 1;
-  g.ws_limit = workspace_limit();
-  g.term = &term;
-  const int parts = term_parts(c, N, K);
-  if (parts > 1) {
-    g.split_mode = parts;
-    g.ws_fixed = ws;
-    g.ws_fixed_bytes = split_ws_bytes(parts, c.M, N);
-  }
-  g.stream = c.stream;
-  return launch_f16_lora(g);
 }
 
 hipError_t join(const LoraCall &c, const float *V, const float *S, int parts) {
@@ -1298,22 +1302,25 @@ hipError_t run(const LoraCall &c, const LoraSpace &s) {
                        s.V, s.split, s.scale};
   hipError_t e = shrink_tiles<T>(c, p, t, 1);
   if (e != hipSuccess) return e;
+  const bool joined = c.half && c.M <= kJoinRows;
+  Call g = product(c, joined, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw, c.beta,
+                   joined ? s.T : c.Y, joined ? c.N : c.ldy);
+  g.ws_fixed = s.W;
+  g.ws_fixed_bytes = s.w_bytes;
   if (!c.half) {
     e = expand<T, true>(c, s.V, c.B, c.ldb, c.stride_b, c.N, c.alpha, c.beta,
                         static_cast<float *>(c.Y), c.ldy);
     if (e != hipSuccess) return e;
-    return product_f32(c, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw, c.Y, c.ldy);
+    return launch_f32(g);
   }
-  if (c.M <= kJoinRows) {
-    const int rc = gemm_f16f32_nt(c.M, c.N, c.K, 1.0f, static_cast<const gemm_half_t *>(c.X),
-                                  c.ldx, static_cast<const gemm_half_t *>(c.W), c.ldw, 0.0f, s.T,
-                                  c.N, c.stream);
-    return rc != 0 ? (hipError_t)rc : join(c, s.V, s.T, 1);
+  if (joined) {
+    e = launch_f16(g);
+    return e != hipSuccess ? e : join(c, s.V, s.T, 1);
   }
   const LowRank term = {s.split, 2 * p.Rp, s.scale, c.B, c.ldb, c.stride_b, c.rows, c.ranks, c.L,
                         c.R};
-  return product_on_term(c, term, true, c.N, c.K, c.X, c.ldx, c.W, c.ldw, c.beta, c.Y, c.ldy,
-                         s.W);
+  g.term = &term;
+  return launch_f16_lora(g);
 }
 
 template <typename T>
@@ -1336,17 +1343,20 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
                               s.SV, s.V, nullptr, nullptr};
   e = shrink_tiles<T>(c, p, t, jobs);
   if (e != hipSuccess) return e;
+  Call g = product(c, false, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw, c.beta_x, c.dX, c.lddx);
+  g.ws_fixed = s.W;
+  g.ws_fixed_bytes = s.w_bytes;
   if (c.dX && c.half) {
     const LowRank term = {s.split, 2 * p.Rp, s.scale, c.A, c.lda, c.stride_a, c.rows,
                           c.ranks, c.L, c.R};
-    e = product_on_term(c, term, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw, c.beta_x, c.dX,
-                        c.lddx, s.W);
+    g.term = &term;
+    e = launch_f16_lora(g);
     if (e != hipSuccess) return e;
   } else if (c.dX) {
     e = expand<T, false>(c, s.G, c.A, c.lda, c.stride_a, c.K, c.alpha, c.beta_x,
                          static_cast<float *>(c.dX), c.lddx);
     if (e != hipSuccess) return e;
-    e = product_f32(c, false, c.K, c.N, c.dY, c.lddy, c.W, c.ldw, c.dX, c.lddx);
+    e = launch_f32(g);
     if (e != hipSuccess) return e;
   }
   if (!c.dA && !c.dB) return hipSuccess;

@@ -11,6 +11,9 @@ using dgemm::MoeCall;
 
 int at_least_one(int n) { return n > 1 ? n : 1; }
 
+// Grids and 32-bit indices hold up to the limit with room to spare.
+bool bad_size(int n) { return n < 0 || n > GEMM_ROWS_MAX_SIZE; }
+
 // A workspace of `bytes` for one call on `stream`: the caller's, or one from
 // the library's pool, given back in stream order by close().  A caller's that
 // is not 256-byte aligned gives status `base`, one too small `base` - 1.
@@ -47,9 +50,9 @@ int lora(bool half, int M, int N, int K, float alpha, const void *X, int ldx, co
          int ldw, float beta, void *Y, int ldy, int L, int R, const void *A, int lda,
          long long stride_a, const void *B, int ldb, long long stride_b, const float *scale,
          const int *ranks, const int *rows, void *ws, size_t ws_bytes, void *stream) {
-  if (M < 0) return -301;
-  if (N < 0) return -302;
-  if (K < 0) return -303;
+  if (bad_size(M)) return -301;
+  if (bad_size(N)) return -302;
+  if (bad_size(K)) return -303;
   if (ldx < at_least_one(K)) return -306;
   if (ldw < at_least_one(K)) return -308;
   if (ldy < at_least_one(N)) return -311;
@@ -119,9 +122,9 @@ int lora_grad(bool half, int M, int N, int K, float alpha, const void *dY, int l
               const int *ranks, const int *rows, float beta_x, void *dX, int lddx, float beta_ab,
               float *dA, int ldda, long long stride_da, float *dB, int lddb, long long stride_db,
               void *ws, size_t ws_bytes, void *stream) {
-  if (M < 0) return -401;
-  if (N < 0) return -402;
-  if (K < 0) return -403;
+  if (bad_size(M)) return -401;
+  if (bad_size(N)) return -402;
+  if (bad_size(K)) return -403;
   if (lddy < at_least_one(N)) return -406;
   if (ldx < at_least_one(K)) return -408;
   if (dX != nullptr && ldw < at_least_one(K)) return -410;
@@ -215,8 +218,8 @@ int moe(bool half, int M, int D, int F, int E, int top_k, int renorm, float alph
         const void *W2, int ld2, long long stride2, float beta, void *Y, int ldy, int *ids,
         float *weights, void *ws, size_t ws_bytes, void *stream) {
   if (M < 0 || M > GEMM_MOE_MAX_TOKENS) return -501;
-  if (D < 1) return -502;
-  if (F < 1) return -503;
+  if (D < 1 || bad_size(D)) return -502;
+  if (F < 1 || bad_size(F)) return -503;
   if (E < 1 || E > GEMM_MOE_MAX_EXPERTS) return -504;
   if (top_k < 1 || top_k > E || top_k > GEMM_MOE_MAX_CHOICES) return -505;
   if (renorm != 0 && renorm != 1) return -506;
@@ -296,8 +299,8 @@ int gemm_lora_f32(int M, int N, int K, float alpha, const float *X, int ldx, con
 }
 
 size_t gemm_lora_workspace(int dtype, int M, int N, int K, int L, int R) {
-  if ((dtype != 0 && dtype != 1) || M <= 0 || N <= 0 || K <= 0 || L <= 0 ||
-      L > GEMM_LORA_MAX_ADAPTERS || R <= 0 || R > GEMM_LORA_MAX_RANK)
+  if ((dtype != 0 && dtype != 1) || M <= 0 || N <= 0 || K <= 0 || L <= 0 || bad_size(M) ||
+      bad_size(N) || bad_size(K) || L > GEMM_LORA_MAX_ADAPTERS || R <= 0 || R > GEMM_LORA_MAX_RANK)
     return 0;
   LoraCall c = {};
   c.half = dtype == 1;
@@ -335,8 +338,8 @@ int gemm_lora_grad_f32(int M, int N, int K, float alpha, const float *dY, int ld
 }
 
 size_t gemm_lora_grad_workspace(int dtype, int M, int N, int K, int L, int R) {
-  if ((dtype != 0 && dtype != 1) || M <= 0 || N <= 0 || K <= 0 || L <= 0 ||
-      L > GEMM_LORA_MAX_ADAPTERS || R <= 0 || R > GEMM_LORA_MAX_RANK)
+  if ((dtype != 0 && dtype != 1) || M <= 0 || N <= 0 || K <= 0 || L <= 0 || bad_size(M) ||
+      bad_size(N) || bad_size(K) || L > GEMM_LORA_MAX_ADAPTERS || R <= 0 || R > GEMM_LORA_MAX_RANK)
     return 0;
   static float some;   // only tells which outputs are wanted: all of them
   LoraCall c = {};
@@ -371,6 +374,7 @@ int gemm_moe_f32(int M, int D, int F, int E, int top_k, int renorm, float alpha,
 
 size_t gemm_moe_workspace(int dtype, int M, int D, int F, int E, int top_k) {
   if ((dtype != 0 && dtype != 1) || M <= 0 || M > GEMM_MOE_MAX_TOKENS || D < 1 || F < 1 || E < 1 ||
+      bad_size(D) || bad_size(F) ||
       E > GEMM_MOE_MAX_EXPERTS || top_k < 1 || top_k > E || top_k > GEMM_MOE_MAX_CHOICES)
     return 0;
   MoeCall c = {};

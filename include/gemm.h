@@ -315,13 +315,18 @@ int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int l
  * call's alone until its work on `stream` is done; NULL takes it from the
  * library's pool in stream order (gemm_set_workspace_limit applies;
  * GEMM_ERR_NO_WORKSPACE if it cannot be had, nothing enqueued).  Nothing in it
- * needs an initial value.  The shared product inside a low-rank call may
- * split K as gemm_* does, with workspace of its own from the pool.
+ * needs an initial value, and a call with a workspace allocates nothing: use one
+ * for calls that are captured into a graph.
  *
  * Status: 0; a positive hipError_t; or for invalid argument i (from 1, in
  * signature order) -300-i (gemm_lora_*), -400-i (gemm_lora_grad_*), -500-i
  * (gemm_moe_*); checked before any HIP call.
+ *
+ * The test switches gemm_set_load_mode, gemm_set_tile_config,
+ * gemm_set_split, gemm_set_tail_split, gemm_set_pack and gemm_set_stream_k do
+ * not apply.
  */
+#define GEMM_ROWS_MAX_SIZE 16777216   /* of M, N, K, D and F */
 #define GEMM_LORA_MAX_RANK 256
 #define GEMM_LORA_MAX_ADAPTERS 65535
 #define GEMM_MOE_MAX_TOKENS 256
@@ -349,9 +354,11 @@ int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int l
  *
  * A row is touched by its own adapter only: an infinity or NaN in another's
  * weights does not reach it.  V = A_a x_i is summed in fp32 and enters the
- * second product in at least 21 significant bits; the sum with W x_i is
- * formed in fp32 and rounded once.  Accuracy, with q = |W||x| + |scale||B|(|A||x|):
- * |err| <= 4*(K+R+4)*u*|alpha|*q + 4*u*|beta*Y| plus the one rounding, u = 2^-24.
+ * second product in at least 21 significant bits (in fp16 calls of more than
+ * 512 rows: or to within 2^-39 of the largest of its row); the sum with W x_i
+ * is formed in fp32 and rounded once.  Accuracy, with q = |W||x| + |scale||B|(|A||x|):
+ * |err| <= 4*(K+R+4)*u*|alpha|*q + 4*u*|beta*Y| plus the one rounding, u = 2^-24
+ * (and the 2^-39, where a row of V spans more than 2^17).
  * alpha == 0 or K == 0: Y := beta * Y.
  */
 int gemm_lora_f16(int M, int N, int K, float alpha,
@@ -437,9 +444,11 @@ size_t gemm_lora_grad_workspace(int dtype, int M, int N, int K, int L, int R);
  *   ids, weights       device, M x top_k, dense: the experts chosen (int) and
  *                      w (float); either may be NULL
  * Logits are summed in 64 bits, since which expert a token takes hangs on
- * their order; a NaN logit ranks below every number.  Weights of experts that
- * no token chose are not read.  alpha == 0: Y := beta * Y, nothing else is
- * read or written (ids and weights included).
+ * their order; a NaN logit ranks below every number.  silu(g) * u is formed in
+ * fp32; in fp16 calls it enters the second product rounded to 11 bits at any
+ * magnitude (what is below 2^-28 of its row's largest: to 2^-39 of that).
+ * Weights of experts that no token chose are not read.  alpha == 0:
+ * Y := beta * Y, nothing else is read or written (ids and weights included).
  */
 int gemm_moe_f16(int M, int D, int F, int E, int top_k, int renorm, float alpha,
                  const gemm_half_t *X, int ldx,

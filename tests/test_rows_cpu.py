@@ -109,7 +109,54 @@ def test_workspace_sizes():
                 assert fn(dtype, *(good[:i] + (0,) + good[i + 1:])) == 0
         assert fn(2, *good) == 0
     # sizes beyond 32 bits
-    assert dg.gemm_lora_grad_workspace(0, 1 << 27, 64, 64, 1, 16) > 1 << 33
+    most = 1 << 24
+    assert dg.gemm_lora_grad_workspace(0, most, 64, 64, 1, 256) > 1 << 33
+    for i in range(3):
+        for fn in (dg.gemm_lora_workspace, dg.gemm_lora_grad_workspace):
+            sizes = [16, 16, 16, 2, 8]
+            sizes[i] = most + 1
+            assert fn(1, *sizes) == 0
+    assert dg.gemm_moe_workspace(1, 2, most + 1, 16, 4, 2) == 0
+    assert dg.gemm_moe_workspace(1, 2, 16, most + 1, 4, 2) == 0
+
+
+def test_sizes_beyond_the_limit():
+    """Refused as argument 1, 2 or 3, whatever the others are."""
+    import dense_gemm_fp32_amd as dg
+    big = (1 << 24) + 1
+    for dt in ("f16", "f32"):
+        for i, n in enumerate("MNK"):
+            for base, args, name in ((-300, LORA, "gemm_lora_"), (-400, GRAD, "gemm_lora_grad_")):
+                got = getattr(dg, name + dt)(*dict(args, **{n: big}).values())
+                assert got == base - 1 - i
+        for i, n in ((2, "D"), (3, "F")):
+            assert getattr(dg, "gemm_moe_" + dt)(*dict(MOE, **{n: big}).values()) == -500 - i
+
+
+def test_calls_run_on_the_tensors_gpu(monkeypatch):
+    """Where another GPU than the tensors' is current, a call changes to theirs
+    and back, since a default stream means the current one's."""
+    from dense_gemm_fp32_amd import binding
+    now, calls = [0], []
+
+    class Change:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.dev
+
+        def __exit__(self, *_):
+            now[0] = self.before
+    monkeypatch.setattr(binding, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Change)
+
+    def entry(*args):
+        calls.append((now[0],) + args)
+        return 0
+    for dev in (0, 1):
+        binding._call_rows(entry, dev, 5, None, 0, (7,))
+        assert calls[-1] == (dev, 7, None, 0, 5) and now[0] == 0
 
 
 def test_wrappers_refuse_cpu_tensors():

@@ -6,6 +6,8 @@
 
 namespace dgemm {
 
-hipError_t launch_f16_lora(const Call &c) { return launch_f16_as_is<true>(c); }
+hipError_t launch_f16_lora(const Call &c) {
+  return run_packed(c, 2, plan_f16, launch_f16_as_is<true>);
+}
 
 }  // namespace dgemm

@@ -1123,21 +1123,23 @@ int outer_chunk(const LoraCall &c) {
 // adapter, which the pass does not mind and the product's epilogue does.
 constexpr int kJoinRows = 512;
 
-// Parts of K of the fp16 product on top of a term (N columns), where its
-// smallest tiles leave half of the CUs without one; the parts share the term's
-// adapters out.  257 x 1024 x 1024, three adapters: 24 us in one part, 15 us
-// in four.
-int term_parts(const LoraCall &c, int N, int K) {
+// Parts of K of an fp16 product, where its smallest tiles leave CUs without one
+// (in a deep K, without two): 257 x 1024 x 1024 on a term of three adapters, who
+// are shared out, 24 us in one part, 15 us in four.
+int product_parts(const LoraCall &c, int N, int K) {
   const long long tiles = (long long)((c.M + 63) / 64) * (((long long)N + 127) / 128);
-  const int want = (int)(kCUs / tiles), most = K / 256 < 8 ? K / 256 : 8;
+  const int want = (int)((K >= 2048 ? 2 * kCUs : kCUs) / tiles);
+  const int most = K / 256 < 8 ? K / 256 : 8;
   return want < 2 || most < 2 ? 1 : (want < most ? want : most);
 }
 
 // The shared product of a call, op(B) K x N: fp32 on top of C, fp16 on top of a
 // term (`term`, whose kernel the launch takes) or, `join`, alone into fp32.
 //
-// fp32 operands whose rows do not allow 16-byte loads are copied first, whatever
-// the size, and a deep K (a gradient's, over a projection's many outputs) is
+// Operands whose rows do not allow 16-byte loads are copied first, whatever the
+// size (fp16 89 x 1216 x 1449 with odd rows, small tiles: 77 us without, 18 us
+// with the copies; on a term 1643 x 3584 x 3886: 153 and 82 us, since the large
+// tile has direct loads only there), and a deep fp32 K (a gradient's, over a projection's many outputs) is
 // split over four 64 x 64 tiles per CU where the product's own choice, made for
 // C of some size, leaves larger tiles and fewer parts: 1000 x 517 x 3000 with odd
 // rows 88 us by that choice, 63 us so.
@@ -1158,10 +1160,10 @@ Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A,
   g.tb = tb;
   g.out32 = join;
   g.splits = 1;
-  g.pack_mode = c.half ? 1 : 2;
+  g.pack_mode = 2;
   g.stream = c.stream;
   if (c.half) {
-    const int parts = join ? 1 : term_parts(c, N, K);
+    const int parts = product_parts(c, N, K);
     if (parts > 1) g.split_mode = parts;
     return g;
   }

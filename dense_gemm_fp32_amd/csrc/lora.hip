@@ -361,7 +361,8 @@ struct ShrinkTiles {
         const int r = r0 + u < rk ? r0 + u : rk - 1;
         wr[q] = load_whole(w + (size_t)r * (size_t)j.ldw + k + v * VEC);
       } else {
-        wr[q] = load_end(w + (size_t)(k + u) * (size_t)j.ldw, r0 + v * VEC, R);
+        const T *row = w + (size_t)(k + u) * (size_t)j.ldw;
+        wr[q] = R < VEC ? load_part(row + v * VEC, R - v * VEC) : load_end(row, r0 + v * VEC, R);
       }
     }
   }
@@ -385,6 +386,11 @@ struct ShrinkTiles {
       } else {
         const bool in = k + u < j.K;
         const int r = r0 + v * VEC, last = R - VEC;
+        if (R < VEC) {
+          wr[q] = load_part(w + (size_t)(in ? k + u : j.K - 1) * (size_t)j.ldw + v * VEC,
+                            in ? R - v * VEC : 0);
+          continue;
+        }
         wr[q] = move_down(load_whole(w + (size_t)(in ? k + u : j.K - 1) * (size_t)j.ldw +
                                      (r < last ? r : last)),
                           in ? r - last : VEC);
@@ -392,7 +398,7 @@ struct ShrinkTiles {
     }
   }
   // Rows shorter than a piece, which no such load fits.
-  __device__ __forceinline__ bool tiny() const { return j.K < VEC || (!KMAJ && R < VEC); }
+  __device__ __forceinline__ bool tiny() const { return j.K < VEC; }
   __device__ __forceinline__ void load(int k, Frag (&xr)[PER], Frag (&wr)[PER]) const {
     if (tiny()) return;
     if (k + BK <= j.K) load_whole_step(k, xr, wr);
@@ -568,69 +574,66 @@ struct ExpandParams {
   float alpha, beta;
 };
 
-// C := alpha * s_a V B_a^T + beta * C, fp32 products: 16 rows x 64 columns a
-// wave.  grid: (ceil(N/256), row blocks, at most 65535 and strided over).
-template <typename T, bool RMAJ>
+// C := alpha * s_a V B_a^T + beta * C in fp32: 16 rows x 16 NB columns a wave.
+// grid: (ceil(N / (64 NB)), row blocks, at most 65535 and strided over).
+template <bool RMAJ, int NB>
 __global__ __launch_bounds__(256) void lora_expand(ExpandParams p) {
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
-  const int n0 = blockIdx.x * 256 + wave * 64;
+  const int n0 = (blockIdx.x * 4 + wave) * 16 * NB;
   if (n0 >= p.N) return;
   for (int rb = blockIdx.y; rb < (p.M + 15) / 16; rb += gridDim.y) {
-  const int row0 = rb * 16;
-  const int row = row0 + li;
-  const int id = adapter_of(p.rows, row, p.M, p.L);
-  unsigned left = (unsigned)(__ballot(id >= 0) & 0xffffu);
-  const float *vrow = p.V + (size_t)(row < p.M ? row : p.M - 1) * p.Rp;
-  f32x4 out[4];
+    const int row0 = rb * 16;
+    const int row = row0 + li;
+    const int id = adapter_of(p.rows, row, p.M, p.L);
+    unsigned left = (unsigned)(__ballot(id >= 0) & 0xffffu);
+    const float *vrow = p.V + (size_t)(row < p.M ? row : p.M - 1) * p.Rp;
+    f32x4 out[NB];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) out[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  while (left != 0) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    const unsigned same = (unsigned)(__ballot(id == a) & 0xffffu);
-    left &= ~same;
-    const int rk = rank_of(p.ranks, a, p.R);
-    const float s = p.scale ? p.scale[a] : 1.0f;
-    const T *w = static_cast<const T *>(p.B) + (size_t)a * (size_t)p.stride;
-    f32x4 t[4];
+    for (int b = 0; b < NB; ++b) out[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    while (left != 0) {
+      const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+      const unsigned same = (unsigned)(__ballot(id == a) & 0xffffu);
+      left &= ~same;
+      const int rk = rank_of(p.ranks, a, p.R);
+      const float s = p.scale ? p.scale[a] : 1.0f;
+      const float *w = static_cast<const float *>(p.B) + (size_t)a * (size_t)p.stride;
+      f32x4 t[NB];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) t[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int r = 4 * lg; r < rk + 4 * lg; r += 16) {
-      f32x4 v;
+      for (int b = 0; b < NB; ++b) t[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int r = 4 * lg; r < rk + 4 * lg; r += 16) {
+        const f32x4 v = load_whole(vrow + r);     // zeros from the rank on
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = r + e < rk ? vrow[r + e] : 0.0f;
+        for (int b = 0; b < NB; ++b) {
+          int n = n0 + 16 * b + li;
+          n = n < p.N ? n : p.N - 1;
+          f32x4 u;
+          if constexpr (RMAJ) u = load_frag(w + (size_t)n * p.ldb, r, p.R);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        int n = n0 + 16 * b + li;
-        n = n < p.N ? n : p.N - 1;
-        f32x4 u;
+          for (int e = 0; e < 4; ++e)
+            u[e] = r + e < rk ? (RMAJ ? u[e] : w[(size_t)(r + e) * p.ldb + n]) : 0.0f;
+          t[b] = mma16(v, u, t[b]);
+        }
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          u[e] = r + e < rk ? (float)(RMAJ ? w[(size_t)n * p.ldb + r + e]
-                                           : w[(size_t)(r + e) * p.ldb + n])
-                            : 0.0f;
-        t[b] = mma16(v, u, t[b]);
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((same >> (4 * lg + j)) & 1) out[b][j] = s * t[b][j];
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int n = n0 + 16 * b + li;
+      if (n >= p.N) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = row0 + 4 * lg + j;
+        if (i >= p.M) continue;
+        float *c = p.C + (size_t)i * (size_t)p.ldc + n;
+        const float o = p.alpha * out[b][j];
+        *c = p.beta != 0.0f ? __builtin_fmaf(p.beta, *c, o) : o;
       }
     }
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if ((same >> (4 * lg + j)) & 1) out[b][j] = s * t[b][j];
-  }
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int n = n0 + 16 * b + li;
-    if (n >= p.N) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = row0 + 4 * lg + j;
-      if (i >= p.M) continue;
-      float *c = p.C + (size_t)i * (size_t)p.ldc + n;
-      const float o = p.alpha * out[b][j];
-      *c = p.beta != 0.0f ? __builtin_fmaf(p.beta, *c, o) : o;
-    }
-  }
   }
 }
 
@@ -1074,7 +1077,9 @@ hipError_t skinny(const LoraCall &c, float *V, float *S) {
   return hipGetLastError();
 }
 
-template <typename T, bool RMAJ>
+// 64 columns a wave read V least often, 16 make the most waves: 4096 x 4096, rank
+// 64, 59 against 73 us; 1000 x 3000, rank 12, 9.2 against 6.9 us.
+template <bool RMAJ>
 hipError_t expand(const LoraCall &c, const float *V, const void *B, int ldb, long long stride,
                   int N, float alpha, float beta, float *C, int ldc) {
   ExpandParams p;
@@ -1095,9 +1100,13 @@ hipError_t expand(const LoraCall &c, const float *V, const void *B, int ldb, lon
   p.alpha = alpha;
   p.beta = beta;
   const int rb = (c.M + 15) / 16;
-  hipLaunchKernelGGL((lora_expand<T, RMAJ>),
-                     dim3((unsigned)((N + 255) / 256), (unsigned)(rb < 65535 ? rb : 65535)), dim3(256),
-                     0, c.stream, p);
+  const unsigned y = (unsigned)(rb < 65535 ? rb : 65535);
+  if ((long long)((N + 255) / 256) * rb >= 8 * kCUs)
+    hipLaunchKernelGGL((lora_expand<RMAJ, 4>), dim3((unsigned)((N + 255) / 256), y), dim3(256), 0,
+                       c.stream, p);
+  else
+    hipLaunchKernelGGL((lora_expand<RMAJ, 1>), dim3((unsigned)((N + 63) / 64), y), dim3(256), 0,
+                       c.stream, p);
   return hipGetLastError();
 }
 
@@ -1160,7 +1169,9 @@ Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A,
   g.tb = tb;
   g.out32 = join;
   g.splits = 1;
-  g.pack_mode = 2;
+  // (fp16 columns of B that do not end with a vector keep the tiles from the direct
+  // loads, copied or not: 2061 x 442 x 424 in all 62 us without, 80 us with copies)
+  g.pack_mode = c.half && !tb && N % 8 != 0 ? 1 : 2;
   g.stream = c.stream;
   if (c.half) {
     const int parts = product_parts(c, N, K);
@@ -1310,7 +1321,7 @@ hipError_t run(const LoraCall &c, const LoraSpace &s) {
   g.ws_fixed = s.W;
   g.ws_fixed_bytes = s.w_bytes;
   if (!c.half) {
-    e = expand<T, true>(c, s.V, c.B, c.ldb, c.stride_b, c.N, c.alpha, c.beta,
+    e = expand<true>(c, s.V, c.B, c.ldb, c.stride_b, c.N, c.alpha, c.beta,
                         static_cast<float *>(c.Y), c.ldy);
     if (e != hipSuccess) return e;
     return launch_f32(g);
@@ -1355,7 +1366,7 @@ hipError_t run_grad(const LoraCall &c, const GradSpace &s) {
     e = launch_f16_lora(g);
     if (e != hipSuccess) return e;
   } else if (c.dX) {
-    e = expand<T, false>(c, s.G, c.A, c.lda, c.stride_a, c.K, c.alpha, c.beta_x,
+    e = expand<false>(c, s.G, c.A, c.lda, c.stride_a, c.K, c.alpha, c.beta_x,
                          static_cast<float *>(c.dX), c.lddx);
     if (e != hipSuccess) return e;
     e = launch_f32(g);

@@ -1349,8 +1349,11 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma_lora(GemmParams p, LowRank t
   zero_acc<T>(acc);
   low_rank_start<T, L>(p, t, m0, n0, lds, steps, n, wm0, wn0, acc, out);
 
-  if constexpr (DIRECT) mainloop_direct<T, L>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
-  else
+  if constexpr (DIRECT) {
+    GemmParams q = p;
+    q.N = t.columns;
+    mainloop_direct<T, L>(q, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
+  } else
     mainloop_staged<T, L>(p, m0, n0, lds, wm0, wn0, vec_width_a(p.vec_ab), vec_width_b(p.vec_ab),
                           acc);
 
@@ -1381,7 +1384,7 @@ static bool vec_ok(const void *p, int ld, int elems) {
 // Whether every tile of a call on top of a term takes the direct loads: the
 // kernel's conditions (direct_ok) for the largest tile.
 static bool term_direct(const Call &c) {
-  return vec_ok(c.A, c.lda, 8) && vec_ok(c.B, c.ldb, 8) && (c.tb || c.N % 8 == 0) &&
+  return vec_ok(c.A, c.lda, 8) && vec_ok(c.B, c.ldb, 8) && (c.tb || c.b_padded || c.N % 8 == 0) &&
          256LL * c.lda < (1LL << 31) && 256LL * c.ldb < (1LL << 31);
 }
 
@@ -1441,12 +1444,14 @@ static hipError_t launch_variant(const Call &c, const Plan &pl) {
   const dim3 grid((unsigned)(pl.blocks * c.splits));
   if constexpr (TERM) {
     constexpr bool STAGED = T::NWAVES < 8;   // the tiles that have a staged form
+    LowRank term = *c.term;
+    term.columns = c.b_padded && !TB ? (c.N + 7) / 8 * 8 : c.N;
     if (STAGED && !term_direct(c))
       hipLaunchKernelGGL((hgemm_mfma_lora<T, TB, VC, OUT32, !STAGED>), grid, dim3(T::NT), 0,
-                         c.stream, p, *c.term);
+                         c.stream, p, term);
     else
       hipLaunchKernelGGL((hgemm_mfma_lora<T, TB, VC, OUT32, true>), grid, dim3(T::NT), 0,
-                         c.stream, p, *c.term);
+                         c.stream, p, term);
   } else
     hipLaunchKernelGGL((hgemm_mfma<T, TA, TB, VC, OUT32>), grid, dim3(T::NT), 0, c.stream, p);
   return hipGetLastError();

@@ -21,6 +21,7 @@ struct LowRank {
   long long stride;
   const int *rows, *ranks;
   int L, R;
+  int columns;           // of B that the direct loads may read (set by the launch)
 };
 
 // One validated GEMM call, after quick returns have been taken: M, N, K > 0
@@ -71,6 +72,7 @@ struct Call {
   // configuration (1, 5, 6, 7) is taken.
   int streamk_mode;
   const LowRank *term;   // launch_f16_lora only
+  bool b_padded;         // B is a copy whose rows end with whole 16 bytes
   hipStream_t stream;
 };
 

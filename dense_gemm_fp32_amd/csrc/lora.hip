@@ -1148,7 +1148,10 @@ int product_parts(const LoraCall &c, int N, int K) {
 // Operands whose rows do not allow 16-byte loads are copied first, whatever the
 // size (fp16 89 x 1216 x 1449 with odd rows, small tiles: 77 us without, 18 us
 // with the copies; on a term 1643 x 3584 x 3886: 153 and 82 us, since the large
-// tile has direct loads only there), and a deep fp32 K (a gradient's, over a projection's many outputs) is
+// tile has direct loads only there; 374 x 1223 x 448, all of the gradients: 93 and
+// 71 us, since columns that end inside a vector do so in the copy no longer).
+// Few tiles of fp32 (224 x 1957 x 1408: 108 us as the product's own choice, all of
+// the gradients 151 us so and 79 us split) and a deep fp32 K (a gradient's, over a projection's many outputs) are
 // split over four 64 x 64 tiles per CU where the product's own choice, made for
 // C of some size, leaves larger tiles and fewer parts: 1000 x 517 x 3000 with odd
 // rows 88 us by that choice, 63 us so.
@@ -1169,9 +1172,7 @@ Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A,
   g.tb = tb;
   g.out32 = join;
   g.splits = 1;
-  // (fp16 columns of B that do not end with a vector keep the tiles from the direct
-  // loads, copied or not: 2061 x 442 x 424 in all 62 us without, 80 us with copies)
-  g.pack_mode = c.half && !tb && N % 8 != 0 ? 1 : 2;
+  g.pack_mode = 2;
   g.stream = c.stream;
   if (c.half) {
     const int parts = product_parts(c, N, K);
@@ -1180,7 +1181,7 @@ Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A,
   }
   const long long tiles = (long long)((c.M + 63) / 64) * ((N + 63) / 64);
   const int parts = (int)((4 * kCUs + tiles - 1) / tiles);
-  if (K >= 2 * (c.M > N ? c.M : N) && parts >= 2 && K / 256 >= 2) {
+  if ((K >= 2 * (c.M > N ? c.M : N) || tiles < kCUs) && parts >= 2 && K / 256 >= 2) {
     g.tile_config = 7;
     g.split_mode = parts < K / 256 ? parts : K / 256;
     if (g.split_mode > 64) g.split_mode = 64;

@@ -251,6 +251,7 @@ hipError_t run_packed(const Call &c, int eb, Plan (*plan)(const Call &),
     jb = PackJob{static_cast<const char *>(c.B), dst, (long long)c.ldb * eb, (long long)cols * eb,
                  cpr, (long long)rows * cpr};
     in.B = dst;
+    in.b_padded = true;
     in.ldb = pk.ldb;
   }
   // The GEMM's own workspace (split K) is the rest of the allocation.

@@ -72,6 +72,7 @@ struct Call {
   // configuration (1, 5, 6, 7) is taken.
   int streamk_mode;
   const LowRank *term;   // launch_f16_lora only
+  bool copy_ragged_b;    // copy B (as stored) also where only its columns do not end with 16 bytes
   bool b_padded;         // B is a copy whose rows end with whole 16 bytes
   hipStream_t stream;
 };

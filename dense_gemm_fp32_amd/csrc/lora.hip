@@ -1148,13 +1148,13 @@ int product_parts(const LoraCall &c, int N, int K) {
 // Operands whose rows do not allow 16-byte loads are copied first, whatever the
 // size (fp16 89 x 1216 x 1449 with odd rows, small tiles: 77 us without, 18 us
 // with the copies; on a term 1643 x 3584 x 3886: 153 and 82 us, since the large
-// tile has direct loads only there; 374 x 1223 x 448, all of the gradients: 93 and
-// 71 us, since columns that end inside a vector do so in the copy no longer).
-// Few tiles of fp32 (224 x 1957 x 1408: 108 us as the product's own choice, all of
-// the gradients 151 us so and 79 us split) and a deep fp32 K (a gradient's, over a projection's many outputs) are
-// split over four 64 x 64 tiles per CU where the product's own choice, made for
-// C of some size, leaves larger tiles and fewer parts: 1000 x 517 x 3000 with odd
-// rows 88 us by that choice, 63 us so.
+// tile has direct loads only there).  So is an fp16
+// B whose columns end inside a vector, which they do not in the copy (gradients of
+// 1261 x 871 x 1314: 199 and 96 us).
+// Few tiles of fp32 (the gradients of 224 x 1957 x 1408: 151 us by the product's
+// own choice, 79 us so) and a deep fp32 K (a gradient's, over a projection's many
+// outputs; 1000 x 517 x 3000 with odd rows: 88 and 63 us) are split over four 64 x
+// 64 tiles per CU.
 Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A, int lda,
              const void *B, int ldb, float beta, void *C, int ldc) {
   Call g = {};
@@ -1173,6 +1173,7 @@ Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A,
   g.out32 = join;
   g.splits = 1;
   g.pack_mode = 2;
+  g.copy_ragged_b = c.half;
   g.stream = c.stream;
   if (c.half) {
     const int parts = product_parts(c, N, K);
@@ -1196,7 +1197,8 @@ Call product(const LoraCall &c, bool join, bool tb, int N, int K, const void *A,
 size_t product_bytes(const LoraCall &c, bool join, bool tb, int N, int K, const void *A, int lda,
                      const void *B, int ldb) {
   const int vec = c.half ? 8 : 4;
-  const bool wide = lda % vec == 0 && ldb % vec == 0 && aligned_to(A, 16) && aligned_to(B, 16);
+  const bool wide = lda % vec == 0 && ldb % vec == 0 && aligned_to(A, 16) && aligned_to(B, 16) &&
+                    (!c.half || tb || N % vec == 0);
   void *p = reinterpret_cast<void *>((uintptr_t)256);
   size_t most = 256;
   for (int odd = 0; odd < 2; ++odd) {

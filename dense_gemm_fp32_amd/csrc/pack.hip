@@ -169,7 +169,8 @@ long long ws_available(const Call &c) {
 PackChoice pack_choice(const Call &c, int eb, Plan (*plan)(const Call &)) {
   PackChoice pk;
   if (c.force_scalar || c.pack_mode == 1) return pk;
-  const bool ua = !rows_aligned(c.A, c.lda, eb), ub = !rows_aligned(c.B, c.ldb, eb);
+  const bool ragged = c.copy_ragged_b && !c.tb && c.N % (16 / eb) != 0;
+  const bool ua = !rows_aligned(c.A, c.lda, eb), ub = ragged || !rows_aligned(c.B, c.ldb, eb);
   if (!ua && !ub) return pk;
   if (c.pack_mode != 2 && !pack_by_size(c, eb)) return pk;
   int ra, ca, rb, cb;

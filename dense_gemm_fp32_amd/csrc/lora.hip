@@ -1148,10 +1148,9 @@ int product_parts(const LoraCall &c, int N, int K) {
 // Operands whose rows do not allow 16-byte loads are copied first, whatever the
 // size (fp16 89 x 1216 x 1449 with odd rows, small tiles: 77 us without, 18 us
 // with the copies; on a term 1643 x 3584 x 3886: 153 and 82 us, since the large
-// tile has direct loads only there).  So is an fp16
-// B whose columns end inside a vector, which they do not in the copy (gradients of
-// 1261 x 871 x 1314: 199 and 96 us).
-// Few tiles of fp32 (the gradients of 224 x 1957 x 1408: 151 us by the product's
+// tile has direct loads only there).  So is an fp16 B whose columns end inside a
+// vector, which they do not in the copy (gradients of 1261 x 871 x 1314: 199 and
+// 96 us).  Few tiles of fp32 (the gradients of 224 x 1957 x 1408: 151 us by the product's
 // own choice, 79 us so) and a deep fp32 K (a gradient's, over a projection's many
 // outputs; 1000 x 517 x 3000 with odd rows: 88 and 63 us) are split over four 64 x
 // 64 tiles per CU.

@@ -693,6 +693,59 @@ def test_captured_graphs_of_many_rows(dt, size):
                 assert ref.worst(o[n], *want[n]) <= 1.0, (turn, n)
 
 
+def far_apart(t, stride, dim=0):
+    """A device copy of t whose entries along `dim` are `stride` elements apart."""
+    steps = [stride if d == dim else n for d, n in enumerate(t.contiguous().stride())]
+    room = torch.empty(stride * (t.shape[dim] - 1) + t[:1].numel() * t.shape[dim], dtype=t.dtype,
+                       device=GPU)
+    view = room.as_strided(t.shape, steps)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("dt,M", [("f16", 20), ("f16", 300), ("f16", 530), ("f32", 300)])
+def test_offsets_beyond_32_bits(dt, M):
+    """Rows and adapters so far apart that offsets pass 2^31 elements."""
+    import dense_gemm_fp32_amd as dg
+    note("far apart %s %d" % (dt, M))
+    g, dtype = gen(M), DT[dt]
+    N, K, L, R = 72, 64, 3, 8
+    ld = max((1 << 31) // (M - 1) // 8 * 8, 1 << 23) + 64
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, K ** -0.5)
+    dY = normal(g, (M, N), dtype, 2.0 ** -6)
+    A, B, scale, _ = adapters(g, L, N, K, R, dtype, False)
+    rows = pattern(g, "segments", M, L)
+    gX, gY, gA = far_apart(X, ld), far_apart(dY, ld), far_apart(A, (1 << 30) + 64)
+    Y = far_apart(torch.zeros(M, N, dtype=dtype), ld)
+    rest = [t.to(GPU) for t in (W, B, rows, scale)]
+    dg.lora(gX, rest[0], gA, rest[1], rest[2], Y, scale=rest[3])
+    assert ref.worst(Y, *ref.lora(X, W, A, B, rows, None, scale, None, 1.0, 0)) <= 1.0
+    dX = far_apart(torch.zeros(M, K, dtype=dtype), ld)
+    dA, dB = torch.empty(L, R, K, device=GPU), torch.empty(L, N, R, device=GPU)
+    dg.lora_grad(gY, gX, rest[0], gA, rest[1], rest[2], dX=dX, dA=dA, dB=dB, scale=rest[3])
+    want = ref.lora_grad(dY, X, W, A, B, rows, None, None, None, scale, None, 1.0, 0, 0)
+    for n, t in (("dX", dX), ("dA", dA), ("dB", dB)):
+        assert ref.worst(t, *want[n]) <= 1.0, n
+
+
+@pytest.mark.parametrize("M", [3, 90])
+def test_experts_beyond_32_bits(M):
+    """Experts so far apart that offsets pass 2^31 elements."""
+    import dense_gemm_fp32_amd as dg
+    note("experts far apart %d" % M)
+    g, dtype = gen(M), torch.float16
+    D, F, E, k = 136, 72, 4, 2
+    X, router = normal(g, (M, D), dtype), normal(g, (E, D), dtype, 1.5 * D ** -0.5)
+    W1, W2 = normal(g, (E, 2 * F, D), dtype, D ** -0.5), normal(g, (E, D, F), dtype, F ** -0.5)
+    want, bound, ids, _, _ = ref.moe(X, router, W1, W2, k, None, True, 1.0, 0)
+    Y, gi = torch.empty(M, D, dtype=dtype, device=GPU), torch.empty(M, k, dtype=torch.int32,
+                                                                    device=GPU)
+    dg.moe(X.to(GPU), router.to(GPU), far_apart(W1, (1 << 30) + 40), far_apart(W2, (1 << 30) + 8),
+           k, Y, ids=gi)
+    assert torch.equal(gi.cpu().long(), ids)
+    assert ref.worst(Y, want, bound) <= 1.0
+
+
 def test_refusals_on_the_gpu():
     """A workspace that is too small or cannot be had is refused before any work."""
     import dense_gemm_fp32_amd as dg

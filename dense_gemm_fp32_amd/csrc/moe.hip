@@ -255,8 +255,10 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
 // ---------------------------------------------------------------- down and weighted sum
 
 // A row of H as fragments of T: for fp16, scaled by the row's power of two
-// and rounded to 11 bits (those of every value within 2^-28 of the row's
-// largest).
+// and held as two halves, 22 bits of every value within 2^-17 of the row's
+// largest (to 2^-39 of that below).  The low halves' instruction stands behind the
+// weights' loads: 343 us a call with and without it at 64 tokens of 4096, 32
+// experts of 2048, and 535 at 256 tokens.
 template <typename T, int NB>
 struct HiddenLoader;
 
@@ -274,14 +276,13 @@ struct HiddenLoader<_Float16, NB> {
   __device__ __forceinline__ Raw masked(int b, int k) const {
     return Raw{load_frag(row[b], k, lim), load_frag(row[b], k + 4, lim)};
   }
-  __device__ __forceinline__ f16x8 frag(int b, const Raw &r) const {
-    f16x8 f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = (_Float16)(r.a[j] * down[b]);
-      f[4 + j] = (_Float16)(r.b[j] * down[b]);
-    }
-    return f;
+  __device__ __forceinline__ Halves frag(int b, const Raw &r) const {
+    typedef float f32x8 __attribute__((ext_vector_type(8)));
+    const f32x8 h = f32x8{r.a[0], r.a[1], r.a[2], r.a[3], r.b[0], r.b[1], r.b[2], r.b[3]} * down[b];
+    const f16x8 hi = __builtin_convertvector(h, f16x8);
+    const f32x8 rest = h - __builtin_convertvector(hi, f32x8);
+    // an infinity's rest is a NaN
+    return Halves{hi, finite(__builtin_convertvector(rest, f16x8))};
   }
 };
 

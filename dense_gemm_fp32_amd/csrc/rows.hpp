@@ -42,6 +42,24 @@ __device__ __forceinline__ f32x4 mma16(f32x4 a, f32x4 b, f32x4 c) {
   return c;
 }
 
+// A row's values as two halves each: hi + lo holds 22 bits.
+struct Halves {
+  f16x8 hi, lo;
+};
+
+// The largest finite values in place of infinities, some finite value in place
+// of a NaN.
+__device__ __forceinline__ f16x8 finite(f16x8 v) {
+  const f16x8 top = (_Float16)65504.0f;
+  return __builtin_elementwise_max(__builtin_elementwise_min(v, top), -top);
+}
+
+// An infinity or NaN among the weights meets the high parts only: a low part,
+// of either sign or zero, would make a NaN of an infinity.
+__device__ __forceinline__ f32x4 mma16(f16x8 w, const Halves &x, f32x4 c) {
+  return mma16(finite(w), x.lo, mma16(w, x.hi, c));
+}
+
 // VEC consecutive elements at any element's address.  Global loads of 16
 // bytes need no more than the element's own alignment on this target, so rows
 // of any length, padding and offset take the same path; only the last, partly
@@ -114,7 +132,8 @@ __device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, i
 // acc[f][b] += W block f (16 rows, this lane's at w[f]) times activation block
 // b over k in [k0, k1).  Activations come from `x`: x.whole(b, kk) loads this
 // lane's values at kk = k + VEC * lane group, x.masked(b, kk) the same with 0
-// at and beyond this lane's end of the row, x.frag makes a fragment of them.
+// at and beyond this lane's end of the row, x.frag makes a fragment (or Halves)
+// of them.
 // Steps that end at or before `kw` are whole for every lane; `lim` is this
 // lane's end of the weights' rows.  The loads of U steps are issued together,
 // ahead of their products (the scheduling barrier keeps the compiler from
@@ -145,7 +164,7 @@ __device__ __forceinline__ void stream_steps(const T *const (&w)[NF], int k, con
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const Frag xf = x.frag(b, xr[u][b]);
+      const auto xf = x.frag(b, xr[u][b]);
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[u][f], xf, acc[f][b]);
     }
@@ -178,7 +197,7 @@ __device__ __forceinline__ void stream_mac(const T *const (&w)[NF], int k0, int 
     for (int f = 0; f < NF; ++f) wf[f] = load_frag(w[f], k + lk, lim);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const Frag xf = x.frag(b, x.masked(b, k + lk));
+      const auto xf = x.frag(b, x.masked(b, k + lk));
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[f], xf, acc[f][b]);
     }

@@ -802,3 +802,56 @@ def test_empty_products():
         dg.moe(s["Y"], s["router"], s["W1"], s["W2"], 2, s["Z"], alpha=0.0, beta=0.25)
         assert bool((s["Z"] == 1.0).all())
         dg.moe(s["Y"][:0], s["router"], s["W1"], s["W2"], 2, s["Z"][:0])
+
+
+def moe_of_differences(g, M, D, F, E, k, dtype=torch.float16):
+    """Inputs whose outputs are differences of two nearly equal hidden values:
+    X has eight numbers a row that are not zero, up row f + 1 is up row f but for
+    a step of fp16 or two, and each row of W2 holds +w and -w at such a pair."""
+    X = torch.zeros(M, D, dtype=dtype)
+    X[:, :8] = normal(g, (M, 8), dtype)
+    router = normal(g, (E, D), dtype, 0.5)
+    W1, W2 = normal(g, (E, 2 * F, D), dtype, 0.4), torch.zeros(E, D, F, dtype=dtype)
+    W1[:, 1:F:2] = W1[:, 0:F - 1:2]
+    W1[:, F + 1::2] = (W1[:, F:2 * F - 1:2].float() * (1 + 2.0 ** -9)).to(dtype)
+    at = 2 * torch.randint(0, F // 2, (E, D, 1), generator=g)
+    W2.scatter_(2, at, 1.0)
+    W2.scatter_(2, at + 1, -1.0)
+    return X, router, W1, W2
+
+
+@pytest.mark.parametrize("case", [(1, 8, 16, 4, 2), (1, 264, 300, 8, 2), (8, 72, 130, 4, 2),
+                                  (16, 520, 64, 16, 2), (40, 136, 258, 4, 2), (200, 264, 72, 5, 2)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_moe_hidden_values_keep_their_bits(case):
+    """silu(g)*u enters the second product in 22 bits.  Each output is a
+    difference that is 2^-9 of its two terms, whose own rounding to 11 bits
+    (2^-12 of a term on average) would stand out.
+
+    The bound: g and u are sums of 8 terms, 4*12*u of the magnitudes; silu's
+    slope is at most 1.1, and its value and the product add 16 u.  A value is
+    held as two halves: half a step of the low one, 2^-11 * 2^-11 of the value,
+    or 2^-25 where the row's largest is 2^14.  An output sums two terms a choice:
+    4*(2k + 4)*u of the magnitudes.  The weights' as in the reference."""
+    import dense_gemm_fp32_amd as dg
+    M, D, F, E, k = case
+    note("moe bits %r" % (case,))
+    X, router, W1, W2 = moe_of_differences(gen(M + F), M, D, F, E, k)
+    _, _, ids, w, dw = ref.moe(X, router, W1, W2, k, None, True, 1.0, 0)
+    U = ref.U32
+    out, bound = torch.zeros(M, D).double(), torch.zeros(M, D).double()
+    for t in range(M):
+        for j in range(k):
+            w1, w2, x = (v.double() for v in (W1[ids[t, j]], W2[ids[t, j]], X[t]))
+            h, dh = w1 @ x, 4 * 12 * U * (w1.abs() @ x.abs())
+            s, u = h[:F] * torch.sigmoid(h[:F]), h[F:]
+            a = s * u
+            da = 1.1 * dh[:F] * (u.abs() + dh[F:]) + s.abs() * dh[F:] + 16 * U * a.abs()
+            top = (a.abs() + da).max()
+            da = da + 2.0 ** -22 * (a.abs() + da) + 2.0 ** -39 * top
+            m = w2.abs() @ a.abs()
+            out[t] += w[t, j] * (w2 @ a)
+            bound[t] += w[t, j] * (w2.abs() @ da + 4 * (2 * k + 4) * U * m) + dw[t, j] * m
+    Y = torch.empty(M, D, dtype=torch.float16, device=GPU)
+    dg.moe(*(v.to(GPU) for v in (X, router, W1, W2)), k, Y)
+    assert ref.worst(Y, out, ref.stored(bound, out, torch.float16)) <= 1.0

@@ -79,7 +79,7 @@ Route route(int M, int N, int K, float alpha, float beta) {
 dgemm::Call make_call(int M, int N, int K, float alpha, const void *A, int lda, const void *B,
                       int ldb, float beta, void *C, int ldc, void *stream, bool out32 = false,
                       bool ta = false, bool tb = false) {
-  dgemm::Call c;
+  dgemm::Call c = {};
   c.out32 = out32;
   c.ta = ta;
   c.tb = tb;

@@ -906,3 +906,50 @@ def test_plans_match_the_committed_sweep_and_table():
         assert _short_plan(plan, False) == cells[-1], (name, plan, cells[-1])
         checked += 1
     assert checked >= 7, sorted(table)
+
+
+def test_plans_do_not_depend_on_the_stack(tmp_path):
+    """A plan is a function of the call's arguments: filling the stack below the
+    call with zeros, ones or any other byte first leaves its text unchanged.
+    Operands with 16-byte rows are not copied, whatever N is."""
+    import ctypes
+    import dense_gemm_fp32_amd as dg
+    from dense_gemm_fp32_amd import binding
+    src = tmp_path / "fill.c"
+    src.write_text("""
+        typedef int (*plan)(int, int, int, int, float, const void *, int, const void *, int, float,
+                            const void *, int, char *, int);
+        __attribute__((noinline)) static void fill(int byte) {
+          volatile char room[32768];
+          for (int i = 0; i < (int)sizeof room; ++i) room[i] = (char)byte;
+        }
+        int filled(plan f, int byte, int dtype, int M, int N, int K, const void *A, int lda,
+                   const void *B, int ldb, const void *C, int ldc, char *buf, int len) {
+          fill(byte);
+          return f(dtype, M, N, K, 1.0f, A, lda, B, ldb, 0.0f, C, ldc, buf, len);
+        }
+    """)
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", "-o", str(tmp_path / "fill.so"), str(src)],
+                   check=True)
+    fn = ctypes.CDLL(str(tmp_path / "fill.so")).filled
+    P, I = ctypes.c_void_p, ctypes.c_int
+    fn.argtypes = [P, I, I, I, I, I, P, I, P, I, P, I, ctypes.c_char_p, I]
+    describe = ctypes.cast(binding._lib.gemm_describe, P)
+    before = dg.gemm_set_pack(0)
+    try:
+        for pack, dtypes in ((0, (0, 1, 2)), (2, (0, 1, 2))):
+            dg.gemm_set_pack(pack)
+            for dtype in dtypes:
+                for M, N, K in ((2000, 2001, 2000), (1000, 3001, 1000), (4096, 4095, 4096),
+                                (512, 512, 512), (100, 33, 70)):
+                    lda, ldb = (K + 7) // 8 * 8, (N + 7) // 8 * 8
+                    texts = set()
+                    for byte in (0, 1, 0x7f, 0xff):
+                        buf = ctypes.create_string_buffer(256)
+                        assert fn(describe, byte, dtype, M, N, K, FAKE, lda, FAKE, ldb, FAKE, ldb,
+                                  buf, 256) == 0
+                        texts.add(buf.value.decode())
+                    assert len(texts) == 1, (dtype, M, N, K, texts)
+                    assert "copies" not in texts.pop()
+    finally:
+        dg.gemm_set_pack(before)

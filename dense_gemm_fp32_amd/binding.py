@@ -403,7 +403,8 @@ def _kind(X):
 def _call_rows(fn, dev, stream, workspace, need, args):
     """Run entry point `fn` on the current stream of GPU `dev` or the one given.
     Without a workspace, one comes from torch's allocator on the current
-    stream, or from the library's pool on a stream that was given."""
+    stream, or from the library's pool on a stream that was given (unless it is
+    the current one and is being captured: then from torch's allocator too)."""
     if dev != _current_device():      # a default stream means the current GPU's
         with torch.cuda.device(dev):
             return _call_rows(fn, dev, stream, workspace, need, args)
@@ -413,7 +414,9 @@ def _call_rows(fn, dev, stream, workspace, need, args):
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on GPU %d" % dev)
         ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif stream is None:
+    elif stream is None or (torch.cuda.is_initialized()
+                            and torch.cuda.is_current_stream_capturing()
+                            and _stream(stream) == _current_stream(dev)):
         workspace = torch.empty(need, dtype=torch.uint8, device=_device(dev))
         ws, size = workspace.data_ptr(), need
     else:

@@ -304,7 +304,7 @@ const char *gemm_status_string(int status) {
     case -10: return "invalid argument 10: C is NULL";
     case -11: return "invalid argument 11: ldc < max(1, N) (row-major) or max(1, M) (column-major)";
     case GEMM_ERR_SCRATCH_LIMIT: return "gemm_f32_noalloc: the call's workspace (split K) would exceed the library's fixed scratch region (64 MiB); nothing was enqueued";
-    case GEMM_ERR_NO_WORKSPACE: return "the call's workspace could not be had from the library's pool (gemm_set_workspace_limit, or out of memory); nothing was enqueued";
+    case GEMM_ERR_NO_WORKSPACE: return "the call's workspace could not be had from the library's pool (gemm_set_workspace_limit, a stream that is being captured, or out of memory); nothing was enqueued";
     case -101: return "invalid probe argument 1: dtype is not 0 (fp32) or 1 (fp16)";
     case -102: return "invalid probe argument 2: iters < 1";
     case -103: return "invalid probe argument 3: operands is NULL";

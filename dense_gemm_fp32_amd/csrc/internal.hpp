@@ -150,6 +150,8 @@ struct SplitReduce {
 // launcher that cannot get its workspace runs the call unsplit.
 hipError_t workspace_alloc(const Call &c, size_t bytes, void **ptr);
 hipError_t workspace_free(const Call &c, void *ptr);
+// Whether work on `s` is being captured into a graph.
+bool capturing(hipStream_t s);
 
 // Bytes of a whole split-K workspace (S slabs of M x ceil(N/4)*4 floats) and
 // of a last-round split (S dense BM x BN fp32 blocks per leftover tile).

@@ -16,7 +16,10 @@ bool bad_size(int n) { return n < 0 || n > GEMM_ROWS_MAX_SIZE; }
 
 // A workspace of `bytes` for one call on `stream`: the caller's, or one from
 // the library's pool, given back in stream order by close().  A caller's that
-// is not 256-byte aligned gives status `base`, one too small `base` - 1.
+// is not 256-byte aligned gives status `base`, one too small `base` - 1.  A
+// stream that is being captured gets none from the pool: it would become an
+// allocation node of the graph, and graphs of such calls have faulted when two
+// were alive and replayed in turn.
 class Space {
  public:
   int open(void *given, size_t given_bytes, size_t bytes, hipStream_t stream, int base) {
@@ -27,8 +30,7 @@ class Space {
       ptr_ = given;
       return 0;
     }
-    pool_.ws_fixed = nullptr;
-    pool_.ws_fixed_bytes = 0;
+    if (dgemm::capturing(stream)) return GEMM_ERR_NO_WORKSPACE;
     pool_.ws_limit = dgemm::workspace_limit();
     pool_.stream = stream;
     if (dgemm::workspace_alloc(pool_, bytes, &ptr_) != hipSuccess) return GEMM_ERR_NO_WORKSPACE;

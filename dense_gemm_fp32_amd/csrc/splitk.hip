@@ -390,6 +390,16 @@ hipError_t workspace_alloc(const Call &c, size_t bytes, void **ptr) {
   return e;
 }
 
+bool capturing(hipStream_t s) {
+  if (s == nullptr) return false;   // cannot be captured
+  hipStreamCaptureStatus now = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(s, &now) != hipSuccess) {
+    (void)hipGetLastError();
+    return false;
+  }
+  return now != hipStreamCaptureStatusNone;
+}
+
 hipError_t workspace_free(const Call &c, void *ptr) {
   if (ptr == nullptr || c.ws_fixed != nullptr) return hipSuccess;
   return hipFreeAsync(ptr, c.stream);

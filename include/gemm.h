@@ -99,7 +99,11 @@
  *   - Calls may be captured into a HIP graph on a capturing stream (no
  *     memset is enqueued; the workspace of a split or operand-copying call
  *     becomes the graph's allocation node); replays repeat the captured
- *     arguments and choice.
+ *     arguments and choice.  Two live graphs with allocation nodes of this
+ *     library, replayed one behind the other, have faulted the GPU once, and
+ *     the cause is not known: where several such graphs are kept, capture
+ *     calls that allocate nothing (gemm_f32_noalloc, or any call while
+ *     gemm_set_workspace_limit is 0).
  *   - The library keeps no per-call state, so calls are thread-safe and
  *     reentrant; the only process-wide state is the workspace pools and the
  *     diagnostic switches at the end of this header (default off).
@@ -315,8 +319,9 @@ int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int l
  * call's alone until its work on `stream` is done; NULL takes it from the
  * library's pool in stream order (gemm_set_workspace_limit applies;
  * GEMM_ERR_NO_WORKSPACE if it cannot be had, nothing enqueued).  Nothing in it
- * needs an initial value, and a call with a workspace allocates nothing: use one
- * for calls that are captured into a graph.
+ * needs an initial value, and a call with a workspace allocates nothing.  Calls
+ * that are captured into a graph need one: on a capturing stream NULL gives
+ * GEMM_ERR_NO_WORKSPACE.
  *
  * Status: 0; a positive hipError_t; or for invalid argument i (from 1, in
  * signature order) -300-i (gemm_lora_*), -400-i (gemm_lora_grad_*), -500-i

@@ -855,3 +855,46 @@ def test_moe_hidden_values_keep_their_bits(case):
     Y = torch.empty(M, D, dtype=torch.float16, device=GPU)
     dg.moe(*(v.to(GPU) for v in (X, router, W1, W2)), k, Y)
     assert ref.worst(Y, out, ref.stored(bound, out, torch.float16)) <= 1.0
+
+
+def test_captured_calls_without_a_workspace():
+    """A capturing stream gets no workspace from the library's pool: such a call is
+    refused and adds nothing to the graph.  The wrappers take one from torch."""
+    import dense_gemm_fp32_amd as dg
+    note("captured without a workspace")
+    s = step_state(71)
+    M, N, K, L, R, E, F = 40, 128, 96, 3, 8, 6, 64
+    three_calls(dg, s)
+    want = snapshot(s)
+    one = torch.zeros(1, device=GPU)
+    for n in OUT:
+        s[n].fill_(7)
+    torch.cuda.synchronize()
+    refused, taken = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(refused):
+        at = torch.cuda.current_stream()
+        for rc in (dg.gemm_lora_f16(M, N, K, 1.0, s["X"], K, s["W"], K, 0.0, s["Y"], N, L, R,
+                                    s["A"], K, R * K, s["B"], R, N * R, s["scale"], None,
+                                    s["rows"], None, 0, at),
+                   dg.gemm_lora_grad_f16(M, N, K, 1.0, s["Z"], N, s["X"], K, s["W"], K, L, R,
+                                         s["A"], K, R * K, s["B"], R, N * R, s["scale"], None,
+                                         s["rows"], 0.0, s["dX"], K, 0.0, s["dA"], K, R * K,
+                                         s["dB"], R, N * R, None, 0, at),
+                   dg.gemm_moe_f16(M, N, F, E, 2, 1, 1.0, s["Y"], N, s["router"], N, s["W1"], N,
+                                   2 * F * N, s["W2"], F, N * F, 0.0, s["Z"], N, s["ids"], None,
+                                   None, 0, at)):
+            assert rc == dg.GEMM_ERR_NO_WORKSPACE
+        one.add_(1.0)
+    with torch.cuda.graph(taken):
+        dg.lora(s["X"], s["W"], s["A"], s["B"], s["rows"], s["Y"], scale=s["scale"],
+                stream=torch.cuda.current_stream())
+    for turn in range(3):
+        refused.replay()
+        torch.cuda.synchronize()
+        assert float(one) == turn + 1
+        assert all(bool((s[n] == 7).all()) for n in OUT)
+    for turn in range(3):
+        taken.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s["Y"], want["Y"])
+        s["Y"].fill_(7)

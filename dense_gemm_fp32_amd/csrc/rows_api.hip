@@ -48,6 +48,36 @@ class Space {
 
 int status(hipError_t e) { return e == hipSuccess ? GEMM_SUCCESS : (int)e; }
 
+// The product of a call without adapters, A op(B), as gemm_* would run it: its
+// copies and K parts take the caller's workspace as far as that reaches, or the
+// library's pool where the caller gave none and the stream is not being captured.
+hipError_t shared_product(bool half, bool tb, int M, int N, int K, float alpha, const void *A,
+                          int lda, const void *B, int ldb, float beta, void *C, int ldc, void *ws,
+                          size_t ws_bytes, hipStream_t stream) {
+  dgemm::Call c = {};
+  c.M = M;
+  c.N = N;
+  c.K = K;
+  c.alpha = alpha;
+  c.beta = beta;
+  c.A = A;
+  c.lda = lda;
+  c.B = B;
+  c.ldb = ldb;
+  c.C = C;
+  c.ldc = ldc;
+  c.tb = tb;
+  c.splits = 1;
+  c.stream = stream;
+  if (ws != nullptr) {
+    c.ws_fixed = ws;
+    c.ws_fixed_bytes = dgemm::aligned_to(ws, 256) ? ws_bytes : 0;
+  } else {
+    c.ws_limit = dgemm::capturing(stream) ? 0 : dgemm::workspace_limit();
+  }
+  return half ? dgemm::launch_f16(c) : dgemm::launch_f32(c);
+}
+
 int lora(bool half, int M, int N, int K, float alpha, const void *X, int ldx, const void *W,
          int ldw, float beta, void *Y, int ldy, int L, int R, const void *A, int lda,
          long long stride_a, const void *B, int ldb, long long stride_b, const float *scale,
@@ -79,12 +109,8 @@ int lora(bool half, int M, int N, int K, float alpha, const void *X, int ldx, co
     return status(half ? dgemm::launch_scale_f16(M, N, beta, static_cast<uint16_t *>(Y), ldy, s)
                        : dgemm::launch_scale_f32(M, N, beta, static_cast<float *>(Y), ldy, s));
   if (!adapters)
-    return half ? gemm_f16_nt(M, N, K, alpha, static_cast<const gemm_half_t *>(X), ldx,
-                              static_cast<const gemm_half_t *>(W), ldw, beta,
-                              static_cast<gemm_half_t *>(Y), ldy, stream)
-                : gemm_f32_nt(M, N, K, alpha, static_cast<const float *>(X), ldx,
-                              static_cast<const float *>(W), ldw, beta, static_cast<float *>(Y),
-                              ldy, stream);
+    return status(shared_product(half, true, M, N, K, alpha, X, ldx, W, ldw, beta, Y, ldy, ws,
+                                 ws_bytes, s));
   LoraCall c = {};
   c.half = half;
   c.M = M;
@@ -167,12 +193,8 @@ int lora_grad(bool half, int M, int N, int K, float alpha, const void *dY, int l
   if (adapters && B == nullptr && (want_x || want_a)) return -416;
   if (adapters && rows == nullptr) return -421;
   if (!adapters)
-    return half ? gemm_f16(M, K, N, alpha, static_cast<const gemm_half_t *>(dY), lddy,
-                           static_cast<const gemm_half_t *>(W), ldw, beta_x,
-                           static_cast<gemm_half_t *>(dX), lddx, stream)
-                : gemm_f32(M, K, N, alpha, static_cast<const float *>(dY), lddy,
-                           static_cast<const float *>(W), ldw, beta_x, static_cast<float *>(dX),
-                           lddx, stream);
+    return status(shared_product(half, false, M, K, N, alpha, dY, lddy, W, ldw, beta_x, dX, lddx,
+                                 ws, ws_bytes, s));
   LoraCall c = {};
   c.half = half;
   c.M = M;

@@ -349,6 +349,8 @@ int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int l
  *   L, R      adapters (0 .. GEMM_LORA_MAX_ADAPTERS) and the rank their
  *             storage has room for (0 .. GEMM_LORA_MAX_RANK); either 0: no
  *             adapter term
+ *             (the product alone, which needs no workspace and runs as
+ *             gemm_*_nt does with what it is given)
  *   A, lda, stride_a   adapter a's R x K matrix at A + a*stride_a, lda >= max(1, K)
  *   B, ldb, stride_b   its N x R matrix at B + a*stride_b, ldb >= max(1, R)
  *   scale     device, L floats (NULL: 1)

@@ -898,3 +898,60 @@ def test_captured_calls_without_a_workspace():
         torch.cuda.synchronize()
         assert torch.equal(s["Y"], want["Y"])
         s["Y"].fill_(7)
+
+
+def node_kinds(graph):
+    """The node types of a captured torch graph (made with keep_graph)."""
+    import ctypes
+    from dense_gemm_fp32_amd import binding
+    raw, n = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert binding._lib.hipGraphGetNodes(raw, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * max(n.value, 1))()
+    assert binding._lib.hipGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
+    kinds = []
+    for node in nodes[:n.value]:
+        kind = ctypes.c_int(-1)
+        assert binding._lib.hipGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        kinds.append(kind.value)
+    return kinds
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_captured_products_without_adapters(dt):
+    """A call without adapters takes its copies and K parts from the caller's
+    workspace, or does without on a capturing stream: its graph holds kernels
+    only, and replays within the bound (with room enough the eager bits)."""
+    import dense_gemm_fp32_amd as dg
+    note("captured products without adapters " + dt)
+    g, dtype = gen(77), DT[dt]
+    M, N, K = 1000, 1000, 1031                 # rows of no alignment
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, K ** -0.5)
+    dY = normal(g, (M, N), dtype, 2.0 ** -6)
+    rows = torch.zeros(M, dtype=torch.int32)
+    want = ref.lora(X, W, X[:0].reshape(0, 4, K), W[:0].reshape(0, N, 4), rows, None, None, None,
+                    1.0, 0)
+    wantX = ref.lora_grad(dY, X, W, X[:0].reshape(0, 4, K), W[:0].reshape(0, N, 4), rows, None,
+                          None, None, None, None, 1.0, 0, 0)["dX"]
+    gX, gW, gY, gr = (t.to(GPU) for t in (X, W, dY, rows))
+    for L, R in ((0, 4), (3, 0)):
+        A = torch.empty(L, R, K, dtype=dtype, device=GPU)
+        B = torch.empty(L, N, R, dtype=dtype, device=GPU)
+        eager, eagerX = (torch.empty(M, n, dtype=dtype, device=GPU) for n in (N, K))
+        dg.lora(gX, gW, A, B, gr, eager)
+        dg.lora_grad(gY, gX, gW, A, B, gr, dX=eagerX)
+        for room in (None, 256, 64 << 20):
+            ws = None if room is None else torch.full((room,), 0xFF, dtype=torch.uint8, device=GPU)
+            Y, dX = torch.empty_like(eager), torch.empty_like(eagerX)
+            graph = torch.cuda.CUDAGraph(keep_graph=True)
+            with torch.cuda.graph(graph):
+                dg.lora(gX, gW, A, B, gr, Y, workspace=ws)
+                dg.lora_grad(gY, gX, gW, A, B, gr, dX=dX, workspace=ws)
+            assert set(node_kinds(graph)) == {0}, room       # 0: a kernel
+            for _ in range(3):
+                Y.fill_(float("nan"))
+                dX.fill_(float("nan"))
+                graph.replay()
+                torch.cuda.synchronize()
+                assert ref.worst(Y, *want) <= 1.0 and ref.worst(dX, *wantX) <= 1.0
+                if room == 64 << 20:
+                    assert torch.equal(Y, eager) and torch.equal(dX, eagerX)

@@ -77,8 +77,13 @@ __global__ __launch_bounds__(256) void moe_logits(const T *X, int ldx, const T *
   }
 }
 
-// A NaN logit ranks below every number.
+// A NaN logit weighs what minus infinity does, and ranks below it.
 __device__ __forceinline__ double logit_key(double l) { return l == l ? l : -__builtin_inf(); }
+
+// Whether expert j with logit a comes before expert e with logit b.
+__device__ __forceinline__ bool logit_before(double a, int j, double b, int e) {
+  return a > b || (b != b && a == a) || ((a == b || (a != a && b != b)) && j < e);
+}
 
 struct MoeParams {
   const void *X, *W1, *W2;
@@ -125,7 +130,7 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
 #pragma unroll
     for (int i = 0; i < TB; ++i) {
       l[i] = p.logits + (size_t)(t0 + i < p.M ? t0 + i : p.M - 1) * p.E;
-      mine[i] = logit_key(l[i][e]);
+      mine[i] = l[i][e];
       larger[i] = 0;
     }
     for (int j0 = 0; j0 < p.E; j0 += kWave) {
@@ -134,10 +139,8 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
 #pragma unroll
       for (int i = 0; i < TB; ++i) v[i] = l[i][j < p.E ? j : p.E - 1];
 #pragma unroll
-      for (int i = 0; i < TB; ++i) {
-        const double k = logit_key(v[i]);
-        larger[i] += __popcll(__ballot(j < p.E && (k > mine[i] || (k == mine[i] && j < e))));
-      }
+      for (int i = 0; i < TB; ++i)
+        larger[i] += __popcll(__ballot(j < p.E && logit_before(v[i], j, mine[i], e)));
     }
 #pragma unroll
     for (int i = 0; i < TB; ++i)

@@ -955,3 +955,28 @@ def test_captured_products_without_adapters(dt):
                 assert ref.worst(Y, *want) <= 1.0 and ref.worst(dX, *wantX) <= 1.0
                 if room == 64 << 20:
                     assert torch.equal(Y, eager) and torch.equal(dX, eagerX)
+
+
+def test_moe_nan_logits_come_last():
+    """A NaN logit ranks below every number, minus infinity among them."""
+    import dense_gemm_fp32_amd as dg
+    for dt in ("f16", "f32"):
+        note("moe nan logits " + dt)
+        g, dtype = gen(14), DT[dt]
+        M, D, F, E = 5, 40, 24, 70
+        X, router = normal(g, (M, D), dtype), normal(g, (E, D), dtype, 0.2)
+        X[:, 0] = 1.0
+        router[[0, 65]], router[[1, 64, 69], 0] = float("nan"), -float("inf")
+        W1, W2 = normal(g, (E, 2 * F, D), dtype, 0.1), normal(g, (E, D, F), dtype, 0.1)
+        order = (X[0].double() @ router.double().t()).nan_to_num(-1e300, neginf=-1e200)
+        for k in (1, 64):
+            gi, gw = (torch.empty(M, k, dtype=t, device=GPU) for t in (torch.int32, torch.float32))
+            Y = torch.empty(M, D, dtype=dtype, device=GPU)
+            dg.moe(*(t.to(GPU) for t in (X, router, W1, W2)), k, Y, ids=gi, weights=gw)
+            assert gi[0].tolist() == sorted(range(E), key=lambda e: (-float(order[e]), e))[:k]
+            assert bool(Y.isfinite().all()) and bool(gw.isfinite().all())
+        few = router[[0, 1, 2, 65, 64, 3]]
+        gi = torch.empty(M, 6, dtype=torch.int32, device=GPU)
+        Y = torch.empty(M, D, dtype=dtype, device=GPU)
+        dg.moe(*(t.to(GPU) for t in (X, few, W1[:6], W2[:6])), 6, Y, ids=gi)
+        assert gi[:, 2:].tolist() == [[1, 4, 0, 3]] * M and bool(Y.isfinite().all())

@@ -91,7 +91,7 @@ struct MoeParams {
   float *prob;            // M x k: each choice's exp(l - max), over their sum unless renorm
   int *count, *list;      // tokens of expert e; their pairs t*k + choice: list[e*M ..]
   float *H;               // M*k x F
-  unsigned *top;          // M*k: bits of the largest |H| of the row
+  unsigned *top;          // M*k: bits of the largest finite |H| of the row
   float *O;               // M*k x D (many tokens only)
   void *Y;
   int *ids;
@@ -241,7 +241,8 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
         const int pair = pairs[i < n ? i : n - 1];
         if (ok) p.H[(size_t)pair * p.F + f0 + r] = h;
         if constexpr (sizeof(T) == 2) {
-          unsigned m = ok ? __builtin_bit_cast(unsigned, fabsf(h)) : 0u;
+          unsigned m = __builtin_bit_cast(unsigned, fabsf(h));
+          m = ok && m < 0x7f800000u ? m : 0u;
 #pragma unroll
           for (int o = RG / 2; o > 0; o >>= 1) {
             const unsigned v = __shfl_xor(m, o);

@@ -231,9 +231,10 @@ struct RowLoader {
   __device__ __forceinline__ Raw frag(int, const Raw &r) const { return r; }
 };
 
-// Power of two that brings a row whose largest magnitude has these bits to
-// [2^14, 2^15) as fp16, and its inverse (1 for a row of zeros, infinities or
-// NaN); its exponent, at least -100.
+// Exponent of the power of two that a row is divided by so that its largest
+// finite magnitude, of these bits, comes to [2^14, 2^15) as fp16 (at least -100;
+// 0 for a row without a normal number): what is not finite must not decide it,
+// or the finite values beside an infinity would become infinities themselves.
 __device__ __forceinline__ int row_exponent(unsigned bits) {
   const int e = (int)(bits >> 23);
   if (e == 0 || e == 255) return 0;

@@ -451,9 +451,9 @@ size_t gemm_lora_grad_workspace(int dtype, int M, int N, int K, int L, int R);
  *   ids, weights       device, M x top_k, dense: the experts chosen (int) and
  *                      w (float); either may be NULL
  * Logits are summed in 64 bits, since which expert a token takes hangs on
- * their order; a NaN logit ranks below every number and weighs nothing.  silu(g) * u is formed in
- * fp32; in fp16 calls it enters the second product in 22 bits (what is below
- * 2^-17 of its row's largest: to 2^-39 of that).
+ * their order; a NaN logit ranks below every number and weighs nothing.
+ * silu(g) * u is formed in fp32; in fp16 calls it enters the second product in
+ * 22 bits (what is below 2^-17 of its row's largest: to 2^-39 of that).
  * Weights of experts that no token chose are not read.  alpha == 0:
  * Y := beta * Y, nothing else is read or written (ids and weights included).
  */

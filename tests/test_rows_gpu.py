@@ -980,3 +980,34 @@ def test_moe_nan_logits_come_last():
         Y = torch.empty(M, D, dtype=dtype, device=GPU)
         dg.moe(*(t.to(GPU) for t in (X, few, W1[:6], W2[:6])), 6, Y, ids=gi)
         assert gi[:, 2:].tolist() == [[1, 4, 0, 3]] * M and bool(Y.isfinite().all())
+
+
+def same_values(got, want):
+    """Equal patterns of NaN and of each infinity, whatever the finite values."""
+    got, want = got.double().cpu(), want.double()
+    return torch.equal(got.isnan(), want.isnan()) \
+        and torch.equal(got == float("inf"), want == float("inf")) \
+        and torch.equal(got == -float("inf"), want == -float("inf"))
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_moe_keeps_infinities(dt):
+    """An infinity in W1 makes one hidden value infinite beside others beyond
+    fp16's range, one in W2 meets finite ones: both stay infinities of their sign."""
+    import dense_gemm_fp32_amd as dg
+    for M, D, F, E, k in ((2, 64, 96, 4, 2), (40, 72, 64, 4, 2), (200, 40, 130, 3, 2)):
+        note("moe inf %s %d" % (dt, M))
+        g, dtype = gen(M), DT[dt]
+        X, router = normal(g, (M, D), dtype, 8.0), normal(g, (E, D), dtype, 0.02)
+        W1, W2 = normal(g, (E, 2 * F, D), dtype, 16.0), normal(g, (E, D, F), dtype, 2.0 ** -10)
+        W2 += torch.where(W2 < 0, -2.0 ** -12, 2.0 ** -12).to(dtype)
+        X[:, 3] = torch.where(X[:, 3] < 0, -1.0, 1.0).to(dtype)
+        W1[0, 5], W1[1, 11] = W1[0, 5].sign() / 64, W1[1, 11].sign() / 64   # small g
+        W1[0, F + 5, 3] = float("inf")
+        W2[1, 7, 11] = -float("inf")
+        want, bound, ids, _, _ = ref.moe(X, router, W1, W2, k, None, False, 1.0, 0)
+        Y = torch.empty(M, D, dtype=dtype, device=GPU)
+        gi = torch.empty(M, k, dtype=torch.int32, device=GPU)
+        dg.moe(*(t.to(GPU) for t in (X, router, W1, W2)), k, Y, renorm=False, ids=gi)
+        assert torch.equal(gi.cpu().long(), ids)
+        assert same_values(Y, want), M

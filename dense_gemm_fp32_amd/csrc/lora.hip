@@ -539,7 +539,7 @@ __global__ __launch_bounds__(256) void lora_shrink_sum(TileShrinkParams p) {
       const float *s = j.S + (size_t)row * p.Rp + r;
       for (int u = 0; u < used; ++u) v[q] += s[(size_t)u * p.M * p.Rp];
     }
-    top = fmaxf(top, fabsf(v[q]));
+    top = fmaxf(top, __builtin_isfinite(v[q]) ? fabsf(v[q]) : 0.0f);
     if (j.V && r < p.Rp) j.V[(size_t)row * p.Rp + r] = v[q];
   }
   if (!j.split) return;

@@ -237,7 +237,7 @@ struct RowLoader {
 // or the finite values beside an infinity would become infinities themselves.
 __device__ __forceinline__ int row_exponent(unsigned bits) {
   const int e = (int)(bits >> 23);
-  if (e == 0 || e == 255) return 0;
+  if (e == 0) return 0;
   return e - 141 > -100 ? e - 141 : -100;
 }
 

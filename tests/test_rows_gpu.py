@@ -1011,3 +1011,29 @@ def test_moe_keeps_infinities(dt):
         dg.moe(*(t.to(GPU) for t in (X, router, W1, W2)), k, Y, renorm=False, ids=gi)
         assert torch.equal(gi.cpu().long(), ids)
         assert same_values(Y, want), M
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("size", [(20, 200, 256, 4, 16), (400, 200, 256, 4, 16),
+                                  (700, 200, 256, 4, 16), (1100, 264, 136, 30, 20)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_infinite_intermediates_keep_their_sign(dt, size):
+    """A row whose A x holds an infinity beside numbers beyond fp16's range: the
+    result is the infinity of that sign."""
+    import dense_gemm_fp32_amd as dg
+    M, N, K, L, R = size
+    note("infinite intermediates %s %r" % (dt, size))
+    g, dtype = gen(M + K), DT[dt]
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, 0.1)
+    A, B, scale, _ = adapters(g, L, N, K, R, dtype, False)
+    A[1::2] *= 2.0 ** 14
+    B[1::2] += torch.where(B[1::2] < 0, -0.25, 0.25).to(dtype)      # no zeros
+    X[:, 5] = torch.where(X[:, 5] < 0, -1.0, 1.0).to(dtype)
+    A[1::2, 3, 5] = float("inf")
+    rows = pattern(g, "mixed", M, L)
+    want, bound = ref.lora(X, W, A, B, rows, None, scale, None, 1.0, 0)
+    assert want.isinf().any() and not want.isnan().any()
+    Y = torch.empty(M, N, dtype=dtype, device=GPU)
+    dg.lora(*(t.to(GPU) for t in (X, W, A, B, rows)), Y, scale=scale.to(GPU))
+    assert same_values(Y, want)
+    assert ref.worst(Y, want, bound) <= 1.0

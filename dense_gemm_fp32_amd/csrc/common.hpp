@@ -149,6 +149,12 @@ __device__ __forceinline__ float f16_bits_to_f32(uint16_t b) {
   return (float)__builtin_bit_cast(_Float16, b);
 }
 
+// The largest finite values in place of infinities, some finite value in place
+// of a NaN.
+__device__ __forceinline__ f16x8 finite(f16x8 v) {
+  const f16x8 top = (_Float16)65504.0f;
+  return __builtin_elementwise_max(__builtin_elementwise_min(v, top), -top);
+}
 
 // ---------------------------------------------------------------- pipeline helpers
 

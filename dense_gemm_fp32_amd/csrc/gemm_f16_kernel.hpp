@@ -616,26 +616,22 @@ __device__ __forceinline__ bool not_finite(_Float16 u) {
   return (__builtin_bit_cast(uint16_t, u) & 0x7c00u) == 0x7c00u;
 }
 
-// The finite values, zeros for the others; and the other way round.
+// The finite values and, with the top bit of their exponent cleared, the others:
+// 1 of an infinity's sign, so that an infinity of V that meets one of U is one
+// of the product's sign here already, and not a NaN.
 __device__ __forceinline__ f16x8 low_rank_finite(f16x8 u) {
+  u32x4 w = __builtin_bit_cast(u32x4, u);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) u[e] = not_finite(u[e]) ? (_Float16)0.0f : u[e];
-  return u;
+  for (int e = 0; e < 4; ++e)   // an exponent of ones carries into the sign's place
+    w[e] &= ~((((w[e] & 0x7c007c00u) + 0x04000400u) & 0x80008000u) >> 1);
+  return __builtin_bit_cast(f16x8, w);
 }
+
+// The values that are not finite, zeros for the others.
 __device__ __forceinline__ f16x8 low_rank_odd(f16x8 u) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) u[e] = not_finite(u[e]) ? u[e] : (_Float16)0.0f;
   return u;
-}
-
-// Infinities as the largest finite values of their sign.
-__device__ __forceinline__ f16x8 low_rank_clamp(f16x8 v) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint16_t b = __builtin_bit_cast(uint16_t, v[e]);
-    v[e] = (b & 0x7fffu) == 0x7c00u ? __builtin_bit_cast(_Float16, (uint16_t)(b - 1)) : v[e];
-  }
-  return v;
 }
 
 // The low-rank term: row i, column n gets scale[i] * sum_r V[i, r] U_a[n, r]
@@ -648,7 +644,7 @@ __device__ __forceinline__ f16x8 low_rank_clamp(f16x8 v) {
 // zeroed against that adapter's U (rank 64: two steps of 64 k beside the K/64
 // of the product).  Zeroed rows must not meet an infinity or NaN of U, which
 // would make them NaN: U passes through registers on its way, where such values
-// become zeros and are noted.
+// become 1 or -1 and are noted.
 //
 // LowRankTerm adds what was left while the accumulators are staged for the
 // stores, 16 rows by 32 columns at a time, keeping by selection the rows that
@@ -897,7 +893,7 @@ struct LowRankTerm {
         const _Float16 *u0 = static_cast<const _Float16 *>(t.U) + (size_t)a * (size_t)t.stride;
         for (int r = 0; r < rk; r += 16) {
           f16x8 vf = *reinterpret_cast<const f16x8 *>(v + 2 * r);
-          if (rw < kWhole) vf = low_rank_clamp(vf);
+          if (rw < kWhole) vf = finite(vf);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             int n = c0 + n0 + 16 * b + li;

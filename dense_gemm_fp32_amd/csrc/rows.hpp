@@ -47,13 +47,6 @@ struct Halves {
   f16x8 hi, lo;
 };
 
-// The largest finite values in place of infinities, some finite value in place
-// of a NaN.
-__device__ __forceinline__ f16x8 finite(f16x8 v) {
-  const f16x8 top = (_Float16)65504.0f;
-  return __builtin_elementwise_max(__builtin_elementwise_min(v, top), -top);
-}
-
 // An infinity or NaN among the weights meets the high parts only: a low part,
 // of either sign or zero, would make a NaN of an infinity.
 __device__ __forceinline__ f32x4 mma16(f16x8 w, const Halves &x, f32x4 c) {

@@ -1018,8 +1018,8 @@ def test_moe_keeps_infinities(dt):
                                   (700, 200, 256, 4, 16), (1100, 264, 136, 30, 20)],
                          ids=lambda c: "x".join(map(str, c)))
 def test_infinite_intermediates_keep_their_sign(dt, size):
-    """A row whose A x holds an infinity beside numbers beyond fp16's range: the
-    result is the infinity of that sign."""
+    """A row whose A x holds an infinity beside numbers beyond fp16's range, and
+    one that meets an infinity in B: the result is the infinity of that sign."""
     import dense_gemm_fp32_amd as dg
     M, N, K, L, R = size
     note("infinite intermediates %s %r" % (dt, size))
@@ -1031,9 +1031,12 @@ def test_infinite_intermediates_keep_their_sign(dt, size):
     X[:, 5] = torch.where(X[:, 5] < 0, -1.0, 1.0).to(dtype)
     A[1::2, 3, 5] = float("inf")
     rows = pattern(g, "mixed", M, L)
-    want, bound = ref.lora(X, W, A, B, rows, None, scale, None, 1.0, 0)
-    assert want.isinf().any() and not want.isnan().any()
-    Y = torch.empty(M, N, dtype=dtype, device=GPU)
-    dg.lora(*(t.to(GPU) for t in (X, W, A, B, rows)), Y, scale=scale.to(GPU))
-    assert same_values(Y, want)
-    assert ref.worst(Y, want, bound) <= 1.0
+    for both in (False, True):
+        if both:
+            B[1::4, 7, 3], B[3::4, 8, 3] = -float("inf"), float("inf")
+        want, bound = ref.lora(X, W, A, B, rows, None, scale, None, 1.0, 0)
+        assert want.isinf().any() and not want.isnan().any()
+        Y = torch.empty(M, N, dtype=dtype, device=GPU)
+        dg.lora(*(t.to(GPU) for t in (X, W, A, B, rows)), Y, scale=scale.to(GPU))
+        assert same_values(Y, want)
+        assert ref.worst(Y, want, bound) <= 1.0

@@ -715,6 +715,14 @@ __device__ __forceinline__ u32x4 low_rank_piece(const GemmParams &p, const LowRa
                                          : low_rank_load(u + (size_t)r * (size_t)t.ldu, n, p.N));
 }
 
+// Room for the steps in LDS, and the tile's scales behind them.
+template <class T>
+constexpr int kStepRoom = kStartAdapters * (256 / (T::BK / 2));
+template <class T>
+__device__ __forceinline__ float *low_rank_scales(int2 *steps) {
+  return reinterpret_cast<float *>(steps + kStepRoom<T>);
+}
+
 // The steps to run, as (adapter, first rank + 256 times its number in the tile)
 // in `steps` (LDS), apart from the accumulators' loop so that one plain loop is
 // all that carries them: one that always runs at least once (a loop that may
@@ -722,11 +730,15 @@ __device__ __forceinline__ u32x4 low_rank_piece(const GemmParams &p, const LowRa
 // do there is one step of no adapter, which adds zeros.  Returns their number;
 // `out`: whether an adapter is beyond the first kStartAdapters.  The splits of a
 // split-K pass take the adapters in turn.
+//
+// Behind the steps, the rows' scales (until a barrier, each its own thread's).
+// Where one is not finite and its row's adapter is none of the steps' (another
+// split has it, or the epilogue) there will be zeros, to be left as they are.
 template <class T>
 __device__ __forceinline__ int low_rank_steps(const GemmParams &p, const LowRank &t, int m0,
                                               int split, int2 *steps, unsigned &out) {
   constexpr int RANKS = T::BK / 2;     // ranks of a step
-  static_assert(kStartAdapters * (256 / RANKS) * 8 <= T::STAGE_BYTES, "room for the steps");
+  static_assert(8 * kStepRoom<T> + 4 * T::BM <= T::STAGE_BYTES, "room for steps and scales");
   TileAdapters<T::BM> tile(t, m0, p.M);
   int n = 0, i = 0;
   out = 0;
@@ -745,13 +757,23 @@ __device__ __forceinline__ int low_rank_steps(const GemmParams &p, const LowRank
     n = 1;
   }
   __syncthreads();
+  for (int r = threadIdx.x; r < T::BM; r += T::NT) {
+    float f = m0 + r < p.M ? t.scale[m0 + r] : 1.0f;
+    if (!__builtin_isfinite(f)) {
+      const int a = t.rows[m0 + r];
+      bool in = false;
+      for (int s = 0; s < n; ++s) in = in || steps[s].x == a;
+      f = in ? f : 1.0f;
+    }
+    low_rank_scales<T>(steps)[r] = f;
+  }
   return n;
 }
 
 // `out` gets bit i where the tile's adapter i has values that are not finite.
 template <class T, class L>
 __device__ __forceinline__ void low_rank_start(const GemmParams &p, const LowRank &t, int m0,
-                                               int n0, char *slot, const int2 *steps, int n,
+                                               int n0, char *slot, int2 *steps, int n,
                                                int wm0, int wn0,
                                                typename T::Acc (&acc)[T::FM][T::FN],
                                                unsigned &out) {
@@ -796,14 +818,14 @@ __device__ __forceinline__ void low_rank_start(const GemmParams &p, const LowRan
       __builtin_amdgcn_sched_barrier(0);
     }
   } while (++i < n);
-  // the rows' scales
+  const float *scales = low_rank_scales<T>(steps);
   const int lg = lane / T::MF;
 #pragma unroll
   for (int bi = 0; bi < T::FM; ++bi)
 #pragma unroll
     for (int e = 0; e < T::ACC_N; e += 4) {
       const f32x4 f = *reinterpret_cast<const f32x4 *>(
-          t.scale + m0 + wm0 + T::MF * bi + (T::MF == 16 ? 0 : 2 * e) + 4 * lg);
+          scales + wm0 + T::MF * bi + (T::MF == 16 ? 0 : 2 * e) + 4 * lg);
 #pragma unroll
       for (int bj = 0; bj < T::FN; ++bj)
 #pragma unroll
@@ -910,7 +932,9 @@ struct LowRankTerm {
         for (int q = 0; q < 4; ++q)
           if ((same >> (4 * lg + q)) & 1)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) o[q * T::EP_STRIDE + 16 * b] = f[q] * s[b][q];
+            for (int b = 0; b < NB; ++b)   // (columns without such a value, an infinite scale)
+              o[q * T::EP_STRIDE + 16 * b] =
+                  rw < kWhole && s[b][q] == 0.0f ? 0.0f : f[q] * s[b][q];
       }
     }
     add_rows<T>(out, acc, g, lane);
@@ -1357,7 +1381,10 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma_lora(GemmParams p, LowRank t
   __syncthreads();   // every wave is done with the pipeline slots
   const LowRankTerm<T::BM, T::WTM, TB> term(t, m0, wm0, p, split, out);
   if constexpr (OUT32) {
-    epilogue_out32<T, VC, true>(p, m0 + wm0, n0 + wn0, lds, acc, term);
+    GemmParams q = p;   // a split-K pass: the sums as they are
+    q.alpha = 1.0f;
+    q.beta = 0.0f;
+    epilogue_out32<T, VC, true>(q, m0 + wm0, n0 + wn0, lds, acc, term);
   } else {
     epilogue<T, VC, true>(p, m0 + wm0, n0 + wn0, lds, acc, term);
   }

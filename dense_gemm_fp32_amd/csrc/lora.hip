@@ -558,7 +558,8 @@ __global__ __launch_bounds__(256) void lora_shrink_sum(TileShrinkParams p) {
     o[0] = hi;
     o[16] = (_Float16)(rest == rest ? rest : 0.0f);   // an infinity has no rest
   }
-  if (lane == 0) j.scale[row] = ldexpf(a >= 0 && p.ascale ? p.ascale[a] : 1.0f, e);
+  // (of an adapter without a rank nothing is to be scaled)
+  if (lane == 0) j.scale[row] = ldexpf(rk > 0 && p.ascale ? p.ascale[a] : 1.0f, e);
 }
 
 // ---------------------------------------------------------------- expand
@@ -596,6 +597,7 @@ __global__ __launch_bounds__(256) void lora_expand(ExpandParams p) {
       const unsigned same = (unsigned)(__ballot(id == a) & 0xffffu);
       left &= ~same;
       const int rk = rank_of(p.ranks, a, p.R);
+      if (rk == 0) continue;
       const float s = p.scale ? p.scale[a] : 1.0f;
       const float *w = static_cast<const float *>(p.B) + (size_t)a * (size_t)p.stride;
       f32x4 t[NB];
@@ -884,7 +886,7 @@ __global__ __launch_bounds__(256) void lora_outer_sum(OuterParams p) {
     const int i = (int)(t / quads), e0 = 4 * (int)(t % quads);
     const int count = len - e0 < 4 ? len - e0 : 4;
     // of these, the ones within the rank
-    const int in = j.tr ? (rk - e0 < count ? rk - e0 : count) : (i < rk ? count : 0);
+    const int in = n == 0 ? 0 : j.tr ? (rk - e0 < count ? rk - e0 : count) : (i < rk ? count : 0);
     if (done && in == count) continue;
     f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (in > 0 && !done) {

@@ -360,7 +360,7 @@ int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int l
  *             outside 0 .. L-1 (-1, say) means no adapter for that row
  *
  * A row is touched by its own adapter only: an infinity or NaN in another's
- * weights does not reach it.  V = A_a x_i is summed in fp32 and enters the
+ * weights or scale, or in its own from the rank on, does not reach it.  V = A_a x_i is summed in fp32 and enters the
  * second product in at least 21 significant bits (in fp16 calls of more than
  * 512 rows, and G in fp16 gradients: or to within 2^-39 of the largest of its
  * row); the sum with W x_i is formed in fp32 and rounded once.  Accuracy, with q = |W||x| + |scale||B|(|A||x|):

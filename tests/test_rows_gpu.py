@@ -1040,3 +1040,44 @@ def test_infinite_intermediates_keep_their_sign(dt, size):
         dg.lora(*(t.to(GPU) for t in (X, W, A, B, rows)), Y, scale=scale.to(GPU))
         assert same_values(Y, want)
         assert ref.worst(Y, want, bound) <= 1.0
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("size", [(20, 200, 96, 6, 16), (400, 200, 96, 6, 16),
+                                  (600, 128, 8192, 6, 16), (1300, 1600, 96, 40, 24)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_infinite_scales_stay_with_their_rows(dt, size):
+    """An adapter whose scale is an infinity reaches its own rows where it has a
+    rank, in whichever part of K or of a tile's adapters it is summed; without
+    rows its gradients are 0."""
+    import dense_gemm_fp32_amd as dg
+    M, N, K, L, R = size
+    note("infinite scales %s %r" % (dt, size))
+    g, dtype = gen(M + N), DT[dt]
+    X, W = normal(g, (M, K), dtype), normal(g, (N, K), dtype, K ** -0.5)
+    dY = normal(g, (M, N), dtype, 2.0 ** -6)
+    A, B, scale, _ = adapters(g, L, N, K, R, dtype, False)
+    ranks = torch.full((L,), R, dtype=torch.int32)
+    ranks[0::5], scale[0::5] = 0, float("inf")              # nothing of it
+    scale[1::6], scale[2::6] = float("inf"), -float("inf")
+    B[1, 7, 3], A[1, 3, 5] = float("inf"), -float("inf")    # infinities on both sides
+    rows = pattern(g, "mixed", M, L)
+    rows[rows == 2] = 3                                     # no rows
+    Y, grads = torch.empty(M, N, dtype=dtype, device=GPU), {}
+    want, bound = ref.lora(X, W, A, B, rows, None, scale, ranks, 1.0, 0)
+    up = [t.to(GPU) for t in (X, W, A, B, rows)]
+    more = {"scale": scale.to(GPU), "ranks": ranks.to(GPU)}
+    dg.lora(*up, Y, **more)
+    assert same_values(Y[:, 8:], want[:, 8:])
+    assert ref.worst(Y, want, bound) <= 1.0
+    A[1, 3, 5] = 0.5
+    want = ref.lora_grad(dY, X, W, A, B, rows, None, None, None, scale, ranks, 1.0, 0, 0)
+    grads = {"dX": torch.empty(M, K, dtype=dtype, device=GPU),
+             "dA": torch.full((L, R, K), float("nan"), device=GPU),
+             "dB": torch.full((L, N, R), float("nan"), device=GPU)}
+    up[2] = A.to(GPU)
+    dg.lora_grad(dY.to(GPU), *up, **grads, **more)
+    for n in grads:
+        assert ref.worst(grads[n], *want[n]) <= 1.0, n
+    assert bool((grads["dA"][2] == 0).all()) and bool((grads["dB"][2] == 0).all())
+    assert bool((grads["dA"][0::5] == 0).all()) and bool((grads["dB"][0::5] == 0).all())

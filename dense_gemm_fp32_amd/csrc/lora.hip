@@ -721,7 +721,7 @@ struct OuterJob {
   float *D;
   long long stride;
   int K, ldx, ldd, tr;
-  float *P;               // partial sums: (chunks + L) x Rp x K (tr: K x Rp)
+  float *P;               // partial sums: part_slots(M) x Rp x K (tr: K x Rp)
 };
 
 struct OuterParams {
@@ -732,14 +732,21 @@ struct OuterParams {
   float alpha, beta;
 };
 
+// Where the partial sums of an adapter's chunks start whose rows start at s0, and
+// of M rows, how many there are: an adapter of n > chunk rows has ceil(n / chunk)
+// <= floor(2 n / chunk) of them, one of fewer none, so that the room goes with the
+// rows, whatever the number of adapters.
+__host__ __device__ __forceinline__ int part_slots(int s0, int chunk) { return 2 * s0 / chunk; }
+
 constexpr int kOuterWaves = 4;
 constexpr int kOuterThreads = kOuterWaves * kWave;
 constexpr int kOuterCols = 128;    // columns of X a workgroup takes
 constexpr int kOuterRanks = 32;    // ranks a workgroup takes
 
-// P[s] = the sums over chunk c of adapter a's rows, s = start[a] / chunk + a + c:
-// of an adapter's n rows there are no more chunks than there are s up to the next
-// adapter's first.  One workgroup each, so that no adapter waits for another's
+// The sums over chunk c of adapter a's rows are workgroup s = start[a] / chunk + a
+// + c's (of an adapter's n rows there are no more chunks than there are s up to the
+// next adapter's first), into P[part_slots(start[a]) + c].  One workgroup each, so
+// that no adapter waits for another's
 // sums (1000 fp32 rows of 3000 + 517 columns, five adapters: 19 us with a chunk's
 // adapters in turn, 12 us so), and an adapter of one chunk goes straight to D.
 //
@@ -830,7 +837,8 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
                     __builtin_amdgcn_mfma_f32_16x16x4f32(v[u][b], x[u][e], acc[b][e], 0, 0, 0);
       }
       const bool all = at == s0 && stop == s1;
-      float *out = j.P + (size_t)s * p.Rp * j.K;
+      float *out =
+          j.P + (size_t)(part_slots(s0, p.chunk) + (at - s0) / p.chunk) * p.Rp * j.K;
 #pragma unroll
       for (int b = 0; b < NR; ++b) {
         if (b >= nb) break;
@@ -890,7 +898,7 @@ __global__ __launch_bounds__(256) void lora_outer_sum(OuterParams p) {
     if (done && in == count) continue;
     f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (in > 0 && !done) {
-      const float *q = j.P + (size_t)(b / p.chunk + a) * slot + (size_t)i * pitch + e0;
+      const float *q = j.P + (size_t)part_slots(b, p.chunk) * slot + (size_t)i * pitch + e0;
       for (int c = 0; c < chunks; ++c, q += slot)
         sum += count == 4 ? load_whole(q) : load_part(q, count);
     }
@@ -1274,8 +1282,7 @@ size_t carve_grad(const LoraCall &c, void *base, GradSpace *s) {
     s->V = w.take<float>((size_t)c.M * rp);
     s->SV = w.take<float>(parts * c.M * rp);
   }
-  const int chunk = outer_chunk(c);
-  const size_t slots = (size_t)((c.M + chunk - 1) / chunk) + c.L;
+  const size_t slots = (size_t)part_slots(c.M, outer_chunk(c));
   if (c.dA) s->PA = w.take<float>(slots * rp * (size_t)c.K);
   if (c.dB) s->PB = w.take<float>(slots * rp * (size_t)c.N);
   return w.used;

@@ -120,6 +120,18 @@ def test_workspace_sizes():
     assert dg.gemm_moe_workspace(1, 2, 16, most + 1, 4, 2) == 0
 
 
+def test_gradients_workspace_goes_with_the_rows():
+    """Adapters without rows in the batch take nothing but their place in the list of
+    first rows: 4 bytes each."""
+    import dense_gemm_fp32_amd as dg
+    for dtype in (0, 1):
+        for M, N, K, R in ((256, 4096, 4096, 16), (5000, 700, 333, 64), (1, 64, 64, 8)):
+            few, many = (dg.gemm_lora_grad_workspace(dtype, M, N, K, L, R) for L in (64, 60000))
+            assert 0 < many - few <= 4 * (60000 - 64) + 256
+    # 256 rows: two sets of partial sums a chunk of 64 rows, beside the products' own
+    assert dg.gemm_lora_grad_workspace(1, 256, 4096, 4096, 1000, 16) < 64 << 20
+
+
 def test_sizes_beyond_the_limit():
     """Refused as argument 1, 2 or 3, whatever the others are."""
     import dense_gemm_fp32_amd as dg

@@ -1081,3 +1081,29 @@ def test_infinite_scales_stay_with_their_rows(dt, size):
         assert ref.worst(grads[n], *want[n]) <= 1.0, n
     assert bool((grads["dA"][2] == 0).all()) and bool((grads["dB"][2] == 0).all())
     assert bool((grads["dA"][0::5] == 0).all()) and bool((grads["dB"][0::5] == 0).all())
+
+
+def test_lora_grad_partial_sums_fit_their_room():
+    """Adapters of one row more than a chunk of the sums (64), which need the most
+    room for their rows, and long ones beside them: what stands behind a workspace
+    of the size that was named stays as it was."""
+    import dense_gemm_fp32_amd as dg
+    for runs in ((65,) * 20, (1,) + (65,) * 19, (129,) * 10, (64, 64, 640, 66), (63, 1, 700)):
+        M, N, K, L, R = sum(runs), 72, 40, len(runs), 5
+        note("partial sums %r" % (runs,))
+        g = gen(M + L)
+        X, W = normal(g, (M, K), torch.float32), normal(g, (N, K), torch.float32, K ** -0.5)
+        dY = normal(g, (M, N), torch.float32)
+        A, B, scale, _ = adapters(g, L, N, K, R, torch.float32, False)
+        rows = torch.repeat_interleave(torch.arange(L), torch.tensor(runs)).to(torch.int32)
+        want = ref.lora_grad(dY, X, W, A, B, rows, None, None, None, scale, None, 1.0, 0, 0)
+        size = dg.gemm_lora_grad_workspace(0, M, N, K, L, R)
+        ws = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device=GPU)
+        out = {"dX": torch.empty(M, K, device=GPU), "dA": torch.empty(L, R, K, device=GPU),
+               "dB": torch.empty(L, N, R, device=GPU)}
+        dg.lora_grad(*(t.to(GPU) for t in (dY, X, W, A, B, rows)), scale=scale.to(GPU),
+                     workspace=ws[:size], **out)
+        torch.cuda.synchronize()
+        for n in out:
+            assert ref.worst(out[n], *want[n]) <= 1.0, n
+        assert bool((ws[size:] == 0xFF).all())

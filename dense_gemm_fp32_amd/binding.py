@@ -346,6 +346,8 @@ _KINDS = {torch.float16: ("f16", 1), torch.float32: ("f32", 0)}
 # The checks below stand in front of calls that take some microseconds on the
 # GPU: each looks at a tensor's shape and strides once.
 
+_INT_MAX = 2 ** 31 - 1     # the entry points' sizes and leading dimensions; ctypes drops what is above
+
 def _rows(name, t, rows, cols, dtype, dev):
     """Leading dimension of a rows x cols matrix with contiguous rows."""
     if t.dtype is not dtype:
@@ -359,6 +361,9 @@ def _rows(name, t, rows, cols, dtype, dev):
         ld = cols
     if (step != 1 and cols > 1) or ld < cols:
         raise ValueError("%s must have contiguous rows (stride(1) == 1)" % name)
+    if ld > _INT_MAX or rows > _INT_MAX:
+        raise ValueError("%s is beyond 32 bits: size %s, rows %d elements apart"
+                         % (name, tuple(t.shape), ld))
     return ld if ld > 1 else 1
 
 
@@ -376,6 +381,9 @@ def _stack(name, t, n, rows, cols, dtype, dev):
         ld = cols
     if (step != 1 and cols > 1) or ld < cols:
         raise ValueError("%s must have contiguous rows (stride(2) == 1)" % name)
+    if ld > _INT_MAX or rows > _INT_MAX or n > _INT_MAX:
+        raise ValueError("%s is beyond 32 bits: size %s, rows %d elements apart"
+                         % (name, tuple(t.shape), ld))
     return (ld if ld > 1 else 1), (stride if n > 1 else 0)
 
 

@@ -186,6 +186,28 @@ def test_wrappers_refuse_cpu_tensors():
         dg.lora(X.double(), W.double(), A.double(), B.double(), rows, torch.zeros(2, 3).double())
 
 
+def test_wrappers_refuse_sizes_beyond_32_bits():
+    """Sizes and distances of rows that an int does not hold are refused, not cut to
+    its 32 bits (which a multiple of 2^32 more would pass)."""
+    from dense_gemm_fp32_amd import binding
+    f16, big = torch.float16, 1 << 32
+
+    def far(shape, strides):
+        return torch.empty_strided(shape, strides, dtype=f16, device="meta")
+    dev = far((1, 1), (1, 1)).get_device()
+    for t in (far((4, 8), (big + 8, 1)), far((big + 4, 8), (8, 1)), far((1, big + 8), (big + 8, 1))):
+        with pytest.raises(ValueError, match="32 bits"):
+            binding._rows("X", t, *t.shape, f16, dev)
+    for t in (far((3, 4, 8), (64, big + 8, 1)), far((3, big + 4, 8), (64, 8, 1)),
+              far((big + 3, 4, 8), (32, 8, 1)), far((3, 1, big + 8), (64, 8, 1))):
+        with pytest.raises(ValueError, match="32 bits"):
+            binding._stack("A", t, *t.shape, f16, dev)
+    t = far((4, 8), ((1 << 31) - 1, 1))
+    assert binding._rows("X", t, 4, 8, f16, dev) == (1 << 31) - 1
+    t = far((3, 4, 8), (big, 8, 1))
+    assert binding._stack("A", t, 3, 4, 8, f16, dev) == (8, big)
+
+
 def test_reference_lora_by_hand():
     X = torch.tensor([[1.0, 2.0], [3.0, -1.0], [1.0, 1.0]])
     W = torch.tensor([[1.0, 0.0], [0.0, 1.0]])

@@ -1345,8 +1345,8 @@ __global__ __launch_bounds__(T::NT) void hgemm_mfma(GemmParams p) {
   }
 }
 
-// The same product on top of a low-rank term (the splits of a
-// split-K pass share its adapters out).  DIRECT: every tile takes the direct loads; false: the
+// The same product on top of a low-rank term (the splits of a split-K pass share
+// its adapters out).  DIRECT: every tile takes the direct loads; false: the
 // register-staged ones.  (With both loops in one kernel the accumulators that
 // the term leaves are copied for either: twice their registers, and spills.)
 template <class T, bool TB, bool VC, bool OUT32, bool DIRECT>
@@ -1492,18 +1492,19 @@ static hipError_t dispatch_out(const Call &c, const Plan &pl) {
   }
   // the low-rank form comes with A as stored only
   if constexpr (!TERM) {
-  switch (key) {
-    case 4: return launch_variant<TERM, T, true, false, false, OUT32>(c, pl);
-    case 5: return launch_variant<TERM, T, true, false, true, OUT32>(c, pl);
-    default: break;
-  }
-  // Both operands stored transposed: with 16x16x32 blocks that kernel needs
-  // more than 256 VGPRs (it spills), so it keeps the 32x32x16 blocks.
-  typedef typename std::conditional<
-      T::MF == 16,
-      H16Tile<T::BM, T::BN, T::BK, T::WAVES_M, T::WAVES_N, T::STAGES, T::GROUP_M, 32>, T>::type TT;
-  if (key == 6) return launch_variant<TERM, TT, true, true, false, OUT32>(c, pl);
-  return launch_variant<TERM, TT, true, true, true, OUT32>(c, pl);
+    switch (key) {
+      case 4: return launch_variant<TERM, T, true, false, false, OUT32>(c, pl);
+      case 5: return launch_variant<TERM, T, true, false, true, OUT32>(c, pl);
+      default: break;
+    }
+    // Both operands stored transposed: with 16x16x32 blocks that kernel needs
+    // more than 256 VGPRs (it spills), so it keeps the 32x32x16 blocks.
+    typedef typename std::conditional<
+        T::MF == 16,
+        H16Tile<T::BM, T::BN, T::BK, T::WAVES_M, T::WAVES_N, T::STAGES, T::GROUP_M, 32>,
+        T>::type TT;
+    if (key == 6) return launch_variant<TERM, TT, true, true, false, OUT32>(c, pl);
+    return launch_variant<TERM, TT, true, true, true, OUT32>(c, pl);
   }
   return hipErrorInvalidValue;
 }

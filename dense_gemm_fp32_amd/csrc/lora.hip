@@ -774,7 +774,8 @@ __global__ __launch_bounds__(kOuterThreads) void lora_outer(OuterParams p) {
   for (int s = blockIdx.y; s < slots; s += gridDim.y) {
     // the last adapter whose first slot is not behind s, 64 steps at once
     int a = 0;
-    for (int step = p.L > kWave * kWave ? kWave * kWave : (p.L > kWave ? kWave : 1); step > 0; step /= kWave) {
+    for (int step = p.L > kWave * kWave ? kWave * kWave : (p.L > kWave ? kWave : 1); step > 0;
+         step /= kWave) {
       const int b = a + lane * step;
       const bool upto = b < p.L && p.start[b < p.L ? b : 0] / p.chunk + b <= s;
       const unsigned long long m = __ballot(upto);
@@ -1021,10 +1022,9 @@ TileShrinkParams tile_params(const LoraCall &c, const TilePlan &t) {
 }
 
 // The shape of a skinny product: blocks of 16 rows of W a workgroup takes, and
-// the parts K is divided into so that there is one workgroup per CU (the adapters beside
-// them then fit in too, two to a CU: 8 parts 18.5 us, 4 parts 14.8 us at 48 x
-// 4096 x 4096), each
-// wave with at least two steps.
+// the parts K is divided into so that there is one workgroup per CU (the adapters
+// beside them then fit in too, two to a CU: 8 parts 18.5 us, 4 parts 14.8 us at 48
+// x 4096 x 4096), each wave with at least two steps.
 struct SkinnyPlan {
   int P, NB, NF, tiles, parts, chunk;
 };

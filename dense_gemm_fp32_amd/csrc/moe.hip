@@ -4,16 +4,19 @@
 //     w = softmax over the k chosen (renorm) or over all E,
 //     Y := alpha * sum_j w_j W2_e (silu(G_e x) * (U_e x)) + beta * Y,
 //
-// G_e, U_e the first and last F rows of W1_e.  Three launches:
+// G_e, U_e the first and last F rows of W1_e.  Three or four launches:
 //   logits  l in 64-bit sums (two logits may lie closer than 32-bit sums
 //           tell apart, and which expert a token takes hangs on it);
-//   up      a workgroup per expert and 16 rows of F finds the tokens that
+//   up      a workgroup per expert and 4 to 32 rows of F finds the tokens that
 //           chose its expert -- those whose rank among the logits is below k:
 //           a count of the larger ones, no search -- and writes
 //           silu(g) * u for each (token, choice) pair;
-//   down    a workgroup per 16 outputs walks all chosen experts in order,
-//           so the weighted sum over a token's experts needs no atomics and
-//           no second pass.
+//   down    few tokens an expert: a workgroup per 4 or 8 outputs walks all
+//           chosen experts in order, so the weighted sum over a token's experts
+//           needs no atomics and no second pass;
+//           more: a workgroup per expert and 16 to 64 outputs writes each
+//           pair's own, and
+//   combine adds up each token's choices in order.
 #include "../../include/gemm.h"
 #include "internal.hpp"
 #include "rows.hpp"
@@ -205,7 +208,8 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up(MoeParams p) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int i = i0 + BR * b + li / P;
-      x.row[b] = static_cast<const T *>(p.X) + (size_t)(pairs[i < n ? i : n - 1] / p.k) * (size_t)p.ldx;
+      x.row[b] =
+          static_cast<const T *>(p.X) + (size_t)(pairs[i < n ? i : n - 1] / p.k) * (size_t)p.ldx;
     }
     f32x4 acc[NF][NB];
 #pragma unroll
@@ -621,7 +625,8 @@ hipError_t launch_down(const MoeCall &c, const MoeParams &p) {
 
 template <typename T>
 hipError_t run(const MoeCall &c, const MoeSpace &s) {
-  hipLaunchKernelGGL((moe_logits<T>), dim3((unsigned)c.E, (unsigned)((c.M + 3) / 4)), dim3(256), 0, c.stream, static_cast<const T *>(c.X), c.ldx,
+  hipLaunchKernelGGL((moe_logits<T>), dim3((unsigned)c.E, (unsigned)((c.M + 3) / 4)), dim3(256),
+                     0, c.stream, static_cast<const T *>(c.X), c.ldx,
                      static_cast<const T *>(c.Wr), c.ldr, c.M, c.D, c.E, s.logits, s.top,
                      c.M * c.k);
   hipError_t e = hipGetLastError();

@@ -234,8 +234,7 @@ __device__ __forceinline__ int row_exponent(unsigned bits) {
   return e - 141 > -100 ? e - 141 : -100;
 }
 
-// The adapter of a row: -1 when it has none (or an index out of range), or
-// when that adapter's rank is at most `r0` (nothing of it from rank r0 on).
+// The adapter of a row: -1 when it has none (or an index out of range).
 __device__ __forceinline__ int adapter_of(const int *rows, int row, int M, int L) {
   if (row >= M) return -1;
   const int a = rows[row];

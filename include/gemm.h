@@ -360,12 +360,14 @@ int gemm_f16f32_tt(int M, int N, int K, float alpha, const gemm_half_t *A, int l
  *             outside 0 .. L-1 (-1, say) means no adapter for that row
  *
  * A row is touched by its own adapter only: an infinity or NaN in another's
- * weights or scale, or in its own from the rank on, does not reach it.  V = A_a x_i is summed in fp32 and enters the
- * second product in at least 21 significant bits (in fp16 calls of more than
- * 512 rows, and G in fp16 gradients: or to within 2^-39 of the largest of its
- * row); the sum with W x_i is formed in fp32 and rounded once.  Accuracy, with q = |W||x| + |scale||B|(|A||x|):
- * |err| <= 4*(K+R+4)*u*|alpha|*q + 4*u*|beta*Y| plus the one rounding, u = 2^-24
- * (and the 2^-39, where a row of V spans more than 2^17).
+ * weights or scale, or in its own from the rank on, does not reach it.
+ * V = A_a x_i is summed in fp32 and enters the second product in at least 21
+ * significant bits (in fp16 calls of more than 512 rows, and G in fp16
+ * gradients: or to within 2^-39 of the largest of its row); the sum with W x_i
+ * is formed in fp32 and rounded once.  Accuracy, with
+ * q = |W||x| + |scale||B|(|A||x|):
+ * |err| <= 4*(K+R+4)*u*|alpha|*q + 4*u*|beta*Y| plus the one rounding,
+ * u = 2^-24 (and the 2^-39, where a row of V spans more than 2^17).
  * alpha == 0 or K == 0: Y := beta * Y.
  */
 int gemm_lora_f16(int M, int N, int K, float alpha,

@@ -73,9 +73,9 @@ def check_spills_only(src):
 # memory would put every MFMA's operands behind memory traffic, so the build
 # refuses one.  The row-indexed kernels are held to it as well.  There it is not
 # speed alone: a form of lora_shrink_tile that spilled 100 bytes gave wrong sums in
-# every fourth row of a process's first call.  Its cause was not found (a register
-# that other lanes read by shuffles and that only part of the lanes had stored
-# would fit); no race or unwritten value is known in the form without spills.
+# every fourth row of its first call.  The cause was not found (a register that
+# other lanes read by shuffles and that only part of the lanes had stored would
+# fit); no race or unwritten value is known in the form without spills.
 NO_SPILL_KERNELS = ("hgemm_mfma", "sgemm_mfma", "sgemm_streamk", "sgemm_valu", "lora_", "moe_")
 
 

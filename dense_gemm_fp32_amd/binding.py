@@ -78,11 +78,32 @@ for _n, _args in (("gemm_lora", _LORA), ("gemm_lora_grad", _LORA_GRAD), ("gemm_m
     getattr(_lib, _n + "_workspace").argtypes = [_I] * 6
     getattr(_lib, _n + "_workspace").restype = _Z
 
+_QUANT = [_I, _I, _P, _I, _P, _I, _P, _P]
+_I8 = [_I, _I, _I, _F, _P, _I, _P, _P, _I, _P, _F, _P, _I, _P, _Z, _P]
+_GLU = [_I, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _Z, _P]
+_GLU_I8 = [_I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _I, _P, _Z, _P]
+_GLU_GRAD = [_I, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _F, _P, _I, _F, _P, _I, _P, _Z, _P]
+BLOCK_NAMES = ("gemm_quant_i8_f16", "gemm_quant_i8_f32", "gemm_i8_f16", "gemm_i8_f32",
+               "gemm_i8_workspace", "gemm_glu_f16", "gemm_glu_f32", "gemm_glu_i8_f16",
+               "gemm_glu_i8_f32", "gemm_glu_workspace", "gemm_glu_grad_f16",
+               "gemm_glu_grad_f16f32", "gemm_glu_grad_f32", "gemm_glu_grad_workspace")
+for _n, _args in (("gemm_quant_i8", _QUANT), ("gemm_i8", _I8), ("gemm_glu", _GLU),
+                  ("gemm_glu_i8", _GLU_I8), ("gemm_glu_grad", _GLU_GRAD)):
+    for _t in ("f16", "f32"):
+        getattr(_lib, "%s_%s" % (_n, _t)).argtypes = _args
+        getattr(_lib, "%s_%s" % (_n, _t)).restype = _I
+_lib.gemm_glu_grad_f16f32.argtypes = _GLU_GRAD
+_lib.gemm_glu_grad_f16f32.restype = _I
+for _n, _args in (("gemm_i8_workspace", 4), ("gemm_glu_workspace", 5),
+                  ("gemm_glu_grad_workspace", 5)):
+    getattr(_lib, _n).argtypes = [_I] * _args
+    getattr(_lib, _n).restype = _Z
+
 EXPORTS = ("gemm_f32", "gemm_f16", "gemm_f16f32", "gemm_f32_valu", "gemm_f32_noalloc",
            "gemm_f32_colmajor", "gemm_f16_colmajor", "gemm_f16f32_colmajor", "gemm_status_string",
            "gemm_describe", "gemm_set_load_mode", "gemm_set_tile_config", "gemm_set_split",
            "gemm_set_tail_split", "gemm_set_pack", "gemm_set_stream_k", "gemm_set_workspace_limit",
-           "gemm_probe_mfma") + LAYOUT_NAMES + ROW_NAMES
+           "gemm_probe_mfma") + LAYOUT_NAMES + ROW_NAMES + BLOCK_NAMES
 GEMM_ERR_SCRATCH_LIMIT = -200
 GEMM_ERR_NO_WORKSPACE = -201
 
@@ -328,7 +349,7 @@ def _row_entry(name):
     return call
 
 
-for _n in ROW_NAMES:
+for _n in ROW_NAMES + BLOCK_NAMES:
     globals()[_n] = getattr(_lib, _n) if _n.endswith("_workspace") else _row_entry(_n)
 
 _LORA_FN = {t: getattr(_lib, "gemm_lora_" + t) for t in ("f16", "f32")}
@@ -338,6 +359,17 @@ _MOE_FN = {t: getattr(_lib, "gemm_moe_" + t) for t in ("f16", "f32")}
 _lora_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_lora_workspace)
 _lora_grad_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_lora_grad_workspace)
 _moe_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_moe_workspace)
+
+_QUANT_FN = {t: getattr(_lib, "gemm_quant_i8_" + t) for t in ("f16", "f32")}
+_I8_FN = {t: getattr(_lib, "gemm_i8_" + t) for t in ("f16", "f32")}
+_GLU_FN = {t: getattr(_lib, "gemm_glu_" + t) for t in ("f16", "f32", "i8_f16", "i8_f32")}
+_GLU_GRAD_FN = {t: getattr(_lib, "gemm_glu_grad_" + t) for t in ("f16", "f16f32", "f32")}
+_i8_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_i8_workspace)
+_glu_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_glu_workspace)
+_glu_grad_bytes = functools.lru_cache(maxsize=4096)(_lib.gemm_glu_grad_workspace)
+
+# activations of gated blocks: include/gemm.h's GEMM_ACT_*
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 # of a call's type: suffix of the entry point, its workspace function's code
 _KINDS = {torch.float16: ("f16", 1), torch.float32: ("f32", 0)}
@@ -431,6 +463,19 @@ def _call_rows(fn, dev, stream, workspace, need, args):
         ws, size = None, 0
     stream = _current_stream(dev) if stream is None else _stream(stream)
     rc = fn(*args, ws, size, stream)
+    if rc != 0:
+        raise GemmError(rc)
+
+
+def _call(fn, dev, stream, args):
+    """Run entry point `fn`, which takes no workspace, on the current stream of
+    GPU `dev` or the one given."""
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, args)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError("the stream must be one of GPU %d, like the first tensor" % dev)
+    rc = fn(*args, _current_stream(dev) if stream is None else _stream(stream))
     if rc != 0:
         raise GemmError(rc)
 
@@ -549,3 +594,138 @@ def moe(X, router, W1, W2, top_k, Y, renorm=True, alpha=1.0, beta=0.0, ids=None,
                 Y.data_ptr(), ldy, _vector("ids", ids, M * top_k, torch.int32, dev),
                 _vector("weights", weights, M * top_k, torch.float32, dev)))
     return Y
+
+
+def _act(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError("act must be one of %s, not %r" % (", ".join(ACTIVATIONS), act))
+    return code
+
+
+def _at_16(X, ldx, W, ldw, eb):
+    """Whether every row of X and of W starts at a multiple of 16 bytes."""
+    return ((X.data_ptr() | W.data_ptr() | ldx * eb | ldw * eb) & 15) == 0
+
+
+def quantize(X, Q=None, scale=None, stream=None):
+    """Rows of X (M x K float16 or float32, contiguous, possibly padded) to 8-bit
+    integers Q (M x K int8) with a scale each (M float32): scale = max |x| / 127,
+    Q = the whole number nearest to x / scale, ties to even.  Q and scale are made
+    where they are not given.  Returns (Q, scale); see gemm_quant_i8_f16 in
+    include/gemm.h."""
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    M, K = X.shape
+    kind, _, dev = _kind(X)
+    ldx = _rows("X", X, M, K, X.dtype, dev)
+    if Q is None:
+        Q = torch.empty(M, K, dtype=torch.int8, device=X.device)
+    if scale is None:
+        scale = torch.empty(M, dtype=torch.float32, device=X.device)
+    _call(_QUANT_FN[kind], dev, stream,
+          (M, K, X.data_ptr(), ldx, Q.data_ptr(), _rows("Q", Q, M, K, torch.int8, dev),
+           _vector("scale", scale, M, torch.float32, dev)))
+    return Q, scale
+
+
+def gemm_i8(X, W, Y, x_scale=None, w_scale=None, alpha=1.0, beta=0.0, workspace=None,
+            stream=None):
+    """Y := alpha * x_scale[:, None] * w_scale * (X @ W.t()) + beta*Y (in place)
+    for 8-bit integers: X M x K and W N x K int8, Y M x N float16 or float32 (rows
+    contiguous, possibly padded), x_scale M and w_scale N float32 or None (1).  The
+    sum is exact.  workspace: a uint8 tensor of gemm_i8_workspace bytes to use
+    instead of a new one.  Uses the current torch stream unless one is given; see
+    gemm_i8_f16 in include/gemm.h."""
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be 2-D")
+    M, K = X.shape
+    N = W.shape[0]
+    kind, _, dev = _kind(Y)
+    ldx, ldw = _rows("X", X, M, K, torch.int8, dev), _rows("W", W, N, K, torch.int8, dev)
+    ldy = _rows("Y", Y, M, N, Y.dtype, dev)
+    _call_rows(_I8_FN[kind], dev, stream, workspace,
+               _i8_bytes(M, N, K, _at_16(X, ldx, W, ldw, 1)),
+               (M, N, K, alpha, X.data_ptr(), ldx, _vector("x_scale", x_scale, M, torch.float32, dev),
+                W.data_ptr(), ldw, _vector("w_scale", w_scale, N, torch.float32, dev), beta,
+                Y.data_ptr(), ldy))
+    return Y
+
+
+def glu(X, W, H, act="silu", Z=None, x_scale=None, w_scale=None, workspace=None, stream=None):
+    """A gated block: H := act(G) * U, [G U] = X @ W.t() (in place), one kernel.
+
+    X is M x K, W 2F x K (gate rows, then up rows), H M x F (float16, or all
+    float32; rows contiguous, possibly padded).  act: "silu", "gelu", "gelu_tanh"
+    or "relu".  Z (M x 2F), if given, receives [G U] for glu_grad().  X and W may be
+    int8 with x_scale (M float32) and w_scale (2F float32), None for 1; Z then is
+    not offered.  workspace: a uint8 tensor of gemm_glu_workspace bytes to use
+    instead of a new one.  Uses the current torch stream unless one is given; see
+    gemm_glu_f16 in include/gemm.h."""
+    if X.dim() != 2 or H.dim() != 2:
+        raise ValueError("X and H must be 2-D")
+    M, K = X.shape
+    F = H.shape[1]
+    kind, code, dev = _kind(H)
+    code_act = _act(act)
+    i8 = X.dtype is torch.int8
+    dt = torch.int8 if i8 else H.dtype
+    ldx, ldw = _rows("X", X, M, K, dt, dev), _rows("W", W, 2 * F, K, dt, dev)
+    ldh = _rows("H", H, M, F, H.dtype, dev)
+    if i8:
+        if Z is not None:
+            raise ValueError("Z goes with float16 or float32 X and W only")
+        _call_rows(_GLU_FN["i8_" + kind], dev, stream, workspace,
+                   _glu_bytes(2, M, F, K, _at_16(X, ldx, W, ldw, 1)),
+                   (M, F, K, code_act, X.data_ptr(), ldx,
+                    _vector("x_scale", x_scale, M, torch.float32, dev), W.data_ptr(), ldw,
+                    _vector("w_scale", w_scale, 2 * F, torch.float32, dev), H.data_ptr(), ldh))
+        return H
+    if x_scale is not None or w_scale is not None:
+        raise ValueError("x_scale and w_scale go with int8 X and W only")
+    z, ldz = None, 0
+    if Z is not None:
+        z, ldz = Z.data_ptr(), _rows("Z", Z, M, 2 * F, dt, dev)
+    _call_rows(_GLU_FN[kind], dev, stream, workspace,
+               _glu_bytes(code, M, F, K, _at_16(X, ldx, W, ldw, 2 if code else 4)),
+               (M, F, K, code_act, X.data_ptr(), ldx, W.data_ptr(), ldw, H.data_ptr(), ldh, z, ldz))
+    return H
+
+
+def glu_grad(dH, X, W, dX=None, dW=None, act="silu", Z=None, beta_x=0.0, beta_w=0.0,
+             workspace=None, stream=None):
+    """Gradients of glu() for dH (M x F), into those of dX (M x K) and dW (2F x K)
+    that are given:
+
+        dG, dU = dH * U * act'(G), dH * act(G)
+        dX := dG @ W[:F] + dU @ W[F:] + beta_x*dX
+        dW := cat(dG.t() @ X, dU.t() @ X) + beta_w*dW
+
+    Z: what glu() left, or None: G and U are computed again.  All float16, or all
+    float32; dW may be float32 beside float16.  workspace: a uint8 tensor of
+    gemm_glu_grad_workspace bytes to use instead of a new one.  Uses the current
+    torch stream unless one is given; see gemm_glu_grad_f16 in include/gemm.h.
+    Returns (dX, dW)."""
+    if X.dim() != 2 or dH.dim() != 2:
+        raise ValueError("X and dH must be 2-D")
+    M, K = X.shape
+    F = dH.shape[1]
+    dt = X.dtype
+    kind, code, dev = _kind(X)
+    code_act = _act(act)
+    ldx, ldw = _rows("X", X, M, K, dt, dev), _rows("W", W, 2 * F, K, dt, dev)
+    lddh = _rows("dH", dH, M, F, dt, dev)
+    z, ldz, lddx, lddw = None, 0, 0, 0
+    if Z is not None:
+        z, ldz = Z.data_ptr(), _rows("Z", Z, M, 2 * F, dt, dev)
+    if dX is not None:
+        lddx = _rows("dX", dX, M, K, dt, dev)
+    if dW is not None:
+        if code and dW.dtype is torch.float32:
+            kind = "f16f32"
+        lddw = _rows("dW", dW, 2 * F, K, torch.float32 if kind == "f16f32" else dt, dev)
+    _call_rows(_GLU_GRAD_FN[kind], dev, stream, workspace,
+               _glu_grad_bytes(code, M, F, K, _at_16(X, ldx, W, ldw, 2 if code else 4)),
+               (M, F, K, code_act, dH.data_ptr(), lddh, X.data_ptr(), ldx, W.data_ptr(), ldw, z,
+                ldz, beta_x, _addr(dX), lddx, beta_w, _addr(dW), lddw))
+    return dX, dW

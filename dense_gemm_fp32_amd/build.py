@@ -26,7 +26,8 @@ POISON_LIB = os.path.join(HERE, "libgemm_lds_poison.so")
 POISON_BUILD_DIR = os.path.join(HERE, "_build_lds_poison")
 SOURCES = ["api.hip", "gemm_f32.hip", "gemm_f16.hip", "gemm_valu.hip", "scale.hip", "splitk.hip",
            "pack.hip", "probe.hip", "gemm_f16_lora.hip", "lora.hip",
-           "moe.hip", "rows_api.hip"]
+           "moe.hip", "rows_api.hip",
+           "quant.hip", "proj.hip", "proj_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -58,7 +59,7 @@ def _compile(src, verbose=False, build_dir=BUILD_DIR, extra=()):
 # touches it: the asm's m0 writes then cannot disturb compiled code.  The
 # same assembly is checked for spills (and that of gemm_valu.hip).
 M0_ASM_SOURCES = ["gemm_f16.hip", "gemm_f16_lora.hip", "gemm_f32.hip"]
-SPILL_ONLY_SOURCES = ["gemm_valu.hip", "lora.hip", "moe.hip"]
+SPILL_ONLY_SOURCES = ["gemm_valu.hip", "lora.hip", "moe.hip", "proj.hip", "quant.hip"]
 
 
 def check_spills_only(src):
@@ -76,7 +77,8 @@ def check_spills_only(src):
 # every fourth row of its first call.  The cause was not found (a register that
 # other lanes read by shuffles and that only part of the lanes had stored would
 # fit); no race or unwritten value is known in the form without spills.
-NO_SPILL_KERNELS = ("hgemm_mfma", "sgemm_mfma", "sgemm_streamk", "sgemm_valu", "lora_", "moe_")
+NO_SPILL_KERNELS = ("hgemm_mfma", "sgemm_mfma", "sgemm_streamk", "sgemm_valu", "lora_", "moe_",
+                    "proj_", "glu_", "quant_")
 
 
 def scratch_sizes(asm_text):

@@ -357,6 +357,64 @@ const char *gemm_status_string(int status) {
     case -431: return "gemm_lora_grad: invalid argument 31: stride_db less than one matrix";
     case -432: return "gemm_lora_grad: invalid argument 32: workspace not 256-byte aligned";
     case -433: return "gemm_lora_grad: invalid argument 33: workspace_bytes too small (gemm_lora_grad_workspace)";
+    case -601: return "gemm_quant_i8: invalid argument 1: M outside 0 .. 16777216";
+    case -602: return "gemm_quant_i8: invalid argument 2: K outside 0 .. 16777216";
+    case -603: return "gemm_quant_i8: invalid argument 3: X is NULL";
+    case -604: return "gemm_quant_i8: invalid argument 4: ldx < max(1, K)";
+    case -605: return "gemm_quant_i8: invalid argument 5: Q is NULL";
+    case -606: return "gemm_quant_i8: invalid argument 6: ldq < max(1, K)";
+    case -607: return "gemm_quant_i8: invalid argument 7: scale is NULL";
+    case -701: return "gemm_i8: invalid argument 1: M outside 0 .. 16777216";
+    case -702: return "gemm_i8: invalid argument 2: N outside 0 .. 16777216";
+    case -703: return "gemm_i8: invalid argument 3: K outside 0 .. 131071";
+    case -705: return "gemm_i8: invalid argument 5: X is NULL";
+    case -706: return "gemm_i8: invalid argument 6: ldx < max(1, K)";
+    case -708: return "gemm_i8: invalid argument 8: W is NULL";
+    case -709: return "gemm_i8: invalid argument 9: ldw < max(1, K)";
+    case -712: return "gemm_i8: invalid argument 12: Y is NULL";
+    case -713: return "gemm_i8: invalid argument 13: ldy < max(1, N)";
+    case -714: return "gemm_i8: invalid argument 14: workspace not 256-byte aligned";
+    case -715: return "gemm_i8: invalid argument 15: workspace_bytes too small (gemm_i8_workspace)";
+    case -801: return "gemm_glu: invalid argument 1: M outside 0 .. 16777216";
+    case -802: return "gemm_glu: invalid argument 2: F outside 0 .. 8388608";
+    case -803: return "gemm_glu: invalid argument 3: K outside 0 .. 16777216";
+    case -804: return "gemm_glu: invalid argument 4: act is no GEMM_ACT_*";
+    case -805: return "gemm_glu: invalid argument 5: X is NULL";
+    case -806: return "gemm_glu: invalid argument 6: ldx < max(1, K)";
+    case -807: return "gemm_glu: invalid argument 7: W is NULL";
+    case -808: return "gemm_glu: invalid argument 8: ldw < max(1, K)";
+    case -809: return "gemm_glu: invalid argument 9: H is NULL";
+    case -810: return "gemm_glu: invalid argument 10: ldh < max(1, F)";
+    case -812: return "gemm_glu: invalid argument 12: ldz < max(1, 2F)";
+    case -813: return "gemm_glu: invalid argument 13: workspace not 256-byte aligned";
+    case -814: return "gemm_glu: invalid argument 14: workspace_bytes too small (gemm_glu_workspace)";
+    case -901: return "gemm_glu_i8: invalid argument 1: M outside 0 .. 16777216";
+    case -902: return "gemm_glu_i8: invalid argument 2: F outside 0 .. 8388608";
+    case -903: return "gemm_glu_i8: invalid argument 3: K outside 0 .. 131071";
+    case -904: return "gemm_glu_i8: invalid argument 4: act is no GEMM_ACT_*";
+    case -905: return "gemm_glu_i8: invalid argument 5: X is NULL";
+    case -906: return "gemm_glu_i8: invalid argument 6: ldx < max(1, K)";
+    case -908: return "gemm_glu_i8: invalid argument 8: W is NULL";
+    case -909: return "gemm_glu_i8: invalid argument 9: ldw < max(1, K)";
+    case -911: return "gemm_glu_i8: invalid argument 11: H is NULL";
+    case -912: return "gemm_glu_i8: invalid argument 12: ldh < max(1, F)";
+    case -913: return "gemm_glu_i8: invalid argument 13: workspace not 256-byte aligned";
+    case -914: return "gemm_glu_i8: invalid argument 14: workspace_bytes too small (gemm_glu_workspace)";
+    case -1001: return "gemm_glu_grad: invalid argument 1: M outside 0 .. 16777216";
+    case -1002: return "gemm_glu_grad: invalid argument 2: F outside 0 .. 8388608";
+    case -1003: return "gemm_glu_grad: invalid argument 3: K outside 0 .. 16777216";
+    case -1004: return "gemm_glu_grad: invalid argument 4: act is no GEMM_ACT_*";
+    case -1005: return "gemm_glu_grad: invalid argument 5: dH is NULL";
+    case -1006: return "gemm_glu_grad: invalid argument 6: lddh < max(1, F)";
+    case -1007: return "gemm_glu_grad: invalid argument 7: X is NULL";
+    case -1008: return "gemm_glu_grad: invalid argument 8: ldx < max(1, K)";
+    case -1009: return "gemm_glu_grad: invalid argument 9: W is NULL";
+    case -1010: return "gemm_glu_grad: invalid argument 10: ldw < max(1, K)";
+    case -1012: return "gemm_glu_grad: invalid argument 12: ldz < max(1, 2F)";
+    case -1015: return "gemm_glu_grad: invalid argument 15: lddx < max(1, K)";
+    case -1018: return "gemm_glu_grad: invalid argument 18: lddw < max(1, K)";
+    case -1019: return "gemm_glu_grad: invalid argument 19: workspace not 256-byte aligned";
+    case -1020: return "gemm_glu_grad: invalid argument 20: workspace_bytes too small (gemm_glu_grad_workspace)";
     case -501: return "gemm_moe: invalid argument 1: M outside 0 .. 256";
     case -502: return "gemm_moe: invalid argument 2: D < 1";
     case -503: return "gemm_moe: invalid argument 3: F < 1";

@@ -311,6 +311,63 @@ constexpr int kMoeMaxExperts = 1024;
 size_t moe_workspace(const MoeCall &c);
 hipError_t launch_moe(const MoeCall &c, void *ws);
 
+// Rows to 8-bit integers with a scale each (quant.hip); M > 0.
+hipError_t launch_quant(bool half, int M, int K, const void *X, int ldx, int8_t *Q, int ldq,
+                        float *scale, hipStream_t stream);
+
+// A projection X W^T with what follows it (proj.hip): a product of 8-bit
+// integers, or a gated block (gated: W has 2N rows), with dH its [dG dU].
+// Validated; M, N, K > 0.
+struct ProjCall {
+  bool i8;                 // X and W hold 8-bit integers, else Y's type
+  bool half;               // Y (Z, dH) holds fp16, else fp32
+  bool gated;
+  bool aligned;            // workspace sizes: every row of X and W starts at 16 bytes
+  int M, N, K;
+  int act;
+  float alpha, beta;       // of a product
+  const void *X;
+  int ldx;
+  const float *xs;
+  const void *W;
+  int ldw;
+  const float *ws;
+  void *Y;
+  int ldy;
+  void *Z;
+  int ldz;
+  const void *dH;
+  int lddh;
+  hipStream_t stream;
+};
+size_t proj_workspace(const ProjCall &c);
+hipError_t launch_proj(const ProjCall &c, void *ws);
+
+// Gradients of a gated block; validated; M, F, K > 0.
+struct GluGradCall {
+  bool half, dw32;         // dw32: dW holds fp32 whatever the others hold
+  bool aligned;
+  int M, F, K;
+  int act;
+  const void *dH;
+  int lddh;
+  const void *X;
+  int ldx;
+  const void *W;
+  int ldw;
+  const void *Z;           // NULL: G and U are computed again
+  int ldz;
+  float beta_x;
+  void *dX;
+  int lddx;
+  float beta_w;
+  void *dW;
+  int lddw;
+  hipStream_t stream;
+};
+size_t glu_grad_workspace(const GluGradCall &c);
+hipError_t launch_glu_grad(const GluGradCall &c, void *ws);
+
 // The process-wide switch the calls above go by (api.hip).
 long long workspace_limit();
 

@@ -1,11 +1,12 @@
-// rows.hpp -- device-side pieces shared by the products whose rows choose
-// their own weights (lora.hip, moe.hip).
+// rows.hpp -- device-side pieces shared by the products of few rows: those
+// whose rows choose their own weights (lora.hip, moe.hip), gated blocks and
+// products of 8-bit integers (proj.hpp).
 //
-// Both are skinny products: 16 rows of activations at a time against rows of
+// All are skinny products: 16 rows of activations at a time against rows of
 // weights that are read once, so the operands go from global memory straight
 // into matrix-core fragments, without a stop in LDS.  One fragment holds, in
-// lane l, VEC consecutive k of row l % 16 (16 bytes: 8 halves or 4 floats), k
-// group l / 16; the 16x16 result holds, in lane l, column l % 16 (the second
+// lane l, VEC consecutive k of row l % 16 (16 bytes: 16 integers, 8 halves or 4
+// floats), k group l / 16; the 16x16 result holds, in lane l, column l % 16 (the second
 // operand's row) and rows 4*(l/16) .. +3 (the first operand's).
 #pragma once
 
@@ -21,6 +22,7 @@ struct El<_Float16> {
   static constexpr int VEC = 8;      // elements per 16 bytes: k per lane of a fragment
   static constexpr int KSTEP = 32;   // k per fragment (4 lane groups)
   typedef f16x8 Frag;
+  typedef f32x4 Acc;                 // of a 16x16 block
 };
 
 template <>
@@ -28,7 +30,20 @@ struct El<float> {
   static constexpr int VEC = 4;
   static constexpr int KSTEP = 16;
   typedef f32x4 Frag;
+  typedef f32x4 Acc;
 };
+
+template <>
+struct El<int8_t> {
+  static constexpr int VEC = 16;
+  static constexpr int KSTEP = 64;
+  typedef i32x4 Frag;
+  typedef i32x4 Acc;
+};
+
+__device__ __forceinline__ i32x4 mma16(i32x4 a, i32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
 
 __device__ __forceinline__ f32x4 mma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -58,6 +73,11 @@ __device__ __forceinline__ f32x4 mma16(f16x8 w, const Halves &x, f32x4 c) {
 // of any length, padding and offset take the same path; only the last, partly
 // filled step of a row is loaded element by element, since what lies behind a
 // row is never read.
+__device__ __forceinline__ i32x4 load_whole(const int8_t *p) {
+  typedef int Any __attribute__((ext_vector_type(4), aligned(1)));
+  return *reinterpret_cast<const Any *>(p);
+}
+
 template <typename T>
 __device__ __forceinline__ typename El<T>::Frag load_whole(const T *p) {
   typedef T Any __attribute__((ext_vector_type(El<T>::VEC), aligned(sizeof(T))));
@@ -85,6 +105,17 @@ __device__ __forceinline__ f32x4 load_part(const float *p, int n) {
   return f;
 }
 
+__device__ __forceinline__ i32x4 load_part(const int8_t *p, int n) {
+  unsigned long long lo = 0, hi = 0;
+#pragma unroll 1
+  for (int e = (n < 16 ? n : 16) - 1; e >= 0; --e) {
+    hi = (hi << 8) | (lo >> 56);
+    lo = (lo << 8) | (uint8_t)p[e];
+  }
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(i32x4, u64x2{lo, hi});
+}
+
 // v's elements moved down by s places (none for s <= 0, all out for s >= VEC),
 // zeros behind them.
 __device__ __forceinline__ f16x8 move_down(f16x8 v, int s) {
@@ -105,6 +136,19 @@ __device__ __forceinline__ f32x4 move_down(f32x4 v, int s) {
   if (s & 1) v = f32x4{v[1], v[2], v[3], 0.0f};
   if (s >= 4) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   return v;
+}
+
+__device__ __forceinline__ i32x4 move_down(i32x4 v, int s) {
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  const u64x2 w = __builtin_bit_cast(u64x2, v);
+  unsigned long long lo = w[0], hi = w[1];
+  s = s > 0 ? s : 0;
+  if (s & 8) lo = hi, hi = 0;
+  if (s & 4) lo = (lo >> 32) | (hi << 32), hi >>= 32;
+  if (s & 2) lo = (lo >> 16) | (hi << 48), hi >>= 16;
+  if (s & 1) lo = (lo >> 8) | (hi << 56), hi >>= 8;
+  if (s >= 16) lo = hi = 0;
+  return __builtin_bit_cast(i32x4, u64x2{lo, hi});
 }
 
 // Elements k .. k+VEC-1 of a row of K >= VEC elements, 0 beyond its end: one
@@ -140,7 +184,7 @@ __device__ __forceinline__ typename El<T>::Frag load_frag(const T *row, int k, i
 // (diagonal_sum adds them up).
 template <typename T, int U, int P, int NF, int NB, class X>
 __device__ __forceinline__ void stream_steps(const T *const (&w)[NF], int k, const X &x,
-                                             f32x4 (&acc)[NF][NB]) {
+                                             typename El<T>::Acc (&acc)[NF][NB]) {
   typedef typename El<T>::Frag Frag;
   constexpr int KS = P * El<T>::KSTEP;
   Frag wf[U][NF];
@@ -165,7 +209,8 @@ __device__ __forceinline__ void stream_steps(const T *const (&w)[NF], int k, con
 
 template <typename T, int U, int P, int NF, int NB, class X>
 __device__ __forceinline__ void stream_mac(const T *const (&w)[NF], int k0, int k1, int kw,
-                                           int lim, const X &x, f32x4 (&acc)[NF][NB]) {
+                                           int lim, const X &x,
+                                           typename El<T>::Acc (&acc)[NF][NB]) {
   typedef typename El<T>::Frag Frag;
   constexpr int KS = P * El<T>::KSTEP;
   const int lane = threadIdx.x % kWave;
@@ -199,12 +244,12 @@ __device__ __forceinline__ void stream_mac(const T *const (&w)[NF], int k0, int 
 
 // The sums of a product made with P stretches (above): element q of the result
 // is row lane/16 * 4/P + q, column lane % 16 / P, in every lane.
-template <int P>
-__device__ __forceinline__ void diagonal_sum(const f32x4 &v, float (&out)[4 / P]) {
+template <int P, class V, typename S>
+__device__ __forceinline__ void diagonal_sum(const V &v, S (&out)[4 / P]) {
   const int p = threadIdx.x % P;
 #pragma unroll
   for (int q = 0; q < 4 / P; ++q) {
-    float s = v[q * P];
+    S s = v[q * P];
 #pragma unroll
     for (int j = 1; j < P; ++j) s = p == j ? v[q * P + j] : s;
 #pragma unroll

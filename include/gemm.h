@@ -477,6 +477,160 @@ int gemm_moe_f32(int M, int D, int F, int E, int top_k, int renorm, float alpha,
                  void *workspace, size_t workspace_bytes, void *stream);
 size_t gemm_moe_workspace(int dtype, int M, int D, int F, int E, int top_k);
 
+/*
+ * Products of 8-bit integers and gated blocks
+ * -------------------------------------------
+ *
+ * Row-major device matrices, pads, streams, workspaces, overlap and repeatable
+ * results as for the products whose rows choose their own weights, above; the
+ * test switches do not apply either.  A captured call needs a workspace unless its
+ * *_workspace function says 0; `aligned` of those functions: nonzero where every
+ * row of X and W starts at a multiple of 16 bytes (base and leading dimension;
+ * otherwise the call may copy them).
+ *
+ * Status: 0; a positive hipError_t; or for invalid argument i (from 1, in
+ * signature order) -600-i (gemm_quant_i8_*), -700-i (gemm_i8_*), -800-i
+ * (gemm_glu_f16/_f32), -900-i (gemm_glu_i8_*), -1000-i (gemm_glu_grad_*); checked
+ * before any HIP call.  Sizes go to GEMM_ROWS_MAX_SIZE, F to half of it, K of
+ * 8-bit integers to GEMM_I8_MAX_K, up to which no sum leaves 32 bits.
+ */
+#define GEMM_I8_MAX_K 131071
+
+/* activations of a gated block */
+#define GEMM_ACT_SILU 0        /* g / (1 + exp(-g)) */
+#define GEMM_ACT_GELU 1        /* g * Phi(g), Phi the normal distribution function */
+#define GEMM_ACT_GELU_TANH 2   /* g * (1 + tanh(sqrt(2/pi) * (g + 0.044715 g^3))) / 2 */
+#define GEMM_ACT_RELU 3        /* max(g, 0) */
+
+/*
+ * Rows to 8-bit integers with a scale each (tokens before a product, or a
+ * weight's output channels once):
+ *
+ *     scale[m] := max_k |X[m, k]| / 127, rounded to binary32
+ *     Q[m, k]  := X[m, k] / scale[m] rounded to a whole number, ties to even, the
+ *                 exact quotient deciding; within -127 .. 127
+ *
+ *   X, ldx   M x K, ldx >= max(1, K);  Q, ldq: M x K, ldq >= max(1, K)
+ *   scale    M floats
+ *
+ * A row of zeros gets scale 0 and Q = 0; a row with an infinity or NaN scale NaN
+ * and Q = 0, so that what is made of it is NaN.
+ */
+int gemm_quant_i8_f16(int M, int K, const gemm_half_t *X, int ldx, int8_t *Q, int ldq,
+                      float *scale, void *stream);
+int gemm_quant_i8_f32(int M, int K, const float *X, int ldx, int8_t *Q, int ldq,
+                      float *scale, void *stream);
+
+/*
+ * Product of 8-bit integers with a scale for each row of X and of W:
+ *
+ *     Y[m, n] := alpha * x_scale[m] * w_scale[n] * sum_k X[m, k] W[n, k] + beta * Y[m, n]
+ *
+ *   X, ldx    M x K;  W, ldw: N x K (as gemm_*_nt's B)
+ *   x_scale, w_scale   device, M and N floats (NULL: 1)
+ *   Y, ldy    M x N, not read when beta == 0
+ *
+ * The sum is exact (32-bit integers); it is rounded to binary32 and the rest
+ * formed in fp32, in the order written from the right: at most 4 roundings of
+ * 2^-24 (and beta * Y's), then one to Y's type.  alpha == 0 or K == 0:
+ * Y := beta * Y.
+ */
+int gemm_i8_f16(int M, int N, int K, float alpha,
+                const int8_t *X, int ldx, const float *x_scale,
+                const int8_t *W, int ldw, const float *w_scale,
+                float beta, gemm_half_t *Y, int ldy,
+                void *workspace, size_t workspace_bytes, void *stream);
+int gemm_i8_f32(int M, int N, int K, float alpha,
+                const int8_t *X, int ldx, const float *x_scale,
+                const int8_t *W, int ldw, const float *w_scale,
+                float beta, float *Y, int ldy,
+                void *workspace, size_t workspace_bytes, void *stream);
+size_t gemm_i8_workspace(int M, int N, int K, int aligned);
+
+/*
+ * A gated block: both projections, the activation and the product:
+ *
+ *     [G U] = X W^T,   H := act(G) * U   (and Z := [G U])
+ *
+ *   X, ldx    M x K
+ *   W, ldw    2F x K, gate rows, then up rows (as an expert's W1)
+ *   H, ldh    M x F
+ *   Z, ldz    M x 2F, or NULL: G and U for a backward pass, ldz >= max(1, 2F)
+ *   act       GEMM_ACT_*
+ *
+ * G and U are summed in fp32 and enter the activation unrounded; H and Z are
+ * rounded once.  K == 0: zeros.  The gemm_glu_i8_* calls take X and W in 8-bit
+ * integers with scales (x_scale: M floats, w_scale: 2F; NULL: 1); their sums are
+ * exact, as gemm_i8_*'s.
+ */
+int gemm_glu_f16(int M, int F, int K, int act,
+                 const gemm_half_t *X, int ldx,
+                 const gemm_half_t *W, int ldw,
+                 gemm_half_t *H, int ldh, gemm_half_t *Z, int ldz,
+                 void *workspace, size_t workspace_bytes, void *stream);
+int gemm_glu_f32(int M, int F, int K, int act,
+                 const float *X, int ldx,
+                 const float *W, int ldw,
+                 float *H, int ldh, float *Z, int ldz,
+                 void *workspace, size_t workspace_bytes, void *stream);
+int gemm_glu_i8_f16(int M, int F, int K, int act,
+                    const int8_t *X, int ldx, const float *x_scale,
+                    const int8_t *W, int ldw, const float *w_scale,
+                    gemm_half_t *H, int ldh,
+                    void *workspace, size_t workspace_bytes, void *stream);
+int gemm_glu_i8_f32(int M, int F, int K, int act,
+                    const int8_t *X, int ldx, const float *x_scale,
+                    const int8_t *W, int ldw, const float *w_scale,
+                    float *H, int ldh,
+                    void *workspace, size_t workspace_bytes, void *stream);
+/* dtype: 0 = fp32, 1 = fp16, 2 = 8-bit integers */
+size_t gemm_glu_workspace(int dtype, int M, int F, int K, int aligned);
+
+/*
+ * Gradients of gemm_glu_f16 / _f32, for dH (M x F) the gradient of H:
+ *
+ *     dG = dH * U * act'(G),  dU = dH * act(G)
+ *     dX := dG W_gate + dU W_up + beta_x * dX          (M x K)
+ *     dW := [dG dU]^T X + beta_w * dW                  (2F x K)
+ *
+ *   Z         the forward call's, or NULL: G and U are computed again from X and
+ *             W (one more product instead of 2F values a row kept)
+ *   dX, dW    may each be NULL: not wanted (with Z, X is read for dW only and W
+ *             for dX only).  With a beta of 0 the output is not read.
+ *
+ * dW holds the matrices' type, in gemm_glu_grad_f16f32 fp32 (gradients summed over
+ * several batches).  dG and dU enter the two products in the matrices' type, each
+ * rounded once, as a stored tensor would be (fp16: an overflow is infinity; scale
+ * the loss so that none is); the sums are fp32 and rounded once.  relu's derivative
+ * at 0 is 0.  M == 0 or F == 0: outputs are scaled by their betas.
+ */
+int gemm_glu_grad_f16(int M, int F, int K, int act,
+                      const gemm_half_t *dH, int lddh,
+                      const gemm_half_t *X, int ldx,
+                      const gemm_half_t *W, int ldw,
+                      const gemm_half_t *Z, int ldz,
+                      float beta_x, gemm_half_t *dX, int lddx,
+                      float beta_w, gemm_half_t *dW, int lddw,
+                      void *workspace, size_t workspace_bytes, void *stream);
+int gemm_glu_grad_f16f32(int M, int F, int K, int act,
+                         const gemm_half_t *dH, int lddh,
+                         const gemm_half_t *X, int ldx,
+                         const gemm_half_t *W, int ldw,
+                         const gemm_half_t *Z, int ldz,
+                         float beta_x, gemm_half_t *dX, int lddx,
+                         float beta_w, float *dW, int lddw,
+                         void *workspace, size_t workspace_bytes, void *stream);
+int gemm_glu_grad_f32(int M, int F, int K, int act,
+                      const float *dH, int lddh,
+                      const float *X, int ldx,
+                      const float *W, int ldw,
+                      const float *Z, int ldz,
+                      float beta_x, float *dX, int lddx,
+                      float beta_w, float *dW, int lddw,
+                      void *workspace, size_t workspace_bytes, void *stream);
+/* dtype: 0 = fp32, 1 = fp16 (either type of dW) */
+size_t gemm_glu_grad_workspace(int dtype, int M, int F, int K, int aligned);
+
 /* Static, human-readable text for a status code returned above (never NULL). */
 const char *gemm_status_string(int status);
 

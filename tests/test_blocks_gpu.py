@@ -1,0 +1,745 @@
+"""Products of 8-bit integers and gated blocks on the GPU, against 64-bit
+references within derived bounds."""
+import math
+
+import pytest
+import torch
+
+import blocks_reference as ref
+from gemm_harness import note
+from rows_reference import worst
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "f32": torch.float32}
+GPU = "cuda:0"
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, shape, dtype, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+def whole(g, shape):
+    return torch.randint(-127, 128, shape, generator=g).to(torch.int8)
+
+
+def scales(g, n):
+    return 0.01 + torch.rand(n, generator=g) / 50
+
+
+def padded(t, pad):
+    """A device copy of t with `pad` elements after each row that no call may
+    read or write (NaN; 99 among integers), and the view of t in it."""
+    fill = float("nan") if t.is_floating_point() else 99
+    big = torch.full(t.shape[:-1] + (t.shape[-1] + pad,), fill, dtype=t.dtype)
+    big[..., :t.shape[-1]] = t
+    big = big.to(GPU)
+    return big, big[..., :t.shape[-1]]
+
+
+def pads_intact(big, cols):
+    tail = big[..., cols:]
+    if tail.numel() == 0:
+        return True
+    return bool((torch.isnan(tail) if tail.is_floating_point() else tail == 99).all())
+
+
+def unset(rows, cols, dtype, pad):
+    """An output that holds nothing yet."""
+    return padded(torch.full((rows, cols), 77 if dtype == torch.int8 else float("nan"),
+                             dtype=dtype), pad)
+
+
+# ---------------------------------------------------------------- rows to 8-bit integers
+
+QUANT = [(1, 1, 0), (1, 4096, 0), (3, 7, 1), (5, 8, 0), (2, 15, 0), (17, 16, 3), (4, 17, 0),
+         (33, 255, 1), (64, 2048, 0), (9, 2049, 0), (130, 517, 8), (3, 20000, 0), (1, 131071, 1),
+         (2000, 64, 0), (300, 8192, 0)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", QUANT, ids=lambda c: "x".join(map(str, c)))
+def test_quantize(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, K, pad = case
+    note("quantize %s %r" % (dt, case))
+    g = gen(M * 7 + K)
+    X = normal(g, (M, K), DT[dt]) * torch.exp2(torch.randint(-8, 6, (M, 1), generator=g)).to(DT[dt])
+    want, scale = ref.quantize(X)
+    x = padded(X, pad)[1]
+    big, q = unset(M, K, torch.int8, pad)
+    s = torch.full((M,), -1.0, device=GPU)
+    out = dg.quantize(x, q, s)
+    assert out[0] is q and out[1] is s
+    torch.cuda.synchronize()
+    assert torch.equal(s.cpu(), scale) and torch.equal(q.cpu(), want)
+    assert pads_intact(big, K)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_quantize_ties_and_odd_rows(dt):
+    """Quotients on and next to the border of two whole numbers; rows of zeros, of
+    the type's smallest and largest values, with infinities and NaN."""
+    import dense_gemm_fp32_amd as dg
+    t, info = DT[dt], torch.finfo(DT[dt])
+    rows = []
+    for top in (127.0, 254.0, 63.5, 127.0 * 2 ** -10):       # scales 1, 2, 0.5, 2^-10
+        k = torch.arange(-126, 127) + 0.5
+        rows.append(torch.cat((torch.tensor([top]), k * (top / 127.0))))
+    for top in (1.0, 3.7, 100.0 / 3, 6.1e-5 * 7):            # borders of scales that are no powers of 2
+        top = float(torch.tensor(top, dtype=t))
+        s = float((torch.tensor([top]).double() / 127).float())
+        x = ((torch.arange(-126, 127) + 0.5).double() * s).to(t)
+        rows.append(torch.cat((torch.tensor([top]), x.float())))
+    n = 254
+    rows += [torch.zeros(n), torch.full((n,), info.max), torch.full((n,), -info.max),
+             torch.full((n,), info.tiny), torch.linspace(-info.max, info.max, n)]
+    tiny = torch.arange(n) * (2.0 ** -24 if dt == "f16" else 2.0 ** -149)
+    rows += [tiny, tiny / tiny.max() * info.tiny * 3]
+    for bad in (math.inf, -math.inf, math.nan):
+        r = torch.arange(n).float()
+        r[n // 2] = bad
+        rows.append(r)
+    X = torch.stack([r.to(t) for r in rows])
+    if dt == "f32":       # one step either side of each border
+        step = X[:8].view(torch.int32)
+        X = torch.cat((X, (step + 1).view(torch.float32), (step - 1).view(torch.float32)))
+        X[-16:, 0] = X[:8, 0].repeat(2)
+    want, scale = ref.quantize(X)
+    q, s = dg.quantize(X.to(GPU))
+    assert torch.equal(torch.isnan(s.cpu()), torch.isnan(scale))
+    assert torch.equal(s.cpu().nan_to_num(), scale.nan_to_num())
+    assert torch.equal(q.cpu(), want)
+
+
+def test_quantize_without_columns():
+    import dense_gemm_fp32_amd as dg
+    q, s = dg.quantize(torch.empty(5, 0, device=GPU))
+    assert q.shape == (5, 0) and s.tolist() == [0.0] * 5
+
+
+# ---------------------------------------------------------------- products of 8-bit integers
+
+I8 = [
+    # M, N, K, pad, alpha, beta, scales
+    (1, 1, 1, 0, 1.0, 0.0, True),
+    (1, 64, 64, 0, 1.0, 0.0, True),
+    (1, 1024, 1024, 0, 1.0, 0.0, True),
+    (2, 5, 15, 1, 1.5, -0.5, True),
+    (3, 33, 16, 0, 1.0, 0.0, False),
+    (7, 130, 17, 3, -1.0, 1.0, True),
+    (16, 256, 4096, 0, 1.0, 0.0, True),
+    (17, 520, 63, 0, 1.0, 1.0, True),
+    (33, 96, 2000, 16, 1.0, 0.0, True),
+    (48, 1000, 130, 1, 1.0, 0.5, False),
+    (64, 4096, 256, 0, 1.0, 0.0, True),
+    (65, 257, 129, 0, 1.0, 0.0, True),
+    (100, 128, 128, 0, 1.0, 0.0, True),
+    (129, 384, 640, 0, 2.0, 0.25, True),
+    (200, 515, 517, 3, 1.0, 0.0, True),
+    (256, 2048, 1024, 0, 1.0, 0.0, True),
+    (300, 260, 1536, 16, 1.0, 1.0, True),
+    (513, 1032, 255, 0, 1.0, 0.0, True),
+    (700, 96, 3000, 0, 1.0, 0.0, True),
+    (1000, 1500, 517, 5, -0.5, 0.0, True),
+    (1030, 2050, 272, 0, 1.0, 0.0, True),
+    (2100, 4160, 144, 0, 1.0, 1.0, True),
+    (4096, 512, 192, 32, 1.0, 0.0, False),
+    (40, 4000, 131071, 0, 1.0, 0.0, True),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", I8, ids=lambda c: "x".join(map(str, c[:4])))
+def test_gemm_i8(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, N, K, pad, alpha, beta, scaled = case
+    note("gemm_i8 %s %r" % (dt, case))
+    g, t = gen(M * 31 + N), DT[dt]
+    X, W = whole(g, (M, K)), whole(g, (N, K))
+    top = 0.5 / math.sqrt(K)
+    xs, ws = (scales(g, M) * top, scales(g, N)) if scaled else (None, None)
+    if not scaled and dt == "f16":
+        alpha *= 2.0 ** -12      # sums of whole numbers pass fp16's largest
+    Y = normal(g, (M, N), t) if beta else torch.full((M, N), float("nan"), dtype=t)
+    want, bound = ref.gemm_i8(X, W, Y, xs, ws, alpha, beta, t)
+    x, w = padded(X, pad)[1], padded(W, pad)[1]
+    big, y = padded(Y, pad)
+    up = lambda v: None if v is None else v.to(GPU)  # noqa: E731
+    assert dg.gemm_i8(x, w, y, x_scale=up(xs), w_scale=up(ws), alpha=alpha, beta=beta) is y
+    torch.cuda.synchronize()
+    assert worst(y, want, bound) <= 1.0
+    assert pads_intact(big, N)
+
+
+def test_gemm_i8_sums_are_exact():
+    """Sums at the edges of 32 bits: -128 and 127 in every place, and sums beyond
+    2^24 that differ by one."""
+    import dense_gemm_fp32_amd as dg
+    K = 131071
+    for M in (1, 40, 300):
+        X = torch.full((M, K), 127, dtype=torch.int8)
+        X[0] = -128
+        W = torch.stack((torch.full((K,), -128), torch.full((K,), 127))).to(torch.int8)
+        y = torch.empty(M, 2, device=GPU)
+        dg.gemm_i8(X.to(GPU), W.to(GPU), y)
+        S = X.double() @ W.double().t()
+        assert torch.equal(y.cpu(), S.float())
+    # 512 columns of 127 * 127, less what makes whole numbers of 24 bits
+    M, N, K = 70, 65, 1040
+    X = torch.full((M, K), 127, dtype=torch.int8)
+    W = torch.full((N, K), 127, dtype=torch.int8)
+    W[:, 1039] = torch.arange(N).to(torch.int8)
+    X[:, 1039] = 1
+    y = torch.empty(M, N, device=GPU)
+    dg.gemm_i8(X.to(GPU), W.to(GPU), y)
+    S = X.double() @ W.double().t()
+    assert float(S.max()) < 2 ** 24 and torch.equal(y.cpu().double(), S)
+
+
+@pytest.mark.parametrize("M", [1, 20, 130, 700])
+def test_gemm_i8_scales_that_are_not_finite_stay_in_their_rows(M):
+    import dense_gemm_fp32_amd as dg
+    g = gen(M)
+    N, K = 200, 144
+    X, W = whole(g, (M, K)), whole(g, (N, K))
+    xs, ws = scales(g, M), scales(g, N)
+    xs[M // 2], ws[3], ws[N - 1] = math.nan, math.inf, math.nan
+    y = torch.empty(M, N, device=GPU)
+    dg.gemm_i8(X.to(GPU), W.to(GPU), y, x_scale=xs.to(GPU), w_scale=ws.to(GPU))
+    want, bound = ref.gemm_i8(X, W, None, xs, ws, 1.0, 0, torch.float32)
+    ok = torch.isfinite(want)
+    y = y.cpu()
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert worst(y[ok], want[ok], bound[ok]) <= 1.0
+
+
+def test_gemm_i8_degenerate():
+    import dense_gemm_fp32_amd as dg
+    y = torch.full((3, 4), 2.0, device=GPU)
+    e = torch.empty(3, 0, dtype=torch.int8, device=GPU), torch.empty(4, 0, dtype=torch.int8,
+                                                                     device=GPU)
+    dg.gemm_i8(*e, y, beta=0.5)
+    assert y.tolist() == [[1.0] * 4] * 3
+    nan = torch.full((3,), math.nan, device=GPU)
+    q = torch.ones(3, 8, dtype=torch.int8, device=GPU), torch.ones(4, 8, dtype=torch.int8,
+                                                                   device=GPU)
+    dg.gemm_i8(*q, y, x_scale=nan, alpha=0.0, beta=3.0)
+    assert y.tolist() == [[3.0] * 4] * 3
+    y.fill_(math.nan)
+    dg.gemm_i8(*e, y)
+    assert y.tolist() == [[0.0] * 4] * 3
+
+
+# ---------------------------------------------------------------- gated blocks
+
+GLU = [
+    # M, F, K, pad, act, Z kept
+    (1, 1, 1, 0, "silu", True),
+    (1, 1024, 1024, 0, "silu", False),
+    (1, 64, 64, 0, "relu", True),
+    (2, 5, 7, 1, "gelu", True),
+    (3, 33, 8, 0, "gelu_tanh", False),
+    (8, 130, 17, 3, "silu", True),
+    (16, 520, 2048, 0, "gelu", False),
+    (17, 96, 1000, 8, "relu", True),
+    (33, 257, 65, 0, "gelu_tanh", True),
+    (48, 1000, 264, 0, "silu", False),
+    (64, 2048, 256, 0, "silu", True),
+    (65, 127, 129, 1, "silu", True),
+    (100, 128, 128, 0, "gelu", True),
+    (129, 384, 328, 0, "silu", False),
+    (200, 515, 517, 3, "gelu_tanh", True),
+    (257, 1024, 512, 0, "silu", True),
+    (300, 260, 768, 8, "relu", False),
+    (513, 1032, 136, 0, "silu", True),
+    (1000, 750, 259, 5, "gelu", True),
+    (1030, 2050, 72, 0, "silu", True),
+    (2100, 2112, 96, 0, "gelu_tanh", False),
+    (2048, 4096, 64, 0, "silu", True),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", GLU, ids=lambda c: "x".join(map(str, c)))
+def test_glu(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, F, K, pad, name, kept = case
+    note("glu %s %r" % (dt, case))
+    g, t = gen(M * 31 + F), DT[dt]
+    X, W = normal(g, (M, K), t), normal(g, (2 * F, K), t, 1.5 / math.sqrt(K))
+    want = ref.glu(X, W, name, t)
+    x, w = padded(X, pad)[1], padded(W, pad)[1]
+    bigh, h = unset(M, F, t, pad)
+    bigz, z = unset(M, 2 * F, t, pad)
+    assert dg.glu(x, w, h, act=name, Z=z if kept else None) is h
+    torch.cuda.synchronize()
+    assert worst(h, *want["H"]) <= 1.0
+    assert pads_intact(bigh, F) and pads_intact(bigz, 2 * F)
+    if kept:
+        assert worst(z, *want["Z"]) <= 1.0
+    else:
+        assert pads_intact(bigz, 0)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", GLU, ids=lambda c: "x".join(map(str, c)))
+def test_glu_i8(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, F, K, pad, name, scaled = case
+    note("glu_i8 %s %r" % (dt, case))
+    g, t = gen(M * 37 + F), DT[dt]
+    X, W = whole(g, (M, K)), whole(g, (2 * F, K))
+    xs, ws = scales(g, M), scales(g, 2 * F) / math.sqrt(K)
+    up = (lambda v: v.to(GPU)) if scaled else (lambda v: None)
+    if not scaled:          # sums of a few units: scales of 1 would leave fp16's range
+        X, W = (torch.randint(-1, 2, m.shape, generator=g).to(torch.int8) for m in (X, W))
+        xs = ws = None
+    want = ref.glu(X, W, name, t, xs, ws)
+    x, w = padded(X, pad)[1], padded(W, pad)[1]
+    bigh, h = unset(M, F, t, pad)
+    dg.glu(x, w, h, act=name, x_scale=up(xs), w_scale=up(ws))
+    torch.cuda.synchronize()
+    assert worst(h, *want["H"]) <= 1.0
+    assert pads_intact(bigh, F)
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_activations_over_their_range(dt, name):
+    """Gates from -100 to 100 and at both zeros, each times an up value: K = 2
+    picks them out of X."""
+    import dense_gemm_fp32_amd as dg
+    t = DT[dt]
+    gates = torch.cat((torch.linspace(-100, 100, 1601), torch.tensor([0.0, -0.0]),
+                       torch.logspace(-6, 1, 100), -torch.logspace(-6, 1, 100)))
+    X = torch.stack((gates, torch.full_like(gates, 1.5)), 1).to(t)
+    W = torch.tensor([[1.0, 0.0], [0.0, 1.0]], dtype=t)
+    want = ref.glu(X, W, name, t)["H"]
+    h = torch.empty(len(gates), 1, dtype=t, device=GPU)
+    dg.glu(X.to(GPU), W.to(GPU), h, act=name)
+    # where act(g) leaves the normal numbers, to their smallest
+    assert worst(h, want[0], want[1] + 150 * torch.finfo(torch.float32).tiny) <= 1.0
+
+
+@pytest.mark.parametrize("M", [3, 70, 300])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_glu_infinities_stay_in_their_rows(dt, M):
+    import dense_gemm_fp32_amd as dg
+    g, t = gen(M), DT[dt]
+    F, K = 200, 136
+    X, W = normal(g, (M, K), t), normal(g, (2 * F, K), t, 0.1)
+    clean = ref.glu(X, W, "silu", t)
+    X[M // 2, K - 1] = math.inf
+    X[0, 0] = math.nan
+    W[7, 3] = math.nan
+    W[F + 11, K - 1] = -math.inf
+    h = torch.empty(M, F, dtype=t, device=GPU)
+    z = torch.empty(M, 2 * F, dtype=t, device=GPU)
+    dg.glu(X.to(GPU), W.to(GPU), h, Z=z)
+    rows = [i for i in range(M) if i not in (0, M // 2)]
+    cols = [i for i in range(F) if i not in (7, 11)]
+    pick = lambda v: v[rows][:, cols]  # noqa: E731
+    assert worst(pick(h.cpu()), *(pick(v) for v in clean["H"])) <= 1.0
+    Z = X.double() @ W.double().t()
+    assert torch.equal(torch.isnan(z.cpu()), torch.isnan(Z))
+    assert torch.equal(torch.isinf(z.cpu()), torch.isinf(Z))
+
+
+def test_glu_without_columns():
+    import dense_gemm_fp32_amd as dg
+    for t in (torch.float16, torch.float32):
+        h, z = torch.ones(3, 4, dtype=t, device=GPU), torch.ones(3, 8, dtype=t, device=GPU)
+        dg.glu(torch.empty(3, 0, dtype=t, device=GPU), torch.empty(8, 0, dtype=t, device=GPU), h,
+               Z=z)
+        assert not h.any() and not z.any()
+        q = torch.empty(3, 0, dtype=torch.int8, device=GPU)
+        h.fill_(1)
+        dg.glu(q, torch.empty(8, 0, dtype=torch.int8, device=GPU), h)
+        assert not h.any()
+
+
+# ---------------------------------------------------------------- their gradients
+
+GRAD = [
+    # M, F, K, pad, act, Z given, beta_x, beta_w, dW in fp32
+    (1, 1, 1, 0, "silu", True, 0.0, 0.0, False),
+    (1, 64, 64, 0, "silu", False, 0.0, 0.0, True),
+    (3, 5, 7, 1, "gelu", True, 1.0, -0.5, False),
+    (17, 130, 96, 8, "gelu_tanh", False, 0.0, 1.0, True),
+    (33, 256, 512, 0, "relu", True, 0.0, 0.0, False),
+    (64, 96, 200, 0, "silu", False, 0.5, 0.0, False),
+    (65, 127, 129, 3, "gelu", False, 0.0, 0.0, True),
+    (129, 300, 264, 0, "silu", True, 0.0, 1.0, True),
+    (257, 512, 384, 0, "silu", False, 0.0, 0.0, False),
+    (300, 515, 131, 5, "gelu_tanh", True, 1.0, 1.0, False),
+    (512, 640, 256, 0, "relu", False, 0.0, 0.0, True),
+    (1000, 375, 259, 1, "gelu", True, 0.0, 0.0, False),
+    (1030, 1024, 136, 0, "silu", False, 0.0, 0.0, False),
+]
+
+
+def grad_inputs(case, dt):
+    M, F, K, pad, name, kept, beta_x, beta_w, dw32 = case
+    g, t = gen(M * 31 + F), DT[dt]
+    X, W = normal(g, (M, K), t), normal(g, (2 * F, K), t, 1.0 / math.sqrt(K))
+    dH = normal(g, (M, F), t, 0.05)
+    Z = (X.double() @ W.double().t()).to(t) if kept else None
+    tw = torch.float32 if dw32 else t
+    return X, W, dH, Z, normal(g, (M, K), t), normal(g, (2 * F, K), tw), tw
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("case", GRAD, ids=lambda c: "x".join(map(str, c)))
+def test_glu_grad(dt, case):
+    import dense_gemm_fp32_amd as dg
+    M, F, K, pad, name, kept, beta_x, beta_w, dw32 = case
+    note("glu_grad %s %r" % (dt, case))
+    X, W, dH, Z, oldx, oldw, tw = grad_inputs(case, dt)
+    want = ref.glu_grad(dH, X, W, Z, name, oldx, oldw, beta_x, beta_w, tw)
+    x, w, d = (padded(v, pad)[1] for v in (X, W, dH))
+    z = padded(Z, pad)[1] if kept else None
+    bigx, dx = padded(oldx, pad) if beta_x else unset(M, K, DT[dt], pad)
+    bigw, dw = padded(oldw, pad) if beta_w else unset(2 * F, K, tw, pad)
+    out = dg.glu_grad(d, x, w, dX=dx, dW=dw, act=name, Z=z, beta_x=beta_x, beta_w=beta_w)
+    torch.cuda.synchronize()
+    assert out[0] is dx and out[1] is dw
+    assert worst(dx, *want["dX"]) <= 1.0 and worst(dw, *want["dW"]) <= 1.0
+    assert pads_intact(bigx, K) and pads_intact(bigw, K)
+    # one of the two alone: the same bits
+    one = torch.full_like(dx, 1.0).copy_(oldx.to(GPU))
+    dg.glu_grad(d, x, w, dX=one, act=name, Z=z, beta_x=beta_x)
+    assert torch.equal(one, dx)
+    one = torch.full_like(dw, 1.0).copy_(oldw.to(GPU))
+    dg.glu_grad(d, x, w, dW=one, act=name, Z=z, beta_w=beta_w)
+    assert torch.equal(one, dw)
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+def test_glu_grad_against_differences(name):
+    """sum(dH * H(X, W)) moved along a direction of X and one of W, both sides in
+    the library's fp32: differences of step h leave h^2 and u/h."""
+    import dense_gemm_fp32_amd as dg
+    g = gen(5)
+    M, F, K = 40, 72, 96
+    X, W, dH = (normal(g, s, torch.float32, q).to(GPU) for s, q in
+                (((M, K), 1.0), ((2 * F, K), 0.1), ((M, F), 1.0)))
+    vx, vw = normal(g, (M, K), torch.float32).to(GPU), normal(g, (2 * F, K), torch.float32).to(GPU)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    dg.glu_grad(dH, X, W, dX=dX, dW=dW, act=name)
+
+    def loss(x, w):
+        h = torch.empty(M, F, device=GPU)
+        dg.glu(x, w, h, act=name)
+        return float((h.double() * dH.double()).sum())
+    h = 2.0 ** -9
+    for slope, f in ((float((dX.double() * vx.double()).sum()), lambda s: loss(X + s * vx, W)),
+                     (float((dW.double() * vw.double()).sum()),
+                      lambda s: loss(X, W + s * 0.1 * vw) * 10)):
+        diff = (f(h) - f(-h)) / (2 * h)
+        # M F terms of order 1, third derivatives of order K^1.5 / 1000 (relu: kinks
+        # within h of a gate, a share h of them): both well under 1% of the norm
+        size = math.sqrt(M * F * K)
+        assert abs(diff - slope) <= 0.02 * size
+
+
+def test_glu_grad_degenerate():
+    import dense_gemm_fp32_amd as dg
+    t = torch.float16
+    e = lambda *s: torch.empty(*s, dtype=t, device=GPU)  # noqa: E731
+    dw = torch.ones(8, 6, dtype=t, device=GPU)
+    dg.glu_grad(e(0, 4), e(0, 6), e(8, 6), dX=e(0, 6), dW=dw, beta_w=2.0)
+    assert bool((dw == 2).all())
+    dw32 = torch.full((8, 6), math.nan, device=GPU)
+    dg.glu_grad(e(0, 4), e(0, 6), e(8, 6), dW=dw32)
+    assert not dw32.any()
+    dx = torch.ones(3, 6, dtype=t, device=GPU)
+    dg.glu_grad(e(3, 0), e(3, 6), e(0, 6), dX=dx, dW=e(0, 6), beta_x=3.0)
+    assert bool((dx == 3).all())
+
+
+# ---------------------------------------------------------------- together, and how they are called
+
+def block_i8(dg, X, W1, s1, W2, s2, Q, xs, H, Q2, hs, Y, stream=None):
+    """A feed-forward block in 8-bit integers, as a model calls it."""
+    dg.quantize(X, Q, xs, stream=stream)
+    dg.glu(Q, W1, H, x_scale=xs, w_scale=s1, stream=stream)
+    dg.quantize(H, Q2, hs, stream=stream)
+    return dg.gemm_i8(Q2, W2, Y, x_scale=hs, w_scale=s2, beta=1.0, stream=stream)
+
+
+def block_inputs(M, D, F, seed):
+    g = gen(seed)
+    X = normal(g, (M, D), torch.float16)
+    W1, s1 = ref.quantize(normal(g, (2 * F, D), torch.float32, D ** -0.5))
+    W2, s2 = ref.quantize(normal(g, (D, F), torch.float32, F ** -0.5))
+    return X, W1, s1, W2, s2
+
+
+def block_buffers(M, D, F):
+    e = lambda *s, dtype=torch.float16: torch.empty(*s, dtype=dtype, device=GPU)  # noqa: E731
+    return (e(M, D, dtype=torch.int8), e(M, dtype=torch.float32), e(M, F),
+            e(M, F, dtype=torch.int8), e(M, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("M,D,F", [(1, 512, 256), (40, 512, 768), (300, 320, 640)])
+def test_block_in_8_bits(M, D, F):
+    """Each step against the 64-bit reference of what the step before left."""
+    import dense_gemm_fp32_amd as dg
+    X, W1, s1, W2, s2 = block_inputs(M, D, F, M)
+    Q, xs, H, Q2, hs = bufs = block_buffers(M, D, F)
+    Y = X.to(GPU)
+    block_i8(dg, Y.clone(), W1.to(GPU), s1.to(GPU), W2.to(GPU), s2.to(GPU), *bufs, Y)
+    torch.cuda.synchronize()
+    q, s = ref.quantize(X)
+    assert torch.equal(Q.cpu(), q) and torch.equal(xs.cpu(), s)
+    assert worst(H, *ref.glu(q, W1, "silu", torch.float16, s, s1)["H"]) <= 1.0
+    q, s = ref.quantize(H.cpu())
+    assert torch.equal(Q2.cpu(), q) and torch.equal(hs.cpu(), s)
+    assert worst(Y, *ref.gemm_i8(q, W2, X, s, s2, 1.0, 1.0, torch.float16)) <= 1.0
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_training_step_of_a_block(kept):
+    """Y = glu(X) W2^T and back, every step with the library: each gradient
+    against the reference of what the step before left."""
+    import dense_gemm_fp32_amd as dg
+    g, t = gen(9), torch.float16
+    M, D, F = 200, 256, 384
+    X, W1 = normal(g, (M, D), t), normal(g, (2 * F, D), t, D ** -0.5)
+    W2, dY = normal(g, (D, F), t, F ** -0.5), normal(g, (M, D), t, 0.05)
+    x, w1, w2, dy = (v.to(GPU) for v in (X, W1, W2, dY))
+    H, dH = (torch.empty(M, F, dtype=t, device=GPU) for _ in range(2))
+    Z = torch.empty(M, 2 * F, dtype=t, device=GPU) if kept else None
+    Y = x.clone()
+    dg.glu(x, w1, H, Z=Z)
+    dg.gemm(H, w2.t(), Y, beta=1.0)
+    dg.gemm(dy, w2, dH)
+    dX, dW1 = dy.clone(), torch.zeros(2 * F, D, device=GPU)
+    for _ in range(2):       # two batches into one fp32 gradient
+        dg.glu_grad(dH, x, w1, dX=dX if _ == 0 else None, dW=dW1, Z=Z, beta_x=1.0, beta_w=1.0)
+    torch.cuda.synchronize()
+    want = ref.glu_grad(dH.cpu(), X, W1, None if Z is None else Z.cpu(), "silu", dY, None, 1.0, 0,
+                        torch.float32)
+    assert worst(dX, *want["dX"]) <= 1.0
+    value, bound = want["dW"]
+    assert worst(dW1, 2 * value, 2 * bound + 2 ** -22 * value.abs()) <= 1.0
+
+
+CALLS = ["quantize", "gemm_i8", "gemm_i8 many", "gemm_i8 odd", "glu", "glu many", "glu odd",
+         "glu f32", "glu_i8", "glu_i8 many", "glu_grad", "glu_grad odd", "glu_grad f32"]
+
+
+def call_of(name):
+    """(call(stream, workspace), outputs, inputs that a caller may fill anew)"""
+    import dense_gemm_fp32_amd as dg
+    g = gen(len(name))
+    M, F, K = {"many": (700, 528, 320), "odd": (130, 131, 259)}.get(name.split()[-1],
+                                                                   (40, 192, 256))
+    t = torch.float32 if "f32" in name else torch.float16
+    X, W = normal(g, (M, K), t).to(GPU), normal(g, (2 * F, K), t, K ** -0.5).to(GPU)
+    q, w = whole(g, (M, K)).to(GPU), whole(g, (2 * F, K)).to(GPU)
+    xs, ws = scales(g, M).to(GPU), (scales(g, 2 * F) / math.sqrt(K)).to(GPU)
+    if name == "quantize":
+        out = torch.empty(M, K, dtype=torch.int8, device=GPU), torch.empty(M, device=GPU)
+        return (lambda s, v: dg.quantize(X, *out, stream=s)), out, [X]
+    if name.startswith("gemm_i8"):
+        out = torch.empty(M, 2 * F, dtype=t, device=GPU)
+        return (lambda s, v: dg.gemm_i8(q, w, out, x_scale=xs, w_scale=ws, workspace=v,
+                                        stream=s)), (out,), [xs]
+    if name.startswith("glu_grad"):
+        dH = normal(g, (M, F), t, 0.05).to(GPU)
+        out = torch.empty_like(X), torch.empty_like(W)
+        return (lambda s, v: dg.glu_grad(dH, X, W, *out, workspace=v, stream=s)), out, [X, dH]
+    out = torch.empty(M, F, dtype=t, device=GPU)
+    if name.startswith("glu_i8"):
+        return (lambda s, v: dg.glu(q, w, out, x_scale=xs, w_scale=ws, workspace=v,
+                                    stream=s)), (out,), [xs]
+    return (lambda s, v: dg.glu(X, W, out, workspace=v, stream=s)), (out,), [X]
+
+
+def clear(outs):
+    for o in outs:
+        o.fill_(77 if o.dtype == torch.int8 else math.nan)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_repeat_bit_for_bit_on_any_stream(name):
+    call, outs, _ = call_of(name)
+    call(None, None)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    side = torch.cuda.Stream()
+    room = torch.empty(64 << 20, dtype=torch.uint8, device=GPU)
+    for how in ("again", "stream", "raw", "current", "workspace"):
+        clear(outs)
+        torch.cuda.synchronize()
+        if how == "again":
+            call(None, None)
+        elif how == "stream":
+            call(side, None)
+        elif how == "raw":
+            call(side.cuda_stream, None)
+        elif how == "current":
+            with torch.cuda.stream(side):
+                call(None, None)
+        else:
+            room.fill_(255)      # nothing in it needs an initial value
+            call(None, room)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), how
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_in_a_graph(name):
+    """Captured and replayed with new inputs, eager calls and synchronisations
+    between the replays; two graphs alive, each with a workspace of its own."""
+    call, outs, inputs = call_of(name)
+    call(None, None)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        room = torch.empty(64 << 20, dtype=torch.uint8, device=GPU)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(None, room)
+        graphs.append((graph, room))
+    for k in range(4):
+        for t in inputs:
+            t.mul_(-0.75)
+        call(None, None)
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        clear(outs)
+        torch.cuda.synchronize()
+        graphs[k % 2][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), k
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_workspaces_of_the_size_named(name, monkeypatch):
+    """A workspace of the bytes that the *_workspace function names is enough and
+    nothing beyond it is written; one that is smaller is refused."""
+    from dense_gemm_fp32_amd import binding
+    import dense_gemm_fp32_amd as dg
+    if name == "quantize":
+        return
+    call, outs, _ = call_of(name)
+    seen = []
+    plain = binding._call_rows
+
+    def watch(fn, dev, stream, workspace, need, args):
+        seen.append(need)
+        return plain(fn, dev, stream, workspace, need, args)
+    monkeypatch.setattr(binding, "_call_rows", watch)
+    call(None, None)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    need = seen[0]
+    room = torch.full((need + 4096,), 170, dtype=torch.uint8, device=GPU)
+    clear(outs)
+    call(None, room[:need] if need else None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert bool((room[need:] == 170).all())
+    if need:
+        with pytest.raises(dg.GemmError, match="too small"):
+            call(None, room[:need - 256])
+        with pytest.raises(dg.GemmError, match="aligned"):
+            call(None, room[1:])
+
+
+@pytest.mark.parametrize("name", ["gemm_i8 odd", "glu odd", "glu_grad", "glu many"])
+def test_calls_at_once_on_two_streams(name):
+    """Two calls under way at the same time, each with outputs of its own."""
+    first, second = call_of(name), call_of(name)
+    first[0](None, None)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in first[1]]
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    clear(first[1])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (call, outs, _) in zip(streams, (first, second)):
+            call(s, None)
+    torch.cuda.synchronize()
+    for _, outs, _ in (first, second):
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_rows_beyond_32_bits():
+    """Rows more than 2^31 elements from the first."""
+    import dense_gemm_fp32_amd as dg
+    g = gen(1)
+    far = (1 << 30) + 64          # three rows of it
+    K, N = 96, 80
+    X, W = whole(g, (3, K)), whole(g, (2 * N, K))
+    big = torch.zeros(2 * far + K, dtype=torch.int8, device=GPU)
+    x = big.as_strided((3, K), (far, 1))
+    x.copy_(X)
+    y = torch.empty(3, 2 * N, device=GPU)
+    dg.gemm_i8(x, W.to(GPU), y)
+    assert torch.equal(y.cpu().double(), X.double() @ W.double().t())
+    w = big.as_strided((3, K), (far, 1))
+    dg.gemm_i8(W.to(GPU), w, torch.empty(2 * N, 3, device=GPU))
+    out = torch.empty(2 * N, 3, device=GPU)
+    dg.gemm_i8(W.to(GPU), w, out)
+    assert torch.equal(out.cpu().double(), (W.double() @ X.double().t()))
+    del big, x, w
+    t = torch.float16
+    far = (1 << 30) + 8
+    big = torch.zeros(2 * far + 4 * N, dtype=t, device=GPU)
+    Xh, Wh = normal(g, (3, K), t), normal(g, (2 * N, K), t, 0.1)
+    want = ref.glu(Xh, Wh, "gelu", t)
+    h = big.as_strided((3, N), (far, 1))
+    z = torch.empty(3, 2 * N, dtype=t, device=GPU)
+    dg.glu(Xh.to(GPU), Wh.to(GPU), h, act="gelu", Z=z)
+    assert worst(h.cpu(), *want["H"]) <= 1.0
+    z2 = big.as_strided((3, 2 * N), (far, 1))
+    dg.glu(Xh.to(GPU), Wh.to(GPU), torch.empty(3, N, dtype=t, device=GPU), act="gelu", Z=z2)
+    assert torch.equal(z2, z)
+    dH = normal(g, (3, N), t, 0.05).to(GPU)
+    near, apart = torch.empty(3, K, dtype=t, device=GPU), big.as_strided((3, K), (far, 1))
+    dg.glu_grad(dH, Xh.to(GPU), Wh.to(GPU), dX=near, act="gelu", Z=z)
+    z2.copy_(z)
+    dg.glu_grad(dH, Xh.to(GPU), Wh.to(GPU), dX=torch.empty_like(near), act="gelu", Z=z2)
+    dg.glu_grad(dH, Xh.to(GPU), Wh.to(GPU), dX=apart, act="gelu", Z=z)
+    assert torch.equal(apart, near)
+
+
+def test_wrappers_refuse_on_the_gpu():
+    import dense_gemm_fp32_amd as dg
+    h = torch.zeros(4, 8, dtype=torch.float16, device=GPU)
+    q = torch.zeros(4, 8, dtype=torch.int8, device=GPU)
+    w, wq = torch.zeros(6, 8, dtype=torch.float16, device=GPU), torch.zeros(6, 8, dtype=torch.int8,
+                                                                            device=GPU)
+    out = torch.zeros(4, 3, dtype=torch.float16, device=GPU)
+    for match, call in (
+            ("Z goes", lambda: dg.glu(q, wq, out, Z=torch.zeros(4, 6, dtype=torch.float16,
+                                                                device=GPU))),
+            ("x_scale", lambda: dg.glu(h, w, out, x_scale=torch.ones(4, device=GPU))),
+            ("W must be", lambda: dg.glu(h, wq, out)), ("W must be", lambda: dg.glu(q, w, out)),
+            ("W must be 6 x 8", lambda: dg.glu(h, w[:5], out)),
+            ("H must be", lambda: dg.glu(h[:3], w, out)),
+            ("rows", lambda: dg.glu(h, w.t().contiguous().t(), out)),
+            ("x_scale must be 4", lambda: dg.gemm_i8(q, wq, torch.zeros(4, 6, device=GPU),
+                                                     x_scale=torch.ones(3, device=GPU))),
+            ("w_scale must be 6", lambda: dg.gemm_i8(q, wq, torch.zeros(4, 6, device=GPU),
+                                                     w_scale=torch.ones(6, device=GPU).half())),
+            ("act must be", lambda: dg.glu(h, w, out, act="tanh")),
+            ("dW must be", lambda: dg.glu_grad(out, h, w, dW=w.double())),
+            ("Q must be", lambda: dg.quantize(h, torch.zeros(4, 7, dtype=torch.int8, device=GPU))),
+            ("scale must be", lambda: dg.quantize(h, q, torch.zeros(5, device=GPU)))):
+        with pytest.raises(ValueError, match=match):
+            call()
+    with pytest.raises(dg.GemmError, match="131071"):
+        dg.gemm_i8(torch.zeros(1, 131072, dtype=torch.int8, device=GPU),
+                   torch.zeros(1, 131072, dtype=torch.int8, device=GPU),
+                   torch.zeros(1, 1, device=GPU))

@@ -604,8 +604,10 @@ def _act(act):
 
 
 def _at_16(X, ldx, W, ldw, eb):
-    """Whether every row of X and of W starts at a multiple of 16 bytes."""
-    return ((X.data_ptr() | W.data_ptr() | ldx * eb | ldw * eb) & 15) == 0
+    """Whether every row of X and of W starts at a multiple of 16 bytes, less than
+    2^23 from the one before."""
+    ldx, ldw = ldx * eb, ldw * eb
+    return ((X.data_ptr() | W.data_ptr() | ldx | ldw) & 15) == 0 and (ldx | ldw) < 1 << 23
 
 
 def quantize(X, Q=None, scale=None, stream=None):

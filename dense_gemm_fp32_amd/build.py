@@ -27,7 +27,7 @@ POISON_BUILD_DIR = os.path.join(HERE, "_build_lds_poison")
 SOURCES = ["api.hip", "gemm_f32.hip", "gemm_f16.hip", "gemm_valu.hip", "scale.hip", "splitk.hip",
            "pack.hip", "probe.hip", "gemm_f16_lora.hip", "lora.hip",
            "moe.hip", "rows_api.hip",
-           "quant.hip", "proj.hip", "proj_api.hip"]
+           "quant.hip", "proj.hip", "gemm_i8.hip", "glu_f16.hip", "glu_i8.hip", "proj_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -58,7 +58,8 @@ def _compile(src, verbose=False, build_dir=BUILD_DIR, extra=()):
 # build verifies that no compiler-generated instruction in these sources
 # touches it: the asm's m0 writes then cannot disturb compiled code.  The
 # same assembly is checked for spills (and that of gemm_valu.hip).
-M0_ASM_SOURCES = ["gemm_f16.hip", "gemm_f16_lora.hip", "gemm_f32.hip"]
+M0_ASM_SOURCES = ["gemm_f16.hip", "gemm_f16_lora.hip", "gemm_f32.hip", "gemm_i8.hip",
+                  "glu_f16.hip", "glu_i8.hip"]
 SPILL_ONLY_SOURCES = ["gemm_valu.hip", "lora.hip", "moe.hip", "proj.hip", "quant.hip"]
 
 
@@ -132,6 +133,9 @@ TILE_OCCUPANCY = (
     ("H16TileILi256ELi256ELi64E", 1, 8),
     ("H16TileILi128ELi128ELi32E", 2, 4),
     ("H16TileILi64ELi128ELi32E", 3, 2),
+    ("H16TileILi256ELi256ELi128E", 1, 8),
+    ("H16TileILi128ELi128ELi64E", 2, 4),
+    ("H16TileILi64ELi128ELi64E", 3, 2),
 )
 
 

@@ -74,6 +74,9 @@
 // The kernel exists in two forms, compiled by one source each: the plain
 // product (gemm_f16.hip), and the product whose accumulators start from a
 // low-rank term of each row's own adapter (gemm_f16_lora.hip; LowRank below).
+// Its tiles, loads and main loop also carry the products of 8-bit integers and
+// the gated blocks (proj_tile.hpp): a tile of elements of one byte holds twice
+// the k in the same bytes, loads and fragments.
 #pragma once
 
 #include <type_traits>
@@ -86,11 +89,13 @@ namespace dgemm {
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
+// EB: bytes per element, 2 (halves) or 1 (8-bit integers, BK twice as long).
 template <int BM_, int BN_, int BK_, int WAVES_M_, int WAVES_N_, int STAGES_, int GROUP_M_,
-          int MF_ = 32>
+          int MF_ = 32, int EB_ = 2>
 struct H16Tile {
+  static constexpr int EB = EB_;
   static constexpr int MF = MF_;                       // MFMA block edge: 32x32x16 or 16x16x32
-  static constexpr int KM = 512 / MF;                  // k per MFMA
+  static constexpr int KM = 1024 / (MF * EB);          // k per MFMA
   static constexpr int BM = BM_, BN = BN_, BK = BK_;
   static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int STAGES = STAGES_;
@@ -103,10 +108,12 @@ struct H16Tile {
   static constexpr int FN = WTN / MF;
   static constexpr int NG = WTM / 32;                   // 32-row epilogue groups per wave
   static constexpr int SUB = BK / KM;                   // MFMA k sub-steps per K step
-  typedef typename std::conditional<MF == 32, f32x16, f32x4>::type Acc;
+  typedef typename std::conditional<
+      EB == 1, typename std::conditional<MF == 32, i32x16, i32x4>::type,
+      typename std::conditional<MF == 32, f32x16, f32x4>::type>::type Acc;
   static constexpr int ACC_N = MF == 32 ? 16 : 4;
-  static constexpr int A_BYTES = BM * BK * 2;           // a slot's A region
-  static constexpr int B_BYTES = BK * BN * 2;           // ... and B region
+  static constexpr int A_BYTES = BM * BK * EB;          // a slot's A region
+  static constexpr int B_BYTES = BK * BN * EB;          // ... and B region
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int QA = A_BYTES / 1024;             // 1 KB wave loads per A tile
   static constexpr int QB = B_BYTES / 1024;
@@ -146,14 +153,16 @@ struct H16Tile {
 //      chunk bits 2-3 with kr % 4 puts the four rows' 64-byte pieces in the
 //      four quarters of the window (rows of 128 bytes, two to a window: bit 2
 //      with (kr/2) % 2).
-template <int EXT, int BK, bool KMAJ>
+template <int EXT, int BK, bool KMAJ, int EB_ = 2>
 struct HRegion {
   static constexpr bool K_MAJOR = KMAJ;
   static constexpr int EXTENT = EXT;
-  static constexpr int ROW = KMAJ ? 2 * BK : 2 * EXT;      // bytes per LDS row
+  static constexpr int EB = EB_;
+  static constexpr int ROW = KMAJ ? EB * BK : EB * EXT;    // bytes per LDS row
   static constexpr int CH = ROW / 16;                       // 16-byte chunks per row
   static constexpr int RPW = ROW >= 256 ? 1 : 256 / ROW;    // rows per 256-byte window
   static constexpr int READS = KMAJ ? 1 : 2;                // LDS reads per fragment
+  static_assert(KMAJ || EB == 2, "transpose reads are of halves");
   static_assert(KMAJ || ROW >= 128, "index-major rows of at least 128 bytes");
   static_assert(!KMAJ || (32 % RPW == 0 && (32 / RPW) % CH == 0),
                 "the swizzle repeats every 32 rows");
@@ -164,7 +173,7 @@ struct HRegion {
     else return 4 * ((row >> 1) & 1);
   }
 
-  // Tile-relative index and k of the 8 elements behind 16-byte chunk
+  // Tile-relative index and k of the 16 / EB elements behind 16-byte chunk
   // (q, lane) of the region (lane L of a 1 KB direct load writes bytes
   // q*1024 + 16L .. +15).
   __device__ static __forceinline__ void chunk(int q, int lane, int &idx, int &kk) {
@@ -173,7 +182,7 @@ struct HRegion {
     const int c = ((o % ROW) / 16) ^ swz(row);
     if constexpr (KMAJ) {
       idx = row;
-      kk = 8 * c;
+      kk = 16 / EB * c;
     } else {
       kk = row;
       idx = 8 * c;
@@ -183,11 +192,31 @@ struct HRegion {
 
 // The two regions of tile T when A is stored transposed (TA) and/or B is
 // (TB), and the LDS reads per k sub-step of one wave.
-template <class T, bool TA_, bool TB_>
+//
+// PAIR (B stored transposed): the tile covers BN/2 columns of two matrices, B
+// and the one `B_up` behind it.  Of the columns of a wave's sub-tile the first
+// half comes from B, the second from the other, the same columns of both, so
+// that a wave holds both sums of an element.
+template <class T, bool TA_, bool TB_, bool PAIR_ = false>
 struct HLayout {
-  static constexpr bool TA = TA_, TB = TB_;
-  typedef HRegion<T::BM, T::BK, !TA_> RA;
-  typedef HRegion<T::BN, T::BK, TB_> RB;
+  static constexpr bool TA = TA_, TB = TB_, PAIR = PAIR_;
+  static constexpr int COLS = PAIR ? T::BN / 2 : T::BN;   // columns of the result
+  typedef HRegion<T::BM, T::BK, !TA_, T::EB> RA;
+  typedef HRegion<T::BN, T::BK, TB_, T::EB> RB;
+  static_assert(!PAIR || (TB && (T::WTN / 2) % (1024 / RB::ROW) == 0),
+                "a 1 KB load reads rows of one of the two matrices");
+  // column of the result behind row `idx` of the B region, and whether it is
+  // the second matrix's
+  __device__ static __forceinline__ int column(int idx) {
+    return PAIR ? idx / T::WTN * (T::WTN / 2) + idx % (T::WTN / 2) : idx;
+  }
+  __device__ static __forceinline__ bool up(int idx) {
+    return PAIR && idx % T::WTN >= T::WTN / 2;
+  }
+  // element offset of the matrix behind 1 KB load q of the region
+  __device__ static __forceinline__ size_t matrix(const GemmParams &p, int q) {
+    return up(q * (1024 / RB::ROW)) ? (size_t)p.N * (size_t)p.ldb : (size_t)0;
+  }
   static constexpr int NREAD = T::FM * RA::READS + T::FN * RB::READS;
 };
 
@@ -223,7 +252,7 @@ __device__ __forceinline__ uint32_t direct_offset(int idx, int kk, int idx0, int
   int g = idx0 + idx;
   if constexpr (R::K_MAJOR) {
     g = g < ext ? g : ext - 1;
-    return 2u * (uint32_t)((g - idx0) * ld + kk);
+    return (uint32_t)R::EB * (uint32_t)((g - idx0) * ld + kk);
   } else {
     g = g + 8 <= ext ? g : ext - 8;
     return 2u * (uint32_t)(kk * ld + (g - idx0));
@@ -231,11 +260,13 @@ __device__ __forceinline__ uint32_t direct_offset(int idx, int kk, int idx0, int
 }
 
 // First element of a K step's tile of an operand stored with leading
-// dimension ld.
+// dimension ld (`skip` elements into X).
 template <class R>
-__device__ __forceinline__ const uint16_t *tile_base(const void *X, int idx0, int k0, int ld) {
-  const uint16_t *x = static_cast<const uint16_t *>(X);
-  return R::K_MAJOR ? x + (size_t)idx0 * (size_t)ld + k0 : x + (size_t)k0 * (size_t)ld + idx0;
+__device__ __forceinline__ const char *tile_base(const void *X, int idx0, int k0, int ld,
+                                                 size_t skip = 0) {
+  const char *x = static_cast<const char *>(X) + R::EB * skip;
+  return R::K_MAJOR ? x + R::EB * ((size_t)idx0 * (size_t)ld + k0)
+                    : x + R::EB * ((size_t)k0 * (size_t)ld + idx0);
 }
 
 // The direct path's conditions for one operand: 32-bit offsets, and for an
@@ -266,7 +297,7 @@ __device__ __forceinline__ void direct_setup(const GemmParams &p, int m0, int n0
     for (int j = 0; j < T::QB_W; ++j) {
       int idx, kk;
       L::RB::chunk(wc * T::QB_W + j, lane, idx, kk);
-      d.b[r * T::QB_W + j] = direct_offset<typename L::RB>(idx, kk, n0, p.N, p.ldb);
+      d.b[r * T::QB_W + j] = direct_offset<typename L::RB>(L::column(idx), kk, n0, p.N, p.ldb);
     }
   }
 }
@@ -276,7 +307,9 @@ __device__ __forceinline__ void direct_issue(const GemmParams &p, const DirectAd
                                              int n0, int k0, uint32_t slot_addr) {
   const int wave = wave_id();
   const BufRsrc ra = buffer_rsrc(tile_base<typename L::RA>(p.A, m0, k0, p.lda));
-  const BufRsrc rb = buffer_rsrc(tile_base<typename L::RB>(p.B, n0, k0, p.ldb));
+  auto rb = [&](int q) {
+    return buffer_rsrc(tile_base<typename L::RB>(p.B, n0, k0, p.ldb, L::matrix(p, q)));
+  };
   if constexpr (kSplitLoaders<T>) {
     if (wave < 4) return;
 #pragma unroll
@@ -287,7 +320,7 @@ __device__ __forceinline__ void direct_issue(const GemmParams &p, const DirectAd
         buffer_load16(d.a[r * T::QA_W + j], ra, slot_addr + (uint32_t)((w * T::QA_W + j) * 1024));
 #pragma unroll
       for (int j = 0; j < T::QB_W; ++j)
-        buffer_load16(d.b[r * T::QB_W + j], rb,
+        buffer_load16(d.b[r * T::QB_W + j], rb(w * T::QB_W + j),
                       slot_addr + (uint32_t)(T::A_BYTES + (w * T::QB_W + j) * 1024));
     }
   } else {
@@ -296,7 +329,8 @@ __device__ __forceinline__ void direct_issue(const GemmParams &p, const DirectAd
       buffer_load16(d.a[j], ra, slot_addr + (uint32_t)((wave * T::QA_W + j) * 1024));
 #pragma unroll
     for (int j = 0; j < T::QB_W; ++j)
-      buffer_load16(d.b[j], rb, slot_addr + (uint32_t)(T::A_BYTES + (wave * T::QB_W + j) * 1024));
+      buffer_load16(d.b[j], rb(wave * T::QB_W + j),
+                    slot_addr + (uint32_t)(T::A_BYTES + (wave * T::QB_W + j) * 1024));
   }
 }
 
@@ -351,7 +385,20 @@ template <class R>
 __device__ __forceinline__ u32x4 staged_chunk(const void *X, int ld, int idx0, int ext, int k0,
                                               int K, int idx, int kk, int w) {
   const int g = idx0 + idx, gk = k0 + kk;
-  if constexpr (R::K_MAJOR) {
+  if constexpr (R::EB == 1) {
+    // 8-bit integers: rows that start at 16 bytes only, so the 16 bytes that
+    // hold a row's last elements are one aligned granule, in the same page as
+    // them; what it holds behind the row is cleared.
+    const uint8_t *src = static_cast<const uint8_t *>(X) + (size_t)g * (size_t)ld + gk;
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    if (g < ext && gk < K) v = *reinterpret_cast<const u32x4 *>(src);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int left = K - gk - 4 * e;
+      if (left < 4) v[e] &= left > 0 ? (1u << (8 * left)) - 1u : 0u;
+    }
+    return v;
+  } else if constexpr (R::K_MAJOR) {
     const uint16_t *src = static_cast<const uint16_t *>(X) + (size_t)g * (size_t)ld + gk;
     const bool ok = g < ext;
     if (ok && gk + 7 < K) return load8_width(src, w);
@@ -381,7 +428,10 @@ __device__ __forceinline__ void reg_load(const GemmParams &p, int m0, int n0, in
   for (int j = 0; j < T::QB_W; ++j) {
     int idx, kk;
     L::RB::chunk(wave * T::QB_W + j, lane, idx, kk);
-    t.b[j] = staged_chunk<typename L::RB>(p.B, p.ldb, n0, p.N, k0, p.K, idx, kk, vb);
+    const void *B = p.B;
+    if constexpr (L::PAIR)
+      B = tile_base<typename L::RB>(p.B, 0, 0, p.ldb, L::matrix(p, wave * T::QB_W + j));
+    t.b[j] = staged_chunk<typename L::RB>(B, p.ldb, n0, p.N, k0, p.K, L::column(idx), kk, vb);
   }
 }
 
@@ -489,20 +539,24 @@ __device__ __forceinline__ void frag_read(const char *slot, const FragAddr<T, L>
   for (int bi = 1; bi < T::FM; ++bi) fr.a[bi] = op_read<T::MF>(slot, f.a, s, bi);
 }
 
+// One MFMA of tile T: its A fragment, B fragment and accumulators.
+template <class T>
+__device__ __forceinline__ typename T::Acc mma(f16x8 a, f16x8 b, typename T::Acc c) {
+  if constexpr (T::EB == 1) {
+    const i32x4 x = __builtin_bit_cast(i32x4, a), y = __builtin_bit_cast(i32x4, b);
+    if constexpr (T::MF == 32) return __builtin_amdgcn_mfma_i32_32x32x32_i8(x, y, c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
+  } else if constexpr (T::MF == 32) return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
 // MFMAs for block rows [BI0, BI1) of one sub-step.
 template <class T, int BI0, int BI1>
 __device__ __forceinline__ void mfma_rows(const Frag<T> &fr, typename T::Acc (&acc)[T::FM][T::FN]) {
 #pragma unroll
   for (int bi = BI0; bi < BI1; ++bi)
 #pragma unroll
-    for (int bj = 0; bj < T::FN; ++bj) {
-      if constexpr (T::MF == 32)
-        acc[bi][bj] =
-            __builtin_amdgcn_mfma_f32_32x32x16_f16(fr.a[bi], fr.b[bj], acc[bi][bj], 0, 0, 0);
-      else
-        acc[bi][bj] =
-            __builtin_amdgcn_mfma_f32_16x16x32_f16(fr.a[bi], fr.b[bj], acc[bi][bj], 0, 0, 0);
-    }
+    for (int bj = 0; bj < T::FN; ++bj) acc[bi][bj] = mma<T>(fr.a[bi], fr.b[bj], acc[bi][bj]);
 }
 
 // Scheduling pattern for a region holding NM MFMAs and NR LDS reads: the
@@ -1129,7 +1183,7 @@ __device__ __forceinline__ void zero_acc(typename T::Acc (&acc)[T::FM][T::FN]) {
 #pragma unroll
     for (int bj = 0; bj < T::FN; ++bj)
 #pragma unroll
-      for (int r = 0; r < T::ACC_N; ++r) acc[bi][bj][r] = 0.0f;
+      for (int r = 0; r < T::ACC_N; ++r) acc[bi][bj][r] = 0;
 }
 
 // All sub-steps of one K step from LDS slot `slot`.  On entry fr[0] holds
@@ -1161,8 +1215,7 @@ __device__ __forceinline__ void kstep_rolling(const char *slot, const char *next
       for (int bi = 0; bi < T::FM; ++bi) {
 #pragma unroll
         for (int bj = 0; bj < T::FN; ++bj)
-          acc[bi][bj] =
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(fr.a[bi], fr.b[bj], acc[bi][bj], 0, 0, 0);
+          acc[bi][bj] = mma<T>(fr.a[bi], fr.b[bj], acc[bi][bj]);
         fr.a[bi] = op_read<T::MF>(slot, fa.a, s + 1, bi);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -1171,8 +1224,7 @@ __device__ __forceinline__ void kstep_rolling(const char *slot, const char *next
       for (int bi = 0; bi < HALF; ++bi)
 #pragma unroll
         for (int bj = 0; bj < T::FN; ++bj)
-          acc[bi][bj] =
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(fr.a[bi], fr.b[bj], acc[bi][bj], 0, 0, 0);
+          acc[bi][bj] = mma<T>(fr.a[bi], fr.b[bj], acc[bi][bj]);
       __builtin_amdgcn_sched_barrier(0);
       next();
 #pragma unroll
@@ -1183,8 +1235,7 @@ __device__ __forceinline__ void kstep_rolling(const char *slot, const char *next
       for (int bi = HALF; bi < T::FM; ++bi) {
 #pragma unroll
         for (int bj = 0; bj < T::FN; ++bj)
-          acc[bi][bj] =
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(fr.a[bi], fr.b[bj], acc[bi][bj], 0, 0, 0);
+          acc[bi][bj] = mma<T>(fr.a[bi], fr.b[bj], acc[bi][bj]);
         fr.a[bi] = op_read<T::MF>(next_slot, fa.a, 0, bi);
       }
       __builtin_amdgcn_sched_barrier(0);

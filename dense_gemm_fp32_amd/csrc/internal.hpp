@@ -197,6 +197,16 @@ struct PackChoice {
 };
 PackChoice pack_choice(const Call &c, int eb, Plan (*plan)(const Call &));
 
+// Copies of one or two matrices, byte for byte, to rows of whole 16 bytes, the
+// last filled up with zeros (dst NULL: none).
+struct RowCopy {
+  const void *src;
+  long long pitch, row_bytes;   // bytes between src's rows, and of a row
+  int rows;
+  void *dst;
+};
+hipError_t launch_row_copies(const RowCopy &a, const RowCopy &b, hipStream_t stream);
+
 // Workspace a call may take: its fixed region, else its limit, else the
 // pool's per-call cap.
 long long ws_available(const Call &c);
@@ -340,6 +350,12 @@ struct ProjCall {
   int lddh;
   hipStream_t stream;
 };
+// Whether every row of a matrix with elements of eb bytes starts at 16 bytes, and
+// its rows are near enough for a tile's 32-bit offsets.
+inline bool rows_at_16(const void *p, int ld, int eb) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (long long)ld * eb % 16 == 0 &&
+         (long long)ld * eb < (1LL << 23);
+}
 size_t proj_workspace(const ProjCall &c);
 hipError_t launch_proj(const ProjCall &c, void *ws);
 

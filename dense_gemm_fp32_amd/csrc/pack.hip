@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kPackThreads) void pack_rows(PackJob j0, PackJob j1
     for (int i = 0; i < 4; ++i) {
       uint32_t v = r == 0 ? f[i] : __builtin_amdgcn_alignbyte(f[i + 1], f[i], (uint32_t)r);
       if (4 * i >= valid) v = 0u;
-      else if (4 * i + 4 > valid) v &= 0xffffu;     // fp16: one half of this dword is in the row
+      else if (4 * i + 4 > valid) v &= (1u << (8 * (int)(valid - 4 * i))) - 1u;
       w[i] = v;
     }
     *reinterpret_cast<u32x4 *>(dst + u * 16) = w;
@@ -221,6 +221,34 @@ Plan plan_packed(const Call &c, int eb, Plan (*plan)(const Call &)) {
   return pl;
 }
 
+namespace {
+
+hipError_t pack(const PackJob &ja, const PackJob &jb, hipStream_t stream) {
+  const long long total = ja.n + jb.n;
+  long long blocks = (total + kPackThreads - 1) / kPackThreads;
+  if (blocks > kPackMaxBlocks) blocks = kPackMaxBlocks;
+  if (blocks < 1) blocks = 1;
+  const dim3 g((unsigned)blocks), b(kPackThreads);
+  if (ja.n >= (1LL << 32) || jb.n >= (1LL << 32))
+    hipLaunchKernelGGL(pack_rows<true>, g, b, 0, stream, ja, jb);
+  else
+    hipLaunchKernelGGL(pack_rows<false>, g, b, 0, stream, ja, jb);
+  return hipGetLastError();
+}
+
+PackJob job_of(const RowCopy &c) {
+  if (c.dst == nullptr) return PackJob{};
+  const unsigned cpr = (unsigned)((c.row_bytes + 15) / 16);
+  return PackJob{static_cast<const char *>(c.src), static_cast<char *>(c.dst), c.pitch,
+                 c.row_bytes, cpr, (long long)c.rows * cpr};
+}
+
+}  // namespace
+
+hipError_t launch_row_copies(const RowCopy &a, const RowCopy &b, hipStream_t stream) {
+  return pack(job_of(a), job_of(b), stream);
+}
+
 hipError_t run_packed(const Call &c, int eb, Plan (*plan)(const Call &),
                       hipError_t (*launch)(const Call &)) {
   const PackChoice pk = pack_choice(c, eb, plan);
@@ -258,16 +286,7 @@ hipError_t run_packed(const Call &c, int eb, Plan (*plan)(const Call &),
   // The GEMM's own workspace (split K) is the rest of the allocation.
   in.ws_fixed = base + pk.a_bytes + pk.b_bytes;
   in.ws_fixed_bytes = pk.bytes - pk.a_bytes - pk.b_bytes;
-  const long long total = ja.n + jb.n;
-  long long blocks = (total + kPackThreads - 1) / kPackThreads;
-  if (blocks > kPackMaxBlocks) blocks = kPackMaxBlocks;
-  if (blocks < 1) blocks = 1;
-  const dim3 g((unsigned)blocks), b(kPackThreads);
-  if (ja.n >= (1LL << 32) || jb.n >= (1LL << 32))
-    hipLaunchKernelGGL(pack_rows<true>, g, b, 0, c.stream, ja, jb);
-  else
-    hipLaunchKernelGGL(pack_rows<false>, g, b, 0, c.stream, ja, jb);
-  hipError_t e = hipGetLastError();
+  hipError_t e = pack(ja, jb, c.stream);
   if (e == hipSuccess) e = launch(in);
   const hipError_t f = workspace_free(c, ws);
   return e != hipSuccess ? e : f;

@@ -32,29 +32,76 @@ ProjParams params_of(const ProjCall &c) {
 }
 
 template <typename T, typename TO, int OUT, int NF, int NB>
-hipError_t skinny(const ProjCall &c) {
+hipError_t skinny(const ProjParams &p, hipStream_t stream) {
   constexpr int BC = OUT == kScaled ? 16 * NF : 8 * NF;
-  const dim3 g((unsigned)((c.N + BC - 1) / BC), (unsigned)((c.M + 16 * NB - 1) / (16 * NB)));
+  const dim3 g((unsigned)((p.N + BC - 1) / BC), (unsigned)((p.M + 16 * NB - 1) / (16 * NB)));
   if (g.y > 65535) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((proj_skinny<T, TO, OUT, NF, NB, 1, 8>), g, dim3(8 * kWave), 0, c.stream,
-                     params_of(c));
+  hipLaunchKernelGGL((proj_skinny<T, TO, OUT, NF, NB, 1, 8>), g, dim3(8 * kWave), 0, stream, p);
   return hipGetLastError();
 }
 
 template <typename T, typename TO, int OUT>
-hipError_t run(const ProjCall &c) {
+hipError_t run_skinny(const ProjParams &p, hipStream_t stream) {
   constexpr int NF = OUT == kScaled ? 1 : 2;
-  return c.M <= 16 ? skinny<T, TO, OUT, NF, 1>(c) : skinny<T, TO, OUT, NF, 4>(c);
+  return p.M <= 16 ? skinny<T, TO, OUT, NF, 1>(p, stream) : skinny<T, TO, OUT, NF, 4>(p, stream);
 }
 
 template <typename TO>
-hipError_t run_out(const ProjCall &c) {
+hipError_t run_skinny(const ProjCall &c, const ProjParams &p) {
   if (c.i8) {
-    if (!c.gated) return run<int8_t, TO, kScaled>(c);
-    return run<int8_t, TO, kGated>(c);
+    if (!c.gated) return run_skinny<int8_t, TO, kScaled>(p, c.stream);
+    return run_skinny<int8_t, TO, kGated>(p, c.stream);
   }
-  if (c.dH != nullptr) return run<TO, TO, kSlopes>(c);
-  return run<TO, TO, kGated>(c);
+  if (c.dH != nullptr) return run_skinny<TO, TO, kSlopes>(p, c.stream);
+  return run_skinny<TO, TO, kGated>(p, c.stream);
+}
+
+constexpr int kSkinnyRows = 64;
+
+int bytes_of(const ProjCall &c) { return c.i8 ? 1 : (c.half ? 2 : 4); }
+
+// Whether a call takes the tiles: more rows than the other kernel is for, and rows
+// short enough that a tile's offsets fit 32 bits.
+bool tiled(const ProjCall &c) {
+  return c.M > kSkinnyRows && (c.i8 || c.half) && (long long)c.K * bytes_of(c) < kTileRowBytes;
+}
+
+struct ProjSpace {
+  char *X, *W;       // copies with rows of whole 16 bytes
+};
+
+size_t carve(const ProjCall &c, void *base, ProjSpace *s) {
+  Carve w(base);
+  *s = ProjSpace{};
+  if (!tiled(c) || c.aligned) return 0;
+  const size_t row = ((size_t)c.K * bytes_of(c) + 15) / 16 * 16;
+  s->X = w.take<char>(row * (size_t)c.M);
+  s->W = w.take<char>(row * (size_t)c.N * (c.gated ? 2 : 1));
+  return w.used;
+}
+
+hipError_t run_tiles(const ProjCall &c, ProjParams p, const ProjSpace &s) {
+  if (!c.aligned) {
+    const int eb = bytes_of(c);
+    const long long row = (long long)c.K * eb;
+    RowCopy x = {c.X, (long long)c.ldx * eb, row, c.M, s.X};
+    RowCopy w = {c.W, (long long)c.ldw * eb, row, c.gated ? 2 * c.N : c.N, s.W};
+    if (rows_at_16(c.X, c.ldx, eb)) x.dst = nullptr;
+    if (rows_at_16(c.W, c.ldw, eb)) w.dst = nullptr;
+    const hipError_t e = launch_row_copies(x, w, c.stream);
+    if (e != hipSuccess) return e;
+    const int ld = (int)((row + 15) / 16 * 16 / eb);
+    if (x.dst != nullptr) {
+      p.X = s.X;
+      p.ldx = ld;
+    }
+    if (w.dst != nullptr) {
+      p.W = s.W;
+      p.ldw = ld;
+    }
+  }
+  if (!c.i8) return launch_glu_f16(p, c.dH != nullptr, c.stream);
+  return c.gated ? launch_glu_i8(p, c.half, c.stream) : launch_proj_i8(p, c.half, c.stream);
 }
 
 // Z[m, f], Z[m, F + f] := dH * u * act'(g), dH * act(g), from g and u that the
@@ -146,10 +193,32 @@ size_t product_bytes(const GluGradCall &c, Call g) {
   return most;
 }
 
+// The forward pass once more, up to [dG dU].
+ProjCall forward_of(const GluGradCall &c, void *D, int ldd) {
+  ProjCall f = {};
+  f.half = c.half;
+  f.gated = true;
+  f.aligned = c.aligned;
+  f.M = c.M;
+  f.N = c.F;
+  f.K = c.K;
+  f.act = c.act;
+  f.X = c.X;
+  f.ldx = c.ldx;
+  f.W = c.W;
+  f.ldw = c.ldw;
+  f.Z = D;
+  f.ldz = ldd;
+  f.dH = c.dH;
+  f.lddh = c.lddh;
+  f.stream = c.stream;
+  return f;
+}
+
 struct GradSpace {
   void *D;         // [dG dU], M rows of ldd elements
   int ldd;
-  char *W;         // the products', one after the other
+  char *W;         // the forward pass's and the products', one after the other
   size_t w_bytes;
 };
 
@@ -158,7 +227,7 @@ size_t carve(const GluGradCall &c, void *base, GradSpace *s) {
   s->ldd = (2 * c.F + 7) / 8 * 8;
   const size_t n = (size_t)c.M * (size_t)s->ldd;
   s->D = c.half ? (void *)w.take<_Float16>(n) : (void *)w.take<float>(n);
-  s->w_bytes = 0;
+  s->w_bytes = c.Z != nullptr ? 0 : proj_workspace(forward_of(c, nullptr, s->ldd));
   if (c.dX != nullptr) {
     const size_t n = product_bytes(c, product_x(c, nullptr, s->ldd));
     s->w_bytes = n > s->w_bytes ? n : s->w_bytes;
@@ -173,10 +242,17 @@ size_t carve(const GluGradCall &c, void *base, GradSpace *s) {
 
 }  // namespace
 
-size_t proj_workspace(const ProjCall &) { return 0; }
+size_t proj_workspace(const ProjCall &c) {
+  ProjSpace s;
+  return carve(c, nullptr, &s);
+}
 
-hipError_t launch_proj(const ProjCall &c, void *) {
-  return c.half ? run_out<_Float16>(c) : run_out<float>(c);
+hipError_t launch_proj(const ProjCall &c, void *ws) {
+  ProjSpace s;
+  carve(c, ws, &s);
+  const ProjParams p = params_of(c);
+  if (tiled(c)) return run_tiles(c, p, s);
+  return c.half ? run_skinny<_Float16>(c, p) : run_skinny<float>(c, p);
 }
 
 size_t glu_grad_workspace(const GluGradCall &c) {
@@ -192,23 +268,7 @@ hipError_t launch_glu_grad(const GluGradCall &c, void *ws) {
     e = c.half ? slopes(c, static_cast<_Float16 *>(s.D), s.ldd)
                : slopes(c, static_cast<float *>(s.D), s.ldd);
   } else {
-    ProjCall f = {};
-    f.half = c.half;
-    f.gated = true;
-    f.M = c.M;
-    f.N = c.F;
-    f.K = c.K;
-    f.act = c.act;
-    f.X = c.X;
-    f.ldx = c.ldx;
-    f.W = c.W;
-    f.ldw = c.ldw;
-    f.Z = s.D;
-    f.ldz = s.ldd;
-    f.dH = c.dH;
-    f.lddh = c.lddh;
-    f.stream = c.stream;
-    e = launch_proj(f, nullptr);
+    e = launch_proj(forward_of(c, s.D, s.ldd), s.W);
   }
   if (e != hipSuccess) return e;
   for (int w = 0; w < 2; ++w) {

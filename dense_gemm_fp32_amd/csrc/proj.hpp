@@ -69,6 +69,14 @@ __device__ __forceinline__ void finish(const ProjParams &p, int m, int n, float 
   }
 }
 
+// Kernels of many rows (gemm_i8.hip, glu_f16.hip, glu_i8.hip): rows of X and W
+// start at 16 bytes and are less than kTileRowBytes apart, so that a tile's
+// offsets fit 32 bits.  half: outputs of fp16, else fp32; slopes: kSlopes.
+constexpr long long kTileRowBytes = 1 << 23;
+hipError_t launch_proj_i8(const ProjParams &p, bool half, hipStream_t stream);
+hipError_t launch_glu_i8(const ProjParams &p, bool half, hipStream_t stream);
+hipError_t launch_glu_f16(const ProjParams &p, bool slopes, hipStream_t stream);
+
 // ---------------------------------------------------------------- few rows
 
 // grid: (columns / BC, rows / BT).  A workgroup's waves divide K among

@@ -9,6 +9,7 @@ namespace {
 
 using dgemm::GluGradCall;
 using dgemm::ProjCall;
+using dgemm::rows_at_16;
 using dgemm::Space;
 
 int at_least_one(int n) { return n > 1 ? n : 1; }
@@ -24,11 +25,6 @@ hipStream_t stream_of(void *s) { return static_cast<hipStream_t>(s); }
 hipError_t scale(bool half, int M, int N, float beta, void *C, int ldc, hipStream_t s) {
   return half ? dgemm::launch_scale_f16(M, N, beta, static_cast<uint16_t *>(C), ldc, s)
               : dgemm::launch_scale_f32(M, N, beta, static_cast<float *>(C), ldc, s);
-}
-
-// Whether every row of a matrix with elements of eb bytes starts at 16 bytes.
-bool rows_at_16(const void *p, int ld, int eb) {
-  return dgemm::aligned_to(p, 16) && ((long long)ld * eb) % 16 == 0;
 }
 
 int run(ProjCall &c, void *ws, size_t ws_bytes, int base) {

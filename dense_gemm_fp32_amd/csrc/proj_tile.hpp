@@ -1,0 +1,204 @@
+// proj_tile.hpp -- products of 8-bit integers and gated blocks of many rows, on
+// the tiles, direct loads and main loop of gemm_f16_kernel.hpp.
+//
+// X and W are both k-contiguous, so a tile of 8-bit integers is byte for byte
+// the fp16 tile of half its k: the same loads, LDS layout and fragment reads
+// feed v_mfma_i32_16x16x64_i8 (32x32x32) in place of the fp16 instruction, at
+// twice the products per cycle.  Sums are 32-bit integers, exact in any order.
+//
+// A gated block's tile covers the gate and the up rows of the same BN/2 columns
+// (HLayout's PAIR), so both sums of an element meet in its wave, and activation,
+// product and scales happen on the way from the accumulators to memory; nothing
+// of G and U is written unless it is wanted.
+//
+// Rows of X and W start at 16 bytes here (the launch copies others to rows
+// that do); a partial last step of k goes through registers with a mask.
+#pragma once
+
+#include "gemm_f16_kernel.hpp"
+#include "proj.hpp"
+
+namespace dgemm {
+
+// Four values from / to four neighbouring elements.
+template <typename TO, bool VEC>
+__device__ __forceinline__ f32x4 load4(const TO *p, int count) {
+  f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (VEC && count >= 4) {
+    if constexpr (sizeof(TO) == 2) {
+      const f16x4 h = *reinterpret_cast<const f16x4 *>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
+    } else {
+      v = *reinterpret_cast<const f32x4 *>(p);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < count) v[e] = (float)p[e];
+  }
+  return v;
+}
+
+template <typename TO, bool VEC>
+__device__ __forceinline__ void store4(TO *p, f32x4 v, int count) {
+  if (VEC && count >= 4) {
+    if constexpr (sizeof(TO) == 2) {
+      f16x4 h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
+      *reinterpret_cast<f16x4 *>(p) = h;
+    } else {
+      *reinterpret_cast<f32x4 *>(p) = v;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < count) p[e] = (TO)v[e];
+  }
+}
+
+__device__ __forceinline__ f32x4 act_values(int act, f32x4 g) {
+  f32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = act_value(act, g[e]);
+  return v;
+}
+
+// From the accumulators, 32 rows at a time through the wave's staging area, to
+// memory: a lane takes four neighbouring columns of a row.  r0, c0: first row
+// and column of the wave's part of the result.
+template <class T, int OUT, typename TO, bool VEC>
+__device__ __forceinline__ void proj_epilogue(const ProjParams &p, int r0, int c0, char *lds,
+                                              const typename T::Acc (&acc)[T::FM][T::FN]) {
+  constexpr int COLS = OUT == kScaled ? T::WTN : T::WTN / 2;
+  constexpr int LPR = COLS / 4;                   // lanes per row
+  constexpr int ROWS = kWave / LPR;               // rows per pass
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  float *stage = reinterpret_cast<float *>(lds + wave * T::EP_BYTES);
+  const int cl = 4 * (lane % LPR);
+  const int col = c0 + cl, count = p.N - col;
+  f32x4 wa = f32x4{1.0f, 1.0f, 1.0f, 1.0f}, wb = wa;
+  if constexpr (T::EB == 1) {
+    if (p.ws != nullptr && count > 0) {
+      wa = load4<float, false>(p.ws + col, count);
+      if constexpr (OUT != kScaled) wb = load4<float, false>(p.ws + p.N + col, count);
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < T::NG; ++g) {
+    stage_rows<T>(stage, acc, g, lane);
+#pragma unroll 1
+    for (int pass = 0; pass < 32 / ROWS; ++pass) {
+      const int rl = pass * ROWS + lane / LPR;
+      const int row = r0 + 32 * g + rl;
+      if (row >= p.M || count <= 0) continue;
+      f32x4 a = *reinterpret_cast<const f32x4 *>(&stage[rl * T::EP_STRIDE + cl]);
+      if constexpr (T::EB == 1) {
+        if (p.xs != nullptr) a *= p.xs[row];
+        a *= wa;
+      }
+      if constexpr (OUT == kScaled) {
+        TO *y = static_cast<TO *>(p.Y) + (size_t)row * (size_t)p.ldy + col;
+        a *= p.alpha;
+        if (p.beta != 0.0f) {
+          const f32x4 c = load4<TO, VEC>(y, count);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = __builtin_fmaf(p.beta, c[e], a[e]);
+        }
+        store4<TO, VEC>(y, a, count);
+      } else {
+        f32x4 b = *reinterpret_cast<const f32x4 *>(&stage[rl * T::EP_STRIDE + COLS + cl]);
+        if constexpr (T::EB == 1) {
+          if (p.xs != nullptr) b *= p.xs[row];
+          b *= wb;
+        }
+        TO *z = static_cast<TO *>(p.Z) + (size_t)row * (size_t)p.ldz + col;
+        if constexpr (OUT == kGated) {
+          store4<TO, VEC>(static_cast<TO *>(p.Y) + (size_t)row * (size_t)p.ldy + col,
+                          act_values(p.act, a) * b, count);
+          if (p.Z != nullptr) {
+            store4<TO, VEC>(z, a, count);
+            store4<TO, VEC>(z + p.N, b, count);
+          }
+        } else {
+          const f32x4 d = load4<TO, VEC>(
+              static_cast<const TO *>(p.dH) + (size_t)row * (size_t)p.lddh + col, count);
+          f32x4 dg, du;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float value, slope;
+            act_both(p.act, a[e], value, slope);
+            dg[e] = d[e] * b[e] * slope;
+            du[e] = d[e] * value;
+          }
+          store4<TO, VEC>(z, dg, count);
+          store4<TO, VEC>(z + p.N, du, count);
+        }
+      }
+    }
+  }
+}
+
+// VEC: four neighbouring elements of every output (and of dH) are one aligned
+// access.
+template <class T, int OUT, typename TO, bool VEC>
+__global__ __launch_bounds__(T::NT) void proj_tile(GemmParams p, ProjParams e) {
+  typedef HLayout<T, false, true, OUT != kScaled> L;
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
+  lds_poison(lds, T::LDS_BYTES);
+  int tm, tn, split;
+  tile_of_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
+  const int m0 = tm * T::BM, n0 = tn * L::COLS;
+  const int wave = threadIdx.x / kWave;
+  const int wm0 = (wave / T::WAVES_N) * T::WTM;
+  const int wn0 = (wave % T::WAVES_N) * T::WTN;
+  typename T::Acc acc[T::FM][T::FN];
+  zero_acc<T>(acc);
+  mainloop_direct<T, L>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
+  __builtin_amdgcn_s_waitcnt(kWaitAll);
+  __syncthreads();   // every wave is done with the pipeline slots
+  proj_epilogue<T, OUT, TO, VEC>(e, m0 + wm0, n0 + L::column(wn0), lds, acc);
+}
+
+template <class T, int OUT, typename TO>
+hipError_t launch_tile(const ProjParams &e, hipStream_t stream) {
+  constexpr int COLS = OUT == kScaled ? T::BN : T::BN / 2;
+  GemmParams p = {};
+  p.A = e.X;
+  p.B = e.W;
+  p.M = e.M;
+  p.N = e.N;
+  p.K = e.K;
+  p.lda = e.ldx;
+  p.ldb = e.ldw;
+  p.tiles_m = (e.M + T::BM - 1) / T::BM;
+  p.tiles_n = (e.N + COLS - 1) / COLS;
+  p.group_m = T::GROUP_M;
+  p.splits = 1;
+  const long long blocks = (long long)p.tiles_m * p.tiles_n;
+  if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  constexpr int B = 4 * (int)sizeof(TO);
+  const bool two = e.Z == nullptr || (e.ldz % 4 == 0 && e.N % 4 == 0 && aligned_to(e.Z, B));
+  const bool vec = two && e.ldy % 4 == 0 && aligned_to(e.Y, B) && e.lddh % 4 == 0 &&
+                   aligned_to(e.dH, B);
+  const dim3 g((unsigned)blocks), b(T::NT);
+  if (vec) hipLaunchKernelGGL((proj_tile<T, OUT, TO, true>), g, b, 0, stream, p, e);
+  else hipLaunchKernelGGL((proj_tile<T, OUT, TO, false>), g, b, 0, stream, p, e);
+  return hipGetLastError();
+}
+
+template <class T, int OUT>
+long long proj_tiles(const ProjParams &e) {
+  constexpr int COLS = OUT == kScaled ? T::BN : T::BN / 2;
+  return (long long)((e.M + T::BM - 1) / T::BM) * ((e.N + COLS - 1) / COLS);
+}
+
+template <class Big, class Mid, class Small, int OUT, typename TO>
+hipError_t launch_tiles(const ProjParams &e, hipStream_t stream) {
+  if (proj_tiles<Big, OUT>(e) >= kCUs / 2) return launch_tile<Big, OUT, TO>(e, stream);
+  if (proj_tiles<Mid, OUT>(e) >= kCUs / 2) return launch_tile<Mid, OUT, TO>(e, stream);
+  return launch_tile<Small, OUT, TO>(e, stream);
+}
+
+}  // namespace dgemm

@@ -454,6 +454,8 @@ def _call_rows(fn, dev, stream, workspace, need, args):
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on GPU %d" % dev)
         ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need == 0:
+        ws, size = None, 0
     elif stream is None or (torch.cuda.is_initialized()
                             and torch.cuda.is_current_stream_capturing()
                             and _stream(stream) == _current_stream(dev)):

@@ -134,8 +134,14 @@ TILE_OCCUPANCY = (
     ("H16TileILi128ELi128ELi32E", 2, 4),
     ("H16TileILi64ELi128ELi32E", 3, 2),
     ("H16TileILi256ELi256ELi128E", 1, 8),
-    ("H16TileILi128ELi128ELi64E", 2, 4),
-    ("H16TileILi64ELi128ELi64E", 3, 2),
+    ("H16TileILi128ELi128ELi64ELi4ELi2ELi2E", 2, 8),
+    ("H16TileILi128ELi128ELi128ELi4ELi2ELi2E", 2, 8),
+    ("H16TileILi128ELi128ELi64ELi4ELi2ELi3E", 1, 8),
+    ("H16TileILi128ELi128ELi128ELi4ELi2ELi3E", 1, 8),
+    ("H16TileILi64ELi64ELi128ELi2ELi2ELi2E", 2, 4),
+    ("H16TileILi64ELi64ELi256ELi2ELi2ELi2E", 2, 4),
+    ("H16TileILi64ELi64ELi128ELi2ELi2ELi3E", 1, 4),
+    ("H16TileILi64ELi64ELi256ELi2ELi2ELi3E", 1, 4),
 )
 
 

@@ -122,17 +122,18 @@ struct H16Tile {
   static constexpr int LOADS = QA_W + QB_W;             // direct loads per wave per K step
   static constexpr int EP_STRIDE = WTN + 4;             // epilogue staging row stride (floats)
   static constexpr int EP_BYTES = 32 * EP_STRIDE * 4;   // per wave
-  static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int LDS_BYTES =
+      STAGES * STAGE_BYTES > NWAVES * EP_BYTES ? STAGES * STAGE_BYTES : NWAVES * EP_BYTES;
   static_assert(BM % (WAVES_M * 32) == 0 && BN % (WAVES_N * 32) == 0, "wave tiling");
   static_assert(BK % 32 == 0 && (SUB % 2 == 0 || MF == 16), "BK multiple of 32");
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "1 KB load granules");
   static_assert(QA % NWAVES == 0 && QB % NWAVES == 0, "loads split over waves");
-  static_assert(WTM % 64 == 0 && WTN % 64 == 0, "wave origins multiples of 64");
+  static_assert(WTM % 32 == 0 && WTN % 32 == 0, "the swizzles repeat every 32 rows");
   static_assert(FM % 2 == 0, "the last sub-step splits the block rows in halves");
   static_assert(STAGES >= 2, "the pipeline needs two or more slots");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
-  static_assert(NWAVES * EP_BYTES <= LDS_BYTES, "epilogue staging fits in the pipeline LDS");
-  static_assert(6 * LOADS <= 63, "vmcnt range");
+  // (loaders of a step's loads for two waves: kSplitLoaders)
+  static_assert((MF == 16 && NWAVES == 8 ? 6 : 3) * LOADS <= 63, "vmcnt range");
 };
 
 // Operand regions.  A slot holds an A region (BM indices m by BK k) and a B

@@ -5,8 +5,8 @@
 namespace dgemm {
 
 hipError_t launch_glu_f16(const ProjParams &e, bool slopes, hipStream_t stream) {
-  return slopes ? launch_tiles<F16Big, F16Mid, F16Small, kSlopes, _Float16>(e, stream)
-                : launch_tiles<F16Big, F16Mid, F16Small, kGated, _Float16>(e, stream);
+  return slopes ? launch_tiles<2, kSlopes, _Float16>(e, stream)
+                : launch_tiles<2, kGated, _Float16>(e, stream);
 }
 
 }  // namespace dgemm

@@ -31,19 +31,45 @@ ProjParams params_of(const ProjCall &c) {
   return p;
 }
 
-template <typename T, typename TO, int OUT, int NF, int NB>
+template <typename T, typename TO, int OUT, int NF, int NB, int P, int WAVES, int U>
 hipError_t skinny(const ProjParams &p, hipStream_t stream) {
-  constexpr int BC = OUT == kScaled ? 16 * NF : 8 * NF;
-  const dim3 g((unsigned)((p.N + BC - 1) / BC), (unsigned)((p.M + 16 * NB - 1) / (16 * NB)));
+  constexpr int BR = 16 / P;
+  constexpr int BC = OUT == kScaled ? BR * NF : BR * NF / 2;
+  const dim3 g((unsigned)((p.N + BC - 1) / BC), (unsigned)((p.M + BR * NB - 1) / (BR * NB)));
   if (g.y > 65535) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((proj_skinny<T, TO, OUT, NF, NB, 1, 8>), g, dim3(8 * kWave), 0, stream, p);
+  hipLaunchKernelGGL((proj_skinny<T, TO, OUT, NF, NB, P, WAVES, U>), g, dim3(WAVES * kWave), 0,
+                     stream, p);
   return hipGetLastError();
+}
+
+// How wide a workgroup is, and how many waves divide its K.  Twice as many
+// columns halve what is read of X, once that leaves a workgroup per CU (64 rows
+// of 8192 8-bit integers, 8192 columns: 27.5 to 23.3 us; 4096 columns, 128
+// workgroups: 10.6 to 13); with one or more per CU four waves are enough (a gated
+// block of 64 x 8192 x 4096 halves: 33.7 us with four, 41.8 with eight), below it
+// eight are better (64 x 1024 8-bit columns of 4096: 7.0 with eight, 8.2 with
+// four).
+template <typename T, typename TO, int OUT, int NB>
+hipError_t skinny_wide(const ProjParams &p, hipStream_t stream) {
+  constexpr int NF = OUT == kScaled ? 1 : 2;
+  constexpr int U = NB == 1 ? 2 : 1;
+  const long long wgs = (long long)((p.N + 15) / 16) * ((p.M + 16 * NB - 1) / (16 * NB));
+  if (NB > 1 && wgs >= 2 * kCUs) return skinny<T, TO, OUT, 2 * NF, NB, 1, 4, U>(p, stream);
+  if (wgs >= kCUs) return skinny<T, TO, OUT, NF, NB, 1, 4, U>(p, stream);
+  return skinny<T, TO, OUT, NF, NB, 1, 8, U>(p, stream);
 }
 
 template <typename T, typename TO, int OUT>
 hipError_t run_skinny(const ProjParams &p, hipStream_t stream) {
-  constexpr int NF = OUT == kScaled ? 1 : 2;
-  return p.M <= 16 ? skinny<T, TO, OUT, NF, 1>(p, stream) : skinny<T, TO, OUT, NF, 4>(p, stream);
+  const bool near = (long long)p.ldx * (int)sizeof(T) < kQuadRowBytes &&
+                    (long long)p.ldw * (int)sizeof(T) < kQuadRowBytes;
+  // up to 8 rows two stretches of k share an instruction (and rows that are
+  // further apart than the other form's offsets hold)
+  if (p.M <= 8 || !near) return skinny<T, TO, OUT, OUT == kScaled ? 1 : 2, 1, 2, 8, 4>(p, stream);
+  if (p.M <= 16) return skinny_wide<T, TO, OUT, 1>(p, stream);
+  if (p.M <= 32) return skinny_wide<T, TO, OUT, 2>(p, stream);
+  if (p.M <= 48) return skinny_wide<T, TO, OUT, 3>(p, stream);
+  return skinny_wide<T, TO, OUT, 4>(p, stream);
 }
 
 template <typename TO>
@@ -56,14 +82,23 @@ hipError_t run_skinny(const ProjCall &c, const ProjParams &p) {
   return run_skinny<TO, TO, kGated>(p, c.stream);
 }
 
-constexpr int kSkinnyRows = 64;
-
 int bytes_of(const ProjCall &c) { return c.i8 ? 1 : (c.half ? 2 : 4); }
 
-// Whether a call takes the tiles: more rows than the other kernel is for, and rows
-// short enough that a tile's offsets fit 32 bits.
+// Whether a call takes the tiles.  Its rows have to be short enough that a
+// tile's offsets fit 32 bits.  Up to 16 rows the streaming kernel is ahead
+// everywhere, and beyond them while its 16 columns by up to 64 rows make at most
+// a workgroup per CU (us, tile first: 192 x 1024 x 1024 8-bit 5.4, 4.5; 300 rows of
+// it 5.4, 5.1; gated 128 x 2048 x 4096 halves 19.2, 18.1; 257 rows of it 23.2,
+// 32.6).  17 to 64 rows take the 64x64 tile where there are 128 of them or more
+// (gated 64 x 8192 x 4096: 8-bit 14.7, 20.7, halves 30.1, 36.7; 20 rows 14.1, 17.5
+// and 30.0, 33.0; but 64 x 4096 x 4096 8-bit, 64 tiles: 11.7, 9.4).  Rows that
+// have to be copied for the tiles pay for it beyond 128 rows only: a copy reads
+// and writes W, which the streaming kernel reads once for every 64 rows.
 bool tiled(const ProjCall &c) {
-  return c.M > kSkinnyRows && (c.i8 || c.half) && (long long)c.K * bytes_of(c) < kTileRowBytes;
+  if (!(c.i8 || c.half) || (long long)c.K * bytes_of(c) >= kTileRowBytes) return false;
+  if (c.M <= 16 || (!c.aligned && c.M <= 128)) return false;
+  if (c.M <= 64) return (c.gated ? c.N / 32 : c.N / 64) >= kCUs / 2;
+  return (long long)((c.N + 15) / 16) * ((c.M + 63) / 64) > kCUs;
 }
 
 struct ProjSpace {
@@ -105,28 +140,53 @@ hipError_t run_tiles(const ProjCall &c, ProjParams p, const ProjSpace &s) {
 }
 
 // Z[m, f], Z[m, F + f] := dH * u * act'(g), dH * act(g), from g and u that the
-// forward pass left.
+// forward pass left: 16 bytes of each at a time, which may lie at any element's
+// address.
+template <typename T>
+__device__ __forceinline__ void store_whole(T *p, const typename El<T>::Frag &v) {
+  typedef T Any __attribute__((ext_vector_type(El<T>::VEC), aligned(sizeof(T))));
+  *reinterpret_cast<Any *>(p) = v;
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void glu_slopes(const T *Zin, int ldi, const T *dH, int lddh,
                                                   T *Z, int ldz, int M, int F, int act) {
-  const long long total = (long long)M * F;
+  constexpr int VEC = El<T>::VEC;
+  const unsigned pieces = (unsigned)((F + VEC - 1) / VEC);
+  const long long total = (long long)M * pieces;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (long long)gridDim.x * 256) {
-    const int m = (int)(i / F), f = (int)(i - (long long)m * F);
+    const int m = total < (1LL << 32) ? (int)((unsigned)i / pieces) : (int)(i / pieces);
+    const int f = VEC * (int)(i - (long long)m * pieces);
     const T *z = Zin + (size_t)m * (size_t)ldi + f;
-    const float g = (float)z[0], u = (float)z[F];
-    const float d = (float)dH[(size_t)m * (size_t)lddh + f];
-    float value, slope;
-    act_both(act, g, value, slope);
+    const T *d = dH + (size_t)m * (size_t)lddh + f;
     T *o = Z + (size_t)m * (size_t)ldz + f;
-    o[0] = (T)(d * u * slope);
-    o[F] = (T)(d * value);
+    if (f + VEC <= F) {
+      const typename El<T>::Frag gs = load_whole(z), us = load_whole(z + F), ds = load_whole(d);
+      typename El<T>::Frag a, b;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float value, slope;
+        act_both(act, (float)gs[e], value, slope);
+        a[e] = (T)((float)ds[e] * (float)us[e] * slope);
+        b[e] = (T)((float)ds[e] * value);
+      }
+      store_whole(o, a);
+      store_whole(o + F, b);
+    } else {
+      for (int e = 0; f + e < F; ++e) {
+        float value, slope;
+        act_both(act, (float)z[e], value, slope);
+        o[e] = (T)((float)d[e] * (float)z[F + e] * slope);
+        o[F + e] = (T)((float)d[e] * value);
+      }
+    }
   }
 }
 
 template <typename T>
 hipError_t slopes(const GluGradCall &c, T *Z, int ldz) {
-  const long long total = (long long)c.M * c.F;
+  const long long total = (long long)c.M * ((c.F + El<T>::VEC - 1) / El<T>::VEC);
   const long long blocks = (total + 255) / 256;
   hipLaunchKernelGGL((glu_slopes<T>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256),
                      0, c.stream, static_cast<const T *>(c.Z), c.ldz,

@@ -79,12 +79,111 @@ hipError_t launch_glu_f16(const ProjParams &p, bool slopes, hipStream_t stream);
 
 // ---------------------------------------------------------------- few rows
 
+// A block of 16 rows as a lane loads it: 256 consecutive bytes of each row, in
+// four loads of four rows each, in which the four lanes of a quad read 64
+// consecutive bytes.  (The texture unit takes a load quad by quad, a cycle for
+// each line that a quad touches.  Loads in the fragments' own layout, where each
+// lane of a quad reads another row, take it four times as long: 64 rows of 4096
+// bytes beside 16 rows of weights on each of 64 CUs, 8.5 us beyond a launch's own
+// time.)  Offsets are 32 bits wide: rows less than kQuadRowBytes apart.
+constexpr long long kQuadRowBytes = 1 << 27;
+
+template <typename T>
+struct QuadRows {
+  const T *base;
+  uint32_t at[4];      // byte offsets of load j: row 4 * (lane % 16 / 4) + j
+
+  // first: the block's first row, in a matrix that ends after `rows` rows
+  __device__ __forceinline__ void set(const void *m, int first, int rows, int ld) {
+    const int lane = threadIdx.x % kWave;
+    const int f = first < rows ? first : rows - 1;
+    base = static_cast<const T *>(m) + (size_t)f * (size_t)ld;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = lane % 16 / 4 * 4 + j, last = rows - 1 - f;
+      at[j] = (uint32_t)(r < last ? r : last) * (uint32_t)ld * (uint32_t)sizeof(T) +
+              (uint32_t)(lane / 16 * 64 + lane % 4 * 16);
+    }
+  }
+  __device__ __forceinline__ typename El<T>::Frag load(int j, int k) const {
+    const char *p = reinterpret_cast<const char *>(base + k);
+    return load_whole(reinterpret_cast<const T *>(p + at[j]));
+  }
+};
+
+// Four loads as four fragments: element j of lane t of a quad changes places with
+// element t of lane j.  Fragment i then holds, in lane l, bytes 64 * (l / 16) + 16 i
+// .. +15 of row l % 16's 256: the same k in all rows of a group of 16 lanes, as
+// the matrix instruction wants it, whose order over k is its own.
+template <class F>
+__device__ __forceinline__ void quad_transpose(F (&v)[4]) {
+  const bool odd = (threadIdx.x & 1) != 0, high = (threadIdx.x & 2) != 0;
+  i32x4 r[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = __builtin_bit_cast(i32x4, v[j]);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    int s[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const int x = __builtin_amdgcn_mov_dpp(r[j + 1][d], 0xB1, 0xf, 0xf, true);   // lane ^ 1
+      const int y = __builtin_amdgcn_mov_dpp(r[j][d], 0xB1, 0xf, 0xf, true);
+      s[j] = odd ? x : r[j][d];
+      s[j + 1] = odd ? r[j + 1][d] : y;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int x = __builtin_amdgcn_mov_dpp(s[j + 2], 0x4E, 0xf, 0xf, true);      // lane ^ 2
+      const int y = __builtin_amdgcn_mov_dpp(s[j], 0x4E, 0xf, 0xf, true);
+      r[j][d] = high ? x : s[j];
+      r[j + 2][d] = high ? s[j + 2] : y;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(F, r[j]);
+}
+
+// acc[f][b] += U chunks of 256 bytes a row from element k on.
+template <typename T, int U, int NF, int NB>
+__device__ __forceinline__ void quad_steps(const QuadRows<T> (&w)[NF], const QuadRows<T> (&x)[NB],
+                                           int k, typename El<T>::Acc (&acc)[NF][NB]) {
+  typedef typename El<T>::Frag Frag;
+  constexpr int CH = 16 * El<T>::VEC;
+  Frag wf[U][NF][4], xf[U][NB][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wf[u][f][j] = w[f].load(j, k + u * CH);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xf[u][b][j] = x[b].load(j, k + u * CH);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f) quad_transpose(wf[u][f]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      quad_transpose(xf[u][b]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) acc[f][b] = mma16(wf[u][f][i], xf[u][b][i], acc[f][b]);
+    }
+  }
+}
+
 // grid: (columns / BC, rows / BT).  A workgroup's waves divide K among
 // themselves; each wave streams its stretch of the weights' rows from memory
-// into matrix-core fragments (stream_mac), then the waves' sums meet in LDS.
-// NF blocks of 16 / P weight rows (gated: the first half gate rows, the rest up
-// rows), NB blocks of 16 / P rows of X, P stretches of k in one instruction.
-template <typename T, typename TO, int OUT, int NF, int NB, int P, int WAVES>
+// into matrix-core fragments, then the waves' sums meet in LDS.  NF blocks of BR
+// weight rows (gated: the first half gate rows, the rest up rows), NB blocks of
+// BR rows of X.  P > 1: blocks of 16 / P rows, P stretches of k in one
+// instruction (stream_mac); P == 1: blocks of 16 rows (quad_steps).
+template <typename T, typename TO, int OUT, int NF, int NB, int P, int WAVES, int U>
 __global__ __launch_bounds__(WAVES *kWave) void proj_skinny(ProjParams p) {
   typedef typename El<T>::Acc Acc;
   typedef typename std::remove_reference<decltype(Acc{}[0])>::type Sum;
@@ -97,31 +196,50 @@ __global__ __launch_bounds__(WAVES *kWave) void proj_skinny(ProjParams p) {
   const int lane = threadIdx.x % kWave, wave = wave_id();
   const int li = lane % 16, lg = lane / 16;
   const int n0 = blockIdx.x * BC, m0 = blockIdx.y * BT;
-  const T *w[NF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    const int r = BR * f + li / P;
+  auto w_row = [&](int r) {      // row r of the workgroup's
     const int n = n0 + (r < BC ? r : r - BC);
-    w[f] = static_cast<const T *>(p.W) +
+    return static_cast<const T *>(p.W) +
            (size_t)((r < BC ? 0 : p.N) + (n < p.N ? n : p.N - 1)) * (size_t)p.ldw;
-  }
-  constexpr int G = 2 * El<T>::KSTEP * P;
+  };
+  auto x_row = [&](int r) {
+    const int m = m0 + r;
+    return static_cast<const T *>(p.X) + (size_t)(m < p.M ? m : p.M - 1) * (size_t)p.ldx;
+  };
+  // each wave a stretch of whole chunks (of at least 256 bytes a row)
+  constexpr int G = P == 1 ? 16 * El<T>::VEC : 2 * El<T>::KSTEP * P;
   const int part = ((p.K + WAVES - 1) / WAVES + G - 1) / G * G;
   const int k0 = wave * part < p.K ? wave * part : p.K;
   const int k1 = k0 + part < p.K ? k0 + part : p.K;
-  RowLoader<T, NB> x;
-  x.lim = k1;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int m = m0 + BR * b + li / P;
-    x.row[b] = static_cast<const T *>(p.X) + (size_t)(m < p.M ? m : p.M - 1) * (size_t)p.ldx;
-  }
   Acc acc[NF][NB];
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[f][b] = Acc{0, 0, 0, 0};
-  stream_mac<T, (NF * NB >= 8 ? 2 : 4), P>(w, k0, k1, k1, k1, x, acc);
+  int k = k0;
+  if constexpr (P == 1) {
+    QuadRows<T> w[NF], x[NB];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const bool up = GATED && f >= NF / 2;
+      w[f].set(static_cast<const T *>(p.W) + (up ? (size_t)p.N * (size_t)p.ldw : 0),
+               n0 + 16 * (up ? f - NF / 2 : f), p.N, p.ldw);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) x[b].set(p.X, m0 + 16 * b, p.M, p.ldx);
+    for (; k + U * G <= k1; k += U * G) quad_steps<T, U>(w, x, k, acc);
+    if constexpr (U > 1)
+      for (; k + G <= k1; k += G) quad_steps<T, 1>(w, x, k, acc);
+  }
+  if (P > 1 || k < k1) {
+    const T *w[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) w[f] = w_row(BR * f + li / P);
+    RowLoader<T, NB> x;
+    x.lim = k1;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) x.row[b] = x_row(BR * b + li / P);
+    stream_mac<T, (P == 1 ? 1 : U), P>(w, k, k1, k1, k1, x, acc);
+  }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     if (m0 + BR * b >= p.M) break;

@@ -194,11 +194,45 @@ long long proj_tiles(const ProjParams &e) {
   return (long long)((e.M + T::BM - 1) / T::BM) * ((e.N + COLS - 1) / COLS);
 }
 
-template <class Big, class Mid, class Small, int OUT, typename TO>
+// The tiles, for elements of EB bytes.  What a launch of n tiles costs, in
+// microseconds at 4096 bytes of k (half of that, and half of the difference between
+// the tiles, at 2048), measured at 65 to 2048 rows and 1024 to 16384 rows of W:
+//   256x256       55 a round of 256 tiles (one workgroup per CU)
+//   128x128       37 a round of 512 (two per CU); 22 where at most 256 are left,
+//                 which then take three LDS slots in place of two (25 with two)
+//   64x64         14.5 a round of 512, 12 where at most 256 are left (three slots;
+//                 16 to 35 against 15 to 30 us at 64 x (2 x 8192) x 4096)
+// The least decides.  (The 128x128 and 64x128 tiles of the plain fp16 product,
+// four and two waves in steps of 64 bytes of k, take 27 and 26 at up to 256 tiles.)
+template <int EB>
+struct ProjTiles {
+  typedef H16Tile<256, 256, 128 / EB, 2, 4, 2, 4, 16, EB> Large;   // 8 waves, 128 KB LDS
+  typedef H16Tile<128, 128, 128 / EB, 4, 2, 2, 8, 16, EB> Mid;     // 8 waves,  68 KB
+  typedef H16Tile<128, 128, 128 / EB, 4, 2, 3, 8, 16, EB> Mid3;    // 8 waves,  96 KB
+  typedef H16Tile<64, 64, 256 / EB, 2, 2, 2, 8, 16, EB> Small;     // 4 waves,  64 KB
+  typedef H16Tile<64, 64, 256 / EB, 2, 2, 3, 8, 16, EB> Small3;    // 4 waves,  96 KB
+};
+
+inline double tile_cost(long long tiles, int round, double whole, double half) {
+  const long long left = tiles % round;
+  return (double)(tiles / round) * whole + (left == 0 ? 0.0 : (2 * left <= round ? half : whole));
+}
+
+template <int EB, int OUT, typename TO>
 hipError_t launch_tiles(const ProjParams &e, hipStream_t stream) {
-  if (proj_tiles<Big, OUT>(e) >= kCUs / 2) return launch_tile<Big, OUT, TO>(e, stream);
-  if (proj_tiles<Mid, OUT>(e) >= kCUs / 2) return launch_tile<Mid, OUT, TO>(e, stream);
-  return launch_tile<Small, OUT, TO>(e, stream);
+  typedef ProjTiles<EB> P;
+  const long long large = proj_tiles<typename P::Large, OUT>(e);
+  const long long mid = proj_tiles<typename P::Mid, OUT>(e);
+  const long long small = proj_tiles<typename P::Small, OUT>(e);
+  const double l = tile_cost(large, kCUs, 55.0, 55.0);
+  const double m = tile_cost(mid, 2 * kCUs, 37.0, 22.0);
+  const double s = tile_cost(small, 2 * kCUs, 14.5, 12.0);
+  if (l <= m && l <= s) return launch_tile<typename P::Large, OUT, TO>(e, stream);
+  if (m <= s)
+    return mid <= kCUs ? launch_tile<typename P::Mid3, OUT, TO>(e, stream)
+                       : launch_tile<typename P::Mid, OUT, TO>(e, stream);
+  return small <= kCUs ? launch_tile<typename P::Small3, OUT, TO>(e, stream)
+                       : launch_tile<typename P::Small, OUT, TO>(e, stream);
 }
 
 }  // namespace dgemm

@@ -27,7 +27,8 @@ POISON_BUILD_DIR = os.path.join(HERE, "_build_lds_poison")
 SOURCES = ["api.hip", "gemm_f32.hip", "gemm_f16.hip", "gemm_valu.hip", "scale.hip", "splitk.hip",
            "pack.hip", "probe.hip", "gemm_f16_lora.hip", "lora.hip",
            "moe.hip", "rows_api.hip",
-           "quant.hip", "proj.hip", "gemm_i8.hip", "glu_f16.hip", "glu_i8.hip", "proj_api.hip"]
+           "quant.hip", "proj.hip", "gemm_i8.hip", "glu_f16.hip", "glu_f32.hip", "glu_i8.hip",
+           "glu_grad.hip", "glu_products.hip", "proj_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -59,8 +60,9 @@ def _compile(src, verbose=False, build_dir=BUILD_DIR, extra=()):
 # touches it: the asm's m0 writes then cannot disturb compiled code.  The
 # same assembly is checked for spills (and that of gemm_valu.hip).
 M0_ASM_SOURCES = ["gemm_f16.hip", "gemm_f16_lora.hip", "gemm_f32.hip", "gemm_i8.hip",
-                  "glu_f16.hip", "glu_i8.hip"]
-SPILL_ONLY_SOURCES = ["gemm_valu.hip", "lora.hip", "moe.hip", "proj.hip", "quant.hip"]
+                  "glu_f16.hip", "glu_f32.hip", "glu_i8.hip", "glu_products.hip"]
+SPILL_ONLY_SOURCES = ["gemm_valu.hip", "lora.hip", "moe.hip", "proj.hip", "quant.hip",
+                      "glu_grad.hip"]
 
 
 def check_spills_only(src):
@@ -131,13 +133,15 @@ TILE_OCCUPANCY = (
     ("S32TileILi32ELi32ELi64E", 5, 1),
     ("S32TileILi32ELi32ELi32E", 6, 1),
     ("H16TileILi256ELi256ELi64E", 1, 8),
-    ("H16TileILi128ELi128ELi32E", 2, 4),
+    ("H16TileILi128ELi128ELi32ELi2ELi2E", 2, 4),
     ("H16TileILi64ELi128ELi32E", 3, 2),
     ("H16TileILi256ELi256ELi128E", 1, 8),
     ("H16TileILi128ELi128ELi64ELi4ELi2ELi2E", 2, 8),
     ("H16TileILi128ELi128ELi128ELi4ELi2ELi2E", 2, 8),
     ("H16TileILi128ELi128ELi64ELi4ELi2ELi3E", 1, 8),
     ("H16TileILi128ELi128ELi128ELi4ELi2ELi3E", 1, 8),
+    ("H16TileILi128ELi128ELi32ELi4ELi2ELi2E", 2, 8),
+    ("H16TileILi64ELi64ELi32ELi2ELi2ELi2E", 4, 4),
     ("H16TileILi64ELi64ELi128ELi2ELi2ELi2E", 2, 4),
     ("H16TileILi64ELi64ELi256ELi2ELi2ELi2E", 2, 4),
     ("H16TileILi64ELi64ELi128ELi2ELi2ELi3E", 1, 4),

@@ -89,7 +89,8 @@ namespace dgemm {
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
-// EB: bytes per element, 2 (halves) or 1 (8-bit integers, BK twice as long).
+// EB: bytes per element: 2 (halves), 1 (8-bit integers, BK twice as long) or 4
+// (floats, half as long; four v_mfma_f32_16x16x4_f32 a fragment).
 template <int BM_, int BN_, int BK_, int WAVES_M_, int WAVES_N_, int STAGES_, int GROUP_M_,
           int MF_ = 32, int EB_ = 2>
 struct H16Tile {
@@ -386,16 +387,16 @@ template <class R>
 __device__ __forceinline__ u32x4 staged_chunk(const void *X, int ld, int idx0, int ext, int k0,
                                               int K, int idx, int kk, int w) {
   const int g = idx0 + idx, gk = k0 + kk;
-  if constexpr (R::EB == 1) {
-    // 8-bit integers: rows that start at 16 bytes only, so the 16 bytes that
-    // hold a row's last elements are one aligned granule, in the same page as
-    // them; what it holds behind the row is cleared.
-    const uint8_t *src = static_cast<const uint8_t *>(X) + (size_t)g * (size_t)ld + gk;
+  if constexpr (R::EB != 2) {
+    // 8-bit integers and floats: rows that start at 16 bytes only, so the 16
+    // bytes that hold a row's last elements are one aligned granule, in the same
+    // page as them; what it holds behind the row is cleared.
+    const char *src = static_cast<const char *>(X) + R::EB * ((size_t)g * (size_t)ld + gk);
     u32x4 v = u32x4{0u, 0u, 0u, 0u};
     if (g < ext && gk < K) v = *reinterpret_cast<const u32x4 *>(src);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int left = K - gk - 4 * e;
+      const int left = R::EB * (K - gk) - 4 * e;
       if (left < 4) v[e] &= left > 0 ? (1u << (8 * left)) - 1u : 0u;
     }
     return v;
@@ -547,6 +548,13 @@ __device__ __forceinline__ typename T::Acc mma(f16x8 a, f16x8 b, typename T::Acc
     const i32x4 x = __builtin_bit_cast(i32x4, a), y = __builtin_bit_cast(i32x4, b);
     if constexpr (T::MF == 32) return __builtin_amdgcn_mfma_i32_32x32x32_i8(x, y, c, 0, 0, 0);
     else return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
+  } else if constexpr (T::EB == 4) {
+    // the j-th takes element j of every lane: k 4h + j of the fragment's 16, h = l / 16
+    static_assert(T::MF == 16, "16x16 blocks of floats");
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], y[j], c, 0, 0, 0);
+    return c;
   } else if constexpr (T::MF == 32) return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   else return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }

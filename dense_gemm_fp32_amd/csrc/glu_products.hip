@@ -1,0 +1,180 @@
+// glu_products.hip -- the two products of a gated block's backward pass in one
+// launch: dX = [dG dU] W and dW = [dG dU]^T X, of middling sizes and of rows that
+// would have to be copied in any case.
+//
+// Both run on the tiles of proj_tile.hpp, and the workgroups of one fill the CUs
+// that the other leaves idle.  In place: fp16 operands as they are, W and X
+// index-major and [dG dU] transposed in LDS (HRegion).  Else k-contiguous copies of
+// all of them, transposed where the operand is.
+#include "proj_tile.hpp"
+
+namespace dgemm {
+
+namespace {
+
+// b_first: the workgroups of b come first.  The first job's are rounded up to a
+// multiple of the XCDs, so that both jobs' tiles keep to one XCD each.
+template <class T, typename TA, typename TB, bool VEC, bool INPLACE>
+__global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob b, int first,
+                                                       bool b_first) {
+  typedef HLayout<T, false, !INPLACE> LA;
+  typedef HLayout<T, INPLACE, !INPLACE> LB;
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
+  lds_poison(lds, T::LDS_BYTES);
+  const bool early = (int)blockIdx.x < first;
+  const bool second = early == b_first;     // whether this is b's
+  const int local = early ? (int)blockIdx.x : (int)blockIdx.x - first;
+  GemmParams p = {};
+  ProjParams e = {};
+  p.A = second ? b.A : a.A;
+  p.B = second ? b.B : a.B;
+  p.M = e.M = second ? b.M : a.M;
+  p.N = e.N = second ? b.N : a.N;
+  p.K = second ? b.K : a.K;
+  p.lda = second ? b.lda : a.lda;
+  p.ldb = second ? b.ldb : a.ldb;
+  const int splits = second ? b.splits : a.splits, chunk = second ? b.chunk : a.chunk;
+  e.alpha = 1.0f;
+  p.tiles_m = (p.M + T::BM - 1) / T::BM;
+  p.tiles_n = (p.N + T::BN - 1) / T::BN;
+  const int tiles = p.tiles_m * p.tiles_n * splits;
+  if (local >= tiles) return;               // (what the first job was rounded up by)
+  int tm, tn, split;
+  tile_of_block(local, tiles, p.tiles_m, p.tiles_n, T::GROUP_M, tm, tn, split);
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
+  if (splits > 1) {
+    const int kb = split * chunk;
+    const bool ta = INPLACE && second, tb = !INPLACE;
+    p.A = static_cast<const char *>(p.A) + (size_t)kb * T::EB * (ta ? (size_t)p.lda : 1);
+    p.B = static_cast<const char *>(p.B) + (size_t)kb * T::EB * (tb ? 1 : (size_t)p.ldb);
+    p.K = p.K - kb < chunk ? p.K - kb : chunk;
+  }
+  const int wave = threadIdx.x / kWave;
+  const int wm0 = (wave / T::WAVES_N) * T::WTM;
+  const int wn0 = (wave % T::WAVES_N) * T::WTN;
+  typename T::Acc acc[T::FM][T::FN];
+  zero_acc<T>(acc);
+  if (INPLACE && second)
+    mainloop_direct<T, LB>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
+  else
+    mainloop_direct<T, LA>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
+  __builtin_amdgcn_s_waitcnt(kWaitAll);
+  __syncthreads();   // every wave is done with the pipeline slots
+  if (splits > 1) {
+    float *slab = second ? b.slab : a.slab;
+    e.ldy = (p.N + 3) / 4 * 4;
+    e.Y = slab + (size_t)split * (size_t)p.M * (size_t)e.ldy;
+    proj_epilogue<T, kScaled, float, true>(e, m0 + wm0, n0 + wn0, lds, acc);
+  } else if (second) {
+    e.Y = b.C;
+    e.ldy = b.ldc;
+    e.beta = b.beta;
+    proj_epilogue<T, kScaled, TB, VEC>(e, m0 + wm0, n0 + wn0, lds, acc);
+  } else {
+    e.Y = a.C;
+    e.ldy = a.ldc;
+    e.beta = a.beta;
+    proj_epilogue<T, kScaled, TA, VEC>(e, m0 + wm0, n0 + wn0, lds, acc);
+  }
+}
+
+template <class T>
+long long tiles_of_job(const ProductJob &j) {
+  if (j.C == nullptr) return 0;
+  return (long long)((j.M + T::BM - 1) / T::BM) * ((j.N + T::BN - 1) / T::BN) * j.splits;
+}
+
+template <class T, typename TA, typename TB, bool INPLACE>
+hipError_t launch(const ProductJob &a, const ProductJob &b, hipStream_t stream) {
+  const long long na = tiles_of_job<T>(a), nb = tiles_of_job<T>(b);
+  // the longer workgroups first
+  const bool b_first = b.C != nullptr && (a.C == nullptr || b.chunk > a.chunk);
+  const long long first = b_first ? nb : na, other = b_first ? na : nb;
+  const long long start = other > 0 ? (first + kXcds - 1) / kXcds * kXcds : first;
+  if (start + other > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  auto vec = [](const ProductJob &j, int eb) {
+    return j.C == nullptr || (j.ldc % 4 == 0 && aligned_to(j.C, 4 * (uintptr_t)eb));
+  };
+  const dim3 g((unsigned)(start + other)), t(T::NT);
+  if (vec(a, (int)sizeof(TA)) && vec(b, (int)sizeof(TB)))
+    hipLaunchKernelGGL((proj_products<T, TA, TB, true, INPLACE>), g, t, 0, stream, a, b, (int)start,
+                       b_first);
+  else
+    hipLaunchKernelGGL((proj_products<T, TA, TB, false, INPLACE>), g, t, 0, stream, a, b, (int)start,
+                       b_first);
+  return hipGetLastError();
+}
+
+template <int EB, typename TA, typename TB, bool INPLACE>
+hipError_t run(const ProductJob &a, const ProductJob &b, bool mid, hipStream_t stream) {
+  return mid ? launch<typename ProjTiles<EB>::Mid, TA, TB, INPLACE>(a, b, stream)
+             : launch<typename ProjTiles<EB>::Small, TA, TB, INPLACE>(a, b, stream);
+}
+
+// One tile's step, in microseconds with the CU full, and how many of its steps a
+// launch's longest workgroup adds: what 64x64 and 128x128 tiles reach in
+// proj_tile.hpp's products.
+struct StepCost {
+  int bm, bk;
+  double step, longest;
+};
+
+double cost(const StepCost &t, const ProductJob &a, const ProductJob &b, int sa, int sb) {
+  double work = 0.0, longest = 0.0, sums = 0.0;
+  for (int i = 0; i < 2; ++i) {
+    const ProductJob &j = i ? b : a;
+    const int s = i ? sb : sa;
+    const double tiles = (double)((j.M + t.bm - 1) / t.bm) * ((j.N + t.bm - 1) / t.bm);
+    const int steps = (j.K + t.bk - 1) / t.bk, chunk = (steps + s - 1) / s;
+    work += tiles * steps;
+    if (chunk > longest) longest = chunk;
+    // a launch of its own, and the parts written and read at 4 TB/s
+    if (s > 1) sums += 3.5 + s * (double)j.M * (double)j.N * 8.0 / 4.0e6;
+  }
+  return t.step * (work / kCUs + t.longest * longest) + sums;
+}
+
+}  // namespace
+
+ProductPlan plan_products(bool half, ProductJob &a, ProductJob &b) {
+  const StepCost f16[2] = {{64, 128, 0.45, 1.0}, {128, 64, 0.58, 1.0}};
+  const StepCost f32[2] = {{64, 32, 0.43, 0.5}, {128, 32, 1.70, 0.5}};
+  ProductPlan best = {false, 1e300};
+  int bsa = 1, bsb = 1;
+  for (int m = 0; m < 2; ++m) {
+    const StepCost &t = half ? f16[m] : f32[m];
+    auto most = [&](const ProductJob &j) {      // parts of at least 8 steps
+      const int s = (j.K + t.bk - 1) / t.bk / 8;
+      return s < 1 ? 1 : (s > 8 ? 8 : s);
+    };
+    for (int sa = 1; sa <= most(a); ++sa)
+      for (int sb = 1; sb <= most(b); ++sb) {
+        const double c = cost(t, a, b, sa, sb);
+        if (c >= 0.98 * best.us) continue;
+        best = ProductPlan{m == 1, c};
+        bsa = sa;
+        bsb = sb;
+      }
+  }
+  const StepCost &t = half ? f16[best.mid] : f32[best.mid];
+  for (int i = 0; i < 2; ++i) {
+    ProductJob &j = i ? b : a;
+    const int steps = (j.K + t.bk - 1) / t.bk, s = i ? bsb : bsa;
+    const int each = (steps + s - 1) / s;
+    j.chunk = each * t.bk;
+    j.splits = (steps + each - 1) / each;
+  }
+  return best;
+}
+
+hipError_t launch_products(bool half, bool b32, bool mid, bool inplace, const ProductJob &a,
+                           const ProductJob &b, hipStream_t stream) {
+  if (!half) return run<4, float, float, false>(a, b, mid, stream);
+  if (inplace)
+    return b32 ? run<2, _Float16, float, true>(a, b, mid, stream)
+               : run<2, _Float16, _Float16, true>(a, b, mid, stream);
+  return b32 ? run<2, _Float16, float, false>(a, b, mid, stream)
+             : run<2, _Float16, _Float16, false>(a, b, mid, stream);
+}
+
+}  // namespace dgemm

@@ -1,7 +1,5 @@
 // proj.hip -- products of 8-bit integers and gated blocks: which kernel runs a
-// call, and the gated block's backward pass.
-#include <type_traits>
-
+// call.
 #include "proj.hpp"
 
 namespace dgemm {
@@ -95,7 +93,7 @@ int bytes_of(const ProjCall &c) { return c.i8 ? 1 : (c.half ? 2 : 4); }
 // have to be copied for the tiles pay for it beyond 128 rows only: a copy reads
 // and writes W, which the streaming kernel reads once for every 64 rows.
 bool tiled(const ProjCall &c) {
-  if (!(c.i8 || c.half) || (long long)c.K * bytes_of(c) >= kTileRowBytes) return false;
+  if ((long long)c.K * bytes_of(c) >= kTileRowBytes) return false;
   if (c.M <= 16 || (!c.aligned && c.M <= 128)) return false;
   if (c.M <= 64) return (c.gated ? c.N / 32 : c.N / 64) >= kCUs / 2;
   return (long long)((c.N + 15) / 16) * ((c.M + 63) / 64) > kCUs;
@@ -135,169 +133,10 @@ hipError_t run_tiles(const ProjCall &c, ProjParams p, const ProjSpace &s) {
       p.ldw = ld;
     }
   }
-  if (!c.i8) return launch_glu_f16(p, c.dH != nullptr, c.stream);
+  if (!c.i8)
+    return c.half ? launch_glu_f16(p, c.dH != nullptr, c.stream)
+                  : launch_glu_f32(p, c.dH != nullptr, c.stream);
   return c.gated ? launch_glu_i8(p, c.half, c.stream) : launch_proj_i8(p, c.half, c.stream);
-}
-
-// Z[m, f], Z[m, F + f] := dH * u * act'(g), dH * act(g), from g and u that the
-// forward pass left: 16 bytes of each at a time, which may lie at any element's
-// address.
-template <typename T>
-__device__ __forceinline__ void store_whole(T *p, const typename El<T>::Frag &v) {
-  typedef T Any __attribute__((ext_vector_type(El<T>::VEC), aligned(sizeof(T))));
-  *reinterpret_cast<Any *>(p) = v;
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void glu_slopes(const T *Zin, int ldi, const T *dH, int lddh,
-                                                  T *Z, int ldz, int M, int F, int act) {
-  constexpr int VEC = El<T>::VEC;
-  const unsigned pieces = (unsigned)((F + VEC - 1) / VEC);
-  const long long total = (long long)M * pieces;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (long long)gridDim.x * 256) {
-    const int m = total < (1LL << 32) ? (int)((unsigned)i / pieces) : (int)(i / pieces);
-    const int f = VEC * (int)(i - (long long)m * pieces);
-    const T *z = Zin + (size_t)m * (size_t)ldi + f;
-    const T *d = dH + (size_t)m * (size_t)lddh + f;
-    T *o = Z + (size_t)m * (size_t)ldz + f;
-    if (f + VEC <= F) {
-      const typename El<T>::Frag gs = load_whole(z), us = load_whole(z + F), ds = load_whole(d);
-      typename El<T>::Frag a, b;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float value, slope;
-        act_both(act, (float)gs[e], value, slope);
-        a[e] = (T)((float)ds[e] * (float)us[e] * slope);
-        b[e] = (T)((float)ds[e] * value);
-      }
-      store_whole(o, a);
-      store_whole(o + F, b);
-    } else {
-      for (int e = 0; f + e < F; ++e) {
-        float value, slope;
-        act_both(act, (float)z[e], value, slope);
-        o[e] = (T)((float)d[e] * (float)z[F + e] * slope);
-        o[F + e] = (T)((float)d[e] * value);
-      }
-    }
-  }
-}
-
-template <typename T>
-hipError_t slopes(const GluGradCall &c, T *Z, int ldz) {
-  const long long total = (long long)c.M * ((c.F + El<T>::VEC - 1) / El<T>::VEC);
-  const long long blocks = (total + 255) / 256;
-  hipLaunchKernelGGL((glu_slopes<T>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256),
-                     0, c.stream, static_cast<const T *>(c.Z), c.ldz,
-                     static_cast<const T *>(c.dH), c.lddh, Z, ldz, c.M, c.F, c.act);
-  return hipGetLastError();
-}
-
-// The two products of the backward pass, on [dG dU] (rows of ldd elements).
-Call product_x(const GluGradCall &c, const void *D, int ldd) {
-  Call g = {};
-  g.M = c.M;
-  g.N = c.K;
-  g.K = 2 * c.F;
-  g.alpha = 1.0f;
-  g.beta = c.beta_x;
-  g.A = D;
-  g.lda = ldd;
-  g.B = c.W;
-  g.ldb = c.ldw;
-  g.C = c.dX;
-  g.ldc = c.lddx;
-  g.splits = 1;
-  g.pack_mode = 2;
-  g.copy_ragged_b = c.half;
-  g.stream = c.stream;
-  return g;
-}
-
-Call product_w(const GluGradCall &c, const void *D, int ldd) {
-  Call g = {};
-  g.M = 2 * c.F;
-  g.N = c.K;
-  g.K = c.M;
-  g.alpha = 1.0f;
-  g.beta = c.beta_w;
-  g.A = D;
-  g.lda = ldd;
-  g.ta = true;
-  g.B = c.X;
-  g.ldb = c.ldx;
-  g.C = c.dW;
-  g.ldc = c.lddw;
-  g.out32 = c.half && c.dw32;
-  g.splits = 1;
-  g.pack_mode = 2;
-  g.copy_ragged_b = c.half;
-  g.stream = c.stream;
-  return g;
-}
-
-// Workspace that such a product may take: for operands whose rows all allow
-// the widest loads, or do not.
-size_t product_bytes(const GluGradCall &c, Call g) {
-  void *p = reinterpret_cast<void *>((uintptr_t)256);
-  size_t most = 0;
-  for (int odd = 0; odd < (c.aligned ? 1 : 2); ++odd) {
-    g.A = g.B = g.C = p;
-    g.ldb = odd ? c.K | 1 : (c.K + 7) / 8 * 8;
-    g.ldc = g.ldb;
-    g.ws_fixed_bytes = (size_t)1 << 40;
-    const size_t n = (c.half ? plan_f16(g) : plan_f32(g)).ws_bytes;
-    most = n > most ? n : most;
-  }
-  return most;
-}
-
-// The forward pass once more, up to [dG dU].
-ProjCall forward_of(const GluGradCall &c, void *D, int ldd) {
-  ProjCall f = {};
-  f.half = c.half;
-  f.gated = true;
-  f.aligned = c.aligned;
-  f.M = c.M;
-  f.N = c.F;
-  f.K = c.K;
-  f.act = c.act;
-  f.X = c.X;
-  f.ldx = c.ldx;
-  f.W = c.W;
-  f.ldw = c.ldw;
-  f.Z = D;
-  f.ldz = ldd;
-  f.dH = c.dH;
-  f.lddh = c.lddh;
-  f.stream = c.stream;
-  return f;
-}
-
-struct GradSpace {
-  void *D;         // [dG dU], M rows of ldd elements
-  int ldd;
-  char *W;         // the forward pass's and the products', one after the other
-  size_t w_bytes;
-};
-
-size_t carve(const GluGradCall &c, void *base, GradSpace *s) {
-  Carve w(base);
-  s->ldd = (2 * c.F + 7) / 8 * 8;
-  const size_t n = (size_t)c.M * (size_t)s->ldd;
-  s->D = c.half ? (void *)w.take<_Float16>(n) : (void *)w.take<float>(n);
-  s->w_bytes = c.Z != nullptr ? 0 : proj_workspace(forward_of(c, nullptr, s->ldd));
-  if (c.dX != nullptr) {
-    const size_t n = product_bytes(c, product_x(c, nullptr, s->ldd));
-    s->w_bytes = n > s->w_bytes ? n : s->w_bytes;
-  }
-  if (c.dW != nullptr) {
-    const size_t n = product_bytes(c, product_w(c, nullptr, s->ldd));
-    s->w_bytes = n > s->w_bytes ? n : s->w_bytes;
-  }
-  s->W = w.take<char>(s->w_bytes);
-  return w.used;
 }
 
 }  // namespace
@@ -313,33 +152,6 @@ hipError_t launch_proj(const ProjCall &c, void *ws) {
   const ProjParams p = params_of(c);
   if (tiled(c)) return run_tiles(c, p, s);
   return c.half ? run_skinny<_Float16>(c, p) : run_skinny<float>(c, p);
-}
-
-size_t glu_grad_workspace(const GluGradCall &c) {
-  GradSpace s;
-  return carve(c, nullptr, &s);
-}
-
-hipError_t launch_glu_grad(const GluGradCall &c, void *ws) {
-  GradSpace s;
-  carve(c, ws, &s);
-  hipError_t e;
-  if (c.Z != nullptr) {
-    e = c.half ? slopes(c, static_cast<_Float16 *>(s.D), s.ldd)
-               : slopes(c, static_cast<float *>(s.D), s.ldd);
-  } else {
-    e = launch_proj(forward_of(c, s.D, s.ldd), s.W);
-  }
-  if (e != hipSuccess) return e;
-  for (int w = 0; w < 2; ++w) {
-    if ((w ? c.dW : c.dX) == nullptr) continue;
-    Call g = w ? product_w(c, s.D, s.ldd) : product_x(c, s.D, s.ldd);
-    g.ws_fixed = s.W;
-    g.ws_fixed_bytes = s.w_bytes;
-    e = c.half ? launch_f16(g) : launch_f32(g);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
 }
 
 }  // namespace dgemm

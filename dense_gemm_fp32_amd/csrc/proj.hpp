@@ -69,13 +69,35 @@ __device__ __forceinline__ void finish(const ProjParams &p, int m, int n, float 
   }
 }
 
-// Kernels of many rows (gemm_i8.hip, glu_f16.hip, glu_i8.hip): rows of X and W
+// Kernels of many rows (gemm_i8.hip, glu_f16.hip, glu_f32.hip, glu_i8.hip): rows of X and W
 // start at 16 bytes and are less than kTileRowBytes apart, so that a tile's
 // offsets fit 32 bits.  half: outputs of fp16, else fp32; slopes: kSlopes.
 constexpr long long kTileRowBytes = 1 << 23;
 hipError_t launch_proj_i8(const ProjParams &p, bool half, hipStream_t stream);
 hipError_t launch_glu_i8(const ProjParams &p, bool half, hipStream_t stream);
 hipError_t launch_glu_f16(const ProjParams &p, bool slopes, hipStream_t stream);
+hipError_t launch_glu_f32(const ProjParams &p, bool slopes, hipStream_t stream);
+
+// One of the two products of a gated block's backward pass (glu_products.hip):
+// C := A B^T + beta * C over k-contiguous rows that start at 16 bytes (in place,
+// fp16: a's B and both of b's operands have k along their columns, whole 16 bytes of
+// it in each row).
+struct ProductJob {
+  const void *A, *B;
+  void *C;                // NULL: not wanted
+  int lda, ldb, ldc, M, N, K;
+  float beta;
+  int splits, chunk;      // K in parts of `chunk`; more than one: their sums to
+  float *slab;            // slab, part after part, in rows of N rounded up to 4
+};
+struct ProductPlan {
+  bool mid;               // 128x128 tiles, else 64x64
+  double us;              // estimate
+};
+ProductPlan plan_products(bool half, ProductJob &a, ProductJob &b);   // sets splits, chunk
+// half: A and B hold fp16 (and C, but b's fp32 with b32), else fp32
+hipError_t launch_products(bool half, bool b32, bool mid, bool inplace, const ProductJob &a,
+                           const ProductJob &b, hipStream_t stream);
 
 // ---------------------------------------------------------------- few rows
 

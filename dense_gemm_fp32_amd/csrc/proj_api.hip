@@ -335,20 +335,17 @@ size_t gemm_glu_grad_workspace(int dtype, int M, int F, int K, int aligned) {
   if (dtype < 0 || dtype > 1 || M <= 0 || F <= 0 || K <= 0 || bad_size(M) || bad_half_size(F) ||
       bad_size(K))
     return 0;
-  static float some;   // only tells which outputs are wanted: all of them
   GluGradCall c = {};
   c.half = dtype == 1;
   c.aligned = aligned != 0;
   c.M = M;
   c.F = F;
   c.K = K;
-  c.dX = &some;
-  c.dW = &some;
-  c.dw32 = true;
-  const size_t with32 = dgemm::glu_grad_workspace(c);
-  c.dw32 = false;
-  const size_t with16 = dgemm::glu_grad_workspace(c);
-  return with32 > with16 ? with32 : with16;
+  // without the 16-byte rows, also what a call takes that has them
+  const size_t bytes = dgemm::glu_grad_workspace(c);
+  c.aligned = true;
+  const size_t least = dgemm::glu_grad_workspace(c);
+  return bytes > least ? bytes : least;
 }
 
 }  // extern "C"

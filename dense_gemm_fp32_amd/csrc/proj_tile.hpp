@@ -213,6 +213,16 @@ struct ProjTiles {
   typedef H16Tile<64, 64, 256 / EB, 2, 2, 3, 8, 16, EB> Small3;    // 4 waves,  96 KB
 };
 
+// fp32 is bound by its matrix instructions, an eighth of fp16's rate, so a tile's
+// time goes with its area and the small one, which leaves less of the last round
+// empty, is ahead up to some 500 of the larger (us, 64x64 first: gated 1000 x 1500 x
+// 517 32.8, 40.7; 2048^3 126, 134; gated 2048^3 249, 242; 4096^3 958, 933).
+template <>
+struct ProjTiles<4> {
+  typedef H16Tile<128, 128, 32, 4, 2, 2, 8, 16, 4> Mid;            // 8 waves,  68 KB
+  typedef H16Tile<64, 64, 32, 2, 2, 2, 8, 16, 4> Small;            // 4 waves,  34 KB
+};
+
 inline double tile_cost(long long tiles, int round, double whole, double half) {
   const long long left = tiles % round;
   return (double)(tiles / round) * whole + (left == 0 ? 0.0 : (2 * left <= round ? half : whole));
@@ -221,18 +231,26 @@ inline double tile_cost(long long tiles, int round, double whole, double half) {
 template <int EB, int OUT, typename TO>
 hipError_t launch_tiles(const ProjParams &e, hipStream_t stream) {
   typedef ProjTiles<EB> P;
-  const long long large = proj_tiles<typename P::Large, OUT>(e);
-  const long long mid = proj_tiles<typename P::Mid, OUT>(e);
-  const long long small = proj_tiles<typename P::Small, OUT>(e);
-  const double l = tile_cost(large, kCUs, 55.0, 55.0);
-  const double m = tile_cost(mid, 2 * kCUs, 37.0, 22.0);
-  const double s = tile_cost(small, 2 * kCUs, 14.5, 12.0);
-  if (l <= m && l <= s) return launch_tile<typename P::Large, OUT, TO>(e, stream);
-  if (m <= s)
-    return mid <= kCUs ? launch_tile<typename P::Mid3, OUT, TO>(e, stream)
-                       : launch_tile<typename P::Mid, OUT, TO>(e, stream);
-  return small <= kCUs ? launch_tile<typename P::Small3, OUT, TO>(e, stream)
-                       : launch_tile<typename P::Small, OUT, TO>(e, stream);
+  if constexpr (EB == 4) {
+    const long long mid = (proj_tiles<typename P::Mid, OUT>(e) + kCUs - 1) / kCUs;
+    const long long small = (proj_tiles<typename P::Small, OUT>(e) + kCUs - 1) / kCUs;
+    if (mid > 1 && 4.0 * (double)mid <= 1.03 * (double)small)
+      return launch_tile<typename P::Mid, OUT, TO>(e, stream);
+    return launch_tile<typename P::Small, OUT, TO>(e, stream);
+  } else {
+    const long long large = proj_tiles<typename P::Large, OUT>(e);
+    const long long mid = proj_tiles<typename P::Mid, OUT>(e);
+    const long long small = proj_tiles<typename P::Small, OUT>(e);
+    const double l = tile_cost(large, kCUs, 55.0, 55.0);
+    const double m = tile_cost(mid, 2 * kCUs, 37.0, 22.0);
+    const double s = tile_cost(small, 2 * kCUs, 14.5, 12.0);
+    if (l <= m && l <= s) return launch_tile<typename P::Large, OUT, TO>(e, stream);
+    if (m <= s)
+      return mid <= kCUs ? launch_tile<typename P::Mid3, OUT, TO>(e, stream)
+                         : launch_tile<typename P::Mid, OUT, TO>(e, stream);
+    return small <= kCUs ? launch_tile<typename P::Small3, OUT, TO>(e, stream)
+                         : launch_tile<typename P::Small, OUT, TO>(e, stream);
+  }
 }
 
 }  // namespace dgemm

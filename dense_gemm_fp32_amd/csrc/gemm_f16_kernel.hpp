@@ -154,7 +154,8 @@ struct H16Tile {
 //   index-major: a transpose-read pass covers four k rows x 64 bytes; XORing
 //      chunk bits 2-3 with kr % 4 puts the four rows' 64-byte pieces in the
 //      four quarters of the window (rows of 128 bytes, two to a window: bit 2
-//      with (kr/2) % 2).
+//      with (kr/2) % 2).  Floats are read one by one, 16 of each of four k rows
+//      four apart at a time: bits 2-3 with (kr/4) % 4.
 template <int EXT, int BK, bool KMAJ, int EB_ = 2>
 struct HRegion {
   static constexpr bool K_MAJOR = KMAJ;
@@ -163,14 +164,15 @@ struct HRegion {
   static constexpr int ROW = KMAJ ? EB * BK : EB * EXT;    // bytes per LDS row
   static constexpr int CH = ROW / 16;                       // 16-byte chunks per row
   static constexpr int RPW = ROW >= 256 ? 1 : 256 / ROW;    // rows per 256-byte window
-  static constexpr int READS = KMAJ ? 1 : 2;                // LDS reads per fragment
-  static_assert(KMAJ || EB == 2, "transpose reads are of halves");
-  static_assert(KMAJ || ROW >= 128, "index-major rows of at least 128 bytes");
+  static constexpr int READS = KMAJ ? 1 : EB;               // LDS reads per fragment
+  static_assert(KMAJ || EB != 1, "index-major operands are halves or floats");
+  static_assert(KMAJ || ROW >= (EB == 4 ? 256 : 128), "index-major rows of at least 128 bytes");
   static_assert(!KMAJ || (32 % RPW == 0 && (32 / RPW) % CH == 0),
                 "the swizzle repeats every 32 rows");
 
   __device__ static __forceinline__ int swz(int row) {
     if constexpr (KMAJ) return (row / RPW) % CH;
+    else if constexpr (EB == 4) return 4 * ((row >> 2) & 3);
     else if constexpr (ROW >= 256) return 4 * (row & 3) + 2 * ((row >> 3) & 1);
     else return 4 * ((row >> 1) & 1);
   }
@@ -187,7 +189,7 @@ struct HRegion {
       kk = 16 / EB * c;
     } else {
       kk = row;
-      idx = 8 * c;
+      idx = 16 / EB * c;
     }
   }
 };
@@ -256,8 +258,8 @@ __device__ __forceinline__ uint32_t direct_offset(int idx, int kk, int idx0, int
     g = g < ext ? g : ext - 1;
     return (uint32_t)R::EB * (uint32_t)((g - idx0) * ld + kk);
   } else {
-    g = g + 8 <= ext ? g : ext - 8;
-    return 2u * (uint32_t)(kk * ld + (g - idx0));
+    g = g + 16 / R::EB <= ext ? g : ext - 16 / R::EB;
+    return (uint32_t)R::EB * (uint32_t)(kk * ld + (g - idx0));
   }
 }
 
@@ -387,7 +389,13 @@ template <class R>
 __device__ __forceinline__ u32x4 staged_chunk(const void *X, int ld, int idx0, int ext, int k0,
                                               int K, int idx, int kk, int w) {
   const int g = idx0 + idx, gk = k0 + kk;
-  if constexpr (R::EB != 2) {
+  if constexpr (R::EB == 4 && !R::K_MAJOR) {
+    // whole 16 bytes of a row up to `ext`, which the launch has rounded up to them
+    const char *src = static_cast<const char *>(X) + 4 * ((size_t)gk * (size_t)ld + g);
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    if (g < ext && gk < K) v = *reinterpret_cast<const u32x4 *>(src);
+    return v;
+  } else if constexpr (R::EB != 2) {
     // 8-bit integers and floats: rows that start at 16 bytes only, so the 16
     // bytes that hold a row's last elements are one aligned granule, in the same
     // page as them; what it holds behind the row is cleared.
@@ -490,6 +498,12 @@ __device__ __forceinline__ void op_setup(int w0, OpAddr<R, SUB, NB> &f) {
     const int sw = R::swz(row);
 #pragma unroll
     for (int s = 0; s < SUB; ++s) f.o[s] = row * R::ROW + 16 * ((G * s + lh) ^ sw);
+  } else if constexpr (R::EB == 4) {
+    // lane l: index l % 16, k rows 4 (l / 16) .. +3 of the sub-step, one read each
+    const int g = lane / 16, i = lane % 16;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      f.o[b] = 4 * g * R::ROW + 16 * ((w0 / 4 + 4 * b + i / 4) ^ R::swz(4 * g)) + 4 * (i % 4);
   } else if constexpr (MF == 32) {
     const int g = lane / 16, i = lane % 16;
     const int kr = 8 * (g / 2) + i / 4;
@@ -521,6 +535,12 @@ __device__ __forceinline__ f16x8 op_read(const char *region, const OpAddr<R, SUB
                                          int b) {
   if constexpr (R::K_MAJOR) {
     return *reinterpret_cast<const f16x8 *>(region + f.o[s] + MF * b * R::ROW);
+  } else if constexpr (R::EB == 4) {
+    const char *base = region + f.o[b] + 16 * s * R::ROW;
+    f32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(base + j * R::ROW);
+    return __builtin_bit_cast(f16x8, v);
   } else {
     const char *base = region + f.o[b] + (512 / MF) * s * R::ROW;
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(base));

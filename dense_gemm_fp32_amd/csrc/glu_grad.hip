@@ -10,10 +10,8 @@
 // their own rounding leaves; two halves an element would halve both products'
 // rate).
 //
-// The two products: large ones of rows that start at 16 bytes run as the library's
-// own, one after the other; the others as one launch of both (glu_products.hip).
-// fp16 operands of whole 16 bytes a row are read as they are, others from copies
-// that a pass before has made, transposed so that k is contiguous in all of them.
+// The two products run as one launch of both (glu_products.hip), large ones as the
+// library's own, one after the other.
 #include "internal.hpp"
 #include "proj.hpp"
 
@@ -75,75 +73,6 @@ hipError_t slopes(const GluGradCall &c, T *Z, int ldz) {
   hipLaunchKernelGGL((glu_slopes<T>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256),
                      0, c.stream, static_cast<const T *>(c.Z), c.ldz,
                      static_cast<const T *>(c.dH), c.lddh, Z, ldz, c.M, c.F, c.act);
-  return hipGetLastError();
-}
-
-// ---------------------------------------------------------------- transposed copies
-
-// dst[c, r] = src[r, c]; dst's rows are filled up with zeros to `ld` elements, a
-// multiple of 16 bytes.
-struct Transpose {
-  const void *src;
-  void *dst;            // NULL: none
-  int rows, cols, lds, ld;
-};
-
-// Tiles of 64 x 64 elements through LDS: 16-byte pieces of src's rows, at any
-// element's address, to 16-byte pieces of dst's.
-template <typename T>
-__global__ __launch_bounds__(256) void glu_transpose(Transpose a, Transpose b, Transpose c,
-                                                     int na, int nb) {
-  constexpr int VEC = El<T>::VEC;
-  constexpr int PIECES = 64 / VEC;                     // of a tile's row
-  __shared__ T tile[64][64 + VEC / 2];                 // [column][row]
-  const int bid = blockIdx.x;
-  const int job = bid < na ? 0 : (bid < na + nb ? 1 : 2);
-  const int local = bid - (job == 0 ? 0 : (job == 1 ? na : na + nb));
-  const T *src = static_cast<const T *>(job == 0 ? a.src : (job == 1 ? b.src : c.src));
-  T *dst = static_cast<T *>(job == 0 ? a.dst : (job == 1 ? b.dst : c.dst));
-  const int rows = job == 0 ? a.rows : (job == 1 ? b.rows : c.rows);
-  const int cols = job == 0 ? a.cols : (job == 1 ? b.cols : c.cols);
-  const int lds = job == 0 ? a.lds : (job == 1 ? b.lds : c.lds);
-  const int ld = job == 0 ? a.ld : (job == 1 ? b.ld : c.ld);
-  const int across = (cols + 63) / 64;
-  const int r0 = local / across * 64, c0 = local % across * 64;
-#pragma unroll
-  for (int i = 0; i < 64 * PIECES / 256; ++i) {
-    const int q = threadIdx.x + 256 * i;
-    const int r = q / PIECES, k = q % PIECES * VEC;
-    typename El<T>::Frag v = {};
-    const T *p = src + (size_t)(r0 + r) * (size_t)lds + c0 + k;
-    if (r0 + r < rows) {
-      if (c0 + k + VEC <= cols) v = load_whole(p);
-      else if (c0 + k < cols) v = load_part(p, cols - c0 - k);
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) tile[k + e][r] = v[e];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 64 * PIECES / 256; ++i) {
-    const int q = threadIdx.x + 256 * i;
-    const int col = q / PIECES, k = q % PIECES * VEC;
-    if (c0 + col >= cols || r0 + k >= ld) continue;
-    typename El<T>::Frag v;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = tile[col][k + e];
-    *reinterpret_cast<typename El<T>::Frag *>(dst + (size_t)(c0 + col) * (size_t)ld + r0 + k) = v;
-  }
-}
-
-template <typename T>
-hipError_t transpose(const Transpose &a, const Transpose &b, const Transpose &c,
-                     hipStream_t stream) {
-  auto tiles = [](const Transpose &t) {
-    return t.dst == nullptr ? 0LL : (long long)((t.rows + 63) / 64) * ((t.cols + 63) / 64);
-  };
-  const long long na = tiles(a), nb = tiles(b), n = na + nb + tiles(c);
-  if (n == 0) return hipSuccess;
-  if (n > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((glu_transpose<T>), dim3((unsigned)n), dim3(256), 0, stream, a, b, c, (int)na,
-                     (int)nb);
   return hipGetLastError();
 }
 
@@ -235,13 +164,13 @@ int vec_ld(const GluGradCall &c, int n) {       // rows of whole 16 bytes
   return (n + v - 1) / v * v;
 }
 
-// The two products on k-contiguous operands, without addresses yet.
+// The two products as one launch's, without addresses yet.
 ProductJob job_x(const GluGradCall &c) {
   ProductJob j = {};
   j.M = c.M;
   j.N = c.K;
   j.K = 2 * c.F;
-  j.lda = j.ldb = vec_ld(c, j.K);
+  j.lda = vec_ld(c, j.K);
   j.ldc = c.lddx;
   j.beta = c.beta_x;
   return j;
@@ -252,33 +181,33 @@ ProductJob job_w(const GluGradCall &c) {
   j.M = 2 * c.F;
   j.N = c.K;
   j.K = c.M;
-  j.lda = j.ldb = vec_ld(c, j.K);
+  j.lda = vec_ld(c, j.M);
   j.ldc = c.lddw;
   j.beta = c.beta_w;
   return j;
 }
 
-constexpr double kTogetherF16 = 1.0e10, kTogetherF32 = 2.0e8;
+// Products of rows, hidden and width below which one launch is ahead of the
+// library's two (us, one launch first: fp16 257 x 1024 x 1024 19, 31; 2048^3 93, 109;
+// 4096 x 1024 x 4096 167, 155; fp32 16 x 2000 x 1024 23, 53; 1024 x 2048 x 2048 265,
+// 267; 2048^3 517, 506).  Rows that the library would copy or load by elements take
+// it at any size (3000 x 2000 x 2050 with odd rows: fp16 156, 387; fp32 833, 1094).
+constexpr double kTogetherF16 = 1.0e10, kTogetherF32 = 5.0e9;
 
-enum class Way { kInTurn, kCopies, kInPlace };
-
-Way way_of(const GluGradCall &c) {
+bool together(const GluGradCall &c) {
   const long long eb = c.half ? 2 : 4;
   // a tile's offsets have to fit 32 bits
-  if (2LL * c.F * eb >= kTileRowBytes || c.M * eb >= kTileRowBytes) return Way::kInTurn;
-  const int v = c.half ? 8 : 4;
-  if (!(c.aligned && c.K % v == 0 && 2 * c.F % v == 0)) return Way::kCopies;
-  if ((double)c.M * c.F * c.K >= (c.half ? kTogetherF16 : kTogetherF32)) return Way::kInTurn;
-  return c.half ? Way::kInPlace : Way::kCopies;
+  if (2LL * c.F * eb >= kTileRowBytes || c.K * eb >= kTileRowBytes) return false;
+  return !c.aligned || (double)c.M * c.F * c.K < (c.half ? kTogetherF16 : kTogetherF32);
 }
 
 struct GradSpace {
-  void *D, *DT;    // [dG dU]: M rows of ldd elements; transposed
-  void *XT, *WT;
-  float *sx, *sw;  // parts of the products along k
+  void *D;         // [dG dU]: M rows of ldd elements
   int ldd;
-  char *W;         // the forward pass's and the library's products', one after the other
-  size_t w_bytes;
+  void *X, *W;     // copies with rows that start at 16 bytes
+  float *sx, *sw;  // parts of the products along k
+  char *ws;        // the forward pass's and the library's products', one after the other
+  size_t ws_bytes;
 };
 
 size_t carve(const GluGradCall &c, void *base, GradSpace *s) {
@@ -287,25 +216,23 @@ size_t carve(const GluGradCall &c, void *base, GradSpace *s) {
   const size_t eb = c.half ? 2 : 4;
   s->ldd = vec_ld(c, 2 * c.F);
   s->D = w.take<char>((size_t)c.M * (size_t)s->ldd * eb);
-  s->w_bytes = c.Z != nullptr ? 0 : proj_workspace(forward_of(c, nullptr, s->ldd));
-  const Way way = way_of(c);
-  if (way != Way::kInTurn) {
+  s->ws_bytes = c.Z != nullptr ? 0 : proj_workspace(forward_of(c, nullptr, s->ldd));
+  if (together(c)) {
     ProductJob x = job_x(c), d = job_w(c);
     plan_products(c.half, x, d);
-    if (way == Way::kCopies) {
-      s->DT = w.take<char>((size_t)d.M * (size_t)d.lda * eb);
-      s->XT = w.take<char>((size_t)d.N * (size_t)d.ldb * eb);
-      s->WT = w.take<char>((size_t)x.N * (size_t)x.ldb * eb);
+    if (!c.aligned) {
+      s->X = w.take<char>((size_t)c.M * (size_t)vec_ld(c, c.K) * eb);
+      s->W = w.take<char>((size_t)c.F * 2 * (size_t)vec_ld(c, c.K) * eb);
     }
     if (x.splits > 1) s->sx = w.take<float>((size_t)x.splits * x.M * (size_t)((x.N + 3) / 4 * 4));
     if (d.splits > 1) s->sw = w.take<float>((size_t)d.splits * d.M * (size_t)((d.N + 3) / 4 * 4));
   } else {
     const size_t x = product_bytes(c, product_x(c, nullptr, s->ldd));
     const size_t d = product_bytes(c, product_w(c, nullptr, s->ldd));
-    s->w_bytes = x > s->w_bytes ? x : s->w_bytes;
-    s->w_bytes = d > s->w_bytes ? d : s->w_bytes;
+    s->ws_bytes = x > s->ws_bytes ? x : s->ws_bytes;
+    s->ws_bytes = d > s->ws_bytes ? d : s->ws_bytes;
   }
-  s->W = w.take<char>(s->w_bytes);
+  s->ws = w.take<char>(s->ws_bytes);
   return w.used;
 }
 
@@ -325,34 +252,36 @@ hipError_t sum_parts(const ProductJob &j, bool half_out, hipStream_t stream) {
   return launch_splitk_reduce(r, stream);
 }
 
-hipError_t products_together(const GluGradCall &c, const GradSpace &s, bool inplace) {
+hipError_t products_together(const GluGradCall &c, const GradSpace &s) {
   ProductJob x = job_x(c), d = job_w(c);
   const ProductPlan plan = plan_products(c.half, x, d);
-  x.A = s.D;
+  x.A = d.A = s.D;
+  x.B = c.W;
+  x.ldb = c.ldw;
   x.C = c.dX;
   x.slab = s.sx;
+  d.B = c.X;
+  d.ldb = c.ldx;
   d.C = c.dW;
   d.slab = s.sw;
   hipError_t e = hipSuccess;
-  if (inplace) {
-    x.B = c.W;
-    x.ldb = c.ldw;
-    d.A = s.D;
-    d.lda = s.ldd;
-    d.B = c.X;
-    d.ldb = c.ldx;
-  } else {
-    x.B = s.WT;
-    d.A = s.DT;
-    d.B = s.XT;
-    const Transpose tw = {c.W, c.dX ? s.WT : nullptr, 2 * c.F, c.K, c.ldw, x.ldb};
-    const Transpose tx = {c.X, c.dW ? s.XT : nullptr, c.M, c.K, c.ldx, d.ldb};
-    const Transpose td = {s.D, c.dW ? s.DT : nullptr, c.M, 2 * c.F, s.ldd, d.lda};
-    e = c.half ? transpose<_Float16>(tw, tx, td, c.stream)
-               : transpose<float>(tw, tx, td, c.stream);
+  if (!c.aligned) {
+    const long long eb = c.half ? 2 : 4, row = c.K * eb;
+    const bool copy_w = c.dX != nullptr && !rows_at_16(c.W, c.ldw, (int)eb);
+    const bool copy_x = c.dW != nullptr && !rows_at_16(c.X, c.ldx, (int)eb);
+    const RowCopy w = {c.W, c.ldw * eb, row, 2 * c.F, copy_w ? s.W : nullptr};
+    const RowCopy v = {c.X, c.ldx * eb, row, c.M, copy_x ? s.X : nullptr};
+    if (copy_w) {
+      x.B = s.W;
+      x.ldb = vec_ld(c, c.K);
+    }
+    if (copy_x) {
+      d.B = s.X;
+      d.ldb = vec_ld(c, c.K);
+    }
+    if (copy_w || copy_x) e = launch_row_copies(w, v, c.stream);
   }
-  if (e != hipSuccess) return e;
-  e = launch_products(c.half, c.dw32, plan.mid, inplace, x, d, c.stream);
+  if (e == hipSuccess) e = launch_products(c.half, c.dw32, plan.mid, x, d, c.stream);
   if (e == hipSuccess && x.C != nullptr && x.splits > 1) e = sum_parts(x, c.half, c.stream);
   if (e == hipSuccess && d.C != nullptr && d.splits > 1)
     e = sum_parts(d, c.half && !c.dw32, c.stream);
@@ -363,8 +292,8 @@ hipError_t products_in_turn(const GluGradCall &c, const GradSpace &s) {
   for (int w = 0; w < 2; ++w) {
     if ((w ? c.dW : c.dX) == nullptr) continue;
     Call g = w ? product_w(c, s.D, s.ldd) : product_x(c, s.D, s.ldd);
-    g.ws_fixed = s.W;
-    g.ws_fixed_bytes = s.w_bytes;
+    g.ws_fixed = s.ws;
+    g.ws_fixed_bytes = s.ws_bytes;
     const hipError_t e = c.half ? launch_f16(g) : launch_f32(g);
     if (e != hipSuccess) return e;
   }
@@ -382,13 +311,11 @@ hipError_t launch_glu_grad(const GluGradCall &c, void *ws) {
   GradSpace s;
   carve(c, ws, &s);
   hipError_t e;
-  if (c.Z == nullptr) e = launch_proj(forward_of(c, s.D, s.ldd), s.W);
+  if (c.Z == nullptr) e = launch_proj(forward_of(c, s.D, s.ldd), s.ws);
   else if (c.half) e = slopes(c, static_cast<_Float16 *>(s.D), s.ldd);
   else e = slopes(c, static_cast<float *>(s.D), s.ldd);
   if (e != hipSuccess) return e;
-  const Way way = way_of(c);
-  return way == Way::kInTurn ? products_in_turn(c, s)
-                             : products_together(c, s, way == Way::kInPlace);
+  return together(c) ? products_together(c, s) : products_in_turn(c, s);
 }
 
 }  // namespace dgemm

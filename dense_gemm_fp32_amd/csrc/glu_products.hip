@@ -1,11 +1,12 @@
 // glu_products.hip -- the two products of a gated block's backward pass in one
-// launch: dX = [dG dU] W and dW = [dG dU]^T X, of middling sizes and of rows that
-// would have to be copied in any case.
+// launch: dX = [dG dU] W and dW = [dG dU]^T X.
 //
 // Both run on the tiles of proj_tile.hpp, and the workgroups of one fill the CUs
-// that the other leaves idle.  In place: fp16 operands as they are, W and X
-// index-major and [dG dU] transposed in LDS (HRegion).  Else k-contiguous copies of
-// all of them, transposed where the operand is.
+// that the other leaves idle.  The operands are read as they lie: k runs along
+// the rows of [dG dU] in the first product, along its columns in the second, and
+// along W's and X's columns in both; such an operand keeps its orientation in LDS
+// (HRegion) and its fragments are read across.  Rows start at 16 bytes; what the
+// last 16 of a row hold behind it only feeds columns that are not stored.
 #include "proj_tile.hpp"
 
 namespace dgemm {
@@ -14,11 +15,11 @@ namespace {
 
 // b_first: the workgroups of b come first.  The first job's are rounded up to a
 // multiple of the XCDs, so that both jobs' tiles keep to one XCD each.
-template <class T, typename TA, typename TB, bool VEC, bool INPLACE>
+template <class T, typename TA, typename TB, bool VEC>
 __global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob b, int first,
                                                        bool b_first) {
-  typedef HLayout<T, false, !INPLACE> LA;
-  typedef HLayout<T, INPLACE, !INPLACE> LB;
+  typedef HLayout<T, false, false> LA;
+  typedef HLayout<T, true, false> LB;
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
   lds_poison(lds, T::LDS_BYTES);
   const bool early = (int)blockIdx.x < first;
@@ -44,9 +45,8 @@ __global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob 
   const int m0 = tm * T::BM, n0 = tn * T::BN;
   if (splits > 1) {
     const int kb = split * chunk;
-    const bool ta = INPLACE && second, tb = !INPLACE;
-    p.A = static_cast<const char *>(p.A) + (size_t)kb * T::EB * (ta ? (size_t)p.lda : 1);
-    p.B = static_cast<const char *>(p.B) + (size_t)kb * T::EB * (tb ? 1 : (size_t)p.ldb);
+    p.A = static_cast<const char *>(p.A) + (size_t)kb * T::EB * (second ? (size_t)p.lda : 1);
+    p.B = static_cast<const char *>(p.B) + (size_t)kb * T::EB * (size_t)p.ldb;
     p.K = p.K - kb < chunk ? p.K - kb : chunk;
   }
   const int wave = threadIdx.x / kWave;
@@ -54,7 +54,11 @@ __global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob 
   const int wn0 = (wave % T::WAVES_N) * T::WTN;
   typename T::Acc acc[T::FM][T::FN];
   zero_acc<T>(acc);
-  if (INPLACE && second)
+  // what the loads may read: whole 16 bytes
+  constexpr int V = 16 / T::EB;
+  p.M = second ? (p.M + V - 1) / V * V : p.M;
+  p.N = (p.N + V - 1) / V * V;
+  if (second)
     mainloop_direct<T, LB>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
   else
     mainloop_direct<T, LA>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
@@ -62,8 +66,8 @@ __global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob 
   __syncthreads();   // every wave is done with the pipeline slots
   if (splits > 1) {
     float *slab = second ? b.slab : a.slab;
-    e.ldy = (p.N + 3) / 4 * 4;
-    e.Y = slab + (size_t)split * (size_t)p.M * (size_t)e.ldy;
+    e.ldy = (e.N + 3) / 4 * 4;
+    e.Y = slab + (size_t)split * (size_t)e.M * (size_t)e.ldy;
     proj_epilogue<T, kScaled, float, true>(e, m0 + wm0, n0 + wn0, lds, acc);
   } else if (second) {
     e.Y = b.C;
@@ -84,7 +88,7 @@ long long tiles_of_job(const ProductJob &j) {
   return (long long)((j.M + T::BM - 1) / T::BM) * ((j.N + T::BN - 1) / T::BN) * j.splits;
 }
 
-template <class T, typename TA, typename TB, bool INPLACE>
+template <class T, typename TA, typename TB>
 hipError_t launch(const ProductJob &a, const ProductJob &b, hipStream_t stream) {
   const long long na = tiles_of_job<T>(a), nb = tiles_of_job<T>(b);
   // the longer workgroups first
@@ -97,18 +101,18 @@ hipError_t launch(const ProductJob &a, const ProductJob &b, hipStream_t stream) 
   };
   const dim3 g((unsigned)(start + other)), t(T::NT);
   if (vec(a, (int)sizeof(TA)) && vec(b, (int)sizeof(TB)))
-    hipLaunchKernelGGL((proj_products<T, TA, TB, true, INPLACE>), g, t, 0, stream, a, b, (int)start,
+    hipLaunchKernelGGL((proj_products<T, TA, TB, true>), g, t, 0, stream, a, b, (int)start,
                        b_first);
   else
-    hipLaunchKernelGGL((proj_products<T, TA, TB, false, INPLACE>), g, t, 0, stream, a, b, (int)start,
+    hipLaunchKernelGGL((proj_products<T, TA, TB, false>), g, t, 0, stream, a, b, (int)start,
                        b_first);
   return hipGetLastError();
 }
 
-template <int EB, typename TA, typename TB, bool INPLACE>
+template <int EB, typename TA, typename TB>
 hipError_t run(const ProductJob &a, const ProductJob &b, bool mid, hipStream_t stream) {
-  return mid ? launch<typename ProjTiles<EB>::Mid, TA, TB, INPLACE>(a, b, stream)
-             : launch<typename ProjTiles<EB>::Small, TA, TB, INPLACE>(a, b, stream);
+  return mid ? launch<typename ProjTiles<EB>::Mid, TA, TB>(a, b, stream)
+             : launch<typename ProjTiles<EB>::Small, TA, TB>(a, b, stream);
 }
 
 // One tile's step, in microseconds with the CU full, and how many of its steps a
@@ -167,14 +171,11 @@ ProductPlan plan_products(bool half, ProductJob &a, ProductJob &b) {
   return best;
 }
 
-hipError_t launch_products(bool half, bool b32, bool mid, bool inplace, const ProductJob &a,
-                           const ProductJob &b, hipStream_t stream) {
-  if (!half) return run<4, float, float, false>(a, b, mid, stream);
-  if (inplace)
-    return b32 ? run<2, _Float16, float, true>(a, b, mid, stream)
-               : run<2, _Float16, _Float16, true>(a, b, mid, stream);
-  return b32 ? run<2, _Float16, float, false>(a, b, mid, stream)
-             : run<2, _Float16, _Float16, false>(a, b, mid, stream);
+hipError_t launch_products(bool half, bool b32, bool mid, const ProductJob &a, const ProductJob &b,
+                           hipStream_t stream) {
+  if (!half) return run<4, float, float>(a, b, mid, stream);
+  return b32 ? run<2, _Float16, float>(a, b, mid, stream)
+             : run<2, _Float16, _Float16>(a, b, mid, stream);
 }
 
 }  // namespace dgemm

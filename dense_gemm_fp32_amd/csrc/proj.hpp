@@ -79,9 +79,8 @@ hipError_t launch_glu_f16(const ProjParams &p, bool slopes, hipStream_t stream);
 hipError_t launch_glu_f32(const ProjParams &p, bool slopes, hipStream_t stream);
 
 // One of the two products of a gated block's backward pass (glu_products.hip):
-// C := A B^T + beta * C over k-contiguous rows that start at 16 bytes (in place,
-// fp16: a's B and both of b's operands have k along their columns, whole 16 bytes of
-// it in each row).
+// C := A B + beta * C, B's rows along k, and A's in the second product.  Rows of
+// both start at 16 bytes.
 struct ProductJob {
   const void *A, *B;
   void *C;                // NULL: not wanted
@@ -96,8 +95,8 @@ struct ProductPlan {
 };
 ProductPlan plan_products(bool half, ProductJob &a, ProductJob &b);   // sets splits, chunk
 // half: A and B hold fp16 (and C, but b's fp32 with b32), else fp32
-hipError_t launch_products(bool half, bool b32, bool mid, bool inplace, const ProductJob &a,
-                           const ProductJob &b, hipStream_t stream);
+hipError_t launch_products(bool half, bool b32, bool mid, const ProductJob &a, const ProductJob &b,
+                           hipStream_t stream);
 
 // ---------------------------------------------------------------- few rows
 

@@ -115,34 +115,46 @@ hipError_t run(const ProductJob &a, const ProductJob &b, bool mid, hipStream_t s
              : launch<typename ProjTiles<EB>::Small, TA, TB>(a, b, stream);
 }
 
-// One tile's step, in microseconds with the CU full, and how many of its steps a
-// launch's longest workgroup adds: what 64x64 and 128x128 tiles reach in
-// proj_tile.hpp's products.
+// A tile: its step in microseconds with the CU full (what it reaches in
+// proj_tile.hpp's products), how many steps the longest workgroup adds to a launch,
+// and, for fp32, how many workgroups a CU holds.  fp32 is bound by its matrix
+// instructions, and a launch whose workgroups all fit at once lasts as long as the
+// CU that was dealt one more than the others (us by parts of the first product's k,
+// 257 x 1024 x 1024: 1 55, 2 38, 3 34, 4 40, 5 37, 6 36; 1000 x 1500 x 517: 1 105,
+// 2 90, 3 93, 4 86, 5 91, 6 94).
 struct StepCost {
   int bm, bk;
   double step, longest;
+  int slots;
 };
 
 double cost(const StepCost &t, const ProductJob &a, const ProductJob &b, int sa, int sb) {
-  double work = 0.0, longest = 0.0, sums = 0.0;
+  double work = 0.0, longest = 0.0, sums = 0.0, wgs = 0.0;
   for (int i = 0; i < 2; ++i) {
     const ProductJob &j = i ? b : a;
     const int s = i ? sb : sa;
     const double tiles = (double)((j.M + t.bm - 1) / t.bm) * ((j.N + t.bm - 1) / t.bm);
     const int steps = (j.K + t.bk - 1) / t.bk, chunk = (steps + s - 1) / s;
     work += tiles * steps;
+    wgs += tiles * s;
     if (chunk > longest) longest = chunk;
     // a launch of its own, and the parts written and read at 4 TB/s
     if (s > 1) sums += 3.5 + s * (double)j.M * (double)j.N * 8.0 / 4.0e6;
   }
-  return t.step * (work / kCUs + t.longest * longest) + sums;
+  double steps = work / kCUs + t.longest * longest;
+  if (wgs <= t.slots * (double)kCUs) {
+    const int most = (int)((wgs + kCUs - 1) / kCUs);
+    steps = most * work / wgs;
+    if (steps < longest) steps = longest;
+  }
+  return t.step * steps + sums;
 }
 
 }  // namespace
 
 ProductPlan plan_products(bool half, ProductJob &a, ProductJob &b) {
-  const StepCost f16[2] = {{64, 128, 0.45, 1.0}, {128, 64, 0.58, 1.0}};
-  const StepCost f32[2] = {{64, 32, 0.43, 0.5}, {128, 32, 1.70, 0.5}};
+  const StepCost f16[2] = {{64, 128, 0.45, 1.0, 0}, {128, 64, 0.58, 1.0, 0}};
+  const StepCost f32[2] = {{64, 32, 0.43, 0.5, 4}, {128, 32, 1.70, 0.5, 2}};
   ProductPlan best = {false, 1e300};
   int bsa = 1, bsb = 1;
   for (int m = 0; m < 2; ++m) {

@@ -448,6 +448,11 @@ def _call_rows(fn, dev, stream, workspace, need, args):
     if dev != _current_device():      # a default stream means the current GPU's
         with torch.cuda.device(dev):
             return _call_rows(fn, dev, stream, workspace, need, args)
+    if stream is None and workspace is None and need == 0:
+        rc = fn(*args, None, 0, _current_stream(dev))
+        if rc != 0:
+            raise GemmError(rc)
+        return
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
         raise ValueError("the stream must be one of GPU %d, like the first tensor" % dev)
     if workspace is not None:

@@ -216,8 +216,10 @@ size_t carve(const GluGradCall &c, void *base, GradSpace *s) {
   const size_t eb = c.half ? 2 : 4;
   s->ldd = vec_ld(c, 2 * c.F);
   s->D = w.take<char>((size_t)c.M * (size_t)s->ldd * eb);
-  s->ws_bytes = c.Z != nullptr ? 0 : proj_workspace(forward_of(c, nullptr, s->ldd));
-  if (together(c)) {
+  const bool one = together(c);
+  // (one launch's operands are copied ahead of the forward pass)
+  if (c.Z == nullptr && !one) s->ws_bytes = proj_workspace(forward_of(c, nullptr, s->ldd));
+  if (one) {
     ProductJob x = job_x(c), d = job_w(c);
     plan_products(c.half, x, d);
     if (!c.aligned) {
@@ -264,28 +266,29 @@ hipError_t products_together(const GluGradCall &c, const GradSpace &s) {
   d.ldb = c.ldx;
   d.C = c.dW;
   d.slab = s.sw;
-  hipError_t e = hipSuccess;
-  if (!c.aligned) {
-    const long long eb = c.half ? 2 : 4, row = c.K * eb;
-    const bool copy_w = c.dX != nullptr && !rows_at_16(c.W, c.ldw, (int)eb);
-    const bool copy_x = c.dW != nullptr && !rows_at_16(c.X, c.ldx, (int)eb);
-    const RowCopy w = {c.W, c.ldw * eb, row, 2 * c.F, copy_w ? s.W : nullptr};
-    const RowCopy v = {c.X, c.ldx * eb, row, c.M, copy_x ? s.X : nullptr};
-    if (copy_w) {
-      x.B = s.W;
-      x.ldb = vec_ld(c, c.K);
-    }
-    if (copy_x) {
-      d.B = s.X;
-      d.ldb = vec_ld(c, c.K);
-    }
-    if (copy_w || copy_x) e = launch_row_copies(w, v, c.stream);
-  }
-  if (e == hipSuccess) e = launch_products(c.half, c.dw32, plan.mid, x, d, c.stream);
+  hipError_t e = launch_products(c.half, c.dw32, plan.mid, x, d, c.stream);
   if (e == hipSuccess && x.C != nullptr && x.splits > 1) e = sum_parts(x, c.half, c.stream);
   if (e == hipSuccess && d.C != nullptr && d.splits > 1)
     e = sum_parts(d, c.half && !c.dw32, c.stream);
   return e;
+}
+
+// Copies of X and W, where their rows need it, in place of them.
+hipError_t copy_operands(GluGradCall &c, const GradSpace &s) {
+  const long long eb = c.half ? 2 : 4, row = c.K * eb;
+  const bool copy_w = (c.dX != nullptr || c.Z == nullptr) && !rows_at_16(c.W, c.ldw, (int)eb);
+  const bool copy_x = (c.dW != nullptr || c.Z == nullptr) && !rows_at_16(c.X, c.ldx, (int)eb);
+  const RowCopy w = {c.W, c.ldw * eb, row, 2 * c.F, copy_w ? s.W : nullptr};
+  const RowCopy x = {c.X, c.ldx * eb, row, c.M, copy_x ? s.X : nullptr};
+  if (copy_w) {
+    c.W = s.W;
+    c.ldw = vec_ld(c, c.K);
+  }
+  if (copy_x) {
+    c.X = s.X;
+    c.ldx = vec_ld(c, c.K);
+  }
+  return copy_w || copy_x ? launch_row_copies(w, x, c.stream) : hipSuccess;
 }
 
 hipError_t products_in_turn(const GluGradCall &c, const GradSpace &s) {
@@ -307,15 +310,22 @@ size_t glu_grad_workspace(const GluGradCall &c) {
   return carve(c, nullptr, &s);
 }
 
-hipError_t launch_glu_grad(const GluGradCall &c, void *ws) {
+hipError_t launch_glu_grad(const GluGradCall &call, void *ws) {
+  GluGradCall c = call;
   GradSpace s;
   carve(c, ws, &s);
-  hipError_t e;
+  const bool one = together(c);
+  hipError_t e = hipSuccess;
+  if (one && !c.aligned) {
+    e = copy_operands(c, s);
+    c.aligned = true;
+  }
+  if (e != hipSuccess) return e;
   if (c.Z == nullptr) e = launch_proj(forward_of(c, s.D, s.ldd), s.ws);
   else if (c.half) e = slopes(c, static_cast<_Float16 *>(s.D), s.ldd);
   else e = slopes(c, static_cast<float *>(s.D), s.ldd);
   if (e != hipSuccess) return e;
-  return together(c) ? products_together(c, s) : products_in_turn(c, s);
+  return one ? products_together(c, s) : products_in_turn(c, s);
 }
 
 }  // namespace dgemm

@@ -15,7 +15,7 @@ namespace {
 
 // b_first: the workgroups of b come first.  The first job's are rounded up to a
 // multiple of the XCDs, so that both jobs' tiles keep to one XCD each.
-template <class T, typename TA, typename TB, bool VEC>
+template <class T, typename TA, typename TB>
 __global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob b, int first,
                                                        bool b_first) {
   typedef HLayout<T, false, false> LA;
@@ -68,17 +68,17 @@ __global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob 
     float *slab = second ? b.slab : a.slab;
     e.ldy = (e.N + 3) / 4 * 4;
     e.Y = slab + (size_t)split * (size_t)e.M * (size_t)e.ldy;
-    proj_epilogue<T, kScaled, float, true>(e, m0 + wm0, n0 + wn0, lds, acc);
+    proj_epilogue<T, kScaled, float>(e, m0 + wm0, n0 + wn0, lds, acc);
   } else if (second) {
     e.Y = b.C;
     e.ldy = b.ldc;
     e.beta = b.beta;
-    proj_epilogue<T, kScaled, TB, VEC>(e, m0 + wm0, n0 + wn0, lds, acc);
+    proj_epilogue<T, kScaled, TB>(e, m0 + wm0, n0 + wn0, lds, acc);
   } else {
     e.Y = a.C;
     e.ldy = a.ldc;
     e.beta = a.beta;
-    proj_epilogue<T, kScaled, TA, VEC>(e, m0 + wm0, n0 + wn0, lds, acc);
+    proj_epilogue<T, kScaled, TA>(e, m0 + wm0, n0 + wn0, lds, acc);
   }
 }
 
@@ -96,16 +96,8 @@ hipError_t launch(const ProductJob &a, const ProductJob &b, hipStream_t stream) 
   const long long first = b_first ? nb : na, other = b_first ? na : nb;
   const long long start = other > 0 ? (first + kXcds - 1) / kXcds * kXcds : first;
   if (start + other > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  auto vec = [](const ProductJob &j, int eb) {
-    return j.C == nullptr || (j.ldc % 4 == 0 && aligned_to(j.C, 4 * (uintptr_t)eb));
-  };
-  const dim3 g((unsigned)(start + other)), t(T::NT);
-  if (vec(a, (int)sizeof(TA)) && vec(b, (int)sizeof(TB)))
-    hipLaunchKernelGGL((proj_products<T, TA, TB, true>), g, t, 0, stream, a, b, (int)start,
-                       b_first);
-  else
-    hipLaunchKernelGGL((proj_products<T, TA, TB, false>), g, t, 0, stream, a, b, (int)start,
-                       b_first);
+  hipLaunchKernelGGL((proj_products<T, TA, TB>), dim3((unsigned)(start + other)), dim3(T::NT), 0,
+                     stream, a, b, (int)start, b_first);
   return hipGetLastError();
 }
 

@@ -40,21 +40,48 @@ hipError_t skinny(const ProjParams &p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// How wide a workgroup is, and how many waves divide its K.  Twice as many
-// columns halve what is read of X, once that leaves a workgroup per CU (64 rows
-// of 8192 8-bit integers, 8192 columns: 27.5 to 23.3 us; 4096 columns, 128
-// workgroups: 10.6 to 13); with one or more per CU four waves are enough (a gated
-// block of 64 x 8192 x 4096 halves: 33.7 us with four, 41.8 with eight), below it
-// eight are better (64 x 1024 8-bit columns of 4096: 7.0 with eight, 8.2 with
-// four).
+// How wide and how high a workgroup is, and how many waves divide its K.
+//
+// Blocks of 16 rows of X, up to four of them: what there are, if the columns alone
+// make a workgroup per CU, so that each row of W is read once.  Twice as many
+// columns halve what is read of X, once that leaves a workgroup per CU (64 rows of
+// 8192 8-bit integers, 8192 columns: 27.5 to 23.3 us; 4096 columns, 128 workgroups:
+// 10.6 to 13).  With fewer columns a workgroup takes fewer rows, W comes from the
+// cache again, and what counts is what a CU reads: blocks of X and of W, a second
+// workgroup on the CU at 0.4 of the first (us by blocks of X: gated 110 x 582 x 6640
+// halves 1 26.4, 2 17.8, 3 19.8, 4 23.2; 64 x 2048 x 4096 1 12.2, 2 9.8, 4 14.5; 64 x
+// 1024 x 4096 1 7.3, 2 9.3, 4 13.6; in 8 bits 1 4.4, 4 6.7; in fp32, gated, 1 19, 4 52).
+//
+// With one workgroup or more per CU four waves are enough (a gated block of 64 x
+// 8192 x 4096 halves: 33.7 us with four, 41.8 with eight), below it eight are better
+// (64 x 1024 8-bit columns of 4096: 7.0 with eight, 8.2 with four).
 template <typename T, typename TO, int OUT, int NB>
-hipError_t skinny_wide(const ProjParams &p, hipStream_t stream) {
+hipError_t skinny_high(const ProjParams &p, hipStream_t stream) {
   constexpr int NF = OUT == kScaled ? 1 : 2;
   constexpr int U = NB == 1 ? 2 : 1;
   const long long wgs = (long long)((p.N + 15) / 16) * ((p.M + 16 * NB - 1) / (16 * NB));
-  if (NB > 1 && wgs >= 2 * kCUs) return skinny<T, TO, OUT, 2 * NF, NB, 1, 4, U>(p, stream);
+  if (NB > 1 && 16 * NB >= p.M && wgs >= 2 * kCUs)
+    return skinny<T, TO, OUT, 2 * NF, NB, 1, 4, U>(p, stream);
   if (wgs >= kCUs) return skinny<T, TO, OUT, NF, NB, 1, 4, U>(p, stream);
   return skinny<T, TO, OUT, NF, NB, 1, 8, U>(p, stream);
+}
+
+int skinny_blocks(const ProjParams &p, int nf) {
+  const long long cols = (p.N + 15) / 16;
+  const int most = p.M >= 64 ? 4 : (p.M + 15) / 16;
+  auto wgs = [&](int nb) { return cols * ((p.M + 16 * nb - 1) / (16 * nb)); };
+  if (wgs(most) >= kCUs) return most;
+  int best = most;
+  double least = 1e300;
+  for (int nb = most; nb >= 1; --nb) {
+    const double rounds = (double)((wgs(nb) + kCUs - 1) / kCUs);
+    const double cost = (rounds > 1.0 ? 0.7 * rounds : 1.0) * (nb + nf);
+    if (cost < least) {
+      least = cost;
+      best = nb;
+    }
+  }
+  return best;
 }
 
 template <typename T, typename TO, int OUT>
@@ -64,10 +91,12 @@ hipError_t run_skinny(const ProjParams &p, hipStream_t stream) {
   // up to 8 rows two stretches of k share an instruction (and rows that are
   // further apart than the other form's offsets hold)
   if (p.M <= 8 || !near) return skinny<T, TO, OUT, OUT == kScaled ? 1 : 2, 1, 2, 8, 4>(p, stream);
-  if (p.M <= 16) return skinny_wide<T, TO, OUT, 1>(p, stream);
-  if (p.M <= 32) return skinny_wide<T, TO, OUT, 2>(p, stream);
-  if (p.M <= 48) return skinny_wide<T, TO, OUT, 3>(p, stream);
-  return skinny_wide<T, TO, OUT, 4>(p, stream);
+  switch (skinny_blocks(p, OUT == kScaled ? 1 : 2)) {
+    case 1: return skinny_high<T, TO, OUT, 1>(p, stream);
+    case 2: return skinny_high<T, TO, OUT, 2>(p, stream);
+    case 3: return skinny_high<T, TO, OUT, 3>(p, stream);
+    default: return skinny_high<T, TO, OUT, 4>(p, stream);
+  }
 }
 
 template <typename TO>
@@ -89,13 +118,14 @@ int bytes_of(const ProjCall &c) { return c.i8 ? 1 : (c.half ? 2 : 4); }
 // it 5.4, 5.1; gated 128 x 2048 x 4096 halves 19.2, 18.1; 257 rows of it 23.2,
 // 32.6).  17 to 64 rows take the 64x64 tile where there are 128 of them or more
 // (gated 64 x 8192 x 4096: 8-bit 14.7, 20.7, halves 30.1, 36.7; 20 rows 14.1, 17.5
-// and 30.0, 33.0; but 64 x 4096 x 4096 8-bit, 64 tiles: 11.7, 9.4).  Rows that
+// and 30.0, 33.0; but 64 x 4096 x 4096 8-bit, 64 tiles: 11.7, 9.4), of fp32 none.
+// Rows that
 // have to be copied for the tiles pay for it beyond 128 rows only: a copy reads
 // and writes W, which the streaming kernel reads once for every 64 rows.
 bool tiled(const ProjCall &c) {
   if ((long long)c.K * bytes_of(c) >= kTileRowBytes) return false;
   if (c.M <= 16 || (!c.aligned && c.M <= 128)) return false;
-  if (c.M <= 64) return (c.gated ? c.N / 32 : c.N / 64) >= kCUs / 2;
+  if (c.M <= 64) return (c.i8 || c.half) && (c.gated ? c.N / 32 : c.N / 64) >= kCUs / 2;
   return (long long)((c.N + 15) / 16) * ((c.M + 63) / 64) > kCUs;
 }
 

@@ -20,40 +20,39 @@
 
 namespace dgemm {
 
-// Four values from / to four neighbouring elements.
-template <typename TO, bool VEC>
+// Four values from / to four neighbouring elements (`count` of them inside the
+// matrix) at any element's address: global accesses of 8 and 16 bytes need no more
+// than the element's own alignment.
+template <typename TO>
+struct Four {
+  typedef TO Any __attribute__((ext_vector_type(4), aligned(sizeof(TO))));
+};
+
+template <typename TO>
 __device__ __forceinline__ f32x4 load4(const TO *p, int count) {
   f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (VEC && count >= 4) {
-    if constexpr (sizeof(TO) == 2) {
-      const f16x4 h = *reinterpret_cast<const f16x4 *>(p);
+  if (count >= 4) {
+    const typename Four<TO>::Any h = *reinterpret_cast<const typename Four<TO>::Any *>(p);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
-    } else {
-      v = *reinterpret_cast<const f32x4 *>(p);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 3; ++e)
       if (e < count) v[e] = (float)p[e];
   }
   return v;
 }
 
-template <typename TO, bool VEC>
+template <typename TO>
 __device__ __forceinline__ void store4(TO *p, f32x4 v, int count) {
-  if (VEC && count >= 4) {
-    if constexpr (sizeof(TO) == 2) {
-      f16x4 h;
+  if (count >= 4) {
+    typename Four<TO>::Any h;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
-      *reinterpret_cast<f16x4 *>(p) = h;
-    } else {
-      *reinterpret_cast<f32x4 *>(p) = v;
-    }
+    for (int e = 0; e < 4; ++e) h[e] = (TO)v[e];
+    *reinterpret_cast<typename Four<TO>::Any *>(p) = h;
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 3; ++e)
       if (e < count) p[e] = (TO)v[e];
   }
 }
@@ -68,7 +67,7 @@ __device__ __forceinline__ f32x4 act_values(int act, f32x4 g) {
 // From the accumulators, 32 rows at a time through the wave's staging area, to
 // memory: a lane takes four neighbouring columns of a row.  r0, c0: first row
 // and column of the wave's part of the result.
-template <class T, int OUT, typename TO, bool VEC>
+template <class T, int OUT, typename TO>
 __device__ __forceinline__ void proj_epilogue(const ProjParams &p, int r0, int c0, char *lds,
                                               const typename T::Acc (&acc)[T::FM][T::FN]) {
   constexpr int COLS = OUT == kScaled ? T::WTN : T::WTN / 2;
@@ -81,8 +80,8 @@ __device__ __forceinline__ void proj_epilogue(const ProjParams &p, int r0, int c
   f32x4 wa = f32x4{1.0f, 1.0f, 1.0f, 1.0f}, wb = wa;
   if constexpr (T::EB == 1) {
     if (p.ws != nullptr && count > 0) {
-      wa = load4<float, false>(p.ws + col, count);
-      if constexpr (OUT != kScaled) wb = load4<float, false>(p.ws + p.N + col, count);
+      wa = load4<float>(p.ws + col, count);
+      if constexpr (OUT != kScaled) wb = load4<float>(p.ws + p.N + col, count);
     }
   }
 #pragma unroll
@@ -102,11 +101,11 @@ __device__ __forceinline__ void proj_epilogue(const ProjParams &p, int r0, int c
         TO *y = static_cast<TO *>(p.Y) + (size_t)row * (size_t)p.ldy + col;
         a *= p.alpha;
         if (p.beta != 0.0f) {
-          const f32x4 c = load4<TO, VEC>(y, count);
+          const f32x4 c = load4<TO>(y, count);
 #pragma unroll
           for (int e = 0; e < 4; ++e) a[e] = __builtin_fmaf(p.beta, c[e], a[e]);
         }
-        store4<TO, VEC>(y, a, count);
+        store4<TO>(y, a, count);
       } else {
         f32x4 b = *reinterpret_cast<const f32x4 *>(&stage[rl * T::EP_STRIDE + COLS + cl]);
         if constexpr (T::EB == 1) {
@@ -115,14 +114,14 @@ __device__ __forceinline__ void proj_epilogue(const ProjParams &p, int r0, int c
         }
         TO *z = static_cast<TO *>(p.Z) + (size_t)row * (size_t)p.ldz + col;
         if constexpr (OUT == kGated) {
-          store4<TO, VEC>(static_cast<TO *>(p.Y) + (size_t)row * (size_t)p.ldy + col,
+          store4<TO>(static_cast<TO *>(p.Y) + (size_t)row * (size_t)p.ldy + col,
                           act_values(p.act, a) * b, count);
           if (p.Z != nullptr) {
-            store4<TO, VEC>(z, a, count);
-            store4<TO, VEC>(z + p.N, b, count);
+            store4<TO>(z, a, count);
+            store4<TO>(z + p.N, b, count);
           }
         } else {
-          const f32x4 d = load4<TO, VEC>(
+          const f32x4 d = load4<TO>(
               static_cast<const TO *>(p.dH) + (size_t)row * (size_t)p.lddh + col, count);
           f32x4 dg, du;
 #pragma unroll
@@ -132,17 +131,15 @@ __device__ __forceinline__ void proj_epilogue(const ProjParams &p, int r0, int c
             dg[e] = d[e] * b[e] * slope;
             du[e] = d[e] * value;
           }
-          store4<TO, VEC>(z, dg, count);
-          store4<TO, VEC>(z + p.N, du, count);
+          store4<TO>(z, dg, count);
+          store4<TO>(z + p.N, du, count);
         }
       }
     }
   }
 }
 
-// VEC: four neighbouring elements of every output (and of dH) are one aligned
-// access.
-template <class T, int OUT, typename TO, bool VEC>
+template <class T, int OUT, typename TO>
 __global__ __launch_bounds__(T::NT) void proj_tile(GemmParams p, ProjParams e) {
   typedef HLayout<T, false, true, OUT != kScaled> L;
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
@@ -158,7 +155,7 @@ __global__ __launch_bounds__(T::NT) void proj_tile(GemmParams p, ProjParams e) {
   mainloop_direct<T, L>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
   __builtin_amdgcn_s_waitcnt(kWaitAll);
   __syncthreads();   // every wave is done with the pipeline slots
-  proj_epilogue<T, OUT, TO, VEC>(e, m0 + wm0, n0 + L::column(wn0), lds, acc);
+  proj_epilogue<T, OUT, TO>(e, m0 + wm0, n0 + L::column(wn0), lds, acc);
 }
 
 template <class T, int OUT, typename TO>
@@ -178,13 +175,7 @@ hipError_t launch_tile(const ProjParams &e, hipStream_t stream) {
   p.splits = 1;
   const long long blocks = (long long)p.tiles_m * p.tiles_n;
   if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  constexpr int B = 4 * (int)sizeof(TO);
-  const bool two = e.Z == nullptr || (e.ldz % 4 == 0 && e.N % 4 == 0 && aligned_to(e.Z, B));
-  const bool vec = two && e.ldy % 4 == 0 && aligned_to(e.Y, B) && e.lddh % 4 == 0 &&
-                   aligned_to(e.dH, B);
-  const dim3 g((unsigned)blocks), b(T::NT);
-  if (vec) hipLaunchKernelGGL((proj_tile<T, OUT, TO, true>), g, b, 0, stream, p, e);
-  else hipLaunchKernelGGL((proj_tile<T, OUT, TO, false>), g, b, 0, stream, p, e);
+  hipLaunchKernelGGL((proj_tile<T, OUT, TO>), dim3((unsigned)blocks), dim3(T::NT), 0, stream, p, e);
   return hipGetLastError();
 }
 

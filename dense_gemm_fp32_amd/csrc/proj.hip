@@ -120,13 +120,15 @@ int bytes_of(const ProjCall &c) { return c.i8 ? 1 : (c.half ? 2 : 4); }
 // (gated 64 x 8192 x 4096: 8-bit 14.7, 20.7, halves 30.1, 36.7; 20 rows 14.1, 17.5
 // and 30.0, 33.0; but 64 x 4096 x 4096 8-bit, 64 tiles: 11.7, 9.4), of fp32 none.
 // Rows that
-// have to be copied for the tiles pay for it beyond 128 rows only: a copy reads
-// and writes W, which the streaming kernel reads once for every 64 rows.
+// have to be copied for the tiles pay a launch and their bytes: from them on three
+// workgroups per CU, and beyond 128 rows, the tiles are ahead (copy and tile first:
+// gated halves 512 x 1500 x 517 16.5, 11.7, 700 rows 17.4, 16.3, 1000 rows 18.1, 19.1;
+// 8-bit 200 x 3000 x 700 11.0, 9.2, 342 rows 10.8, 13.6; 129 x 8000 x 3001 27.6, 31.0).
 bool tiled(const ProjCall &c) {
   if ((long long)c.K * bytes_of(c) >= kTileRowBytes) return false;
   if (c.M <= 16 || (!c.aligned && c.M <= 128)) return false;
   if (c.M <= 64) return (c.i8 || c.half) && (c.gated ? c.N / 32 : c.N / 64) >= kCUs / 2;
-  return (long long)((c.N + 15) / 16) * ((c.M + 63) / 64) > kCUs;
+  return (long long)((c.N + 15) / 16) * ((c.M + 63) / 64) > (c.aligned ? 1 : 3) * kCUs;
 }
 
 struct ProjSpace {

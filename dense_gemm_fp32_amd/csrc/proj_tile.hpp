@@ -235,16 +235,18 @@ long long proj_tiles(const ProjParams &e) {
   return (long long)((e.M + T::BM - 1) / T::BM) * ((e.N + COLS - 1) / COLS);
 }
 
-// The tiles, for elements of EB bytes.  What a launch of n tiles costs, in
-// microseconds at 4096 bytes of k (half of that, and half of the difference between
-// the tiles, at 2048), measured at 65 to 2048 rows and 1024 to 16384 rows of W:
-//   256x256       55 a round of 256 tiles (one workgroup per CU)
-//   128x128       37 a round of 512 (two per CU); 22 where at most 256 are left,
-//                 which then take three LDS slots in place of two (25 with two)
-//   64x64         14.5 a round of 512, 12 where at most 256 are left (three slots;
-//                 16 to 35 against 15 to 30 us at 64 x (2 x 8192) x 4096)
-// The least decides.  (The 128x128 and 64x128 tiles of the plain fp16 product,
-// four and two waves in steps of 64 bytes of k, take 27 and 26 at up to 256 tiles.)
+// The tiles, for elements of EB bytes.  What a round of them costs, in microseconds:
+// a start and an end, and so much for every 128 bytes of k (measured at 65 to 2048
+// rows, 1024 to 16384 rows of W, 1024 and 4096 bytes of k):
+//   256x256       12.6 + 1.45 for 256 tiles (one workgroup per CU), where at most
+//                 three quarters are left 1.16
+//   128x128       4.8 + 0.93 for 512 (two per CU), 0.56 where at most half are left
+//   64x64         2.9 + 0.33 for 512, 0.26 where at most half are left
+// with 1 and 1.8 less to start for the two smaller ones if that is all there is; they
+// then take three LDS slots in place of two (64 x (2 x 8192) x 4096 halves 30 us, with
+// two 35).  The least decides.  (The 128x128 and 64x128 tiles of the plain fp16
+// product, four and two waves in steps of 64 bytes of k, take 27 and 26 us at 4096
+// bytes of k for up to 256 tiles, against 22 and 12.)
 template <int EB>
 struct ProjTiles {
   typedef H16Tile<256, 256, 128 / EB, 2, 4, 2, 4, 16, EB> Large;   // 8 waves, 128 KB LDS
@@ -264,9 +266,15 @@ struct ProjTiles<4> {
   typedef H16Tile<64, 64, 32, 2, 2, 2, 8, 16, 4> Small;            // 4 waves,  34 KB
 };
 
-inline double tile_cost(long long tiles, int round, double whole, double half) {
-  const long long left = tiles % round;
-  return (double)(tiles / round) * whole + (left == 0 ? 0.0 : (2 * left <= round ? half : whole));
+// n tiles in rounds of `round` at `start` + `step` each; what is left, up to `few`, at
+// `step_few` for a step, and `less` sooner if there is nothing before it.
+inline double tile_cost(long long n, int round, int few, double start, double step,
+                        double step_few, double less) {
+  const long long whole = n / round, left = n % round;
+  double c = (double)whole * (start + step);
+  if (left > few) c += start + step;
+  else if (left > 0) c += start + step_few - (whole == 0 ? less : 0.0);
+  return c;
 }
 
 template <int EB, int OUT, typename TO>
@@ -282,9 +290,10 @@ hipError_t launch_tiles(const ProjParams &e, hipStream_t stream) {
     const long long large = proj_tiles<typename P::Large, OUT>(e);
     const long long mid = proj_tiles<typename P::Mid, OUT>(e);
     const long long small = proj_tiles<typename P::Small, OUT>(e);
-    const double l = tile_cost(large, kCUs, 55.0, 55.0);
-    const double m = tile_cost(mid, 2 * kCUs, 37.0, 22.0);
-    const double s = tile_cost(small, 2 * kCUs, 14.5, 12.0);
+    const double k = (double)(((long long)e.K * EB + 127) / 128);
+    const double l = tile_cost(large, kCUs, kCUs * 3 / 4, 12.6, 1.45 * k, 1.16 * k, 0.0);
+    const double m = tile_cost(mid, 2 * kCUs, kCUs, 4.8, 0.93 * k, 0.56 * k, 1.0);
+    const double s = tile_cost(small, 2 * kCUs, kCUs, 2.9, 0.33 * k, 0.26 * k, 1.8);
     if (l <= m && l <= s) return launch_tile<typename P::Large, OUT, TO>(e, stream);
     if (m <= s)
       return mid <= kCUs ? launch_tile<typename P::Mid3, OUT, TO>(e, stream)

@@ -205,7 +205,8 @@ struct GradSpace {
   void *D;         // [dG dU]: M rows of ldd elements
   int ldd;
   void *X, *W;     // copies with rows that start at 16 bytes
-  float *sx, *sw;  // parts of the products along k
+  ProductJob x, d;    // the products of one launch, as planned, with their parts' sums
+  ProductPlan plan;
   char *ws;        // the forward pass's and the library's products', one after the other
   size_t ws_bytes;
 };
@@ -220,14 +221,16 @@ size_t carve(const GluGradCall &c, void *base, GradSpace *s) {
   // (one launch's operands are copied ahead of the forward pass)
   if (c.Z == nullptr && !one) s->ws_bytes = proj_workspace(forward_of(c, nullptr, s->ldd));
   if (one) {
-    ProductJob x = job_x(c), d = job_w(c);
-    plan_products(c.half, x, d);
+    ProductJob &x = s->x, &d = s->d;
+    x = job_x(c);
+    d = job_w(c);
+    s->plan = plan_products(c.half, x, d);
     if (!c.aligned) {
       s->X = w.take<char>((size_t)c.M * (size_t)vec_ld(c, c.K) * eb);
       s->W = w.take<char>((size_t)c.F * 2 * (size_t)vec_ld(c, c.K) * eb);
     }
-    if (x.splits > 1) s->sx = w.take<float>((size_t)x.splits * x.M * (size_t)((x.N + 3) / 4 * 4));
-    if (d.splits > 1) s->sw = w.take<float>((size_t)d.splits * d.M * (size_t)((d.N + 3) / 4 * 4));
+    if (x.splits > 1) x.slab = w.take<float>((size_t)x.splits * x.M * (size_t)((x.N + 3) / 4 * 4));
+    if (d.splits > 1) d.slab = w.take<float>((size_t)d.splits * d.M * (size_t)((d.N + 3) / 4 * 4));
   } else {
     const size_t x = product_bytes(c, product_x(c, nullptr, s->ldd));
     const size_t d = product_bytes(c, product_w(c, nullptr, s->ldd));
@@ -255,18 +258,15 @@ hipError_t sum_parts(const ProductJob &j, bool half_out, hipStream_t stream) {
 }
 
 hipError_t products_together(const GluGradCall &c, const GradSpace &s) {
-  ProductJob x = job_x(c), d = job_w(c);
-  const ProductPlan plan = plan_products(c.half, x, d);
+  ProductJob x = s.x, d = s.d;
   x.A = d.A = s.D;
   x.B = c.W;
   x.ldb = c.ldw;
   x.C = c.dX;
-  x.slab = s.sx;
   d.B = c.X;
   d.ldb = c.ldx;
   d.C = c.dW;
-  d.slab = s.sw;
-  hipError_t e = launch_products(c.half, c.dw32, plan.mid, x, d, c.stream);
+  hipError_t e = launch_products(c.half, c.dw32, s.plan.mid, x, d, c.stream);
   if (e == hipSuccess && x.C != nullptr && x.splits > 1) e = sum_parts(x, c.half, c.stream);
   if (e == hipSuccess && d.C != nullptr && d.splits > 1)
     e = sum_parts(d, c.half && !c.dw32, c.stream);

@@ -60,8 +60,9 @@ hipError_t skinny_high(const ProjParams &p, hipStream_t stream) {
   constexpr int NF = OUT == kScaled ? 1 : 2;
   constexpr int U = NB == 1 ? 2 : 1;
   const long long wgs = (long long)((p.N + 15) / 16) * ((p.M + 16 * NB - 1) / (16 * NB));
-  if (NB > 1 && 16 * NB >= p.M && wgs >= 2 * kCUs)
-    return skinny<T, TO, OUT, 2 * NF, NB, 1, 4, U>(p, stream);
+  if constexpr (NB > 1)
+    if (16 * NB >= p.M && wgs >= 2 * kCUs)
+      return skinny<T, TO, OUT, 2 * NF, NB, 1, 4, U>(p, stream);
   if (wgs >= kCUs) return skinny<T, TO, OUT, NF, NB, 1, 4, U>(p, stream);
   return skinny<T, TO, OUT, NF, NB, 1, 8, U>(p, stream);
 }

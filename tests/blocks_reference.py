@@ -24,15 +24,15 @@ def quantize(X):
     return q.clamp(-127, 127).to(torch.int8), scale
 
 
-def _ones(n, t):
-    return torch.ones(n, dtype=torch.float64) if t is None else t.double()
+def _ones(n, t, like):
+    return torch.ones(n, dtype=torch.float64, device=like.device) if t is None else t.double()
 
 
 def i8_sums(X, W, xs, ws):
     """(value, bound) of the scaled sums: the sum's rounding to fp32 and the two
     products with the scales."""
     S = X.double() @ W.double().t()
-    S = S * _ones(X.shape[0], xs)[:, None] * _ones(W.shape[0], ws)[None, :]
+    S = S * _ones(X.shape[0], xs, X)[:, None] * _ones(W.shape[0], ws, X)[None, :]
     return S, 3.01 * U32 * S.abs()
 
 
@@ -98,7 +98,7 @@ def glu_grad(dH, X, W, Z, name, dX, dW, beta_x, beta_w, dw_dt):
     if Z is None:
         Z, e = X @ W.t(), 4 * (K + 4) * U32 * (X.abs() @ W.abs().t())
     else:
-        Z, e = Z.double(), torch.zeros(M, 2 * F, dtype=torch.float64)
+        Z, e = Z.double(), torch.zeros_like(Z, dtype=torch.float64)
     g, u, eg, eu = Z[:, :F], Z[:, F:], e[:, :F], e[:, F:]
     a, d, ea, ed = act(name, g)
     ea = ea + 1.2 * eg

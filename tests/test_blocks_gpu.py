@@ -50,6 +50,11 @@ def pads_intact(big, cols):
     return bool((torch.isnan(tail) if tail.is_floating_point() else tail == 99).all())
 
 
+def near(work, *tensors):
+    """The tensors where their reference is computed: large ones on the GPU."""
+    return [t if t is None or work < 1e9 else t.to(GPU) for t in tensors]
+
+
 def unset(rows, cols, dtype, pad):
     """An output that holds nothing yet."""
     return padded(torch.full((rows, cols), 77 if dtype == torch.int8 else float("nan"),
@@ -152,6 +157,15 @@ I8 = [
     (2100, 4160, 144, 0, 1.0, 1.0, True),
     (4096, 512, 192, 32, 1.0, 0.0, False),
     (40, 4000, 131071, 0, 1.0, 0.0, True),
+    (1100, 8200, 2000, 0, 1.0, 0.5, True),
+    (200, 6000, 1040, 0, 1.0, -1.0, True),
+    (300, 6000, 1031, 1, 1.0, 0.0, True),
+    (16, 9000, 300, 4, 1.0, 0.0, True),
+    (64, 8200, 512, 0, 1.0, 1.0, True),
+    (90, 700, 6643, 8, 1.0, 0.0, True),
+    (30, 8300, 390, 1, 1.0, 0.0, True),
+    (40, 9000, 300, 1, 1.0, 1.0, True),
+    (64, 8200, 270, 1, 1.0, 0.0, True),
 ]
 
 
@@ -168,7 +182,7 @@ def test_gemm_i8(dt, case):
     if not scaled and dt == "f16":
         alpha *= 2.0 ** -12      # sums of whole numbers pass fp16's largest
     Y = normal(g, (M, N), t) if beta else torch.full((M, N), float("nan"), dtype=t)
-    want, bound = ref.gemm_i8(X, W, Y, xs, ws, alpha, beta, t)
+    want, bound = (v.cpu() for v in ref.gemm_i8(*near(M * N * K, X, W, Y, xs, ws), alpha, beta, t))
     x, w = padded(X, pad)[1], padded(W, pad)[1]
     big, y = padded(Y, pad)
     up = lambda v: None if v is None else v.to(GPU)  # noqa: E731
@@ -263,6 +277,16 @@ GLU = [
     (1030, 2050, 72, 0, "silu", True),
     (2100, 2112, 96, 0, "gelu_tanh", False),
     (2048, 4096, 64, 0, "silu", True),
+    (1100, 4100, 1000, 0, "gelu_tanh", True),
+    (64, 4200, 528, 0, "relu", True),
+    (150, 1800, 1030, 2, "silu", False),
+    (17, 8000, 96, 8, "gelu", True),
+    (700, 1100, 1040, 0, "silu", True),
+    (30, 4300, 390, 1, "silu", False),
+    (40, 8300, 200, 1, "gelu", True),
+    (64, 8200, 270, 1, "relu", False),
+    (1500, 1024, 1104, 0, "silu", True),
+    (1100, 4100, 2600, 0, "silu", False),
 ]
 
 
@@ -274,7 +298,7 @@ def test_glu(dt, case):
     note("glu %s %r" % (dt, case))
     g, t = gen(M * 31 + F), DT[dt]
     X, W = normal(g, (M, K), t), normal(g, (2 * F, K), t, 1.5 / math.sqrt(K))
-    want = ref.glu(X, W, name, t)
+    want = {k: [v.cpu() for v in e] for k, e in ref.glu(*near(M * F * K, X, W), name, t).items()}
     x, w = padded(X, pad)[1], padded(W, pad)[1]
     bigh, h = unset(M, F, t, pad)
     bigz, z = unset(M, 2 * F, t, pad)
@@ -301,7 +325,8 @@ def test_glu_i8(dt, case):
     if not scaled:          # sums of a few units: scales of 1 would leave fp16's range
         X, W = (torch.randint(-1, 2, m.shape, generator=g).to(torch.int8) for m in (X, W))
         xs = ws = None
-    want = ref.glu(X, W, name, t, xs, ws)
+    X_, W_, xs_, ws_ = near(M * F * K, X, W, xs, ws)
+    want = {k: [v.cpu() for v in e] for k, e in ref.glu(X_, W_, name, t, xs_, ws_).items()}
     x, w = padded(X, pad)[1], padded(W, pad)[1]
     bigh, h = unset(M, F, t, pad)
     dg.glu(x, w, h, act=name, x_scale=up(xs), w_scale=up(ws))
@@ -382,6 +407,15 @@ GRAD = [
     (512, 640, 256, 0, "relu", False, 0.0, 0.0, True),
     (1000, 375, 259, 1, "gelu", True, 0.0, 0.0, False),
     (1030, 1024, 136, 0, "silu", False, 0.0, 0.0, False),
+    (19, 700, 2100, 0, "gelu_tanh", True, 0.0, 1.0, False),
+    (40, 2100, 1000, 4, "silu", False, 1.0, 0.0, True),
+    (900, 1000, 520, 0, "silu", True, 0.5, 0.0, False),
+    (2000, 100, 1500, 2, "gelu", True, 0.0, 0.0, True),
+    (130, 1500, 1001, 1, "silu", False, 0.0, -1.0, False),
+    (1024, 1536, 1024, 0, "silu", True, 0.0, 1.0, True),
+    (1100, 1500, 1024, 0, "gelu", False, 1.0, 0.0, False),
+    (257, 2048, 520, 0, "relu", False, 0.0, 0.0, False),
+    (2048, 1024, 2048, 0, "silu", True, 0.0, 0.0, False),
 ]
 
 
@@ -402,7 +436,9 @@ def test_glu_grad(dt, case):
     M, F, K, pad, name, kept, beta_x, beta_w, dw32 = case
     note("glu_grad %s %r" % (dt, case))
     X, W, dH, Z, oldx, oldw, tw = grad_inputs(case, dt)
-    want = ref.glu_grad(dH, X, W, Z, name, oldx, oldw, beta_x, beta_w, tw)
+    old = near(M * F * K, oldx, oldw)
+    want = ref.glu_grad(*near(M * F * K, dH, X, W, Z), name, *old, beta_x, beta_w, tw)
+    want = {k: [v.cpu() for v in e] for k, e in want.items()}
     x, w, d = (padded(v, pad)[1] for v in (X, W, dH))
     z = padded(Z, pad)[1] if kept else None
     bigx, dx = padded(oldx, pad) if beta_x else unset(M, K, DT[dt], pad)
@@ -419,6 +455,25 @@ def test_glu_grad(dt, case):
     one = torch.full_like(dw, 1.0).copy_(oldw.to(GPU))
     dg.glu_grad(d, x, w, dW=one, act=name, Z=z, beta_w=beta_w)
     assert torch.equal(one, dw)
+
+
+@pytest.mark.parametrize("dt,M,F,K", [("f32", 1536, 1664, 2048), ("f16", 2048, 2304, 2176),
+                                      ("f16", 2050, 2304, 2183), ("f32", 1536, 1664, 2051)])
+def test_glu_grad_large(dt, M, F, K):
+    """Sizes at which the products run one after the other, and beside them those
+    whose rows do not start at 16 bytes; the reference in 64 bits on the GPU."""
+    import dense_gemm_fp32_amd as dg
+    note("glu_grad large %s %d %d %d" % (dt, M, F, K))
+    g, t = torch.Generator(device=GPU), DT[dt]
+    g.manual_seed(M)
+    draw = lambda s, q: (torch.randn(*s, generator=g, device=GPU) * q).to(t)  # noqa: E731
+    X, W, dH = draw((M, K), 1.0), draw((2 * F, K), K ** -0.5), draw((M, F), 0.05)
+    oldx, oldw = draw((M, K), 0.1), draw((2 * F, K), 0.1)
+    want = ref.glu_grad(dH, X, W, None, "silu", oldx, oldw, 1.0, 1.0, t)
+    dX, dW = oldx.clone(), oldw.clone()
+    dg.glu_grad(dH, X, W, dX=dX, dW=dW, beta_x=1.0, beta_w=1.0)
+    for got, (value, bound) in ((dX, want["dX"]), (dW, want["dW"])):
+        assert worst(got, value.cpu(), bound.cpu()) <= 1.0
 
 
 @pytest.mark.parametrize("name", ref.ACTS)
@@ -712,6 +767,46 @@ def test_rows_beyond_32_bits():
     dg.glu_grad(dH, Xh.to(GPU), Wh.to(GPU), dX=torch.empty_like(near), act="gelu", Z=z2)
     dg.glu_grad(dH, Xh.to(GPU), Wh.to(GPU), dX=apart, act="gelu", Z=z)
     assert torch.equal(apart, near)
+
+
+@pytest.mark.parametrize("N", [6016, 6600])
+def test_many_rows_far_apart(N):
+    """200 rows, 2^24 bytes from one to the next: operands are copied for the tiles
+    (the more columns) or streamed, outputs are written where they lie.  Another way
+    sums in another order, so halves are held to the reference."""
+    import dense_gemm_fp32_amd as dg
+    g = gen(2)
+    M, K, far, t = 200, 144, (1 << 24) + 16, torch.float16
+    X, W = whole(g, (M, K)), whole(g, (N, K))
+    big = torch.zeros(M * far, dtype=torch.int8, device=GPU)
+    x = big.as_strided((M, K), (far, 1))
+    x.copy_(X)
+    near, w = torch.empty(M, N, device=GPU), W.to(GPU)
+    dg.gemm_i8(X.to(GPU), w, near)
+    assert torch.equal(near.cpu().double(), X.double() @ W.double().t())
+    out = torch.empty(M, N, device=GPU)
+    dg.gemm_i8(x, w, out)
+    assert torch.equal(out, near)
+    wide = big.view(torch.float32).as_strided((M, N), (far // 4, 1))
+    dg.gemm_i8(X.to(GPU), w, wide)
+    assert torch.equal(wide, near)
+    F = N // 2
+    X, W, dH = normal(g, (M, K), t), normal(g, (N, K), t, 0.1), normal(g, (M, F), t, 0.05)
+    xh, wh, d = X.to(GPU), W.to(GPU), dH.to(GPU)
+    half = big.view(t)
+    xf, zf = half.as_strided((M, K), (far // 2, 1)), half[K:].as_strided((M, N), (far // 2, 1))
+    want = ref.glu(X, W, "silu", t)
+    h, z = torch.empty(M, F, dtype=t, device=GPU), torch.empty(M, N, dtype=t, device=GPU)
+    dg.glu(xh, wh, h, Z=zf)
+    assert worst(h, *want["H"]) <= 1.0 and worst(zf, *want["Z"]) <= 1.0
+    xf.copy_(xh)
+    dg.glu(xf, wh, h, Z=z)
+    assert worst(h, *want["H"]) <= 1.0 and worst(z, *want["Z"]) <= 1.0
+    want = ref.glu_grad(dH, X, W, z.cpu(), "silu", None, None, 0, 0, t)
+    a = [torch.empty(M, K, dtype=t, device=GPU), torch.empty(N, K, dtype=t, device=GPU)]
+    for rows, kept in ((xh, z), (xf, z), (xh, zf.copy_(z))):
+        dg.glu_grad(d, rows, wh, *a, Z=kept)
+        assert worst(a[0], *want["dX"]) <= 1.0 and worst(a[1], *want["dW"]) <= 1.0
 
 
 def test_wrappers_refuse_on_the_gpu():

@@ -63,8 +63,12 @@ hipError_t skinny_high(const ProjParams &p, hipStream_t stream) {
   if constexpr (NB > 1)
     if (16 * NB >= p.M && wgs >= 2 * kCUs)
       return skinny<T, TO, OUT, 2 * NF, NB, 1, 4, U>(p, stream);
-  if (wgs >= kCUs) return skinny<T, TO, OUT, NF, NB, 1, 4, U>(p, stream);
-  return skinny<T, TO, OUT, NF, NB, 1, 8, U>(p, stream);
+  // (fewer workgroups than CUs and four blocks of X: two make twice the workgroups at
+  // most, which skinny_blocks prices lower; so does it one block before two, where
+  // W's is one)
+  if constexpr (NB < 4 && !(NB == 2 && NF == 1))
+    if (wgs < kCUs) return skinny<T, TO, OUT, NF, NB, 1, 8, U>(p, stream);
+  return skinny<T, TO, OUT, NF, NB, 1, 4, U>(p, stream);
 }
 
 int skinny_blocks(const ProjParams &p, int nf) {

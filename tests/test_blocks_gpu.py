@@ -65,7 +65,7 @@ def unset(rows, cols, dtype, pad):
 
 QUANT = [(1, 1, 0), (1, 4096, 0), (3, 7, 1), (5, 8, 0), (2, 15, 0), (17, 16, 3), (4, 17, 0),
          (33, 255, 1), (64, 2048, 0), (9, 2049, 0), (130, 517, 8), (3, 20000, 0), (1, 131071, 1),
-         (2000, 64, 0), (300, 8192, 0)]
+         (2000, 64, 0), (300, 8192, 0), (3, 12345, 1), (40, 16384, 0)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
@@ -167,6 +167,12 @@ I8 = [
     (40, 9000, 300, 1, 1.0, 1.0, True),
     (64, 8200, 270, 1, 1.0, 0.0, True),
 ]
+
+
+# few rows: each height and width of a workgroup, in rows that start anywhere
+FEW = [(33, 2070), (17, 4096), (17, 2070), (33, 4096), (33, 2749), (65, 2070), (17, 8181),
+       (33, 8181), (49, 8181)]
+I8 += [(M, N, 71, 1, 1.0, 0.0, True) for M, N in FEW]
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
@@ -288,6 +294,9 @@ GLU = [
     (1500, 1024, 1104, 0, "silu", True),
     (1100, 4100, 2600, 0, "silu", False),
 ]
+
+
+GLU += [(M, F, 71, 1, "silu", True) for M, F in FEW]
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
@@ -427,6 +436,12 @@ def grad_inputs(case, dt):
     Z = (X.double() @ W.double().t()).to(t) if kept else None
     tw = torch.float32 if dw32 else t
     return X, W, dH, Z, normal(g, (M, K), t), normal(g, (2 * F, K), tw), tw
+
+
+GRAD += [(M, F, 71, 1, "silu", False, 0.0, 0.0, False) for M, F in FEW]
+GRAD += [(2048, 1024, 2048, 0, "silu", True, 0.0, 0.0, True),
+         (2048, 2048, 200, 0, "gelu_tanh", False, 0.0, 0.0, False),
+         (1200, 2048, 264, 0, "silu", False, 0.0, 0.0, False)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])

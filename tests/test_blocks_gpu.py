@@ -297,6 +297,7 @@ GLU = [
 
 
 GLU += [(M, F, 71, 1, "silu", True) for M, F in FEW]
+GLU += [(33, 4082, 70, 1, "silu", True), (17, 8216, 70, 1, "gelu", True)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
@@ -441,7 +442,10 @@ def grad_inputs(case, dt):
 GRAD += [(M, F, 71, 1, "silu", False, 0.0, 0.0, False) for M, F in FEW]
 GRAD += [(2048, 1024, 2048, 0, "silu", True, 0.0, 0.0, True),
          (2048, 2048, 200, 0, "gelu_tanh", False, 0.0, 0.0, False),
-         (1200, 2048, 264, 0, "silu", False, 0.0, 0.0, False)]
+         (1200, 2048, 264, 0, "silu", False, 0.0, 0.0, False),
+         (17, 4082, 72, 0, "silu", False, 0.0, 0.0, False),
+         (33, 4082, 72, 0, "gelu", False, 0.0, 0.0, False),
+         (49, 4082, 72, 0, "silu", False, 1.0, 0.0, False)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
@@ -489,6 +493,24 @@ def test_glu_grad_large(dt, M, F, K):
     dg.glu_grad(dH, X, W, dX=dX, dW=dW, beta_x=1.0, beta_w=1.0)
     for got, (value, bound) in ((dX, want["dX"]), (dW, want["dW"])):
         assert worst(got, value.cpu(), bound.cpu()) <= 1.0
+
+
+@pytest.mark.parametrize("M", [17, 33, 49])
+def test_glu_grad_widest(M):
+    """A width at which the rows of [dG dU] pass 8 MiB, in rows of X and W that
+    start anywhere."""
+    import dense_gemm_fp32_amd as dg
+    F, K, t = (1 << 21) + 5, 17, torch.float16
+    note("glu_grad widest %d" % M)
+    g = torch.Generator(device=GPU)
+    g.manual_seed(M)
+    draw = lambda s, q: (torch.randn(*s, generator=g, device=GPU) * q).to(t)  # noqa: E731
+    X, W, dH = draw((M, K), 1.0), draw((2 * F, K), K ** -0.5), draw((M, F), 0.05)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    dg.glu_grad(dH, X, W, dX=dX, dW=dW, act="silu")
+    want = ref.glu_grad(dH, X, W, None, "silu", None, None, 0.0, 0.0, t)
+    assert worst(dX, *(v.cpu() for v in want["dX"])) <= 1.0
+    assert worst(dW, *(v.cpu() for v in want["dW"])) <= 1.0
 
 
 @pytest.mark.parametrize("name", ref.ACTS)

@@ -610,11 +610,12 @@ def _act(act):
     return code
 
 
-def _at_16(X, ldx, W, ldw, eb):
-    """Whether every row of X and of W starts at a multiple of 16 bytes, less than
-    2^23 from the one before."""
+def _in_place(X, ldx, W, ldw, eb):
+    """Whether every row of X and of W starts at a multiple of 16 bytes (floats:
+    anywhere), less than 2^23 from the one before."""
     ldx, ldw = ldx * eb, ldw * eb
-    return ((X.data_ptr() | W.data_ptr() | ldx | ldw) & 15) == 0 and (ldx | ldw) < 1 << 23
+    return (eb == 4 or ((X.data_ptr() | W.data_ptr() | ldx | ldw) & 15) == 0) and \
+        (ldx | ldw) < 1 << 23
 
 
 def quantize(X, Q=None, scale=None, stream=None):
@@ -654,7 +655,7 @@ def gemm_i8(X, W, Y, x_scale=None, w_scale=None, alpha=1.0, beta=0.0, workspace=
     ldx, ldw = _rows("X", X, M, K, torch.int8, dev), _rows("W", W, N, K, torch.int8, dev)
     ldy = _rows("Y", Y, M, N, Y.dtype, dev)
     _call_rows(_I8_FN[kind], dev, stream, workspace,
-               _i8_bytes(M, N, K, _at_16(X, ldx, W, ldw, 1)),
+               _i8_bytes(M, N, K, _in_place(X, ldx, W, ldw, 1)),
                (M, N, K, alpha, X.data_ptr(), ldx, _vector("x_scale", x_scale, M, torch.float32, dev),
                 W.data_ptr(), ldw, _vector("w_scale", w_scale, N, torch.float32, dev), beta,
                 Y.data_ptr(), ldy))
@@ -685,7 +686,7 @@ def glu(X, W, H, act="silu", Z=None, x_scale=None, w_scale=None, workspace=None,
         if Z is not None:
             raise ValueError("Z goes with float16 or float32 X and W only")
         _call_rows(_GLU_FN["i8_" + kind], dev, stream, workspace,
-                   _glu_bytes(2, M, F, K, _at_16(X, ldx, W, ldw, 1)),
+                   _glu_bytes(2, M, F, K, _in_place(X, ldx, W, ldw, 1)),
                    (M, F, K, code_act, X.data_ptr(), ldx,
                     _vector("x_scale", x_scale, M, torch.float32, dev), W.data_ptr(), ldw,
                     _vector("w_scale", w_scale, 2 * F, torch.float32, dev), H.data_ptr(), ldh))
@@ -696,7 +697,7 @@ def glu(X, W, H, act="silu", Z=None, x_scale=None, w_scale=None, workspace=None,
     if Z is not None:
         z, ldz = Z.data_ptr(), _rows("Z", Z, M, 2 * F, dt, dev)
     _call_rows(_GLU_FN[kind], dev, stream, workspace,
-               _glu_bytes(code, M, F, K, _at_16(X, ldx, W, ldw, 2 if code else 4)),
+               _glu_bytes(code, M, F, K, _in_place(X, ldx, W, ldw, 2 if code else 4)),
                (M, F, K, code_act, X.data_ptr(), ldx, W.data_ptr(), ldw, H.data_ptr(), ldh, z, ldz))
     return H
 
@@ -734,7 +735,7 @@ def glu_grad(dH, X, W, dX=None, dW=None, act="silu", Z=None, beta_x=0.0, beta_w=
             kind = "f16f32"
         lddw = _rows("dW", dW, 2 * F, K, torch.float32 if kind == "f16f32" else dt, dev)
     _call_rows(_GLU_GRAD_FN[kind], dev, stream, workspace,
-               _glu_grad_bytes(code, M, F, K, _at_16(X, ldx, W, ldw, 2 if code else 4)),
+               _glu_grad_bytes(code, M, F, K, _in_place(X, ldx, W, ldw, 2 if code else 4)),
                (M, F, K, code_act, dH.data_ptr(), lddh, X.data_ptr(), ldx, W.data_ptr(), ldw, z,
                 ldz, beta_x, _addr(dX), lddx, beta_w, _addr(dW), lddw))
     return dX, dW

@@ -257,6 +257,11 @@ __device__ __forceinline__ uint32_t direct_offset(int idx, int kk, int idx0, int
   if constexpr (R::K_MAJOR) {
     g = g < ext ? g : ext - 1;
     return (uint32_t)R::EB * (uint32_t)((g - idx0) * ld + kk);
+  } else if constexpr (R::EB == 4) {
+    // floats: to the chunk that holds the last one; what it holds behind that only
+    // feeds columns that are not stored
+    g = g < ext ? g : (ext - 1) / 4 * 4;
+    return 4u * (uint32_t)(kk * ld + (g - idx0));
   } else {
     g = g + 16 / R::EB <= ext ? g : ext - 16 / R::EB;
     return (uint32_t)R::EB * (uint32_t)(kk * ld + (g - idx0));
@@ -389,16 +394,26 @@ template <class R>
 __device__ __forceinline__ u32x4 staged_chunk(const void *X, int ld, int idx0, int ext, int k0,
                                               int K, int idx, int kk, int w) {
   const int g = idx0 + idx, gk = k0 + kk;
-  if constexpr (R::EB == 4 && !R::K_MAJOR) {
-    // whole 16 bytes of a row up to `ext`, which the launch has rounded up to them
-    const char *src = static_cast<const char *>(X) + 4 * ((size_t)gk * (size_t)ld + g);
+  if constexpr (R::EB == 4) {
+    // floats, at any address of theirs
+    typedef uint32_t Any __attribute__((ext_vector_type(4), aligned(4)));
+    const uint32_t *src =
+        static_cast<const uint32_t *>(X) +
+        (R::K_MAJOR ? (size_t)g * (size_t)ld + gk : (size_t)gk * (size_t)ld + g);
+    const int left = g < ext && gk < K ? (R::K_MAJOR ? K - gk : ext - g) : 0;
     u32x4 v = u32x4{0u, 0u, 0u, 0u};
-    if (g < ext && gk < K) v = *reinterpret_cast<const u32x4 *>(src);
+    if (left >= 4) {
+      v = *reinterpret_cast<const Any *>(src);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < left) v[e] = src[e];
+    }
     return v;
-  } else if constexpr (R::EB != 2) {
-    // 8-bit integers and floats: rows that start at 16 bytes only, so the 16
-    // bytes that hold a row's last elements are one aligned granule, in the same
-    // page as them; what it holds behind the row is cleared.
+  } else if constexpr (R::EB == 1) {
+    // 8-bit integers: rows that start at 16 bytes only, so the 16 bytes that hold
+    // a row's last elements are one aligned granule, in the same page as them;
+    // what it holds behind the row is cleared.
     const char *src = static_cast<const char *>(X) + R::EB * ((size_t)g * (size_t)ld + gk);
     u32x4 v = u32x4{0u, 0u, 0u, 0u};
     if (g < ext && gk < K) v = *reinterpret_cast<const u32x4 *>(src);
@@ -1304,11 +1319,17 @@ __device__ __forceinline__ void kstep(const char *slot, const char *next_slot,
 }
 
 // Direct-load pipeline over STAGES slots: slot j % STAGES holds step j.
+// masked_last: the last step goes through registers where it is a whole one too.
 template <class T, class L>
 __device__ __forceinline__ void mainloop_direct(const GemmParams &p, int m0, int n0, char *lds,
                                                 uint32_t lds_u32, int wm0, int wn0,
-                                                typename T::Acc (&acc)[T::FM][T::FN]) {
-  const KSteps ks = make_steps(p.K, T::BK);
+                                                typename T::Acc (&acc)[T::FM][T::FN],
+                                                bool masked_last = false) {
+  KSteps ks = make_steps(p.K, T::BK);
+  if (masked_last && ks.tail == 0) {
+    ks.tail = T::BK;
+    --ks.nfull;
+  }
   DirectAddr<T> da;
   direct_setup<T, L>(p, m0, n0, da);
   FragAddr<T, L> fa;

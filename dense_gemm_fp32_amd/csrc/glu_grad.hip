@@ -124,7 +124,7 @@ Call product_w(const GluGradCall &c, const void *D, int ldd) {
 size_t product_bytes(const GluGradCall &c, Call g) {
   void *p = reinterpret_cast<void *>((uintptr_t)256);
   size_t most = 0;
-  for (int odd = 0; odd < (c.aligned ? 1 : 2); ++odd) {
+  for (int odd = 0; odd < (c.at_16 ? 1 : 2); ++odd) {
     g.A = g.B = g.C = p;
     g.ldb = odd ? c.K | 1 : (c.K + 7) / 8 * 8;
     g.ldc = g.ldb;
@@ -198,7 +198,8 @@ bool together(const GluGradCall &c) {
   const long long eb = c.half ? 2 : 4;
   // a tile's offsets have to fit 32 bits
   if (2LL * c.F * eb >= kTileRowBytes || c.K * eb >= kTileRowBytes) return false;
-  return !c.aligned || (double)c.M * c.F * c.K < (c.half ? kTogetherF16 : kTogetherF32);
+  if (!c.half && c.K < 4) return false;        // glu_products.hip: rows of floats
+  return !c.at_16 || (double)c.M * c.F * c.K < (c.half ? kTogetherF16 : kTogetherF32);
 }
 
 struct GradSpace {
@@ -262,9 +263,11 @@ hipError_t products_together(const GluGradCall &c, const GradSpace &s) {
   x.A = d.A = s.D;
   x.B = c.W;
   x.ldb = c.ldw;
+  x.odd = !c.half && c.dX != nullptr && !rows_at_16(c.W, c.ldw, 4);
   x.C = c.dX;
   d.B = c.X;
   d.ldb = c.ldx;
+  d.odd = !c.half && c.dW != nullptr && !rows_at_16(c.X, c.ldx, 4);
   d.C = c.dW;
   hipError_t e = launch_products(c.half, c.dw32, s.plan.mid, x, d, c.stream);
   if (e == hipSuccess && x.C != nullptr && x.splits > 1) e = sum_parts(x, c.half, c.stream);
@@ -273,11 +276,11 @@ hipError_t products_together(const GluGradCall &c, const GradSpace &s) {
   return e;
 }
 
-// Copies of X and W, where their rows need it, in place of them.
+// Copies of X and W, where the tiles need them, in place of them.
 hipError_t copy_operands(GluGradCall &c, const GradSpace &s) {
   const long long eb = c.half ? 2 : 4, row = c.K * eb;
-  const bool copy_w = (c.dX != nullptr || c.Z == nullptr) && !rows_at_16(c.W, c.ldw, (int)eb);
-  const bool copy_x = (c.dW != nullptr || c.Z == nullptr) && !rows_at_16(c.X, c.ldx, (int)eb);
+  const bool copy_w = (c.dX != nullptr || c.Z == nullptr) && !rows_for_tiles(c.W, c.ldw, (int)eb);
+  const bool copy_x = (c.dW != nullptr || c.Z == nullptr) && !rows_for_tiles(c.X, c.ldx, (int)eb);
   const RowCopy w = {c.W, c.ldw * eb, row, 2 * c.F, copy_w ? s.W : nullptr};
   const RowCopy x = {c.X, c.ldx * eb, row, c.M, copy_x ? s.X : nullptr};
   if (copy_w) {

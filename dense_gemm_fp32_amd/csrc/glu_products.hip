@@ -5,8 +5,13 @@
 // that the other leaves idle.  The operands are read as they lie: k runs along
 // the rows of [dG dU] in the first product, along its columns in the second, and
 // along W's and X's columns in both; such an operand keeps its orientation in LDS
-// (HRegion) and its fragments are read across.  Rows start at 16 bytes; what the
-// last 16 of a row hold behind it only feeds columns that are not stored.
+// (HRegion) and its fragments are read across.  What a row's last 16 bytes hold
+// behind it only feeds columns that are not stored.  fp16 rows start at 16 bytes
+// (others are copied).  Rows of floats start anywhere: a direct load asks for no
+// more than 4, and the last row of all, whose last 16 bytes may pass the end of the
+// matrix, goes through registers with a mask (in rows of four or more; with fewer
+// the rows before it would pass the end too).  With copies of them 1000 x 1500 x 517
+// takes 81 us, so 77; 257 x 1024 x 1027 44 and 37.
 #include "proj_tile.hpp"
 
 namespace dgemm {
@@ -55,13 +60,15 @@ __global__ __launch_bounds__(T::NT) void proj_products(ProductJob a, ProductJob 
   typename T::Acc acc[T::FM][T::FN];
   zero_acc<T>(acc);
   // what the loads may read: whole 16 bytes
-  constexpr int V = 16 / T::EB;
-  p.M = second ? (p.M + V - 1) / V * V : p.M;
-  p.N = (p.N + V - 1) / V * V;
+  if constexpr (T::EB == 2) {
+    p.M = second ? (p.M + 7) / 8 * 8 : p.M;
+    p.N = (p.N + 7) / 8 * 8;
+  }
+  const bool masked = T::EB == 4 && (second ? b.odd : a.odd) && split == splits - 1;
   if (second)
-    mainloop_direct<T, LB>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
+    mainloop_direct<T, LB>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc, masked);
   else
-    mainloop_direct<T, LA>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc);
+    mainloop_direct<T, LA>(p, m0, n0, lds, lds_address(lds), wm0, wn0, acc, masked);
   __builtin_amdgcn_s_waitcnt(kWaitAll);
   __syncthreads();   // every wave is done with the pipeline slots
   if (splits > 1) {

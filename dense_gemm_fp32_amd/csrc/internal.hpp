@@ -332,7 +332,7 @@ struct ProjCall {
   bool i8;                 // X and W hold 8-bit integers, else Y's type
   bool half;               // Y (Z, dH) holds fp16, else fp32
   bool gated;
-  bool aligned;            // workspace sizes: every row of X and W starts at 16 bytes
+  bool aligned;            // X and W are rows_for_tiles
   int M, N, K;
   int act;
   float alpha, beta;       // of a product
@@ -352,9 +352,16 @@ struct ProjCall {
 };
 // Whether every row of a matrix with elements of eb bytes starts at 16 bytes, and
 // its rows are near enough for a tile's 32-bit offsets.
-inline bool rows_at_16(const void *p, int ld, int eb) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (long long)ld * eb % 16 == 0 &&
-         (long long)ld * eb < (1LL << 23);
+inline bool rows_at(uintptr_t bytes, const void *p, int ld, int eb) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 &&
+         (long long)ld * eb % (long long)bytes == 0 && (long long)ld * eb < (1LL << 23);
+}
+inline bool rows_at_16(const void *p, int ld, int eb) { return rows_at(16, p, ld, eb); }
+// Whether the tiles' loads take it as it lies: a direct load of 16 bytes asks for an
+// address of 4, which every float has, and the last ones of a row of fewer bytes
+// for one of 16.
+inline bool rows_for_tiles(const void *p, int ld, int eb) {
+  return rows_at(eb == 4 ? 4 : 16, p, ld, eb);
 }
 size_t proj_workspace(const ProjCall &c);
 hipError_t launch_proj(const ProjCall &c, void *ws);
@@ -362,7 +369,8 @@ hipError_t launch_proj(const ProjCall &c, void *ws);
 // Gradients of a gated block; validated; M, F, K > 0.
 struct GluGradCall {
   bool half, dw32;         // dw32: dW holds fp32 whatever the others hold
-  bool aligned;
+  bool aligned;            // X and W are rows_for_tiles
+  bool at_16;              // X and W are rows_at_16
   int M, F, K;
   int act;
   const void *dH;

@@ -137,7 +137,7 @@ bool tiled(const ProjCall &c) {
 }
 
 struct ProjSpace {
-  char *X, *W;       // copies with rows of whole 16 bytes
+  char *X, *W;       // copies of rows that the tiles do not take as they lie
 };
 
 size_t carve(const ProjCall &c, void *base, ProjSpace *s) {
@@ -156,8 +156,8 @@ hipError_t run_tiles(const ProjCall &c, ProjParams p, const ProjSpace &s) {
     const long long row = (long long)c.K * eb;
     RowCopy x = {c.X, (long long)c.ldx * eb, row, c.M, s.X};
     RowCopy w = {c.W, (long long)c.ldw * eb, row, c.gated ? 2 * c.N : c.N, s.W};
-    if (rows_at_16(c.X, c.ldx, eb)) x.dst = nullptr;
-    if (rows_at_16(c.W, c.ldw, eb)) w.dst = nullptr;
+    if (rows_for_tiles(c.X, c.ldx, eb)) x.dst = nullptr;
+    if (rows_for_tiles(c.W, c.ldw, eb)) w.dst = nullptr;
     const hipError_t e = launch_row_copies(x, w, c.stream);
     if (e != hipSuccess) return e;
     const int ld = (int)((row + 15) / 16 * 16 / eb);

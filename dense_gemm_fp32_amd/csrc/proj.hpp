@@ -86,6 +86,7 @@ struct ProductJob {
   void *C;                // NULL: not wanted
   int lda, ldb, ldc, M, N, K;
   float beta;
+  bool odd;               // fp32: not every row of B starts at 16 bytes
   int splits, chunk;      // K in parts of `chunk`; more than one: their sums to
   float *slab;            // slab, part after part, in rows of N rounded up to 4
 };

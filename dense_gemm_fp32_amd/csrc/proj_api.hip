@@ -10,6 +10,7 @@ namespace {
 using dgemm::GluGradCall;
 using dgemm::ProjCall;
 using dgemm::rows_at_16;
+using dgemm::rows_for_tiles;
 using dgemm::Space;
 
 int at_least_one(int n) { return n > 1 ? n : 1; }
@@ -29,7 +30,7 @@ hipError_t scale(bool half, int M, int N, float beta, void *C, int ldc, hipStrea
 
 int run(ProjCall &c, void *ws, size_t ws_bytes, int base) {
   const int eb = c.i8 ? 1 : (c.half ? 2 : 4);
-  c.aligned = rows_at_16(c.X, c.ldx, eb) && rows_at_16(c.W, c.ldw, eb);
+  c.aligned = rows_for_tiles(c.X, c.ldx, eb) && rows_for_tiles(c.W, c.ldw, eb);
   Space space;
   const int rc = space.open(ws, ws_bytes, dgemm::proj_workspace(c), c.stream, base);
   if (rc != 0) return rc;
@@ -194,7 +195,9 @@ int glu_grad(bool half, bool dw32, int M, int F, int K, int act, const void *dH,
   c.half = half;
   c.dw32 = dw32;
   const int eb = half ? 2 : 4;
-  c.aligned = (X == nullptr || rows_at_16(X, ldx, eb)) && (W == nullptr || rows_at_16(W, ldw, eb));
+  c.aligned = (X == nullptr || rows_for_tiles(X, ldx, eb)) &&
+              (W == nullptr || rows_for_tiles(W, ldw, eb));
+  c.at_16 = (X == nullptr || rows_at_16(X, ldx, eb)) && (W == nullptr || rows_at_16(W, ldw, eb));
   c.M = M;
   c.F = F;
   c.K = K;
@@ -337,15 +340,18 @@ size_t gemm_glu_grad_workspace(int dtype, int M, int F, int K, int aligned) {
     return 0;
   GluGradCall c = {};
   c.half = dtype == 1;
-  c.aligned = aligned != 0;
   c.M = M;
   c.F = F;
   c.K = K;
-  // without the 16-byte rows, also what a call takes that has them
-  const size_t bytes = dgemm::glu_grad_workspace(c);
-  c.aligned = true;
-  const size_t least = dgemm::glu_grad_workspace(c);
-  return bytes > least ? bytes : least;
+  // also what a call takes whose rows allow more
+  size_t bytes = 0;
+  for (int least = aligned != 0 ? 1 : 0; least <= 2; ++least) {
+    c.aligned = least >= 1;
+    c.at_16 = least >= 2;
+    const size_t n = dgemm::glu_grad_workspace(c);
+    bytes = n > bytes ? n : bytes;
+  }
+  return bytes;
 }
 
 }  // extern "C"

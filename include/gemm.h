@@ -485,8 +485,8 @@ size_t gemm_moe_workspace(int dtype, int M, int D, int F, int E, int top_k);
  * results as for the products whose rows choose their own weights, above; the
  * test switches do not apply either.  A captured call needs a workspace unless its
  * *_workspace function says 0; `aligned` of those functions: nonzero where every
- * row of X and W starts at a multiple of 16 bytes, less than 2^23 bytes behind the
- * one before (otherwise the call may copy them).
+ * row of X and W starts at a multiple of 16 bytes (floats: anywhere), less than 2^23
+ * bytes behind the one before (otherwise the call may copy them).
  *
  * Status: 0; a positive hipError_t; or for invalid argument i (from 1, in
  * signature order) -600-i (gemm_quant_i8_*), -700-i (gemm_i8_*), -800-i

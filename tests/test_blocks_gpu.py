@@ -444,6 +444,14 @@ GRAD += [(2048, 1024, 2048, 0, "silu", True, 0.0, 0.0, True),
          (2048, 2048, 200, 0, "gelu_tanh", False, 0.0, 0.0, False),
          (1200, 2048, 264, 0, "silu", False, 0.0, 0.0, False),
          (17, 4082, 72, 0, "silu", False, 0.0, 0.0, False),
+         # rows that start anywhere, sums over whole steps; rows of one to four
+         (128, 160, 101, 1, "silu", False, 1.0, 1.0, False),
+         (320, 256, 37, 3, "gelu", True, 0.0, 1.0, False),
+         (64, 32, 130, 1, "relu", True, 0.0, 0.0, True),
+         (70, 80, 1, 0, "silu", False, 0.0, 0.0, False),
+         (70, 80, 2, 0, "silu", True, 1.0, 0.0, False),
+         (70, 80, 3, 2, "gelu", False, 0.0, 0.0, False),
+         (70, 80, 4, 1, "silu", False, 0.0, 1.0, False),
          (33, 4082, 72, 0, "gelu", False, 0.0, 0.0, False),
          (49, 4082, 72, 0, "silu", False, 1.0, 0.0, False)]
 

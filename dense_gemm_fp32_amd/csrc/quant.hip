@@ -17,6 +17,7 @@ namespace dgemm {
 namespace {
 
 constexpr int kQuantThreads = 256;
+constexpr int kQuantGrid = 1 << 20;     // rows to a grid's x: a dimension's threads fit 32 bits
 
 // A row's scale s and what its elements are divided by it with.
 struct Divisor {
@@ -98,12 +99,14 @@ __device__ __forceinline__ unsigned top_bits(unsigned top, const typename El<T>:
 // A workgroup a row.  NV: pieces of a row that a thread holds; 0: rows of any
 // length, read twice.
 template <typename T, int NV>
-__global__ __launch_bounds__(kQuantThreads) void quant_rows(const T *X, int ldx, int K, int8_t *Q,
-                                                            int ldq, float *scale) {
+__global__ __launch_bounds__(kQuantThreads) void quant_rows(const T *X, int ldx, int M, int K,
+                                                            int8_t *Q, int ldq, float *scale) {
   constexpr int STEP = kQuantThreads * El<T>::VEC;
   __shared__ unsigned part[kQuantThreads / kWave];
-  const T *x = X + (size_t)blockIdx.x * (size_t)ldx;
-  int8_t *q = Q + (size_t)blockIdx.x * (size_t)ldq;
+  const int row = (int)(blockIdx.y * kQuantGrid + blockIdx.x);
+  if (row >= M) return;
+  const T *x = X + (size_t)row * (size_t)ldx;
+  int8_t *q = Q + (size_t)row * (size_t)ldq;
   const int k0 = threadIdx.x * El<T>::VEC;
   typename El<T>::Frag f[NV > 0 ? NV : 1];
   unsigned top = 0;
@@ -128,7 +131,7 @@ __global__ __launch_bounds__(kQuantThreads) void quant_rows(const T *X, int ldx,
   for (int w = 0; w < kQuantThreads / kWave; ++w) top = part[w] > top ? part[w] : top;
   const bool bad = top >= 0x7f800000u;
   const float s = __builtin_bit_cast(float, top) / 127.0f;
-  if (threadIdx.x == 0) scale[blockIdx.x] = bad ? __builtin_nanf("") : s;
+  if (threadIdx.x == 0) scale[row] = bad ? __builtin_nanf("") : s;
   Divisor d;
   d.zero = bad || s == 0.0f;
   d.up = s < 0x1p-60f ? 0x1p64f : 1.0f;
@@ -153,8 +156,10 @@ __global__ __launch_bounds__(kQuantThreads) void quant_rows(const T *X, int ldx,
 template <typename T, int NV>
 void launch(int M, int K, const void *X, int ldx, int8_t *Q, int ldq, float *scale,
             hipStream_t stream) {
-  hipLaunchKernelGGL((quant_rows<T, NV>), dim3((unsigned)M), dim3(kQuantThreads), 0, stream,
-                     static_cast<const T *>(X), ldx, K, Q, ldq, scale);
+  const dim3 grid((unsigned)(M < kQuantGrid ? M : kQuantGrid),
+                  (unsigned)((M + kQuantGrid - 1) / kQuantGrid));
+  hipLaunchKernelGGL((quant_rows<T, NV>), grid, dim3(kQuantThreads), 0, stream,
+                     static_cast<const T *>(X), ldx, M, K, Q, ldq, scale);
 }
 
 template <typename T>

@@ -87,6 +87,18 @@ def test_quantize(dt, case):
     assert pads_intact(big, K)
 
 
+def test_quantize_most_rows():
+    """As many rows as a call takes, of one element each."""
+    import dense_gemm_fp32_amd as dg
+    M = 1 << 24
+    note("quantize %d rows" % M)
+    x = ((torch.arange(M, device=GPU) % 4001 - 2000).float() / 16).half()[:, None]
+    q, s = dg.quantize(x)
+    assert torch.equal(q[:, 0], (torch.sign(x[:, 0]) * 127).to(torch.int8))
+    top = torch.full((1,), 127.0, device=GPU)
+    assert torch.equal(s, x[:, 0].float().abs() / top)
+
+
 @pytest.mark.parametrize("dt", ["f16", "f32"])
 def test_quantize_ties_and_odd_rows(dt):
     """Quotients on and next to the border of two whole numbers; rows of zeros, of
@@ -361,6 +373,24 @@ def test_activations_over_their_range(dt, name):
     dg.glu(X.to(GPU), W.to(GPU), h, act=name)
     # where act(g) leaves the normal numbers, to their smallest
     assert worst(h, want[0], want[1] + 150 * torch.finfo(torch.float32).tiny) <= 1.0
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+def test_activations_of_gates_whose_square_leaves_fp32(name):
+    """Gates up to 1e30: the activation is the gate or 0, its derivative 1 or 0."""
+    import dense_gemm_fp32_amd as dg
+    gates = torch.tensor([1e10, 1e18, 1e20, 1e30, -1e10, -1e18, -1e20, -1e30])
+    n, on = len(gates), (gates > 0).float()
+    Z = torch.stack((gates, torch.full((n,), 2.0)), 1)
+    X, dH = gates[:, None], torch.full((n, 1), 3.0)
+    h, dX = (torch.empty(n, 1, device=GPU) for _ in range(2))
+    dg.glu(X.to(GPU), torch.tensor([[1.0], [1e-30]], device=GPU), h, act=name)
+    up = gates * torch.tensor(1e-30)
+    assert torch.allclose(h[:, 0].cpu(), gates * on * up, rtol=2 ** -20, atol=1e-30)
+    dg.glu_grad(dH.to(GPU), X.to(GPU), torch.tensor([[1.0], [0.0]], device=GPU), dX=dX, act=name,
+                Z=Z.to(GPU))
+    # dX = dG * 1 + dU * 0, dG = 3 * 2 * act'(g)
+    assert torch.equal(dX[:, 0].cpu() + 0.0, 6.0 * on)
 
 
 @pytest.mark.parametrize("M", [3, 70, 300])

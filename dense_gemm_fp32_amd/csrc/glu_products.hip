@@ -114,46 +114,64 @@ hipError_t run(const ProductJob &a, const ProductJob &b, bool mid, hipStream_t s
              : launch<typename ProjTiles<EB>::Small, TA, TB>(a, b, stream);
 }
 
-// A tile: its step in microseconds with the CU full (what it reaches in
-// proj_tile.hpp's products), how many steps the longest workgroup adds to a launch,
-// and, for fp32, how many workgroups a CU holds.  fp32 is bound by its matrix
-// instructions, and a launch whose workgroups all fit at once lasts as long as the
-// CU that was dealt one more than the others (us by parts of the first product's k,
-// 257 x 1024 x 1024: 1 55, 2 38, 3 34, 4 40, 5 37, 6 36; 1000 x 1500 x 517: 1 105,
-// 2 90, 3 93, 4 86, 5 91, 6 94).
+// A tile: its step in microseconds with the CU full, how many steps a workgroup's
+// start and end take, how much of the longest is added where more workgroups than
+// fit at once follow each other, and how many a CU holds.
+//
+// A launch whose workgroups all fit at once lasts as long as the CU that was dealt
+// the most steps; parts of a sum even that out, cost a start each, and a launch that
+// sums them.  (us by parts of the first product's k, [dG dU] included: fp32 1000 x
+// 1500 x 517 2 77, 3 83, 4 70, 5 76, 8 75; 512 x 1408 x 512 3 46, 4 42, 5 41, 6 38, 8
+// 42; fp16 in 128x128 tiles 48 x 8192 x 2048 3 63, 4 51, 8 39, in 64x64 tiles 81; 1024 x
+// 1024 x 2048 1 32, 2 30, 4 35, 64x64 36.  Over 14 sizes in fp32 and 18 in fp16 the plan
+// is the fastest or within 4% of it.)
 struct StepCost {
   int bm, bk;
-  double step, longest;
+  double step, start, longest;
   int slots;
 };
 
+// Steps of the CU that is dealt the most: n1 workgroups of c1, then n2 of c2, one
+// CU after another.
+double most_steps(long long n1, double c1, long long n2, double c2) {
+  const long long r1 = n1 % kCUs, rt = (n1 + n2) % kCUs;
+  double most = 0.0;
+  for (const long long i : {0LL, r1, r1 - 1, rt, rt - 1}) {   // a CU of each kind there is
+    if (i < 0) continue;
+    const double first = (double)(n1 / kCUs + (i < r1));
+    const double all = (double)((n1 + n2) / kCUs + (i < rt));
+    const double steps = first * c1 + (all - first) * c2;
+    most = steps > most ? steps : most;
+  }
+  return most;
+}
+
 double cost(const StepCost &t, const ProductJob &a, const ProductJob &b, int sa, int sb) {
-  double work = 0.0, longest = 0.0, sums = 0.0, wgs = 0.0;
+  double work = 0.0, sums = 0.0, chunk[2];
+  long long wgs[2];
   for (int i = 0; i < 2; ++i) {
     const ProductJob &j = i ? b : a;
     const int s = i ? sb : sa;
-    const double tiles = (double)((j.M + t.bm - 1) / t.bm) * ((j.N + t.bm - 1) / t.bm);
-    const int steps = (j.K + t.bk - 1) / t.bk, chunk = (steps + s - 1) / s;
-    work += tiles * steps;
-    wgs += tiles * s;
-    if (chunk > longest) longest = chunk;
-    // a launch of its own, and the parts written and read at 4 TB/s
-    if (s > 1) sums += 3.5 + s * (double)j.M * (double)j.N * 8.0 / 4.0e6;
+    const long long tiles = (long long)((j.M + t.bm - 1) / t.bm) * ((j.N + t.bm - 1) / t.bm);
+    const int steps = (j.K + t.bk - 1) / t.bk, each = (steps + s - 1) / s;
+    wgs[i] = tiles * ((steps + each - 1) / each);
+    chunk[i] = each + t.start;
+    work += (double)wgs[i] * chunk[i];
+    // what a launch adds behind another, and the parts written and read at 4 TB/s
+    if (s > 1) sums += 1.5 + s * (double)j.M * (double)j.N * 8.0 / 4.0e6;
   }
-  double steps = work / kCUs + t.longest * longest;
-  if (wgs <= t.slots * (double)kCUs) {
-    const int most = (int)((wgs + kCUs - 1) / kCUs);
-    steps = most * work / wgs;
-    if (steps < longest) steps = longest;
-  }
+  const int f = chunk[1] > chunk[0] ? 1 : 0;                  // the longer workgroups first
+  const double steps = wgs[0] + wgs[1] <= t.slots * kCUs
+                           ? most_steps(wgs[f], chunk[f], wgs[1 - f], chunk[1 - f])
+                           : work / kCUs + t.longest * chunk[f];
   return t.step * steps + sums;
 }
 
 }  // namespace
 
 ProductPlan plan_products(bool half, ProductJob &a, ProductJob &b) {
-  const StepCost f16[2] = {{64, 128, 0.45, 1.0, 0}, {128, 64, 0.58, 1.0, 0}};
-  const StepCost f32[2] = {{64, 32, 0.43, 0.5, 4}, {128, 32, 1.70, 0.5, 2}};
+  const StepCost f16[2] = {{64, 128, 0.40, 2.5, 0.3, 2}, {128, 64, 0.65, 1.0, 0.3, 2}};
+  const StepCost f32[2] = {{64, 32, 0.43, 2.0, 0.5, 4}, {128, 32, 1.75, 2.0, 0.5, 2}};
   ProductPlan best = {false, 1e300};
   int bsa = 1, bsb = 1;
   for (int m = 0; m < 2; ++m) {
@@ -165,7 +183,7 @@ ProductPlan plan_products(bool half, ProductJob &a, ProductJob &b) {
     for (int sa = 1; sa <= most(a); ++sa)
       for (int sb = 1; sb <= most(b); ++sb) {
         const double c = cost(t, a, b, sa, sb);
-        if (c >= 0.98 * best.us) continue;
+        if (c >= best.us) continue;
         best = ProductPlan{m == 1, c};
         bsa = sa;
         bsb = sb;

@@ -188,18 +188,24 @@ ProductJob job_w(const GluGradCall &c) {
 }
 
 // Products of rows, hidden and width below which one launch is ahead of the
-// library's two (us, one launch first: fp16 257 x 1024 x 1024 19, 31; 2048^3 93, 109;
-// 4096 x 1024 x 4096 167, 155; fp32 16 x 2000 x 1024 23, 53; 1024 x 2048 x 2048 265,
-// 267; 2048^3 517, 506).  Rows that the library would copy or load by elements take
-// it at any size (3000 x 2000 x 2050 with odd rows: fp16 156, 387; fp32 833, 1094).
-constexpr double kTogetherF16 = 1.0e10, kTogetherF32 = 5.0e9;
+// library's two (us, one launch first: fp16 257 x 1024 x 1024 17, 31; 2048^3 87, 116;
+// 4096 x 1024 x 4096 132, 148; 3000^3 291, 340; 4096 x 2048 x 4096 292, 236; 4096^3 600,
+// 476; fp32 16 x 2000 x 1024 23, 53; 1024 x 2048 x 2048 267, 270; 2048^3 512, 510; 4096 x
+// 1024 x 4096 996, 956).  In fp16 it is ahead up to kFewTogether rows at any size, the
+// library's large tiles having few steps of dW's then (1024 x 8192 x 4096 302, 335;
+// 1024 x 16384 x 4096 595, 671; 512 x 16384 x 4096 346, 396; but 2048 x 8192 x 4096 518,
+// 465).  Rows that the library would copy or load by elements take it at any size
+// (3000 x 2000 x 2050 with odd rows: fp16 145, 387; fp32 787, 1094).
+constexpr double kTogetherF16 = 3.0e10, kTogetherF32 = 5.0e9;
+constexpr int kFewTogether = 1024;
 
 bool together(const GluGradCall &c) {
   const long long eb = c.half ? 2 : 4;
   // a tile's offsets have to fit 32 bits
   if (2LL * c.F * eb >= kTileRowBytes || c.K * eb >= kTileRowBytes) return false;
   if (!c.half && c.K < 4) return false;        // glu_products.hip: rows of floats
-  return !c.at_16 || (double)c.M * c.F * c.K < (c.half ? kTogetherF16 : kTogetherF32);
+  return !c.at_16 || (c.half && c.M <= kFewTogether) ||
+         (double)c.M * c.F * c.K < (c.half ? kTogetherF16 : kTogetherF32);
 }
 
 struct GradSpace {

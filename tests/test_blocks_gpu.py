@@ -515,7 +515,8 @@ def test_glu_grad(dt, case):
 
 
 @pytest.mark.parametrize("dt,M,F,K", [("f32", 1536, 1664, 2048), ("f16", 2048, 2304, 2176),
-                                      ("f16", 2050, 2304, 2183), ("f32", 1536, 1664, 2051)])
+                                      ("f16", 2050, 2304, 2183), ("f32", 1536, 1664, 2051),
+                                      ("f16", 2048, 3712, 4096)])
 def test_glu_grad_large(dt, M, F, K):
     """Sizes at which the products run one after the other, and beside them those
     whose rows do not start at 16 bytes; the reference in 64 bits on the GPU."""

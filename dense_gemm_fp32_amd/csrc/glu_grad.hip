@@ -120,17 +120,24 @@ Call product_w(const GluGradCall &c, const void *D, int ldd) {
 }
 
 // Workspace that such a product may take: for operands whose rows all allow
-// the widest loads, or do not.
+// the widest loads, or do not, and for a beta of 0 or another (which of the fp32
+// splits is chosen goes by whether C is read).  It must not depend on what the
+// workspace's size is asked without: the betas, dW's type, the outputs' addresses
+// and distances of rows.
 size_t product_bytes(const GluGradCall &c, Call g) {
   void *p = reinterpret_cast<void *>((uintptr_t)256);
   size_t most = 0;
+  g.A = g.B = g.C = p;
+  g.out32 = false;
+  g.ws_fixed_bytes = (size_t)1 << 40;
   for (int odd = 0; odd < (c.at_16 ? 1 : 2); ++odd) {
-    g.A = g.B = g.C = p;
     g.ldb = odd ? c.K | 1 : (c.K + 7) / 8 * 8;
     g.ldc = g.ldb;
-    g.ws_fixed_bytes = (size_t)1 << 40;
-    const size_t n = (c.half ? plan_f16(g) : plan_f32(g)).ws_bytes;
-    most = n > most ? n : most;
+    for (const float beta : {0.0f, 1.0f}) {
+      g.beta = beta;
+      const size_t n = (c.half ? plan_f16(g) : plan_f32(g)).ws_bytes;
+      most = n > most ? n : most;
+    }
   }
   return most;
 }

@@ -102,6 +102,48 @@ def test_workspace_sizes():
         assert dg.gemm_glu_workspace(2, 16, 16, 131072, aligned) == 0
 
 
+def whole_rows(n, dt):
+    """n elements filled up to whole 16 bytes."""
+    v = 4 if dt == "f32" else 8
+    return (n + v - 1) // v * v
+
+
+def grad_call(dt, M, F, K, ws, odd=0, **change):
+    """A call whose arguments are valid, for rows of X and W that start at 16 bytes, or
+    (odd) do not."""
+    ldk = whole_rows(K, dt) + odd
+    return entry("gemm_glu_grad_" + dt, dict(
+        GRAD, M=M, F=F, K=K, lddh=F, ldx=ldk, ldw=ldk, ldz=2 * F, lddx=K, lddw=K,
+        workspace_bytes=ws, **change))
+
+
+# The addresses are no memory: without a GPU a call whose arguments pass ends with the
+# runtime's error, on a GPU it would run.
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would run on the GPU")
+@pytest.mark.parametrize("dt", ["f32", "f16", "f16f32"])
+def test_gradients_take_the_workspace_named_whatever_is_asked(dt):
+    """Betas, the outputs' rows, which outputs are wanted and whether Z is kept change
+    how the products of the backward pass are split, but never ask for more than
+    gemm_glu_grad_workspace says."""
+    import random
+    import dense_gemm_fp32_amd as dg
+    rng = random.Random(7)
+    sizes = [(2760, 5504, 3344), (5376, 5632, 2560), (4608, 6912, 4096), (7040, 8160, 3824),
+             (2464, 6176, 3152), (2992, 5392, 5808)]
+    sizes += [tuple(rng.randrange(16, 8192) // 16 * 16 + rng.choice((0, 0, 0, 5))
+                    for _ in range(3)) for _ in range(400)]
+    changes = [dict(beta_x=bx, beta_w=bw, Z=z) for bx in (0.0, 1.0) for bw in (0.0, 1.0)
+               for z in (None, P)]
+    changes += [dict(beta_x=0.5, dW=None), dict(beta_w=-1.0, dX=None), dict(beta_x=math.nan),
+                dict(dX=P + 4, dW=P + 4, beta_x=1.0, beta_w=1.0)]
+    for s in sizes:
+        for odd in (0, 1):
+            need = dg.gemm_glu_grad_workspace(0 if dt == "f32" else 1, *s, 0 if odd else 1)
+            for c in changes:
+                assert grad_call(dt, *s, need, odd, **c) > 0, (s, odd, c)
+            assert grad_call(dt, *s, 0, odd) == -1020
+
+
 def test_wrappers_refuse():
     import dense_gemm_fp32_amd as dg
     h, q = torch.zeros(2, 4), torch.zeros(2, 4, dtype=torch.int8)

@@ -641,7 +641,7 @@ def quantize(X, Q=None, scale=None, stream=None):
 
 def gemm_i8(X, W, Y, x_scale=None, w_scale=None, alpha=1.0, beta=0.0, workspace=None,
             stream=None):
-    """Y := alpha * x_scale[:, None] * w_scale * (X @ W.t()) + beta*Y (in place)
+    """Y := alpha * (w_scale * (x_scale[:, None] * (X @ W.t()))) + beta*Y (in place)
     for 8-bit integers: X M x K and W N x K int8, Y M x N float16 or float32 (rows
     contiguous, possibly padded), x_scale M and w_scale N float32 or None (1).  The
     sum is exact.  workspace: a uint8 tensor of gemm_i8_workspace bytes to use

@@ -14,7 +14,7 @@
 namespace dgemm {
 
 // What becomes of the sums.
-//   kScaled  Y[m, n] := alpha * xs[m] ws[n] * sum + beta * Y[m, n]
+//   kScaled  Y[m, n] := alpha * (ws[n] * (xs[m] * sum)) + beta * Y[m, n]
 //   kGated   H[m, f] := act(g) * u, and Z[m, f], Z[m, F + f] := g, u where
 //            wanted; g and u: the sums of W's rows f and F + f (times their
 //            scales)

@@ -524,15 +524,17 @@ int gemm_quant_i8_f32(int M, int K, const float *X, int ldx, int8_t *Q, int ldq,
 /*
  * Product of 8-bit integers with a scale for each row of X and of W:
  *
- *     Y[m, n] := alpha * x_scale[m] * w_scale[n] * sum_k X[m, k] W[n, k] + beta * Y[m, n]
+ *     Y[m, n] := alpha * (w_scale[n] * (x_scale[m] * sum_k X[m, k] W[n, k])) + beta * Y[m, n]
  *
  *   X, ldx    M x K;  W, ldw: N x K (as gemm_*_nt's B)
  *   x_scale, w_scale   device, M and N floats (NULL: 1)
  *   Y, ldy    M x N, not read when beta == 0
  *
  * The sum is exact (32-bit integers); it is rounded to binary32 and the rest
- * formed in fp32, in the order written from the right: at most 4 roundings of
- * 2^-24 (and beta * Y's), then one to Y's type.  alpha == 0 or K == 0:
+ * formed in fp32, from the innermost brackets out: at most 4 roundings of 2^-24
+ * (and one for alpha * (...) + beta * Y), then one to Y's type.  A product that
+ * leaves fp32 on the way is infinite, or loses digits below its normal numbers,
+ * also where a later scale would bring it back.  alpha == 0 or K == 0:
  * Y := beta * Y.
  */
 int gemm_i8_f16(int M, int N, int K, float alpha,
@@ -561,7 +563,7 @@ size_t gemm_i8_workspace(int M, int N, int K, int aligned);
  * G and U are summed in fp32 and enter the activation unrounded; H and Z are
  * rounded once.  K == 0: zeros.  The gemm_glu_i8_* calls take X and W in 8-bit
  * integers with scales (x_scale: M floats, w_scale: 2F; NULL: 1); their sums are
- * exact, as gemm_i8_*'s.
+ * exact and scaled as gemm_i8_*'s (alpha 1).
  */
 int gemm_glu_f16(int M, int F, int K, int act,
                  const gemm_half_t *X, int ldx,

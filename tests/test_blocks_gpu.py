@@ -235,6 +235,38 @@ def test_gemm_i8_sums_are_exact():
     assert float(S.max()) < 2 ** 24 and torch.equal(y.cpu().double(), S)
 
 
+# few rows in two forms, then each tile
+SCALED = [(1, 200, 144), (3, 40, 1000), (20, 300, 256), (64, 8200, 270), (130, 1030, 300),
+          (700, 1500, 130), (2100, 4160, 144)]
+
+
+@pytest.mark.parametrize("M,N,K", SCALED)
+def test_scales_are_taken_in_the_order_that_is_documented(M, N, K):
+    """The sum, rounded to fp32, times the row's scale, times the column's, times alpha:
+    bit for bit; a product that leaves fp32 on the way does not come back."""
+    import dense_gemm_fp32_amd as dg
+    g = gen(M + N)
+    X, W = whole(g, (M, K)), whole(g, (N, K))
+    xs, ws = scales(g, M), scales(g, N)
+    xs[0], ws[:N // 2] = 2.0 ** 120, ws[:N // 2] * 2.0 ** -100
+    if M > 1:
+        xs[1], ws[N // 2:] = 2.0 ** -110, ws[N // 2:] * 2.0 ** 100
+    S = (X.double() @ W.double().t()).float()
+    Z = (S * xs[:, None]) * ws[None, :]
+    assert not torch.equal(Z, (S * ws[None, :]) * xs[:, None])
+    alpha = 1.37
+    want = torch.tensor(alpha) * Z
+    y = torch.empty(M, N, device=GPU)
+    dg.gemm_i8(X.to(GPU), W.to(GPU), y, x_scale=xs.to(GPU), w_scale=ws.to(GPU), alpha=alpha)
+    same = lambda a, b: torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))  # noqa: E731
+    assert torch.isinf(want[0]).any() and same(y.cpu(), want)
+    F = N // 2
+    h = torch.empty(M, F, device=GPU)
+    dg.glu(X.to(GPU), W.to(GPU), h, act="relu", x_scale=xs.to(GPU), w_scale=ws.to(GPU))
+    want = torch.where(Z[:, :F] <= 0, torch.zeros(()), Z[:, :F]) * Z[:, F:]
+    assert same(h.cpu(), want)
+
+
 @pytest.mark.parametrize("M", [1, 20, 130, 700])
 def test_gemm_i8_scales_that_are_not_finite_stay_in_their_rows(M):
     import dense_gemm_fp32_amd as dg

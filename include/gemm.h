@@ -501,6 +501,8 @@ size_t gemm_moe_workspace(int dtype, int M, int D, int F, int E, int top_k);
 #define GEMM_ACT_GELU 1        /* g * Phi(g), Phi the normal distribution function */
 #define GEMM_ACT_GELU_TANH 2   /* g * (1 + tanh(sqrt(2/pi) * (g + 0.044715 g^3))) / 2 */
 #define GEMM_ACT_RELU 3        /* max(g, 0) */
+/* In fp32; an exponential below 2^-126 (silu: of gates below -87.3) may count as 0:
+ * activation and derivative are then off by less than 2^-117. */
 
 /*
  * Rows to 8-bit integers with a scale each (tokens before a product, or a

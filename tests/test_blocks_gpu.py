@@ -407,6 +407,41 @@ def test_activations_over_their_range(dt, name):
     assert worst(h, want[0], want[1] + 150 * torch.finfo(torch.float32).tiny) <= 1.0
 
 
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_activations_at_the_end_of_the_normal_numbers(name):
+    """Gates whose exponential is one of the smallest normal numbers, or below them,
+    where it may count as 0: the activation and its derivative are then within 2^-117,
+    above that as good as anywhere.  An up value and a gradient of 2^20 bring them into
+    range."""
+    import dense_gemm_fp32_amd as dg
+    g = torch.linspace(-105.0, -80.0, 2001) if name == "silu" else \
+        torch.linspace(-14.6, -12.0, 1001) if name == "gelu" else torch.linspace(-10.9, -9.5, 1001)
+    n, up = len(g), 2.0 ** 20
+    G = g.double()
+    v, d, ev, ed = ref.act(name, G)
+    if name == "gelu":     # (the reference's distribution function ends near g = -8)
+        p, f = 0.5 * torch.erfc(-G / math.sqrt(2)), torch.exp(-G * G / 2) / math.sqrt(2 * math.pi)
+        c = (16 + 4 * G * G) * ref.U32
+        v, d, ev, ed = G * p, p + G * f, c * (G * p).abs(), 2 * c * (p + G.abs() * f)
+    # |t| of exp(-|t|); gelu: -g^2 / 2, whose two ends meet the same exponential
+    t = {"silu": G.abs(), "gelu": G * G / 2,
+         "gelu_tanh": math.sqrt(8 / math.pi) * (G + 0.044715 * G ** 3).abs()}[name]
+    low = torch.where(t > 125 * math.log(2), 2.0 ** -117, 0.0).double()
+    assert 100 < int((low == 0).sum()) < n - 100
+    ev, ed = ev + low, ed + low
+    W = torch.tensor([[1.0, 0.0], [0.0, up]], device=GPU)
+    h = torch.empty(n, 1, device=GPU)
+    dg.glu(torch.stack((g, torch.ones(n)), 1).to(GPU), W, h, act=name)
+    assert worst(h[:, 0], v * up, ev * up + ref.U32 * (v * up).abs()) <= 1.0
+    # dX = [dG, dU], dG = 2^20 * 1 * act'(g), dU = 2^20 * act(g)
+    dX = torch.empty(n, 2, device=GPU)
+    dg.glu_grad(torch.full((n, 1), up, device=GPU), torch.zeros(n, 2, device=GPU),
+                torch.eye(2, device=GPU), dX=dX, act=name,
+                Z=torch.stack((g, torch.ones(n)), 1).to(GPU))
+    assert worst(dX[:, 0], d * up, ed * up + 2 * ref.U32 * (d * up).abs()) <= 1.0
+    assert worst(dX[:, 1], v * up, ev * up + 2 * ref.U32 * (v * up).abs()) <= 1.0
+
+
 @pytest.mark.parametrize("name", ref.ACTS)
 def test_activations_of_gates_whose_square_leaves_fp32(name):
     """Gates up to 1e30: the activation is the gate or 0, its derivative 1 or 0."""

@@ -1,5 +1,6 @@
 """Products of 8-bit integers and gated blocks on the GPU, against 64-bit
 references within derived bounds."""
+import ctypes
 import math
 
 import pytest
@@ -601,6 +602,168 @@ def test_glu_grad_large(dt, M, F, K):
         assert worst(got, value.cpu(), bound.cpu()) <= 1.0
 
 
+class KernelNode(ctypes.Structure):
+    """hipKernelNodeParams"""
+    _fields_ = [("block", ctypes.c_uint * 3), ("extra", ctypes.c_void_p), ("func", ctypes.c_void_p),
+                ("grid", ctypes.c_uint * 3), ("params", ctypes.c_void_p),
+                ("shared", ctypes.c_uint)]
+
+
+def kernels_of(call):
+    """Names of the kernels that call() launches, from a graph of them that is never
+    replayed."""
+    from dense_gemm_fp32_amd import binding
+    lib = binding._lib
+    lib.hipKernelNameRefByPtr.restype = ctypes.c_char_p
+    lib.hipKernelNameRefByPtr.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    raw, n = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t()
+    assert lib.hipGraphGetNodes(raw, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * max(n.value, 1))()
+    assert lib.hipGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
+    names = []
+    for node in nodes[:n.value]:
+        p = KernelNode()
+        assert lib.hipGraphKernelNodeGetParams(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        names.append(lib.hipKernelNameRefByPtr(p.func, None).decode())
+    return names
+
+
+def on_gpu(g, shape, dtype, std, ld=None):
+    """Normal numbers on the GPU, in rows `ld` elements apart with NaN between them."""
+    big = torch.full((shape[0], ld or shape[1]), math.nan, dtype=dtype, device=GPU)
+    view = big[:, :shape[1]]
+    view.copy_(torch.randn(*shape, generator=g, device=GPU) * std)
+    return big, view
+
+
+IN_TURN = [
+    # dtype, M, F, K, distance of rows (None: K), act, Z given, beta_x, beta_w, dW in fp32
+    ("f16", 2048, 3712, 4096, None, "gelu", True, 0.0, 0.0, False),
+    ("f16", 2048, 3712, 4096, None, "silu", True, 0.0, 1.0, True),
+    ("f16", 1100, 6800, 4100, 4104, "silu", False, 0.5, 0.0, True),
+    ("f16", 2050, 3701, 4003, 4016, "gelu_tanh", True, -1.0, 0.5, False),
+    ("f16", 17, (1 << 21) + 8, 16, None, "silu", True, 0.0, 0.0, False),
+    ("f32", 1536, 1664, 2048, None, "gelu", True, 0.0, 0.0, False),
+    ("f32", 1537, 1665, 2051, 2052, "silu", False, 0.0, 1.0, False),
+    # (whether C is read decides how the first product is split)
+    ("f32", 2760, 5504, 3344, None, "relu", True, 1.0, 0.0, False),
+    ("f32", 2760, 5504, 3344, None, "silu", True, 0.0, 0.0, False),
+]
+
+
+def in_turn(case):
+    """(call(dX, dW, stream, workspace), [old dX, old dW], reference's arguments)"""
+    import dense_gemm_fp32_amd as dg
+    dt, M, F, K, ld, name, kept, beta_x, beta_w, dw32 = case
+    g, t = torch.Generator(device=GPU), DT[dt]
+    g.manual_seed(M + F)
+    X, W = on_gpu(g, (M, K), t, 1.0, ld)[1], on_gpu(g, (2 * F, K), t, K ** -0.5, ld)[1]
+    dH = on_gpu(g, (M, F), t, 0.05)[1]
+    Z = on_gpu(g, (M, 2 * F), t, 1.0)[1] if kept else None
+    tw = torch.float32 if dw32 else t
+    old = [on_gpu(g, (M, K), t, 0.1 if beta_x else math.nan, ld),
+           on_gpu(g, (2 * F, K), tw, 0.1 if beta_w else math.nan, ld)]
+
+    def call(dX, dW, stream=None, workspace=None):
+        dg.glu_grad(dH, X, W, dX=dX, dW=dW, act=name, Z=Z, beta_x=beta_x, beta_w=beta_w,
+                    stream=stream, workspace=workspace)
+    return call, old, (dH, X, W, Z, name, old[0][1], old[1][1], beta_x, beta_w, tw)
+
+
+@pytest.mark.parametrize("case", IN_TURN, ids=lambda c: "x".join(map(str, c)))
+def test_glu_grad_products_in_turn(case):
+    """Gradients whose products run one after the other: with and without Z, in either
+    type of dW, over outputs that are not read, columns that end inside 16 bytes, one
+    output alone; the reference in 64 bits on the GPU."""
+    dt, M, F, K, ld = case[:5]
+    note("glu_grad in turn %r" % (case,))
+    call, old, args = in_turn(case)
+    want = ref.glu_grad(*args)
+    bigs, outs = zip(*((b, b[:, :K]) for b in (o[0].clone() for o in old)))
+    call(*outs)
+    torch.cuda.synchronize()
+    for out, big, n in zip(outs, bigs, ("dX", "dW")):
+        assert worst(out, *(v.cpu() for v in want[n])) <= 1.0, n
+        assert pads_intact(big, K)
+    for i in (0, 1):
+        one = old[i][1].clone()
+        call(*((one, None) if i == 0 else (None, one)))
+        assert torch.equal(one, outs[i])
+    names = kernels_of(lambda: call(*outs))
+    assert not any("proj_products" in k for k in names), names
+
+
+@pytest.mark.parametrize("dt,M,F,K,ld", [("f16", 257, 1024, 1024, None), ("f16", 1024, 6000, 5200, None),
+                                         ("f16", 2048, 2304, 2176, None), ("f16", 1100, 40, 61, None),
+                                         ("f16", 17, 4082, 72, 73), ("f32", 1000, 1500, 517, None),
+                                         ("f32", 1300, 1800, 2051, None)])
+def test_glu_grad_products_in_one_launch(dt, M, F, K, ld):
+    """Which sizes take the one launch of both products: fewer rows than 1025 or less
+    work in fp16, less work in fp32, rows that do not start at 16 bytes."""
+    import dense_gemm_fp32_amd as dg
+    g, t = torch.Generator(device=GPU), DT[dt]
+    g.manual_seed(M)
+    X, W, dH = (on_gpu(g, s, t, 0.1, ld if s[1] == K else None)[1]
+                for s in ((M, K), (2 * F, K), (M, F)))
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    names = kernels_of(lambda: dg.glu_grad(dH, X, W, dX=dX, dW=dW))
+    assert sum("proj_products" in k for k in names) == 1, names
+
+
+@pytest.mark.parametrize("case", [IN_TURN[1], IN_TURN[2], IN_TURN[3], IN_TURN[6], IN_TURN[7]],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_glu_grad_products_in_turn_as_they_are_called(case, monkeypatch):
+    """The same bits again, on another stream, in a workspace of exactly the bytes named
+    (nothing beyond it is written, a smaller one is refused) and in captured graphs, two
+    of them alive, each with a workspace of its own."""
+    import dense_gemm_fp32_amd as dg
+    from dense_gemm_fp32_amd import binding
+    note("glu_grad in turn, calls %r" % (case,))
+    call, old, args = in_turn(case)
+    plain, needs = binding._call_rows, []
+
+    def watch(fn, dev, stream, workspace, need, rest):
+        needs.append(need)
+        return plain(fn, dev, stream, workspace, need, rest)
+    monkeypatch.setattr(binding, "_call_rows", watch)
+    fresh = lambda: [o[1].clone() for o in old]  # noqa: E731
+    want = fresh()
+    call(*want)
+    need = needs[0]
+    side = torch.cuda.Stream()
+    room = torch.full((need + 4096,), 170, dtype=torch.uint8, device=GPU)
+    for how in (dict(), dict(stream=side), dict(workspace=room[:need])):
+        outs = fresh()
+        torch.cuda.synchronize()
+        call(*outs, **how)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), how
+    assert bool((room[need:] == 170).all())
+    with pytest.raises(dg.GemmError, match="too small"):
+        call(*fresh(), workspace=room[:need - 256])
+    graphs, X = [], args[1]
+    outs = fresh()
+    for _ in range(2):
+        space = torch.empty(need, dtype=torch.uint8, device=GPU)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(*outs, workspace=space)
+        graphs.append((graph, space))
+    for k in range(4):
+        X.mul_(-0.75)
+        want = fresh()
+        call(*want)
+        for o, v in zip(outs, fresh()):
+            o.copy_(v)
+        torch.cuda.synchronize()
+        graphs[k % 2][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), k
+
+
 @pytest.mark.parametrize("M", [17, 33, 49])
 def test_glu_grad_widest(M):
     """A width at which the rows of [dG dU] pass 8 MiB, in rows of X and W that
@@ -910,6 +1073,32 @@ def test_rows_beyond_32_bits():
     dg.glu_grad(dH, Xh.to(GPU), Wh.to(GPU), dX=torch.empty_like(near), act="gelu", Z=z2)
     dg.glu_grad(dH, Xh.to(GPU), Wh.to(GPU), dX=apart, act="gelu", Z=z)
     assert torch.equal(apart, near)
+
+
+def test_gradients_of_rows_beyond_32_bits():
+    """dH, the kept [G U], X and both outputs in rows more than 2^31 elements from the
+    first: the bits of the same rows close together."""
+    import dense_gemm_fp32_amd as dg
+    g, t = gen(4), torch.float16
+    far, F, K = (1 << 30) + 8, 80, 96
+    X, W = normal(g, (3, K), t).to(GPU), normal(g, (2 * F, K), t, 0.1).to(GPU)
+    dH, Z = normal(g, (3, F), t, 0.05).to(GPU), normal(g, (3, 2 * F), t).to(GPU)
+    near = torch.empty(3, K, dtype=t, device=GPU), torch.empty(2 * F, K, dtype=t, device=GPU)
+    dg.glu_grad(dH, X, W, *near, act="gelu", Z=Z)
+    want = ref.glu_grad(dH.cpu(), X.cpu(), W.cpu(), Z.cpu(), "gelu", None, None, 0, 0, t)
+    assert worst(near[0], *want["dX"]) <= 1.0 and worst(near[1], *want["dW"]) <= 1.0
+    big = torch.zeros(2 * far + 1024, dtype=t, device=GPU)
+    apart = lambda cols, at: big[at:].as_strided((3, cols), (far, 1))  # noqa: E731
+    z, d = apart(2 * F, 0).copy_(Z), apart(F, 256).copy_(dH)
+    for h, kept in ((dH, z), (d, Z), (d, z)):
+        out = torch.full_like(near[0], math.nan), torch.full_like(near[1], math.nan)
+        dg.glu_grad(h, X, W, *out, act="gelu", Z=kept)
+        assert all(torch.equal(a, b) for a, b in zip(out, near))
+    # rows of X are copied, so the sums' order may be another one
+    x, dx = apart(K, 512).copy_(X), apart(K, 768)
+    dw = torch.full_like(near[1], math.nan)
+    dg.glu_grad(d, x, W, dX=dx, dW=dw, act="gelu", Z=z)
+    assert worst(dx, *want["dX"]) <= 1.0 and worst(dw, *want["dW"]) <= 1.0
 
 
 @pytest.mark.parametrize("N", [6016, 6600])

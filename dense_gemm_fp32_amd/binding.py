@@ -712,7 +712,9 @@ def glu_grad(dH, X, W, dX=None, dW=None, act="silu", Z=None, beta_x=0.0, beta_w=
         dW := cat(dG.t() @ X, dU.t() @ X) + beta_w*dW
 
     Z: what glu() left, or None: G and U are computed again.  All float16, or all
-    float32; dW may be float32 beside float16.  workspace: a uint8 tensor of
+    float32; dW may be float32 beside float16.  In float16 dG and dU are rounded to it
+    once (scale the loss: below 2^-14 they lose digits, from 65520 on they are
+    infinite).  workspace: a uint8 tensor of
     gemm_glu_grad_workspace bytes to use instead of a new one.  Uses the current
     torch stream unless one is given; see gemm_glu_grad_f16 in include/gemm.h.
     Returns (dX, dW)."""

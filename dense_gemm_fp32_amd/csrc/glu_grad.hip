@@ -5,10 +5,12 @@
 //
 // [dG dU] is one pass over G, U and dH where the forward pass kept G and U, else
 // the forward product once more with another end (proj.hip); it is a matrix of the
-// inputs' type, as a stored gradient would be: each element is rounded once (fp16:
-// dX and dW are then off by 2.9e-4 of their norm in place of the 2.1e-4 that
-// their own rounding leaves; two halves an element would halve both products'
-// rate).
+// inputs' type, as a stored gradient would be: each element is rounded once.  In
+// fp16 dX and dW are then off by 2.9e-4 of their norm in place of the 2.1e-4 that
+// their own rounding leaves, and what is below 2^-14 or beyond 65504 in [dG dU] loses
+// digits or is infinite, which the caller's scale of the loss has to keep it from, as
+// it does for dH; two halves an element would halve both products' rate (4096^3: 440
+// of 470 us).
 //
 // The two products run as one launch of both (glu_products.hip), large ones as the
 // library's own, one after the other.

@@ -604,8 +604,10 @@ size_t gemm_glu_workspace(int dtype, int M, int F, int K, int aligned);
  *
  * dW holds the matrices' type, in gemm_glu_grad_f16f32 fp32 (gradients summed over
  * several batches).  dG and dU enter the two products in the matrices' type, each
- * rounded once, as a stored tensor would be (fp16: an overflow is infinity; scale
- * the loss so that none is); the sums are fp32 and rounded once.  relu's derivative
+ * rounded once, as a stored tensor would be: in fp16 to 11 bits, below 2^-14 to
+ * multiples of 2^-24 (to 0 up to 2^-25), and an overflow is infinity, also where dW
+ * holds fp32.  Scale the loss so that they stay inside; gemm_glu_grad_f32 on the same
+ * values keeps all of them.  The sums are fp32 and rounded once.  relu's derivative
  * at 0 is 0.  M == 0 or F == 0: outputs are scaled by their betas.
  */
 int gemm_glu_grad_f16(int M, int F, int K, int act,

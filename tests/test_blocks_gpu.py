@@ -810,6 +810,37 @@ def test_glu_grad_against_differences(name):
         assert abs(diff - slope) <= 0.02 * size
 
 
+@pytest.mark.parametrize("kept", [True, False])
+@pytest.mark.parametrize("M,F", [(1, 1), (40, 3), (700, 600)])
+def test_halves_of_the_gate_s_gradients(M, F, kept):
+    """dG and dU of halves are rounded once, ties to even, with subnormal numbers kept
+    and an overflow infinite: seen through weights of 2^10 and an fp32 dW.  Every sum is
+    of multiples of 2^-24 (2^-34 in dW), fewer than 2^24 of them: exact in any order."""
+    import dense_gemm_fp32_amd as dg
+    g, t = gen(M), torch.float16
+    dH = (torch.randint(-40, 41, (M, F), generator=g) * 2.0 ** -24).to(t)
+    up = 0.125 * (1 + torch.arange(M) % 7).to(t)[:, None]
+    # G = 1, U = up: X = [2^-10, up, 0 ..], gate rows [2^10, 0 ..], up rows [0, 1, 0 ..]
+    X, W = torch.zeros(M, 8, dtype=t), torch.zeros(2 * F, 8, dtype=t)
+    X[:, 0], X[:, 1:2], W[:F, 0], W[F:, 1] = 2.0 ** -10, up, 2.0 ** 10, 1.0
+    Z = torch.cat((torch.ones(M, F), up.expand(M, F)), 1).to(t) if kept else None
+    D = torch.cat((dH.double() * up.double(), dH.double()), 1)
+    assert M == 1 or float((D.half().double() - D).abs().max()) == 2.0 ** -25
+    D = D.half().double()                      # torch's rounding: to even, subnormals kept
+    dX, dW = torch.empty(M, 8, dtype=t, device=GPU), torch.empty(2 * F, 8, device=GPU)
+    args = [v.to(GPU) for v in (dH, X, W)]
+    z = None if Z is None else Z.to(GPU)
+    dg.glu_grad(*args, dX=dX, dW=dW, act="relu", Z=z)
+    assert torch.equal(dX.cpu(), (D @ W.double()).half())
+    assert torch.equal(dW.cpu(), (D.t() @ X.double()).float())
+    args[0][M - 1, F - 1], args[1][M - 1, 1] = 60000.0, 2.0
+    if z is not None:
+        z[M - 1, F:] = 2.0
+    dg.glu_grad(*args, dX=dX, dW=dW, act="relu", Z=z)
+    dX = dX.cpu()
+    assert torch.isinf(dX[M - 1, 0]) and torch.isfinite(dX[:M - 1]).all()
+
+
 def test_glu_grad_degenerate():
     import dense_gemm_fp32_amd as dg
     t = torch.float16

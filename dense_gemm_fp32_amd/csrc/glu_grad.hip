@@ -204,7 +204,14 @@ ProductJob job_w(const GluGradCall &c) {
 // library's large tiles having few steps of dW's then (1024 x 8192 x 4096 302, 335;
 // 1024 x 16384 x 4096 595, 671; 512 x 16384 x 4096 346, 396; but 2048 x 8192 x 4096 518,
 // 465).  Rows that the library would copy or load by elements take it at any size
-// (3000 x 2000 x 2050 with odd rows: fp16 145, 387; fp32 787, 1094).
+// (odd rows, one launch first: 3000 x 2000 x 2050 fp16 145, 387, fp32 787, 1094).  Beyond
+// kTogetherF16 neither way is ahead everywhere there (fp16 with Z: 8192 x 4096 x 1024
+// 370, 431; 1100 x 6800 x 4100 378, 574; 2048 x 4096 x 4096 325, 297; 2048 x 8192 x
+// 4096 662, 570; 4096^3 610, 506; without Z 469, 524; 542, 771; 429, 428; 843, 836;
+// 812, 749).
+// All of this is measured with both gradients wanted.  One of the two alone takes the
+// same way and the same parts, so that it gets the bits that it has beside the other
+// (fp16 1024 x 8192 x 4096: dX 161, dW 173, both 330; 2048^3 55, 48, 85).
 constexpr double kTogetherF16 = 3.0e10, kTogetherF32 = 5.0e9;
 constexpr int kFewTogether = 1024;
 

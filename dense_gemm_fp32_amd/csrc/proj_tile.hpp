@@ -265,7 +265,7 @@ struct ProjTiles {
 template <>
 struct ProjTiles<4> {
   typedef H16Tile<128, 128, 32, 4, 2, 2, 8, 16, 4> Mid;            // 8 waves,  68 KB
-  typedef H16Tile<64, 64, 32, 2, 2, 2, 8, 16, 4> Small;            // 4 waves,  34 KB
+  typedef H16Tile<64, 64, 32, 2, 2, 2, 8, 16, 4> Small;            // 4 waves,  32 KB
 };
 
 // n tiles in rounds of `round` at `start` + `step` each; what is left, up to `few`, at

@@ -1132,6 +1132,64 @@ def test_gradients_of_rows_beyond_32_bits():
     assert worst(dx, *want["dX"]) <= 1.0 and worst(dw, *want["dW"]) <= 1.0
 
 
+MOST = 1 << 24
+
+
+@pytest.mark.parametrize("what", ["rows", "columns of few rows", "columns of many rows"])
+def test_products_of_the_most_rows_and_columns(what):
+    """As many rows, or rows of W, as a call takes, 4096 of them over and over: whole
+    numbers, so that the results are those of the 4096 bit for bit."""
+    import dense_gemm_fp32_amd as dg
+    P, K = 4096, 16
+    note("products of the most %s" % what)
+    g = gen(len(what))
+    M, N = (MOST, 6) if what == "rows" else (3 if "few" in what else 70, MOST)
+    X, W = whole(g, (min(M, P), K)), whole(g, (min(N, P), K))
+    xs, ws = 2.0 ** -(torch.arange(len(X)) % 5), 2.0 ** -(torch.arange(len(W)) % 7)
+    S = (X.double() @ W.double().t()) * xs.double()[:, None] * ws.double()[None, :]
+    over = lambda t, n: t.to(GPU).repeat(n // len(t), *(1,) * (t.dim() - 1))  # noqa: E731
+    x, w, a, b = over(X, M), over(W, N), over(xs, M), over(ws, N)
+    y = torch.full((M, N), math.nan, device=GPU)
+    dg.gemm_i8(x, w, y, x_scale=a, w_scale=b)
+    want = S.float().to(GPU)
+    assert bool((y.view(M // len(X), len(X), N // len(W), len(W)) == want[:, None]).all())
+
+
+@pytest.mark.parametrize("what", ["rows", "columns of few rows", "columns of many rows"])
+def test_blocks_of_the_most_rows_and_columns(what):
+    """The same of gated blocks and their gradients: relu of whole numbers."""
+    import dense_gemm_fp32_amd as dg
+    P, K, t = 4096, 8, torch.float16
+    note("blocks of the most %s" % what)
+    g = gen(len(what))
+    M, F = (MOST, 2) if what == "rows" else (3 if "few" in what else 70, MOST // 2)
+    small = lambda *s: torch.randint(-2, 3, s, generator=g).to(t)  # noqa: E731
+    X, G, U = small(min(M, P), K), small(min(F, P), K), small(min(F, P), K)
+    dH = torch.zeros(min(M, P), min(F, P))
+    dH[::16, ::max(1, F // 32768)] = 1.0  # few: sums stay below 2^24
+    over = lambda v, n: v.to(GPU).repeat(n // len(v), 1)  # noqa: E731
+    x, w = over(X, M), torch.cat((over(G, F), over(U, F)))
+    d = dH.to(t).to(GPU).repeat(M // len(dH), F // dH.shape[1])
+    g1, u1 = X.float() @ G.float().t(), X.float() @ U.float().t()
+    H = (g1.clamp(min=0) * u1).to(GPU)
+    h = torch.full((M, F), math.nan, dtype=t, device=GPU)
+    dg.glu(x, w, h, act="relu")
+    periods = (M // len(X), len(X), F // len(G), len(G))
+    assert bool((h.view(periods).float() == H.half().float()[:, None]).all())
+    del h
+    dX = torch.full((M, K), math.nan, dtype=t, device=GPU)
+    dW = torch.full((2 * F, K), math.nan, device=GPU)
+    dg.glu_grad(d, x, w, dX=dX, dW=dW, act="relu")
+    dG, dU = dH * u1 * (g1 > 0), dH * g1.clamp(min=0)
+    once = (dG.double() @ G.double() + dU.double() @ U.double()) * periods[2]
+    assert float(once.abs().max()) < 2 ** 24
+    assert bool((dX.view(-1, len(X), K) == once.float().half().to(GPU)).all())
+    for part, D in ((dW[:F], dG), (dW[F:], dU)):
+        sums = (D.double().t() @ X.double()) * periods[0]
+        assert float(sums.abs().max()) < 2 ** 24
+        assert bool((part.view(-1, len(G), K) == sums.float().to(GPU)).all())
+
+
 @pytest.mark.parametrize("N", [6016, 6600])
 def test_many_rows_far_apart(N):
     """200 rows, 2^24 bytes from one to the next: operands are copied for the tiles
